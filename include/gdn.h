@@ -50,7 +50,7 @@ extern "C" {
 
 /* Status codes.  Host-side validation errors (INVALID_ARG, UNSUPPORTED,
  * WORKSPACE) are returned before anything is enqueued.  Device-detected errors
- * (TIMEOUT, BAD_SEQLENS, DEVICE_CHECK) are recorded in the workspace status
+ * (TIMEOUT, BAD_SEQLENS, DEVICE_CHECK, NO_PAGES) are recorded in the workspace status
  * word by the kernels and reported later by gdn_check. */
 typedef enum gdn_status {
   GDN_OK = 0,
@@ -60,7 +60,8 @@ typedef enum gdn_status {
   GDN_ERR_CUDA = 4,         /* a CUDA runtime call or a launch failed         */
   GDN_ERR_TIMEOUT = 5,      /* a bounded device-side wait gave up             */
   GDN_ERR_BAD_SEQLENS = 6,  /* cu_seqlens not 0 = cu[0] < cu[1] < ... = T     */
-  GDN_ERR_DEVICE_CHECK = 7  /* a device-side consistency check failed         */
+  GDN_ERR_DEVICE_CHECK = 7, /* a device-side consistency check failed         */
+  GDN_ERR_NO_PAGES = 8      /* a pool has fewer free pages than a fork needs  */
 } gdn_status;
 
 /* Storage type of q, k, v, beta and o.  g, the states and all arithmetic are
@@ -118,7 +119,9 @@ enum {
    * the later segments' outputs.  The result equals the unsplit one up to
    * rounding.  The workspace must be sized with gdn_fwd_split_workspace_size.
    * Other calls ignore the flag. */
-  GDN_SEQ_SPLIT = 1u << 5
+  GDN_SEQ_SPLIT = 1u << 5,
+  /* gdn_group_norm and gdn_group_norm_bwd: SiLU on the normalised value. */
+  GDN_NORM_SILU = 1u << 6
 };
 
 /* Bytes of device workspace gdn_fwd needs for these sizes (>= 256; the first
@@ -543,6 +546,218 @@ gdn_status gdn_bwd(const void *q, const void *k, const void *v, const float *g,
                    int32_t seq_len, int32_t num_heads, int32_t head_dim_k, int32_t head_dim_v,
                    int32_t num_seqs, gdn_dtype dtype, uint32_t flags, void *workspace,
                    size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_lin_fwd -- linear attention with a decay for each head, the chunked form
+ * for prompts.  Per sequence n and head h, tokens t = 1..L_n:
+ *
+ *     S_t = lam_h S_{t-1} + k_t v_t^T,    o_t = S_t^T q_t,   lam_h = exp(log_decay[h])
+ *
+ * the recurrence of gdn_fwd without erase, write strength and per-token gate
+ * (linear attention with a constant decay: "Model Architecture Walkthrough",
+ * section 5.2.1, with a fixed rate per head).  There is no 1/sqrt(dk) scale.
+ * The state is dk x dv, fp32; sums are fp32 and o is stored in the caller's
+ * dtype.
+ *
+ *   q, k          [batch, seq_len, num_heads, head_dim_k]    dtype     device
+ *   v             [batch, seq_len, num_heads, head_dim_v]    dtype     device
+ *   log_decay     [num_heads]                                float32   device
+ *   initial_state [num_seqs, num_heads, head_dim_k, head_dim_v] float32 device, or NULL (= zeros)
+ *   cu_seqlens    [num_seqs + 1] int32 device, or NULL       (sequences as in gdn_fwd)
+ *   o             [batch, seq_len, num_heads, head_dim_v]    dtype     device (written)
+ *   final_state   as initial_state                           float32   device (written), or NULL
+ *
+ * q_stride, k_stride, v_stride: elements from one token row to the next (the
+ * rows of a batch follow one another), so that q, k and v may be slices of one
+ * projection; 0 stands for densely packed rows.  A row (num_heads * head_dim
+ * elements) is contiguous, and strides are multiples of 16 bytes.  o is dense.
+ *
+ * Values: log_decay is expected <= 0 (0: no decay); it is not clamped.
+ * Supported sizes: head_dim_k and head_dim_v multiples of 32 in [32, 256];
+ * num_seqs <= 16384; num_heads <= 65535.  flags: GDN_FORCE_SIMT (the fp32
+ * CUDA-core kernel for bf16 storage too) or 0.  Empty sequences and seq_len =
+ * 0 are legal (states pass through).  Aliasing, workspace (at least
+ * gdn_lin_workspace_size(...) bytes; the first 256 are the status word, zeroed
+ * once with gdn_workspace_init) and errors as gdn_fwd.
+ */
+size_t gdn_lin_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_heads,
+                              int32_t head_dim_k, int32_t head_dim_v, uint32_t flags);
+gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                       const float *initial_state, const int32_t *cu_seqlens, void *o,
+                       float *final_state, int32_t batch, int32_t seq_len, int32_t num_heads,
+                       int32_t head_dim_k, int32_t head_dim_v, int32_t num_seqs,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, gdn_dtype dtype,
+                       uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_lin_bwd -- backward pass of gdn_lin_fwd.  With G_t the gradient of S_t,
+ * for t = L..1 (lam G_{L+1} standing for d_final_state):
+ *
+ *     G_t = lam G_{t+1} + q_t do_t^T,   dq_t = S_t do_t,  dk_t = G_t v_t,
+ *     dv_t = G_t^T k_t,                 d_initial_state = lam G_1
+ *
+ * (log_decay is a constant of the layer: no gradient.)
+ *
+ *   q, k, v, log_decay, initial_state, cu_seqlens, strides  as gdn_lin_fwd
+ *   d_o              [batch, seq_len, num_heads, head_dim_v]   dtype    device
+ *   d_final_state    as initial_state                          float32  device, or NULL (= zeros)
+ *   dq, dk           [batch, seq_len, num_heads, head_dim_k]   dtype    device (written)
+ *   dv               [batch, seq_len, num_heads, head_dim_v]   dtype    device (written)
+ *   d_initial_state  as initial_state                          float32  device (written), or NULL
+ *
+ * The gradients of q, k and v have the storage dtype of q, k and v (sums are
+ * fp32, one rounding at the end); every one is written once, so results are
+ * bitwise reproducible.  Sizes, flags, workspace (the same size) and errors as
+ * gdn_lin_fwd; no output may overlap an input or another output.
+ */
+gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                       const float *initial_state, const int32_t *cu_seqlens, const void *d_o,
+                       const float *d_final_state, void *dq, void *dk, void *dv,
+                       float *d_initial_state, int32_t batch, int32_t seq_len, int32_t num_heads,
+                       int32_t head_dim_k, int32_t head_dim_v, int32_t num_seqs, int64_t q_stride,
+                       int64_t k_stride, int64_t v_stride, gdn_dtype dtype, uint32_t flags,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_lin_decode -- one token of gdn_lin_fwd's recurrence per (sequence, head)
+ * on states held in the pages of a pool: S' = lam S + k v^T, o = S'^T q.
+ *
+ *   q, k       [num_seqs, num_heads, head_dim_k]              dtype    device
+ *   v, o       [num_seqs, num_heads, head_dim_v]              dtype    device (o written)
+ *   log_decay  [num_heads]                                    float32  device
+ *   state_in   num_pages pages of [num_heads, head_dim_k, head_dim_v] float32 device, page_stride
+ *              floats apart (0: densely packed; a multiple of 4), or NULL (= zeros)
+ *   state_out  laid out as state_in                           float32  device (written)
+ *   pages      [num_seqs] int32 device: the page of each sequence, or NULL (sequence n: page n)
+ *
+ * state_out may be state_in (the usual call: pages updated in place).  A page
+ * number of -1 marks a padded row: nothing of the pool is touched and its o is
+ * zero.  A number outside -1 .. num_pages - 1 does the same and, where a
+ * workspace is given (>= 256 bytes, or NULL), records GDN_ERR_DEVICE_CHECK for
+ * gdn_check.  Sequences of one call must name different pages.  flags: 0.
+ * Sizes as gdn_lin_fwd, num_seqs <= 65535.  Outputs overlap no input (but
+ * state_out may be state_in).
+ */
+gdn_status gdn_lin_decode(const void *q, const void *k, const void *v, const float *log_decay,
+                          const float *state_in, float *state_out, const int32_t *pages, void *o,
+                          int32_t num_seqs, int32_t num_heads, int32_t head_dim_k,
+                          int32_t head_dim_v, int32_t num_pages, int64_t page_stride,
+                          gdn_dtype dtype, uint32_t flags, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_group_norm -- group norm with an activation, channels last.  With D =
+ * channels / groups, mean and variance are taken over the spatial * D values
+ * of each (sample, group), and with xh the normalised value
+ *
+ *     u = xh weight[c] + bias[c],   xh = (x - mean) / sqrt(var + eps)
+ *     y = act(u) silu(gate)         act: silu with GDN_NORM_SILU, else identity;
+ *                                   a NULL gate leaves its factor out
+ *
+ * spatial = 1 with groups = heads is the norm of a linear-attention layer's
+ * output before its gate (one sample per token).
+ *
+ *   x, gate, y    [batch, spatial, channels]   dtype    device (gate or NULL; y written)
+ *   weight, bias  [channels]                   float32  device, or NULL (= 1 / 0)
+ *   mean, rstd    [batch, groups]              float32  device (written), or NULL
+ *
+ * channels <= 8192, a multiple of groups.  batch = 0 or spatial = 0 writes
+ * nothing.  Statistics and arithmetic are fp32.  workspace: at least
+ * gdn_group_norm_workspace_size(...) bytes, of any contents; calls sharing it
+ * are ordered (same stream).  No device-detected error.  Outputs overlap
+ * neither inputs nor one another.
+ */
+size_t gdn_group_norm_workspace_size(int32_t batch, int32_t spatial, int32_t channels,
+                                     int32_t groups);
+gdn_status gdn_group_norm(const void *x, const float *weight, const float *bias, const void *gate,
+                          void *y, float *mean, float *rstd, int32_t batch, int32_t spatial,
+                          int32_t channels, int32_t groups, float eps, gdn_dtype dtype,
+                          uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_group_norm_bwd -- backward pass of gdn_group_norm, from the mean and rstd
+ * that it wrote.  With du = d_y silu(gate) act'(u) and dxh = du weight:
+ *
+ *     dx = rstd (dxh - mean(dxh) - xh mean(dxh xh)),   dgate = d_y act(u) silu'(gate)
+ *     dweight = sum du xh,  dbias = sum du      (over samples and rows)
+ *
+ *   x, weight, bias, gate, mean, rstd, flags   as gdn_group_norm (inputs)
+ *   d_y, dx, dgate    [batch, spatial, channels]  dtype    device (dx, dgate written; dgate with
+ *                     a gate only)
+ *   dweight, dbias    [channels]                  float32  device (written), or NULL
+ *
+ * Sums are taken in a fixed order: results are bitwise reproducible.
+ */
+gdn_status gdn_group_norm_bwd(const void *x, const float *weight, const float *bias,
+                              const void *gate, const float *mean, const float *rstd,
+                              const void *d_y, void *dx, void *dgate, float *dweight, float *dbias,
+                              int32_t batch, int32_t spatial, int32_t channels, int32_t groups,
+                              gdn_dtype dtype, uint32_t flags, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_pages_* -- the pages of a state cache: copying, forking, freeing and
+ * compacting.  A pool holds num_pages pages of page_bytes (a multiple of 16).
+ *
+ *   table   [num_rows, max_pages] int32   the pages of each row (sequence): shared snapshots first,
+ *                                         the row's own current page last; -1 past the count
+ *   counts  [num_rows] int32              pages of each row
+ *   refs    [num_pages] int32             rows that hold each page; 0: the page is free
+ *
+ * All of them are device memory.  table_out, counts_out and refs_out receive
+ * the new bookkeeping; each may be its input (updated in place).  Every result
+ * depends on the arguments alone (new pages are the lowest free ones, in the
+ * order of the list), so it is the same from run to run.  A job that breaks a
+ * rule is left out and recorded for gdn_check (GDN_ERR_DEVICE_CHECK with the
+ * job's place in `seq`); the other jobs run.
+ *
+ * gdn_pages_copy: page dst[i] becomes a copy of page src[i], i < n.  The
+ * targets differ from one another and from every source.
+ *
+ * gdn_pages_fork: for i < n, row children[i] becomes a fork of row parents[i]:
+ * it shares the parent's pages (refs + 1) but the last, of which it gets a copy
+ * in a new page.  The child is empty before the call; of two jobs with one
+ * child the first counts.  A parent without pages leaves its child empty.
+ * parents[i] = -1 starts a row: one new page of zeros.  parents[i] =
+ * children[i] takes a snapshot: the row gains a new page, a copy of its last,
+ * and keeps the old one.  fresh[i] (written) is the new page, or -1 where there
+ * is none.  Parents are read as they were at the start of the call.  Without
+ * enough free pages the last jobs of the list are left out and
+ * GDN_ERR_NO_PAGES is recorded.
+ *
+ * gdn_pages_free: rows rows[i], i < n, give their pages back (refs - 1) and are
+ * empty afterwards; a row listed twice is freed once.
+ *
+ * gdn_pages_compact: the live pages move to the lowest numbers, keeping those
+ * already there: the k-th live page at or above num_live moves to the k-th free
+ * page below it.  *num_live (device, written) is the number of live pages; table and refs
+ * are rewritten, counts do not change.
+ *
+ * workspace: at least gdn_pages_workspace_size(num_pages, num_rows, n) bytes
+ * (n = 0 for compact); its first 256 bytes are the status word, zeroed once
+ * with gdn_workspace_init.  Calls sharing it are ordered (same stream).
+ * num_pages, num_rows, n <= 2^24.
+ */
+size_t gdn_pages_workspace_size(int32_t num_pages, int32_t num_rows, int32_t n);
+gdn_status gdn_pages_copy(void *pool, int64_t page_bytes, int32_t num_pages, const int32_t *src,
+                          const int32_t *dst, int32_t n, void *workspace, size_t workspace_bytes,
+                          void *stream);
+gdn_status gdn_pages_fork(void *pool, int64_t page_bytes, int32_t num_pages, const int32_t *table,
+                          const int32_t *counts, const int32_t *refs, int32_t num_rows,
+                          int32_t max_pages, const int32_t *parents, const int32_t *children,
+                          int32_t n, int32_t *fresh, int32_t *table_out, int32_t *counts_out,
+                          int32_t *refs_out, void *workspace, size_t workspace_bytes,
+                          void *stream);
+gdn_status gdn_pages_free(const int32_t *table, const int32_t *counts, const int32_t *refs,
+                          int32_t num_pages, int32_t num_rows, int32_t max_pages,
+                          const int32_t *rows, int32_t n, int32_t *table_out, int32_t *counts_out,
+                          int32_t *refs_out, void *workspace, size_t workspace_bytes,
+                          void *stream);
+gdn_status gdn_pages_compact(void *pool, int64_t page_bytes, int32_t num_pages,
+                             const int32_t *table, const int32_t *counts, const int32_t *refs,
+                             int32_t num_rows, int32_t max_pages, int32_t *num_live,
+                             int32_t *table_out, int32_t *refs_out, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, read the status word in `workspace`, clear it, and
  * return it (GDN_OK if no kernel recorded an error since the last check).

@@ -396,7 +396,7 @@ gdn_status gdn_check_record(void *workspace, void *stream, int32_t *seq, int32_t
   if (seq) *seq = (int32_t)st.seq;
   if (head) *head = (int32_t)st.head;
   if (site) *site = (int32_t)st.aux;
-  return st.code <= GDN_ERR_DEVICE_CHECK ? (gdn_status)st.code : GDN_ERR_DEVICE_CHECK;
+  return st.code <= GDN_ERR_NO_PAGES ? (gdn_status)st.code : GDN_ERR_DEVICE_CHECK;
 }
 
 gdn_status gdn_check(void *workspace, void *stream) {
@@ -413,6 +413,7 @@ const char *gdn_status_string(int32_t status) {
     case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT: a bounded device wait gave up";
     case GDN_ERR_BAD_SEQLENS: return "GDN_ERR_BAD_SEQLENS: cu_seqlens does not rise from 0 to T without decreasing";
     case GDN_ERR_DEVICE_CHECK: return "GDN_ERR_DEVICE_CHECK: a device-side check failed";
+    case GDN_ERR_NO_PAGES: return "GDN_ERR_NO_PAGES: a pool has too few free pages";
     default: return "GDN_ERR_UNKNOWN";
   }
 }

@@ -19,10 +19,10 @@ LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
 GDN_OK = 0
 (GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_ERR_CUDA, GDN_ERR_TIMEOUT,
- GDN_ERR_BAD_SEQLENS, GDN_ERR_DEVICE_CHECK) = range(1, 8)
+ GDN_ERR_BAD_SEQLENS, GDN_ERR_DEVICE_CHECK, GDN_ERR_NO_PAGES) = range(1, 9)
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED",
                 3: "GDN_ERR_WORKSPACE", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_TIMEOUT",
-                6: "GDN_ERR_BAD_SEQLENS", 7: "GDN_ERR_DEVICE_CHECK"}
+                6: "GDN_ERR_BAD_SEQLENS", 7: "GDN_ERR_DEVICE_CHECK", 8: "GDN_ERR_NO_PAGES"}
 GDN_F32, GDN_BF16 = 0, 1
 GDN_QK_L2NORM = 1 << 0
 GDN_FORCE_SIMT = 1 << 1
@@ -30,6 +30,7 @@ GDN_GATE_SIGMOID = 1 << 2
 GDN_BETA_LOGITS = 1 << 3
 GDN_DEBUG_CHECKS = 1 << 4
 GDN_SEQ_SPLIT = 1 << 5
+GDN_NORM_SILU = 1 << 6
 # site codes of a GDN_ERR_DEVICE_CHECK record (gdn_check_record)
 DEBUG_SITES = {1: "q", 2: "k", 3: "v", 4: "g", 5: "beta", 6: "o", 7: "initial_state",
                8: "final_state", 9: "out_gate", 10: "tma_x"}
@@ -41,7 +42,11 @@ EXPORTED = ("gdn_fwd_workspace_size", "gdn_workspace_init", "gdn_fwd", "gdn_chec
             "gdn_decode", "gdn_diag_workspace_size", "gdn_diag_fwd", "gdn_conv_silu",
             "gdn_bwd_workspace_size", "gdn_bwd", "gdn_fwd_debug", "gdn_check_record",
             "gdn_fwd_kernel_name_chunk", "gdn_fwd_split_segments", "gdn_fwd_split_workspace_size",
-            "gdn_diag_delta_workspace_size", "gdn_diag_delta_fwd")
+            "gdn_diag_delta_workspace_size", "gdn_diag_delta_fwd",
+            "gdn_lin_workspace_size", "gdn_lin_fwd", "gdn_lin_bwd", "gdn_lin_decode",
+            "gdn_group_norm_workspace_size", "gdn_group_norm", "gdn_group_norm_bwd",
+            "gdn_pages_workspace_size", "gdn_pages_copy", "gdn_pages_fork", "gdn_pages_free",
+            "gdn_pages_compact")
 # ... and include/gdn_debug.h (self-tests of the failure reporting).
 DEBUG_EXPORTED = ("gdn_debug_wait_timeout",)
 
@@ -120,6 +125,25 @@ def lib() -> ctypes.CDLL:
             L.gdn_diag_delta_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                              i32, i32, i32, i32, i32, ctypes.c_int, u32, vp, sz,
                                              vp]
+            i64, st = ctypes.c_int64, ctypes.c_int
+            for name, res, args in (
+                    ("gdn_lin_workspace_size", sz, [i32] * 5 + [u32]),
+                    ("gdn_lin_fwd", st, [vp] * 8 + [i32] * 6 + [i64] * 3 + [st, u32, vp, sz, vp]),
+                    ("gdn_lin_bwd", st, [vp] * 12 + [i32] * 6 + [i64] * 3 + [st, u32, vp, sz, vp]),
+                    ("gdn_lin_decode", st, [vp] * 8 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
+                    ("gdn_group_norm_workspace_size", sz, [i32] * 4),
+                    ("gdn_group_norm", st, [vp] * 7 + [i32] * 4 + [ctypes.c_float, st, u32, vp, sz,
+                                                                   vp]),
+                    ("gdn_group_norm_bwd", st, [vp] * 11 + [i32] * 4 + [st, u32, vp, sz, vp]),
+                    ("gdn_pages_workspace_size", sz, [i32] * 3),
+                    ("gdn_pages_copy", st, [vp, i64, i32, vp, vp, i32, vp, sz, vp]),
+                    ("gdn_pages_fork", st, [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, i32, vp, vp,
+                                            vp, vp, vp, sz, vp]),
+                    ("gdn_pages_free", st, [vp] * 3 + [i32] * 3 + [vp, i32] + [vp] * 4 + [sz, vp]),
+                    ("gdn_pages_compact", st, [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp,
+                                               sz, vp])):
+                getattr(L, name).restype = res
+                getattr(L, name).argtypes = args
             _lib = L
     return _lib
 
@@ -646,3 +670,421 @@ def gdn_bwd(q, k, v, g, beta, d_o, initial_state=None, cu_seqlens=None, d_final_
         if st != GDN_OK:
             raise GdnError(st, "gdn_bwd (device)")
     return grads
+
+
+# ---------------------------------------------------------------------------
+# Linear attention with a decay for each head, group norm, pages of states
+# ---------------------------------------------------------------------------
+def _use(where, tensors, contiguous=True):
+    """Every tensor given (name -> tensor or None) is on a CUDA device and, if
+    asked for, contiguous."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be on a CUDA device")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+
+
+def _like(where, name, t, shape, dtype):
+    """``t`` (may be None) has this shape and dtype."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]} {list(shape)}")
+
+
+class _Made:
+    """Makes a call's outputs and workspace on the stream that the call runs on,
+    so that the allocator orders their reuse after it."""
+
+    def __init__(self, stream, device):
+        self.stream, self.device = stream, device
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, size, status):
+        """``given``, or a new one; its status word is zeroed if it will be read."""
+        if given is not None:
+            return given
+        ws = self.empty(size, torch.uint8)
+        if status:
+            ws_head = ws[:256]
+            if self.stream is None:
+                ws_head.zero_()
+            else:
+                with torch.cuda.stream(self.stream):
+                    ws_head.zero_()
+        return ws
+
+
+def _finish(where, st, check, workspace, stream):
+    if st != GDN_OK:
+        raise GdnError(st, where)
+    if check:
+        st = gdn_check(workspace, stream)
+        if st != GDN_OK:
+            raise GdnError(st, f"{where} (device)")
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _row_stride(where, name, t):
+    """Elements from one token row of ``t`` ``[B, T, H, D]`` to the next (rows
+    contiguous, the rows of a batch one after the other)."""
+    B, T, H, D = t.shape
+    s = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else H * D)
+    if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or s < H * D or \
+            (B > 1 and T > 0 and t.stride(0) != T * s):
+        raise ValueError(f"{where}: {name} must have contiguous rows [H, D] at one stride")
+    if s * t.element_size() % 16:
+        raise ValueError(f"{where}: the row stride of {name} must be a multiple of 16 bytes")
+    return s
+
+
+def _lin_check(where, q, k, v, log_decay, initial_state, cu_seqlens, extra):
+    """Checks shared by gdn_lin_fwd and gdn_lin_bwd; ``extra``: further tensors,
+    name -> (tensor, shape or None for the state's, dtype or None for q's)."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"{where}: q, k, v must be [B, T, H, D]")
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+    _use(where, dict(q=q, k=k, v=v), contiguous=False)
+    _use(where, dict(log_decay=log_decay, initial_state=initial_state, cu_seqlens=cu_seqlens,
+                     **{n: e[0] for n, e in extra.items()}))
+    _dtype_code(q.dtype)
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"{where}: q, k and v must share one storage dtype")
+    if k.shape != q.shape or v.shape[:3] != q.shape[:3]:
+        raise ValueError(f"{where}: shape mismatch among q, k, v")
+    _like(where, "log_decay", log_decay, (H,), torch.float32)
+    _like(where, "initial_state", initial_state, (N, H, dk, dv), torch.float32)
+    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1):
+        raise TypeError(f"{where}: cu_seqlens must be int32 [N + 1]")
+    for name, (t, shape, dtype) in extra.items():
+        _like(where, name, t, (N, H, dk, dv) if shape is None else shape, dtype or q.dtype)
+    return B, T, H, dk, dv, N
+
+
+def gdn_lin_workspace_size(num_seqs: int, seq_len: int, num_heads: int, head_dim_k: int,
+                           head_dim_v: int, flags: int = 0) -> int:
+    return int(lib().gdn_lin_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v,
+                                            flags))
+
+
+def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=None,
+                final_state=None, output_final_state=True, workspace=None, force_simt=False,
+                stream=None, check=False):
+    """Linear attention with a decay for each head, through the C ABI:
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k ``[B, T, H, dk]``, v ``[B, T, H, dv]`` (float32 or bfloat16; slices of
+    one projection are taken as they are: rows ``[H, D]`` contiguous, one stride
+    between tokens); log_decay ``[H]`` fp32; initial_state ``[N, H, dk, dv]``
+    fp32 or None; cu_seqlens int32 ``[N+1]`` on the device (then B must be 1) or
+    None.  ``o`` / ``final_state`` may be given (``final_state`` may be
+    ``initial_state``).  Returns ``(o, final_state)``.  With ``check=True`` the
+    call synchronises and raises on a device-side error."""
+    w = "gdn_lin_fwd"
+    B, T, H, dk, dv, N = _lin_check(
+        w, q, k, v, log_decay, initial_state, cu_seqlens,
+        dict(o=(o, v.shape, None), final_state=(final_state, None, torch.float32)))
+    made = _Made(stream, q.device)
+    if o is None:
+        o = made.empty(v.shape, v.dtype)
+    if final_state is None and output_final_state:
+        final_state = made.empty((N, H, dk, dv), torch.float32)
+    flags = GDN_FORCE_SIMT if force_simt else 0
+    workspace = made.workspace(workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
+    st = lib().gdn_lin_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
+                           _ptr(cu_seqlens), _ptr(o), _ptr(final_state), B, T, H, dk, dv, N,
+                           _row_stride(w, "q", q), _row_stride(w, "k", k), _row_stride(w, "v", v),
+                           _dtype_code(q.dtype), flags, _ptr(workspace), _nbytes(workspace),
+                           _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return o, final_state
+
+
+def gdn_lin_bwd(q, k, v, log_decay, d_o, initial_state=None, cu_seqlens=None, d_final_state=None,
+                *, grads=None, workspace=None, force_simt=False, stream=None, check=False):
+    """Backward pass of ``gdn_lin_fwd`` through the C ABI.
+
+    Inputs as ``gdn_lin_fwd`` plus ``d_o`` (like o) and ``d_final_state``
+    (``[N, H, dk, dv]`` fp32 or None).  Returns a dict ``dq, dk, dv`` (storage
+    dtype) and ``dh0`` (fp32) (``grads`` may supply them; one without ``dh0``
+    leaves it out)."""
+    w = "gdn_lin_bwd"
+    given = grads or {}
+    B, T, H, dk, dv, N = _lin_check(
+        w, q, k, v, log_decay, initial_state, cu_seqlens,
+        dict(d_o=(d_o, v.shape, None), d_final_state=(d_final_state, None, torch.float32),
+             dq=(given.get("dq"), q.shape, None), dk=(given.get("dk"), q.shape, None),
+             dv=(given.get("dv"), v.shape, None), dh0=(given.get("dh0"), None, torch.float32)))
+    made = _Made(stream, q.device)
+    if grads is None:
+        grads = {"dq": made.empty(q.shape, q.dtype), "dk": made.empty(q.shape, q.dtype),
+                 "dv": made.empty(v.shape, v.dtype),
+                 "dh0": made.empty((N, H, dk, dv), torch.float32)}
+    flags = GDN_FORCE_SIMT if force_simt else 0
+    workspace = made.workspace(workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
+    st = lib().gdn_lin_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
+                           _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state), _ptr(grads["dq"]),
+                           _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads.get("dh0")), B, T, H,
+                           dk, dv, N, _row_stride(w, "q", q), _row_stride(w, "k", k),
+                           _row_stride(w, "v", v), _dtype_code(q.dtype), flags, _ptr(workspace),
+                           _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return grads
+
+
+def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=None,
+                   workspace=None, stream=None, check=False):
+    """One token per (sequence, head) of ``gdn_lin_fwd``'s recurrence.
+
+    q, k ``[N, H, dk]``; v ``[N, H, dv]``; log_decay ``[H]`` fp32; ``state``
+    ``[P, H, dk, dv]`` fp32: the pages of a pool, each contiguous, at any stride
+    (``pool[:, layer]``), or None (zeros; then give ``state_out``).  ``pages``
+    int32 ``[N]``: the page of each sequence (-1: a padded row, o = 0), or None
+    (sequence n has page n).  The pages are updated in place unless
+    ``state_out`` (laid out like ``state``) is given.  Returns
+    ``(o, state_out)``.  With ``check=True`` the call synchronises and raises if
+    a page number was out of range."""
+    w = "gdn_lin_decode"
+    N, H, dk = q.shape
+    dv = v.shape[-1]
+    if state_out is None:
+        if state is None:
+            raise ValueError(f"{w}: give state, or state_out")
+        state_out = state
+    P = state_out.shape[0]
+    _use(w, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o))
+    _use(w, dict(state=state, state_out=state_out), contiguous=False)
+    _dtype_code(q.dtype)
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError(f"{w}: q, k and v must share one storage dtype")
+    if k.shape != q.shape or v.shape[:2] != (N, H):
+        raise ValueError(f"{w}: shape mismatch among q, k, v")
+    _like(w, "log_decay", log_decay, (H,), torch.float32)
+    _like(w, "pages", pages, (N,), torch.int32)
+    _like(w, "o", o, v.shape, v.dtype)
+    for name, t in (("state", state), ("state_out", state_out)):
+        _like(w, name, t, (P, H, dk, dv), torch.float32)
+        if t is not None and (not t[0].is_contiguous() or
+                              (P > 1 and t.stride(0) != state_out.stride(0))):
+            raise ValueError(f"{w}: {name} must have contiguous pages at one stride")
+    made = _Made(stream, q.device)
+    if o is None:
+        o = made.empty(v.shape, v.dtype)
+    if check:
+        workspace = made.workspace(workspace, 256, True)
+    st = lib().gdn_lin_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
+                              _ptr(state_out), _ptr(pages), _ptr(o), N, H, dk, dv, P,
+                              state_out.stride(0) if P > 1 else 0, _dtype_code(q.dtype), 0,
+                              _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                              _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return o, state_out
+
+
+def gdn_group_norm_workspace_size(batch: int, spatial: int, channels: int, groups: int) -> int:
+    return int(lib().gdn_group_norm_workspace_size(batch, spatial, channels, groups))
+
+
+def _norm_check(where, x, weight, bias, groups, gate, extra):
+    if x.dim() != 3:
+        raise ValueError(f"{where}: x must be [N, S, C]")
+    N, S, C = x.shape
+    _use(where, dict(x=x, weight=weight, bias=bias, gate=gate,
+                     **{n: e[0] for n, e in extra.items()}))
+    _dtype_code(x.dtype)
+    _like(where, "weight", weight, (C,), torch.float32)
+    _like(where, "bias", bias, (C,), torch.float32)
+    _like(where, "gate", gate, x.shape, x.dtype)
+    for name, (t, shape, dtype) in extra.items():
+        _like(where, name, t, shape, dtype)
+    return N, S, C
+
+
+def gdn_group_norm(x, weight, bias, groups, *, gate=None, silu=False, eps=1e-5, y=None, mean=None,
+                   rstd=None, workspace=None, stream=None):
+    """Group norm with an activation, channels last, through the C ABI.
+
+    x ``[N, S, C]`` (float32 or bfloat16), ``groups`` groups of C / groups
+    channels, statistics over the S rows and the group's channels; weight, bias
+    ``[C]`` fp32 or None.  y = act(u) * silu(gate) with u the normalised, scaled
+    value, act = SiLU with ``silu`` (else the identity) and ``gate`` like x, or
+    None (no factor).  Returns ``(y, mean, rstd)``, the last two ``[N, groups]``
+    fp32 (kept for the backward pass)."""
+    w = "gdn_group_norm"
+    f32 = torch.float32
+    N, S, C = _norm_check(w, x, weight, bias, groups, gate,
+                          dict(y=(y, x.shape, x.dtype), mean=(mean, (x.shape[0], groups), f32),
+                               rstd=(rstd, (x.shape[0], groups), f32)))
+    made = _Made(stream, x.device)
+    y = made.empty(x.shape, x.dtype) if y is None else y
+    mean = made.empty((N, groups), f32) if mean is None else mean
+    rstd = made.empty((N, groups), f32) if rstd is None else rstd
+    workspace = made.workspace(workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
+    st = lib().gdn_group_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), _ptr(mean),
+                              _ptr(rstd), N, S, C, groups, eps, _dtype_code(x.dtype),
+                              GDN_NORM_SILU if silu else 0, _ptr(workspace), _nbytes(workspace),
+                              _stream_handle(stream))
+    _finish(w, st, False, workspace, stream)
+    return y, mean, rstd
+
+
+def gdn_group_norm_bwd(x, weight, bias, groups, mean, rstd, d_y, *, gate=None, silu=False,
+                       grads=None, workspace=None, stream=None):
+    """Backward pass of ``gdn_group_norm`` from the ``mean`` and ``rstd`` it
+    returned.  Returns a dict ``dx``, ``dgate`` (storage dtype; dgate None
+    without a gate), ``dweight``, ``dbias`` (fp32 ``[C]``); ``grads`` may supply
+    them."""
+    w = "gdn_group_norm_bwd"
+    f32 = torch.float32
+    given = grads or {}
+    C = x.shape[-1]
+    N, S, C = _norm_check(w, x, weight, bias, groups, gate,
+                          dict(mean=(mean, (x.shape[0], groups), f32),
+                               rstd=(rstd, (x.shape[0], groups), f32),
+                               d_y=(d_y, x.shape, x.dtype), dx=(given.get("dx"), x.shape, x.dtype),
+                               dgate=(given.get("dgate"), x.shape, x.dtype),
+                               dweight=(given.get("dweight"), (C,), f32),
+                               dbias=(given.get("dbias"), (C,), f32)))
+    made = _Made(stream, x.device)
+    if grads is None:
+        grads = {"dx": made.empty(x.shape, x.dtype),
+                 "dgate": None if gate is None else made.empty(x.shape, x.dtype),
+                 "dweight": made.empty((C,), f32), "dbias": made.empty((C,), f32)}
+    workspace = made.workspace(workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
+    st = lib().gdn_group_norm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(mean),
+                                  _ptr(rstd), _ptr(d_y), _ptr(grads["dx"]),
+                                  _ptr(grads.get("dgate")), _ptr(grads.get("dweight")),
+                                  _ptr(grads.get("dbias")), N, S, C, groups, _dtype_code(x.dtype),
+                                  GDN_NORM_SILU if silu else 0, _ptr(workspace),
+                                  _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, False, workspace, stream)
+    return grads
+
+
+def gdn_pages_workspace_size(num_pages: int, num_rows: int, n: int) -> int:
+    return int(lib().gdn_pages_workspace_size(num_pages, num_rows, n))
+
+
+def _pages_check(where, pool, table, counts, refs, lists, outs):
+    """Returns (page bytes, pages, rows, most pages of a row)."""
+    _use(where, dict(pool=pool, table=table, counts=counts, refs=refs, **lists, **outs))
+    for name, t in dict(lists, table=table, counts=counts, refs=refs, **outs).items():
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{where}: {name} must be int32")
+    R, M, P = (0, 1, pool.shape[0]) if table is None else (*table.shape, refs.shape[0])
+    if table is not None:
+        _like(where, "counts", counts, (R,), torch.int32)
+        _like(where, "refs", refs, (P,), torch.int32)
+        for name, like in (("table_out", (R, M)), ("counts_out", (R,)), ("refs_out", (P,))):
+            _like(where, name, outs.get(name), like, torch.int32)
+    n = {t.numel() for t in lists.values()}
+    if len(n) > 1 or any(t.dim() != 1 for t in lists.values()):
+        raise ValueError(f"{where}: {', '.join(lists)} must be lists of one length")
+    bytes_ = 16
+    if pool is not None:
+        if pool.shape[0] != P:
+            raise ValueError(f"{where}: refs must have one entry for each page of the pool")
+        bytes_ = _nbytes(pool) // P if P else 0
+    return bytes_, P, R, M
+
+
+def gdn_pages_copy(pool, src, dst, *, workspace=None, stream=None, check=False):
+    """Pages ``dst`` of ``pool`` ``[P, ...]`` become copies of pages ``src``
+    (int32 ``[n]`` each).  Returns ``pool``."""
+    w = "gdn_pages_copy"
+    bytes_, P, _, _ = _pages_check(w, pool, None, None, None, dict(src=src, dst=dst), {})
+    n = src.numel()
+    workspace = _Made(stream, pool.device).workspace(workspace, gdn_pages_workspace_size(P, 0, n),
+                                                     check)
+    st = lib().gdn_pages_copy(_ptr(pool), bytes_, P, _ptr(src), _ptr(dst), n, _ptr(workspace),
+                              _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return pool
+
+
+def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, table_out=None,
+                   counts_out=None, refs_out=None, workspace=None, stream=None, check=False):
+    """Fork rows of a page table: row ``children[i]`` shares the pages of row
+    ``parents[i]`` but the last, of which it gets a copy in the lowest free page
+    (parent -1: a new row with one page of zeros; parent = child: a snapshot,
+    the row goes on in a copy of its last page).
+
+    pool ``[P, ...]`` (pages a multiple of 16 bytes); table int32 ``[R, M]``;
+    counts int32 ``[R]``; refs int32 ``[P]``; parents, children int32 ``[n]``.
+    ``table_out`` / ``counts_out`` / ``refs_out`` may be the inputs (updated in
+    place) and are new tensors if not given; the pool is updated in place.
+    Returns ``(fresh, table_out, counts_out, refs_out)``, ``fresh[i]`` the new
+    page of child i (-1: none).  With ``check=True`` the call synchronises and
+    raises if a job was left out (a bad row or too few free pages)."""
+    w = "gdn_pages_fork"
+    bytes_, P, R, M = _pages_check(w, pool, table, counts, refs,
+                                   dict(parents=parents, children=children),
+                                   dict(fresh=fresh, table_out=table_out, counts_out=counts_out,
+                                        refs_out=refs_out))
+    n = parents.numel()
+    _like(w, "fresh", fresh, (n,), torch.int32)
+    made = _Made(stream, pool.device)
+    fresh = made.empty((n,), torch.int32) if fresh is None else fresh
+    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
+    counts_out = made.empty((R,), torch.int32) if counts_out is None else counts_out
+    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
+    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, n), check)
+    st = lib().gdn_pages_fork(_ptr(pool), bytes_, P, _ptr(table), _ptr(counts), _ptr(refs), R, M,
+                              _ptr(parents), _ptr(children), n, _ptr(fresh), _ptr(table_out),
+                              _ptr(counts_out), _ptr(refs_out), _ptr(workspace),
+                              _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return fresh, table_out, counts_out, refs_out
+
+
+def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None, refs_out=None,
+                   workspace=None, stream=None, check=False):
+    """Rows ``rows`` (int32 ``[n]``) give their pages back and are empty
+    afterwards.  Tensors and outputs as ``gdn_pages_fork``.  Returns
+    ``(table_out, counts_out, refs_out)``."""
+    w = "gdn_pages_free"
+    _, P, R, M = _pages_check(w, None, table, counts, refs, dict(rows=rows),
+                              dict(table_out=table_out, counts_out=counts_out, refs_out=refs_out))
+    n = rows.numel()
+    made = _Made(stream, table.device)
+    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
+    counts_out = made.empty((R,), torch.int32) if counts_out is None else counts_out
+    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
+    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, n), check)
+    st = lib().gdn_pages_free(_ptr(table), _ptr(counts), _ptr(refs), P, R, M, _ptr(rows), n,
+                              _ptr(table_out), _ptr(counts_out), _ptr(refs_out), _ptr(workspace),
+                              _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return table_out, counts_out, refs_out
+
+
+def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=None, refs_out=None,
+                      workspace=None, stream=None, check=False):
+    """Move the live pages of ``pool`` to the lowest numbers and rewrite the
+    table.  Tensors as ``gdn_pages_fork``.  Returns ``(num_live, table_out,
+    refs_out)``, num_live int32 ``[1]`` on the device."""
+    w = "gdn_pages_compact"
+    bytes_, P, R, M = _pages_check(w, pool, table, counts, refs, {},
+                                   dict(num_live=num_live, table_out=table_out, refs_out=refs_out))
+    _like(w, "num_live", num_live, (1,), torch.int32)
+    made = _Made(stream, pool.device)
+    num_live = made.empty((1,), torch.int32) if num_live is None else num_live
+    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
+    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
+    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, 0), check)
+    st = lib().gdn_pages_compact(_ptr(pool), bytes_, P, _ptr(table), _ptr(counts), _ptr(refs), R,
+                                 M, _ptr(num_live), _ptr(table_out), _ptr(refs_out),
+                                 _ptr(workspace), _nbytes(workspace), _stream_handle(stream))
+    _finish(w, st, check, workspace, stream)
+    return num_live, table_out, refs_out
