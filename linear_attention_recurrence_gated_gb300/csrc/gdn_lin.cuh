@@ -69,6 +69,9 @@ __device__ __forceinline__ float state_in(const Scan &s, int64_t unit, int i, in
   return s.s_in[base + (s.s_in_t ? (int64_t)j * s.da + i : (int64_t)i * s.dc + j)];
 }
 
+// The tensor-core form: bf16 storage, da 64 or 128, dc a multiple of 64.
+bool tc_scan(const Scan &s);
+cudaError_t launch_tc(const Params &p, cudaStream_t stream);
 cudaError_t launch_simt(const Params &p, gdn_dtype dtype, cudaStream_t stream);
 
 }  // namespace lin

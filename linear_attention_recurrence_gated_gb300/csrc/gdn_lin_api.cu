@@ -42,6 +42,20 @@ gdn_status check_sizes(int32_t batch, int32_t seq_len, int32_t num_heads, int32_
   return GDN_OK;
 }
 
+// Every scan on the tensor cores where its sizes allow, else on the CUDA cores.
+cudaError_t launch(const Params &p, gdn_dtype dtype, uint32_t flags, cudaStream_t stream) {
+  Params on = p, off = p;
+  on.num_scans = off.num_scans = 0;
+  for (int i = 0; i < p.num_scans; ++i) {
+    const bool tensor = dtype == GDN_BF16 && !(flags & GDN_FORCE_SIMT) && tc_scan(p.scan[i]);
+    Params &to = tensor ? on : off;
+    to.scan[to.num_scans++] = p.scan[i];
+  }
+  cudaError_t err = on.num_scans ? launch_tc(on, stream) : cudaSuccess;
+  if (err == cudaSuccess && off.num_scans) err = launch_simt(off, dtype, stream);
+  return err;
+}
+
 }  // namespace
 }  // namespace lin
 }  // namespace gdn
@@ -106,7 +120,7 @@ gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float 
   p.seq_len = seq_len;
   p.num_heads = num_heads;
   p.num_seqs = num_seqs;
-  return launch_simt(p, dtype, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch(p, dtype, flags, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float *log_decay,
@@ -170,7 +184,7 @@ gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float 
   p.seq_len = seq_len;
   p.num_heads = num_heads;
   p.num_seqs = num_seqs;
-  return launch_simt(p, dtype, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return launch(p, dtype, flags, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"
