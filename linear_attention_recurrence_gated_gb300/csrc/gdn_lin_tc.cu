@@ -17,12 +17,14 @@
 //
 // Rounding.  The state is a sum that runs over the whole sequence and is
 // returned in fp32, so X must be exact to fp32: b and c are bf16 already, and
-// V^ is split into three bf16 terms (8 + 8 + 8 bits of the 24 of w_j c_j).  P'
+// V^ is split into three bf16 terms (8 + 8 + 8 bits of the 24 of w_j c_j), or
+// two where the third could not reach the returned state.  P'
 // and the S that O1 reads are rounded to bf16 once: each enters an output that
 // is itself rounded to bf16, so an output carries two such roundings in all.
 //
-// Roles (18 warps): P' (warps 0-3), o (4-7), V^ (8-11), S (12-15), TMA (16),
-// MMA issue (17).  Every wait is bounded; a timeout records GDN_ERR_TIMEOUT,
+// Roles (18 warps): P' (warps 0-3), o (4-7), V^ of the first 64 tokens (8-11),
+// of the others and S (12-15), TMA (16), MMA issue (17).  V^ and X go by halves,
+// so that one half is weighed while the other is multiplied.  Every wait is bounded; a timeout records GDN_ERR_TIMEOUT,
 // raises the abort flag and every role leaves its loop.
 //
 // Rows past a sequence's end in its last tile may belong to a neighbour.  Their
@@ -43,6 +45,7 @@ using tc::swz;
 constexpr int kC = 128;
 constexpr int kTile = kC * 128;   // [128][64] bf16
 constexpr int kThreads = 18 * 32;
+constexpr uint32_t kWaitTries = 1u << 19;   // probes of 4 us each before a wait gives up (2 s)
 constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColX = 384, kCols = 512;
 
 template <int DK>
@@ -62,8 +65,8 @@ struct Lay {
 };
 
 // mbarriers
-enum Bar { kFull = 0, kEmpty = 3, kPFull = 6, kPReady = 8, kClean = 10, kVhReady, kXFull, kXRead,
-           kSReady, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars };
+enum Bar { kFull = 0, kEmpty = 3, kPFull = 6, kPReady = 8, kVhReady = 10, kXHalf = 12, kXFull,
+           kClean, kXRead, kSReady, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars };
 
 struct TcArgs {
   Params p;
@@ -74,31 +77,62 @@ struct TcArgs {
 struct Waits {
   uint32_t bars;
   volatile int *abort_flag;
-  DeviceStatus *status;
-  int n, h;
   __device__ __forceinline__ uint32_t at(int b) const { return bars + 8 * b; }
 };
 
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                       DeviceStatus *status, int n, int h, uint32_t where) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 0) {
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
-        *abort_flag = 1;
-        report(status, GDN_ERR_TIMEOUT, (uint32_t)n, (uint32_t)h, where);
-        return false;
-      }
-    }
-  }
-}
-// Wait for the phase that completes for the `count`-th time (from 0).
+// Wait for the phase that completes for the `count`-th time (from 0).  A wait
+// that gives up leaves its number in the abort flag; the CTA reports it as it
+// ends.  Short, because every wait of every role is inline: the roles' code has
+// to fit the instruction cache together.
 __device__ __forceinline__ bool wait(const Waits &w, int b, uint32_t count) {
-  const uint32_t parity = count & 1u;
-  if (mbar_try_wait(w.at(b), parity)) return true;
-  return wait_slow(w.at(b), parity, w.abort_flag, w.status, w.n, w.h, 60u + (uint32_t)b);
+  const uint32_t bar = w.at(b), parity = count & 1u;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
+    if ((it & 63u) == 0 && (*w.abort_flag || it >= kWaitTries)) {
+      *w.abort_flag = 60 + b;
+      return false;
+    }
+  return true;
+}
+// The same for a whole warp that goes on together.
+__device__ __forceinline__ bool wait_all(const Waits &w, int b, uint32_t count) {
+  return __all_sync(0xffffffffu, wait(w, b, count));
+}
+
+// tcgen05.mma by the lane whose `leader` is set.  The whole warp comes here with
+// equal operands, so that they stay in uniform registers; issued from a branch
+// of one lane each product cost some 70 cycles of moves.
+__device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
+                                    uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ta(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
+// A warp's arrival, after the shared- or tensor-memory accesses of its lanes.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 __device__ __forceinline__ float power(float ld, float n) { return n == 0.f ? 1.f : expf(ld * n); }
@@ -142,7 +176,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   float *mal = lam + 136;                                   // lam^(128 - n)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::BAR + 8 * kBars);
   volatile uint32_t *tmem_at = reinterpret_cast<volatile uint32_t *>(smem + L::BAR + 8 * kBars + 8);
-  const Waits w{sb + L::BAR, abort_flag, p.status, n, h};
+  const Waits w{sb + L::BAR, abort_flag};
   const float ld = p.log_decay[h];
   for (int i = tid; i <= kC; i += kThreads) {
     const float x = power(ld, (float)i);
@@ -152,9 +186,9 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
-      const bool all = i == kPReady || i == kPReady + 1 || i == kClean || i == kVhReady ||
-                       i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
-      mbar_init(w.at(i), all ? 128 : 1);
+      const bool role = i == kPReady || i == kPReady + 1 || i == kVhReady || i == kVhReady + 1 ||
+                        i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
+      mbar_init(w.at(i), i == kClean ? 8 : role ? 4 : 1);  // one arrival per warp
     }
     fence_mbar_init();
   }
@@ -168,8 +202,68 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     return *reinterpret_cast<uint4 *>(smem + (addr - sb));
   };
 
+  // Steps from c3 on weigh with three terms, earlier ones with two: the third,
+  // 2^-17 of its row, reaches the returned state times lam^rest, rest the tokens
+  // that follow the tile; below lam^rest = 2^-5 that is less than fp32 holds.
+  int c3 = nc;
+  if (scan.s_out) {
+    const float reach = ld < 0.f ? 3.4657f / -ld : 1e9f;   // lam^reach = 2^-5
+    c3 = nc - 2 - (int)(fminf(reach, 1e9f) / kC);
+  }
+  // Half a row of V^ (columns 32 (t >> 6) .. + 31 of row j): w_j c_j as bf16
+  // terms.  A row past the end is zeros, whatever lies there.
+  auto weigh = [&](int c, int half, int t) -> bool {
+    const int e = rows_of(c), j = 64 * half + (t & 63), q0 = 4 * (t >> 6);
+    const uint32_t stage = sb + (c % L::STAGES) * L::STAGE, v = stage + L::V;
+    if (e < kC) {  // (one ragged tile per sequence)
+      if (j >= e) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          S4(swz<kTile>(v, j, 8 * (q0 + q))) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int u = 0; u < L::SUB; ++u)
+            S4(swz<kTile>(stage + L::B + u * kTile, j, 8 * (q0 + q))) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(w.at(kClean));
+    }
+    if (c > 0 && !wait(w, half ? kXFull : kXHalf, c - 1)) return false;  // V^ has been read
+    const float wj = j < e ? lam[rev ? j + 1 : e - 1 - j] : 0.f;
+    const bool three = c >= c3;
+#pragma unroll 2
+    for (int q = 0; q < 4; ++q) {
+      const uint4 x = S4(swz<kTile>(v, j, 8 * (q0 + q)));
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+      uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float lo = bf16_lo(xs[u]) * wj, hi = bf16_hi(xs[u]) * wj;
+        t1[u] = pack_bf16(lo, hi);
+        lo -= bf16_lo(t1[u]);
+        hi -= bf16_hi(t1[u]);
+        t2[u] = pack_bf16(lo, hi);
+        if (three) t3[u] = pack_bf16(lo - bf16_lo(t2[u]), hi - bf16_hi(t2[u]));
+      }
+      const uint32_t to = swz<kTile>(sb + L::VH, j, 8 * (q0 + q));
+      S4(to) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+      S4(to + kTile) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      if (three) S4(to + 2 * kTile) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+    }
+    fence_proxy_async_smem();
+    warp_arrive(w.at(kVhReady + half));
+    return true;
+  };
+
   if (warp < 4) {
     // ---- P' : lane l of warp w holds row 32 w + l; columns in blocks of 32 ----
+    float diag[32];   // lam^|i-j| of the diagonal block
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      const int d = rev ? x - lane : lane - x;
+      diag[x] = lam[d >= 0 ? d : 0];
+    }
+    const float r = rev ? lam[32 - lane] : lam[lane];
     for (int c = 0; c < nc; ++c) {
       const int b = c & 1;
       if (!wait(w, kPFull + b, c >> 1)) break;
@@ -185,33 +279,33 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
           uint32_t v[32];
           tmem_ld32(P + 32 * jb, v);
           tmem_wait_ld();
-          const int e = rows_of(c) - 32 * jb;  // columns past the end are zeros
+          uint32_t keep = ~0u;   // columns of the block that count
           if (jb == wq) {
+            keep = rev ? ~0u << lane : ~0u >> (31 - lane);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              float f[2];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int d = rev ? 2 * x + u - lane : lane - (2 * x + u);
-                f[u] = d >= 0 && 2 * x + u < e ? __uint_as_float(v[2 * x + u]) * lam[d >= 0 ? d : 0]
-                                                 : 0.f;
-              }
-              pk[x] = pack_bf16(f[0], f[1]);
-            }
+            for (int x = 0; x < 16; ++x)
+              pk[x] = pack_bf16(__uint_as_float(v[2 * x]) * diag[2 * x],
+                                __uint_as_float(v[2 * x + 1]) * diag[2 * x + 1]);
           } else {
             // lam^|i-j| as a power up to the row block's edge times one from
             // there (both exponents >= 0)
-            const float r = rev ? lam[32 - lane] : lam[lane];
             const float *col = rev ? lam + 32 * (jb - wq - 1) : mal + 128 - 32 * (wq - jb);
 #pragma unroll
             for (int x = 0; x < 16; x += 2) {
               const float4 f = *reinterpret_cast<const float4 *>(col + 2 * x);
-              const float y0 = __uint_as_float(v[2 * x]) * (r * f.x),
-                          y1 = __uint_as_float(v[2 * x + 1]) * (r * f.y),
-                          y2 = __uint_as_float(v[2 * x + 2]) * (r * f.z),
-                          y3 = __uint_as_float(v[2 * x + 3]) * (r * f.w);
-              pk[x] = pack_bf16(2 * x < e ? y0 : 0.f, 2 * x + 1 < e ? y1 : 0.f);
-              pk[x + 1] = pack_bf16(2 * x + 2 < e ? y2 : 0.f, 2 * x + 3 < e ? y3 : 0.f);
+              pk[x] = pack_bf16(__uint_as_float(v[2 * x]) * (r * f.x),
+                                __uint_as_float(v[2 * x + 1]) * (r * f.y));
+              pk[x + 1] = pack_bf16(__uint_as_float(v[2 * x + 2]) * (r * f.z),
+                                    __uint_as_float(v[2 * x + 3]) * (r * f.w));
+            }
+          }
+          const int e = rows_of(c) - 32 * jb;  // columns past the end do not
+          if (e < 32) keep &= e > 0 ? ~0u >> (32 - e) : 0u;
+          if (jb == wq || e < 32) {  // by selection: a product with 0 keeps a NaN
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              if (!(keep & (1u << (2 * x)))) pk[x] &= 0xffff0000u;
+              if (!(keep & (2u << (2 * x)))) pk[x] &= 0xffffu;
             }
           }
         }
@@ -219,7 +313,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(w.at(kPReady + b));
+      warp_arrive(w.at(kPReady + b));
     }
   } else if (warp < 8) {
     // ---- o : lane i holds row i ----
@@ -249,7 +343,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
               fmaf(f, __uint_as_float(x[2 * u + 1]), __uint_as_float(y[2 * u + 1])));
       }
       tc_fence_before();
-      mbar_arrive(w.at(kOFree));
+      warp_arrive(w.at(kOFree));
       if (e == kC) {
         if (DK == 64) {  // the last store has read the buffer
           if (lead) {
@@ -263,7 +357,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
           S4(swz<kTile>(so, i, 8 * q)) =
               make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
         fence_proxy_async_smem();
-        mbar_arrive(w.at(kOWritten));
+        warp_arrive(w.at(kOWritten));
         if (lead) {
           if (!wait(w, kOWritten, stores)) break;
           tma_store_3d(mo, col0, h, (int)tok, so);
@@ -283,63 +377,22 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
     }
     if (lead) bulk_wait_all();
-  } else if (warp < 12) {
-    // ---- V^ : thread j holds row j ----
-    const int j = tid - 256;
-    for (int c = 0; c < nc; ++c) {
-      const int s = c % L::STAGES, e = rows_of(c);
-      const uint32_t stage = sb + s * L::STAGE;
-      if (!wait(w, kFull + s, c / L::STAGES)) break;
-      if (e < kC) {
-        if (j >= e) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            S4(swz<kTile>(stage + L::V, j, 8 * q)) = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int u = 0; u < L::SUB; ++u)
-              S4(swz<kTile>(stage + L::B + u * kTile, j, 8 * q)) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(w.at(kClean));  // (one ragged tile per sequence)
-      }
-      if (c > 0 && !wait(w, kXFull, c - 1)) break;  // V^ has been read
-      const float wj = j < e ? lam[rev ? j + 1 : e - 1 - j] : 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint4 x = S4(swz<kTile>(stage + L::V, j, 8 * q));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-        uint32_t t[3][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float lo = bf16_lo(xs[u]) * wj, hi = bf16_hi(xs[u]) * wj;
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            t[k][u] = pack_bf16(lo, hi);
-            lo -= bf16_lo(t[k][u]);
-            hi -= bf16_hi(t[k][u]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          S4(swz<kTile>(sb + L::VH + k * kTile, j, 8 * q)) =
-              make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(w.at(kVhReady));
-    }
   } else if (warp < 16) {
-    // ---- S : DK 128: lane i holds row i, 64 columns; DK 64: X holds its rows
-    // twice, lanes 0-63 take columns 0-31 of them and lanes 64-127 the others ----
+    // ---- V^ of a chunk's first 64 tokens (warps 8-11), or of the others and S
+    // (warps 12-15; one loop, so that the code of V^ is there once) ----
+    const bool last = warp >= 12;
+    // S : DK 128: lane i holds row i, 64 columns; DK 64: X holds its rows
+    // twice, lanes 0-63 take columns 0-31 of them and lanes 64-127 the others
     constexpr int N = DK == 64 ? 32 : 64;
     const int i = (32 * wq + lane) & (DK - 1), c0 = DK == 64 ? 32 * (wq >> 1) : 0;
     float s[N];
 #pragma unroll
     for (int x = 0; x < N; ++x) s[x] = 0.f;
-    if (scan.s_in && scan.s_in_t) {
+    if (last && scan.s_in && scan.s_in_t) {
 #pragma unroll
-      for (int x = 0; x < N; ++x) s[x] = state_in(scan, unit, i, col0 + c0 + x);
-    } else if (scan.s_in) {
+      for (int x = 0; x < N; ++x)
+        s[x] = scan.s_in[unit * DK * dc + (int64_t)(col0 + c0 + x) * DK + i];
+    } else if (last && scan.s_in) {
       const float4 *row =
           reinterpret_cast<const float4 *>(scan.s_in + (unit * DK + i) * dc + col0 + c0);
 #pragma unroll
@@ -358,32 +411,35 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
             pack_bf16(s[8 * q], s[8 * q + 1]), pack_bf16(s[8 * q + 2], s[8 * q + 3]),
             pack_bf16(s[8 * q + 4], s[8 * q + 5]), pack_bf16(s[8 * q + 6], s[8 * q + 7]));
       fence_proxy_async_smem();
-      mbar_arrive(w.at(kSReady));
+      warp_arrive(w.at(kSReady));
     };
-    put();
+    if (last) put();
     int done = 0;
     for (int c = 0; c < nc; ++c) {
+      if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, last, tid & 127)) break;
+      if (!last) continue;
+      if (c > 0) {
+        if (!wait(w, kOFull, c - 1)) break;  // O1 has read the last state
+        put();
+      }
       if (!wait(w, kXFull, c)) break;
       tc_fence_after();
       const float le = lam[rows_of(c)];
 #pragma unroll
-      for (int q = 0; q < N / 16; ++q) {
-        uint32_t x[16];
-        tmem_ld16(tlane + kColX + c0 + 16 * q, x);
+      for (int q = 0; q < N / 8; ++q) {
+        uint32_t x[8], y[8];  // first (and third) term's sum; the second's
+        tmem_ld8(tlane + kColX + c0 + 8 * q, x);
+        tmem_ld8(tlane + kColX + 64 + c0 + 8 * q, y);
         tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
-          s[16 * q + u] = fmaf(le, s[16 * q + u], __uint_as_float(x[u]));
+        for (int u = 0; u < 8; ++u)
+          s[8 * q + u] = fmaf(le, s[8 * q + u], __uint_as_float(x[u]) + __uint_as_float(y[u]));
       }
       tc_fence_before();
-      mbar_arrive(w.at(kXRead));
+      warp_arrive(w.at(kXRead));
       ++done;
-      if (c + 1 < nc) {
-        if (!wait(w, kOFull, c)) break;  // O1 has read the last state
-        put();
-      }
     }
-    if (scan.s_out && done == nc) {
+    if (last && scan.s_out && done == nc) {
       float4 *row = reinterpret_cast<float4 *>(scan.s_out + (unit * DK + i) * dc + col0 + c0);
 #pragma unroll
       for (int x = 0; x < N / 4; ++x)
@@ -412,69 +468,101 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       for (int c = issued > L::STAGES ? issued - L::STAGES : 0; c < issued; ++c)
         mbar_wait_bounded(w.at(kFull + c % L::STAGES), (c / L::STAGES) & 1, kWaitTimeoutNs);
     }
-  } else if (lane == 0) {
-    // ---- MMA issue ----
+  } else {
+    // ---- MMA issue: the warp together, one lane elected ----
+    const uint32_t leader = elect();
+    int sp = 0, np = 0;   // stage and round of the next P's chunk
     auto issue_p = [&](int c) -> bool {
-      if (!wait(w, kFull + c % L::STAGES, c / L::STAGES)) return false;
-      if (rows_of(c) < kC && !wait(w, kClean, 0)) return false;
+      if (!wait_all(w, kFull + sp, np)) return false;
+      if (rows_of(c) < kC && !wait_all(w, kClean, 0)) return false;
       tc_fence_after();
-      const uint32_t stage = sb + (c % L::STAGES) * L::STAGE;
-#pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kTile + (kk & 3) * 32;
-        umma_bf16(tmem + kColP + 128 * (c & 1), umma_desc_sw128(stage + L::A + off),
-                  umma_desc_sw128(stage + L::B + off), umma_idesc_bf16(128, 128), kk > 0);
+      const uint32_t stage = sb + sp * L::STAGE;
+      const uint64_t da = umma_desc_sw128(stage + L::A), db = umma_desc_sw128(stage + L::B);
+#pragma unroll 1
+      for (int u = 0; u < L::SUB; ++u)
+#pragma unroll 1
+        for (int kk = 0; kk < 4; ++kk)
+          mma(leader, tmem + kColP + 128 * (c & 1), da + u * (kTile >> 4) + 2 * kk,
+              db + u * (kTile >> 4) + 2 * kk, umma_idesc_bf16(128, 128), u + kk > 0);
+      if (leader) umma_commit(w.at(kPFull + (c & 1)));
+      __syncwarp();
+      if (++sp == L::STAGES) {
+        sp = 0;
+        ++np;
       }
-      umma_commit(w.at(kPFull + (c & 1)));
       return true;
     };
     bool ok = issue_p(0);
+    int s = 0;
     for (int c = 0; ok && c < nc; ++c) {
-      const uint32_t stage = sb + (c % L::STAGES) * L::STAGE;
-      ok = wait(w, kVhReady, c) && (c == 0 || wait(w, kXRead, c - 1));
-      if (!ok) break;
-      tc_fence_after();
+      const uint32_t stage = sb + s * L::STAGE;
+      // X in two halves of 64 tokens; the first two terms side by side (N = 128:
+      // one read of B for both), the third onto the first
 #pragma unroll 1
-      for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          umma_bf16(tmem + kColX, umma_desc_sw128_mn(stage + L::B + kk * 2048, DK == 64 ? 0 : kTile),
-                    umma_desc_sw128_mn(sb + L::VH + k * kTile + kk * 2048, 8192),
-                    umma_idesc_bf16(128, 64, 1, 1), k + kk > 0);
-      umma_commit(w.at(kXFull));
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && wait_all(w, kVhReady + half, c) &&
+             (half > 0 || c == 0 || wait_all(w, kXRead, c - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t db = umma_desc_sw128_mn(stage + L::B + half * 8192, DK == 64 ? 0 : kTile),
+                       dv = umma_desc_sw128_mn(sb + L::VH + half * 8192, kTile);
+#pragma unroll 1
+        for (int kk = 0; kk < 4; ++kk)
+          mma(leader, tmem + kColX, db + 128 * kk, dv + 128 * kk, umma_idesc_bf16(128, 128, 1, 1),
+              half + kk > 0);
+        if (c >= c3) {
+#pragma unroll 1
+          for (int kk = 0; kk < 4; ++kk)
+            mma(leader, tmem + kColX, db + 128 * kk, dv + 2 * (kTile >> 4) + 128 * kk,
+                umma_idesc_bf16(128, 64, 1, 1), 1);
+        }
+        if (leader) umma_commit(w.at(half ? kXFull : kXHalf));
+        __syncwarp();
+      }
+      if (!ok) break;
       // the next chunk's P, now if its tiles are there, else after this chunk
       // (P' of the chunk before last has been read: its O2 is done)
-      ok = c == 0 || wait(w, kOFull, c - 1);
+      ok = c == 0 || wait_all(w, kOFull, c - 1);
       if (!ok) break;
-      const bool early = c + 1 < nc && mbar_test(w.at(kFull + (c + 1) % L::STAGES),
-                                                 ((c + 1) / L::STAGES) & 1);
+      const bool early =
+          c + 1 < nc && __all_sync(0xffffffffu, mbar_test(w.at(kFull + sp), np & 1));
       if (early && !(ok = issue_p(c + 1))) break;
-      ok = wait(w, kSReady, c) && (c == 0 || wait(w, kOFree, c - 1));
+      ok = wait_all(w, kSReady, c) && (c == 0 || wait_all(w, kOFree, c - 1));
       if (!ok) break;
       tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk)
-        umma_bf16(tmem + kColO1,
-                  umma_desc_sw128(stage + L::A + (kk >> 2) * kTile + (kk & 3) * 32),
-                  umma_desc_sw128_mn(sb + L::S + kk * 2048, 8192), umma_idesc_bf16(128, 64, 0, 1),
-                  kk > 0);
-      if (!(ok = wait(w, kPReady + (c & 1), c >> 1))) break;
+      const uint64_t da = umma_desc_sw128(stage + L::A), ds = umma_desc_sw128_mn(sb + L::S, 8192),
+                     dv = umma_desc_sw128_mn(stage + L::V, 8192);
+#pragma unroll 1
+      for (int u = 0; u < L::SUB; ++u)
+#pragma unroll 1
+        for (int kk = 0; kk < 4; ++kk)
+          mma(leader, tmem + kColO1, da + u * (kTile >> 4) + 2 * kk, ds + 512 * u + 128 * kk,
+              umma_idesc_bf16(128, 64, 0, 1), u + kk > 0);
+      if (!(ok = wait_all(w, kPReady + (c & 1), c >> 1))) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int kk = 0; kk < kC / 16; ++kk)
-        umma_bf16_ta(tmem + kColO2, tmem + kColP + 128 * (c & 1) + 8 * kk,
-                     umma_desc_sw128_mn(stage + L::V + kk * 2048, 8192),
-                     umma_idesc_bf16(128, 64, 0, 1), kk > 0);
-      umma_commit(w.at(kOFull));
-      if (DK == 64) umma_commit(w.at(kEmpty + c % L::STAGES));
+        mma_ta(leader, tmem + kColO2, tmem + kColP + 128 * (c & 1) + 8 * kk, dv + 128 * kk,
+               umma_idesc_bf16(128, 64, 0, 1), kk > 0);
+      if (leader) {
+        umma_commit(w.at(kOFull));
+        if (DK == 64) umma_commit(w.at(kEmpty + s));
+      }
+      __syncwarp();
       if (c + 1 < nc && !early) ok = issue_p(c + 1);
+      if (++s == L::STAGES) s = 0;
     }
     // products still in flight end before the CTA leaves
-    umma_commit(w.at(kLast));
-    mbar_wait_bounded(w.at(kLast), 0, kWaitTimeoutNs);
+    if (leader) {
+      umma_commit(w.at(kLast));
+      mbar_wait_bounded(w.at(kLast), 0, kWaitTimeoutNs);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag)
+    report(p.status, GDN_ERR_TIMEOUT, (uint32_t)n, (uint32_t)h, (uint32_t)*abort_flag);
   if (warp == 17) {
     __syncwarp();
     tc_fence_after();
