@@ -18,14 +18,14 @@
 // Rounding.  The state is a sum that runs over the whole sequence and is
 // returned in fp32, so X must be exact to fp32: b and c are bf16 already, and
 // V^ is split into three bf16 terms (8 + 8 + 8 bits of the 24 of w_j c_j), or
-// two where the third could not reach the returned state.  P'
-// and the S that O1 reads are rounded to bf16 once: each enters an output that
-// is itself rounded to bf16, so an output carries two such roundings in all.
+// two where the third could not reach the returned state.  P' and the S that O1
+// reads are rounded to bf16 once: each enters an output that is itself rounded
+// to bf16, so an output carries two such roundings in all.
 //
-// Roles (18 warps): P' (warps 0-3), o (4-7), V^ of the first 64 tokens (8-11),
-// of the others and S (12-15), TMA (16), MMA issue (17).  V^ and X go by halves,
-// so that one half is weighed while the other is multiplied.  Every wait is bounded; a timeout records GDN_ERR_TIMEOUT,
-// raises the abort flag and every role leaves its loop.
+// Roles (16 warps): P' (warps 0-3), S and o (4-7), V^ (8-11), TMA (12), and the
+// issue of X (13), of P (14), of O1 and O2 (15): none of the three waits for what
+// another needs.  V^ and X go by halves, so that one half is weighed while the
+// other is multiplied.  Every wait is bounded; a timeout records GDN_ERR_TIMEOUT.
 //
 // Rows past a sequence's end in its last tile may belong to a neighbour.  Their
 // b and c rows are overwritten with zeros before any product reads them as a
@@ -39,12 +39,11 @@ namespace lin {
 namespace {
 
 using namespace ptx;
-using tc::kWaitTimeoutNs;
 using tc::swz;
 
 constexpr int kC = 128;
 constexpr int kTile = kC * 128;   // [128][64] bf16
-constexpr int kThreads = 18 * 32;
+constexpr int kThreads = 16 * 32;   // 128 registers a thread: P' spilled with 20 warps
 constexpr uint32_t kWaitTries = 1u << 19;   // probes of 4 us each before a wait gives up (2 s)
 constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColX = 384, kCols = 512;
 
@@ -57,16 +56,17 @@ struct Lay {
   static constexpr int S = VH + 3 * kTile;                // [DK][64] bf16
   // the o tile: its own buffer, or (DK 128: no room) the A tile of its stage
   static constexpr int O = S + DK * 128;
-  static constexpr int TAB = O + (DK == 64 ? kTile : 0);  // lam^0 .. lam^128, then reversed
-  static constexpr int BAR = TAB + 272 * 4;
+  // 32 zeros, lam^0 .. lam^128 (at 32), lam^128 .. lam^0 (at 168), 31 zeros
+  static constexpr int TAB = O + (DK == 64 ? kTile : 0);
+  static constexpr int BAR = TAB + 328 * 4;
   static constexpr int BYTES = BAR + 256;
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
 // mbarriers
-enum Bar { kFull = 0, kEmpty = 3, kPFull = 6, kPReady = 8, kVhReady = 10, kXHalf = 12, kXFull,
-           kClean, kXRead, kSReady, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars };
+enum Bar { kFull = 0, kEmpty = 3, kPFull = 6, kPReady = 8, kVhReady = 10, kPFree = 12, kXHalf = 14, kXFull,
+           kClean, kXRead, kSReady, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars = kLast + 3 };
 
 struct TcArgs {
   Params p;
@@ -80,18 +80,28 @@ struct Waits {
   __device__ __forceinline__ uint32_t at(int b) const { return bars + 8 * b; }
 };
 
-// Wait for the phase that completes for the `count`-th time (from 0).  A wait
-// that gives up leaves its number in the abort flag; the CTA reports it as it
-// ends.  Short, because every wait of every role is inline: the roles' code has
-// to fit the instruction cache together.
+// Wait for the phase that completes for the `count`-th time (from 0), for at most
+// kWaitTries probes.  A wait that gives up leaves its number in the abort flag;
+// the CTA reports it as it ends, each role leaving its loop at its own next wait.
+// A handful of instructions: every wait of every role is inline, and the roles'
+// loops have to fit the instruction cache together.
 __device__ __forceinline__ bool wait(const Waits &w, int b, uint32_t count) {
-  const uint32_t bar = w.at(b), parity = count & 1u;
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it)
-    if ((it & 63u) == 0 && (*w.abort_flag || it >= kWaitTries)) {
-      *w.abort_flag = 60 + b;
-      return false;
-    }
-  return true;
+  uint32_t left;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mov.u32 %0, %3;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "sub.u32 %0, %0, 1;\n\t"
+      "setp.ne.u32 q, %0, 0;\n\t"
+      "@q bra AGAIN;\n"
+      "DONE:\n\t}"
+      : "=&r"(left)
+      : "r"(w.at(b)), "r"(count & 1u), "r"(kWaitTries)
+      : "memory");
+  if (left == 0) *w.abort_flag = 60 + b;
+  return left != 0;
 }
 // The same for a whole warp that goes on together.
 __device__ __forceinline__ bool wait_all(const Waits &w, int b, uint32_t count) {
@@ -127,6 +137,41 @@ __device__ __forceinline__ uint32_t elect() {
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(is));
   return is;
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  return pair(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+  return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) {
+  return *reinterpret_cast<const __nv_bfloat162 *>(&x);
+}
+__device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) {
+  return *reinterpret_cast<const uint32_t *>(&x);
 }
 
 // A warp's arrival, after the shared- or tensor-memory accesses of its lanes.
@@ -172,27 +217,29 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   auto tile_of = [&](int c) { return rev ? nc - 1 - c : c; };
   auto rows_of = [&](int c) { return tile_of(c) == nc - 1 ? e_last : kC; };
 
-  float *lam = reinterpret_cast<float *>(smem + L::TAB);    // lam^n, n = 0 .. 128
-  float *mal = lam + 136;                                   // lam^(128 - n)
+  float *lam = reinterpret_cast<float *>(smem + L::TAB) + 32;  // lam^n, n = 0 .. 128
+  float *mal = lam + 136;                                      // lam^(128 - n)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::BAR + 8 * kBars);
   volatile uint32_t *tmem_at = reinterpret_cast<volatile uint32_t *>(smem + L::BAR + 8 * kBars + 8);
   const Waits w{sb + L::BAR, abort_flag};
   const float ld = p.log_decay[h];
-  for (int i = tid; i <= kC; i += kThreads) {
-    const float x = power(ld, (float)i);
-    lam[i] = x;
-    mal[kC - i] = x;
+  for (int i = tid; i < 328; i += kThreads) {
+    const int up = i - 32, down = 32 + 136 + kC - i;
+    const int e = up >= 0 && up <= kC ? up : down >= 0 && down <= kC ? down : -1;
+    lam[up] = e < 0 ? 0.f : power(ld, (float)e);
   }
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
-      const bool role = i == kPReady || i == kPReady + 1 || i == kVhReady || i == kVhReady + 1 ||
-                        i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
-      mbar_init(w.at(i), i == kClean ? 8 : role ? 4 : 1);  // one arrival per warp
+      const bool role = i == kVhReady || i == kVhReady + 1 ||
+                        i == kClean || i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
+      // one arrival per warp; a stage is freed by both issuing warps (DK 128: one
+      // of them and the o warps)
+      mbar_init(w.at(i), i == kPReady || i == kPReady + 1 ? 8 : role ? 4 : i >= kEmpty && i < kPFull ? 2 : 1);
     }
     fence_mbar_init();
   }
-  if (warp == 17) tmem_alloc(sb + L::BAR + 8 * kBars + 8, kCols);
+  if (warp == 12) tmem_alloc(sb + L::BAR + 8 * kBars + 8, kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -212,150 +259,273 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   }
   // Half a row of V^ (columns 32 (t >> 6) .. + 31 of row j): w_j c_j as bf16
   // terms.  A row past the end is zeros, whatever lies there.
+  const float w_full[2] = {lam[rev ? (tid & 63) + 1 : kC - 1 - (tid & 63)],
+                           lam[rev ? (tid & 63) + 65 : 63 - (tid & 63)]};
   auto weigh = [&](int c, int half, int t) -> bool {
     const int e = rows_of(c), j = 64 * half + (t & 63), q0 = 4 * (t >> 6);
     const uint32_t stage = sb + (c % L::STAGES) * L::STAGE, v = stage + L::V;
-    if (e < kC) {  // (one ragged tile per sequence)
-      if (j >= e) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          S4(swz<kTile>(v, j, 8 * (q0 + q))) = make_uint4(0, 0, 0, 0);
+    if (e < kC && half == 0) {  // (one ragged tile per sequence)
+      if (t >= e) {
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          S4(swz<kTile>(v, t, 8 * q)) = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int u = 0; u < L::SUB; ++u)
-            S4(swz<kTile>(stage + L::B + u * kTile, j, 8 * (q0 + q))) = make_uint4(0, 0, 0, 0);
+            S4(swz<kTile>(stage + L::B + u * kTile, t, 8 * q)) = make_uint4(0, 0, 0, 0);
         }
       }
       fence_proxy_async_smem();
       warp_arrive(w.at(kClean));
     }
     if (c > 0 && !wait(w, half ? kXFull : kXHalf, c - 1)) return false;  // V^ has been read
-    const float wj = j < e ? lam[rev ? j + 1 : e - 1 - j] : 0.f;
-    const bool three = c >= c3;
-#pragma unroll 2
-    for (int q = 0; q < 4; ++q) {
-      const uint4 x = S4(swz<kTile>(v, j, 8 * (q0 + q)));
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-      uint32_t t1[4], t2[4], t3[4];
+    float wj = half ? w_full[1] : w_full[0];
+    if (e < kC) wj = j < e ? lam[rev ? j + 1 : e - 1 - j] : 0.f;
+    const uint32_t to = sb + L::VH;
+    if (c < c3) {
+      // two terms on bf16 pairs: with w = wa + wb (8 bits each), t1 = c wa rounded
+      // and its remainder c wa - t1 are exact together, t2 = c wb + remainder
+      const __nv_bfloat162 wa = __float2bfloat162_rn(wj),
+                           wb = __float2bfloat162_rn(wj - __low2float(wa));
+      uint4 x[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float lo = bf16_lo(xs[u]) * wj, hi = bf16_hi(xs[u]) * wj;
-        t1[u] = pack_bf16(lo, hi);
-        lo -= bf16_lo(t1[u]);
-        hi -= bf16_hi(t1[u]);
-        t2[u] = pack_bf16(lo, hi);
-        if (three) t3[u] = pack_bf16(lo - bf16_lo(t2[u]), hi - bf16_hi(t2[u]));
+      for (int q = 0; q < 4; ++q)
+        x[q] = j < e ? S4(swz<kTile>(v, j, 8 * (q0 + q))) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t xs[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
+        uint32_t t1[4], t2[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 y = as_bf162(xs[u]), m = __hmul2_rn(y, wa);
+          t1[u] = bits(m);
+          t2[u] = bits(__hfma2(y, wb, __hfma2(y, wa, __hneg2(m))));
+        }
+        S4(swz<kTile>(to, j, 8 * (q0 + q))) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        S4(swz<kTile>(to, j, 8 * (q0 + q)) + kTile) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
       }
-      const uint32_t to = swz<kTile>(sb + L::VH, j, 8 * (q0 + q));
-      S4(to) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-      S4(to + kTile) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-      if (three) S4(to + 2 * kTile) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const uint4 x = j < e ? S4(swz<kTile>(v, j, 8 * (q0 + q))) : make_uint4(0, 0, 0, 0);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float lo = bf16_lo(xs[u]) * wj, hi = bf16_hi(xs[u]) * wj;
+          t1[u] = pack_bf16(lo, hi);
+          lo -= bf16_lo(t1[u]);
+          hi -= bf16_hi(t1[u]);
+          t2[u] = pack_bf16(lo, hi);
+          t3[u] = pack_bf16(lo - bf16_lo(t2[u]), hi - bf16_hi(t2[u]));
+        }
+        const uint32_t at = swz<kTile>(to, j, 8 * (q0 + q));
+        S4(at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        S4(at + kTile) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        S4(at + 2 * kTile) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+      }
     }
     fence_proxy_async_smem();
     warp_arrive(w.at(kVhReady + half));
     return true;
   };
 
-  if (warp < 4) {
-    // ---- P' : lane l of warp w holds row 32 w + l; columns in blocks of 32 ----
-    float diag[32];   // lam^|i-j| of the diagonal block
+  // P' : lane l of a group's warp w holds row i = 32 w + l; columns in units of 16
+  // from the diagonal outwards (k = 0, 1: the diagonal block), the next one on its
+  // way while one is weighed.  At a distance of d units from the row's own,
+  // lam^|i-j| = (lam^|i - edge| lam^(16 (d-1))) lam^|edge - j| with the edge
+  // between them, so 16 powers of the column, 16 of the triangle (d = 0) and a
+  // running scalar serve them all, from registers.  A unit of P' (two columns a
+  // word) goes over the first half of its own P.  The last rows have eight units,
+  // the first two, and only one warp of a group reaches their lanes: so units 0 to
+  // 3 are the P' warps' and the others the V^ warps'.
+  const int l16 = lane & 15, far0 = 4;
+  const int units = rev ? 8 - 2 * wq : 2 * wq + 2;
+  const uint32_t half16 = lane >> 4;
+  auto unit_at = [&](int k) { return rev ? 2 * wq + k : 2 * wq + 1 - k; };
+  auto drop = [&](uint32_t (&pk)[8], uint32_t keep) {
+    // columns that do not count, by selection: a product with 0 keeps a NaN
 #pragma unroll
-    for (int x = 0; x < 32; ++x) {
-      const int d = rev ? x - lane : lane - x;
-      diag[x] = lam[d >= 0 ? d : 0];
+    for (int x = 0; x < 8; ++x) {
+      if (!(keep & (1u << (2 * x)))) pk[x] &= 0xffff0000u;
+      if (!(keep & (2u << (2 * x)))) pk[x] &= 0xffffu;
     }
-    const float r = rev ? lam[32 - lane] : lam[lane];
+  };
+  auto ragged = [&](int e, int u) { return e > 16 * u ? 0xffffu >> (16 * u + 16 - e) : 0u; };
+  auto far_unit = [&](uint32_t P, int k, int e, float &sd, const uint64_t (&g)[8],
+                      const uint32_t (&v)[16]) {
+    const int u = unit_at(k);
+    uint32_t pk[8];
+    const uint64_t s2 = pair(sd, sd);
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      pk[x] = pack_pair(mul2(pair(v[2 * x], v[2 * x + 1]), mul2(s2, g[x])));
+    if (e < 16 * u + 16) drop(pk, ragged(e, u));
+    tmem_st8(P + 16 * u, pk);
+    sd *= lam[16];
+  };
+  // units k0 .. k1 - 1 (an even number), all beyond the diagonal block
+  auto far_units = [&](uint32_t P, int k0, int k1, int e, float sd, const uint64_t (&g)[8]) {
+    uint32_t va[16], vb[16];
+    tmem_ld16(P + 16 * unit_at(k0), va);
+#pragma unroll 1
+    for (int k = k0; k < k1; k += 2) {
+      tmem_wait_ld();
+      tmem_ld16(P + 16 * unit_at(k + 1), vb);
+      far_unit(P, k, e, sd, g, va);
+      tmem_wait_ld();
+      if (k + 2 < k1) tmem_ld16(P + 16 * unit_at(k + 2), va);
+      far_unit(P, k + 1, e, sd, g, vb);
+    }
+  };
+  uint64_t g[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    g[x] = rev ? pair(lam[2 * x], lam[2 * x + 1]) : pair(lam[16 - 2 * x], lam[15 - 2 * x]);
+  // the running scalar of unit k of this lane (k >= 2)
+  auto scalar_at = [&](int k) {
+    const int d = k - (int)(rev ? half16 : 1 - half16);
+    return lam[(rev ? 16 - l16 : l16) + 16 * (d - 1)];
+  };
+
+  if (warp < 4) {
+    // ---- P', the units next to the diagonal ----
+    uint64_t tri[8];   // (the table's zeros on the far side; they are not kept)
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      tri[x] = rev ? pair(lam[2 * x - l16], lam[2 * x + 1 - l16])
+                   : pair(mal[kC + 2 * x - l16], mal[kC + 2 * x + 1 - l16]);
+    const uint32_t tri_keep = rev ? 0xffffu << l16 : 0xffffu >> (15 - l16);
+    const float s_far = units > 2 ? scalar_at(2) : 0.f, s_near = lam[rev ? 16 - l16 : l16];
+    const bool mine = rev ? half16 == 0 : half16 == 1;   // k = 0 holds this lane's triangle
     for (int c = 0; c < nc; ++c) {
-      const int b = c & 1;
+      const int b = c & 1, e = rows_of(c);
       if (!wait(w, kPFull + b, c >> 1)) break;
       tc_fence_after();
       const uint32_t P = tlane + kColP + 128 * b;
-#pragma unroll 1
-      for (int jb = 0; jb < 4; ++jb) {
-        uint32_t pk[16];
-        if (rev ? jb < wq : jb > wq) {
+      uint32_t va[16], vb[16], pk[8];
+      tmem_ld16(P + 16 * unit_at(0), va);
+      tmem_ld16(P + 16 * unit_at(1), vb);
+      tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) pk[x] = 0;
-        } else {
-          uint32_t v[32];
-          tmem_ld32(P + 32 * jb, v);
-          tmem_wait_ld();
-          uint32_t keep = ~0u;   // columns of the block that count
-          if (jb == wq) {
-            keep = rev ? ~0u << lane : ~0u >> (31 - lane);
+      for (int x = 0; x < 8; ++x) pk[x] = pack_pair(mul2(pair(va[2 * x], va[2 * x + 1]), tri[x]));
+      drop(pk, (mine ? tri_keep : 0u) & (e < 16 * unit_at(0) + 16 ? ragged(e, unit_at(0)) : ~0u));
+      tmem_st8(P + 16 * unit_at(0), pk);
+      const uint64_t s2 = pair(s_near, s_near);
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              pk[x] = pack_bf16(__uint_as_float(v[2 * x]) * diag[2 * x],
-                                __uint_as_float(v[2 * x + 1]) * diag[2 * x + 1]);
-          } else {
-            // lam^|i-j| as a power up to the row block's edge times one from
-            // there (both exponents >= 0)
-            const float *col = rev ? lam + 32 * (jb - wq - 1) : mal + 128 - 32 * (wq - jb);
-#pragma unroll
-            for (int x = 0; x < 16; x += 2) {
-              const float4 f = *reinterpret_cast<const float4 *>(col + 2 * x);
-              pk[x] = pack_bf16(__uint_as_float(v[2 * x]) * (r * f.x),
-                                __uint_as_float(v[2 * x + 1]) * (r * f.y));
-              pk[x + 1] = pack_bf16(__uint_as_float(v[2 * x + 2]) * (r * f.z),
-                                    __uint_as_float(v[2 * x + 3]) * (r * f.w));
-            }
-          }
-          const int e = rows_of(c) - 32 * jb;  // columns past the end do not
-          if (e < 32) keep &= e > 0 ? ~0u >> (32 - e) : 0u;
-          if (jb == wq || e < 32) {  // by selection: a product with 0 keeps a NaN
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              if (!(keep & (1u << (2 * x)))) pk[x] &= 0xffff0000u;
-              if (!(keep & (2u << (2 * x)))) pk[x] &= 0xffffu;
-            }
-          }
-        }
-        tmem_st16(P + 16 * jb, pk);
+      for (int x = 0; x < 8; ++x) {
+        const uint64_t wt = mul2(s2, g[x]);
+        pk[x] = pack_pair(mul2(pair(vb[2 * x], vb[2 * x + 1]), mine ? wt : tri[x]));
       }
+      drop(pk, (mine ? 0xffffu : tri_keep) & (e < 16 * unit_at(1) + 16 ? ragged(e, unit_at(1)) : ~0u));
+      tmem_st8(P + 16 * unit_at(1), pk);
+      if (units > 2) far_units(P, 2, units < far0 ? units : far0, e, s_far, g);
+      const uint32_t zero[8] = {};
+#pragma unroll 1
+      for (int u = rev ? 0 : 2 * wq + 2; u < (rev ? 2 * wq : 8); ++u) tmem_st8(P + 16 * u, zero);
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(w.at(kPReady + b));
     }
   } else if (warp < 8) {
-    // ---- o : lane i holds row i ----
+    // ---- S and o ----
+    // DK 128: lane i holds row i of S, 64 columns; DK 64: X holds its rows
+    // twice, lanes 0-63 take columns 0-31 of them and lanes 64-127 the others
+    constexpr int N = DK == 64 ? 32 : 64;
+    const int si = (32 * wq + lane) & (DK - 1), c0 = DK == 64 ? 32 * (wq >> 1) : 0;
+    uint64_t s[N / 2];   // pairs of columns
+#pragma unroll
+    for (int x = 0; x < N / 2; ++x) s[x] = 0;
+    if (scan.s_in && scan.s_in_t) {
+      const float *at = scan.s_in + unit * DK * dc + (int64_t)(col0 + c0) * DK + si;
+#pragma unroll
+      for (int x = 0; x < N / 2; ++x) s[x] = pair(at[2 * x * DK], at[(2 * x + 1) * DK]);
+    } else if (scan.s_in) {
+      const float4 *row =
+          reinterpret_cast<const float4 *>(scan.s_in + (unit * DK + si) * dc + col0 + c0);
+#pragma unroll
+      for (int x = 0; x < N / 4; ++x) {
+        const float4 y = row[x];
+        s[2 * x] = pair(y.x, y.y);
+        s[2 * x + 1] = pair(y.z, y.w);
+      }
+    }
+    auto put = [&]() {
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q)
+        S4(swz<kTile>(sb + L::S, si, c0 + 8 * q)) =
+            make_uint4(pack_pair(s[4 * q]), pack_pair(s[4 * q + 1]), pack_pair(s[4 * q + 2]),
+                       pack_pair(s[4 * q + 3]));
+      fence_proxy_async_smem();
+      warp_arrive(w.at(kSReady));
+    };
+    put();
+    const float lam_c = lam[kC];
+    // o : lane i holds row i
     const int i = 32 * wq + lane;
     const bool lead = warp == 4 && lane == 0;
     const CUtensorMap *mo = &args.map[sc][3];
+    const float f_full = lam[rev ? kC - 1 - i : i + 1];
     int stores = 0;  // whole tiles so far
+    int done = 0;
     for (int c = 0; c < nc; ++c) {
-      if (!wait(w, kOFull, c)) break;
-      tc_fence_after();
       const int e = rows_of(c);
+      if (!wait(w, kXFull, c)) break;
+      tc_fence_after();
+      const float le = e == kC ? lam_c : lam[e];
+#pragma unroll
+      for (int q = 0; q < N / 8; ++q) {
+        uint32_t x[8], y[8];  // first (and third) term's sum; the second's
+        tmem_ld8(tlane + kColX + c0 + 8 * q, x);
+        tmem_ld8(tlane + kColX + 64 + c0 + 8 * q, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          s[4 * q + u] = fma2(pair(le, le), s[4 * q + u],
+                              add2(pair(x[2 * u], x[2 * u + 1]), pair(y[2 * u], y[2 * u + 1])));
+      }
+      tc_fence_before();
+      warp_arrive(w.at(kXRead));
       const int64_t tok = start + (int64_t)tile_of(c) * kC;
       const uint32_t stage = sb + (c % L::STAGES) * L::STAGE;
       const uint32_t so = DK == 64 ? sb + L::O : stage + L::A;
-      const float f = i < e ? lam[rev ? e - 1 - i : i + 1] : 0.f;
-      uint32_t out[32];
+      float f = f_full;
+      if (e < kC) f = i < e ? lam[rev ? e - 1 - i : i + 1] : 0.f;
+      if (DK == 64 && e == kC) {  // the last store has read the buffer
+        if (lead) {
+          bulk_wait_read<0>();
+          mbar_arrive(w.at(kOBuf));
+        }
+        if (!wait(w, kOBuf, stores)) break;
+      }
+      if (!wait(w, kOFull, c)) break;
+      tc_fence_after();
+      if (c + 1 < nc) put();   // O1 has read the last state
+      ++done;
+      uint4 *row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(scan.o) +
+                                             ((tok + i) * H + h) * dc + col0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t x[16], y[16];
+        uint32_t x[16], y[16], out[8];
         tmem_ld16(tlane + kColO1 + 16 * q, x);
         tmem_ld16(tlane + kColO2 + 16 * q, y);
         tmem_wait_ld();
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          out[8 * q + u] = pack_bf16(
-              fmaf(f, __uint_as_float(x[2 * u]), __uint_as_float(y[2 * u])),
-              fmaf(f, __uint_as_float(x[2 * u + 1]), __uint_as_float(y[2 * u + 1])));
+          out[u] = pack_pair(fma2(pair(f, f), pair(x[2 * u], x[2 * u + 1]),
+                                  pair(y[2 * u], y[2 * u + 1])));
+        const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]),
+                    hi = make_uint4(out[4], out[5], out[6], out[7]);
+        if (e == kC) {
+          S4(swz<kTile>(so, i, 16 * q)) = lo;
+          S4(swz<kTile>(so, i, 16 * q + 8)) = hi;
+        } else if (i < e) {
+          row[2 * q] = lo;
+          row[2 * q + 1] = hi;
+        }
       }
       tc_fence_before();
       warp_arrive(w.at(kOFree));
       if (e == kC) {
-        if (DK == 64) {  // the last store has read the buffer
-          if (lead) {
-            bulk_wait_read<0>();
-            mbar_arrive(w.at(kOBuf));
-          }
-          if (!wait(w, kOBuf, stores)) break;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          S4(swz<kTile>(so, i, 8 * q)) =
-              make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
         fence_proxy_async_smem();
         warp_arrive(w.at(kOWritten));
         if (lead) {
@@ -364,12 +534,6 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
           bulk_commit();
         }
         ++stores;
-      } else if (i < e) {
-        uint4 *row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(scan.o) +
-                                               ((tok + i) * H + h) * dc + col0);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          row[q] = make_uint4(out[4 * q], out[4 * q + 1], out[4 * q + 2], out[4 * q + 3]);
       }
       if (DK == 128 && lead) {
         bulk_wait_read<0>();
@@ -377,82 +541,35 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
     }
     if (lead) bulk_wait_all();
-  } else if (warp < 16) {
-    // ---- V^ of a chunk's first 64 tokens (warps 8-11), or of the others and S
-    // (warps 12-15; one loop, so that the code of V^ is there once) ----
-    const bool last = warp >= 12;
-    // S : DK 128: lane i holds row i, 64 columns; DK 64: X holds its rows
-    // twice, lanes 0-63 take columns 0-31 of them and lanes 64-127 the others
-    constexpr int N = DK == 64 ? 32 : 64;
-    const int i = (32 * wq + lane) & (DK - 1), c0 = DK == 64 ? 32 * (wq >> 1) : 0;
-    float s[N];
+    if (scan.s_out && done == nc) {
+      ulonglong2 *row =
+          reinterpret_cast<ulonglong2 *>(scan.s_out + (unit * DK + si) * dc + col0 + c0);
 #pragma unroll
-    for (int x = 0; x < N; ++x) s[x] = 0.f;
-    if (last && scan.s_in && scan.s_in_t) {
-#pragma unroll
-      for (int x = 0; x < N; ++x)
-        s[x] = scan.s_in[unit * DK * dc + (int64_t)(col0 + c0 + x) * DK + i];
-    } else if (last && scan.s_in) {
-      const float4 *row =
-          reinterpret_cast<const float4 *>(scan.s_in + (unit * DK + i) * dc + col0 + c0);
-#pragma unroll
-      for (int x = 0; x < N / 4; ++x) {
-        const float4 y = row[x];
-        s[4 * x] = y.x;
-        s[4 * x + 1] = y.y;
-        s[4 * x + 2] = y.z;
-        s[4 * x + 3] = y.w;
-      }
+      for (int x = 0; x < N / 4; ++x) row[x] = make_ulonglong2(s[2 * x], s[2 * x + 1]);
     }
-    auto put = [&]() {
-#pragma unroll
-      for (int q = 0; q < N / 8; ++q)
-        S4(swz<kTile>(sb + L::S, i, c0 + 8 * q)) = make_uint4(
-            pack_bf16(s[8 * q], s[8 * q + 1]), pack_bf16(s[8 * q + 2], s[8 * q + 3]),
-            pack_bf16(s[8 * q + 4], s[8 * q + 5]), pack_bf16(s[8 * q + 6], s[8 * q + 7]));
-      fence_proxy_async_smem();
-      warp_arrive(w.at(kSReady));
-    };
-    if (last) put();
-    int done = 0;
+  } else if (warp < 12) {
+    // ---- V^, then the far units of P' ----
+    const float s_far = units > far0 ? scalar_at(far0) : 0.f;
     for (int c = 0; c < nc; ++c) {
-      if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, last, tid & 127)) break;
-      if (!last) continue;
-      if (c > 0) {
-        if (!wait(w, kOFull, c - 1)) break;  // O1 has read the last state
-        put();
+      if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, 0, tid & 127) ||
+          !weigh(c, 1, tid & 127))
+        break;
+      if (units > far0) {
+        if (!wait(w, kPFull + (c & 1), c >> 1)) break;
+        tc_fence_after();
+        far_units(tlane + kColP + 128 * (c & 1), far0, units, rows_of(c), s_far, g);
+        tmem_wait_st();
+        tc_fence_before();
       }
-      if (!wait(w, kXFull, c)) break;
-      tc_fence_after();
-      const float le = lam[rows_of(c)];
-#pragma unroll
-      for (int q = 0; q < N / 8; ++q) {
-        uint32_t x[8], y[8];  // first (and third) term's sum; the second's
-        tmem_ld8(tlane + kColX + c0 + 8 * q, x);
-        tmem_ld8(tlane + kColX + 64 + c0 + 8 * q, y);
-        tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          s[8 * q + u] = fmaf(le, s[8 * q + u], __uint_as_float(x[u]) + __uint_as_float(y[u]));
-      }
-      tc_fence_before();
-      warp_arrive(w.at(kXRead));
-      ++done;
+      warp_arrive(w.at(kPReady + (c & 1)));
     }
-    if (last && scan.s_out && done == nc) {
-      float4 *row = reinterpret_cast<float4 *>(scan.s_out + (unit * DK + i) * dc + col0 + c0);
-#pragma unroll
-      for (int x = 0; x < N / 4; ++x)
-        row[x] = make_float4(s[4 * x], s[4 * x + 1], s[4 * x + 2], s[4 * x + 3]);
-    }
-  } else if (warp == 16) {
+  } else if (warp == 12) {
     // ---- TMA ----
     if (lane == 0) {
       int issued = 0;
       for (int c = 0; c < nc; ++c) {
         const int s = c % L::STAGES;
         if (c >= L::STAGES && !wait(w, kEmpty + s, c / L::STAGES - 1)) break;
-        if (*abort_flag) break;
         const int tok = (int)(start + (int64_t)tile_of(c) * kC);
         const uint32_t stage = sb + s * L::STAGE, full = w.at(kFull + s);
         mbar_arrive_expect_tx(full, L::STAGE);
@@ -466,33 +583,12 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       // loads still in flight land before the CTA leaves
       for (int c = issued > L::STAGES ? issued - L::STAGES : 0; c < issued; ++c)
-        mbar_wait_bounded(w.at(kFull + c % L::STAGES), (c / L::STAGES) & 1, kWaitTimeoutNs);
+        wait(w, kFull + c % L::STAGES, c / L::STAGES);
     }
-  } else {
-    // ---- MMA issue: the warp together, one lane elected ----
+  } else if (warp == 13) {
+    // ---- issue of X: the warp together, one lane elected ----
     const uint32_t leader = elect();
-    int sp = 0, np = 0;   // stage and round of the next P's chunk
-    auto issue_p = [&](int c) -> bool {
-      if (!wait_all(w, kFull + sp, np)) return false;
-      if (rows_of(c) < kC && !wait_all(w, kClean, 0)) return false;
-      tc_fence_after();
-      const uint32_t stage = sb + sp * L::STAGE;
-      const uint64_t da = umma_desc_sw128(stage + L::A), db = umma_desc_sw128(stage + L::B);
-#pragma unroll 1
-      for (int u = 0; u < L::SUB; ++u)
-#pragma unroll 1
-        for (int kk = 0; kk < 4; ++kk)
-          mma(leader, tmem + kColP + 128 * (c & 1), da + u * (kTile >> 4) + 2 * kk,
-              db + u * (kTile >> 4) + 2 * kk, umma_idesc_bf16(128, 128), u + kk > 0);
-      if (leader) umma_commit(w.at(kPFull + (c & 1)));
-      __syncwarp();
-      if (++sp == L::STAGES) {
-        sp = 0;
-        ++np;
-      }
-      return true;
-    };
-    bool ok = issue_p(0);
+    bool ok = true;
     int s = 0;
     for (int c = 0; ok && c < nc; ++c) {
       const uint32_t stage = sb + s * L::STAGE;
@@ -504,31 +600,69 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
              (half > 0 || c == 0 || wait_all(w, kXRead, c - 1));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t db = umma_desc_sw128_mn(stage + L::B + half * 8192, DK == 64 ? 0 : kTile),
+        const uint64_t dx = umma_desc_sw128_mn(stage + L::B + half * 8192, DK == 64 ? 0 : kTile),
                        dv = umma_desc_sw128_mn(sb + L::VH + half * 8192, kTile);
 #pragma unroll 1
         for (int kk = 0; kk < 4; ++kk)
-          mma(leader, tmem + kColX, db + 128 * kk, dv + 128 * kk, umma_idesc_bf16(128, 128, 1, 1),
+          mma(leader, tmem + kColX, dx + 128 * kk, dv + 128 * kk, umma_idesc_bf16(128, 128, 1, 1),
               half + kk > 0);
         if (c >= c3) {
 #pragma unroll 1
           for (int kk = 0; kk < 4; ++kk)
-            mma(leader, tmem + kColX, db + 128 * kk, dv + 2 * (kTile >> 4) + 128 * kk,
+            mma(leader, tmem + kColX, dx + 128 * kk, dv + 2 * (kTile >> 4) + 128 * kk,
                 umma_idesc_bf16(128, 64, 1, 1), 1);
         }
-        if (leader) umma_commit(w.at(half ? kXFull : kXHalf));
+        if (leader) {
+          umma_commit(w.at(half ? kXFull : kXHalf));
+          if (half) umma_commit(w.at(kEmpty + s));
+        }
         __syncwarp();
       }
-      if (!ok) break;
-      // the next chunk's P, now if its tiles are there, else after this chunk
-      // (P' of the chunk before last has been read: its O2 is done)
-      ok = c == 0 || wait_all(w, kOFull, c - 1);
-      if (!ok) break;
-      const bool early =
-          c + 1 < nc && __all_sync(0xffffffffu, mbar_test(w.at(kFull + sp), np & 1));
-      if (early && !(ok = issue_p(c + 1))) break;
-      ok = wait_all(w, kSReady, c) && (c == 0 || wait_all(w, kOFree, c - 1));
-      if (!ok) break;
+      if (++s == L::STAGES) s = 0;
+    }
+    // products still in flight end before the CTA leaves
+    if (leader) {
+      umma_commit(w.at(kLast));
+      wait(w, kLast, 0);
+    }
+    __syncwarp();
+  } else if (warp == 14) {
+    // ---- issue of P ----
+    const uint32_t leader = elect();
+    int s = 0;
+    for (int c = 0; c < nc; ++c) {
+      const uint32_t stage = sb + s * L::STAGE;
+      // the P buffer is free once O2 of the chunk before last has read it
+      if (!wait_all(w, kFull + s, c / L::STAGES) ||
+          (c >= 2 && !wait_all(w, kPFree + (c & 1), (c >> 1) - 1)) ||
+          (rows_of(c) < kC && !wait_all(w, kClean, 0)))
+        break;
+      tc_fence_after();
+      const uint64_t da = umma_desc_sw128(stage + L::A), db = umma_desc_sw128(stage + L::B);
+#pragma unroll 1
+      for (int u = 0; u < L::SUB; ++u)
+#pragma unroll 1
+        for (int kk = 0; kk < 4; ++kk)
+          mma(leader, tmem + kColP + 128 * (c & 1), da + u * (kTile >> 4) + 2 * kk,
+              db + u * (kTile >> 4) + 2 * kk, umma_idesc_bf16(128, 128), u + kk > 0);
+      if (leader) umma_commit(w.at(kPFull + (c & 1)));
+      __syncwarp();
+      if (++s == L::STAGES) s = 0;
+    }
+    if (leader) {
+      umma_commit(w.at(kLast + 2));
+      wait(w, kLast + 2, 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- issue of O1 and O2 ----
+    const uint32_t leader = elect();
+    int s = 0;
+    for (int c = 0; c < nc; ++c) {
+      const uint32_t stage = sb + s * L::STAGE;
+      if (!wait_all(w, kSReady, c) || (c > 0 && !wait_all(w, kOFree, c - 1)) ||
+          !wait_all(w, kFull + s, c / L::STAGES))
+        break;
       tc_fence_after();
       const uint64_t da = umma_desc_sw128(stage + L::A), ds = umma_desc_sw128_mn(sb + L::S, 8192),
                      dv = umma_desc_sw128_mn(stage + L::V, 8192);
@@ -538,24 +672,24 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int kk = 0; kk < 4; ++kk)
           mma(leader, tmem + kColO1, da + u * (kTile >> 4) + 2 * kk, ds + 512 * u + 128 * kk,
               umma_idesc_bf16(128, 64, 0, 1), u + kk > 0);
-      if (!(ok = wait_all(w, kPReady + (c & 1), c >> 1))) break;
+      if (!wait_all(w, kPReady + (c & 1), c >> 1)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int kk = 0; kk < kC / 16; ++kk)
-        mma_ta(leader, tmem + kColO2, tmem + kColP + 128 * (c & 1) + 8 * kk, dv + 128 * kk,
+        mma_ta(leader, tmem + kColO2, tmem + kColP + 128 * (c & 1) + 16 * kk,
+               dv + 128 * kk,
                umma_idesc_bf16(128, 64, 0, 1), kk > 0);
       if (leader) {
         umma_commit(w.at(kOFull));
+        umma_commit(w.at(kPFree + (c & 1)));
         if (DK == 64) umma_commit(w.at(kEmpty + s));
       }
       __syncwarp();
-      if (c + 1 < nc && !early) ok = issue_p(c + 1);
       if (++s == L::STAGES) s = 0;
     }
-    // products still in flight end before the CTA leaves
     if (leader) {
-      umma_commit(w.at(kLast));
-      mbar_wait_bounded(w.at(kLast), 0, kWaitTimeoutNs);
+      umma_commit(w.at(kLast + 1));
+      wait(w, kLast + 1, 0);
     }
     __syncwarp();
   }
@@ -563,7 +697,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   __syncthreads();
   if (tid == 0 && *abort_flag)
     report(p.status, GDN_ERR_TIMEOUT, (uint32_t)n, (uint32_t)h, (uint32_t)*abort_flag);
-  if (warp == 17) {
+  if (warp == 12) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, kCols);
