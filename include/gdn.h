@@ -576,9 +576,14 @@ gdn_status gdn_bwd(const void *q, const void *k, const void *v, const float *g,
  * Supported sizes: head_dim_k and head_dim_v multiples of 32 in [32, 256];
  * num_seqs <= 16384; num_heads <= 65535.  flags: GDN_FORCE_SIMT (the fp32
  * CUDA-core kernel for bf16 storage too) or 0.  Empty sequences and seq_len =
- * 0 are legal (states pass through).  Aliasing, workspace (at least
- * gdn_lin_workspace_size(...) bytes; the first 256 are the status word, zeroed
- * once with gdn_workspace_init) and errors as gdn_fwd.
+ * 0 are legal (states pass through).  Aliasing and errors as gdn_fwd.
+ *
+ * workspace: the first 256 bytes are the status word (zeroed once with
+ * gdn_workspace_init); fewer bytes return GDN_ERR_WORKSPACE.  The bytes after it,
+ * of any contents, hold the state increments of segments when few long sequences are
+ * cut along time to fill the GPU.  gdn_lin_workspace_size(...) is enough for any call
+ * of these sizes; with less the sequences may run uncut, with the same results
+ * up to rounding.  Calls sharing a workspace are ordered (same stream).
  */
 size_t gdn_lin_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_heads,
                               int32_t head_dim_k, int32_t head_dim_v, uint32_t flags);
@@ -607,7 +612,7 @@ gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float 
  *
  * The gradients of q, k and v have the storage dtype of q, k and v (sums are
  * fp32, one rounding at the end); every one is written once, so results are
- * bitwise reproducible.  Sizes, flags, workspace (the same size) and errors as
+ * bitwise reproducible.  Sizes, flags, workspace and errors as
  * gdn_lin_fwd; no output may overlap an input or another output.
  */
 gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float *log_decay,

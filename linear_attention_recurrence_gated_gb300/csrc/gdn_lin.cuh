@@ -49,6 +49,24 @@ struct Params {
   DeviceStatus *status;
   int64_t seq_len;     // tokens of a batch row, or of all packed sequences
   int32_t num_heads, num_seqs, num_scans;
+  // Split along time (seg_len 0: none): sequences are cut into segments of
+  // seg_len tokens, a multiple of 128, each run by CTAs of its own.  A first
+  // launch leaves every segment's state increment, run from zero, in seg_x
+  // ([scan][slot][H][da][dc]); the second starts each segment from the states of
+  // those before it, joined in order: S <- lam^len S + X.  The segments of
+  // sequence n have the slots first(n) + 0, 1, ... with first(n) = n ceil(T /
+  // seg_len) for dense rows and cu[n] / seg_len + n for packed sequences.
+  int64_t seg_len;
+  int32_t slots;
+  float *seg_x;
+  size_t seg_x_bytes;  // room there; calls that need more are not split
+};
+
+// What one CTA runs: segment `seg` of `count` of sequence n, its first token and
+// length; `total` tokens in the sequence.
+struct Span {
+  int n, seg, count;
+  int64_t start, len, total;
 };
 
 // Bounds of sequence n as sequence_bounds (gdn_internal.cuh) gives them.
@@ -62,6 +80,44 @@ __device__ __forceinline__ bool bounds(const Params &p, int n, int h, int64_t &s
   return sequence_bounds(f, n, h, start, len);
 }
 
+// The span of slot z; false if it has none (or the offsets are bad: recorded).
+// Uniform over the CTA.
+__device__ __forceinline__ bool span_of(const Params &p, int z, int h, Span &s) {
+  s.seg = 0;
+  s.count = 1;
+  s.n = z;
+  if (p.seg_len == 0) {
+    if (!bounds(p, z, h, s.start, s.len)) return false;
+    s.total = s.len;
+    return true;
+  }
+  if (p.cu == nullptr) {
+    const int segs = (int)((p.seq_len + p.seg_len - 1) / p.seg_len);
+    s.n = z / segs;
+    s.seg = z % segs;
+  } else {
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {  // the last n with first(n) <= z
+      const int mid = (lo + hi + 1) / 2;
+      if (p.cu[mid] / p.seg_len + mid <= z) lo = mid;
+      else hi = mid - 1;
+    }
+    s.n = lo;
+    const int64_t at = z - (p.cu[lo] / p.seg_len + lo);
+    int64_t a, b;  // every sequence's bounds are looked at, also one that no slot finds
+    if (z < p.num_seqs && z != lo && !bounds(p, z, h, a, b)) return false;
+    if (at < 0 || at > p.slots) return false;
+    s.seg = (int)at;
+  }
+  if (!bounds(p, s.n, h, s.start, s.total)) return false;
+  s.count = s.total > 0 ? (int)((s.total + p.seg_len - 1) / p.seg_len) : 1;
+  if (s.seg >= s.count) return false;
+  const int64_t from = s.seg * p.seg_len;
+  s.start += from;
+  s.len = s.total - from < p.seg_len ? s.total - from : p.seg_len;
+  return true;
+}
+
 // Element (i, j) of the state of (n, h) that scan s starts from.
 __device__ __forceinline__ float state_in(const Scan &s, int64_t unit, int i, int j) {
   if (s.s_in == nullptr) return 0.f;
@@ -73,6 +129,55 @@ __device__ __forceinline__ float state_in(const Scan &s, int64_t unit, int i, in
 bool tc_scan(const Scan &s);
 cudaError_t launch_tc(const Params &p, cudaStream_t stream);
 cudaError_t launch_simt(const Params &p, gdn_dtype dtype, cudaStream_t stream);
+
+// Segments for a launch of `units` CTAs per slot (value tiles and scans, times
+// heads) on a GPU that runs `width` of them at a time.  A segment costs its
+// chunks of 128 tokens, some 3 more to start, and in the first launch about 0.6
+// of its chunks (half the reads, one product of four); joining reads a state for
+// every segment before.  One segment per sequence unless a split gains a tenth.
+struct Plan {
+  int64_t seg_len;
+  int32_t slots;
+};
+constexpr int kSMs = 152;
+constexpr int kSimtWidth = 2 * kSMs;   // CTAs of the CUDA-core form at a time
+inline size_t split_bytes(const Plan &plan, int64_t scans, int64_t heads, int64_t dk, int64_t dv) {
+  return plan.seg_len ? (size_t)(4 * scans * plan.slots * heads * dk * dv) : 0;
+}
+inline Plan plan_segments(int64_t num_seqs, int64_t seq_len, bool packed, int64_t units,
+                          int64_t width) {
+  const int64_t rows = packed ? 1 : num_seqs;           // packed: as one long row
+  if (!packed && units * num_seqs >= 4 * width) return {0, (int32_t)num_seqs};
+  const int64_t chunks = (seq_len + 127) / 128;
+  const auto waves = [&](int64_t ctas) { return (double)((ctas + width - 1) / width); };
+  // packed sequences: of their mean length, if they are not cut
+  const double whole = packed ? (double)chunks / (double)num_seqs : (double)chunks;
+  double best = 0.9 * (waves(units * num_seqs) * (whole + 3));
+  if (packed && num_seqs * units < width)               // a single one may hold nearly all
+    best = 0.9 * (double)(chunks + 3);
+  Plan plan{0, (int32_t)num_seqs};
+  for (int64_t s = 2; s <= 64 && s <= chunks; ++s) {
+    const int64_t len = (chunks + s - 1) / s, count = (chunks + len - 1) / len;
+    if (count < 2) continue;
+    const int64_t slots = packed ? seq_len / (128 * len) + num_seqs : rows * count;
+    const double cost = waves(units * slots) * ((double)len + 3 + 0.1 * (double)count) +
+                        waves(units * rows * (count - 1)) * (0.6 * (double)len + 3);
+    if (cost < best) {
+      best = cost;
+      plan = {128 * len, (int32_t)slots};
+    }
+  }
+  return plan;
+}
+// Fills in the split of a launch of `tiles` value tiles per scan and head.
+inline void split(Params &p, int64_t tiles, int64_t width) {
+  const Plan plan = plan_segments(p.num_seqs, p.seq_len, p.cu != nullptr,
+                                  tiles * p.num_scans * p.num_heads, width);
+  const bool fits = split_bytes(plan, p.num_scans, p.num_heads, p.scan[0].da, p.scan[0].dc) <=
+                    p.seg_x_bytes;
+  p.seg_len = fits ? plan.seg_len : 0;
+  p.slots = fits ? plan.slots : p.num_seqs;
+}
 
 }  // namespace lin
 }  // namespace gdn

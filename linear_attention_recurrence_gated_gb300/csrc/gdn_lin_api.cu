@@ -64,10 +64,26 @@ extern "C" {
 
 size_t gdn_lin_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_heads,
                               int32_t head_dim_k, int32_t head_dim_v, uint32_t flags) {
+  using namespace gdn::lin;
   if (num_seqs <= 0 || seq_len < 0 || num_heads <= 0 || head_dim_k <= 0 || head_dim_v <= 0)
     return 0;
   (void)flags;
-  return gdn::kStatusBytes;
+  // the largest of every launch that a forward or backward call of these sizes
+  // may make (packed or not, each storage type)
+  size_t most = 0;
+  const int dims[] = {head_dim_k, head_dim_v};
+  for (int scans = 1; scans <= 3; ++scans)
+    for (int d : dims)
+      for (int tile : {32, 64})
+        for (bool packed : {false, true}) {
+          const int64_t units = (int64_t)(d / tile) * scans * num_heads;
+          if (units == 0) continue;
+          const Plan plan = plan_segments(num_seqs, seq_len, packed, units,
+                                          tile == 64 ? kSMs : kSimtWidth);
+          const size_t n = split_bytes(plan, scans, num_heads, head_dim_k, head_dim_v);
+          most = n > most ? n : most;
+        }
+  return gdn::kStatusBytes + most;
 }
 
 gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float *log_decay,
@@ -94,9 +110,7 @@ gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float 
     if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
   if (!workspace) return GDN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GDN_ERR_INVALID_ARG;
-  if (workspace_bytes <
-      gdn_lin_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v, flags))
-    return GDN_ERR_WORKSPACE;
+  if (workspace_bytes < kStatusBytes) return GDN_ERR_WORKSPACE;
 
   const size_t rows = (size_t)batch * seq_len;
   const Range out = {o, rows * H * dv * e}, sT = {final_state, b_state},
@@ -117,6 +131,8 @@ gdn_status gdn_lin_fwd(const void *q, const void *k, const void *v, const float 
   p.log_decay = log_decay;
   p.cu = cu_seqlens;
   p.status = static_cast<DeviceStatus *>(workspace);
+  p.seg_x = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+  p.seg_x_bytes = workspace_bytes - kStatusBytes;
   p.seq_len = seq_len;
   p.num_heads = num_heads;
   p.num_seqs = num_seqs;
@@ -150,9 +166,7 @@ gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float 
     if (x && !aligned16(x)) return GDN_ERR_INVALID_ARG;
   if (!workspace) return GDN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GDN_ERR_INVALID_ARG;
-  if (workspace_bytes <
-      gdn_lin_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v, flags))
-    return GDN_ERR_WORKSPACE;
+  if (workspace_bytes < kStatusBytes) return GDN_ERR_WORKSPACE;
 
   const size_t rows = (size_t)batch * seq_len;
   const Range outs[] = {{dq, rows * H * nk * e}, {dk, rows * H * nk * e}, {dv, rows * H * nv * e},
@@ -181,6 +195,8 @@ gdn_status gdn_lin_bwd(const void *q, const void *k, const void *v, const float 
   p.log_decay = log_decay;
   p.cu = cu_seqlens;
   p.status = static_cast<DeviceStatus *>(workspace);
+  p.seg_x = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+  p.seg_x_bytes = workspace_bytes - kStatusBytes;
   p.seq_len = seq_len;
   p.num_heads = num_heads;
   p.num_seqs = num_seqs;

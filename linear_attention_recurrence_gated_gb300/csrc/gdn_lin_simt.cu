@@ -25,25 +25,42 @@ __host__ __device__ constexpr size_t smem_floats(int da) {
   return (size_t)2 * da * kLd + kC * kCols + kC * (kC + 1) + (size_t)da * kCols + kC + 1;
 }
 
-template <typename T>
+// STATES: the first launch of a split along time (the state increments alone).
+template <typename T, bool STATES>
 __global__ void __launch_bounds__(kThreads)
 gdn_lin_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   const Scan &s = p.scan[blockIdx.z % p.num_scans];
-  const int n = blockIdx.z / p.num_scans, h = blockIdx.y, col0 = blockIdx.x * kCols;
+  const int z = blockIdx.z / p.num_scans, h = blockIdx.y, col0 = blockIdx.x * kCols;
   if (col0 >= s.dc) return;  // (the scans of a launch may have fewer tiles)
   const int tid = threadIdx.x, H = p.num_heads, da = s.da, dc = s.dc;
   const bool rev = s.reverse != 0;
   float *At = sm, *Bt = At + (size_t)da * kLd, *V = Bt + (size_t)da * kLd, *P = V + kC * kCols,
         *S = P + kC * (kC + 1), *lam = S + (size_t)da * kCols;
 
-  int64_t start, len;
-  if (!bounds(p, n, h, start, len)) return;
-  const int64_t unit = (int64_t)n * H + h;
+  Span span;
+  if (!span_of(p, z, h, span)) return;
+  const int64_t start = span.start, len = span.len;
+  const int64_t unit = (int64_t)span.n * H + h;
+  // the segment whose end is the sequence's, in the scan's direction
+  const bool last = span.seg == (rev ? 0 : span.count - 1);
+  if (STATES && last) return;
+  const int64_t x_unit = ((int64_t)(blockIdx.z % p.num_scans) * p.slots + z) * H + h;  // of seg_x
+  float *const s_out = STATES ? p.seg_x + x_unit * da * dc
+                              : s.s_out && last ? s.s_out + unit * da * dc : nullptr;
   const float ld = p.log_decay[h];
   for (int i = tid; i <= kC; i += kThreads) lam[i] = i ? expf(ld * (float)i) : 1.f;
-  for (int i = tid; i < da * kCols; i += kThreads)
-    S[i] = state_in(s, unit, i / kCols, col0 + i % kCols);
+  for (int i = tid; i < da * kCols; i += kThreads) {
+    const int row = i / kCols, col = col0 + i % kCols;
+    float v = STATES ? 0.f : state_in(s, unit, row, col);
+    if (!STATES)  // the segments before this one, in order
+      for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
+        const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
+        v = fmaf(expf(ld * (float)length), v,
+                 p.seg_x[(x_unit + (int64_t)(k - span.seg) * H) * da * dc + (int64_t)row * dc + col]);
+      }
+    S[i] = v;
+  }
   const T *a = static_cast<const T *>(s.a) + (int64_t)h * da;
   const T *b = static_cast<const T *>(s.b) + (int64_t)h * da;
   const T *c = static_cast<const T *>(s.c) + (int64_t)h * dc + col0;
@@ -56,7 +73,7 @@ gdn_lin_simt_kernel(const Params p) {
     __syncthreads();  // the last chunk's reads of the tiles are done
     for (int x = tid; x < kC * da; x += kThreads) {
       const int i = x / da, k = x % da;
-      At[k * kLd + i] = i < e ? to_f32(a[(tok + i) * s.sa + k]) : 0.f;
+      if (!STATES) At[k * kLd + i] = i < e ? to_f32(a[(tok + i) * s.sa + k]) : 0.f;
       Bt[k * kLd + i] = i < e ? to_f32(b[(tok + i) * s.sb + k]) : 0.f;
     }
     for (int x = tid; x < kC * kCols; x += kThreads) {
@@ -64,7 +81,7 @@ gdn_lin_simt_kernel(const Params p) {
       V[x] = i < e ? to_f32(c[(tok + i) * s.sc + j]) : 0.f;
     }
     __syncthreads();
-    {  // P, 4 x 4 per thread
+    if (!STATES) {  // P, 4 x 4 per thread
       const int i0 = (tid >> 4) * 4, j0 = (tid & 15) * 4;
       float acc[4][4] = {};
       for (int k = 0; k < da; ++k) {
@@ -85,7 +102,7 @@ gdn_lin_simt_kernel(const Params p) {
         }
     }
     __syncthreads();
-    {  // o, 8 columns per thread
+    if (!STATES) {  // o, 8 columns per thread
       const int i = tid >> 2, c0 = (tid & 3) * 8;
       float acc[8] = {};
       for (int k = 0; k < da; ++k) {
@@ -137,10 +154,21 @@ gdn_lin_simt_kernel(const Params p) {
       }
     }
   }
-  if (s.s_out == nullptr) return;
+  if (s_out == nullptr) return;
   __syncthreads();
   for (int i = tid; i < da * kCols; i += kThreads)
-    s.s_out[unit * da * dc + (int64_t)(i / kCols) * dc + col0 + i % kCols] = S[i];
+    s_out[(int64_t)(i / kCols) * dc + col0 + i % kCols] = S[i];
+}
+
+template <typename T, bool STATES>
+cudaError_t run(const Params &p, int da, int dc, cudaStream_t stream) {
+  const size_t bytes = smem_floats(da) * 4;
+  const cudaError_t err = cudaFuncSetAttribute(
+      gdn_lin_simt_kernel<T, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err != cudaSuccess) return err;
+  const dim3 grid(dc / kCols, p.num_heads, p.slots * p.num_scans);
+  gdn_lin_simt_kernel<T, STATES><<<grid, kThreads, bytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -150,13 +178,13 @@ cudaError_t launch_t(const Params &p, cudaStream_t stream) {
     da = p.scan[i].da > da ? p.scan[i].da : da;
     dc = p.scan[i].dc > dc ? p.scan[i].dc : dc;
   }
-  const size_t bytes = smem_floats(da) * 4;
-  const cudaError_t err = cudaFuncSetAttribute(
-      gdn_lin_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (err != cudaSuccess) return err;
-  const dim3 grid(dc / kCols, p.num_heads, p.num_seqs * p.num_scans);
-  gdn_lin_simt_kernel<T><<<grid, kThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  Params on = p;
+  split(on, dc / kCols, kSimtWidth);
+  if (on.seg_len) {
+    const cudaError_t err = run<T, true>(on, da, dc, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return run<T, false>(on, da, dc, stream);
 }
 
 }  // namespace

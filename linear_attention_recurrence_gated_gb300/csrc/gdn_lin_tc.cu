@@ -182,7 +182,9 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 
 __device__ __forceinline__ float power(float ld, float n) { return n == 0.f ? 1.f : expf(ld * n); }
 
-template <int DK>
+// STATES: the first launch of a split along time, which runs a segment from a zero
+// state and leaves its state increment (X and S alone).
+template <int DK, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   using L = Lay<DK>;
@@ -195,19 +197,26 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wq = warp & 3;
   const int tile = blockIdx.x % args.tiles, sc = blockIdx.x / args.tiles;
-  const int h = blockIdx.y, n = blockIdx.z, H = p.num_heads;
+  const int h = blockIdx.y, z = blockIdx.z, H = p.num_heads;
   const Scan &scan = p.scan[sc];
   const int dc = scan.dc, col0 = tile * 64;
   if (col0 >= dc) return;
   const bool rev = scan.reverse != 0;
-  const int64_t unit = (int64_t)n * H + h;
 
-  int64_t start, len;
-  if (!bounds(p, n, h, start, len)) return;  // uniform over the CTA
+  Span span;
+  if (!span_of(p, z, h, span)) return;  // uniform over the CTA
+  const int64_t start = span.start, len = span.len;
+  const int64_t unit = (int64_t)span.n * H + h;
+  // the segment whose end is the sequence's, in the scan's direction
+  const bool last = span.seg == (rev ? 0 : span.count - 1);
+  if (STATES && last) return;
+  const int64_t x_unit = ((int64_t)sc * p.slots + z) * H + h;   // of seg_x
+  float *const s_out = STATES ? p.seg_x + x_unit * DK * dc
+                              : scan.s_out && last ? scan.s_out + unit * DK * dc : nullptr;
   if (len == 0) {  // the state passes through
-    if (scan.s_out)
+    if (s_out)
       for (int i = tid; i < DK * 64; i += kThreads)
-        scan.s_out[unit * DK * dc + (int64_t)(i >> 6) * dc + col0 + (i & 63)] =
+        s_out[(int64_t)(i >> 6) * dc + col0 + (i & 63)] =
             state_in(scan, unit, i >> 6, col0 + (i & 63));
     return;
   }
@@ -235,7 +244,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
                         i == kClean || i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
       // one arrival per warp; a stage is freed by both issuing warps (DK 128: one
       // of them and the o warps)
-      mbar_init(w.at(i), i == kPReady || i == kPReady + 1 ? 8 : role ? 4 : i >= kEmpty && i < kPFull ? 2 : 1);
+      mbar_init(w.at(i), i == kPReady || i == kPReady + 1 ? 8 : role ? 4 : !STATES && i >= kEmpty && i < kPFull ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -253,9 +262,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   // 2^-17 of its row, reaches the returned state times lam^rest, rest the tokens
   // that follow the tile; below lam^rest = 2^-5 that is less than fp32 holds.
   int c3 = nc;
-  if (scan.s_out) {
+  if (scan.s_out && (STATES || last)) {
+    const int64_t after =
+        rev ? span.seg * p.seg_len : span.total - span.seg * p.seg_len - len;
     const float reach = ld < 0.f ? 3.4657f / -ld : 1e9f;   // lam^reach = 2^-5
-    c3 = nc - 2 - (int)(fminf(reach, 1e9f) / kC);
+    if (reach >= (float)after) c3 = nc - 2 - (int)(fminf(reach - (float)after, 1e9f) / kC);
   }
   // Half a row of V^ (columns 32 (t >> 6) .. + 31 of row j): w_j c_j as bf16
   // terms.  A row past the end is zeros, whatever lies there.
@@ -388,6 +399,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   };
 
   if (warp < 4) {
+    if constexpr (!STATES) {
     // ---- P', the units next to the diagonal ----
     uint64_t tri[8];   // (the table's zeros on the far side; they are not kept)
 #pragma unroll
@@ -426,6 +438,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       tc_fence_before();
       warp_arrive(w.at(kPReady + b));
     }
+    }
   } else if (warp < 8) {
     // ---- S and o ----
     // DK 128: lane i holds row i of S, 64 columns; DK 64: X holds its rows
@@ -435,20 +448,30 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     uint64_t s[N / 2];   // pairs of columns
 #pragma unroll
     for (int x = 0; x < N / 2; ++x) s[x] = 0;
-    if (scan.s_in && scan.s_in_t) {
-      const float *at = scan.s_in + unit * DK * dc + (int64_t)(col0 + c0) * DK + si;
-#pragma unroll
-      for (int x = 0; x < N / 2; ++x) s[x] = pair(at[2 * x * DK], at[(2 * x + 1) * DK]);
-    } else if (scan.s_in) {
-      const float4 *row =
-          reinterpret_cast<const float4 *>(scan.s_in + (unit * DK + si) * dc + col0 + c0);
+    const auto add_row = [&](const float *state, float f) {  // s <- f s + row si of it
+      const float4 *row = reinterpret_cast<const float4 *>(state + (int64_t)si * dc + col0 + c0);
 #pragma unroll
       for (int x = 0; x < N / 4; ++x) {
         const float4 y = row[x];
-        s[2 * x] = pair(y.x, y.y);
-        s[2 * x + 1] = pair(y.z, y.w);
+        s[2 * x] = fma2(pair(f, f), s[2 * x], pair(y.x, y.y));
+        s[2 * x + 1] = fma2(pair(f, f), s[2 * x + 1], pair(y.z, y.w));
+      }
+    };
+    if (!STATES && scan.s_in) {
+      if (scan.s_in_t) {
+        const float *at = scan.s_in + unit * DK * dc + (int64_t)(col0 + c0) * DK + si;
+#pragma unroll
+        for (int x = 0; x < N / 2; ++x) s[x] = pair(at[2 * x * DK], at[(2 * x + 1) * DK]);
+      } else {
+        add_row(scan.s_in + unit * DK * dc, 0.f);
       }
     }
+    if (!STATES)  // the segments before this one, in order
+      for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
+        const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
+        add_row(p.seg_x + (x_unit + (int64_t)(k - span.seg) * H) * DK * dc,
+                power(ld, (float)length));
+      }
     auto put = [&]() {
 #pragma unroll
       for (int q = 0; q < N / 8; ++q)
@@ -458,7 +481,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       fence_proxy_async_smem();
       warp_arrive(w.at(kSReady));
     };
-    put();
+    if (!STATES) put();
     const float lam_c = lam[kC];
     // o : lane i holds row i
     const int i = 32 * wq + lane;
@@ -485,6 +508,10 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       tc_fence_before();
       warp_arrive(w.at(kXRead));
+      if (STATES) {
+        ++done;
+        continue;
+      }
       const int64_t tok = start + (int64_t)tile_of(c) * kC;
       const uint32_t stage = sb + (c % L::STAGES) * L::STAGE;
       const uint32_t so = DK == 64 ? sb + L::O : stage + L::A;
@@ -541,9 +568,8 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
     }
     if (lead) bulk_wait_all();
-    if (scan.s_out && done == nc) {
-      ulonglong2 *row =
-          reinterpret_cast<ulonglong2 *>(scan.s_out + (unit * DK + si) * dc + col0 + c0);
+    if (s_out && done == nc) {
+      ulonglong2 *row = reinterpret_cast<ulonglong2 *>(s_out + (int64_t)si * dc + col0 + c0);
 #pragma unroll
       for (int x = 0; x < N / 4; ++x) row[x] = make_ulonglong2(s[2 * x], s[2 * x + 1]);
     }
@@ -554,6 +580,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, 0, tid & 127) ||
           !weigh(c, 1, tid & 127))
         break;
+      if (STATES) continue;
       if (units > far0) {
         if (!wait(w, kPFull + (c & 1), c >> 1)) break;
         tc_fence_after();
@@ -572,10 +599,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         if (c >= L::STAGES && !wait(w, kEmpty + s, c / L::STAGES - 1)) break;
         const int tok = (int)(start + (int64_t)tile_of(c) * kC);
         const uint32_t stage = sb + s * L::STAGE, full = w.at(kFull + s);
-        mbar_arrive_expect_tx(full, L::STAGE);
+        mbar_arrive_expect_tx(full, STATES ? L::STAGE - L::B : L::STAGE);
 #pragma unroll
         for (int u = 0; u < L::SUB; ++u) {
-          tma_load_3d(stage + L::A + u * kTile, &args.map[sc][0], 64 * u, h, tok, full);
+          if (!STATES)
+            tma_load_3d(stage + L::A + u * kTile, &args.map[sc][0], 64 * u, h, tok, full);
           tma_load_3d(stage + L::B + u * kTile, &args.map[sc][1], 64 * u, h, tok, full);
         }
         tma_load_3d(stage + L::V, &args.map[sc][2], col0, h, tok, full);
@@ -626,7 +654,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       wait(w, kLast, 0);
     }
     __syncwarp();
-  } else if (warp == 14) {
+  } else if (!STATES && warp == 14) {
     // ---- issue of P ----
     const uint32_t leader = elect();
     int s = 0;
@@ -654,7 +682,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       wait(w, kLast + 2, 0);
     }
     __syncwarp();
-  } else {
+  } else if (!STATES) {
     // ---- issue of O1 and O2 ----
     const uint32_t leader = elect();
     int s = 0;
@@ -696,7 +724,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *abort_flag)
-    report(p.status, GDN_ERR_TIMEOUT, (uint32_t)n, (uint32_t)h, (uint32_t)*abort_flag);
+    report(p.status, GDN_ERR_TIMEOUT, (uint32_t)span.n, (uint32_t)h, (uint32_t)*abort_flag);
   if (warp == 12) {
     __syncwarp();
     tc_fence_after();
@@ -719,6 +747,17 @@ bool make_map(CUtensorMap *m, const void *ptr, int cols, int heads, int64_t toke
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int DK, bool STATES>
+cudaError_t run(const TcArgs &args, cudaStream_t stream) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(gdn_lin_tc_kernel<DK, STATES>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DK>::ALLOC);
+  if (err != cudaSuccess) return err;
+  const dim3 grid(args.tiles * args.p.num_scans, args.p.num_heads, args.p.slots);
+  gdn_lin_tc_kernel<DK, STATES><<<grid, kThreads, Lay<DK>::ALLOC, stream>>>(args);
+  return cudaGetLastError();
+}
+
 template <int DK>
 cudaError_t launch_dk(const Params &p, cudaStream_t stream) {
   TcArgs args;
@@ -739,13 +778,12 @@ cudaError_t launch_dk(const Params &p, cudaStream_t stream) {
     if (s.dc / 64 > args.tiles) args.tiles = s.dc / 64;
   }
   if (args.p.num_scans == 0) return cudaSuccess;
-  const cudaError_t err =
-      cudaFuncSetAttribute(gdn_lin_tc_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           Lay<DK>::ALLOC);
-  if (err != cudaSuccess) return err;
-  const dim3 grid(args.tiles * args.p.num_scans, p.num_heads, p.num_seqs);
-  gdn_lin_tc_kernel<DK><<<grid, kThreads, Lay<DK>::ALLOC, stream>>>(args);
-  return cudaGetLastError();
+  split(args.p, args.tiles, kSMs);
+  if (args.p.seg_len) {
+    const cudaError_t err = run<DK, true>(args, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return run<DK, false>(args, stream);
 }
 
 }  // namespace

@@ -9,6 +9,7 @@ is missing or CUDA is unavailable it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -772,6 +773,7 @@ def _lin_check(where, q, k, v, log_decay, initial_state, cu_seqlens, extra):
     return B, T, H, dk, dv, N
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_lin_workspace_size(num_seqs: int, seq_len: int, num_heads: int, head_dim_k: int,
                            head_dim_v: int, flags: int = 0) -> int:
     return int(lib().gdn_lin_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v,
