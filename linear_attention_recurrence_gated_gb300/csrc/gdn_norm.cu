@@ -115,9 +115,19 @@ __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[V]) {
 // own rounding.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-z));
-  return __fdividef(1.f, 1.f + __expf(-z));
+  if constexpr (sizeof(T) == 4) {
+    return 1.f / (1.f + expf(-z));
+  } else {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+  }
 }
+
+// What is applied after the norm: bit 0 SiLU, bit 1 a gate; or (kAny) what the
+// arguments say at run time.  The widest vectors have an instance of each.
+constexpr int kAny = -1;
 
 // (count, mean, squared deviation) of two disjoint sets of values as one.
 struct Stat {
@@ -131,8 +141,10 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
 }
 
 // y of one value.
-template <typename T>
-__device__ __forceinline__ float activate(float u, float z, bool silu, bool gated) {
+template <typename T, int M>
+__device__ __forceinline__ float activate(float u, float z, const Params &p) {
+  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   if (silu) u *= sigmoid<T>(u);
   return gated ? u * z * sigmoid<T>(z) : u;
 }
@@ -141,9 +153,10 @@ __device__ __forceinline__ float activate(float u, float z, bool silu, bool gate
 // normalisation in a second (which finds a small sample in L1 or L2).  Threads
 // are tiled over (row, vector of V channels).  Shared memory: a (count, mean,
 // m2) triple per channel vector, then mean and rstd per group.
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_fwd_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -207,11 +220,10 @@ gdn_norm_fwd_kernel(const Params p) {
         const int64_t at = base + r * p.C + cv * V;
         float v[V], z[V];
         load<V>(xs + at, v);
-        if (zs) load<V>(zs + at, z);
+        if (gated) load<V>(zs + at, z);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          v[i] = activate<T>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), zs ? z[i] : 0.f, p.silu,
-                          zs != nullptr);
+          v[i] = activate<T, M>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), gated ? z[i] : 0.f, p);
         store<V>(static_cast<T *>(p.y) + at, v);
       }
     }
@@ -219,9 +231,10 @@ gdn_norm_fwd_kernel(const Params p) {
 }
 
 // du of one value, and dz where there is a gate.
-template <typename T>
-__device__ __forceinline__ float grad_u(float u, float z, float dy, bool silu, bool gated,
-                                        float &dz) {
+template <typename T, int M>
+__device__ __forceinline__ float grad_u(float u, float z, float dy, const Params &p, float &dz) {
+  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   float act = u, dact = 1.f;
   if (silu) {
     const float s = sigmoid<T>(u);
@@ -240,9 +253,10 @@ __device__ __forceinline__ float grad_u(float u, float z, float dy, bool silu, b
 // of du xh and du) in one pass, dx in a second.  Shared memory: two sums per
 // channel vector and row of threads, two means per group, then the channels'
 // running sums over the CTA's samples.
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_bwd_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -272,13 +286,12 @@ gdn_norm_bwd_kernel(const Params p) {
         float v[V], z[V], dy[V];
         load<V>(xs + at, v);
         load<V>(dys + at, dy);
-        if (zs) load<V>(zs + at, z);
+        if (gated) load<V>(zs + at, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float xh = (v[i] - mean) * rstd;
           float dz;
-          const float du = grad_u<T>(fmaf(xh, w[i], b[i]), zs ? z[i] : 0.f, dy[i], p.silu,
-                                  zs != nullptr, dz);
+          const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
           a1[i] += du;
           a2[i] = fmaf(du, xh, a2[i]);
         }
@@ -325,18 +338,17 @@ gdn_norm_bwd_kernel(const Params p) {
         float v[V], z[V], dy[V];
         load<V>(xs + at, v);
         load<V>(dys + at, dy);
-        if (zs) load<V>(zs + at, z);
+        if (gated) load<V>(zs + at, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float xh = (v[i] - mean) * rstd;
           float dz = 0.f;
-          const float du = grad_u<T>(fmaf(xh, w[i], b[i]), zs ? z[i] : 0.f, dy[i], p.silu,
-                                  zs != nullptr, dz);
+          const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
           v[i] = rstd * (du * w[i] - m.x - xh * m.y);
           z[i] = dz;
         }
         store<V>(static_cast<T *>(p.dx) + at, v);
-        if (zs) store<V>(static_cast<T *>(p.dgate) + at, z);
+        if (gated) store<V>(static_cast<T *>(p.dgate) + at, z);
       }
     }
   }
@@ -355,7 +367,7 @@ gdn_norm_bwd_kernel(const Params p) {
 // ---- rows: S = 1, a group in the registers of LPG lanes -----------------------
 // Thread t holds vectors l, l + LPG, ... (R at most) of group gx of a row; the
 // group is the thread's own for every row, so its weights stay in registers.
-// The lanes of a group add up by shuffles.  Memory bound: one read, one write.
+// The lanes of a group add up by shuffles.  FULL: the group fills its lanes.
 template <int R>
 __device__ __forceinline__ float lanes_sum(float x, int lpg) {
   for (int off = 1; off < lpg; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -371,9 +383,10 @@ __host__ __device__ inline RowMap row_map(int G, int DV) {
   return {lpg, groups, slots / groups};
 }
 
-template <typename T, int V, int R>
+template <typename T, int V, int R, bool FULL, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_rows_fwd_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   const int DV = p.D / V, tid = threadIdx.x;
   const RowMap m = row_map(p.G, DV);
   const int l = tid % m.lpg, slot = tid / m.lpg, gx = blockIdx.y * m.groups + slot % m.groups;
@@ -388,7 +401,7 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int cv = l + r * m.lpg, c = gx * p.D + cv * V + i;
-      const bool in = on && cv < DV;
+      const bool in = on && (FULL || cv < DV);
       w[r][i] = in && p.w ? p.w[c] : 1.f;
       b[r][i] = in && p.b ? p.b[c] : 0.f;
     }
@@ -401,9 +414,9 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (have && cv < DV) {
+      if (have && (FULL || cv < DV)) {
         load<V>(xs + base + cv * V, v[r]);
-        if (zs) load<V>(zs + base + cv * V, z[r]);
+        if (gated) load<V>(zs + base + cv * V, z[r]);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[r][i] = 0.f;
@@ -417,7 +430,7 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         v[r][i] -= x0;
-        if (l + r * m.lpg < DV) s += v[r][i];
+        if (FULL || l + r * m.lpg < DV) s += v[r][i];
       }
     const float mean = lanes_sum<R>(s, m.lpg) * inv;
     s = 0.f;
@@ -426,9 +439,9 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         v[r][i] -= mean;
-        if (l + r * m.lpg < DV) s = fmaf(v[r][i], v[r][i], s);
+        if (FULL || l + r * m.lpg < DV) s = fmaf(v[r][i], v[r][i], s);
       }
-    const float rstd = 1.f / sqrtf(lanes_sum<R>(s, m.lpg) * inv + p.eps);
+    const float rstd = rsqrtf(lanes_sum<R>(s, m.lpg) * inv + p.eps);
     if (!have) continue;
     if (l == 0) {
       if (p.mean) p.mean[n * p.G + gx] = x0 + mean;
@@ -437,20 +450,20 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (cv < DV) {
+      if ((FULL || cv < DV)) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          v[r][i] = activate<T>(fmaf(v[r][i] * rstd, w[r][i], b[r][i]), zs ? z[r][i] : 0.f, p.silu,
-                                zs != nullptr);
+          v[r][i] = activate<T, M>(fmaf(v[r][i] * rstd, w[r][i], b[r][i]), gated ? z[r][i] : 0.f, p);
         store<V>(ys + base + cv * V, v[r]);
       }
     }
   }
 }
 
-template <typename T, int V, int R>
+template <typename T, int V, int R, bool FULL, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_rows_bwd_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];   // [rows][groups D] float2
   const int DV = p.D / V, tid = threadIdx.x;
   const RowMap m = row_map(p.G, DV);
@@ -466,7 +479,7 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int cv = l + r * m.lpg, c = gx * p.D + cv * V + i;
-      const bool in = on && cv < DV;
+      const bool in = on && (FULL || cv < DV);
       w[r][i] = in && p.w ? p.w[c] : 1.f;
       b[r][i] = in && p.b ? p.b[c] : 0.f;
       a1[r][i] = a2[r][i] = 0.f;
@@ -486,17 +499,16 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (have && cv < DV) {
+      if (have && (FULL || cv < DV)) {
         float z[V];
         load<V>(xs + base + cv * V, xh[r]);
         load<V>(dys + base + cv * V, du[r]);
-        if (zs) load<V>(zs + base + cv * V, z);
+        if (gated) load<V>(zs + base + cv * V, z);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           xh[r][i] = (xh[r][i] - mean) * rstd;
           dz[r][i] = 0.f;
-          du[r][i] = grad_u<T>(fmaf(xh[r][i], w[r][i], b[r][i]), zs ? z[i] : 0.f, du[r][i], p.silu,
-                               zs != nullptr, dz[r][i]);
+          du[r][i] = grad_u<T, M>(fmaf(xh[r][i], w[r][i], b[r][i]), gated ? z[i] : 0.f, du[r][i], p, dz[r][i]);
           a1[r][i] += du[r][i];
           a2[r][i] = fmaf(du[r][i], xh[r][i], a2[r][i]);
           du[r][i] *= w[r][i];
@@ -511,11 +523,11 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (cv < DV) {
+      if ((FULL || cv < DV)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) du[r][i] = rstd * (du[r][i] - t1 - xh[r][i] * t2);
         store<V>(static_cast<T *>(p.dx) + base + cv * V, du[r]);
-        if (zs) store<V>(static_cast<T *>(p.dgate) + base + cv * V, dz[r]);
+        if (gated) store<V>(static_cast<T *>(p.dgate) + base + cv * V, dz[r]);
       }
     }
   }
@@ -526,7 +538,7 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (cv < DV)
+      if ((FULL || cv < DV))
 #pragma unroll
         for (int i = 0; i < V; ++i)
           sc[(size_t)ry * width + (slot % m.groups) * p.D + cv * V + i] =
@@ -608,9 +620,10 @@ gdn_norm_slab_stats_kernel(const Params p) {
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_slab_apply_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -655,20 +668,20 @@ gdn_norm_slab_apply_kernel(const Params p) {
       const int64_t at = r * p.C + cv * V;
       float v[V], z[V];
       load<V>(xs + at, v);
-      if (zs) load<V>(zs + at, z);
+      if (gated) load<V>(zs + at, z);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        v[i] = activate<T>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), zs ? z[i] : 0.f, p.silu,
-                           zs != nullptr);
+        v[i] = activate<T, M>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), gated ? z[i] : 0.f, p);
       store<V>(static_cast<T *>(p.y) + base + at, v);
     }
   }
 }
 
 // The slab's channel sums of du xh and du, and its group sums of dxh and dxh xh.
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_slab_grads_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -695,13 +708,12 @@ gdn_norm_slab_grads_kernel(const Params p) {
       float v[V], z[V], dy[V];
       load<V>(xs + at, v);
       load<V>(dys + at, dy);
-      if (zs) load<V>(zs + at, z);
+      if (gated) load<V>(zs + at, z);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (v[i] - mean) * rstd;
         float dz;
-        const float du = grad_u<T>(fmaf(xh, w[i], b[i]), zs ? z[i] : 0.f, dy[i], p.silu,
-                                   zs != nullptr, dz);
+        const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
         a1[i] += du;
         a2[i] = fmaf(du, xh, a2[i]);
       }
@@ -739,9 +751,10 @@ gdn_norm_slab_grads_kernel(const Params p) {
   }
 }
 
-template <typename T, int V>
+template <typename T, int V, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_slab_dx_kernel(const Params p) {
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -785,18 +798,17 @@ gdn_norm_slab_dx_kernel(const Params p) {
       float v[V], z[V], dy[V];
       load<V>(xs + at, v);
       load<V>(dys + at, dy);
-      if (zs) load<V>(zs + at, z);
+      if (gated) load<V>(zs + at, z);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (v[i] - mean) * rstd;
         float dz = 0.f;
-        const float du = grad_u<T>(fmaf(xh, w[i], b[i]), zs ? z[i] : 0.f, dy[i], p.silu,
-                                   zs != nullptr, dz);
+        const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
         v[i] = rstd * (du * w[i] - m.x - xh * m.y);
         z[i] = dz;
       }
       store<V>(static_cast<T *>(p.dx) + base + at, v);
-      if (zs) store<V>(static_cast<T *>(p.dgate) + base + at, z);
+      if (gated) store<V>(static_cast<T *>(p.dgate) + base + at, z);
     }
   }
 }
@@ -846,7 +858,7 @@ cudaError_t sum_parts(const Params &p, int parts, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, int V, int R>
+template <typename T, int V, int R, bool FULL, int M>
 cudaError_t run_rows(const Params &p, bool backward, cudaStream_t stream) {
   const RowMap m = row_map(p.G, p.D / V);
   const int gy = (p.G + m.groups - 1) / m.groups;
@@ -854,51 +866,73 @@ cudaError_t run_rows(const Params &p, bool backward, cudaStream_t stream) {
   const int64_t most = backward ? (kParts / 2 + gy - 1) / gy : 8 * kSMs;
   if (gx > most) gx = most;
   const dim3 grid((unsigned)gx, gy);
-  if (!backward) return go(gdn_norm_rows_fwd_kernel<T, V, R>, grid, 0, p, stream);
+  if (!backward) return go(gdn_norm_rows_fwd_kernel<T, V, R, FULL, M>, grid, 0, p, stream);
   const size_t bytes = (size_t)8 * m.rows * m.groups * p.D;
-  const cudaError_t err = go(gdn_norm_rows_bwd_kernel<T, V, R>, grid, bytes, p, stream);
+  const cudaError_t err = go(gdn_norm_rows_bwd_kernel<T, V, R, FULL, M>, grid, bytes, p, stream);
   return err == cudaSuccess ? sum_parts(p, (int)gx, stream) : err;
 }
 
-template <typename T, int V>
-cudaError_t run(Params p, bool backward, cudaStream_t stream) {
-  const int CV = p.C / V, DV = p.D / V, TY = tile_rows(p.C, V);
-  if (p.S == 1 && DV <= 32) return run_rows<T, V, 1>(p, backward, stream);
-  if (p.S == 1 && DV <= 128) return run_rows<T, V, 4>(p, backward, stream);
+template <typename T, int V, int M>
+cudaError_t run_slabs(Params p, bool backward, cudaStream_t stream) {
+  const int CV = p.C / V, TY = tile_rows(p.C, V);
+  p.slabs = slab_count(p.N, p.S, p.C, V);
+  const int parts = (int)p.N * p.slabs;
+  p.sums = p.part + (backward ? (size_t)parts * 2 * p.C : 0);
+  const dim3 grid(p.slabs, (unsigned)p.N);
   cudaError_t err;
-  if (use_slabs(p.N, p.S)) {
-    p.slabs = slab_count(p.N, p.S, p.C, V);
-    const int parts = (int)p.N * p.slabs;
-    p.sums = p.part + (backward ? (size_t)parts * 2 * p.C : 0);
-    const dim3 grid(p.slabs, (unsigned)p.N);
-    if (!backward) {
-      err = go(gdn_norm_slab_stats_kernel<T, V>, grid, (size_t)12 * TY * CV, p, stream);
-      return err != cudaSuccess
-                 ? err
-                 : go(gdn_norm_slab_apply_kernel<T, V>, grid, (size_t)8 * p.G, p, stream);
-    }
-    err = go(gdn_norm_slab_grads_kernel<T, V>, grid, (size_t)8 * TY * p.C, p, stream);
-    if (err == cudaSuccess)
-      err = go(gdn_norm_slab_dx_kernel<T, V>, grid, (size_t)8 * p.G, p, stream);
-    return err == cudaSuccess ? sum_parts(p, parts, stream) : err;
+  if (!backward) {
+    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, (size_t)12 * TY * CV, p, stream);
+    return err != cudaSuccess
+               ? err
+               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream);
   }
+  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, (size_t)8 * TY * p.C, p, stream);
+  if (err == cudaSuccess)
+    err = go(gdn_norm_slab_dx_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream);
+  return err == cudaSuccess ? sum_parts(p, parts, stream) : err;
+}
+
+// The widest vectors: an instance for each activation.
+template <typename T, int V, int M>
+cudaError_t run_wide(const Params &p, bool backward, cudaStream_t stream) {
+  return p.S == 1 ? run_rows<T, V, 1, true, M>(p, backward, stream)
+                  : run_slabs<T, V, M>(p, backward, stream);
+}
+
+template <typename T, int V, bool WIDE>
+cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
+  const int CV = p.C / V, DV = p.D / V, TY = tile_rows(p.C, V);
+  if constexpr (WIDE) {
+    const bool full = p.S == 1 && DV <= 32 && (DV & (DV - 1)) == 0;
+    if (full || use_slabs(p.N, p.S)) {
+      const int mode = (p.silu ? 1 : 0) | (p.gate ? 2 : 0);
+      return mode == 0   ? run_wide<T, V, 0>(p, backward, stream)
+             : mode == 1 ? run_wide<T, V, 1>(p, backward, stream)
+             : mode == 2 ? run_wide<T, V, 2>(p, backward, stream)
+                         : run_wide<T, V, 3>(p, backward, stream);
+    }
+  }
+  if (p.S == 1 && DV <= 32) return run_rows<T, V, 1, false, kAny>(p, backward, stream);
+  if (p.S == 1 && DV <= 128) return run_rows<T, V, 4, false, kAny>(p, backward, stream);
+  if constexpr (!WIDE)
+    if (use_slabs(p.N, p.S)) return run_slabs<T, V, kAny>(p, backward, stream);
   const int grid = (int)(p.N < kParts ? p.N : kParts);
   if (!backward)
-    return go(gdn_norm_fwd_kernel<T, V>, grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
-  err = go(gdn_norm_bwd_kernel<T, V>, grid, ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8, p,
-           stream);
+    return go(gdn_norm_fwd_kernel<T, V, kAny>, grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
+  const cudaError_t err = go(gdn_norm_bwd_kernel<T, V, kAny>, grid,
+                             ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8, p, stream);
   return err == cudaSuccess ? sum_parts(p, grid, stream) : err;
 }
 
 // 16-byte vectors where a group holds whole ones, else pairs or single values.
 cudaError_t dispatch(const Params &p, gdn_dtype dtype, bool backward, cudaStream_t stream) {
   if (dtype == GDN_F32)
-    return p.D % 4 == 0   ? run<float, 4>(p, backward, stream)
-           : p.D % 2 == 0 ? run<float, 2>(p, backward, stream)
-                          : run<float, 1>(p, backward, stream);
-  return p.D % 8 == 0   ? run<__nv_bfloat16, 8>(p, backward, stream)
-         : p.D % 2 == 0 ? run<__nv_bfloat16, 2>(p, backward, stream)
-                        : run<__nv_bfloat16, 1>(p, backward, stream);
+    return p.D % 4 == 0   ? run<float, 4, true>(p, backward, stream)
+           : p.D % 2 == 0 ? run<float, 2, false>(p, backward, stream)
+                          : run<float, 1, false>(p, backward, stream);
+  return p.D % 8 == 0   ? run<__nv_bfloat16, 8, true>(p, backward, stream)
+         : p.D % 2 == 0 ? run<__nv_bfloat16, 2, false>(p, backward, stream)
+                        : run<__nv_bfloat16, 1, false>(p, backward, stream);
 }
 
 bool aligned16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }
