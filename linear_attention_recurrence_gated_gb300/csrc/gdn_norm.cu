@@ -560,7 +560,11 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 
 // ---- slabs: few samples, many rows ---------------------------------------------
 // CTA (slab, n) owns rows [slab R, slab R + R) of sample n, threads tiled over
-// (row, vector of V channels) as in the sample form.
+// (row, vector of V channels): TX vectors of one row, TY rows, blockDim.x = TX TY
+// up to a whole warp.
+constexpr int kSlabThreads = 512;
+__host__ __device__ inline int slab_tx(int CV) { return CV < 256 ? CV : 256; }
+__host__ __device__ inline int slab_ty(int CV) { return kSlabThreads / slab_tx(CV); }
 __device__ __forceinline__ void slab_rows(const Params &p, int64_t &r0, int64_t &r1) {
   const int64_t per = (p.S + p.slabs - 1) / p.slabs;
   r0 = blockIdx.x * per;
@@ -569,11 +573,11 @@ __device__ __forceinline__ void slab_rows(const Params &p, int64_t &r0, int64_t 
 
 // The slab's (count, mean relative to the group's first value, m2) of each group.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSlabThreads)
 gdn_norm_slab_stats_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
-  const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
+  const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   Stat *st = reinterpret_cast<Stat *>(sm);  // [TY][CV]
   int64_t r0, r1;
@@ -608,7 +612,7 @@ gdn_norm_slab_stats_kernel(const Params p) {
   }
   __syncthreads();
   Stat *out = reinterpret_cast<Stat *>(p.sums) + ((size_t)blockIdx.y * p.slabs + blockIdx.x) * p.G;
-  for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
+  for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     Stat a = {0.f, 0.f, 0.f};
     for (int i = tid & 31; i < DV * TY; i += 32) a = join(a, st[(i / DV) * CV + g * DV + i % DV]);
 #pragma unroll
@@ -621,12 +625,12 @@ gdn_norm_slab_stats_kernel(const Params p) {
 }
 
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSlabThreads)
 gdn_norm_slab_apply_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
-  const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
+  const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float *smean = sm, *srstd = sm + p.G;
   const int64_t n = blockIdx.y;
@@ -636,7 +640,7 @@ gdn_norm_slab_apply_kernel(const Params p) {
   const int64_t base = n * p.S * p.C;
   const T *xs = static_cast<const T *>(p.x) + base;
   const T *zs = p.gate ? static_cast<const T *>(p.gate) + base : nullptr;
-  for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
+  for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     Stat a = {0.f, 0.f, 0.f};
     for (int i = tid & 31; i < p.slabs; i += 32) a = join(a, in[(size_t)i * p.G + g]);
 #pragma unroll
@@ -679,12 +683,12 @@ gdn_norm_slab_apply_kernel(const Params p) {
 
 // The slab's channel sums of du xh and du, and its group sums of dxh and dxh xh.
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSlabThreads)
 gdn_norm_slab_grads_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
-  const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
+  const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float2 *sc = reinterpret_cast<float2 *>(sm);  // [TY][C]
   const int64_t n = blockIdx.y, base = n * p.S * p.C;
@@ -723,7 +727,7 @@ gdn_norm_slab_grads_kernel(const Params p) {
   }
   __syncthreads();
   const size_t slab = (size_t)n * p.slabs + blockIdx.x;
-  for (int c = tid; c < p.C; c += kThreads) {
+  for (int c = tid; c < p.C; c += blockDim.x) {
     float2 a = sc[c];
     for (int r = 1; r < TY; ++r) {
       a.x += sc[(size_t)r * p.C + c].x;
@@ -735,7 +739,7 @@ gdn_norm_slab_grads_kernel(const Params p) {
   }
   __syncthreads();
   float2 *out = reinterpret_cast<float2 *>(p.sums) + slab * p.G;
-  for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
+  for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     float t1 = 0.f, t2 = 0.f;
     for (int i = tid & 31; i < p.D; i += 32) {
       const float wc = p.w ? p.w[g * p.D + i] : 1.f;
@@ -752,12 +756,12 @@ gdn_norm_slab_grads_kernel(const Params p) {
 }
 
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kSlabThreads)
 gdn_norm_slab_dx_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
-  const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
+  const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float2 *sg = reinterpret_cast<float2 *>(sm);
   const int64_t n = blockIdx.y, base = n * p.S * p.C;
@@ -767,7 +771,7 @@ gdn_norm_slab_dx_kernel(const Params p) {
   int64_t r0, r1;
   slab_rows(p, r0, r1);
   const float2 *in = reinterpret_cast<const float2 *>(p.sums) + (size_t)n * p.slabs * p.G;
-  for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
+  for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     float t1 = 0.f, t2 = 0.f;
     for (int i = tid & 31; i < p.slabs; i += 32) {
       const float2 t = in[(size_t)i * p.G + g];
@@ -792,7 +796,7 @@ gdn_norm_slab_dx_kernel(const Params p) {
       w[i] = p.w ? p.w[cv * V + i] : 1.f;
       b[i] = p.b ? p.b[cv * V + i] : 0.f;
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t r = r0 + ty; r < r1; r += TY) {
       const int64_t at = r * p.C + cv * V;
       float v[V], z[V], dy[V];
@@ -832,23 +836,24 @@ __global__ void __launch_bounds__(1024) gdn_norm_dwdb_kernel(const Params p, int
 }
 
 int tile_rows(int C, int V) { return C / V < kThreads ? kThreads / (C / V) : 1; }
-// Slabs of a sample when there are few: two CTAs for each SM, four rows of every
+// Slabs of a sample when there are few: four CTAs for each SM, four rows of every
 // row of threads at least.
 int slab_count(int64_t N, int64_t S, int C, int V) {
-  const int64_t want = (2 * kSMs + N - 1) / N, most = S / (4 * tile_rows(C, V));
+  const int64_t want = (kParts + N - 1) / N, most = S / (4 * slab_ty(C / V));
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : (int)n;
 }
 bool use_slabs(int64_t N, int64_t S) { return N < kSMs && S > 1; }
 
 template <typename K>
-cudaError_t go(K kernel, dim3 grid, size_t bytes, const Params &p, cudaStream_t stream) {
+cudaError_t go(K kernel, dim3 grid, size_t bytes, const Params &p, cudaStream_t stream,
+               int threads = kThreads) {
   const cudaError_t err =
       bytes > 48 * 1024
           ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
           : cudaSuccess;
   if (err != cudaSuccess) return err;
-  kernel<<<grid, kThreads, bytes, stream>>>(p);
+  kernel<<<grid, threads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -874,21 +879,21 @@ cudaError_t run_rows(const Params &p, bool backward, cudaStream_t stream) {
 
 template <typename T, int V, int M>
 cudaError_t run_slabs(Params p, bool backward, cudaStream_t stream) {
-  const int CV = p.C / V, TY = tile_rows(p.C, V);
+  const int CV = p.C / V, TY = slab_ty(CV), threads = (slab_tx(CV) * TY + 31) / 32 * 32;
   p.slabs = slab_count(p.N, p.S, p.C, V);
   const int parts = (int)p.N * p.slabs;
   p.sums = p.part + (backward ? (size_t)parts * 2 * p.C : 0);
   const dim3 grid(p.slabs, (unsigned)p.N);
   cudaError_t err;
   if (!backward) {
-    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, (size_t)12 * TY * CV, p, stream);
+    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, (size_t)12 * TY * CV, p, stream, threads);
     return err != cudaSuccess
                ? err
-               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream);
+               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream, threads);
   }
-  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, (size_t)8 * TY * p.C, p, stream);
+  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, (size_t)8 * TY * p.C, p, stream, threads);
   if (err == cudaSuccess)
-    err = go(gdn_norm_slab_dx_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream);
+    err = go(gdn_norm_slab_dx_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream, threads);
   return err == cudaSuccess ? sum_parts(p, parts, stream) : err;
 }
 
@@ -967,7 +972,7 @@ size_t gdn_group_norm_workspace_size(int32_t batch, int32_t spatial, int32_t cha
   if (batch <= 0 || spatial <= 0 || channels <= 0 || groups <= 0) return 0;
   // partial sums of dweight and dbias, and of the groups of every slab
   using namespace gdn::norm;
-  const size_t parts = use_slabs(batch, spatial) ? (size_t)(2 * kSMs + batch) : (size_t)kParts;
+  const size_t parts = use_slabs(batch, spatial) ? (size_t)(kParts + batch) : (size_t)kParts;
   return parts * ((size_t)8 * channels + (size_t)12 * groups);
 }
 
