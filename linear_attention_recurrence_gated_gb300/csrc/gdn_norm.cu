@@ -149,6 +149,147 @@ __device__ __forceinline__ float activate(float u, float z, const Params &p) {
   return gated ? u * z * sigmoid<T>(z) : u;
 }
 
+// ---- pairs of values: two lanes of packed fp32 arithmetic ----------------------
+using Pair = uint64_t;
+__device__ __forceinline__ Pair pk(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 un(Pair x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair both(float x) { return pk(x, x); }
+
+// V values as they lie in memory, unpacked when they are used.  A pair of a
+// single value (V = 1) has a zero beside it.
+template <typename T, int V>
+struct Raw;
+template <int V>
+struct Raw<float, V> {
+  float v[V];
+  __device__ __forceinline__ void load(const float *p) {
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(p);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else if constexpr (V == 2) {
+      const float2 x = *reinterpret_cast<const float2 *>(p);
+      v[0] = x.x; v[1] = x.y;
+    } else {
+      v[0] = *p;
+    }
+  }
+  __device__ __forceinline__ Pair at(int i) const { return pk(v[2 * i], V > 1 ? v[(2 * i + 1) % V] : 0.f); }
+};
+template <int V>
+struct Raw<__nv_bfloat16, V> {
+  uint32_t v[(V + 1) / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    if constexpr (V == 8) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(p);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else if constexpr (V == 2) {
+      v[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+      v[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+  }
+  __device__ __forceinline__ Pair at(int i) const {
+    return pk(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
+  }
+};
+template <typename T, int V>
+__device__ __forceinline__ void put(T *p, const Pair (&x)[(V + 1) / 2]) {
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = i & 1 ? un(x[i / 2]).y : un(x[i / 2]).x;
+  store<V>(p, v);
+}
+
+template <typename T>
+__device__ __forceinline__ Pair sigmoid2(Pair z) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 x = un(z);
+    return pk(sigmoid<T>(x.x), sigmoid<T>(x.y));
+  } else {
+    const float2 x = un(mul2(z, both(-1.4426950408889634f)));
+    float e0, e1, r0, r1;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(x.y));
+    const float2 d = un(add2(pk(e0, e1), both(1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d.y));
+    return pk(r0, r1);
+  }
+}
+template <typename T, int M>
+__device__ __forceinline__ Pair activate2(Pair u, Pair z, const Params &p) {
+  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
+  if (silu) u = mul2(u, sigmoid2<T>(u));
+  return gated ? mul2(u, mul2(z, sigmoid2<T>(z))) : u;
+}
+// silu'(x) = s (1 + x (1 - s)), s = sigmoid(x)
+__device__ __forceinline__ Pair dsilu2(Pair x, Pair s) {
+  return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+}
+template <typename T, int M>
+__device__ __forceinline__ Pair grad_u2(Pair u, Pair z, Pair dy, const Params &p, Pair &dz) {
+  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
+  Pair act = u, dact = both(1.f);
+  if (silu) {
+    const Pair s = sigmoid2<T>(u);
+    act = mul2(u, s);
+    dact = dsilu2(u, s);
+  }
+  if (gated) {
+    const Pair s = sigmoid2<T>(z);
+    dz = mul2(mul2(dy, act), dsilu2(z, s));
+    dy = mul2(dy, mul2(z, s));
+  }
+  return silu ? mul2(dy, dact) : dy;
+}
+// V weights from channel c on (a missing vector reads as `other`).
+template <int V>
+__device__ __forceinline__ void weights(const float *w, int c, bool in, float other,
+                                        Pair (&to)[(V + 1) / 2]) {
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = other;
+  if (in && w) {
+    if constexpr (V % 4 == 0) {   // (c is a multiple of V)
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(w + c + i);
+        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = w[c + i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (V + 1) / 2; ++i) to[i] = pk(v[2 * i], 2 * i + 1 < V ? v[(2 * i + 1) % V] : 0.f);
+}
+
 // One CTA per sample: statistics in one pass over the sample's rows, the
 // normalisation in a second (which finds a small sample in L1 or L2).  Threads
 // are tiled over (row, vector of V channels).  Shared memory: a (count, mean,
@@ -364,6 +505,26 @@ gdn_norm_bwd_kernel(const Params p) {
   }
 }
 
+// dw and db: 32 columns a CTA, its rows of threads over the partial sums, both in
+// a fixed order.
+__device__ __forceinline__ void sum_columns(const Params &p, int parts, int col0, float *sm) {
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, rows = blockDim.x >> 5, i = col0 + tx;
+  float a = 0.f;
+  if (i < 2 * p.C)
+#pragma unroll 4
+    for (int k = ty; k < parts; k += rows) a += p.part[(size_t)k * 2 * p.C + i];
+  sm[ty * 33 + tx] = a;
+  __syncthreads();
+  if (ty) return;
+  for (int k = 1; k < rows; ++k) a += sm[k * 33 + tx];
+  float *to = i < p.C ? p.dw : p.db;
+  if (i < 2 * p.C && to) to[i < p.C ? i : i - p.C] = a;
+}
+__global__ void __launch_bounds__(1024) gdn_norm_dwdb_kernel(const Params p, int parts) {
+  __shared__ float sm[32 * 33];
+  sum_columns(p, parts, 32 * blockIdx.x, sm);
+}
+
 // ---- rows: S = 1, a group in the registers of LPG lanes -----------------------
 // Thread t holds vectors l, l + LPG, ... (R at most) of group gx of a row; the
 // group is the thread's own for every row, so its weights stay in registers.
@@ -386,6 +547,7 @@ __host__ __device__ inline RowMap row_map(int G, int DV) {
 template <typename T, int V, int R, bool FULL, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_rows_fwd_kernel(const Params p) {
+  constexpr int NP = (V + 1) / 2;
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   const int DV = p.D / V, tid = threadIdx.x;
   const RowMap m = row_map(p.G, DV);
@@ -395,67 +557,78 @@ gdn_norm_rows_fwd_kernel(const Params p) {
   const T *xs = static_cast<const T *>(p.x), *zs = static_cast<const T *>(p.gate);
   T *ys = static_cast<T *>(p.y);
   const float inv = 1.f / (float)p.D;
-  float w[R][V], b[R][V];
+  Pair w[R][NP], b[R][NP];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int cv = l + r * m.lpg, c = gx * p.D + cv * V + i;
-      const bool in = on && (FULL || cv < DV);
-      w[r][i] = in && p.w ? p.w[c] : 1.f;
-      b[r][i] = in && p.b ? p.b[c] : 0.f;
-    }
+  for (int r = 0; r < R; ++r) {
+    const int cv = l + r * m.lpg;
+    weights<V>(p.w, gx * p.D + cv * V, on && cv < DV, 1.f, w[r]);
+    weights<V>(p.b, gx * p.D + cv * V, on && cv < DV, 0.f, b[r]);
+  }
   const int64_t step = (int64_t)gridDim.x * m.rows;
-  for (int64_t n0 = (int64_t)blockIdx.x * m.rows; n0 < p.N; n0 += step) {  // uniform: shuffles
-    const int64_t n = n0 + ry;
-    const bool have = on && n < p.N;
+  const auto read = [&](int64_t n, Raw<T, V> (&x)[R], Raw<T, V> (&z)[R]) {
+    if (!on || n >= p.N) return;
     const int64_t base = n * p.C + (int64_t)gx * p.D;
-    float v[R][V], z[R][V];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if (have && (FULL || cv < DV)) {
-        load<V>(xs + base + cv * V, v[r]);
-        if (gated) load<V>(zs + base + cv * V, z[r]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[r][i] = 0.f;
+      if (FULL || cv < DV) {
+        x[r].load(xs + base + cv * V);
+        if (gated) z[r].load(zs + base + cv * V);
       }
     }
+  };
+  Raw<T, V> x[R] = {}, z[R] = {}, x_next[R] = {}, z_next[R] = {};
+  int64_t n = (int64_t)blockIdx.x * m.rows + ry;
+  read(n, x, z);
+  // (a uniform count of turns: the lanes of a warp shuffle together)
+  for (int64_t n0 = (int64_t)blockIdx.x * m.rows; n0 < p.N; n0 += step, n += step) {
+    read(n + step, x_next, z_next);   // the next row is on its way
+    const bool have = on && n < p.N;
     // relative to the group's first value: a mean far from zero cancels nothing
-    const float x0 = __shfl_sync(0xffffffffu, v[0][0], (tid & 31) - l);
-    float s = 0.f;
+    const float first = un(x[0].at(0)).x;
+    const float x0 = __shfl_sync(0xffffffffu, first, (tid & 31) - l);
+    Pair v[R][NP], s = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r)
+      if (FULL || l + r * m.lpg < DV)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[r][i] -= x0;
-        if (FULL || l + r * m.lpg < DV) s += v[r][i];
-      }
-    const float mean = lanes_sum<R>(s, m.lpg) * inv;
-    s = 0.f;
+        for (int i = 0; i < NP; ++i) {
+          v[r][i] = add2(x[r].at(i), pk(-x0, V > 1 ? -x0 : 0.f));
+          s = add2(s, v[r][i]);
+        }
+    float2 t = un(s);
+    const float mean = lanes_sum<R>(t.x + t.y, m.lpg) * inv;
+    s = 0;
 #pragma unroll
     for (int r = 0; r < R; ++r)
+      if (FULL || l + r * m.lpg < DV)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[r][i] -= mean;
-        if (FULL || l + r * m.lpg < DV) s = fmaf(v[r][i], v[r][i], s);
+        for (int i = 0; i < NP; ++i) {
+          v[r][i] = add2(v[r][i], pk(-mean, V > 1 ? -mean : 0.f));
+          s = fma2(v[r][i], v[r][i], s);
+        }
+    t = un(s);
+    const float rstd = rsqrtf(lanes_sum<R>(t.x + t.y, m.lpg) * inv + p.eps);
+    if (have) {
+      if (l == 0) {
+        if (p.mean) p.mean[n * p.G + gx] = x0 + mean;
+        if (p.rstd) p.rstd[n * p.G + gx] = rstd;
       }
-    const float rstd = rsqrtf(lanes_sum<R>(s, m.lpg) * inv + p.eps);
-    if (!have) continue;
-    if (l == 0) {
-      if (p.mean) p.mean[n * p.G + gx] = x0 + mean;
-      if (p.rstd) p.rstd[n * p.G + gx] = rstd;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int cv = l + r * m.lpg;
+        if (FULL || cv < DV) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            v[r][i] = activate2<T, M>(fma2(mul2(v[r][i], both(rstd)), w[r][i], b[r][i]), z[r].at(i), p);
+          put<T, V>(ys + n * p.C + (int64_t)gx * p.D + cv * V, v[r]);
+        }
+      }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int cv = l + r * m.lpg;
-      if ((FULL || cv < DV)) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          v[r][i] = activate<T, M>(fmaf(v[r][i] * rstd, w[r][i], b[r][i]), gated ? z[r][i] : 0.f, p);
-        store<V>(ys + base + cv * V, v[r]);
-      }
+      x[r] = x_next[r];
+      z[r] = z_next[r];
     }
   }
 }
@@ -463,8 +636,9 @@ gdn_norm_rows_fwd_kernel(const Params p) {
 template <typename T, int V, int R, bool FULL, int M>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_rows_bwd_kernel(const Params p) {
-  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];   // [rows][groups D] float2
+  constexpr int NP = (V + 1) / 2;
+  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   const int DV = p.D / V, tid = threadIdx.x;
   const RowMap m = row_map(p.G, DV);
   const int l = tid % m.lpg, slot = tid / m.lpg, gx = blockIdx.y * m.groups + slot % m.groups;
@@ -473,63 +647,71 @@ gdn_norm_rows_bwd_kernel(const Params p) {
   const T *xs = static_cast<const T *>(p.x), *zs = static_cast<const T *>(p.gate),
           *dys = static_cast<const T *>(p.dy);
   const float inv = 1.f / (float)p.D;
-  float w[R][V], b[R][V], a1[R][V], a2[R][V];
+  Pair w[R][NP], b[R][NP], a1[R][NP], a2[R][NP];
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
+    const int cv = l + r * m.lpg;
+    weights<V>(p.w, gx * p.D + cv * V, on && cv < DV, 1.f, w[r]);
+    weights<V>(p.b, gx * p.D + cv * V, on && cv < DV, 0.f, b[r]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int cv = l + r * m.lpg, c = gx * p.D + cv * V + i;
-      const bool in = on && (FULL || cv < DV);
-      w[r][i] = in && p.w ? p.w[c] : 1.f;
-      b[r][i] = in && p.b ? p.b[c] : 0.f;
-      a1[r][i] = a2[r][i] = 0.f;
-    }
+    for (int i = 0; i < NP; ++i) a1[r][i] = a2[r][i] = 0;
+  }
   const int64_t step = (int64_t)gridDim.x * m.rows;
   for (int64_t n0 = (int64_t)blockIdx.x * m.rows; n0 < p.N; n0 += step) {
     const int64_t n = n0 + ry;
     const bool have = on && n < p.N;
     const int64_t base = n * p.C + (int64_t)gx * p.D;
-    float xh[R][V], du[R][V], dz[R][V];
+    Raw<T, V> x[R], dy[R], z[R];
     float mean = 0.f, rstd = 0.f;
     if (have) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int cv = l + r * m.lpg;
+        if (FULL || cv < DV) {
+          x[r].load(xs + base + cv * V);
+          dy[r].load(dys + base + cv * V);
+          if (gated) z[r].load(zs + base + cv * V);
+        }
+      }
       mean = p.mean[n * p.G + gx];
       rstd = p.rstd[n * p.G + gx];
     }
-    float t1 = 0.f, t2 = 0.f;
+    Pair xh[R][NP], du[R][NP], t1 = 0, t2 = 0;
+    if (have)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int cv = l + r * m.lpg;
-      if (have && (FULL || cv < DV)) {
-        float z[V];
-        load<V>(xs + base + cv * V, xh[r]);
-        load<V>(dys + base + cv * V, du[r]);
-        if (gated) load<V>(zs + base + cv * V, z);
+      for (int r = 0; r < R; ++r) {
+        const int cv = l + r * m.lpg;
+        if (FULL || cv < DV) {
+          Pair dz[NP];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          xh[r][i] = (xh[r][i] - mean) * rstd;
-          dz[r][i] = 0.f;
-          du[r][i] = grad_u<T, M>(fmaf(xh[r][i], w[r][i], b[r][i]), gated ? z[i] : 0.f, du[r][i], p, dz[r][i]);
-          a1[r][i] += du[r][i];
-          a2[r][i] = fmaf(du[r][i], xh[r][i], a2[r][i]);
-          du[r][i] *= w[r][i];
-          t1 += du[r][i];
-          t2 = fmaf(du[r][i], xh[r][i], t2);
+          for (int i = 0; i < NP; ++i) {
+            xh[r][i] = mul2(add2(x[r].at(i), both(-mean)), both(rstd));
+            dz[i] = 0;
+            du[r][i] = grad_u2<T, M>(fma2(xh[r][i], w[r][i], b[r][i]), gated ? z[r].at(i) : 0, dy[r].at(i),
+                                     p, dz[i]);
+            a1[r][i] = add2(a1[r][i], du[r][i]);
+            a2[r][i] = fma2(du[r][i], xh[r][i], a2[r][i]);
+            du[r][i] = mul2(du[r][i], w[r][i]);
+            t1 = add2(t1, du[r][i]);
+            t2 = fma2(du[r][i], xh[r][i], t2);
+          }
+          if (gated) put<T, V>(static_cast<T *>(p.dgate) + base + cv * V, dz);
         }
       }
-    }
-    t1 = lanes_sum<R>(t1, m.lpg) * inv;
-    t2 = lanes_sum<R>(t2, m.lpg) * inv;
-    if (!have) continue;
+    // (a single value's empty second lane: du and w are zero there)
+    const float2 u1 = un(t1), u2 = un(t2);
+    const float c1 = lanes_sum<R>(u1.x + u1.y, m.lpg) * inv, c2 = lanes_sum<R>(u2.x + u2.y, m.lpg) * inv;
+    if (have)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int cv = l + r * m.lpg;
-      if ((FULL || cv < DV)) {
+      for (int r = 0; r < R; ++r) {
+        const int cv = l + r * m.lpg;
+        if (FULL || cv < DV) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) du[r][i] = rstd * (du[r][i] - t1 - xh[r][i] * t2);
-        store<V>(static_cast<T *>(p.dx) + base + cv * V, du[r]);
-        if (gated) store<V>(static_cast<T *>(p.dgate) + base + cv * V, dz[r]);
+          for (int i = 0; i < NP; ++i)
+            du[r][i] = mul2(both(rstd), fma2(xh[r][i], both(-c2), add2(du[r][i], both(-c1))));
+          put<T, V>(static_cast<T *>(p.dx) + base + cv * V, du[r]);
+        }
       }
-    }
   }
   // the channels' sums of this CTA, over its rows of threads
   float2 *sc = reinterpret_cast<float2 *>(sm);
@@ -538,11 +720,13 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int cv = l + r * m.lpg;
-      if ((FULL || cv < DV))
+      if (FULL || cv < DV)
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int i = 0; i < V; ++i) {
+          const float2 q1 = un(a1[r][i / 2]), q2 = un(a2[r][i / 2]);
           sc[(size_t)ry * width + (slot % m.groups) * p.D + cv * V + i] =
-              make_float2(a2[r][i], a1[r][i]);
+              i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
+        }
     }
   __syncthreads();
   for (int i = tid; i < width; i += kThreads) {
@@ -571,15 +755,82 @@ __device__ __forceinline__ void slab_rows(const Params &p, int64_t &r0, int64_t 
   r1 = r0 + per < p.S ? r0 + per : p.S;
 }
 
+// Calls `use(row, x, dy, z)` for this thread's rows r0, r0 + step, ...  With 16-byte
+// vectors the rows come through a ring in shared memory, kDepth ahead: every
+// thread copies its own vectors and reads only those, so no thread waits for
+// another, and some 100 KB are on their way to an SM at any time.  (With the next
+// two rows in registers instead, a backward pass over [4, 4096, 1280] took 79 us,
+// each thread going through 14 latencies of memory one after the other.)
+constexpr int kDepth = 4;
+template <typename T, int V>
+constexpr bool kRing = sizeof(T) * V == 16;
+template <typename T, int V>
+size_t ring_bytes(int threads, int tensors) {
+  return kRing<T, V> ? (size_t)16 * kDepth * tensors * threads : 0;
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+template <typename T, int V, bool DY, typename F>
+__device__ __forceinline__ void for_rows(uint4 *ring, const T *xs, const T *dys, const T *zs,
+                                         bool gated, int64_t r0, int64_t r1, int64_t step,
+                                         int64_t C, int c, F use) {
+  if constexpr (kRing<T, V>) {
+    const int nt = 1 + (DY ? 1 : 0) + (gated ? 1 : 0);
+    uint4 *mine = ring + threadIdx.x;            // [stage][tensor][thread]
+    const int th = blockDim.x;
+    const uint32_t at0 = (uint32_t)__cvta_generic_to_shared(mine);
+    const auto ask = [&](int64_t r, int stage) {
+      if (r < r1) {
+        const int64_t at = r * C + c;
+        uint32_t to = at0 + 16 * th * nt * stage;
+        copy16(to, xs + at);
+        if (DY) copy16(to += 16 * th, dys + at);
+        if (gated) copy16(to += 16 * th, zs + at);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int64_t next = r0;
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k, next += step) ask(next, k);
+    int stage = 0, ahead = kDepth - 1;
+#pragma unroll 1
+    for (int64_t r = r0; r < r1; r += step, next += step) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+      ask(next, ahead);
+      const uint4 *from = mine + (size_t)th * nt * stage;
+      Raw<T, V> x, dy = {}, z = {};
+      x.load(reinterpret_cast<const T *>(from));
+      if (DY) dy.load(reinterpret_cast<const T *>(from += th));
+      if (gated) z.load(reinterpret_cast<const T *>(from += th));
+      use(r, x, dy, z);
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+      ahead = ahead + 1 == kDepth ? 0 : ahead + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else {
+#pragma unroll 4
+    for (int64_t r = r0; r < r1; r += step) {
+      const int64_t at = r * C + c;
+      Raw<T, V> x, dy = {}, z = {};
+      x.load(xs + at);
+      if (DY) dy.load(dys + at);
+      if (gated) z.load(zs + at);
+      use(r, x, dy, z);
+    }
+  }
+}
+
 // The slab's (count, mean relative to the group's first value, m2) of each group.
 template <typename T, int V>
-__global__ void __launch_bounds__(kSlabThreads)
+__global__ void __launch_bounds__(kSlabThreads, 2)
 gdn_norm_slab_stats_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   Stat *st = reinterpret_cast<Stat *>(sm);  // [TY][CV]
+  uint4 *ring = reinterpret_cast<uint4 *>(sm + ((size_t)3 * TY * CV + 3) / 4 * 4);
   int64_t r0, r1;
   slab_rows(p, r0, r1);
   const int64_t base = (int64_t)blockIdx.y * p.S * p.C;
@@ -587,27 +838,29 @@ gdn_norm_slab_stats_kernel(const Params p) {
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
     const float x0 = to_f32(xs[(cv / DV) * p.D]);
     Stat all = {0.f, 0.f, 0.f};
-    for (int64_t ra = r0 + ty; ra < r1; ra += kBlock * TY) {
-      float c = 0.f, s1 = 0.f, s2 = 0.f, cnt = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < kBlock; ++k) {
-        const int64_t r = ra + k * TY;
-        if (r < r1) {
-          float v[V];
-          load<V>(xs + r * p.C + cv * V, v);
-          if (k == 0) c = v[0];
+    float c = 0.f, cnt = 0.f;
+    Pair s1 = 0, s2 = 0;
+    const auto close = [&]() {
+      const float2 t1 = un(s1), t2 = un(s2);
+      const float t = t1.x + t1.y, m = t / cnt;
+      all = join(all, Stat{cnt, (c - x0) + m, (t2.x + t2.y) - t * m});
+      cnt = 0.f;
+      s1 = s2 = 0;
+    };
+    for_rows<T, V, false>(
+        ring, xs, xs, nullptr, false, r0 + ty, r1, TY, p.C, cv * V,
+        [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &) {
+          if (cnt == 0.f) c = un(x.at(0)).x;
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float d = v[i] - c;
-            s1 += d;
-            s2 = fmaf(d, d, s2);
+          for (int i = 0; i < (V + 1) / 2; ++i) {
+            const Pair d = add2(x.at(i), pk(-c, V > 1 ? -c : 0.f));
+            s1 = add2(s1, d);
+            s2 = fma2(d, d, s2);
           }
           cnt += V;
-        }
-      }
-      const float m = s1 / cnt;
-      all = join(all, Stat{cnt, (c - x0) + m, s2 - s1 * m});
-    }
+          if (cnt == (float)(kBlock * V)) close();
+        });
+    if (cnt > 0.f) close();
     st[ty * CV + cv] = all;
   }
   __syncthreads();
@@ -625,7 +878,7 @@ gdn_norm_slab_stats_kernel(const Params p) {
 }
 
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kSlabThreads)
+__global__ void __launch_bounds__(kSlabThreads, 2)
 gdn_norm_slab_apply_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
@@ -633,6 +886,7 @@ gdn_norm_slab_apply_kernel(const Params p) {
   const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float *smean = sm, *srstd = sm + p.G;
+  uint4 *ring = reinterpret_cast<uint4 *>(sm + (2 * p.G + 3) / 4 * 4);
   const int64_t n = blockIdx.y;
   const Stat *in = reinterpret_cast<const Stat *>(p.sums) + (size_t)n * p.slabs * p.G;
   int64_t r0, r1;
@@ -661,29 +915,27 @@ gdn_norm_slab_apply_kernel(const Params p) {
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
     const int g = cv / DV;
     const float x0 = to_f32(xs[g * p.D]), mean = smean[g], rstd = srstd[g];
-    float w[V], b[V];
+    constexpr int NP = (V + 1) / 2;
+    Pair w[NP], b[NP];
+    weights<V>(p.w, cv * V, true, 1.f, w);
+    weights<V>(p.b, cv * V, true, 0.f, b);
+    for_rows<T, V, false>(
+        ring, xs, xs, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
+        [&](int64_t r, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &z) {
+          Pair y[NP];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[i] = p.w ? p.w[cv * V + i] : 1.f;
-      b[i] = p.b ? p.b[cv * V + i] : 0.f;
-    }
-#pragma unroll 4
-    for (int64_t r = r0 + ty; r < r1; r += TY) {
-      const int64_t at = r * p.C + cv * V;
-      float v[V], z[V];
-      load<V>(xs + at, v);
-      if (gated) load<V>(zs + at, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        v[i] = activate<T, M>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), gated ? z[i] : 0.f, p);
-      store<V>(static_cast<T *>(p.y) + base + at, v);
-    }
+          for (int i = 0; i < NP; ++i) {
+            const Pair d = add2(add2(x.at(i), both(-x0)), both(-mean));
+            y[i] = activate2<T, M>(fma2(mul2(d, both(rstd)), w[i], b[i]), gated ? z.at(i) : 0, p);
+          }
+          put<T, V>(static_cast<T *>(p.y) + base + r * p.C + cv * V, y);
+        });
   }
 }
 
 // The slab's channel sums of du xh and du, and its group sums of dxh and dxh xh.
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kSlabThreads)
+__global__ void __launch_bounds__(kSlabThreads, 2)
 gdn_norm_slab_grads_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
@@ -691,6 +943,7 @@ gdn_norm_slab_grads_kernel(const Params p) {
   const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float2 *sc = reinterpret_cast<float2 *>(sm);  // [TY][C]
+  uint4 *ring = reinterpret_cast<uint4 *>(sm + ((size_t)2 * TY * p.C + 3) / 4 * 4);
   const int64_t n = blockIdx.y, base = n * p.S * p.C;
   const T *xs = static_cast<const T *>(p.x) + base, *dys = static_cast<const T *>(p.dy) + base;
   const T *zs = p.gate ? static_cast<const T *>(p.gate) + base : nullptr;
@@ -699,31 +952,30 @@ gdn_norm_slab_grads_kernel(const Params p) {
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
     const int g = cv / DV;
     const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
-    float w[V], b[V], a1[V], a2[V];
+    constexpr int NP = (V + 1) / 2;
+    Pair w[NP], b[NP], a1[NP], a2[NP];
+    weights<V>(p.w, cv * V, true, 1.f, w);
+    weights<V>(p.b, cv * V, true, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) a1[i] = a2[i] = 0;
+    for_rows<T, V, true>(
+        ring, xs, dys, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
+        [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) {
+            const Pair xh = mul2(add2(x.at(i), both(-mean)), both(rstd));
+            Pair dz;
+            const Pair du =
+                grad_u2<T, M>(fma2(xh, w[i], b[i]), gated ? z.at(i) : 0, dy.at(i), p, dz);
+            a1[i] = add2(a1[i], du);
+            a2[i] = fma2(du, xh, a2[i]);
+          }
+        });
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      w[i] = p.w ? p.w[cv * V + i] : 1.f;
-      b[i] = p.b ? p.b[cv * V + i] : 0.f;
-      a1[i] = a2[i] = 0.f;
+      const float2 q1 = un(a1[i / 2]), q2 = un(a2[i / 2]);
+      sc[(size_t)ty * p.C + cv * V + i] = i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
     }
-#pragma unroll 4
-    for (int64_t r = r0 + ty; r < r1; r += TY) {
-      const int64_t at = r * p.C + cv * V;
-      float v[V], z[V], dy[V];
-      load<V>(xs + at, v);
-      load<V>(dys + at, dy);
-      if (gated) load<V>(zs + at, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = (v[i] - mean) * rstd;
-        float dz;
-        const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
-        a1[i] += du;
-        a2[i] = fmaf(du, xh, a2[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) sc[(size_t)ty * p.C + cv * V + i] = make_float2(a2[i], a1[i]);
   }
   __syncthreads();
   const size_t slab = (size_t)n * p.slabs + blockIdx.x;
@@ -756,14 +1008,20 @@ gdn_norm_slab_grads_kernel(const Params p) {
 }
 
 template <typename T, int V, int M>
-__global__ void __launch_bounds__(kSlabThreads)
+__global__ void __launch_bounds__(kSlabThreads, 2)
 gdn_norm_slab_dx_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
+  if (blockIdx.y >= p.N) {  // the last CTAs sum up dweight and dbias meanwhile
+    const int col0 = 32 * ((blockIdx.y - (int)p.N) * gridDim.x + blockIdx.x);
+    if (col0 < 2 * p.C) sum_columns(p, (int)p.N * p.slabs, col0, sm);
+    return;
+  }
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
   float2 *sg = reinterpret_cast<float2 *>(sm);
+  uint4 *ring = reinterpret_cast<uint4 *>(sm + (2 * p.G + 3) / 4 * 4);
   const int64_t n = blockIdx.y, base = n * p.S * p.C;
   const T *xs = static_cast<const T *>(p.x) + base, *dys = static_cast<const T *>(p.dy) + base;
   const T *zs = p.gate ? static_cast<const T *>(p.gate) + base : nullptr;
@@ -790,56 +1048,34 @@ gdn_norm_slab_dx_kernel(const Params p) {
     const int g = cv / DV;
     const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
     const float2 m = sg[g];
-    float w[V], b[V];
+    constexpr int NP = (V + 1) / 2;
+    Pair w[NP], b[NP];
+    weights<V>(p.w, cv * V, true, 1.f, w);
+    weights<V>(p.b, cv * V, true, 0.f, b);
+    for_rows<T, V, true>(
+        ring, xs, dys, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
+        [&](int64_t r, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+          const int64_t at = r * p.C + cv * V;
+          Pair dx[NP], dz[NP];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[i] = p.w ? p.w[cv * V + i] : 1.f;
-      b[i] = p.b ? p.b[cv * V + i] : 0.f;
-    }
-#pragma unroll 4
-    for (int64_t r = r0 + ty; r < r1; r += TY) {
-      const int64_t at = r * p.C + cv * V;
-      float v[V], z[V], dy[V];
-      load<V>(xs + at, v);
-      load<V>(dys + at, dy);
-      if (gated) load<V>(zs + at, z);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float xh = (v[i] - mean) * rstd;
-        float dz = 0.f;
-        const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
-        v[i] = rstd * (du * w[i] - m.x - xh * m.y);
-        z[i] = dz;
-      }
-      store<V>(static_cast<T *>(p.dx) + base + at, v);
-      if (gated) store<V>(static_cast<T *>(p.dgate) + base + at, z);
-    }
+          for (int i = 0; i < NP; ++i) {
+            const Pair xh = mul2(add2(x.at(i), both(-mean)), both(rstd));
+            dz[i] = 0;
+            const Pair du =
+                grad_u2<T, M>(fma2(xh, w[i], b[i]), gated ? z.at(i) : 0, dy.at(i), p, dz[i]);
+            dx[i] = mul2(both(rstd), fma2(xh, both(-m.y), fma2(du, w[i], both(-m.x))));
+          }
+          put<T, V>(static_cast<T *>(p.dx) + base + at, dx);
+          if (gated) put<T, V>(static_cast<T *>(p.dgate) + base + at, dz);
+        });
   }
 }
 
-// dw and db: 32 columns a CTA, its 32 rows of threads over the partial sums, both
-// in a fixed order.
-__global__ void __launch_bounds__(1024) gdn_norm_dwdb_kernel(const Params p, int parts) {
-  __shared__ float sm[32][33];
-  const int tx = threadIdx.x, ty = threadIdx.y, i = blockIdx.x * 32 + tx;
-  float a = 0.f;
-  if (i < 2 * p.C)
-#pragma unroll 4
-    for (int k = ty; k < parts; k += 32) a += p.part[(size_t)k * 2 * p.C + i];
-  sm[ty][tx] = a;
-  __syncthreads();
-  if (ty) return;
-#pragma unroll
-  for (int k = 1; k < 32; ++k) a += sm[k][tx];
-  float *to = i < p.C ? p.dw : p.db;
-  if (i < 2 * p.C && to) to[i < p.C ? i : i - p.C] = a;
-}
-
 int tile_rows(int C, int V) { return C / V < kThreads ? kThreads / (C / V) : 1; }
-// Slabs of a sample when there are few: four CTAs for each SM, four rows of every
-// row of threads at least.
+// Slabs of a sample when there are few: two CTAs (all that fit) for each SM, four
+// rows of every row of threads at least.
 int slab_count(int64_t N, int64_t S, int C, int V) {
-  const int64_t want = (kParts + N - 1) / N, most = S / (4 * slab_ty(C / V));
+  const int64_t want = (2 * kSMs + N - 1) / N, most = S / (4 * slab_ty(C / V));
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : (int)n;
 }
@@ -859,7 +1095,7 @@ cudaError_t go(K kernel, dim3 grid, size_t bytes, const Params &p, cudaStream_t 
 
 cudaError_t sum_parts(const Params &p, int parts, cudaStream_t stream) {
   if (!p.dw && !p.db) return cudaSuccess;
-  gdn_norm_dwdb_kernel<<<(2 * p.C + 31) / 32, dim3(32, 32), 0, stream>>>(p, parts);
+  gdn_norm_dwdb_kernel<<<(2 * p.C + 31) / 32, 1024, 0, stream>>>(p, parts);
   return cudaGetLastError();
 }
 
@@ -884,17 +1120,27 @@ cudaError_t run_slabs(Params p, bool backward, cudaStream_t stream) {
   const int parts = (int)p.N * p.slabs;
   p.sums = p.part + (backward ? (size_t)parts * 2 * p.C : 0);
   const dim3 grid(p.slabs, (unsigned)p.N);
+  const size_t groups = ((size_t)8 * p.G + 15) / 16 * 16;
+  const int gates = p.gate ? 1 : 0;
   cudaError_t err;
   if (!backward) {
-    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, (size_t)12 * TY * CV, p, stream, threads);
+    const size_t own = ((size_t)12 * TY * CV + 15) / 16 * 16;
+    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, own + ring_bytes<T, V>(threads, 1), p, stream,
+             threads);
     return err != cudaSuccess
                ? err
-               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream, threads);
+               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid,
+                    groups + ring_bytes<T, V>(threads, 1 + gates), p, stream, threads);
   }
-  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, (size_t)8 * TY * p.C, p, stream, threads);
-  if (err == cudaSuccess)
-    err = go(gdn_norm_slab_dx_kernel<T, V, M>, grid, (size_t)8 * p.G, p, stream, threads);
-  return err == cudaSuccess ? sum_parts(p, parts, stream) : err;
+  const size_t own = ((size_t)8 * TY * p.C + 15) / 16 * 16;
+  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, own + ring_bytes<T, V>(threads, 2 + gates), p,
+           stream, threads);
+  if (err != cudaSuccess) return err;
+  const int columns = p.dw || p.db ? (2 * p.C + 31) / 32 : 0;
+  const size_t room = groups + ring_bytes<T, V>(threads, 2 + gates), least = (size_t)33 * threads / 8;
+  return go(gdn_norm_slab_dx_kernel<T, V, M>,
+            dim3(p.slabs, (unsigned)p.N + (columns + p.slabs - 1) / p.slabs),
+            room > least ? room : least, p, stream, threads);
 }
 
 // The widest vectors: an instance for each activation.
@@ -972,7 +1218,7 @@ size_t gdn_group_norm_workspace_size(int32_t batch, int32_t spatial, int32_t cha
   if (batch <= 0 || spatial <= 0 || channels <= 0 || groups <= 0) return 0;
   // partial sums of dweight and dbias, and of the groups of every slab
   using namespace gdn::norm;
-  const size_t parts = use_slabs(batch, spatial) ? (size_t)(kParts + batch) : (size_t)kParts;
+  const size_t parts = use_slabs(batch, spatial) ? (size_t)(2 * kSMs + batch) : (size_t)kParts;
   return parts * ((size_t)8 * channels + (size_t)12 * groups);
 }
 
