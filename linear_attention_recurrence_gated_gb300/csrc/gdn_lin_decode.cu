@@ -5,8 +5,11 @@
 //
 // The step reads and writes each state once and does 5 dk dv operations on
 // it, so it is bound by HBM bandwidth (by latency for a few sequences).  One
-// CTA of 256 threads owns a 32-column slice of one head's state: thread t
-// holds columns 4 (t % 8) .. +3 of rows t / 8 + 32 m in registers.
+// CTA of 256 threads owns COLS columns of one head's state: thread t holds
+// columns 4 (t % (COLS/4)) .. +3 of rows t / (COLS/4) + m rows apart in
+// registers.  32 columns for few heads (more CTAs), 64 where there are enough:
+// the page number is one more latency ahead of the state, and twice the bytes on
+// their way cover it.
 #include "gdn_lin.cuh"
 
 namespace gdn {
@@ -14,7 +17,6 @@ namespace lin {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCols = 32;
 
 struct DecodeParams {
   const void *q, *k, *v;
@@ -28,15 +30,15 @@ struct DecodeParams {
   int32_t num_heads, dk, dv, num_pages;
 };
 
-template <typename T, int DKT>
+template <typename T, int DKT, int COLS>
 __global__ void __launch_bounds__(kThreads)
 gdn_lin_decode_kernel(const DecodeParams p) {
-  constexpr int RPT = DKT / 32;
+  constexpr int kCols = COLS, LANES = COLS / 4, ROWS = kThreads / LANES, RPT = DKT / ROWS;
   __shared__ float sk[DKT], sq[DKT];
   __shared__ float part[8][kCols];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tile = blockIdx.x, h = blockIdx.y, n = blockIdx.z;
-  const int dv = p.dv, cg = tid & 7, rg = tid >> 3, col = tile * kCols + 4 * cg;
+  const int dv = p.dv, cg = tid % LANES, rg = tid / LANES, col = tile * kCols + 4 * cg;
   const size_t head = (size_t)n * p.num_heads + h;
   T *o = static_cast<T *>(p.o) + head * dv + tile * kCols;
 
@@ -51,7 +53,7 @@ gdn_lin_decode_kernel(const DecodeParams p) {
   float4 s[RPT];
 #pragma unroll
   for (int m = 0; m < RPT; ++m)
-    s[m] = p.s_in ? *reinterpret_cast<const float4 *>(p.s_in + base + (size_t)(rg + 32 * m) * dv)
+    s[m] = p.s_in ? *reinterpret_cast<const float4 *>(p.s_in + base + (size_t)(rg + ROWS * m) * dv)
                   : make_float4(0.f, 0.f, 0.f, 0.f);
   const T *v = static_cast<const T *>(p.v) + head * dv + col;
   const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);
@@ -64,7 +66,7 @@ gdn_lin_decode_kernel(const DecodeParams p) {
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int m = 0; m < RPT; ++m) {
-    const int i = rg + 32 * m;
+    const int i = rg + ROWS * m;
     const float ki = sk[i], qi = sq[i];
     float4 x = s[m];
     x.x = fmaf(lam, x.x, ki * v0);
@@ -77,15 +79,15 @@ gdn_lin_decode_kernel(const DecodeParams p) {
     a.z = fmaf(qi, x.z, a.z);
     a.w = fmaf(qi, x.w, a.w);
   }
-  // lanes cg, cg + 8, cg + 16, cg + 24 hold the same columns
+  // lanes cg, cg + LANES, ... hold the same columns
 #pragma unroll
-  for (int off = 8; off < 32; off <<= 1) {
+  for (int off = LANES; off < 32; off <<= 1) {
     a.x += __shfl_xor_sync(0xffffffffu, a.x, off);
     a.y += __shfl_xor_sync(0xffffffffu, a.y, off);
     a.z += __shfl_xor_sync(0xffffffffu, a.z, off);
     a.w += __shfl_xor_sync(0xffffffffu, a.w, off);
   }
-  if (lane < 8) *reinterpret_cast<float4 *>(&part[warp][4 * lane]) = a;
+  if (lane < LANES) *reinterpret_cast<float4 *>(&part[warp][4 * lane]) = a;
   __syncthreads();
   if (tid < kCols) {
     float r = 0.f;
@@ -95,21 +97,28 @@ gdn_lin_decode_kernel(const DecodeParams p) {
   }
 }
 
-template <typename T>
-cudaError_t launch_t(const DecodeParams &p, int num_seqs, cudaStream_t stream) {
-  const dim3 grid(p.dv / kCols, p.num_heads, num_seqs);
+template <typename T, int COLS>
+cudaError_t launch_c(const DecodeParams &p, int num_seqs, cudaStream_t stream) {
+  const dim3 grid(p.dv / COLS, p.num_heads, num_seqs);
   switch (p.dk) {
-    case 32: gdn_lin_decode_kernel<T, 32><<<grid, kThreads, 0, stream>>>(p); break;
-    case 64: gdn_lin_decode_kernel<T, 64><<<grid, kThreads, 0, stream>>>(p); break;
-    case 96: gdn_lin_decode_kernel<T, 96><<<grid, kThreads, 0, stream>>>(p); break;
-    case 128: gdn_lin_decode_kernel<T, 128><<<grid, kThreads, 0, stream>>>(p); break;
-    case 160: gdn_lin_decode_kernel<T, 160><<<grid, kThreads, 0, stream>>>(p); break;
-    case 192: gdn_lin_decode_kernel<T, 192><<<grid, kThreads, 0, stream>>>(p); break;
-    case 224: gdn_lin_decode_kernel<T, 224><<<grid, kThreads, 0, stream>>>(p); break;
-    case 256: gdn_lin_decode_kernel<T, 256><<<grid, kThreads, 0, stream>>>(p); break;
+    case 32: gdn_lin_decode_kernel<T, 32, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 64: gdn_lin_decode_kernel<T, 64, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 96: gdn_lin_decode_kernel<T, 96, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 128: gdn_lin_decode_kernel<T, 128, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 160: gdn_lin_decode_kernel<T, 160, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 192: gdn_lin_decode_kernel<T, 192, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 224: gdn_lin_decode_kernel<T, 224, COLS><<<grid, kThreads, 0, stream>>>(p); break;
+    case 256: gdn_lin_decode_kernel<T, 256, COLS><<<grid, kThreads, 0, stream>>>(p); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
+}
+// 64 columns a CTA where that still gives every SM two rounds of eight CTAs.
+template <typename T>
+cudaError_t launch_t(const DecodeParams &p, int num_seqs, cudaStream_t stream) {
+  const int64_t ctas = (int64_t)(p.dv / 64) * p.num_heads * num_seqs;
+  return p.dv % 64 == 0 && ctas >= 16 * kSMs ? launch_c<T, 64>(p, num_seqs, stream)
+                                             : launch_c<T, 32>(p, num_seqs, stream);
 }
 
 bool aligned16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }

@@ -256,12 +256,21 @@ __global__ void __launch_bounds__(kCopy) copy_pages_kernel(const Params p, int p
     const int64_t at = (w % pieces) * piece_bytes;
     const int64_t left = p.page_bytes - at, bytes = left < piece_bytes ? left : piece_bytes;
     uint4 *to = reinterpret_cast<uint4 *>(p.pool + (int64_t)job.y * p.page_bytes + at);
+    const int n = (int)(bytes / 16);
     if (job.x == kZero) {
-      for (int64_t i = threadIdx.x; i < bytes / 16; i += kCopy) to[i] = make_uint4(0, 0, 0, 0);
+      for (int i = threadIdx.x; i < n; i += kCopy) to[i] = make_uint4(0, 0, 0, 0);
     } else {
       const uint4 *from =
           reinterpret_cast<const uint4 *>(p.pool + (int64_t)job.x * p.page_bytes + at);
-      for (int64_t i = threadIdx.x; i < bytes / 16; i += kCopy) to[i] = from[i];
+      int i = threadIdx.x;
+      for (; i + 7 * kCopy < n; i += 8 * kCopy) {  // eight loads on their way
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __ldcs(from + i + k * kCopy);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) to[i + k * kCopy] = x[k];
+      }
+      for (; i < n; i += kCopy) to[i] = from[i];
     }
   }
 }

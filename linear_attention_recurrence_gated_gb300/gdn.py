@@ -675,70 +675,105 @@ def gdn_bwd(q, k, v, g, beta, d_o, initial_state=None, cu_seqlens=None, d_final_
 
 # ---------------------------------------------------------------------------
 # Linear attention with a decay for each head, group norm, pages of states
+#
+# These calls are also made for single tokens, where a step takes a few
+# microseconds on the GPU: each looks its arguments over in one expression and
+# names what is wrong (`_explain`) only if something is.
 # ---------------------------------------------------------------------------
-def _use(where, tensors, contiguous=True):
-    """Every tensor given (name -> tensor or None) is on a CUDA device and, if
-    asked for, contiguous."""
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+_calls = {}
+
+
+def _call(name):
+    """The library's function of this name."""
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(lib(), name)
+    return f
+
+
+def _dense(*tensors):
+    """Every tensor given (None: not given) is a contiguous CUDA tensor."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.is_contiguous()):
+            return False
+    return True
+
+
+def _explain(where, tensors, specs, lists=()):
+    """Raise for the first thing wrong: ``tensors`` name -> tensor (or None) that
+    must be contiguous on a CUDA device; ``specs`` name -> (tensor, shape, dtype);
+    ``lists``: names whose tensors must be lists of one length."""
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{where}: {name} must be on a CUDA device")
-        if contiguous and not t.is_contiguous():
+        if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
+    for name, (t, shape, dtype) in specs.items():
+        if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+            kind = TypeError if t.dtype != dtype and dtype == _I32 else ValueError
+            raise kind(f"{where}: {name} must be {str(dtype).split('.')[-1]} {list(shape)}")
+    raise ValueError(f"{where}: {', '.join(lists) or 'arguments'} do not match in shape or dtype")
 
 
-def _like(where, name, t, shape, dtype):
-    """``t`` (may be None) has this shape and dtype."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]} {list(shape)}")
+def _fits(t, shape, dtype):
+    return t is None or (t.dtype == dtype and t.shape == shape)
 
 
-class _Made:
-    """Makes a call's outputs and workspace on the stream that the call runs on,
-    so that the allocator orders their reuse after it."""
-
-    def __init__(self, stream, device):
-        self.stream, self.device = stream, device
-
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def workspace(self, given, size, status):
-        """``given``, or a new one; its status word is zeroed if it will be read."""
-        if given is not None:
-            return given
-        ws = self.empty(size, torch.uint8)
-        if status:
-            ws_head = ws[:256]
-            if self.stream is None:
-                ws_head.zero_()
-            else:
-                with torch.cuda.stream(self.stream):
-                    ws_head.zero_()
-        return ws
+def _raw_stream(stream, device):
+    """The CUDA stream handle: of ``stream``, or the current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _finish(where, st, check, workspace, stream):
-    if st != GDN_OK:
-        raise GdnError(st, where)
-    if check:
-        st = gdn_check(workspace, stream)
-        if st != GDN_OK:
-            raise GdnError(st, f"{where} (device)")
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _empty(stream, like, shape, dtype):
+    """A new tensor for the call's results, made on the stream that the call runs
+    on, so that the allocator orders its reuse after it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(stream, like, given, size, status):
+    """``given``, or a new one; its status word is zeroed if it will be read."""
+    if given is not None:
+        return given
+    ws = _empty(stream, like, (size,), _U8)
+    if status:
+        if stream is None:
+            ws[:256].zero_()
+        else:
+            with torch.cuda.stream(stream):
+                ws[:256].zero_()
+    return ws
 
 
 def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+def _done(where, st, check, workspace, stream):
+    if st:
+        raise GdnError(st, where)
+    if check:
+        st = gdn_check(workspace, stream)
+        if st:
+            raise GdnError(st, f"{where} (device)")
+
+
 def _row_stride(where, name, t):
     """Elements from one token row of ``t`` ``[B, T, H, D]`` to the next (rows
     contiguous, the rows of a batch one after the other)."""
     B, T, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
     s = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else H * D)
     if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or s < H * D or \
             (B > 1 and T > 0 and t.stride(0) != T * s):
@@ -748,28 +783,41 @@ def _row_stride(where, name, t):
     return s
 
 
-def _lin_check(where, q, k, v, log_decay, initial_state, cu_seqlens, extra):
-    """Checks shared by gdn_lin_fwd and gdn_lin_bwd; ``extra``: further tensors,
-    name -> (tensor, shape or None for the state's, dtype or None for q's)."""
+def _lin_check(where, q, k, v, log_decay, cu_seqlens, dense, specs):
+    """Checks shared by gdn_lin_fwd and gdn_lin_bwd; ``specs``: further tensors,
+    name -> (tensor, 0: the state's shape and fp32, 1: like q, 2: like v)."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError(f"{where}: q, k, v must be [B, T, H, D]")
     B, T, H, dk = q.shape
-    dv = v.shape[-1]
+    dv = v.shape[3]
     N = B if cu_seqlens is None else cu_seqlens.numel() - 1
-    _use(where, dict(q=q, k=k, v=v), contiguous=False)
-    _use(where, dict(log_decay=log_decay, initial_state=initial_state, cu_seqlens=cu_seqlens,
-                     **{n: e[0] for n, e in extra.items()}))
-    _dtype_code(q.dtype)
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError(f"{where}: q, k and v must share one storage dtype")
-    if k.shape != q.shape or v.shape[:3] != q.shape[:3]:
-        raise ValueError(f"{where}: shape mismatch among q, k, v")
-    _like(where, "log_decay", log_decay, (H,), torch.float32)
-    _like(where, "initial_state", initial_state, (N, H, dk, dv), torch.float32)
-    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1):
-        raise TypeError(f"{where}: cu_seqlens must be int32 [N + 1]")
-    for name, (t, shape, dtype) in extra.items():
-        _like(where, name, t, (N, H, dk, dv) if shape is None else shape, dtype or q.dtype)
+    dt = q.dtype
+    state = (N, H, dk, dv)
+    ok = q.is_cuda and k.is_cuda and v.is_cuda and dt in _CODES and k.dtype == dt and \
+        v.dtype == dt and k.shape == q.shape and v.shape[:3] == q.shape[:3] and \
+        _dense(log_decay, cu_seqlens, *dense) and log_decay.dtype == _F32 and \
+        log_decay.shape == (H,) and (cu_seqlens is None or (cu_seqlens.dtype == _I32 and
+                                                            cu_seqlens.dim() == 1))
+    if ok:
+        for t, kind in specs.values():
+            if t is not None and not (_fits(t, state, _F32) if kind == 0 else
+                                      _fits(t, q.shape if kind == 1 else v.shape, dt)):
+                ok = False
+                break
+    if not ok:
+        _dtype_code(dt)
+        if k.dtype != dt or v.dtype != dt:
+            raise TypeError(f"{where}: q, k and v must share one storage dtype")
+        if k.shape != q.shape or v.shape[:3] != q.shape[:3]:
+            raise ValueError(f"{where}: shape mismatch among q, k, v")
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            if not t.is_cuda:
+                raise ValueError(f"{where}: {name} must be on a CUDA device")
+        full = {n: (t, state if kind == 0 else q.shape if kind == 1 else v.shape,
+                    _F32 if kind == 0 else dt) for n, (t, kind) in specs.items()}
+        full["log_decay"] = (log_decay, (H,), _F32)
+        full["cu_seqlens"] = (cu_seqlens, (N + 1,), _I32)
+        _explain(where, {n: e[0] for n, e in full.items()}, full)
     return B, T, H, dk, dv, N
 
 
@@ -795,21 +843,21 @@ def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=No
     call synchronises and raises on a device-side error."""
     w = "gdn_lin_fwd"
     B, T, H, dk, dv, N = _lin_check(
-        w, q, k, v, log_decay, initial_state, cu_seqlens,
-        dict(o=(o, v.shape, None), final_state=(final_state, None, torch.float32)))
-    made = _Made(stream, q.device)
+        w, q, k, v, log_decay, cu_seqlens, (initial_state, o, final_state),
+        dict(initial_state=(initial_state, 0), o=(o, 2), final_state=(final_state, 0)))
     if o is None:
-        o = made.empty(v.shape, v.dtype)
+        o = _empty(stream, v, (B, T, H, dv), v.dtype)
     if final_state is None and output_final_state:
-        final_state = made.empty((N, H, dk, dv), torch.float32)
+        final_state = _empty(stream, v, (N, H, dk, dv), _F32)
     flags = GDN_FORCE_SIMT if force_simt else 0
-    workspace = made.workspace(workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
-    st = lib().gdn_lin_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                           _ptr(cu_seqlens), _ptr(o), _ptr(final_state), B, T, H, dk, dv, N,
-                           _row_stride(w, "q", q), _row_stride(w, "k", k), _row_stride(w, "v", v),
-                           _dtype_code(q.dtype), flags, _ptr(workspace), _nbytes(workspace),
-                           _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
+    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                  _p(initial_state), _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk,
+                  dv, N, _row_stride(w, "q", q), _row_stride(w, "k", k), _row_stride(w, "v", v),
+                  _CODES[q.dtype], flags, ws.data_ptr(), _nbytes(ws),
+                  _raw_stream(stream, q.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return o, final_state
 
 
@@ -823,25 +871,26 @@ def gdn_lin_bwd(q, k, v, log_decay, d_o, initial_state=None, cu_seqlens=None, d_
     leaves it out)."""
     w = "gdn_lin_bwd"
     given = grads or {}
+    dq_, dk_, dv_, dh_ = (given.get(n) for n in ("dq", "dk", "dv", "dh0"))
     B, T, H, dk, dv, N = _lin_check(
-        w, q, k, v, log_decay, initial_state, cu_seqlens,
-        dict(d_o=(d_o, v.shape, None), d_final_state=(d_final_state, None, torch.float32),
-             dq=(given.get("dq"), q.shape, None), dk=(given.get("dk"), q.shape, None),
-             dv=(given.get("dv"), v.shape, None), dh0=(given.get("dh0"), None, torch.float32)))
-    made = _Made(stream, q.device)
+        w, q, k, v, log_decay, cu_seqlens, (d_o, initial_state, d_final_state, dq_, dk_, dv_, dh_),
+        dict(d_o=(d_o, 2), initial_state=(initial_state, 0), d_final_state=(d_final_state, 0),
+             dq=(dq_, 1), dk=(dk_, 1), dv=(dv_, 2), dh0=(dh_, 0)))
     if grads is None:
-        grads = {"dq": made.empty(q.shape, q.dtype), "dk": made.empty(q.shape, q.dtype),
-                 "dv": made.empty(v.shape, v.dtype),
-                 "dh0": made.empty((N, H, dk, dv), torch.float32)}
+        qs, vs = (B, T, H, dk), (B, T, H, dv)
+        grads = {"dq": _empty(stream, q, qs, q.dtype), "dk": _empty(stream, q, qs, q.dtype),
+                 "dv": _empty(stream, q, vs, q.dtype),
+                 "dh0": _empty(stream, q, (N, H, dk, dv), _F32)}
     flags = GDN_FORCE_SIMT if force_simt else 0
-    workspace = made.workspace(workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
-    st = lib().gdn_lin_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state),
-                           _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state), _ptr(grads["dq"]),
-                           _ptr(grads["dk"]), _ptr(grads["dv"]), _ptr(grads.get("dh0")), B, T, H,
-                           dk, dv, N, _row_stride(w, "q", q), _row_stride(w, "k", k),
-                           _row_stride(w, "v", v), _dtype_code(q.dtype), flags, _ptr(workspace),
-                           _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
+    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                  _p(initial_state), _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state),
+                  grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
+                  _p(grads.get("dh0")), B, T, H, dk, dv, N, _row_stride(w, "q", q),
+                  _row_stride(w, "k", k), _row_stride(w, "v", v), _CODES[q.dtype], flags,
+                  ws.data_ptr(), _nbytes(ws), _raw_stream(stream, q.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return grads
 
 
@@ -859,57 +908,81 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
     a page number was out of range."""
     w = "gdn_lin_decode"
     N, H, dk = q.shape
-    dv = v.shape[-1]
+    dv = v.shape[2]
+    dt = q.dtype
     if state_out is None:
         if state is None:
             raise ValueError(f"{w}: give state, or state_out")
         state_out = state
     P = state_out.shape[0]
-    _use(w, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o))
-    _use(w, dict(state=state, state_out=state_out), contiguous=False)
-    _dtype_code(q.dtype)
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise TypeError(f"{w}: q, k and v must share one storage dtype")
-    if k.shape != q.shape or v.shape[:2] != (N, H):
-        raise ValueError(f"{w}: shape mismatch among q, k, v")
-    _like(w, "log_decay", log_decay, (H,), torch.float32)
-    _like(w, "pages", pages, (N,), torch.int32)
-    _like(w, "o", o, v.shape, v.dtype)
-    for name, t in (("state", state), ("state_out", state_out)):
-        _like(w, name, t, (P, H, dk, dv), torch.float32)
-        if t is not None and (not t[0].is_contiguous() or
-                              (P > 1 and t.stride(0) != state_out.stride(0))):
-            raise ValueError(f"{w}: {name} must have contiguous pages at one stride")
-    made = _Made(stream, q.device)
+    stride = state_out.stride(0) if P > 1 else 0
+    page = (H, dk, dv)
+    ok = _dense(q, k, v, log_decay, pages, o) and dt in _CODES and k.dtype == dt and \
+        v.dtype == dt and k.shape == q.shape and v.shape == (N, H, dv) and \
+        log_decay.dtype == _F32 and log_decay.shape == (H,) and \
+        _fits(pages, (N,), _I32) and _fits(o, v.shape, dt)
+    if ok:
+        for t in (state_out,) if state is state_out or state is None else (state_out, state):
+            # a page is contiguous: [H, dk, dv] packed at every stride(0)
+            if not (t.is_cuda and t.dtype == _F32 and t.shape == (P, *page) and
+                    (P <= 1 or t.stride(0) == stride) and
+                    (t.is_contiguous() or (P > 0 and t[0].is_contiguous()))):
+                ok = False
+    if not ok:
+        _dtype_code(dt)
+        if k.dtype != dt or v.dtype != dt:
+            raise TypeError(f"{w}: q, k and v must share one storage dtype")
+        if k.shape != q.shape or v.shape[:2] != (N, H):
+            raise ValueError(f"{w}: shape mismatch among q, k, v")
+        specs = dict(log_decay=(log_decay, (H,), _F32), pages=(pages, (N,), _I32),
+                     o=(o, v.shape, dt), state=(state, (P, *page), _F32),
+                     state_out=(state_out, (P, *page), _F32))
+        for name in ("state", "state_out"):
+            t = specs[name][0]
+            if t is not None and t.is_cuda and t.dim() == 4 and P > 0 and \
+                    (not t[0].is_contiguous() or (P > 1 and t.stride(0) != stride)):
+                raise ValueError(f"{w}: {name} must have contiguous pages at one stride")
+        _explain(w, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o,
+                         state=None if state is None else state[0], state_out=state_out[0]), specs)
     if o is None:
-        o = made.empty(v.shape, v.dtype)
+        o = _empty(stream, v, (N, H, dv), dt)
     if check:
-        workspace = made.workspace(workspace, 256, True)
-    st = lib().gdn_lin_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state),
-                              _ptr(state_out), _ptr(pages), _ptr(o), N, H, dk, dv, P,
-                              state_out.stride(0) if P > 1 else 0, _dtype_code(q.dtype), 0,
-                              _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
-                              _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+        workspace = _workspace(stream, v, workspace, 256, True)
+    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
+                  state_out.data_ptr(), _p(pages), o.data_ptr(), N, H, dk, dv, P, stride,
+                  _CODES[dt], 0, _p(workspace), 0 if workspace is None else _nbytes(workspace),
+                  _raw_stream(stream, q.get_device()))
+    if st or check:
+        _done(w, st, check, workspace, stream)
     return o, state_out
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_group_norm_workspace_size(batch: int, spatial: int, channels: int, groups: int) -> int:
     return int(lib().gdn_group_norm_workspace_size(batch, spatial, channels, groups))
 
 
-def _norm_check(where, x, weight, bias, groups, gate, extra):
+def _norm_check(where, x, weight, bias, gate, groups, specs):
+    """``specs``: name -> (tensor, 0: like x, 1: [N, groups] fp32, 2: [C] fp32)."""
     if x.dim() != 3:
         raise ValueError(f"{where}: x must be [N, S, C]")
     N, S, C = x.shape
-    _use(where, dict(x=x, weight=weight, bias=bias, gate=gate,
-                     **{n: e[0] for n, e in extra.items()}))
-    _dtype_code(x.dtype)
-    _like(where, "weight", weight, (C,), torch.float32)
-    _like(where, "bias", bias, (C,), torch.float32)
-    _like(where, "gate", gate, x.shape, x.dtype)
-    for name, (t, shape, dtype) in extra.items():
-        _like(where, name, t, shape, dtype)
+    dt, stat, chan = x.dtype, (N, groups), (C,)
+    ok = dt in _CODES and _dense(x, weight, bias, gate) and _fits(weight, chan, _F32) and \
+        _fits(bias, chan, _F32) and _fits(gate, x.shape, dt)
+    if ok:
+        for t, kind in specs.values():
+            if t is not None and not (t.is_cuda and t.is_contiguous() and
+                                      (_fits(t, x.shape, dt) if kind == 0 else
+                                       _fits(t, stat if kind == 1 else chan, _F32))):
+                ok = False
+                break
+    if not ok:
+        _dtype_code(dt)
+        full = {n: (t, x.shape if kind == 0 else stat if kind == 1 else chan,
+                    dt if kind == 0 else _F32) for n, (t, kind) in specs.items()}
+        full.update(weight=(weight, chan, _F32), bias=(bias, chan, _F32), gate=(gate, x.shape, dt))
+        _explain(where, {"x": x, **{n: e[0] for n, e in full.items()}}, full)
     return N, S, C
 
 
@@ -924,20 +997,18 @@ def gdn_group_norm(x, weight, bias, groups, *, gate=None, silu=False, eps=1e-5, 
     None (no factor).  Returns ``(y, mean, rstd)``, the last two ``[N, groups]``
     fp32 (kept for the backward pass)."""
     w = "gdn_group_norm"
-    f32 = torch.float32
-    N, S, C = _norm_check(w, x, weight, bias, groups, gate,
-                          dict(y=(y, x.shape, x.dtype), mean=(mean, (x.shape[0], groups), f32),
-                               rstd=(rstd, (x.shape[0], groups), f32)))
-    made = _Made(stream, x.device)
-    y = made.empty(x.shape, x.dtype) if y is None else y
-    mean = made.empty((N, groups), f32) if mean is None else mean
-    rstd = made.empty((N, groups), f32) if rstd is None else rstd
-    workspace = made.workspace(workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
-    st = lib().gdn_group_norm(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(y), _ptr(mean),
-                              _ptr(rstd), N, S, C, groups, eps, _dtype_code(x.dtype),
-                              GDN_NORM_SILU if silu else 0, _ptr(workspace), _nbytes(workspace),
-                              _stream_handle(stream))
-    _finish(w, st, False, workspace, stream)
+    N, S, C = _norm_check(w, x, weight, bias, gate, groups,
+                          dict(y=(y, 0), mean=(mean, 1), rstd=(rstd, 1)))
+    y = _empty(stream, x, (N, S, C), x.dtype) if y is None else y
+    mean = _empty(stream, x, (N, groups), _F32) if mean is None else mean
+    rstd = _empty(stream, x, (N, groups), _F32) if rstd is None else rstd
+    ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
+    st = _call(w)(x.data_ptr(), _p(weight), _p(bias), _p(gate), y.data_ptr(), mean.data_ptr(),
+                  rstd.data_ptr(), N, S, C, groups, eps, _CODES[x.dtype],
+                  GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws),
+                  _raw_stream(stream, x.get_device()))
+    if st:
+        raise GdnError(st, w)
     return y, mean, rstd
 
 
@@ -948,56 +1019,57 @@ def gdn_group_norm_bwd(x, weight, bias, groups, mean, rstd, d_y, *, gate=None, s
     without a gate), ``dweight``, ``dbias`` (fp32 ``[C]``); ``grads`` may supply
     them."""
     w = "gdn_group_norm_bwd"
-    f32 = torch.float32
     given = grads or {}
-    C = x.shape[-1]
-    N, S, C = _norm_check(w, x, weight, bias, groups, gate,
-                          dict(mean=(mean, (x.shape[0], groups), f32),
-                               rstd=(rstd, (x.shape[0], groups), f32),
-                               d_y=(d_y, x.shape, x.dtype), dx=(given.get("dx"), x.shape, x.dtype),
-                               dgate=(given.get("dgate"), x.shape, x.dtype),
-                               dweight=(given.get("dweight"), (C,), f32),
-                               dbias=(given.get("dbias"), (C,), f32)))
-    made = _Made(stream, x.device)
+    N, S, C = _norm_check(w, x, weight, bias, gate, groups,
+                          dict(mean=(mean, 1), rstd=(rstd, 1), d_y=(d_y, 0),
+                               dx=(given.get("dx"), 0), dgate=(given.get("dgate"), 0),
+                               dweight=(given.get("dweight"), 2), dbias=(given.get("dbias"), 2)))
     if grads is None:
-        grads = {"dx": made.empty(x.shape, x.dtype),
-                 "dgate": None if gate is None else made.empty(x.shape, x.dtype),
-                 "dweight": made.empty((C,), f32), "dbias": made.empty((C,), f32)}
-    workspace = made.workspace(workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
-    st = lib().gdn_group_norm_bwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), _ptr(mean),
-                                  _ptr(rstd), _ptr(d_y), _ptr(grads["dx"]),
-                                  _ptr(grads.get("dgate")), _ptr(grads.get("dweight")),
-                                  _ptr(grads.get("dbias")), N, S, C, groups, _dtype_code(x.dtype),
-                                  GDN_NORM_SILU if silu else 0, _ptr(workspace),
-                                  _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, False, workspace, stream)
+        grads = {"dx": _empty(stream, x, (N, S, C), x.dtype),
+                 "dgate": None if gate is None else _empty(stream, x, (N, S, C), x.dtype),
+                 "dweight": _empty(stream, x, (C,), _F32), "dbias": _empty(stream, x, (C,), _F32)}
+    ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
+    st = _call(w)(x.data_ptr(), _p(weight), _p(bias), _p(gate), mean.data_ptr(), rstd.data_ptr(),
+                  d_y.data_ptr(), grads["dx"].data_ptr(), _p(grads.get("dgate")),
+                  _p(grads.get("dweight")), _p(grads.get("dbias")), N, S, C, groups,
+                  _CODES[x.dtype], GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws),
+                  _raw_stream(stream, x.get_device()))
+    if st:
+        raise GdnError(st, w)
     return grads
 
 
+@functools.lru_cache(maxsize=256)
 def gdn_pages_workspace_size(num_pages: int, num_rows: int, n: int) -> int:
     return int(lib().gdn_pages_workspace_size(num_pages, num_rows, n))
 
 
 def _pages_check(where, pool, table, counts, refs, lists, outs):
-    """Returns (page bytes, pages, rows, most pages of a row)."""
-    _use(where, dict(pool=pool, table=table, counts=counts, refs=refs, **lists, **outs))
-    for name, t in dict(lists, table=table, counts=counts, refs=refs, **outs).items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{where}: {name} must be int32")
-    R, M, P = (0, 1, pool.shape[0]) if table is None else (*table.shape, refs.shape[0])
-    if table is not None:
-        _like(where, "counts", counts, (R,), torch.int32)
-        _like(where, "refs", refs, (P,), torch.int32)
-        for name, like in (("table_out", (R, M)), ("counts_out", (R,)), ("refs_out", (P,))):
-            _like(where, name, outs.get(name), like, torch.int32)
-    n = {t.numel() for t in lists.values()}
-    if len(n) > 1 or any(t.dim() != 1 for t in lists.values()):
-        raise ValueError(f"{where}: {', '.join(lists)} must be lists of one length")
-    bytes_ = 16
-    if pool is not None:
-        if pool.shape[0] != P:
+    """``lists`` and ``outs``: name -> tensor.  Returns (page bytes, pages, rows,
+    most pages of a row)."""
+    R, M = (0, 1) if table is None else table.shape
+    P = pool.shape[0] if table is None else refs.shape[0]
+    n = None
+    ok = _dense(pool, table, counts, refs, *lists.values(), *outs.values()) and \
+        (pool is None or pool.shape[0] == P)
+    if ok and table is not None:
+        ok = table.dtype == _I32 and _fits(counts, (R,), _I32) and _fits(refs, (P,), _I32)
+    for t in lists.values():
+        n = t.numel() if n is None else n
+        ok = ok and t.dtype == _I32 and t.shape == (n,)
+    shapes = dict(table_out=(R, M), counts_out=(R,), refs_out=(P,), fresh=(n,), num_live=(1,))
+    for name, t in outs.items():
+        ok = ok and _fits(t, shapes[name], _I32)
+    if not ok:
+        if pool is not None and pool.shape[0] != P:
             raise ValueError(f"{where}: refs must have one entry for each page of the pool")
-        bytes_ = _nbytes(pool) // P if P else 0
+        specs = {n_: (t, (n,), _I32) for n_, t in lists.items()}
+        specs.update({n_: (t, shapes[n_], _I32) for n_, t in outs.items()})
+        if table is not None:
+            specs.update(table=(table, (R, M), _I32), counts=(counts, (R,), _I32),
+                         refs=(refs, (P,), _I32))
+        _explain(where, dict(pool=pool, **{n_: e[0] for n_, e in specs.items()}), specs, lists)
+    bytes_ = 16 if pool is None or P == 0 else _nbytes(pool) // P
     return bytes_, P, R, M
 
 
@@ -1007,11 +1079,11 @@ def gdn_pages_copy(pool, src, dst, *, workspace=None, stream=None, check=False):
     w = "gdn_pages_copy"
     bytes_, P, _, _ = _pages_check(w, pool, None, None, None, dict(src=src, dst=dst), {})
     n = src.numel()
-    workspace = _Made(stream, pool.device).workspace(workspace, gdn_pages_workspace_size(P, 0, n),
-                                                     check)
-    st = lib().gdn_pages_copy(_ptr(pool), bytes_, P, _ptr(src), _ptr(dst), n, _ptr(workspace),
-                              _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, 0, n), check)
+    st = _call(w)(pool.data_ptr(), bytes_, P, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(),
+                  _nbytes(ws), _raw_stream(stream, pool.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return pool
 
 
@@ -1035,18 +1107,18 @@ def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, 
                                    dict(fresh=fresh, table_out=table_out, counts_out=counts_out,
                                         refs_out=refs_out))
     n = parents.numel()
-    _like(w, "fresh", fresh, (n,), torch.int32)
-    made = _Made(stream, pool.device)
-    fresh = made.empty((n,), torch.int32) if fresh is None else fresh
-    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
-    counts_out = made.empty((R,), torch.int32) if counts_out is None else counts_out
-    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
-    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, n), check)
-    st = lib().gdn_pages_fork(_ptr(pool), bytes_, P, _ptr(table), _ptr(counts), _ptr(refs), R, M,
-                              _ptr(parents), _ptr(children), n, _ptr(fresh), _ptr(table_out),
-                              _ptr(counts_out), _ptr(refs_out), _ptr(workspace),
-                              _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    fresh = _empty(stream, pool, (n,), _I32) if fresh is None else fresh
+    table_out = _empty(stream, pool, (R, M), _I32) if table_out is None else table_out
+    counts_out = _empty(stream, pool, (R,), _I32) if counts_out is None else counts_out
+    refs_out = _empty(stream, pool, (P,), _I32) if refs_out is None else refs_out
+    ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, n), check)
+    st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
+                  refs.data_ptr(), R, M, parents.data_ptr(), children.data_ptr(), n,
+                  fresh.data_ptr(), table_out.data_ptr(), counts_out.data_ptr(),
+                  refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                  _raw_stream(stream, pool.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return fresh, table_out, counts_out, refs_out
 
 
@@ -1059,15 +1131,15 @@ def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None
     _, P, R, M = _pages_check(w, None, table, counts, refs, dict(rows=rows),
                               dict(table_out=table_out, counts_out=counts_out, refs_out=refs_out))
     n = rows.numel()
-    made = _Made(stream, table.device)
-    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
-    counts_out = made.empty((R,), torch.int32) if counts_out is None else counts_out
-    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
-    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, n), check)
-    st = lib().gdn_pages_free(_ptr(table), _ptr(counts), _ptr(refs), P, R, M, _ptr(rows), n,
-                              _ptr(table_out), _ptr(counts_out), _ptr(refs_out), _ptr(workspace),
-                              _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    table_out = _empty(stream, table, (R, M), _I32) if table_out is None else table_out
+    counts_out = _empty(stream, table, (R,), _I32) if counts_out is None else counts_out
+    refs_out = _empty(stream, table, (P,), _I32) if refs_out is None else refs_out
+    ws = _workspace(stream, table, workspace, gdn_pages_workspace_size(P, R, n), check)
+    st = _call(w)(table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M, rows.data_ptr(),
+                  n, table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(),
+                  ws.data_ptr(), _nbytes(ws), _raw_stream(stream, table.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return table_out, counts_out, refs_out
 
 
@@ -1079,14 +1151,14 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     w = "gdn_pages_compact"
     bytes_, P, R, M = _pages_check(w, pool, table, counts, refs, {},
                                    dict(num_live=num_live, table_out=table_out, refs_out=refs_out))
-    _like(w, "num_live", num_live, (1,), torch.int32)
-    made = _Made(stream, pool.device)
-    num_live = made.empty((1,), torch.int32) if num_live is None else num_live
-    table_out = made.empty((R, M), torch.int32) if table_out is None else table_out
-    refs_out = made.empty((P,), torch.int32) if refs_out is None else refs_out
-    workspace = made.workspace(workspace, gdn_pages_workspace_size(P, R, 0), check)
-    st = lib().gdn_pages_compact(_ptr(pool), bytes_, P, _ptr(table), _ptr(counts), _ptr(refs), R,
-                                 M, _ptr(num_live), _ptr(table_out), _ptr(refs_out),
-                                 _ptr(workspace), _nbytes(workspace), _stream_handle(stream))
-    _finish(w, st, check, workspace, stream)
+    num_live = _empty(stream, pool, (1,), _I32) if num_live is None else num_live
+    table_out = _empty(stream, pool, (R, M), _I32) if table_out is None else table_out
+    refs_out = _empty(stream, pool, (P,), _I32) if refs_out is None else refs_out
+    ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, 0), check)
+    st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
+                  refs.data_ptr(), R, M, num_live.data_ptr(), table_out.data_ptr(),
+                  refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
+                  _raw_stream(stream, pool.get_device()))
+    if st or check:
+        _done(w, st, check, ws, stream)
     return num_live, table_out, refs_out
