@@ -50,7 +50,7 @@ struct Params {
   int64_t seq_len;     // tokens of a batch row, or of all packed sequences
   int32_t num_heads, num_seqs, num_scans;
   // Split along time (seg_len 0: none): sequences are cut into segments of
-  // seg_len tokens, a multiple of 128, each run by CTAs of its own.  A first
+  // seg_len tokens, whole chunks, each run by CTAs of its own.  A first
   // launch leaves every segment's state increment, run from zero, in seg_x
   // ([scan][slot][H][da][dc]); the second starts each segment from the states of
   // those before it, joined in order: S <- lam^len S + X.  The segments of
@@ -131,10 +131,13 @@ cudaError_t launch_tc(const Params &p, cudaStream_t stream);
 cudaError_t launch_simt(const Params &p, gdn_dtype dtype, cudaStream_t stream);
 
 // Segments for a launch of `units` CTAs per slot (value tiles and scans, times
-// heads) on a GPU that runs `width` of them at a time.  A segment costs its
-// chunks of 128 tokens, some 3 more to start, and in the first launch about 0.6
-// of its chunks (half the reads, one product of four); joining reads a state for
-// every segment before.  One segment per sequence unless a split gains a tenth.
+// heads) on a GPU that runs `width` of them at a time.  A segment costs its chunks
+// of `chunk` tokens, `start` more to begin, and in the first launch the share
+// `first` of its chunks; joining reads a state for every segment before.  One
+// segment per sequence unless a split gains a tenth.  On the tensor cores a chunk
+// of 128 tokens takes some 2 us, a CTA's start 3 of them and the first launch 0.6
+// (half the reads, one product of four); on the CUDA cores a chunk of 64 tokens
+// takes some 8 us, next to which a start is 0.4.
 struct Plan {
   int64_t seg_len;
   int32_t slots;
@@ -145,34 +148,36 @@ inline size_t split_bytes(const Plan &plan, int64_t scans, int64_t heads, int64_
   return plan.seg_len ? (size_t)(4 * scans * plan.slots * heads * dk * dv) : 0;
 }
 inline Plan plan_segments(int64_t num_seqs, int64_t seq_len, bool packed, int64_t units,
-                          int64_t width) {
+                          int64_t width, int64_t chunk, double start, double first) {
   const int64_t rows = packed ? 1 : num_seqs;           // packed: as one long row
-  if (!packed && units * num_seqs >= 4 * width) return {0, (int32_t)num_seqs};
-  const int64_t chunks = (seq_len + 127) / 128;
+  if (units * num_seqs >= 4 * width) return {0, (int32_t)num_seqs};
+  const int64_t chunks = (seq_len + chunk - 1) / chunk;
   const auto waves = [&](int64_t ctas) { return (double)((ctas + width - 1) / width); };
   // packed sequences: of their mean length, if they are not cut
   const double whole = packed ? (double)chunks / (double)num_seqs : (double)chunks;
-  double best = 0.9 * (waves(units * num_seqs) * (whole + 3));
+  double best = 0.9 * (waves(units * num_seqs) * (whole + start));
   if (packed && num_seqs * units < width)               // a single one may hold nearly all
-    best = 0.9 * (double)(chunks + 3);
+    best = 0.9 * ((double)chunks + start);
   Plan plan{0, (int32_t)num_seqs};
   for (int64_t s = 2; s <= 64 && s <= chunks; ++s) {
     const int64_t len = (chunks + s - 1) / s, count = (chunks + len - 1) / len;
     if (count < 2) continue;
-    const int64_t slots = packed ? seq_len / (128 * len) + num_seqs : rows * count;
-    const double cost = waves(units * slots) * ((double)len + 3 + 0.1 * (double)count) +
-                        waves(units * rows * (count - 1)) * (0.6 * (double)len + 3);
+    const int64_t slots = packed ? seq_len / (chunk * len) + num_seqs : rows * count;
+    const double cost =
+        waves(units * slots) * ((double)len + start + 0.03 * start * (double)count) +
+        waves(units * rows * (count - 1)) * (first * (double)len + start);
     if (cost < best) {
       best = cost;
-      plan = {128 * len, (int32_t)slots};
+      plan = {chunk * len, (int32_t)slots};
     }
   }
   return plan;
 }
 // Fills in the split of a launch of `tiles` value tiles per scan and head.
-inline void split(Params &p, int64_t tiles, int64_t width) {
+inline void split(Params &p, int64_t tiles, int64_t width, int64_t chunk, double start,
+                  double first) {
   const Plan plan = plan_segments(p.num_seqs, p.seq_len, p.cu != nullptr,
-                                  tiles * p.num_scans * p.num_heads, width);
+                                  tiles * p.num_scans * p.num_heads, width, chunk, start, first);
   const bool fits = split_bytes(plan, p.num_scans, p.num_heads, p.scan[0].da, p.scan[0].dc) <=
                     p.seg_x_bytes;
   p.seg_len = fits ? plan.seg_len : 0;

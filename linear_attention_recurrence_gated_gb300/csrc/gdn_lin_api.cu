@@ -78,8 +78,12 @@ size_t gdn_lin_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_hea
         for (bool packed : {false, true}) {
           const int64_t units = (int64_t)(d / tile) * scans * num_heads;
           if (units == 0) continue;
-          const Plan plan = plan_segments(num_seqs, seq_len, packed, units,
-                                          tile == 64 ? kSMs : kSimtWidth);
+          const Plan plan =
+              tile == 64 ? plan_segments(num_seqs, seq_len, packed, units, kSMs, 128, 3.0, 0.6)
+                         : plan_segments(num_seqs, seq_len, packed, units, kSimtWidth, 64, 0.4, 0.4);
+          const Plan wide = plan_segments(num_seqs, seq_len, packed, units, kSimtWidth, 64, 0.4, 0.4);
+          const size_t w = split_bytes(wide, scans, num_heads, head_dim_k, head_dim_v);
+          most = w > most ? w : most;
           const size_t n = split_bytes(plan, scans, num_heads, head_dim_k, head_dim_v);
           most = n > most ? n : most;
         }

@@ -2,14 +2,19 @@
 // gdn_lin.cuh in fp32, for fp32 storage and for head sizes without a
 // tensor-core form.
 //
-// One CTA owns 32 value columns of one (sequence, head) and walks its chunks
-// of 64 tokens.  Per chunk, with rows i, j of the tile and e valid rows:
+// One CTA owns NV value columns of one (sequence, head) and walks its chunks of
+// 64 tokens.  Per chunk, with rows i, j of the tile and e valid rows:
 //   P_ij = lam^|i-j| (a_i.b_j) for j <= i (j >= i backward in time), else 0
 //   o_i  = lam^(i+1) S^T a_i + sum_j P_ij c_j      (lam^(e-1-i) backward)
 //   S   <- lam^e S + sum_j lam^(e-1-j) b_j c_j^T   (lam^(j+1)   backward)
-// The state stays in shared memory in fp32; masked products are replaced by
-// zeros and rows past the sequence's end are never loaded, so nothing that
-// lies there (an infinity, a NaN of the next sequence) reaches a result.
+// The four products are fp32 fused multiply-adds on 4 x 4 register tiles: two
+// 16-byte shared loads for every sixteen of them, so the fp32 pipes bound it (a
+// chunk of 64 x 64 x 64 takes 4 x 2^18 of them, eight times what its bytes cost).
+// P and the weighting skip the half that the mask leaves out, in steps of 16.
+// S stays in registers and is put into shared memory once a chunk; masked
+// products are replaced by zeros and rows past the sequence's end are never
+// loaded, so nothing that lies there (an infinity, a NaN of the next sequence)
+// reaches a result.
 #include "gdn_lin.cuh"
 
 namespace gdn {
@@ -18,25 +23,88 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kC = 64;        // tokens per chunk
-constexpr int kCols = 32;     // value columns per CTA
-constexpr int kLd = kC + 4;   // row of the transposed tiles
+constexpr int kPd = kC + 4;   // row of P
 
-__host__ __device__ constexpr size_t smem_floats(int da) {
-  return (size_t)2 * da * kLd + kC * kCols + kC * (kC + 1) + (size_t)da * kCols + kC + 1;
+// floats of shared memory: A, B [64][da + 4], V [64][NV], P [64][68], S [da][NV],
+// lam^0 .. lam^64
+__host__ __device__ constexpr size_t smem_floats(int da, int nv, bool states) {
+  return (size_t)(states ? 1 : 2) * kC * (da + 4) + kC * nv + (states ? 0 : kC * kPd + da * nv) +
+         kC + 4;
 }
 
-// STATES: the first launch of a split along time (the state increments alone).
-template <typename T, bool STATES>
+// Rows 0 .. 63 of a tile (cols values each, rows `stride` apart in memory) into
+// shared memory, rows from e on as zeros; fp32 by asynchronous copies.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *to, int ld, const T *from, int64_t stride, int cols,
+                                          int e) {
+  const int per = cols / 4;
+  for (int x = threadIdx.x; x < kC * per; x += kThreads) {
+    const int i = x / per, k = 4 * (x % per);
+    float *dst = to + i * ld + k;
+    const T *src = from + (i < e ? i * stride + k : 0);
+    if constexpr (sizeof(T) == 4) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(dst)),
+                   "l"(src), "r"(i < e ? 16 : 0)
+                   : "memory");
+    } else {
+      uint2 v = make_uint2(0, 0);
+      if (i < e) v = *reinterpret_cast<const uint2 *>(src);
+      *reinterpret_cast<float4 *>(dst) =
+          make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                      __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+    }
+  }
+}
+__device__ __forceinline__ void loads_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+}
+
+__device__ __forceinline__ float4 at4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+// acc[u][.] += x[u][.] . y rows: rows u of x (4 values of the sum's index each)
+// times 4 rows of y
+__device__ __forceinline__ void mul44(float (&acc)[4][4], const float4 (&x)[4], const float4 (&y)[4]) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[u][0] = fmaf(xs[k], y[k].x, acc[u][0]);
+      acc[u][1] = fmaf(xs[k], y[k].y, acc[u][1]);
+      acc[u][2] = fmaf(xs[k], y[k].z, acc[u][2]);
+      acc[u][3] = fmaf(xs[k], y[k].w, acc[u][3]);
+    }
+  }
+}
+
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
+                                             *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// NV value columns a CTA; the state's rows are held RT groups of four a pass, MK
+// passes.  Where that takes fewer threads than there are (small heads), JS lanes
+// share a tile of the state, each summing every JS-th token; they add up once a
+// chunk.  STATES: the first launch of a split along time (the state increments
+// alone).
+template <typename T, int NV, int RT, int MK, bool STATES>
 __global__ void __launch_bounds__(kThreads)
 gdn_lin_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
+  constexpr int CG = NV / 4, RG = kThreads / CG;   // column and row groups of o
+  constexpr int JS = RG / RT;
   const Scan &s = p.scan[blockIdx.z % p.num_scans];
-  const int z = blockIdx.z / p.num_scans, h = blockIdx.y, col0 = blockIdx.x * kCols;
+  const int z = blockIdx.z / p.num_scans, h = blockIdx.y, col0 = blockIdx.x * NV;
   if (col0 >= s.dc) return;  // (the scans of a launch may have fewer tiles)
-  const int tid = threadIdx.x, H = p.num_heads, da = s.da, dc = s.dc;
+  const int tid = threadIdx.x, H = p.num_heads, da = s.da, dc = s.dc, ld = da + 4;
   const bool rev = s.reverse != 0;
-  float *At = sm, *Bt = At + (size_t)da * kLd, *V = Bt + (size_t)da * kLd, *P = V + kC * kCols,
-        *S = P + kC * (kC + 1), *lam = S + (size_t)da * kCols;
+  float *B = sm, *V = B + kC * ld, *lam = V + kC * NV, *A = lam + kC + 4, *P = A + kC * ld,
+        *S = P + kC * kPd;
 
   Span span;
   if (!span_of(p, z, h, span)) return;
@@ -48,143 +116,264 @@ gdn_lin_simt_kernel(const Params p) {
   const int64_t x_unit = ((int64_t)(blockIdx.z % p.num_scans) * p.slots + z) * H + h;  // of seg_x
   float *const s_out = STATES ? p.seg_x + x_unit * da * dc
                               : s.s_out && last ? s.s_out + unit * da * dc : nullptr;
-  const float ld = p.log_decay[h];
-  for (int i = tid; i <= kC; i += kThreads) lam[i] = i ? expf(ld * (float)i) : 1.f;
-  for (int i = tid; i < da * kCols; i += kThreads) {
-    const int row = i / kCols, col = col0 + i % kCols;
-    float v = STATES ? 0.f : state_in(s, unit, row, col);
-    if (!STATES)  // the segments before this one, in order
-      for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
-        const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
-        v = fmaf(expf(ld * (float)length), v,
-                 p.seg_x[(x_unit + (int64_t)(k - span.seg) * H) * da * dc + (int64_t)row * dc + col]);
+  const float rate = p.log_decay[h];
+  for (int i = tid; i <= kC; i += kThreads) lam[i] = i ? expf(rate * (float)i) : 1.f;
+
+  const int rg = tid / CG, c0 = 4 * (tid % CG);   // of o
+  // S: rows 4 rs + 4 RT m .. + 3, columns cs .. + 3, tokens js, js + JS, ...
+  const int js = tid % JS, cs = 4 * (tid / JS % CG), rs = tid / (JS * CG);
+  float st[MK][4][4];
+#pragma unroll
+  for (int m = 0; m < MK; ++m)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 4 * (rs + RT * m) + u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v = 0.f;
+        if (!STATES && row < da && js == 0) {
+          v = state_in(s, unit, row, col0 + cs + x);
+          // the segments before this one, in order
+          for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
+            const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
+            v = fmaf(expf(rate * (float)length), v,
+                     p.seg_x[(x_unit + (int64_t)(k - span.seg) * H) * da * dc + (int64_t)row * dc +
+                             col0 + cs + x]);
+          }
+        }
+        st[m][u][x] = v;
       }
-    S[i] = v;
-  }
+    }
   const T *a = static_cast<const T *>(s.a) + (int64_t)h * da;
   const T *b = static_cast<const T *>(s.b) + (int64_t)h * da;
   const T *c = static_cast<const T *>(s.c) + (int64_t)h * dc + col0;
   T *o = static_cast<T *>(s.o) + (int64_t)h * dc + col0;
 
   const int64_t nc = (len + kC - 1) / kC;
-  for (int64_t step = 0; step < nc; ++step) {
-    const int64_t t0 = (rev ? nc - 1 - step : step) * kC, tok = start + t0;
-    const int e = (int)(len - t0 < kC ? len - t0 : kC);
-    __syncthreads();  // the last chunk's reads of the tiles are done
-    for (int x = tid; x < kC * da; x += kThreads) {
-      const int i = x / da, k = x % da;
-      if (!STATES) At[k * kLd + i] = i < e ? to_f32(a[(tok + i) * s.sa + k]) : 0.f;
-      Bt[k * kLd + i] = i < e ? to_f32(b[(tok + i) * s.sb + k]) : 0.f;
-    }
-    for (int x = tid; x < kC * kCols; x += kThreads) {
-      const int i = x / kCols, j = x % kCols;
-      V[x] = i < e ? to_f32(c[(tok + i) * s.sc + j]) : 0.f;
-    }
-    __syncthreads();
-    if (!STATES) {  // P, 4 x 4 per thread
-      const int i0 = (tid >> 4) * 4, j0 = (tid & 15) * 4;
-      float acc[4][4] = {};
-      for (int k = 0; k < da; ++k) {
-        const float4 x = *reinterpret_cast<const float4 *>(At + k * kLd + i0);
-        const float4 y = *reinterpret_cast<const float4 *>(Bt + k * kLd + j0);
-        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const auto token = [&](int64_t step) { return start + (rev ? nc - 1 - step : step) * kC; };
+  const auto rows = [&](int64_t step) {
+    const int64_t left = start + len - token(step);
+    return (int)(left < kC ? left : kC);
+  };
+  if (nc > 0) {
+    if (!STATES) load_tile(A, ld, a + token(0) * s.sa, s.sa, da, rows(0));
+    load_tile(B, ld, b + token(0) * s.sb, s.sb, da, rows(0));
+    load_tile(V, NV, c + token(0) * s.sc, s.sc, NV, rows(0));
+  }
+  // every lane of a tile gets its sum; the first keeps it
+  const auto join = [&]() {
+    if constexpr (JS > 1)
+#pragma unroll
+      for (int m = 0; m < MK; ++m)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
-          for (int w = 0; w < 4; ++w) acc[u][w] = fmaf(xs[u], ys[w], acc[u][w]);
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int off = 1; off < JS; off <<= 1)
+              st[m][u][x] += __shfl_xor_sync(0xffffffffu, st[m][u][x], off);
+  };
+  for (int64_t step = 0; step < nc; ++step) {
+    const int64_t tok = token(step);
+    const int e = rows(step);
+    if (!STATES) {  // the state that this chunk reads
+      join();
+#pragma unroll
+      for (int m = 0; m < MK; ++m)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = 4 * (rs + RT * m) + u;
+          if (row < da && u % JS == js) store4(S + row * NV + cs, st[m][u]);
+        }
+    }
+    loads_done();
+    if (!STATES) {
+      {  // P: rows i = tid / 16 + 16 u, columns j = tid % 16 + 16 w
+        const int i0 = tid >> 4, j0 = tid & 15;
+        float acc[4][4] = {};
+#pragma unroll 2
+        for (int k = 0; k < da; k += 4) {
+          float4 x[4], y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            x[u] = at4(A + (i0 + 16 * u) * ld + k);
+            y[u] = at4(B + (j0 + 16 * u) * ld + k);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (!rev && w > u) continue;  // (blocks of 16 beyond the mask)
+              acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
+              acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
+              acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
+              acc[u][w] = fmaf(x[u].w, y[w].w, acc[u][w]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int i = i0 + 16 * u, j = j0 + 16 * w, d = rev ? j - i : i - j;
+            P[i * kPd + j] = d >= 0 ? acc[u][w] * lam[d] : 0.f;
+          }
       }
+      __syncthreads();
+      // o: rows rg + RG u (NV 32: two of them), columns c0 .. + 3
+      constexpr int U = kC / RG;
+      float acc[4][4] = {};
+#pragma unroll 2
+      for (int k = 0; k < da; k += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[u] = at4(A + (rg + RG * (u % U)) * ld + k);
+          y[u] = at4(S + (k + u) * NV + c0);
+        }
+        if constexpr (U == 4) {
+          mul44(acc, x, y);
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
+              acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
+              acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
+              acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = rg + RG * u;
+        const float f = i < e ? lam[rev ? e - 1 - i : i + 1] : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[u][x] *= f;
+      }
+#pragma unroll 2
+      for (int j = 0; j < kC; j += 4) {
+        float4 y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) y[u] = at4(V + (j + u) * NV + c0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = rg + RG * u;
+          const float4 x = at4(P + i * kPd + j);
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
+            acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
+            acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
+            acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = rg + RG * u;
+        if (i < e) store4(o + (tok + i) * ((int64_t)H * dc) + c0, acc[u]);
+      }
+      __syncthreads();
+    }
+    const bool more = step + 1 < nc;
+    if (!STATES && more)  // A is free: its next tile loads meanwhile
+      load_tile(A, ld, a + token(step + 1) * s.sa, s.sa, da, rows(step + 1));
+    // S <- lam^e S + sum_j b_j (w_j c_j)^T
+    const float le = STATES || js == 0 ? lam[e] : 0.f;   // (joined: the first lane's)
+#pragma unroll
+    for (int m = 0; m < MK; ++m)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int i = i0 + u, j = j0 + w, d = rev ? j - i : i - j;
-          P[i * (kC + 1) + j] = d >= 0 ? acc[u][w] * lam[d] : 0.f;
+        for (int x = 0; x < 4; ++x) st[m][u][x] *= le;
+#pragma unroll 4
+    for (int j = js; j < e; j += JS) {
+      const float w = lam[rev ? j + 1 : e - 1 - j];
+      float4 v = at4(V + j * NV + cs);
+      v.x *= w;
+      v.y *= w;
+      v.z *= w;
+      v.w *= w;
+#pragma unroll
+      for (int m = 0; m < MK; ++m) {
+        const int row = 4 * (rs + RT * m);
+        if (row < da) {
+          const float4 x = at4(B + j * ld + row);
+          const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            st[m][u][0] = fmaf(xs[u], v.x, st[m][u][0]);
+            st[m][u][1] = fmaf(xs[u], v.y, st[m][u][1]);
+            st[m][u][2] = fmaf(xs[u], v.z, st[m][u][2]);
+            st[m][u][3] = fmaf(xs[u], v.w, st[m][u][3]);
+          }
         }
-    }
-    __syncthreads();
-    if (!STATES) {  // o, 8 columns per thread
-      const int i = tid >> 2, c0 = (tid & 3) * 8;
-      float acc[8] = {};
-      for (int k = 0; k < da; ++k) {
-        const float x = At[k * kLd + i];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) acc[u] = fmaf(x, S[k * kCols + c0 + u], acc[u]);
-      }
-      if (i < e) {
-        const float f = lam[rev ? e - 1 - i : i + 1];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) acc[u] *= f;
-      }
-      for (int j = 0; j < kC; ++j) {
-        const float x = P[i * (kC + 1) + j];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) acc[u] = fmaf(x, V[j * kCols + c0 + u], acc[u]);
-      }
-      if (i < e) {
-        T *row = o + (tok + i) * ((int64_t)H * dc) + c0;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) store_out(row + u, acc[u]);
       }
     }
     __syncthreads();
-    for (int x = tid; x < kC * kCols; x += kThreads) {  // values times their weight
-      const int j = x / kCols;
-      if (j < e) V[x] *= lam[rev ? j + 1 : e - 1 - j];
-    }
-    __syncthreads();
-    {  // the state, 4 columns per thread and step of 32 rows
-      const int c0 = (tid & 7) * 4;
-      const float le = lam[e];
-      for (int k = tid >> 3; k < da; k += kThreads / 8) {
-        float4 *st = reinterpret_cast<float4 *>(S + k * kCols + c0);
-        float4 acc = *st;
-        acc.x *= le;
-        acc.y *= le;
-        acc.z *= le;
-        acc.w *= le;
-        for (int j = 0; j < kC; ++j) {
-          const float x = Bt[k * kLd + j];
-          const float4 v = *reinterpret_cast<const float4 *>(V + j * kCols + c0);
-          acc.x = fmaf(x, v.x, acc.x);
-          acc.y = fmaf(x, v.y, acc.y);
-          acc.z = fmaf(x, v.z, acc.z);
-          acc.w = fmaf(x, v.w, acc.w);
-        }
-        *st = acc;
-      }
+    if (more) {
+      load_tile(B, ld, b + token(step + 1) * s.sb, s.sb, da, rows(step + 1));
+      load_tile(V, NV, c + token(step + 1) * s.sc, s.sc, NV, rows(step + 1));
     }
   }
+  join();
   if (s_out == nullptr) return;
-  __syncthreads();
-  for (int i = tid; i < da * kCols; i += kThreads)
-    s_out[(int64_t)(i / kCols) * dc + col0 + i % kCols] = S[i];
+#pragma unroll
+  for (int m = 0; m < MK; ++m)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 4 * (rs + RT * m) + u;
+      if (row < da && u % JS == js) store4(s_out + (int64_t)row * dc + col0 + cs, st[m][u]);
+    }
 }
 
-template <typename T, bool STATES>
+template <typename T, int NV, int RT, int MK, bool STATES>
 cudaError_t run(const Params &p, int da, int dc, cudaStream_t stream) {
-  const size_t bytes = smem_floats(da) * 4;
-  const cudaError_t err = cudaFuncSetAttribute(
-      gdn_lin_simt_kernel<T, STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  const size_t bytes = smem_floats(da, NV, STATES) * 4;
+  const cudaError_t err =
+      cudaFuncSetAttribute(gdn_lin_simt_kernel<T, NV, RT, MK, STATES>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (err != cudaSuccess) return err;
-  const dim3 grid(dc / kCols, p.num_heads, p.slots * p.num_scans);
-  gdn_lin_simt_kernel<T, STATES><<<grid, kThreads, bytes, stream>>>(p);
+  const dim3 grid((dc + NV - 1) / NV, p.num_heads, p.slots * p.num_scans);
+  gdn_lin_simt_kernel<T, NV, RT, MK, STATES><<<grid, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
+}
+template <typename T, int NV, int RT, int MK>
+cudaError_t run_split(const Params &p, int da, int dc, cudaStream_t stream) {
+  if (p.seg_len) {
+    const cudaError_t err = run<T, NV, RT, MK, true>(p, da, dc, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return run<T, NV, RT, MK, false>(p, da, dc, stream);
 }
 
 template <typename T>
 cudaError_t launch_t(const Params &p, cudaStream_t stream) {
   int da = 0, dc = 0;
+  bool wide = true;   // every scan in tiles of 64 columns
   for (int i = 0; i < p.num_scans; ++i) {
     da = p.scan[i].da > da ? p.scan[i].da : da;
     dc = p.scan[i].dc > dc ? p.scan[i].dc : dc;
+    wide = wide && p.scan[i].dc % 64 == 0;
   }
+  // 64 value columns a CTA share P twice as widely, if enough CTAs are left and
+  // the tiles fit (da <= 128); 32 otherwise
+  const int64_t units = (int64_t)p.num_seqs * p.num_heads * p.num_scans;
+  wide = wide && da <= 128 && units * (dc / 64) >= kSMs / 2;
   Params on = p;
-  split(on, dc / kCols, kSimtWidth);
-  if (on.seg_len) {
-    const cudaError_t err = run<T, true>(on, da, dc, stream);
-    if (err != cudaSuccess) return err;
-  }
-  return run<T, false>(on, da, dc, stream);
+  split(on, dc / (wide ? 64 : 32), kSimtWidth, kC, 0.4, 0.4);
+  if (wide)
+    return da <= 32   ? run_split<T, 64, 8, 1>(on, da, dc, stream)
+           : da <= 64 ? run_split<T, 64, 16, 1>(on, da, dc, stream)
+                      : run_split<T, 64, 16, 2>(on, da, dc, stream);
+  return da <= 32    ? run_split<T, 32, 8, 1>(on, da, dc, stream)
+         : da <= 64  ? run_split<T, 32, 16, 1>(on, da, dc, stream)
+         : da <= 128 ? run_split<T, 32, 32, 1>(on, da, dc, stream)
+                     : run_split<T, 32, 32, 2>(on, da, dc, stream);
 }
 
 }  // namespace

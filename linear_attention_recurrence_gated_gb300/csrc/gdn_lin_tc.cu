@@ -778,7 +778,7 @@ cudaError_t launch_dk(const Params &p, cudaStream_t stream) {
     if (s.dc / 64 > args.tiles) args.tiles = s.dc / 64;
   }
   if (args.p.num_scans == 0) return cudaSuccess;
-  split(args.p, args.tiles, kSMs);
+  split(args.p, args.tiles, kSMs, kC, 3.0, 0.6);
   if (args.p.seg_len) {
     const cudaError_t err = run<DK, true>(args, stream);
     if (err != cudaSuccess) return err;
