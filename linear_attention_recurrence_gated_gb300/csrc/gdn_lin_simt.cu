@@ -93,7 +93,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
 // chunk.  STATES: the first launch of a split along time (the state increments
 // alone).
 template <typename T, int NV, int RT, int MK, bool STATES>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 gdn_lin_simt_kernel(const Params p) {
   extern __shared__ __align__(16) float sm[];
   constexpr int CG = NV / 4, RG = kThreads / CG;   // column and row groups of o
@@ -126,24 +126,49 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
   for (int m = 0; m < MK; ++m)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int row = 4 * (rs + RT * m) + u;
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        float v = 0.f;
-        if (!STATES && row < da && js == 0) {
-          v = state_in(s, unit, row, col0 + cs + x);
-          // the segments before this one, in order
-          for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
-            const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
-            v = fmaf(expf(rate * (float)length), v,
-                     p.seg_x[(x_unit + (int64_t)(k - span.seg) * H) * da * dc + (int64_t)row * dc +
-                             col0 + cs + x]);
+      for (int x = 0; x < 4; ++x) st[m][u][x] = 0.f;
+  const auto add_state = [&](const float *from, float f) {  // st <- f st + [da][dc] rows of it
+#pragma unroll
+    for (int m = 0; m < MK; ++m)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = 4 * (rs + RT * m) + u;
+        if (row < da) {
+          const float4 y = at4(from + (int64_t)row * dc + col0 + cs);
+          st[m][u][0] = fmaf(f, st[m][u][0], y.x);
+          st[m][u][1] = fmaf(f, st[m][u][1], y.y);
+          st[m][u][2] = fmaf(f, st[m][u][2], y.z);
+          st[m][u][3] = fmaf(f, st[m][u][3], y.w);
+        }
+      }
+  };
+  if (!STATES && js == 0) {
+    if (s.s_in && s.s_in_t) {
+#pragma unroll
+      for (int m = 0; m < MK; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = 4 * (rs + RT * m);
+          if (row < da) {
+            const float4 y = at4(s.s_in + unit * da * dc + (int64_t)(col0 + cs + x) * da + row);
+            st[m][0][x] = y.x;
+            st[m][1][x] = y.y;
+            st[m][2][x] = y.z;
+            st[m][3][x] = y.w;
           }
         }
-        st[m][u][x] = v;
-      }
+    } else if (s.s_in) {
+      add_state(s.s_in + unit * da * dc, 0.f);
     }
+    // the segments before this one, in order
+    for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
+      const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
+      add_state(p.seg_x + (x_unit + (int64_t)(k - span.seg) * H) * da * dc,
+                length ? expf(rate * (float)length) : 1.f);
+    }
+  }
   const T *a = static_cast<const T *>(s.a) + (int64_t)h * da;
   const T *b = static_cast<const T *>(s.b) + (int64_t)h * da;
   const T *c = static_cast<const T *>(s.c) + (int64_t)h * dc + col0;
@@ -191,7 +216,7 @@ gdn_lin_simt_kernel(const Params p) {
       {  // P: rows i = tid / 16 + 16 u, columns j = tid % 16 + 16 w
         const int i0 = tid >> 4, j0 = tid & 15;
         float acc[4][4] = {};
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < da; k += 4) {
           float4 x[4], y[4];
 #pragma unroll
@@ -222,7 +247,7 @@ gdn_lin_simt_kernel(const Params p) {
       // o: rows rg + RG u (NV 32: two of them), columns c0 .. + 3
       constexpr int U = kC / RG;
       float acc[4][4] = {};
-#pragma unroll 2
+#pragma unroll 1
       for (int k = 0; k < da; k += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -253,7 +278,7 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[u][x] *= f;
       }
-#pragma unroll 2
+#pragma unroll 1
       for (int j = 0; j < kC; j += 4) {
         float4 y[4];
 #pragma unroll
@@ -363,7 +388,7 @@ cudaError_t launch_t(const Params &p, cudaStream_t stream) {
   // 64 value columns a CTA share P twice as widely, if enough CTAs are left and
   // the tiles fit (da <= 128); 32 otherwise
   const int64_t units = (int64_t)p.num_seqs * p.num_heads * p.num_scans;
-  wide = wide && da <= 128 && units * (dc / 64) >= kSMs / 2;
+  wide = wide && da <= 128 && units * (dc / 64) >= 16;
   Params on = p;
   split(on, dc / (wide ? 64 : 32), kSimtWidth, kC, 0.4, 0.4);
   if (wide)

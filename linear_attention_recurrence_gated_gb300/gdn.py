@@ -741,6 +741,13 @@ def _empty(stream, like, shape, dtype):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _like_new(stream, t):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _workspace(stream, like, given, size, status):
     """``given``, or a new one; its status word is zeroed if it will be read."""
     if given is not None:
@@ -846,7 +853,8 @@ def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=No
         w, q, k, v, log_decay, cu_seqlens, (initial_state, o, final_state),
         dict(initial_state=(initial_state, 0), o=(o, 2), final_state=(final_state, 0)))
     if o is None:
-        o = _empty(stream, v, (B, T, H, dv), v.dtype)
+        o = _empty(stream, v, (B, T, H, dv), v.dtype) if stream is not None or \
+            not v.is_contiguous() else torch.empty_like(v)
     if final_state is None and output_final_state:
         final_state = _empty(stream, v, (N, H, dk, dv), _F32)
     flags = GDN_FORCE_SIMT if force_simt else 0
@@ -945,7 +953,7 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
         _explain(w, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o,
                          state=None if state is None else state[0], state_out=state_out[0]), specs)
     if o is None:
-        o = _empty(stream, v, (N, H, dv), dt)
+        o = _like_new(stream, v)
     if check:
         workspace = _workspace(stream, v, workspace, 256, True)
     st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
@@ -1044,6 +1052,17 @@ def gdn_pages_workspace_size(num_pages: int, num_rows: int, n: int) -> int:
     return int(lib().gdn_pages_workspace_size(num_pages, num_rows, n))
 
 
+def _pages_fine(pool, table, counts, refs, rows, *ints):
+    """The bookkeeping of a call matches (the quick look before _pages_check): all
+    tensors dense, ``rows`` (may be None) a list, ``ints`` all int32."""
+    P = refs.shape[0]
+    return _dense(pool, table, counts, refs, rows, *ints) and table.dtype == _I32 and \
+        counts.dtype == _I32 and refs.dtype == _I32 and counts.shape == table.shape[:1] and \
+        refs.dim() == 1 and (pool is None or pool.shape[0] == P) and \
+        (rows is None or (rows.dtype == _I32 and rows.dim() == 1)) and \
+        all(t is None for t in ints)
+
+
 def _pages_check(where, pool, table, counts, refs, lists, outs):
     """``lists`` and ``outs``: name -> tensor.  Returns (page bytes, pages, rows,
     most pages of a row)."""
@@ -1102,15 +1121,20 @@ def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, 
     page of child i (-1: none).  With ``check=True`` the call synchronises and
     raises if a job was left out (a bad row or too few free pages)."""
     w = "gdn_pages_fork"
-    bytes_, P, R, M = _pages_check(w, pool, table, counts, refs,
-                                   dict(parents=parents, children=children),
-                                   dict(fresh=fresh, table_out=table_out, counts_out=counts_out,
-                                        refs_out=refs_out))
-    n = parents.numel()
-    fresh = _empty(stream, pool, (n,), _I32) if fresh is None else fresh
-    table_out = _empty(stream, pool, (R, M), _I32) if table_out is None else table_out
-    counts_out = _empty(stream, pool, (R,), _I32) if counts_out is None else counts_out
-    refs_out = _empty(stream, pool, (P,), _I32) if refs_out is None else refs_out
+    if _pages_fine(pool, table, counts, refs, parents, fresh, table_out, counts_out, refs_out) and \
+            _dense(children) and children.dtype == _I32 and children.shape == parents.shape:
+        (R, M), P = table.shape, refs.shape[0]
+        bytes_ = _nbytes(pool) // P if P else 16
+    else:
+        bytes_, P, R, M = _pages_check(w, pool, table, counts, refs,
+                                       dict(parents=parents, children=children),
+                                       dict(fresh=fresh, table_out=table_out,
+                                            counts_out=counts_out, refs_out=refs_out))
+    n = parents.shape[0]
+    fresh = _like_new(stream, parents) if fresh is None else fresh
+    table_out = _like_new(stream, table) if table_out is None else table_out
+    counts_out = _like_new(stream, counts) if counts_out is None else counts_out
+    refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, n), check)
     st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
                   refs.data_ptr(), R, M, parents.data_ptr(), children.data_ptr(), n,
@@ -1128,12 +1152,16 @@ def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None
     afterwards.  Tensors and outputs as ``gdn_pages_fork``.  Returns
     ``(table_out, counts_out, refs_out)``."""
     w = "gdn_pages_free"
-    _, P, R, M = _pages_check(w, None, table, counts, refs, dict(rows=rows),
-                              dict(table_out=table_out, counts_out=counts_out, refs_out=refs_out))
-    n = rows.numel()
-    table_out = _empty(stream, table, (R, M), _I32) if table_out is None else table_out
-    counts_out = _empty(stream, table, (R,), _I32) if counts_out is None else counts_out
-    refs_out = _empty(stream, table, (P,), _I32) if refs_out is None else refs_out
+    if _pages_fine(None, table, counts, refs, rows, table_out, counts_out, refs_out):
+        (R, M), P = table.shape, refs.shape[0]
+    else:
+        _, P, R, M = _pages_check(w, None, table, counts, refs, dict(rows=rows),
+                                  dict(table_out=table_out, counts_out=counts_out,
+                                       refs_out=refs_out))
+    n = rows.shape[0]
+    table_out = _like_new(stream, table) if table_out is None else table_out
+    counts_out = _like_new(stream, counts) if counts_out is None else counts_out
+    refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, table, workspace, gdn_pages_workspace_size(P, R, n), check)
     st = _call(w)(table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M, rows.data_ptr(),
                   n, table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(),
@@ -1152,8 +1180,8 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     bytes_, P, R, M = _pages_check(w, pool, table, counts, refs, {},
                                    dict(num_live=num_live, table_out=table_out, refs_out=refs_out))
     num_live = _empty(stream, pool, (1,), _I32) if num_live is None else num_live
-    table_out = _empty(stream, pool, (R, M), _I32) if table_out is None else table_out
-    refs_out = _empty(stream, pool, (P,), _I32) if refs_out is None else refs_out
+    table_out = _like_new(stream, table) if table_out is None else table_out
+    refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, 0), check)
     st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
                   refs.data_ptr(), R, M, num_live.data_ptr(), table_out.data_ptr(),
