@@ -232,21 +232,37 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   volatile uint32_t *tmem_at = reinterpret_cast<volatile uint32_t *>(smem + L::BAR + 8 * kBars + 8);
   const Waits w{sb + L::BAR, abort_flag};
   const float ld = p.log_decay[h];
-  for (int i = tid; i < 328; i += kThreads) {
-    const int up = i - 32, down = 32 + 136 + kC - i;
-    const int e = up >= 0 && up <= kC ? up : down >= 0 && down <= kC ? down : -1;
-    lam[up] = e < 0 ? 0.f : power(ld, (float)e);
-  }
-  if (tid == 0) {
+  // the tiles of step c into its stage (one thread)
+  auto load_step = [&](int c) {
+    const int s = c % L::STAGES;
+    const int tok = (int)(start + (int64_t)tile_of(c) * kC);
+    const uint32_t stage = sb + s * L::STAGE, full = w.at(kFull + s);
+    mbar_arrive_expect_tx(full, STATES ? L::STAGE - L::B : L::STAGE);
+#pragma unroll
+    for (int u = 0; u < L::SUB; ++u) {
+      if (!STATES)
+        tma_load_3d(stage + L::A + u * kTile, &args.map[sc][0], 64 * u, h, tok, full);
+      tma_load_3d(stage + L::B + u * kTile, &args.map[sc][1], 64 * u, h, tok, full);
+    }
+    tma_load_3d(stage + L::V, &args.map[sc][2], col0, h, tok, full);
+  };
+  if (tid == 12 * 32) {
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
       const bool role = i == kVhReady || i == kVhReady + 1 ||
                         i == kClean || i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
-      // one arrival per warp; a stage is freed by both issuing warps (DK 128: one
-      // of them and the o warps)
+      // one arrival per warp; a stage is freed by the issue of X and by that of O2
+      // (or by the o warps, where they use its A tile)
       mbar_init(w.at(i), i == kPReady || i == kPReady + 1 ? 8 : role ? 4 : !STATES && i >= kEmpty && i < kPFull ? 2 : 1);
     }
     fence_mbar_init();
+    // the first tiles, ahead of the tables and of the other warps
+    for (int c = 0; c < L::STAGES && c < nc; ++c) load_step(c);
+  }
+  for (int i = tid; i < 328; i += kThreads) {
+    const int up = i - 32, down = 32 + 136 + kC - i;
+    const int e = up >= 0 && up <= kC ? up : down >= 0 && down <= kC ? down : -1;
+    lam[up] = e < 0 ? 0.f : power(ld, (float)e);
   }
   if (warp == 12) tmem_alloc(sb + L::BAR + 8 * kBars + 8, kCols);
   tc_fence_before();
@@ -268,6 +284,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     const float reach = ld < 0.f ? 3.4657f / -ld : 1e9f;   // lam^reach = 2^-5
     if (reach >= (float)after) c3 = nc - 2 - (int)(fminf(reach - (float)after, 1e9f) / kC);
   }
+  // Where the o tile of step c waits for its store: a buffer of its own, or with DK
+  // 128 (no room) the third term's, or while that is in use the A tile of the
+  // step's stage.  (Two steps apart from the first third term: the store has read
+  // the buffer before the S warps let that step's X begin.)
+  auto own_buffer = [&](int c) { return DK == 64 || c + 2 < c3; };
   // Half a row of V^ (columns 32 (t >> 6) .. + 31 of row j): w_j c_j as bf16
   // terms.  A row past the end is zeros, whatever lies there.
   const float w_full[2] = {lam[rev ? (tid & 63) + 1 : kC - 1 - (tid & 63)],
@@ -488,7 +509,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     const bool lead = warp == 4 && lane == 0;
     const CUtensorMap *mo = &args.map[sc][3];
     const float f_full = lam[rev ? kC - 1 - i : i + 1];
-    int stores = 0;  // whole tiles so far
+    int stores = 0, own_stores = 0;  // whole tiles so far
     int done = 0;
     for (int c = 0; c < nc; ++c) {
       const int e = rows_of(c);
@@ -514,15 +535,17 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       const int64_t tok = start + (int64_t)tile_of(c) * kC;
       const uint32_t stage = sb + (c % L::STAGES) * L::STAGE;
-      const uint32_t so = DK == 64 ? sb + L::O : stage + L::A;
+      const bool own = own_buffer(c);
+      const uint32_t so = DK == 64 ? sb + L::O : own ? sb + L::VH + 2 * kTile : stage + L::A;
       float f = f_full;
       if (e < kC) f = i < e ? lam[rev ? e - 1 - i : i + 1] : 0.f;
-      if (DK == 64 && e == kC) {  // the last store has read the buffer
+      if (own && e == kC) {  // the last store has read the buffer
         if (lead) {
           bulk_wait_read<0>();
           mbar_arrive(w.at(kOBuf));
         }
-        if (!wait(w, kOBuf, stores)) break;
+        if (!wait(w, kOBuf, own_stores)) break;
+        ++own_stores;
       }
       if (!wait(w, kOFull, c)) break;
       tc_fence_after();
@@ -562,9 +585,9 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         }
         ++stores;
       }
-      if (DK == 128 && lead) {
+      if (DK == 128 && lead && (!own || !own_buffer(c + 1))) {
         bulk_wait_read<0>();
-        mbar_arrive(w.at(kEmpty + c % L::STAGES));
+        if (!own) mbar_arrive(w.at(kEmpty + c % L::STAGES));
       }
     }
     if (lead) bulk_wait_all();
@@ -593,20 +616,10 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   } else if (warp == 12) {
     // ---- TMA ----
     if (lane == 0) {
-      int issued = 0;
-      for (int c = 0; c < nc; ++c) {
-        const int s = c % L::STAGES;
-        if (c >= L::STAGES && !wait(w, kEmpty + s, c / L::STAGES - 1)) break;
-        const int tok = (int)(start + (int64_t)tile_of(c) * kC);
-        const uint32_t stage = sb + s * L::STAGE, full = w.at(kFull + s);
-        mbar_arrive_expect_tx(full, STATES ? L::STAGE - L::B : L::STAGE);
-#pragma unroll
-        for (int u = 0; u < L::SUB; ++u) {
-          if (!STATES)
-            tma_load_3d(stage + L::A + u * kTile, &args.map[sc][0], 64 * u, h, tok, full);
-          tma_load_3d(stage + L::B + u * kTile, &args.map[sc][1], 64 * u, h, tok, full);
-        }
-        tma_load_3d(stage + L::V, &args.map[sc][2], col0, h, tok, full);
+      int issued = nc < L::STAGES ? nc : L::STAGES;
+      for (int c = L::STAGES; c < nc; ++c) {
+        if (!wait(w, kEmpty + c % L::STAGES, c / L::STAGES - 1)) break;
+        load_step(c);
         ++issued;
       }
       // loads still in flight land before the CTA leaves
@@ -710,7 +723,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       if (leader) {
         umma_commit(w.at(kOFull));
         umma_commit(w.at(kPFree + (c & 1)));
-        if (DK == 64) umma_commit(w.at(kEmpty + s));
+        if (own_buffer(c)) umma_commit(w.at(kEmpty + s));
       }
       __syncwarp();
       if (++s == L::STAGES) s = 0;
