@@ -249,11 +249,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   if (tid == 12 * 32) {
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
-      const bool role = i == kVhReady || i == kVhReady + 1 ||
+      const bool role = i == kPReady || i == kPReady + 1 || i == kVhReady || i == kVhReady + 1 ||
                         i == kClean || i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
       // one arrival per warp; a stage is freed by the issue of X and by that of O2
       // (or by the o warps, where they use its A tile)
-      mbar_init(w.at(i), i == kPReady || i == kPReady + 1 ? 8 : role ? 4 : !STATES && i >= kEmpty && i < kPFull ? 2 : 1);
+      mbar_init(w.at(i), role ? 4 : !STATES && i >= kEmpty && i < kPFull ? 2 : 1);
     }
     fence_mbar_init();
     // the first tiles, ahead of the tables and of the other warps
@@ -367,10 +367,8 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   // lam^|i-j| = (lam^|i - edge| lam^(16 (d-1))) lam^|edge - j| with the edge
   // between them, so 16 powers of the column, 16 of the triangle (d = 0) and a
   // running scalar serve them all, from registers.  A unit of P' (two columns a
-  // word) goes over the first half of its own P.  The last rows have eight units,
-  // the first two, and only one warp of a group reaches their lanes: so units 0 to
-  // 3 are the P' warps' and the others the V^ warps'.
-  const int l16 = lane & 15, far0 = 4;
+  // word) goes over the first half of its own P.
+  const int l16 = lane & 15;
   const int units = rev ? 8 - 2 * wq : 2 * wq + 2;
   const uint32_t half16 = lane >> 4;
   auto unit_at = [&](int k) { return rev ? 2 * wq + k : 2 * wq + 1 - k; };
@@ -421,7 +419,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
 
   if (warp < 4) {
     if constexpr (!STATES) {
-    // ---- P', the units next to the diagonal ----
+    // ---- P' ----
     uint64_t tri[8];   // (the table's zeros on the far side; they are not kept)
 #pragma unroll
     for (int x = 0; x < 8; ++x)
@@ -451,7 +449,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       drop(pk, (mine ? 0xffffu : tri_keep) & (e < 16 * unit_at(1) + 16 ? ragged(e, unit_at(1)) : ~0u));
       tmem_st8(P + 16 * unit_at(1), pk);
-      if (units > 2) far_units(P, 2, units < far0 ? units : far0, e, s_far, g);
+      if (units > 2) far_units(P, 2, units, e, s_far, g);
       const uint32_t zero[8] = {};
 #pragma unroll 1
       for (int u = rev ? 0 : 2 * wq + 2; u < (rev ? 2 * wq : 8); ++u) tmem_st8(P + 16 * u, zero);
@@ -597,21 +595,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       for (int x = 0; x < N / 4; ++x) row[x] = make_ulonglong2(s[2 * x], s[2 * x + 1]);
     }
   } else if (warp < 12) {
-    // ---- V^, then the far units of P' ----
-    const float s_far = units > far0 ? scalar_at(far0) : 0.f;
+    // ---- V^ ----
     for (int c = 0; c < nc; ++c) {
       if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, 0, tid & 127) ||
           !weigh(c, 1, tid & 127))
         break;
-      if (STATES) continue;
-      if (units > far0) {
-        if (!wait(w, kPFull + (c & 1), c >> 1)) break;
-        tc_fence_after();
-        far_units(tlane + kColP + 128 * (c & 1), far0, units, rows_of(c), s_far, g);
-        tmem_wait_st();
-        tc_fence_before();
-      }
-      warp_arrive(w.at(kPReady + (c & 1)));
     }
   } else if (warp == 12) {
     // ---- TMA ----
