@@ -59,14 +59,15 @@ struct Lay {
   // 32 zeros, lam^0 .. lam^128 (at 32), lam^128 .. lam^0 (at 168), 31 zeros
   static constexpr int TAB = O + (DK == 64 ? kTile : 0);
   static constexpr int BAR = TAB + 328 * 4;
-  static constexpr int BYTES = BAR + 256;
+  static constexpr int BYTES = BAR + 384;
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory budget");
 };
 
 // mbarriers
-enum Bar { kFull = 0, kEmpty = 3, kPFull = 6, kPReady = 8, kVhReady = 10, kPFree = 12, kXHalf = 14, kXFull,
-           kClean, kXRead, kSReady, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars = kLast + 3 };
+enum Bar { kFullA = 0, kFullB = 3, kFullV = 6, kEmptyA = 9, kEmptyB = 12, kEmptyV = 15, kPFull = 18,
+           kPReady = 20, kVhReady = 22, kPFree = 24, kXHalf = 26, kXFull, kClean, kXRead, kSReady,
+           kOFull, kOFree, kOBuf, kOWritten, kLast, kBars = kLast + 3 };
 
 struct TcArgs {
   Params p;
@@ -233,31 +234,36 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   const Waits w{sb + L::BAR, abort_flag};
   const float ld = p.log_decay[h];
   // the tiles of step c into its stage (one thread)
-  auto load_step = [&](int c) {
-    const int s = c % L::STAGES;
-    const int tok = (int)(start + (int64_t)tile_of(c) * kC);
-    const uint32_t stage = sb + s * L::STAGE, full = w.at(kFull + s);
-    mbar_arrive_expect_tx(full, STATES ? L::STAGE - L::B : L::STAGE);
+  auto load_ab = [&](int c, bool of_a) {
+    const int s = c % L::STAGES, tok = (int)(start + (int64_t)tile_of(c) * kC);
+    const uint32_t to = sb + s * L::STAGE + (of_a ? L::A : L::B), full = w.at((of_a ? kFullA : kFullB) + s);
+    mbar_arrive_expect_tx(full, L::SUB * kTile);
 #pragma unroll
-    for (int u = 0; u < L::SUB; ++u) {
-      if (!STATES)
-        tma_load_3d(stage + L::A + u * kTile, &args.map[sc][0], 64 * u, h, tok, full);
-      tma_load_3d(stage + L::B + u * kTile, &args.map[sc][1], 64 * u, h, tok, full);
-    }
-    tma_load_3d(stage + L::V, &args.map[sc][2], col0, h, tok, full);
+    for (int u = 0; u < L::SUB; ++u)
+      tma_load_3d(to + u * kTile, &args.map[sc][of_a ? 0 : 1], 64 * u, h, tok, full);
+  };
+  auto load_v = [&](int c) {
+    const int s = c % L::STAGES, tok = (int)(start + (int64_t)tile_of(c) * kC);
+    mbar_arrive_expect_tx(w.at(kFullV + s), kTile);
+    tma_load_3d(sb + s * L::STAGE + L::V, &args.map[sc][2], col0, h, tok, w.at(kFullV + s));
   };
   if (tid == 12 * 32) {
     *abort_flag = 0;
     for (int i = 0; i < kBars; ++i) {
       const bool role = i == kPReady || i == kPReady + 1 || i == kVhReady || i == kVhReady + 1 ||
                         i == kClean || i == kXRead || i == kSReady || i == kOFree || i == kOWritten;
-      // one arrival per warp; a stage is freed by the issue of X and by that of O2
-      // (or by the o warps, where they use its A tile)
-      mbar_init(w.at(i), role ? 4 : !STATES && i >= kEmpty && i < kPFull ? 2 : 1);
+      // one arrival per warp; a tile is freed by the two products that read it (V: by
+      // O2 and, through V^, by X; A: by the o warps where they use it)
+      const bool two = !STATES && i >= kEmptyA && i < kPFull;
+      mbar_init(w.at(i), role ? 4 : two ? 2 : 1);
     }
     fence_mbar_init();
     // the first tiles, ahead of the tables and of the other warps
-    for (int c = 0; c < L::STAGES && c < nc; ++c) load_step(c);
+    for (int c = 0; c < L::STAGES && c < nc; ++c) {
+      load_ab(c, false);
+      load_v(c);
+      if (!STATES) load_ab(c, true);
+    }
   }
   for (int i = tid; i < 328; i += kThreads) {
     const int up = i - 32, down = 32 + 136 + kC - i;
@@ -297,6 +303,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     const int e = rows_of(c), j = 64 * half + (t & 63), q0 = 4 * (t >> 6);
     const uint32_t stage = sb + (c % L::STAGES) * L::STAGE, v = stage + L::V;
     if (e < kC && half == 0) {  // (one ragged tile per sequence)
+      if (!wait(w, kFullB + c % L::STAGES, c / L::STAGES)) return false;
       if (t >= e) {
 #pragma unroll 1
         for (int q = 0; q < 8; ++q) {
@@ -585,7 +592,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       }
       if (DK == 128 && lead && (!own || !own_buffer(c + 1))) {
         bulk_wait_read<0>();
-        if (!own) mbar_arrive(w.at(kEmpty + c % L::STAGES));
+        if (!own) mbar_arrive(w.at(kEmptyA + c % L::STAGES));
       }
     }
     if (lead) bulk_wait_all();
@@ -597,22 +604,37 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   } else if (warp < 12) {
     // ---- V^ ----
     for (int c = 0; c < nc; ++c) {
-      if (!wait(w, kFull + c % L::STAGES, c / L::STAGES) || !weigh(c, 0, tid & 127) ||
+      if (!wait(w, kFullV + c % L::STAGES, c / L::STAGES) || !weigh(c, 0, tid & 127) ||
           !weigh(c, 1, tid & 127))
         break;
     }
   } else if (warp == 12) {
     // ---- TMA ----
     if (lane == 0) {
-      int issued = nc < L::STAGES ? nc : L::STAGES;
+      const int ahead = nc < L::STAGES ? nc : L::STAGES;
+      int in_a = STATES ? 0 : ahead, in_b = ahead, in_v = ahead;   // steps loaded
       for (int c = L::STAGES; c < nc; ++c) {
-        if (!wait(w, kEmpty + c % L::STAGES, c / L::STAGES - 1)) break;
-        load_step(c);
-        ++issued;
+        const int s = c % L::STAGES, round = c / L::STAGES - 1;
+        if (!wait(w, kEmptyB + s, round)) break;
+        load_ab(c, false);
+        ++in_b;
+        if (!STATES) {
+          if (!wait(w, kEmptyA + s, round)) break;
+          load_ab(c, true);
+          ++in_a;
+        }
+        if (!wait(w, kEmptyV + s, round)) break;
+        load_v(c);
+        ++in_v;
       }
       // loads still in flight land before the CTA leaves
-      for (int c = issued > L::STAGES ? issued - L::STAGES : 0; c < issued; ++c)
-        wait(w, kFull + c % L::STAGES, c / L::STAGES);
+      auto landed = [&](int bar, int n) {
+        for (int c = n > L::STAGES ? n - L::STAGES : 0; c < n; ++c)
+          wait(w, bar + c % L::STAGES, c / L::STAGES);
+      };
+      landed(kFullA, in_a);
+      landed(kFullB, in_b);
+      landed(kFullV, in_v);
     }
   } else if (warp == 13) {
     // ---- issue of X: the warp together, one lane elected ----
@@ -621,6 +643,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     int s = 0;
     for (int c = 0; ok && c < nc; ++c) {
       const uint32_t stage = sb + s * L::STAGE;
+      if (!(ok = wait_all(w, kFullB + s, c / L::STAGES))) break;
       // X in two halves of 64 tokens; the first two terms side by side (N = 128:
       // one read of B for both), the third onto the first
 #pragma unroll 1
@@ -643,7 +666,10 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         }
         if (leader) {
           umma_commit(w.at(half ? kXFull : kXHalf));
-          if (half) umma_commit(w.at(kEmpty + s));
+          if (half) {
+            umma_commit(w.at(kEmptyB + s));
+            umma_commit(w.at(kEmptyV + s));
+          }
         }
         __syncwarp();
       }
@@ -662,7 +688,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     for (int c = 0; c < nc; ++c) {
       const uint32_t stage = sb + s * L::STAGE;
       // the P buffer is free once O2 of the chunk before last has read it
-      if (!wait_all(w, kFull + s, c / L::STAGES) ||
+      if (!wait_all(w, kFullA + s, c / L::STAGES) || !wait_all(w, kFullB + s, c / L::STAGES) ||
           (c >= 2 && !wait_all(w, kPFree + (c & 1), (c >> 1) - 1)) ||
           (rows_of(c) < kC && !wait_all(w, kClean, 0)))
         break;
@@ -674,7 +700,11 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int kk = 0; kk < 4; ++kk)
           mma(leader, tmem + kColP + 128 * (c & 1), da + u * (kTile >> 4) + 2 * kk,
               db + u * (kTile >> 4) + 2 * kk, umma_idesc_bf16(128, 128), u + kk > 0);
-      if (leader) umma_commit(w.at(kPFull + (c & 1)));
+      if (leader) {
+        umma_commit(w.at(kPFull + (c & 1)));
+        umma_commit(w.at(kEmptyA + s));
+        umma_commit(w.at(kEmptyB + s));
+      }
       __syncwarp();
       if (++s == L::STAGES) s = 0;
     }
@@ -690,7 +720,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     for (int c = 0; c < nc; ++c) {
       const uint32_t stage = sb + s * L::STAGE;
       if (!wait_all(w, kSReady, c) || (c > 0 && !wait_all(w, kOFree, c - 1)) ||
-          !wait_all(w, kFull + s, c / L::STAGES))
+          !wait_all(w, kFullA + s, c / L::STAGES))
         break;
       tc_fence_after();
       const uint64_t da = umma_desc_sw128(stage + L::A), ds = umma_desc_sw128_mn(sb + L::S, 8192),
@@ -701,7 +731,9 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int kk = 0; kk < 4; ++kk)
           mma(leader, tmem + kColO1, da + u * (kTile >> 4) + 2 * kk, ds + 512 * u + 128 * kk,
               umma_idesc_bf16(128, 64, 0, 1), u + kk > 0);
-      if (!wait_all(w, kPReady + (c & 1), c >> 1)) break;
+      if (leader && own_buffer(c)) umma_commit(w.at(kEmptyA + s));
+      __syncwarp();
+      if (!wait_all(w, kPReady + (c & 1), c >> 1) || !wait_all(w, kFullV + s, c / L::STAGES)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int kk = 0; kk < kC / 16; ++kk)
@@ -711,7 +743,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       if (leader) {
         umma_commit(w.at(kOFull));
         umma_commit(w.at(kPFree + (c & 1)));
-        if (own_buffer(c)) umma_commit(w.at(kEmpty + s));
+        umma_commit(w.at(kEmptyV + s));
       }
       __syncwarp();
       if (++s == L::STAGES) s = 0;
