@@ -67,7 +67,7 @@ struct Lay {
 // mbarriers
 enum Bar { kFullA = 0, kFullB = 3, kFullV = 6, kEmptyA = 9, kEmptyB = 12, kEmptyV = 15, kPFull = 18,
            kPReady = 20, kVhReady = 22, kPFree = 24, kXHalf = 26, kXFull, kClean, kXRead, kSReady,
-           kOFull, kOFree, kOBuf, kOWritten, kLast, kBars = kLast + 3 };
+           kSRead, kOFull, kOFree, kOBuf, kOWritten, kLast, kBars = kLast + 3 };
 
 struct TcArgs {
   Params p;
@@ -552,9 +552,12 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         if (!wait(w, kOBuf, own_stores)) break;
         ++own_stores;
       }
+      if (c + 1 < nc) {
+        if (!wait(w, kSRead, c)) break;   // O1 has read the last state
+        put();
+      }
       if (!wait(w, kOFull, c)) break;
       tc_fence_after();
-      if (c + 1 < nc) put();   // O1 has read the last state
       ++done;
       uint4 *row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(scan.o) +
                                              ((tok + i) * H + h) * dc + col0);
@@ -731,7 +734,10 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         for (int kk = 0; kk < 4; ++kk)
           mma(leader, tmem + kColO1, da + u * (kTile >> 4) + 2 * kk, ds + 512 * u + 128 * kk,
               umma_idesc_bf16(128, 64, 0, 1), u + kk > 0);
-      if (leader && own_buffer(c)) umma_commit(w.at(kEmptyA + s));
+      if (leader) {
+        umma_commit(w.at(kSRead));
+        if (own_buffer(c)) umma_commit(w.at(kEmptyA + s));
+      }
       __syncwarp();
       if (!wait_all(w, kPReady + (c & 1), c >> 1) || !wait_all(w, kFullV + s, c / L::STAGES)) break;
       tc_fence_after();
