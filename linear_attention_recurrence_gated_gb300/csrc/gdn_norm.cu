@@ -505,24 +505,28 @@ gdn_norm_bwd_kernel(const Params p) {
   }
 }
 
-// dw and db: 32 columns a CTA, its rows of threads over the partial sums, both in
+// dw and db: W columns for a CTA, its rows of threads over the partial sums, both in
 // a fixed order.
+template <int W>
 __device__ __forceinline__ void sum_columns(const Params &p, int parts, int col0, float *sm) {
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, rows = blockDim.x >> 5, i = col0 + tx;
+  const int tx = threadIdx.x % W, ty = threadIdx.x / W, rows = blockDim.x / W, i = col0 + tx;
   float a = 0.f;
   if (i < 2 * p.C)
 #pragma unroll 4
     for (int k = ty; k < parts; k += rows) a += p.part[(size_t)k * 2 * p.C + i];
-  sm[ty * 33 + tx] = a;
+  sm[ty * (W + 1) + tx] = a;
   __syncthreads();
-  if (ty) return;
-  for (int k = 1; k < rows; ++k) a += sm[k * 33 + tx];
-  float *to = i < p.C ? p.dw : p.db;
-  if (i < 2 * p.C && to) to[i < p.C ? i : i - p.C] = a;
+  if (ty == 0) {
+#pragma unroll 4
+    for (int k = 1; k < rows; ++k) a += sm[k * (W + 1) + tx];
+    float *to = i < p.C ? p.dw : p.db;
+    if (i < 2 * p.C && to) to[i < p.C ? i : i - p.C] = a;
+  }
+  __syncthreads();
 }
 __global__ void __launch_bounds__(1024) gdn_norm_dwdb_kernel(const Params p, int parts) {
   __shared__ float sm[32 * 33];
-  sum_columns(p, parts, 32 * blockIdx.x, sm);
+  sum_columns<32>(p, parts, 32 * blockIdx.x, sm);
 }
 
 // ---- rows: S = 1, a group in the registers of LPG lanes -----------------------
@@ -755,12 +759,15 @@ __device__ __forceinline__ void slab_rows(const Params &p, int64_t &r0, int64_t 
   r1 = r0 + per < p.S ? r0 + per : p.S;
 }
 
-// Calls `use(row, x, dy, z)` for this thread's rows r0, r0 + step, ...  With 16-byte
+// A thread's rows first, first + step, ... below r1, of its vector at channel c: `run`
+// calls `use(at, x, dy, z)` for each, `at` its offset in a sample; with `down` they are
+// the mirror images of these rows in the slab.  With 16-byte
 // vectors the rows come through a ring in shared memory, kDepth ahead: every
 // thread copies its own vectors and reads only those, so no thread waits for
-// another, and some 100 KB are on their way to an SM at any time.  (With the next
-// two rows in registers instead, a backward pass over [4, 4096, 1280] took 79 us,
-// each thread going through 14 latencies of memory one after the other.)
+// another, and some 100 KB are on their way to an SM at any time.  `start` sends for
+// the first ones.  (With the next two rows in registers instead, a backward pass over
+// [4, 4096, 1280] took 79 us, each thread going through 14 latencies of memory one
+// after the other.)
 constexpr int kDepth = 4;
 template <typename T, int V>
 constexpr bool kRing = sizeof(T) * V == 16;
@@ -771,55 +778,75 @@ size_t ring_bytes(int threads, int tensors) {
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-template <typename T, int V, bool DY, typename F>
-__device__ __forceinline__ void for_rows(uint4 *ring, const T *xs, const T *dys, const T *zs,
-                                         bool gated, int64_t r0, int64_t r1, int64_t step,
-                                         int64_t C, int c, F use) {
-  if constexpr (kRing<T, V>) {
-    const int nt = 1 + (DY ? 1 : 0) + (gated ? 1 : 0);
-    uint4 *mine = ring + threadIdx.x;            // [stage][tensor][thread]
-    const int th = blockDim.x;
-    const uint32_t at0 = (uint32_t)__cvta_generic_to_shared(mine);
-    const auto ask = [&](int64_t r, int stage) {
-      if (r < r1) {
-        const int64_t at = r * C + c;
-        uint32_t to = at0 + 16 * th * nt * stage;
-        copy16(to, xs + at);
-        if (DY) copy16(to += 16 * th, dys + at);
-        if (gated) copy16(to += 16 * th, zs + at);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int64_t next = r0;
-#pragma unroll
-    for (int k = 0; k < kDepth - 1; ++k, next += step) ask(next, k);
-    int stage = 0, ahead = kDepth - 1;
-#pragma unroll 1
-    for (int64_t r = r0; r < r1; r += step, next += step) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
-      ask(next, ahead);
-      const uint4 *from = mine + (size_t)th * nt * stage;
-      Raw<T, V> x, dy = {}, z = {};
-      x.load(reinterpret_cast<const T *>(from));
-      if (DY) dy.load(reinterpret_cast<const T *>(from += th));
-      if (gated) z.load(reinterpret_cast<const T *>(from += th));
-      use(r, x, dy, z);
-      stage = stage + 1 == kDepth ? 0 : stage + 1;
-      ahead = ahead + 1 == kDepth ? 0 : ahead + 1;
+template <typename T, int V, bool DY>
+struct Rows {
+  const T *xs, *dys, *zs;
+  bool gated;
+  int n;               // rows
+  int64_t at, by;      // offset of the first one's channel 0, from one to the next
+  uint4 *mine;         // [stage][tensor][thread]
+  uint32_t to;
+  int th;
+  __device__ __forceinline__ Rows(uint4 *ring, const T *xs, const T *dys, const T *zs, bool gated,
+                                  int64_t C, int64_t r0, int64_t r1, int64_t first, int64_t step,
+                                  bool down)
+      : xs(xs), dys(dys), zs(zs), gated(gated),
+        n(first < r1 ? (int)((r1 - first + step - 1) / step) : 0),
+        at((down ? r0 + r1 - 1 - first : first) * C), by(down ? -step * C : step * C),
+        mine(ring + threadIdx.x), to((uint32_t)__cvta_generic_to_shared(mine)),
+        th(blockDim.x) {}
+  __device__ __forceinline__ int tensors() const { return 1 + (DY ? 1 : 0) + (gated ? 1 : 0); }
+  __device__ __forceinline__ void ask(bool there, int64_t o, int stage) const {
+    if (there) {
+      uint32_t a = to + 16 * th * tensors() * stage;
+      copy16(a, xs + o);
+      if (DY) copy16(a += 16 * th, dys + o);
+      if (gated) copy16(a += 16 * th, zs + o);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-  } else {
-#pragma unroll 4
-    for (int64_t r = r0; r < r1; r += step) {
-      const int64_t at = r * C + c;
-      Raw<T, V> x, dy = {}, z = {};
-      x.load(xs + at);
-      if (DY) dy.load(dys + at);
-      if (gated) z.load(zs + at);
-      use(r, x, dy, z);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void start(int c) const {
+    if constexpr (kRing<T, V>) {
+#pragma unroll
+      for (int k = 0; k < kDepth - 1; ++k) ask(k < n, at + k * by + c, k);
     }
   }
-}
+  template <typename F>
+  __device__ __forceinline__ void run(int c, F use) const {
+    int64_t o = at + c;
+    if constexpr (kRing<T, V>) {
+      int64_t next = o + (kDepth - 1) * by;
+      int stage = 0, ahead = kDepth - 1;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, o += by, next += by) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        ask(i + kDepth - 1 < n, next, ahead);
+        const uint4 *from = mine + th * tensors() * stage;
+        Raw<T, V> x, dy = {}, z = {};
+        x.load(reinterpret_cast<const T *>(from));
+        if (DY) dy.load(reinterpret_cast<const T *>(from += th));
+        if (gated) z.load(reinterpret_cast<const T *>(from += th));
+        use(o, x, dy, z);
+        ahead = stage;
+        stage = stage + 1 == kDepth ? 0 : stage + 1;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < n; ++i, o += by) {
+        Raw<T, V> x, dy = {}, z = {};
+        x.load(xs + o);
+        if (DY) dy.load(dys + o);
+        if (gated) z.load(zs + o);
+        use(o, x, dy, z);
+      }
+    }
+  }
+};
+// The second launch of a pair starts beside the first and sends for its first rows
+// (inputs of both); what the first has written is read after `wait_first`.
+__device__ __forceinline__ void let_second() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The slab's (count, mean relative to the group's first value, m2) of each group.
 template <typename T, int V>
@@ -835,7 +862,10 @@ gdn_norm_slab_stats_kernel(const Params p) {
   slab_rows(p, r0, r1);
   const int64_t base = (int64_t)blockIdx.y * p.S * p.C;
   const T *xs = static_cast<const T *>(p.x) + base;
+  const Rows<T, V, false> rows(ring, xs, xs, nullptr, false, p.C, r0, r1, r0 + ty, TY, false);
+  let_second();
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
+    rows.start(cv * V);
     const float x0 = to_f32(xs[(cv / DV) * p.D]);
     Stat all = {0.f, 0.f, 0.f};
     float c = 0.f, cnt = 0.f;
@@ -847,9 +877,8 @@ gdn_norm_slab_stats_kernel(const Params p) {
       cnt = 0.f;
       s1 = s2 = 0;
     };
-    for_rows<T, V, false>(
-        ring, xs, xs, nullptr, false, r0 + ty, r1, TY, p.C, cv * V,
-        [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &) {
+    rows.run(
+        cv * V, [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &) {
           if (cnt == 0.f) c = un(x.at(0)).x;
 #pragma unroll
           for (int i = 0; i < (V + 1) / 2; ++i) {
@@ -894,6 +923,9 @@ gdn_norm_slab_apply_kernel(const Params p) {
   const int64_t base = n * p.S * p.C;
   const T *xs = static_cast<const T *>(p.x) + base;
   const T *zs = p.gate ? static_cast<const T *>(p.gate) + base : nullptr;
+  const Rows<T, V, false> rows(ring, xs, xs, zs, gated, p.C, r0, r1, r0 + ty, TY, true);
+  if (ty < TY) rows.start(tx * V);
+  wait_first();
   for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     Stat a = {0.f, 0.f, 0.f};
     for (int i = tid & 31; i < p.slabs; i += 32) a = join(a, in[(size_t)i * p.G + g]);
@@ -919,16 +951,16 @@ gdn_norm_slab_apply_kernel(const Params p) {
     Pair w[NP], b[NP];
     weights<V>(p.w, cv * V, true, 1.f, w);
     weights<V>(p.b, cv * V, true, 0.f, b);
-    for_rows<T, V, false>(
-        ring, xs, xs, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
-        [&](int64_t r, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &z) {
+    if (cv != tx) rows.start(cv * V);
+    rows.run(
+        cv * V, [&](int64_t at, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &z) {
           Pair y[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             const Pair d = add2(add2(x.at(i), both(-x0)), both(-mean));
             y[i] = activate2<T, M>(fma2(mul2(d, both(rstd)), w[i], b[i]), gated ? z.at(i) : 0, p);
           }
-          put<T, V>(static_cast<T *>(p.y) + base + r * p.C + cv * V, y);
+          put<T, V>(static_cast<T *>(p.y) + base + at, y);
         });
   }
 }
@@ -949,7 +981,10 @@ gdn_norm_slab_grads_kernel(const Params p) {
   const T *zs = p.gate ? static_cast<const T *>(p.gate) + base : nullptr;
   int64_t r0, r1;
   slab_rows(p, r0, r1);
+  const Rows<T, V, true> rows(ring, xs, dys, zs, gated, p.C, r0, r1, r0 + ty, TY, false);
+  let_second();
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
+    rows.start(cv * V);
     const int g = cv / DV;
     const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
     constexpr int NP = (V + 1) / 2;
@@ -958,9 +993,8 @@ gdn_norm_slab_grads_kernel(const Params p) {
     weights<V>(p.b, cv * V, true, 0.f, b);
 #pragma unroll
     for (int i = 0; i < NP; ++i) a1[i] = a2[i] = 0;
-    for_rows<T, V, true>(
-        ring, xs, dys, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
-        [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+    rows.run(
+        cv * V, [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             const Pair xh = mul2(add2(x.at(i), both(-mean)), both(rstd));
@@ -1012,14 +1046,10 @@ __global__ void __launch_bounds__(kSlabThreads, 2)
 gdn_norm_slab_dx_kernel(const Params p) {
   const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   extern __shared__ __align__(16) float sm[];
-  if (blockIdx.y >= p.N) {  // the last CTAs sum up dweight and dbias meanwhile
-    const int col0 = 32 * ((blockIdx.y - (int)p.N) * gridDim.x + blockIdx.x);
-    if (col0 < 2 * p.C) sum_columns(p, (int)p.N * p.slabs, col0, sm);
-    return;
-  }
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = slab_tx(CV), TY = slab_ty(CV);
   const int tx = tid % TX, ty = tid / TX;
+  __shared__ float cs[kSlabThreads / 8 * 9];
   float2 *sg = reinterpret_cast<float2 *>(sm);
   uint4 *ring = reinterpret_cast<uint4 *>(sm + (2 * p.G + 3) / 4 * 4);
   const int64_t n = blockIdx.y, base = n * p.S * p.C;
@@ -1028,6 +1058,9 @@ gdn_norm_slab_dx_kernel(const Params p) {
   const float inv = 1.f / ((float)p.S * (float)p.D);
   int64_t r0, r1;
   slab_rows(p, r0, r1);
+  const Rows<T, V, true> rows(ring, xs, dys, zs, gated, p.C, r0, r1, r0 + ty, TY, true);
+  if (ty < TY) rows.start(tx * V);
+  wait_first();
   const float2 *in = reinterpret_cast<const float2 *>(p.sums) + (size_t)n * p.slabs * p.G;
   for (int g = tid >> 5; g < p.G; g += blockDim.x / 32) {
     float t1 = 0.f, t2 = 0.f;
@@ -1043,6 +1076,12 @@ gdn_norm_slab_dx_kernel(const Params p) {
     }
     if ((tid & 31) == 0) sg[g] = make_float2(t1 * inv, t2 * inv);
   }
+  if (p.dw || p.db) {
+    // dweight and dbias: eight columns of the slabs' sums at a time, spread over the
+    // CTAs while their first rows are on their way
+    const int all = (int)p.N * p.slabs, id = (int)(n * p.slabs) + blockIdx.x;
+    for (int c0 = 8 * id; c0 < 2 * p.C; c0 += 8 * all) sum_columns<8>(p, all, c0, cs);
+  }
   __syncthreads();
   for (int cv = tx; cv < CV && ty < TY; cv += TX) {
     const int g = cv / DV;
@@ -1052,10 +1091,9 @@ gdn_norm_slab_dx_kernel(const Params p) {
     Pair w[NP], b[NP];
     weights<V>(p.w, cv * V, true, 1.f, w);
     weights<V>(p.b, cv * V, true, 0.f, b);
-    for_rows<T, V, true>(
-        ring, xs, dys, zs, gated, r0 + ty, r1, TY, p.C, cv * V,
-        [&](int64_t r, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
-          const int64_t at = r * p.C + cv * V;
+    if (cv != tx) rows.start(cv * V);
+    rows.run(
+        cv * V, [&](int64_t at, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
           Pair dx[NP], dz[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -1083,14 +1121,27 @@ bool use_slabs(int64_t N, int64_t S) { return N < kSMs && S > 1; }
 
 template <typename K>
 cudaError_t go(K kernel, dim3 grid, size_t bytes, const Params &p, cudaStream_t stream,
-               int threads = kThreads) {
+               int threads = kThreads, bool second = false) {
   const cudaError_t err =
       bytes > 48 * 1024
           ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
           : cudaSuccess;
   if (err != cudaSuccess) return err;
-  kernel<<<grid, threads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  if (!second) {
+    kernel<<<grid, threads, bytes, stream>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchAttribute at{};   // beside the launch before (programmatic dependent launch)
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t sum_parts(const Params &p, int parts, cudaStream_t stream) {
@@ -1130,17 +1181,14 @@ cudaError_t run_slabs(Params p, bool backward, cudaStream_t stream) {
     return err != cudaSuccess
                ? err
                : go(gdn_norm_slab_apply_kernel<T, V, M>, grid,
-                    groups + ring_bytes<T, V>(threads, 1 + gates), p, stream, threads);
+                    groups + ring_bytes<T, V>(threads, 1 + gates), p, stream, threads, true);
   }
   const size_t own = ((size_t)8 * TY * p.C + 15) / 16 * 16;
   err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, own + ring_bytes<T, V>(threads, 2 + gates), p,
            stream, threads);
   if (err != cudaSuccess) return err;
-  const int columns = p.dw || p.db ? (2 * p.C + 31) / 32 : 0;
-  const size_t room = groups + ring_bytes<T, V>(threads, 2 + gates), least = (size_t)33 * threads / 8;
-  return go(gdn_norm_slab_dx_kernel<T, V, M>,
-            dim3(p.slabs, (unsigned)p.N + (columns + p.slabs - 1) / p.slabs),
-            room > least ? room : least, p, stream, threads);
+  return go(gdn_norm_slab_dx_kernel<T, V, M>, grid, groups + ring_bytes<T, V>(threads, 2 + gates), p,
+            stream, threads, true);
 }
 
 // The widest vectors: an instance for each activation.
