@@ -1,0 +1,56 @@
+// Launches: dynamic shared memory beyond 48 KB, and pairs of launches that overlap.
+#pragma once
+
+#include <atomic>
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gdn {
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per device and size
+// class: the driver call takes a microsecond or two, a tenth of a small call.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint32_t> allowed[64];
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint32_t want = (uint32_t)bytes;
+  if (dev < 64 && allowed[dev].load(std::memory_order_acquire) >= want) return cudaSuccess;
+  err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
+  if (err != cudaSuccess || dev >= 64) return err;
+  uint32_t had = allowed[dev].load(std::memory_order_relaxed);
+  while (had < want && !allowed[dev].compare_exchange_weak(had, want, std::memory_order_release)) {
+  }
+  return cudaSuccess;
+}
+
+// Programmatic dependent launch.  The first kernel of a pair calls `let_second` as it
+// begins; the second, launched with `launch_beside`, begins as the first's CTAs leave
+// room, does what needs none of the first's results, and calls `wait_first` (the
+// hardware's wait for the end of the first) before what does.
+__device__ __forceinline__ void let_second() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_first() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename K, typename... A>
+cudaError_t launch_beside(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                          const A &...args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace gdn

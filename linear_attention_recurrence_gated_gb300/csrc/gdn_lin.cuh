@@ -118,6 +118,14 @@ __device__ __forceinline__ bool span_of(const Params &p, int z, int h, Span &s) 
   return true;
 }
 
+// A scan forward in time may leave its last state where the first one is.  Cut into
+// segments, the last one's CTA could then write it before another's has read it: the
+// first launch keeps a copy, in the last segment's place in seg_x (which has no
+// increment), and the second reads that.
+__device__ __forceinline__ bool keeps_copy(const Params &p, const Scan &s) {
+  return p.seg_len != 0 && s.s_in != nullptr && s.s_in == s.s_out;
+}
+
 // Element (i, j) of the state of (n, h) that scan s starts from.
 __device__ __forceinline__ float state_in(const Scan &s, int64_t unit, int i, int j) {
   if (s.s_in == nullptr) return 0.f;

@@ -16,6 +16,7 @@
 // loaded, so nothing that lies there (an infinity, a NaN of the next sequence)
 // reaches a result.
 #include "gdn_lin.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace lin {
@@ -95,6 +96,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
 template <typename T, int NV, int RT, int MK, bool STATES>
 __global__ void __launch_bounds__(kThreads, 2)
 gdn_lin_simt_kernel(const Params p) {
+  if (STATES) let_second();
   extern __shared__ __align__(16) float sm[];
   constexpr int CG = NV / 4, RG = kThreads / CG;   // column and row groups of o
   constexpr int JS = RG / RT;
@@ -112,8 +114,16 @@ gdn_lin_simt_kernel(const Params p) {
   const int64_t unit = (int64_t)span.n * H + h;
   // the segment whose end is the sequence's, in the scan's direction
   const bool last = span.seg == (rev ? 0 : span.count - 1);
-  if (STATES && last) return;
   const int64_t x_unit = ((int64_t)(blockIdx.z % p.num_scans) * p.slots + z) * H + h;  // of seg_x
+  if (STATES && last) {
+    if (keeps_copy(p, s))
+      for (int i = tid; i < da * NV; i += kThreads) {
+        const int j = col0 + i % NV;
+        const int64_t at = (int64_t)(i / NV) * dc + j;
+        if (j < dc) p.seg_x[x_unit * da * dc + at] = s.s_in[unit * da * dc + at];
+      }
+    return;
+  }
   float *const s_out = STATES ? p.seg_x + x_unit * da * dc
                               : s.s_out && last ? s.s_out + unit * da * dc : nullptr;
   const float rate = p.log_decay[h];
@@ -144,31 +154,6 @@ gdn_lin_simt_kernel(const Params p) {
         }
       }
   };
-  if (!STATES && js == 0) {
-    if (s.s_in && s.s_in_t) {
-#pragma unroll
-      for (int m = 0; m < MK; ++m)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 4 * (rs + RT * m);
-          if (row < da) {
-            const float4 y = at4(s.s_in + unit * da * dc + (int64_t)(col0 + cs + x) * da + row);
-            st[m][0][x] = y.x;
-            st[m][1][x] = y.y;
-            st[m][2][x] = y.z;
-            st[m][3][x] = y.w;
-          }
-        }
-    } else if (s.s_in) {
-      add_state(s.s_in + unit * da * dc, 0.f);
-    }
-    // the segments before this one, in order
-    for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
-      const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
-      add_state(p.seg_x + (x_unit + (int64_t)(k - span.seg) * H) * da * dc,
-                length ? expf(rate * (float)length) : 1.f);
-    }
-  }
   const T *a = static_cast<const T *>(s.a) + (int64_t)h * da;
   const T *b = static_cast<const T *>(s.b) + (int64_t)h * da;
   const T *c = static_cast<const T *>(s.c) + (int64_t)h * dc + col0;
@@ -184,6 +169,35 @@ gdn_lin_simt_kernel(const Params p) {
     if (!STATES) load_tile(A, ld, a + token(0) * s.sa, s.sa, da, rows(0));
     load_tile(B, ld, b + token(0) * s.sb, s.sb, da, rows(0));
     load_tile(V, NV, c + token(0) * s.sc, s.sc, NV, rows(0));
+  }
+  if (!STATES && js == 0) {
+    if (p.seg_len) wait_first();
+    if (s.s_in && s.s_in_t) {
+#pragma unroll
+      for (int m = 0; m < MK; ++m)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int row = 4 * (rs + RT * m);
+          if (row < da) {
+            const float4 y = at4(s.s_in + unit * da * dc + (int64_t)(col0 + cs + x) * da + row);
+            st[m][0][x] = y.x;
+            st[m][1][x] = y.y;
+            st[m][2][x] = y.z;
+            st[m][3][x] = y.w;
+          }
+        }
+    } else if (s.s_in) {
+      add_state(keeps_copy(p, s)
+                    ? p.seg_x + (x_unit + (int64_t)(span.count - 1 - span.seg) * H) * da * dc
+                    : s.s_in + unit * da * dc,
+                0.f);
+    }
+    // the segments before this one, in order
+    for (int k = rev ? span.count - 1 : 0; k != span.seg; k += rev ? -1 : 1) {
+      const int64_t length = k == span.count - 1 ? span.total - k * p.seg_len : p.seg_len;
+      add_state(p.seg_x + (x_unit + (int64_t)(k - span.seg) * H) * da * dc,
+                length ? expf(rate * (float)length) : 1.f);
+    }
   }
   // every lane of a tile gets its sum; the first keeps it
   const auto join = [&]() {
@@ -359,12 +373,12 @@ gdn_lin_simt_kernel(const Params p) {
 template <typename T, int NV, int RT, int MK, bool STATES>
 cudaError_t run(const Params &p, int da, int dc, cudaStream_t stream) {
   const size_t bytes = smem_floats(da, NV, STATES) * 4;
-  const cudaError_t err =
-      cudaFuncSetAttribute(gdn_lin_simt_kernel<T, NV, RT, MK, STATES>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  constexpr auto kernel = gdn_lin_simt_kernel<T, NV, RT, MK, STATES>;
+  const cudaError_t err = allow_smem<kernel>(bytes);
   if (err != cudaSuccess) return err;
   const dim3 grid((dc + NV - 1) / NV, p.num_heads, p.slots * p.num_scans);
-  gdn_lin_simt_kernel<T, NV, RT, MK, STATES><<<grid, kThreads, bytes, stream>>>(p);
+  if (!STATES && p.seg_len) return launch_beside(kernel, grid, kThreads, bytes, stream, p);
+  kernel<<<grid, kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int NV, int RT, int MK>

@@ -32,6 +32,7 @@
 // term of a sum (0 * NaN would spoil it); their P' columns are zeros by
 // selection, their o rows are not stored.
 #include "gdn_lin.cuh"
+#include "gdn_launch.cuh"
 #include "gdn_tc_common.cuh"
 
 namespace gdn {
@@ -189,6 +190,7 @@ template <int DK, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   using L = Lay<DK>;
+  if (STATES) let_second();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
@@ -210,8 +212,15 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   const int64_t unit = (int64_t)span.n * H + h;
   // the segment whose end is the sequence's, in the scan's direction
   const bool last = span.seg == (rev ? 0 : span.count - 1);
-  if (STATES && last) return;
   const int64_t x_unit = ((int64_t)sc * p.slots + z) * H + h;   // of seg_x
+  if (STATES && last) {
+    if (keeps_copy(p, scan))
+      for (int i = tid; i < DK * 64; i += kThreads) {
+        const int64_t at = (int64_t)(i >> 6) * dc + col0 + (i & 63);
+        p.seg_x[x_unit * DK * dc + at] = scan.s_in[unit * DK * dc + at];
+      }
+    return;
+  }
   float *const s_out = STATES ? p.seg_x + x_unit * DK * dc
                               : scan.s_out && last ? scan.s_out + unit * DK * dc : nullptr;
   if (len == 0) {  // the state passes through
@@ -483,13 +492,17 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         s[2 * x + 1] = fma2(pair(f, f), s[2 * x + 1], pair(y.z, y.w));
       }
     };
+    if (!STATES && p.seg_len) wait_first();
     if (!STATES && scan.s_in) {
       if (scan.s_in_t) {
         const float *at = scan.s_in + unit * DK * dc + (int64_t)(col0 + c0) * DK + si;
 #pragma unroll
         for (int x = 0; x < N / 2; ++x) s[x] = pair(at[2 * x * DK], at[(2 * x + 1) * DK]);
       } else {
-        add_row(scan.s_in + unit * DK * dc, 0.f);
+        add_row(keeps_copy(p, scan)
+                    ? p.seg_x + (x_unit + (int64_t)(span.count - 1 - span.seg) * H) * DK * dc
+                    : scan.s_in + unit * DK * dc,
+                0.f);
       }
     }
     if (!STATES)  // the segments before this one, in order
@@ -788,12 +801,13 @@ bool make_map(CUtensorMap *m, const void *ptr, int cols, int heads, int64_t toke
 
 template <int DK, bool STATES>
 cudaError_t run(const TcArgs &args, cudaStream_t stream) {
-  const cudaError_t err =
-      cudaFuncSetAttribute(gdn_lin_tc_kernel<DK, STATES>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<DK>::ALLOC);
+  constexpr auto kernel = gdn_lin_tc_kernel<DK, STATES>;
+  const cudaError_t err = allow_smem<kernel>(Lay<DK>::ALLOC);
   if (err != cudaSuccess) return err;
   const dim3 grid(args.tiles * args.p.num_scans, args.p.num_heads, args.p.slots);
-  gdn_lin_tc_kernel<DK, STATES><<<grid, kThreads, Lay<DK>::ALLOC, stream>>>(args);
+  if (!STATES && args.p.seg_len)
+    return launch_beside(kernel, grid, kThreads, Lay<DK>::ALLOC, stream, args);
+  kernel<<<grid, kThreads, Lay<DK>::ALLOC, stream>>>(args);
   return cudaGetLastError();
 }
 

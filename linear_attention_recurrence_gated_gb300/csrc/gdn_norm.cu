@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include "gdn_internal.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace norm {
@@ -843,10 +844,8 @@ struct Rows {
     }
   }
 };
-// The second launch of a pair starts beside the first and sends for its first rows
-// (inputs of both); what the first has written is read after `wait_first`.
-__device__ __forceinline__ void let_second() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The second launch of a pair sends for its first rows (inputs of both) beside the
+// first; what that has written is read after `wait_first`.
 
 // The slab's (count, mean relative to the group's first value, m2) of each group.
 template <typename T, int V>
@@ -1119,29 +1118,14 @@ int slab_count(int64_t N, int64_t S, int C, int V) {
 }
 bool use_slabs(int64_t N, int64_t S) { return N < kSMs && S > 1; }
 
-template <typename K>
-cudaError_t go(K kernel, dim3 grid, size_t bytes, const Params &p, cudaStream_t stream,
+template <auto Kernel>
+cudaError_t go(dim3 grid, size_t bytes, const Params &p, cudaStream_t stream,
                int threads = kThreads, bool second = false) {
-  const cudaError_t err =
-      bytes > 48 * 1024
-          ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)
-          : cudaSuccess;
+  const cudaError_t err = allow_smem<Kernel>(bytes);
   if (err != cudaSuccess) return err;
-  if (!second) {
-    kernel<<<grid, threads, bytes, stream>>>(p);
-    return cudaGetLastError();
-  }
-  cudaLaunchAttribute at{};   // beside the launch before (programmatic dependent launch)
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = bytes;
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  if (second) return launch_beside(Kernel, grid, threads, bytes, stream, p);
+  Kernel<<<grid, threads, bytes, stream>>>(p);
+  return cudaGetLastError();
 }
 
 cudaError_t sum_parts(const Params &p, int parts, cudaStream_t stream) {
@@ -1155,12 +1139,12 @@ cudaError_t run_rows(const Params &p, bool backward, cudaStream_t stream) {
   const RowMap m = row_map(p.G, p.D / V);
   const int gy = (p.G + m.groups - 1) / m.groups;
   int64_t gx = (p.N + m.rows - 1) / m.rows;
-  const int64_t most = backward ? (kParts / 2 + gy - 1) / gy : 8 * kSMs;
+  const int64_t most = backward ? (kParts / 2 + gy - 1) / gy : 4 * kSMs;
   if (gx > most) gx = most;
   const dim3 grid((unsigned)gx, gy);
-  if (!backward) return go(gdn_norm_rows_fwd_kernel<T, V, R, FULL, M>, grid, 0, p, stream);
+  if (!backward) return go<gdn_norm_rows_fwd_kernel<T, V, R, FULL, M>>(grid, 0, p, stream);
   const size_t bytes = (size_t)8 * m.rows * m.groups * p.D;
-  const cudaError_t err = go(gdn_norm_rows_bwd_kernel<T, V, R, FULL, M>, grid, bytes, p, stream);
+  const cudaError_t err = go<gdn_norm_rows_bwd_kernel<T, V, R, FULL, M>>(grid, bytes, p, stream);
   return err == cudaSuccess ? sum_parts(p, (int)gx, stream) : err;
 }
 
@@ -1176,18 +1160,18 @@ cudaError_t run_slabs(Params p, bool backward, cudaStream_t stream) {
   cudaError_t err;
   if (!backward) {
     const size_t own = ((size_t)12 * TY * CV + 15) / 16 * 16;
-    err = go(gdn_norm_slab_stats_kernel<T, V>, grid, own + ring_bytes<T, V>(threads, 1), p, stream,
+    err = go<gdn_norm_slab_stats_kernel<T, V>>(grid, own + ring_bytes<T, V>(threads, 1), p, stream,
              threads);
     return err != cudaSuccess
                ? err
-               : go(gdn_norm_slab_apply_kernel<T, V, M>, grid,
+               : go<gdn_norm_slab_apply_kernel<T, V, M>>(grid,
                     groups + ring_bytes<T, V>(threads, 1 + gates), p, stream, threads, true);
   }
   const size_t own = ((size_t)8 * TY * p.C + 15) / 16 * 16;
-  err = go(gdn_norm_slab_grads_kernel<T, V, M>, grid, own + ring_bytes<T, V>(threads, 2 + gates), p,
+  err = go<gdn_norm_slab_grads_kernel<T, V, M>>(grid, own + ring_bytes<T, V>(threads, 2 + gates), p,
            stream, threads);
   if (err != cudaSuccess) return err;
-  return go(gdn_norm_slab_dx_kernel<T, V, M>, grid, groups + ring_bytes<T, V>(threads, 2 + gates), p,
+  return go<gdn_norm_slab_dx_kernel<T, V, M>>(grid, groups + ring_bytes<T, V>(threads, 2 + gates), p,
             stream, threads, true);
 }
 
@@ -1217,8 +1201,8 @@ cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
     if (use_slabs(p.N, p.S)) return run_slabs<T, V, kAny>(p, backward, stream);
   const int grid = (int)(p.N < kParts ? p.N : kParts);
   if (!backward)
-    return go(gdn_norm_fwd_kernel<T, V, kAny>, grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
-  const cudaError_t err = go(gdn_norm_bwd_kernel<T, V, kAny>, grid,
+    return go<gdn_norm_fwd_kernel<T, V, kAny>>(grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
+  const cudaError_t err = go<gdn_norm_bwd_kernel<T, V, kAny>>(grid,
                              ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8, p, stream);
   return err == cudaSuccess ? sum_parts(p, grid, stream) : err;
 }

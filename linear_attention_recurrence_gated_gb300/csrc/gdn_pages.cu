@@ -15,6 +15,7 @@
 #include <stdint.h>
 
 #include "gdn_internal.cuh"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace pages {
@@ -76,7 +77,7 @@ __device__ __forceinline__ void copy_ints(int32_t *to, const int32_t *from, int6
 // tmp0: count of the job's parent, -1 for a job that is left out (num jobs);
 // tmp1: the job that owns a child row (num_rows); tmp2: the lowest free pages.
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Params p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_second();
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x, n = p.n, R = p.num_rows, M = p.max_pages;
   copy_ints(p.table_out, p.table, (int64_t)R * M);
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Params p) {
 }
 
 __global__ void __launch_bounds__(kPlan) copy_plan_kernel(const Params p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_second();
   for (int i = threadIdx.x; i < p.n; i += kPlan) {
     const int s = p.a[i], d = p.b[i];
     const bool ok = s >= 0 && s < p.num_pages && d >= 0 && d < p.num_pages;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const Params p) {
 // tmp0: the new number of every page; tmp1: the free pages below the live
 // count, ascending.  The k-th live page above it moves to the k-th of them.
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Params p) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_second();
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x, P = p.num_pages;
   int mine = 0, live;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Params p) {
 // Copies the pages of the list (and, for compact, rewrites the table).
 __global__ void __launch_bounds__(kCopy) copy_pages_kernel(const Params p, int pieces,
                                                             int64_t piece_bytes, bool rewrite) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the bookkeeping is done
+  wait_first();  // the bookkeeping is done
   if (rewrite) {
     const int64_t all = (int64_t)p.num_rows * p.max_pages;
     for (int64_t i = (int64_t)blockIdx.x * kCopy + threadIdx.x; i < all;
@@ -295,16 +296,7 @@ cudaError_t launch_copies(const Params &p, int64_t most, bool rewrite, cudaStrea
   const int64_t pieces = (p.page_bytes + piece - 1) / piece;
   const int64_t want = most * pieces;
   const int grid = (int)(want < 1 ? 1 : want < 152 * 8 ? want : 152 * 8);
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kCopy);
-  cfg.stream = stream;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, copy_pages_kernel, p, (int)pieces, piece, rewrite);
+  return launch_beside(copy_pages_kernel, dim3(grid), kCopy, 0, stream, p, (int)pieces, piece, rewrite);
 }
 
 bool aligned16(const void *x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; }

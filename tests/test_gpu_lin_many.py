@@ -94,3 +94,23 @@ def test_bad_offsets_are_reported():
         with pytest.raises(G.GdnError) as e:
             G.gdn_lin_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["s0"], cud, check=True)
         assert e.value.status == 6
+
+
+@pytest.mark.parametrize("dtype,shape", [("bf16", (1, 6000, 4, 64, 64)), ("bf16", (2, 4100, 3, 128, 128)),
+                                         ("fp32", (1, 3000, 4, 64, 64)), ("fp32", (2, 2000, 1, 32, 96)),
+                                         ("bf16", (1, 3000, 2, 32, 64))])
+def test_long_sequences_update_their_state_in_place(dtype, shape):
+    """Cut along time, with the last state written over the first."""
+    d = make(*shape, dtype, seed=7)
+    want_o, want_s = G.gdn_lin_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["s0"], check=True)
+    for _ in range(3):
+        state = d["s0"].clone()
+        o, s = G.gdn_lin_fwd(d["q"], d["k"], d["v"], d["log_decay"], state, final_state=state,
+                             check=True)
+        assert s is state and torch.equal(o, want_o) and torch.equal(s, want_s)
+    cu = torch.tensor([0, 0, shape[0] * shape[1]], dtype=torch.int32, device="cuda")
+    flat = [d[n].reshape(1, -1, *d[n].shape[2:]) for n in "qkv"]
+    state = torch.randn(2, *d["s0"].shape[1:], device="cuda")
+    want_o, want_s = G.gdn_lin_fwd(*flat, d["log_decay"], state, cu, check=True)
+    o, s = G.gdn_lin_fwd(*flat, d["log_decay"], state, cu, final_state=state, check=True)
+    assert torch.equal(o, want_o) and torch.equal(s, want_s)
