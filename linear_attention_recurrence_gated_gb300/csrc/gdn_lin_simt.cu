@@ -3,14 +3,15 @@
 // tensor-core form.
 //
 // One CTA owns NV value columns of one (sequence, head) and walks its chunks of
-// 64 tokens.  Per chunk, with rows i, j of the tile and e valid rows:
-//   P_ij = lam^|i-j| (a_i.b_j) for j <= i (j >= i backward in time), else 0
-//   o_i  = lam^(i+1) S^T a_i + sum_j P_ij c_j      (lam^(e-1-i) backward)
-//   S   <- lam^e S + sum_j lam^(e-1-j) b_j c_j^T   (lam^(j+1)   backward)
+// 64 tokens.  A chunk's e rows are loaded in the scan's order (the last token first
+// backward in time), so that both directions are, with rows i, j of the tile:
+//   P_ij = lam^(i-j) (a_i.b_j) for j <= i, else 0
+//   o_i  = lam^(i+1) S^T a_i + sum_j P_ij c_j      (lam^i       backward)
+//   S   <- lam^e S + sum_j lam^(e-1-j) b_j c_j^T   (lam^(e-j)   backward)
 // The four products are fp32 fused multiply-adds on 4 x 4 register tiles: two
 // 16-byte shared loads for every sixteen of them, so the fp32 pipes bound it (a
 // chunk of 64 x 64 x 64 takes 4 x 2^18 of them, eight times what its bytes cost).
-// P and the weighting skip the half that the mask leaves out, in steps of 16.
+// P and its product skip what the mask leaves out, in blocks of 16 rows and columns.
 // S stays in registers and is put into shared memory once a chunk; masked
 // products are replaced by zeros and rows past the sequence's end are never
 // loaded, so nothing that lies there (an infinity, a NaN of the next sequence)
@@ -34,15 +35,16 @@ __host__ __device__ constexpr size_t smem_floats(int da, int nv, bool states) {
 }
 
 // Rows 0 .. 63 of a tile (cols values each, rows `stride` apart in memory) into
-// shared memory, rows from e on as zeros; fp32 by asynchronous copies.
+// shared memory, backwards from row e - 1 with `flip`, rows from e on as zeros; fp32
+// by asynchronous copies.
 template <typename T>
 __device__ __forceinline__ void load_tile(float *to, int ld, const T *from, int64_t stride, int cols,
-                                          int e) {
+                                          int e, bool flip) {
   const int per = cols / 4;
   for (int x = threadIdx.x; x < kC * per; x += kThreads) {
     const int i = x / per, k = 4 * (x % per);
     float *dst = to + i * ld + k;
-    const T *src = from + (i < e ? i * stride + k : 0);
+    const T *src = from + (i < e ? (flip ? e - 1 - i : i) * stride + k : 0);
     if constexpr (sizeof(T) == 4) {
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                        (uint32_t)__cvta_generic_to_shared(dst)),
@@ -166,9 +168,9 @@ gdn_lin_simt_kernel(const Params p) {
     return (int)(left < kC ? left : kC);
   };
   if (nc > 0) {
-    if (!STATES) load_tile(A, ld, a + token(0) * s.sa, s.sa, da, rows(0));
-    load_tile(B, ld, b + token(0) * s.sb, s.sb, da, rows(0));
-    load_tile(V, NV, c + token(0) * s.sc, s.sc, NV, rows(0));
+    if (!STATES) load_tile(A, ld, a + token(0) * s.sa, s.sa, da, rows(0), rev);
+    load_tile(B, ld, b + token(0) * s.sb, s.sb, da, rows(0), rev);
+    load_tile(V, NV, c + token(0) * s.sc, s.sc, NV, rows(0), rev);
   }
   if (!STATES && js == 0) {
     if (p.seg_len) wait_first();
@@ -242,7 +244,7 @@ gdn_lin_simt_kernel(const Params p) {
           for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              if (!rev && w > u) continue;  // (blocks of 16 beyond the mask)
+              if (w > u) continue;  // (beyond the mask)
               acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
               acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
               acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
@@ -253,8 +255,8 @@ gdn_lin_simt_kernel(const Params p) {
         for (int u = 0; u < 4; ++u)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const int i = i0 + 16 * u, j = j0 + 16 * w, d = rev ? j - i : i - j;
-            P[i * kPd + j] = d >= 0 ? acc[u][w] * lam[d] : 0.f;
+            const int i = i0 + 16 * u, j = j0 + 16 * w;
+            P[i * kPd + j] = i >= j ? acc[u][w] * lam[i - j] : 0.f;
           }
       }
       __syncthreads();
@@ -288,39 +290,43 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = rg + RG * u;
-        const float f = i < e ? lam[rev ? e - 1 - i : i + 1] : 0.f;
+        const float f = i < e ? lam[rev ? i : i + 1] : 0.f;
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[u][x] *= f;
       }
+#pragma unroll
+      for (int b16 = 0; b16 < kC; b16 += 16) {
+        if (b16 >= e) break;
 #pragma unroll 1
-      for (int j = 0; j < kC; j += 4) {
-        float4 y[4];
+        for (int j = b16; j < b16 + 16; j += 4) {
+          float4 y[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) y[u] = at4(V + (j + u) * NV + c0);
+          for (int u = 0; u < 4; ++u) y[u] = at4(V + (j + u) * NV + c0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = rg + RG * u;
-          const float4 x = at4(P + i * kPd + j);
-          const float xs[4] = {x.x, x.y, x.z, x.w};
+          for (int u = 0; u < U; ++u) {
+            if (RG * (u + 1) <= b16) continue;  // (beyond the mask)
+            const float4 x = at4(P + (rg + RG * u) * kPd + j);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
-            acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
-            acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
-            acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
+            for (int q = 0; q < 4; ++q) {
+              acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
+              acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
+              acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
+              acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
+            }
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = rg + RG * u;
-        if (i < e) store4(o + (tok + i) * ((int64_t)H * dc) + c0, acc[u]);
+        if (i < e) store4(o + (tok + (rev ? e - 1 - i : i)) * ((int64_t)H * dc) + c0, acc[u]);
       }
       __syncthreads();
     }
     const bool more = step + 1 < nc;
     if (!STATES && more)  // A is free: its next tile loads meanwhile
-      load_tile(A, ld, a + token(step + 1) * s.sa, s.sa, da, rows(step + 1));
+      load_tile(A, ld, a + token(step + 1) * s.sa, s.sa, da, rows(step + 1), rev);
     // S <- lam^e S + sum_j b_j (w_j c_j)^T
     const float le = STATES || js == 0 ? lam[e] : 0.f;   // (joined: the first lane's)
 #pragma unroll
@@ -331,7 +337,7 @@ gdn_lin_simt_kernel(const Params p) {
         for (int x = 0; x < 4; ++x) st[m][u][x] *= le;
 #pragma unroll 4
     for (int j = js; j < e; j += JS) {
-      const float w = lam[rev ? j + 1 : e - 1 - j];
+      const float w = lam[rev ? e - j : e - 1 - j];
       float4 v = at4(V + j * NV + cs);
       v.x *= w;
       v.y *= w;
@@ -355,8 +361,8 @@ gdn_lin_simt_kernel(const Params p) {
     }
     __syncthreads();
     if (more) {
-      load_tile(B, ld, b + token(step + 1) * s.sb, s.sb, da, rows(step + 1));
-      load_tile(V, NV, c + token(step + 1) * s.sc, s.sc, NV, rows(step + 1));
+      load_tile(B, ld, b + token(step + 1) * s.sb, s.sb, da, rows(step + 1), rev);
+      load_tile(V, NV, c + token(step + 1) * s.sc, s.sc, NV, rows(step + 1), rev);
     }
   }
   join();
