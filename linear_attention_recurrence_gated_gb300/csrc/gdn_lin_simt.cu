@@ -28,10 +28,9 @@ constexpr int kC = 64;        // tokens per chunk
 constexpr int kPd = kC + 4;   // row of P
 
 // floats of shared memory: A, B [64][da + 4], V [64][NV], P [64][68], S [da][NV],
-// lam^0 .. lam^64
+// lam^0 .. lam^64; for the states alone B and V twice
 __host__ __device__ constexpr size_t smem_floats(int da, int nv, bool states) {
-  return (size_t)(states ? 1 : 2) * kC * (da + 4) + kC * nv + (states ? 0 : kC * kPd + da * nv) +
-         kC + 4;
+  return 2 * (size_t)kC * (da + 4) + kC * nv + (states ? kC * nv : kC * kPd + da * nv) + kC + 4;
 }
 
 // Rows 0 .. 63 of a tile (cols values each, rows `stride` apart in memory) into
@@ -107,8 +106,8 @@ gdn_lin_simt_kernel(const Params p) {
   if (col0 >= s.dc) return;  // (the scans of a launch may have fewer tiles)
   const int tid = threadIdx.x, H = p.num_heads, da = s.da, dc = s.dc, ld = da + 4;
   const bool rev = s.reverse != 0;
-  float *B = sm, *V = B + kC * ld, *lam = V + kC * NV, *A = lam + kC + 4, *P = A + kC * ld,
-        *S = P + kC * kPd;
+  float *lam = sm, *B = lam + kC + 4, *V = B + kC * ld, *A = V + kC * NV, *P = A + kC * ld,
+        *S = P + kC * kPd, *B2 = A, *V2 = B2 + kC * ld;   // (states alone: B and V twice)
 
   Span span;
   if (!span_of(p, z, h, span)) return;
@@ -167,10 +166,19 @@ gdn_lin_simt_kernel(const Params p) {
     const int64_t left = start + len - token(step);
     return (int)(left < kC ? left : kC);
   };
+  const auto load_a = [&](int64_t step) {
+    load_tile(A, ld, a + token(step) * s.sa, s.sa, da, rows(step), rev);
+  };
+  const auto load_b = [&](int64_t step, float *to) {
+    load_tile(to, ld, b + token(step) * s.sb, s.sb, da, rows(step), rev);
+  };
+  const auto load_v = [&](int64_t step, float *to) {
+    load_tile(to, NV, c + token(step) * s.sc, s.sc, NV, rows(step), rev);
+  };
   if (nc > 0) {
-    if (!STATES) load_tile(A, ld, a + token(0) * s.sa, s.sa, da, rows(0), rev);
-    load_tile(B, ld, b + token(0) * s.sb, s.sb, da, rows(0), rev);
-    load_tile(V, NV, c + token(0) * s.sc, s.sc, NV, rows(0), rev);
+    if (!STATES) load_a(0);
+    load_b(0, B);
+    load_v(0, V);
   }
   if (!STATES && js == 0) {
     if (p.seg_len) wait_first();
@@ -214,9 +222,14 @@ gdn_lin_simt_kernel(const Params p) {
             for (int off = 1; off < JS; off <<= 1)
               st[m][u][x] += __shfl_xor_sync(0xffffffffu, st[m][u][x], off);
   };
+  // Every tile's next load hides behind the products that it is not in: A behind the
+  // state's update and P V, B behind P V, V behind A S and P of the next chunk.
+  constexpr int U = kC / RG;
   for (int64_t step = 0; step < nc; ++step) {
     const int64_t tok = token(step);
     const int e = rows(step);
+    const bool more = step + 1 < nc;
+    float acc[4][4] = {};
     if (!STATES) {  // the state that this chunk reads
       join();
 #pragma unroll
@@ -228,41 +241,13 @@ gdn_lin_simt_kernel(const Params p) {
         }
     }
     loads_done();
+    if (STATES && more) {  // into the other B and V
+      load_b(step + 1, B2);
+      load_v(step + 1, V2);
+    }
     if (!STATES) {
-      {  // P: rows i = tid / 16 + 16 u, columns j = tid % 16 + 16 w
-        const int i0 = tid >> 4, j0 = tid & 15;
-        float acc[4][4] = {};
-#pragma unroll 1
-        for (int k = 0; k < da; k += 4) {
-          float4 x[4], y[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            x[u] = at4(A + (i0 + 16 * u) * ld + k);
-            y[u] = at4(B + (j0 + 16 * u) * ld + k);
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              if (w > u) continue;  // (beyond the mask)
-              acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
-              acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
-              acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
-              acc[u][w] = fmaf(x[u].w, y[w].w, acc[u][w]);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int i = i0 + 16 * u, j = j0 + 16 * w;
-            P[i * kPd + j] = i >= j ? acc[u][w] * lam[i - j] : 0.f;
-          }
-      }
-      __syncthreads();
+      if (step) load_v(step, V);
       // o: rows rg + RG u (NV 32: two of them), columns c0 .. + 3
-      constexpr int U = kC / RG;
-      float acc[4][4] = {};
 #pragma unroll 1
       for (int k = 0; k < da; k += 4) {
         float4 x[4], y[4];
@@ -294,39 +279,39 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[u][x] *= f;
       }
-#pragma unroll
-      for (int b16 = 0; b16 < kC; b16 += 16) {
-        if (b16 >= e) break;
+      {  // P: rows i = tid / 16 + 16 u, columns j = tid % 16 + 16 w
+        const int i0 = tid >> 4, j0 = tid & 15;
+        float pij[4][4] = {};
 #pragma unroll 1
-        for (int j = b16; j < b16 + 16; j += 4) {
-          float4 y[4];
+        for (int k = 0; k < da; k += 4) {
+          float4 x[4], y[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) y[u] = at4(V + (j + u) * NV + c0);
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (RG * (u + 1) <= b16) continue;  // (beyond the mask)
-            const float4 x = at4(P + (rg + RG * u) * kPd + j);
-            const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
-              acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
-              acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
-              acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
-            }
+          for (int u = 0; u < 4; ++u) {
+            x[u] = at4(A + (i0 + 16 * u) * ld + k);
+            y[u] = at4(B + (j0 + 16 * u) * ld + k);
           }
-        }
-      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = rg + RG * u;
-        if (i < e) store4(o + (tok + (rev ? e - 1 - i : i)) * ((int64_t)H * dc) + c0, acc[u]);
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              if (w > u) continue;  // (beyond the mask)
+              pij[u][w] = fmaf(x[u].x, y[w].x, pij[u][w]);
+              pij[u][w] = fmaf(x[u].y, y[w].y, pij[u][w]);
+              pij[u][w] = fmaf(x[u].z, y[w].z, pij[u][w]);
+              pij[u][w] = fmaf(x[u].w, y[w].w, pij[u][w]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int i = i0 + 16 * u, j = j0 + 16 * w;
+            P[i * kPd + j] = i >= j ? pij[u][w] * lam[i - j] : 0.f;
+          }
       }
-      __syncthreads();
+      loads_done();
+      if (more) load_a(step + 1);
     }
-    const bool more = step + 1 < nc;
-    if (!STATES && more)  // A is free: its next tile loads meanwhile
-      load_tile(A, ld, a + token(step + 1) * s.sa, s.sa, da, rows(step + 1), rev);
     // S <- lam^e S + sum_j b_j (w_j c_j)^T
     const float le = STATES || js == 0 ? lam[e] : 0.f;   // (joined: the first lane's)
 #pragma unroll
@@ -359,10 +344,41 @@ gdn_lin_simt_kernel(const Params p) {
         }
       }
     }
-    __syncthreads();
-    if (more) {
-      load_tile(B, ld, b + token(step + 1) * s.sb, s.sb, da, rows(step + 1), rev);
-      load_tile(V, NV, c + token(step + 1) * s.sc, s.sc, NV, rows(step + 1), rev);
+    if (!STATES) {
+      __syncthreads();
+      if (more) load_b(step + 1, B);
+#pragma unroll
+      for (int b16 = 0; b16 < kC; b16 += 16) {
+        if (b16 >= e) break;
+#pragma unroll 1
+        for (int j = b16; j < b16 + 16; j += 4) {
+          float4 y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y[u] = at4(V + (j + u) * NV + c0);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (RG * (u + 1) <= b16) continue;  // (beyond the mask)
+            const float4 x = at4(P + (rg + RG * u) * kPd + j);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
+              acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
+              acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);
+              acc[u][3] = fmaf(xs[q], y[q].w, acc[u][3]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = rg + RG * u;
+        if (i < e) store4(o + (tok + (rev ? e - 1 - i : i)) * ((int64_t)H * dc) + c0, acc[u]);
+      }
+    }
+    if (STATES) {
+      float *const b2 = B, *const v2 = V;
+      B = B2, V = V2, B2 = b2, V2 = v2;
     }
   }
   join();
