@@ -248,7 +248,7 @@ gdn_lin_simt_kernel(const Params p) {
     if (!STATES) {
       if (step) load_v(step, V);
       // o: rows rg + RG u (NV 32: two of them), columns c0 .. + 3
-#pragma unroll 1
+#pragma unroll 2
       for (int k = 0; k < da; k += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -282,7 +282,7 @@ gdn_lin_simt_kernel(const Params p) {
       {  // P: rows i = tid / 16 + 16 u, columns j = tid % 16 + 16 w
         const int i0 = tid >> 4, j0 = tid & 15;
         float pij[4][4] = {};
-#pragma unroll 1
+#pragma unroll 2
         for (int k = 0; k < da; k += 4) {
           float4 x[4], y[4];
 #pragma unroll
@@ -350,7 +350,7 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
       for (int b16 = 0; b16 < kC; b16 += 16) {
         if (b16 >= e) break;
-#pragma unroll 1
+#pragma unroll 2
         for (int j = b16; j < b16 + 16; j += 4) {
           float4 y[4];
 #pragma unroll
@@ -421,10 +421,10 @@ cudaError_t launch_t(const Params &p, cudaStream_t stream) {
     dc = p.scan[i].dc > dc ? p.scan[i].dc : dc;
     wide = wide && p.scan[i].dc % 64 == 0;
   }
-  // 64 value columns a CTA share P twice as widely, if enough CTAs are left and
-  // the tiles fit (da <= 128); 32 otherwise
-  const int64_t units = (int64_t)p.num_seqs * p.num_heads * p.num_scans;
-  wide = wide && da <= 128 && units * (dc / 64) >= 16;
+  // 64 value columns a CTA share P twice as widely where the tiles fit (da <= 128):
+  // [4, 1024, 16 heads] 64/64 102 us against 145 with 32 columns, [1, 1024, 4] 24 / 26;
+  // 128/128 375 / 352 (one CTA a SM instead of two), its backward pass 856 / 1041
+  wide = wide && da <= 128;
   Params on = p;
   split(on, dc / (wide ? 64 : 32), kSimtWidth, kC, 0.4, 0.4);
   if (wide)

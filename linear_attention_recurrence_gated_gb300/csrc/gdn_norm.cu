@@ -31,9 +31,9 @@ constexpr int kParts = 4 * kSMs;   // partial sums of dweight and dbias at most
 // Three forms, by the sample's size:
 //   rows    S = 1 and a group fits a warp's registers: a group is a power of two
 //           of lanes, its values never leave the registers (one read, one write);
-//   slabs   fewer samples than SMs: a sample's rows are cut into slabs, one
-//           launch sums them up, the next one applies (its reads hit L2 up to
-//           some 100 MB);
+//   slabs   few or large samples: a sample's rows are cut into slabs, one launch sums
+//           them up, the next one applies, from the last rows to the first (some of
+//           which L2 still holds);
 //   sample  otherwise: one CTA per sample, two passes over it.
 struct Params {
   const void *x, *gate, *dy;
@@ -1116,7 +1116,14 @@ int slab_count(int64_t N, int64_t S, int C, int V) {
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : (int)n;
 }
-bool use_slabs(int64_t N, int64_t S) { return N < kSMs && S > 1; }
+// Fewer samples than SMs, or large ones.  us, slabs against sample: forward N 300,
+// [256, 512] each, 46 / 90; 1000 of [49, 512] 43 / 33; backward 70 / 134; 60 / 94; 16000
+// of [8, 256] 405 / 282.  (The slabs' sums are 8 C bytes each: 16 rows at least keep them
+// a small part of the samples.)
+bool use_slabs(int64_t N, int64_t S, int64_t C, bool backward) {
+  return S > 1 && (N < kSMs ||
+                   (N <= 65535 && S >= 16 && S * C >= (backward ? 16384 : 65536)));
+}
 
 template <auto Kernel>
 cudaError_t go(dim3 grid, size_t bytes, const Params &p, cudaStream_t stream,
@@ -1187,7 +1194,7 @@ cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
   const int CV = p.C / V, DV = p.D / V, TY = tile_rows(p.C, V);
   if constexpr (WIDE) {
     const bool full = p.S == 1 && DV <= 32 && (DV & (DV - 1)) == 0;
-    if (full || use_slabs(p.N, p.S)) {
+    if (full || use_slabs(p.N, p.S, p.C, backward)) {
       const int mode = (p.silu ? 1 : 0) | (p.gate ? 2 : 0);
       return mode == 0   ? run_wide<T, V, 0>(p, backward, stream)
              : mode == 1 ? run_wide<T, V, 1>(p, backward, stream)
@@ -1198,7 +1205,7 @@ cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
   if (p.S == 1 && DV <= 32) return run_rows<T, V, 1, false, kAny>(p, backward, stream);
   if (p.S == 1 && DV <= 128) return run_rows<T, V, 4, false, kAny>(p, backward, stream);
   if constexpr (!WIDE)
-    if (use_slabs(p.N, p.S)) return run_slabs<T, V, kAny>(p, backward, stream);
+    if (use_slabs(p.N, p.S, p.C, backward)) return run_slabs<T, V, kAny>(p, backward, stream);
   const int grid = (int)(p.N < kParts ? p.N : kParts);
   if (!backward)
     return go<gdn_norm_fwd_kernel<T, V, kAny>>(grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
@@ -1250,7 +1257,8 @@ size_t gdn_group_norm_workspace_size(int32_t batch, int32_t spatial, int32_t cha
   if (batch <= 0 || spatial <= 0 || channels <= 0 || groups <= 0) return 0;
   // partial sums of dweight and dbias, and of the groups of every slab
   using namespace gdn::norm;
-  const size_t parts = use_slabs(batch, spatial) ? (size_t)(2 * kSMs + batch) : (size_t)kParts;
+  const size_t slabs = use_slabs(batch, spatial, channels, true) ? (size_t)(2 * kSMs + batch) : 0,
+               parts = slabs > (size_t)kParts ? slabs : (size_t)kParts;
   return parts * ((size_t)8 * channels + (size_t)12 * groups);
 }
 
