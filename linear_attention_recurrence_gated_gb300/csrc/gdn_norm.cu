@@ -35,6 +35,11 @@ constexpr int kParts = 4 * kSMs;   // partial sums of dweight and dbias at most
 //           them up, the next one applies, from the last rows to the first (some of
 //           which L2 still holds);
 //   sample  otherwise: one CTA per sample, two passes over it.
+// All are bound by memory (forward: x, gate and y once; the slabs' backward pass reads x
+// and dy twice).  Measured, bf16: rows, gated, [32768, 1, 1024], 201 MB, 35.9 us (5.6
+// TB/s; a CTA for each place on the SMs: a second wave cost 1 us); slabs backward with
+// SiLU, [4, 4096, 1280], 126 MB, 41 us (two passes at 5.2 TB/s; without its arithmetic
+// 34 us: five warps a scheduler cover most of it).
 struct Params {
   const void *x, *gate, *dy;
   const float *w, *b;

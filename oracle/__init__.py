@@ -24,6 +24,9 @@ Contents
                  torch.autograd over the fp64 token loop on the CPU.
 ``block``        the GDN block's prologue (causal depthwise conv1d + SiLU) and
                  epilogue ((o + D v) * g_gate), same page, sections 5.4-5.5.
+``lin``          linear attention with a fixed decay for each head and its
+                 gradients, group norm with an activation, and the pages of a
+                 state cache: token by token and page by page in fp64 numpy.
 
 Parity status of each function is recorded in its docstring; every function
 here is pinned by a CPU test in ``tests/test_oracle_pins.py``.
