@@ -752,8 +752,8 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     int s = 0;
     for (int c = 0; c < nc; ++c) {
       const uint32_t stage = sb + s * L::STAGE;
-      if (!wait_all(w, kSReady, c) || (c > 0 && !wait_all(w, kOFree, c - 1)) ||
-          !wait_all(w, kFullA + s, c / L::STAGES))
+      if (!wait_all(w, kFullA + s, c / L::STAGES) || !wait_all(w, kFullV + s, c / L::STAGES) ||
+          !wait_all(w, kSReady, c) || (c > 0 && !wait_all(w, kOFree, c - 1)))
         break;
       tc_fence_after();
       const uint64_t da = umma_desc_sw128(stage + L::A), ds = umma_desc_sw128_mn(sb + L::S, 8192),
@@ -769,7 +769,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         if (own_buffer(c)) umma_commit(w.at(kEmptyA + s));
       }
       __syncwarp();
-      if (!wait_all(w, kPReady + (c & 1), c >> 1) || !wait_all(w, kFullV + s, c / L::STAGES)) break;
+      if (!wait_all(w, kPReady + (c & 1), c >> 1)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int kk = 0; kk < kC / 16; ++kk)
