@@ -49,6 +49,7 @@ struct Params {
   DeviceStatus *status;
   int64_t seq_len;     // tokens of a batch row, or of all packed sequences
   int32_t num_heads, num_seqs, num_scans;
+  int32_t ranked;      // slot z holds the z-th longest packed sequence (uncut ones only)
   // Split along time (seg_len 0: none): sequences are cut into segments of
   // seg_len tokens, whole chunks, each run by CTAs of its own.  A first
   // launch leaves every segment's state increment, run from zero, in seg_x
@@ -80,6 +81,37 @@ __device__ __forceinline__ bool bounds(const Params &p, int n, int h, int64_t &s
   return sequence_bounds(f, n, h, start, len);
 }
 
+// The z-th longest of up to kRanked packed sequences (of equal ones the first).  The
+// whole warp together.
+constexpr int kRanked = 128;
+__device__ __forceinline__ int longest(const Params &p, int z) {
+  const int lane = threadIdx.x & 31;
+  int len[kRanked / 32], rank[kRanked / 32] = {}, n = 0;
+#pragma unroll
+  for (int k = 0; k < kRanked / 32; ++k) {
+    const int i = 32 * k + lane;
+    len[k] = i < p.num_seqs ? p.cu[i + 1] - p.cu[i] : 0;
+  }
+#pragma unroll
+  for (int b = 0; b < kRanked / 32; ++b) {
+    const int m = p.num_seqs - 32 * b < 32 ? p.num_seqs - 32 * b : 32;
+#pragma unroll 4
+    for (int u = 0; u < m; ++u) {
+      const int other = __shfl_sync(0xffffffffu, len[b], u);
+#pragma unroll
+      for (int k = 0; k < kRanked / 32; ++k)
+        rank[k] += other > len[k] || (other == len[k] && 32 * b + u < 32 * k + lane);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRanked / 32; ++k) {
+    const uint32_t is =
+        __ballot_sync(0xffffffffu, rank[k] == z && 32 * k + lane < p.num_seqs);
+    if (is) n = 32 * k + __ffs(is) - 1;
+  }
+  return n;
+}
+
 // The span of slot z; false if it has none (or the offsets are bad: recorded).
 // Uniform over the CTA.
 __device__ __forceinline__ bool span_of(const Params &p, int z, int h, Span &s) {
@@ -87,7 +119,8 @@ __device__ __forceinline__ bool span_of(const Params &p, int z, int h, Span &s) 
   s.count = 1;
   s.n = z;
   if (p.seg_len == 0) {
-    if (!bounds(p, z, h, s.start, s.len)) return false;
+    if (p.ranked) s.n = longest(p, z);
+    if (!bounds(p, s.n, h, s.start, s.len)) return false;
     s.total = s.len;
     return true;
   }
@@ -190,6 +223,10 @@ inline void split(Params &p, int64_t tiles, int64_t width, int64_t chunk, double
                     p.seg_x_bytes;
   p.seg_len = fits ? plan.seg_len : 0;
   p.slots = fits ? plan.slots : p.num_seqs;
+  // More CTAs than run at a time: those of the longest sequences begin first, or one
+  // of them may run alone at the end
+  p.ranked = p.cu != nullptr && p.seg_len == 0 && p.num_seqs > 1 && p.num_seqs <= kRanked &&
+             tiles * p.num_scans * p.num_heads * p.num_seqs > width;
 }
 
 }  // namespace lin
