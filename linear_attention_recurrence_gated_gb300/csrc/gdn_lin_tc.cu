@@ -27,17 +27,17 @@
 // three terms of V^ and S).  The three tiles of a stage are freed and loaded one by one:
 // B after P and X, A after P and O1, V after O2.
 //
-// Bound.  Head size 64: memory.  [8, 4096, 16 heads, 64/64], 270 MB, takes 50 us, 5.4
+// Bound.  Head size 64: memory.  [8, 4096, 16 heads, 64/64], 270 MB, takes 48 us, 5.6
 // TB/s with the start and the end of its one wave; in between a chunk takes as long as
 // its tiles at the copy bandwidth.  Head size 128: the chain O1, O2, read o, O1 of the
 // next chunk (each accumulator is there once: P twice, X, O1 and O2 fill the 512
 // columns), some 3100 cycles a chunk of which the tensor pipe is busy for half:
-//   packed, 140k tokens, 8 heads, 128/256    433 us (1.54 GB: 3.6 TB/s)
-//   [1, 65536, 16, 128/128], cut along time  341 us (1.08 GB; 781 us uncut)
-//   backward [4, 8192, 16, 128/128]          327 us (0.95 GB; 384 CTAs: 2.5 waves)
-// Tried and slower: O1 twice in place of X's second half (packed 448 us: X then reads B
-// twice), o by the V^ warps (503 us), shares of equal size handed on between resident
-// CTAs (532 us: the heads of one token are no longer read together).
+//   packed, 140k tokens, 8 heads, 128/256    405 us (1.54 GB: 3.8 TB/s)
+//   [1, 65536, 16, 128/128], cut along time  338 us (1.08 GB; 781 us uncut)
+//   backward [4, 8192, 16, 128/128]          310 us (0.95 GB; 384 CTAs: 2.5 waves)
+// Tried and slower (packed 440 us before each): O1 twice in place of X's second half
+// (448 us: X then reads B twice), o by the V^ warps (503 us), shares of equal size handed
+// on between resident CTAs (532 us: the heads of one token are no longer read together).
 //
 // Roles (16 warps): P' (warps 0-3), S and o (4-7), V^ (8-11), TMA (12), and the
 // issue of X (13), of P (14), of O1 and O2 (15): none of the three waits for what
