@@ -107,14 +107,21 @@ gdn_lin_simt_kernel(const Params p) {
   constexpr int JS = RG / RT;
   const Scan &s = p.scan[blockIdx.z % p.num_scans];
   const int z = blockIdx.z / p.num_scans, h = blockIdx.y, col0 = blockIdx.x * NV;
-  if (col0 >= s.dc) return;  // (the scans of a launch may have fewer tiles)
+  const bool second = !STATES && p.seg_len;   // (a CTA ends after the first launch in any case)
+  if (col0 >= s.dc) {  // (the scans of a launch may have fewer tiles)
+    if (second) wait_first();
+    return;
+  }
   const int tid = threadIdx.x, H = p.num_heads, da = s.da, dc = s.dc, ld = da + 4;
   const bool rev = s.reverse != 0;
   float *lam = sm, *B = lam + kC + 4, *V = B + kC * ld, *A = V + kC * NV, *P = A + kC * ld,
         *S = P + kC * kPd, *B2 = A, *V2 = B2 + kC * ld;   // (states alone: B and V twice)
 
   Span span;
-  if (!span_of(p, z, h, span)) return;
+  if (!span_of(p, z, h, span)) {
+    if (second) wait_first();
+    return;
+  }
   const int64_t start = span.start, len = span.len;
   const int64_t unit = (int64_t)span.n * H + h;
   // the segment whose end is the sequence's, in the scan's direction
@@ -185,7 +192,7 @@ gdn_lin_simt_kernel(const Params p) {
     load_v(0, V);
   }
   if (!STATES && js == 0) {
-    if (p.seg_len) wait_first();
+    if (second) wait_first();
     if (s.s_in && s.s_in_t) {
 #pragma unroll
       for (int m = 0; m < MK; ++m)

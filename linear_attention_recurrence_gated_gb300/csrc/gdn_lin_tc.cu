@@ -220,11 +220,18 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   const int h = blockIdx.y, z = blockIdx.z, H = p.num_heads;
   const Scan &scan = p.scan[sc];
   const int dc = scan.dc, col0 = tile * 64;
-  if (col0 >= dc) return;
+  const bool second = !STATES && p.seg_len;   // (a CTA ends after the first launch in any case)
+  if (col0 >= dc) {
+    if (second) wait_first();
+    return;
+  }
   const bool rev = scan.reverse != 0;
 
   Span span;
-  if (!span_of(p, z, h, span)) return;  // uniform over the CTA
+  if (!span_of(p, z, h, span)) {  // uniform over the CTA
+    if (second) wait_first();
+    return;
+  }
   const int64_t start = span.start, len = span.len;
   const int64_t unit = (int64_t)span.n * H + h;
   // the segment whose end is the sequence's, in the scan's direction
@@ -241,6 +248,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
   float *const s_out = STATES ? p.seg_x + x_unit * DK * dc
                               : scan.s_out && last ? scan.s_out + unit * DK * dc : nullptr;
   if (len == 0) {  // the state passes through
+    if (second) wait_first();
     if (s_out)
       for (int i = tid; i < DK * 64; i += kThreads)
         s_out[(int64_t)(i >> 6) * dc + col0 + (i & 63)] =
@@ -509,7 +517,7 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
         s[2 * x + 1] = fma2(pair(f, f), s[2 * x + 1], pair(y.z, y.w));
       }
     };
-    if (!STATES && p.seg_len) wait_first();
+    if (second) wait_first();
     if (!STATES && scan.s_in) {
       if (scan.s_in_t) {
         const float *at = scan.s_in + unit * DK * dc + (int64_t)(col0 + c0) * DK + si;
