@@ -778,12 +778,12 @@ def _done(where, st, check, workspace, stream):
             raise GdnError(st, f"{where} (device)")
 
 
-def _row_stride(where, name, t):
+def _stride(where, name, t):
     """Elements from one token row of ``t`` ``[B, T, H, D]`` to the next (rows
-    contiguous, the rows of a batch one after the other)."""
-    B, T, H, D = t.shape
+    contiguous, the rows of a batch one after the other); 0: packed."""
     if t.is_contiguous():
-        return H * D
+        return 0
+    B, T, H, D = t.shape
     s = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else H * D)
     if (D > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != D) or s < H * D or \
             (B > 1 and T > 0 and t.stride(0) != T * s):
@@ -863,9 +863,8 @@ def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=No
     ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
     st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                   _p(initial_state), _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk,
-                  dv, N, _row_stride(w, "q", q), _row_stride(w, "k", k), _row_stride(w, "v", v),
-                  _CODES[q.dtype], flags, ws.data_ptr(), _nbytes(ws),
-                  _raw_stream(stream, q.get_device()))
+                  dv, N, _stride(w, "q", q), _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype],
+                  flags, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, q.get_device()))
     if st or check:
         _done(w, st, check, ws, stream)
     return o, final_state
@@ -894,8 +893,8 @@ def gdn_lin_bwd(q, k, v, log_decay, d_o, initial_state=None, cu_seqlens=None, d_
     st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                   _p(initial_state), _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state),
                   grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
-                  _p(grads.get("dh0")), B, T, H, dk, dv, N, _row_stride(w, "q", q),
-                  _row_stride(w, "k", k), _row_stride(w, "v", v), _CODES[q.dtype], flags,
+                  _p(grads.get("dh0")), B, T, H, dk, dv, N, _stride(w, "q", q),
+                  _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags,
                   ws.data_ptr(), _nbytes(ws), _raw_stream(stream, q.get_device()))
     if st or check:
         _done(w, st, check, ws, stream)
@@ -1052,15 +1051,17 @@ def gdn_pages_workspace_size(num_pages: int, num_rows: int, n: int) -> int:
     return int(lib().gdn_pages_workspace_size(num_pages, num_rows, n))
 
 
-def _pages_fine(pool, table, counts, refs, rows, *ints):
+def _pages_fine(pool, table, counts, refs, rows, own, table_out, counts_out, refs_out):
     """The bookkeeping of a call matches (the quick look before _pages_check): all
-    tensors dense, ``rows`` (may be None) a list, ``ints`` all int32."""
-    P = refs.shape[0]
-    return _dense(pool, table, counts, refs, rows, *ints) and table.dtype == _I32 and \
-        counts.dtype == _I32 and refs.dtype == _I32 and counts.shape == table.shape[:1] and \
-        refs.dim() == 1 and (pool is None or pool.shape[0] == P) and \
-        (rows is None or (rows.dtype == _I32 and rows.dim() == 1)) and \
-        all(t is None for t in ints)
+    tensors dense, ``rows`` (may be None) a list; no output is given (``own``: the
+    call's own one) but inputs updated in place."""
+    return own is None and (table_out is None or table_out is table) and \
+        (counts_out is None or counts_out is counts) and \
+        (refs_out is None or refs_out is refs) and _dense(pool, table, counts, refs, rows) and \
+        table.dtype == _I32 and counts.dtype == _I32 and refs.dtype == _I32 and \
+        table.dim() == 2 and refs.dim() == 1 and counts.shape == table.shape[:1] and \
+        (pool is None or pool.shape[0] == refs.shape[0]) and \
+        (rows is None or (rows.dtype == _I32 and rows.dim() == 1))
 
 
 def _pages_check(where, pool, table, counts, refs, lists, outs):
@@ -1152,7 +1153,7 @@ def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None
     afterwards.  Tensors and outputs as ``gdn_pages_fork``.  Returns
     ``(table_out, counts_out, refs_out)``."""
     w = "gdn_pages_free"
-    if _pages_fine(None, table, counts, refs, rows, table_out, counts_out, refs_out):
+    if _pages_fine(None, table, counts, refs, rows, None, table_out, counts_out, refs_out):
         (R, M), P = table.shape, refs.shape[0]
     else:
         _, P, R, M = _pages_check(w, None, table, counts, refs, dict(rows=rows),
@@ -1177,8 +1178,13 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     table.  Tensors as ``gdn_pages_fork``.  Returns ``(num_live, table_out,
     refs_out)``, num_live int32 ``[1]`` on the device."""
     w = "gdn_pages_compact"
-    bytes_, P, R, M = _pages_check(w, pool, table, counts, refs, {},
-                                   dict(num_live=num_live, table_out=table_out, refs_out=refs_out))
+    if _pages_fine(pool, table, counts, refs, None, num_live, table_out, None, refs_out):
+        (R, M), P = table.shape, refs.shape[0]
+        bytes_ = _nbytes(pool) // P if P else 16
+    else:
+        bytes_, P, R, M = _pages_check(w, pool, table, counts, refs, {},
+                                       dict(num_live=num_live, table_out=table_out,
+                                            refs_out=refs_out))
     num_live = _empty(stream, pool, (1,), _I32) if num_live is None else num_live
     table_out = _like_new(stream, table) if table_out is None else table_out
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
