@@ -73,9 +73,30 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums) {
   return x - v + (warp ? warp_sums[warp - 1] : 0);
 }
 
-__device__ __forceinline__ void copy_ints(int32_t *to, const int32_t *from, int64_t n) {
-  if (to != from)
-    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) to[i] = from[i];
+// The bookkeeping into its new tensors (those updated in place stay): 16 bytes at a
+// time, the loads of all three ahead of the stores, one latency of memory for them.
+__device__ __forceinline__ void copy_bookkeeping(const Params &p) {
+  int32_t *const to[3] = {p.table_out, p.counts_out, p.refs_out};
+  const int32_t *const from[3] = {p.table, p.counts, p.refs};
+  const int64_t n[3] = {(int64_t)p.num_rows * p.max_pages, p.num_rows, p.num_pages};
+  int64_t most = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (to[k] != from[k] && n[k] > most) most = n[k];
+  for (int64_t i = threadIdx.x; 4 * i < most; i += kPlan) {
+    int4 x[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (to[k] != from[k] && 4 * i + 4 <= n[k]) x[k] = reinterpret_cast<const int4 *>(from[k])[i];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (to[k] == from[k]) continue;
+      if (4 * i + 4 <= n[k])
+        reinterpret_cast<int4 *>(to[k])[i] = x[k];
+      else
+        for (int64_t j = 4 * i; j < n[k]; ++j) to[k][j] = from[k][j];
+    }
+  }
 }
 
 // tmp0: count of the job's parent, -1 for a job that is left out (num jobs);
@@ -84,9 +105,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const Params p) {
   let_second();
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x, n = p.n, R = p.num_rows, M = p.max_pages;
-  copy_ints(p.table_out, p.table, (int64_t)R * M);
-  copy_ints(p.counts_out, p.counts, R);
-  copy_ints(p.refs_out, p.refs, p.num_pages);
+  copy_bookkeeping(p);
   for (int i = tid; i < n; i += kPlan) {
     const int c = p.b[i];
     if (c >= 0 && c < R) p.tmp1[c] = INT32_MAX;
@@ -179,9 +198,7 @@ __global__ void __launch_bounds__(kPlan) copy_plan_kernel(const Params p) {
 
 __global__ void __launch_bounds__(kPlan) free_kernel(const Params p) {
   const int tid = threadIdx.x, R = p.num_rows, M = p.max_pages;
-  copy_ints(p.table_out, p.table, (int64_t)R * M);
-  copy_ints(p.counts_out, p.counts, R);
-  copy_ints(p.refs_out, p.refs, p.num_pages);
+  copy_bookkeeping(p);
   __syncthreads();
   for (int i = tid; i < p.n; i += kPlan) {
     const int r = p.a[i];
@@ -219,25 +236,36 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Params p) {
   let_second();
   __shared__ int warp_sums[kPlan / 32];
   const int tid = threadIdx.x, P = p.num_pages;
-  int mine = 0, live;
-  for (int pg = tid; pg < P; pg += kPlan) mine += p.refs[pg] > 0;
+  constexpr int kHeld = 4;   // blocks of pages whose counts stay in registers
+  int held[kHeld], mine = 0, live;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int pg = k * kPlan + tid;
+    held[k] = pg < P ? p.refs[pg] : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) mine += held[k] > 0;
+  for (int pg = kHeld * kPlan + tid; pg < P; pg += kPlan) mine += p.refs[pg] > 0;
   block_scan(mine, live, warp_sums);
   int holes = 0, moves = 0;
-  for (int p0 = 0; p0 < P; p0 += kPlan) {
+  const auto block = [&](int p0, int r) {
     const int pg = p0 + tid;
-    const int r = pg < P ? p.refs[pg] : 0;
     const int hole = pg < live && r <= 0, move = pg >= live && pg < P && r > 0;
     int total;
     const int at = block_scan(hole | (move << 16), total, warp_sums);
     if (hole) p.tmp1[holes + (at & 0xffff)] = pg;
     if (move) p.jobs[moves + (at >> 16)] = make_int2(pg, r);
-    if (pg < P) p.tmp0[pg] = pg;
+    if (pg < P) {
+      p.tmp0[pg] = pg;
+      if (p.refs_out != p.refs) p.refs_out[pg] = r;
+    }
     holes += total & 0xffff;
     moves += total >> 16;
-  }
-  __syncthreads();
-  if (p.refs_out != p.refs)
-    for (int pg = tid; pg < P; pg += kPlan) p.refs_out[pg] = p.refs[pg];
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kPlan < P) block(k * kPlan, held[k]);
+  for (int p0 = kHeld * kPlan; p0 < P; p0 += kPlan) block(p0, p0 + tid < P ? p.refs[p0 + tid] : 0);
   __syncthreads();
   for (int k = tid; k < moves; k += kPlan) {  // as many holes as moves
     const int2 m = p.jobs[k];
