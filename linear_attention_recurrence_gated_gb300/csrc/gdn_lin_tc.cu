@@ -33,7 +33,7 @@
 // next chunk (each accumulator is there once: P twice, X, O1 and O2 fill the 512
 // columns), some 3100 cycles a chunk of which the tensor pipe is busy for half:
 //   packed, 140k tokens, 8 heads, 128/256    405 us (1.54 GB: 3.8 TB/s)
-//   [1, 65536, 16, 128/128], cut along time  338 us (1.08 GB; 781 us uncut)
+//   [1, 65536, 16, 128/128], cut along time  311 us (1.08 GB; 781 us uncut)
 //   backward [4, 8192, 16, 128/128]          310 us (0.95 GB; 384 CTAs: 2.5 waves)
 // Tried and slower (packed 440 us before each): O1 twice in place of X's second half
 // (448 us: X then reads B twice), o by the V^ warps (503 us), shares of equal size handed
@@ -65,11 +65,14 @@ constexpr int kThreads = 16 * 32;   // 128 registers a thread: P' spilled with 2
 constexpr uint32_t kWaitTries = 1u << 19;   // probes of 4 us each before a wait gives up (2 s)
 constexpr uint32_t kColP = 0, kColO1 = 256, kColO2 = 320, kColX = 384, kCols = 512;
 
-template <int DK>
+template <int DK, bool STATES>
 struct Lay {
   static constexpr int SUB = DK / 64;
-  static constexpr int STAGES = DK == 64 ? 3 : 2;
-  static constexpr int A = 0, B = SUB * kTile, V = 2 * SUB * kTile, STAGE = (2 * SUB + 1) * kTile;
+  // The states alone read no A: with DK 128 its room is a third stage's ([1, 65536, 16,
+  // 128/128] 340 -> 311 us)
+  static constexpr bool NO_A = STATES && DK == 128;
+  static constexpr int STAGES = DK == 64 || NO_A ? 3 : 2;
+  static constexpr int A = 0, B = NO_A ? 0 : SUB * kTile, V = B + SUB * kTile, STAGE = V + kTile;
   static constexpr int VH = STAGES * STAGE;               // three terms of V^
   static constexpr int S = VH + 3 * kTile;                // [DK][64] bf16
   // the o tile: its own buffer, or (DK 128: no room) the A tile of its stage
@@ -206,7 +209,7 @@ __device__ __forceinline__ float power(float ld, float n) { return n == 0.f ? 1.
 template <int DK, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
 gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
-  using L = Lay<DK>;
+  using L = Lay<DK, STATES>;
   if (STATES) let_second();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -827,12 +830,12 @@ bool make_map(CUtensorMap *m, const void *ptr, int cols, int heads, int64_t toke
 template <int DK, bool STATES>
 cudaError_t run(const TcArgs &args, cudaStream_t stream) {
   constexpr auto kernel = gdn_lin_tc_kernel<DK, STATES>;
-  const cudaError_t err = allow_smem<kernel>(Lay<DK>::ALLOC);
+  const cudaError_t err = allow_smem<kernel>(Lay<DK, STATES>::ALLOC);
   if (err != cudaSuccess) return err;
   const dim3 grid(args.tiles * args.p.num_scans, args.p.num_heads, args.p.slots);
   if (!STATES && args.p.seg_len)
-    return launch_beside(kernel, grid, kThreads, Lay<DK>::ALLOC, stream, args);
-  kernel<<<grid, kThreads, Lay<DK>::ALLOC, stream>>>(args);
+    return launch_beside(kernel, grid, kThreads, Lay<DK, STATES>::ALLOC, stream, args);
+  kernel<<<grid, kThreads, Lay<DK, STATES>::ALLOC, stream>>>(args);
   return cudaGetLastError();
 }
 
