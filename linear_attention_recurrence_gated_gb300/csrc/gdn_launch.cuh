@@ -1,4 +1,4 @@
-// Launches: dynamic shared memory beyond 48 KB, and pairs of launches that overlap.
+// Launches: dynamic shared memory, and pairs of launches that overlap.
 #pragma once
 
 #include <atomic>
@@ -8,19 +8,27 @@
 
 namespace gdn {
 
+// An error that the caller returns to its own caller, not left behind in the runtime for
+// the next call's look at its own launch.
+inline cudaError_t taken(cudaError_t err) {
+  if (err != cudaSuccess) (void)cudaGetLastError();
+  return err;
+}
+
 // Lets a kernel have `bytes` of dynamic shared memory, once per device and size
-// class: the driver call takes a microsecond or two, a tenth of a small call.
+// class: the driver call takes a microsecond or two, a tenth of a small call.  (Also
+// below 48 KB: a kernel's static shared memory counts towards those too.)
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
   static std::atomic<uint32_t> allowed[64];
-  if (bytes <= 48 * 1024) return cudaSuccess;
+  if (bytes == 0) return cudaSuccess;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess) return taken(err);
   const uint32_t want = (uint32_t)bytes;
   if (dev < 64 && allowed[dev].load(std::memory_order_acquire) >= want) return cudaSuccess;
   err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
-  if (err != cudaSuccess || dev >= 64) return err;
+  if (err != cudaSuccess || dev >= 64) return taken(err);
   uint32_t had = allowed[dev].load(std::memory_order_relaxed);
   while (had < want && !allowed[dev].compare_exchange_weak(had, want, std::memory_order_release)) {
   }
@@ -50,7 +58,7 @@ cudaError_t launch_beside(K kernel, dim3 grid, int threads, size_t smem, cudaStr
   cfg.stream = stream;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return taken(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 }  // namespace gdn

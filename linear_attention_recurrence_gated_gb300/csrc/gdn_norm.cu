@@ -1317,7 +1317,7 @@ gdn_status gdn_group_norm_bwd(const void *x, const float *weight, const float *b
   if (batch == 0 || spatial == 0) {  // no rows: the channels' sums are empty
     for (float *to : {dweight, dbias}) {
       if (to && !aligned16(to)) return GDN_ERR_INVALID_ARG;
-      if (to && cudaMemsetAsync(to, 0, b_c, (cudaStream_t)stream) != cudaSuccess)
+      if (to && taken(cudaMemsetAsync(to, 0, b_c, (cudaStream_t)stream)) != cudaSuccess)
         return GDN_ERR_CUDA;
     }
     return GDN_OK;
