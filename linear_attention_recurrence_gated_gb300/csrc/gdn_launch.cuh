@@ -15,23 +15,28 @@ inline cudaError_t taken(cudaError_t err) {
   return err;
 }
 
-// Lets a kernel have `bytes` of dynamic shared memory, once per device and size
-// class: the driver call takes a microsecond or two, a tenth of a small call.  (Also
-// below 48 KB: a kernel's static shared memory counts towards those too.)
+// Lets a kernel have as much dynamic shared memory as the GPU holds beside its static
+// one, once per device (the driver call takes a microsecond or two, a tenth of a small
+// call).  Every caller sets the same limit, whatever it needs itself: of threads that
+// come here together none can lower it for another.  Also below 48 KB: the static
+// shared memory counts towards those too.  A launch that needs more than there is fails
+// by itself.
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {
-  static std::atomic<uint32_t> allowed[64];
+  static std::atomic<bool> done[64];
   if (bytes == 0) return cudaSuccess;
-  int dev = 0;
+  int dev = 0, most = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return taken(err);
-  const uint32_t want = (uint32_t)bytes;
-  if (dev < 64 && allowed[dev].load(std::memory_order_acquire) >= want) return cudaSuccess;
-  err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)want);
-  if (err != cudaSuccess || dev >= 64) return taken(err);
-  uint32_t had = allowed[dev].load(std::memory_order_relaxed);
-  while (had < want && !allowed[dev].compare_exchange_weak(had, want, std::memory_order_release)) {
-  }
+  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  cudaFuncAttributes own;
+  err = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  if (err == cudaSuccess) err = cudaFuncGetAttributes(&own, Kernel);
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               most - (int)own.sharedSizeBytes);
+  if (err != cudaSuccess) return taken(err);
+  if (dev < 64) done[dev].store(true, std::memory_order_release);
   return cudaSuccess;
 }
 

@@ -13,16 +13,26 @@ from linear_attention_recurrence_gated_gb300 import build as gbuild
 PROGRAM = r"""
 #include <cuda_runtime.h>
 #include <atomic>
+#include <condition_variable>
 #include <cstdio>
 #include <cstring>
+#include <mutex>
+#include <thread>
 
 // A kernel with `kStatic` bytes of static shared memory on a GPU that allows 232448 in
 // all and 49152 without opting in.
 static const int kStatic = 2304, kOptin = 232448;
 static std::atomic<int> allowed{49152 - kStatic};   // dynamic bytes a launch may have
 static std::atomic<int> pending{0};                 // the runtime's last error
+static std::mutex m;
+static std::condition_variable cv;
+static int hold_first = 0, sets = 0;
 
 template <typename K> cudaError_t fake_set(K, cudaFuncAttribute, int bytes) {
+  std::unique_lock<std::mutex> lock(m);
+  const int mine = sets++;
+  // the first caller is overtaken by the second one, which ends its whole call
+  if (hold_first && mine == 0) cv.wait_for(lock, std::chrono::seconds(2), [] { return sets > 100; });
   if (bytes + kStatic > kOptin) { pending = cudaErrorInvalidValue; return cudaErrorInvalidValue; }
   allowed = bytes;
   return cudaSuccess;
@@ -45,6 +55,7 @@ static cudaError_t fake_last() { return (cudaError_t)pending.exchange(0); }
 
 __global__ void one() {}
 __global__ void two() {}
+__global__ void three() {}
 
 // a launch with these dynamic bytes
 static bool fits(size_t n) { return (int)n <= allowed; }
@@ -59,6 +70,25 @@ int main(int, char **argv) {
   } else if (!strcmp(argv[1], "error")) {
     if (gdn::allow_smem<two>(kOptin) == cudaSuccess && fits(kOptin)) return 1;
     if (pending) { printf("an error is left behind\n"); return 1; }
+  } else {
+    hold_first = 1;
+    cudaError_t a, b;
+    std::thread t([&] { a = gdn::allow_smem<three>(100000); });
+    for (;;) {
+      std::unique_lock<std::mutex> lock(m);
+      if (sets > 0) break;
+      lock.unlock();
+      std::this_thread::yield();
+    }
+    b = gdn::allow_smem<three>(200000);
+    { std::unique_lock<std::mutex> lock(m); sets = 1000; }
+    cv.notify_all();
+    t.join();
+    if (a != cudaSuccess || b != cudaSuccess) return 1;
+    if (gdn::allow_smem<three>(200000) != cudaSuccess || !fits(200000)) {
+      printf("200000 bytes were allowed and are not any more\n");
+      return 1;
+    }
   }
   return 0;
 }
@@ -87,3 +117,9 @@ def test_static_shared_memory_counts(program):
 def test_a_refused_size_leaves_no_error_behind(program):
     """The next call's check of its own launch would report it."""
     passes(program, "error")
+
+
+def test_first_calls_from_two_threads(program):
+    """Threads that call one kernel with different sizes for the first time: whoever
+    sets the limit last, the larger size stays allowed."""
+    passes(program, "threads")
