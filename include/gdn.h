@@ -578,6 +578,11 @@ gdn_status gdn_bwd(const void *q, const void *k, const void *v, const float *g,
  * CUDA-core kernel for bf16 storage too) or 0.  Empty sequences and seq_len =
  * 0 are legal (states pass through).  Aliasing and errors as gdn_fwd.
  *
+ * Values that are not finite go where the recurrence takes them and nowhere else: to the
+ * outputs of their own token and later ones (gradients that run backward in time: and
+ * earlier ones), and to the state.  What they reach is NaN or infinite, not always the
+ * one that the recurrence gives.  Outputs before a tail of garbage are the sequence's.
+ *
  * workspace: the first 256 bytes are the status word (zeroed once with
  * gdn_workspace_init); fewer bytes return GDN_ERR_WORKSPACE.  The bytes after it,
  * of any contents, hold the state increments of segments when few long sequences are

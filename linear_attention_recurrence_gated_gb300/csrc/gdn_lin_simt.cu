@@ -16,10 +16,10 @@
 // in 66 % of the cycles (the rest waits for shared memory).  Small calls are latency:
 // [1, 256, 2, 32/32], four chunks cut apart, takes 12 us on the device (28 uncut).
 // P and its product skip what the mask leaves out, in blocks of 16 rows and columns.
-// S stays in registers and is put into shared memory once a chunk; masked
-// products are replaced by zeros and rows past the sequence's end are never
-// loaded, so nothing that lies there (an infinity, a NaN of the next sequence)
-// reaches a result.
+// S stays in registers and is put into shared memory once a chunk.  Products beyond the
+// mask are left out and rows past the sequence's end are never loaded, so nothing that
+// lies there (an infinity, a NaN of a later token or of the next sequence) reaches a
+// result.
 #include "gdn_lin.cuh"
 #include "gdn_launch.cuh"
 
@@ -369,10 +369,13 @@ gdn_lin_simt_kernel(const Params p) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             if (RG * (u + 1) <= b16) continue;  // (beyond the mask)
+            const bool edge = RG * u < b16 + 16;   // the mask runs through this block
             const float4 x = at4(P + (rg + RG * u) * kPd + j);
             const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+              // left out, not multiplied by zero: a later value may not be finite
+              if (edge && j + q > rg + RG * u) continue;
               acc[u][0] = fmaf(xs[q], y[q].x, acc[u][0]);
               acc[u][1] = fmaf(xs[q], y[q].y, acc[u][1]);
               acc[u][2] = fmaf(xs[q], y[q].z, acc[u][2]);

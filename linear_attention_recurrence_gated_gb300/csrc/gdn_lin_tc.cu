@@ -48,6 +48,12 @@
 // b and c rows are overwritten with zeros before any product reads them as a
 // term of a sum (0 * NaN would spoil it); their P' columns are zeros by
 // selection, their o rows are not stored.
+//
+// Values that are not finite.  O2 multiplies every value of the tile, those beyond the
+// mask by zero, and 0 * NaN makes NaN of a token's output that only a later token's
+// value could spoil.  The o warps look for it (one packed operation for four outputs) and
+// take such an output's sum again, over the tokens that it may see (`causal_sums`).  It
+// happens in the tile where a bad value first appears; from then on S has it too.
 #include "gdn_lin.cuh"
 #include "gdn_launch.cuh"
 #include "gdn_tc_common.cuh"
@@ -203,6 +209,78 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 __device__ __forceinline__ float power(float ld, float n) { return n == 0.f ? 1.f : expf(ld * n); }
+
+// A tile's row of o once more, for outputs whose O2 is NaN where O1 is not: the sum over
+// tokens from the row's own to the tile's first (backward: last of e) of lam^|i-j|
+// (a_i.b_j) c_j, in fp32 and from memory, goes over O2 in tensor memory (`t`: the warp's
+// lanes of it).  The whole warp together, a row a lane; registers are the caller's, so
+// the sums wait in local memory.
+__device__ __noinline__ void causal_sums(const Scan &s, int64_t tok, int h, int col0, int e,
+                                         const float *lam, uint32_t t) {
+  const int i = threadIdx.x & 127, H8 = s.da / 8;
+  const bool rev = s.reverse != 0;
+  bool some = false;
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint32_t x[8], y[8];
+    tmem_ld8(t + kColO1 + 8 * q, x);
+    tmem_ld8(t + kColO2 + 8 * q, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      some = some || (isnan(__uint_as_float(y[u])) && isfinite(__uint_as_float(x[u])));
+  }
+  some = some && i < e;
+  if (!__any_sync(0xffffffffu, some)) return;
+  float sum[64];
+#pragma unroll 1
+  for (int q = 0; q < 64; ++q) sum[q] = 0.f;
+  const auto row = [&](const void *p, int64_t stride, int j, int first) {
+    return reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p) +
+                                           (tok + j) * stride + first);
+  };
+  if (some) {
+    const uint4 *ai = row(s.a, s.sa, i, h * s.da);
+#pragma unroll 1
+    for (int j = i; rev ? j < e : j >= 0; j += rev ? 1 : -1) {
+      const uint4 *bj = row(s.b, s.sb, j, h * s.da), *cj = row(s.c, s.sc, j, h * s.dc + col0);
+      float p = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < H8; ++k) {
+        const uint4 a = ai[k], b = bj[k];
+        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          p = fmaf(bf16_lo(as[u]), bf16_lo(bs[u]), p);
+          p = fmaf(bf16_hi(as[u]), bf16_hi(bs[u]), p);
+        }
+      }
+      p *= lam[rev ? j - i : i - j];
+#pragma unroll 1
+      for (int q = 0; q < 8; ++q) {
+        const uint4 c = cj[q];
+        const uint32_t cs[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          sum[8 * q + 2 * u] = fmaf(p, bf16_lo(cs[u]), sum[8 * q + 2 * u]);
+          sum[8 * q + 2 * u + 1] = fmaf(p, bf16_hi(cs[u]), sum[8 * q + 2 * u + 1]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int q = 0; q < 8; ++q) {
+    uint32_t y[8];
+    tmem_ld8(t + kColO2 + 8 * q, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (some && isnan(__uint_as_float(y[u]))) y[u] = __float_as_uint(sum[8 * q + u]);
+    tmem_st8(t + kColO2 + 8 * q, y);
+  }
+  tmem_wait_st();
+}
 
 // STATES: the first launch of a split along time, which runs a segment from a zero
 // state and leaves its state increment (X and S alone).
@@ -602,25 +680,34 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
       ++done;
       uint4 *row = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(scan.o) +
                                              ((tok + i) * H + h) * dc + col0);
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        __nv_bfloat162 bad = __float2bfloat162_rn(0.f);   // NaN once one has been read
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t x[16], y[16], out[8];
-        tmem_ld16(tlane + kColO1 + 16 * q, x);
-        tmem_ld16(tlane + kColO2 + 16 * q, y);
-        tmem_wait_ld();
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[16], y[16], out[8];
+          tmem_ld16(tlane + kColO1 + 16 * q, x);
+          tmem_ld16(tlane + kColO2 + 16 * q, y);
+          tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          out[u] = pack_pair(fma2(pair(f, f), pair(x[2 * u], x[2 * u + 1]),
-                                  pair(y[2 * u], y[2 * u + 1])));
-        const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]),
-                    hi = make_uint4(out[4], out[5], out[6], out[7]);
-        if (e == kC) {
-          S4(swz<kTile>(so, i, 16 * q)) = lo;
-          S4(swz<kTile>(so, i, 16 * q + 8)) = hi;
-        } else if (i < e) {
-          row[2 * q] = lo;
-          row[2 * q + 1] = hi;
+          for (int u = 0; u < 8; ++u)
+            out[u] = pack_pair(fma2(pair(f, f), pair(x[2 * u], x[2 * u + 1]),
+                                    pair(y[2 * u], y[2 * u + 1])));
+#pragma unroll
+          for (int u = 0; u < 8; u += 2) bad = __hfma2(as_bf162(out[u]), as_bf162(out[u + 1]), bad);
+          const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]),
+                      hi = make_uint4(out[4], out[5], out[6], out[7]);
+          if (e == kC) {
+            S4(swz<kTile>(so, i, 16 * q)) = lo;
+            S4(swz<kTile>(so, i, 16 * q + 8)) = hi;
+          } else if (i < e) {
+            row[2 * q] = lo;
+            row[2 * q + 1] = hi;
+          }
         }
+        const bool nan = __hisnan(__low2bfloat16(bad)) || __hisnan(__high2bfloat16(bad));
+        if (again || !__any_sync(0xffffffffu, nan && i < e)) break;
+        causal_sums(scan, tok, h, col0, e, lam, tlane);
       }
       tc_fence_before();
       warp_arrive(w.at(kOFree));
