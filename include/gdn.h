@@ -736,7 +736,9 @@ gdn_status gdn_group_norm_bwd(const void *x, const float *weight, const float *b
  * GDN_ERR_NO_PAGES is recorded.
  *
  * gdn_pages_free: rows rows[i], i < n, give their pages back (refs - 1) and are
- * empty afterwards; a row listed twice is freed once.
+ * empty afterwards; a row listed twice is freed once.  A job whose row, count, or one of
+ * whose pages is out of range, or that holds a page with refs 0, is left out.  A page
+ * held by more of the rows than its refs say ends at refs 0 and is recorded.
  *
  * gdn_pages_compact: the live pages move to the lowest numbers, keeping those
  * already there: the k-th live page at or above num_live moves to the k-th free

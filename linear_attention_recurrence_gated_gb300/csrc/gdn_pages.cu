@@ -196,37 +196,60 @@ __global__ void __launch_bounds__(kPlan) copy_plan_kernel(const Params p) {
   if (threadIdx.x == 0) *p.num_jobs = p.n;
 }
 
+// Pages four at a time: one latency for all.  `use(m, page)` for each of `cnt` entries.
+template <typename F>
+__device__ __forceinline__ void four_at_a_time(const int32_t *row, int cnt, F use) {
+  for (int m0 = 0; m0 < cnt; m0 += 4) {
+    int pg[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pg[k] = m0 + k < cnt ? row[m0 + k] : -1;
+    use(m0, pg);
+  }
+}
+
+// Two passes: what breaks a rule is judged by the arguments as they came, before any of
+// them changes, so that a job is left out whole and whatever the others do.  The jobs go
+// to the last threads, which have the least to copy.  tmp0: the jobs' counts, -1 for one
+// that is left out.
 __global__ void __launch_bounds__(kPlan) free_kernel(const Params p) {
-  const int tid = threadIdx.x, R = p.num_rows, M = p.max_pages;
+  const int R = p.num_rows, M = p.max_pages, first = kPlan - 1 - (int)threadIdx.x;
+  for (int i = first; i < p.n; i += kPlan) {
+    const int r = p.a[i];
+    const bool there = r >= 0 && r < R;
+    const int cnt = there ? p.counts[r] : -1;
+    bool ok = cnt >= 0 && cnt <= M;
+    if (ok)
+      four_at_a_time(p.table + (int64_t)r * M, cnt, [&](int m0, const int (&pg)[4]) {
+        int held[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          held[k] = pg[k] >= 0 && pg[k] < p.num_pages ? p.refs[pg[k]] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ok = ok && (m0 + k >= cnt || held[k] > 0);
+      });
+    if (!ok) bad(p, i, GDN_ERR_DEVICE_CHECK, 0u);
+    p.tmp0[i] = ok ? cnt : -1;
+  }
   copy_bookkeeping(p);
   __syncthreads();
-  for (int i = tid; i < p.n; i += kPlan) {
+  for (int i = first; i < p.n; i += kPlan) {
+    if (p.tmp0[i] < 0) continue;
     const int r = p.a[i];
-    if (r < 0 || r >= R) {
-      bad(p, i, GDN_ERR_DEVICE_CHECK, 0u);
-      continue;
-    }
-    // a row listed twice is freed once
-    const int cnt = atomicExch(&p.counts_out[r], 0);
-    if (cnt < 0 || cnt > M) {
-      bad(p, i, GDN_ERR_DEVICE_CHECK, 0u);
-      continue;
-    }
+    const int cnt = atomicExch(&p.counts_out[r], 0);   // a row listed twice is freed once
     int32_t *row = p.table_out + (int64_t)r * M;
-    for (int m0 = 0; m0 < cnt; m0 += 4) {  // four at a time: one latency for all
-      int pg[4], held[4];
+    four_at_a_time(row, cnt, [&](int m0, const int (&pg)[4]) {
+      int held[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pg[k] = m0 + k < cnt ? row[m0 + k] : -2;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        held[k] = pg[k] >= 0 && pg[k] < p.num_pages ? atomicSub(&p.refs_out[pg[k]], 1) : 0;
+      for (int k = 0; k < 4; ++k) held[k] = m0 + k < cnt ? atomicSub(&p.refs_out[pg[k]], 1) : 1;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (m0 + k >= cnt) continue;
-        row[m0 + k] = -1;
-        if (held[k] <= 0) bad(p, i, GDN_ERR_DEVICE_CHECK, 0u);
+        if (m0 + k < cnt) row[m0 + k] = -1;
+        if (held[k] <= 0) {   // held by more rows than it counts: it stays at zero
+          atomicAdd(&p.refs_out[pg[k]], 1);
+          bad(p, i, GDN_ERR_DEVICE_CHECK, 0u);
+        }
       }
-    }
+    });
   }
 }
 

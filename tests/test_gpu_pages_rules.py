@@ -1,0 +1,75 @@
+"""Page calls whose bookkeeping is out of step (jobs that break a rule are left out and
+recorded).  Whole numbers: no tolerance."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from linear_attention_recurrence_gated_gb300 import gdn as G
+from test_gpu_pages import dev
+
+pytestmark = pytest.mark.gpu
+
+
+def host(*tensors):
+    return [t.cpu().numpy() for t in tensors]
+
+
+def free(table, counts, refs, rows, in_place, P):
+    t, c, r = dev(table), dev(counts), dev(refs)
+    ws = torch.zeros(G.gdn_pages_workspace_size(P, len(counts), len(rows)), dtype=torch.uint8,
+                     device="cuda")
+    kw = dict(table_out=t, counts_out=c, refs_out=r) if in_place else {}
+    out = G.gdn_pages_free(t, c, r, dev(rows), workspace=ws, **kw)
+    return host(*out), G.gdn_check_record(ws)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n_more", [0, 1500])
+@pytest.mark.parametrize("bad", ["count below zero", "count too large", "page below zero",
+                                 "page too large", "free page"])
+def test_free_leaves_a_bad_job_out(in_place, bad, n_more):
+    """The row of such a job keeps its count, its pages and their references; the other
+    jobs run (also when there are more of them than one pass of the CTA takes)."""
+    P, R, M = 4000, 1600, 3
+    table, counts, refs = np.full((R, M), -1), np.zeros(R, int), np.zeros(P, int)
+    for r in range(R):
+        counts[r] = 1 + r % M
+        table[r, : counts[r]] = 2 * r + np.arange(counts[r])
+        np.add.at(refs, table[r, : counts[r]], 1)
+    which = 5                                             # three pages
+    if bad == "count below zero":
+        counts[which] = -2
+    elif bad == "count too large":
+        counts[which] = M + 1
+    elif bad == "page below zero":
+        table[which, 1] = -1
+    elif bad == "page too large":
+        table[which, 1] = P
+    else:
+        refs[table[which, 1]] = 0
+    rows = [3, which, 9] + list(range(20, 20 + n_more))
+    (t, c, r), (st, job, _, _) = free(table, counts, refs, rows, in_place, P)
+    assert (st, job) == (7, 1)
+    for row in rows:
+        if row != which:
+            refs[table[row, : counts[row]]] -= 1
+            table[row], counts[row] = -1, 0
+    assert np.array_equal(t, table) and np.array_equal(c, counts) and np.array_equal(r, refs)
+    # a bad job that is listed twice stays left out
+    (t, c, r), (st, _, _, _) = free(table, counts, refs, [which, which], in_place, P)
+    assert st == 7
+    assert np.array_equal(t, table) and np.array_equal(c, counts) and np.array_equal(r, refs)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_references_do_not_fall_below_zero(in_place):
+    """Two rows hold a page that counts one: both rows give it back and are empty, its
+    count ends at zero and the call says that something was wrong."""
+    table = np.array([[4, 1], [4, 2], [4, 3]])
+    counts, refs = np.array([2, 2, 2]), np.array([0, 1, 1, 1, 1, 0])
+    (t, c, r), (st, job, _, _) = free(table, counts, refs, [0, 2], in_place, 6)
+    assert st == 7 and job in (0, 1)
+    assert np.array_equal(t, [[-1, -1], [4, 2], [-1, -1]]) and np.array_equal(c, [0, 2, 0])
+    assert np.array_equal(r, [0, 0, 1, 0, 0, 0])
