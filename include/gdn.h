@@ -743,7 +743,8 @@ gdn_status gdn_group_norm_bwd(const void *x, const float *weight, const float *b
  * gdn_pages_compact: the live pages move to the lowest numbers, keeping those
  * already there: the k-th live page at or above num_live moves to the k-th free
  * page below it.  *num_live (device, written) is the number of live pages; table and refs
- * are rewritten, counts do not change.
+ * are rewritten, counts do not change.  An entry within its row's count whose number is
+ * out of range or a free page's becomes -1 and is recorded, with its row in `seq`.
  *
  * workspace: at least gdn_pages_workspace_size(num_pages, num_rows, n) bytes
  * (n = 0 for compact); its first 256 bytes are the status word, zeroed once

@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const Params p) {
   }
 }
 
-// tmp0: the new number of every page; tmp1: the free pages below the live
-// count, ascending.  The k-th live page above it moves to the k-th of them.
+// tmp0: the new number of every page, -1 for a free one; tmp1: the free pages below the
+// live count, ascending.  The k-th live page above it moves to the k-th of them.
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Params p) {
   let_second();
   __shared__ int warp_sums[kPlan / 32];
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const Params p) {
     if (hole) p.tmp1[holes + (at & 0xffff)] = pg;
     if (move) p.jobs[moves + (at >> 16)] = make_int2(pg, r);
     if (pg < P) {
-      p.tmp0[pg] = pg;
+      p.tmp0[pg] = r > 0 ? pg : -1;
       if (p.refs_out != p.refs) p.refs_out[pg] = r;
     }
     holes += total & 0xffff;
@@ -313,9 +313,12 @@ __global__ void __launch_bounds__(kCopy) copy_pages_kernel(const Params p, int p
     for (int64_t i = (int64_t)blockIdx.x * kCopy + threadIdx.x; i < all;
          i += (int64_t)gridDim.x * kCopy) {
       const int r = (int)(i / p.max_pages), m = (int)(i % p.max_pages);
-      const int pg = m < p.counts[r] ? p.table[i] : -1;
-      if (pg >= p.num_pages || (pg < 0 && m < p.counts[r])) bad(p, r, GDN_ERR_DEVICE_CHECK, 0u);
-      p.table_out[i] = pg >= 0 && pg < p.num_pages ? p.tmp0[pg] : -1;
+      const bool held = m < p.counts[r];
+      const int pg = held ? p.table[i] : -1;
+      const int to = pg >= 0 && pg < p.num_pages ? p.tmp0[pg] : -1;
+      // a number out of range, or of a free page, where another may have moved to
+      if (held && to < 0) bad(p, r, GDN_ERR_DEVICE_CHECK, 0u);
+      p.table_out[i] = to;
     }
   }
   const int64_t work = (int64_t)*p.num_jobs * pieces;

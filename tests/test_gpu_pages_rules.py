@@ -73,3 +73,26 @@ def test_references_do_not_fall_below_zero(in_place):
     assert st == 7 and job in (0, 1)
     assert np.array_equal(t, [[-1, -1], [4, 2], [-1, -1]]) and np.array_equal(c, [0, 2, 0])
     assert np.array_equal(r, [0, 0, 1, 0, 0, 0])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("P", [12, 6000])
+def test_compact_drops_a_free_page_that_a_row_names(in_place, P):
+    """Rows 0 and 1 name page 1, which is free: another page moves there, and they must
+    not come to share it.  Their entries become -1 and the call records the rule."""
+    pool = torch.arange(P, dtype=torch.float32, device="cuda")[:, None].repeat(1, 4)
+    table = np.full((4, 2), -1)
+    table[0], table[1], table[2, 0], table[3, 0] = (0, 1), (1, 3), P - 1, P - 4
+    counts, refs = np.array([2, 2, 1, 1]), np.zeros(P, int)
+    refs[[0, 3, P - 1, P - 4]] = 1
+    t, c, r = dev(table), dev(counts), dev(refs)
+    ws = torch.zeros(G.gdn_pages_workspace_size(P, 4, 0), dtype=torch.uint8, device="cuda")
+    kw = dict(table_out=t, refs_out=r) if in_place else {}
+    num, t, r = G.gdn_pages_compact(pool, t, c, r, workspace=ws, **kw)
+    st, row, _, _ = G.gdn_check_record(ws)
+    assert st == 7 and row in (0, 1)
+    t, r = host(t, r)
+    assert num.item() == 4
+    assert np.array_equal(t, [[0, -1], [-1, 3], [2, -1], [1, -1]])
+    assert np.array_equal(np.flatnonzero(r), [0, 1, 2, 3])
+    assert pool[:4, 0].tolist() == [0, P - 4, P - 1, 3]
