@@ -715,7 +715,9 @@ gdn_status gdn_group_norm_bwd(const void *x, const float *weight, const float *b
  *   refs    [num_pages] int32             rows that hold each page; 0: the page is free
  *
  * All of them are device memory.  table_out, counts_out and refs_out receive
- * the new bookkeeping; each may be its input (updated in place).  Every result
+ * the new bookkeeping; each may be its input (updated in place).  A table without rows
+ * (num_rows 0, n 0; table, counts and their outputs are not looked at) is legal: refs_out
+ * is written all the same.  Every result
  * depends on the arguments alone (new pages are the lowest free ones, in the
  * order of the list), so it is the same from run to run.  A job that breaks a
  * rule is left out and recorded for gdn_check (GDN_ERR_DEVICE_CHECK with the

@@ -466,9 +466,9 @@ gdn_status gdn_pages_fork(void *pool, int64_t page_bytes, int32_t num_pages, con
   const gdn_status st =
       check(num_pages, num_rows, max_pages, n, page_bytes, workspace, workspace_bytes);
   if (st != GDN_OK) return st;
-  if (num_rows == 0) return n == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
-  if (!pool || !table || !counts || !refs || !table_out || !counts_out || !refs_out)
-    return GDN_ERR_INVALID_ARG;
+  if (num_rows == 0 && n > 0) return GDN_ERR_INVALID_ARG;
+  if (!pool || !refs || !refs_out) return GDN_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!table || !counts || !table_out || !counts_out)) return GDN_ERR_INVALID_ARG;
   if (n > 0 && (!parents || !children || !fresh)) return GDN_ERR_INVALID_ARG;
   const void *ptrs[] = {pool, table, counts, refs, parents, children, fresh, table_out, counts_out,
                         refs_out};
@@ -503,9 +503,9 @@ gdn_status gdn_pages_free(const int32_t *table, const int32_t *counts, const int
   using namespace gdn::pages;
   const gdn_status st = check(num_pages, num_rows, max_pages, n, 16, workspace, workspace_bytes);
   if (st != GDN_OK) return st;
-  if (num_rows == 0) return n == 0 ? GDN_OK : GDN_ERR_INVALID_ARG;
-  if (!table || !counts || !refs || !table_out || !counts_out || !refs_out || (n > 0 && !rows))
-    return GDN_ERR_INVALID_ARG;
+  if (num_rows == 0 && n > 0) return GDN_ERR_INVALID_ARG;
+  if (!refs || !refs_out || (n > 0 && !rows)) return GDN_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!table || !counts || !table_out || !counts_out)) return GDN_ERR_INVALID_ARG;
   const void *ptrs[] = {table, counts, refs, rows, table_out, counts_out, refs_out};
   for (const void *q : ptrs)
     if (q && !aligned16(q)) return GDN_ERR_INVALID_ARG;
@@ -535,9 +535,8 @@ gdn_status gdn_pages_compact(void *pool, int64_t page_bytes, int32_t num_pages,
   const gdn_status st =
       check(num_pages, num_rows, max_pages, 0, page_bytes, workspace, workspace_bytes);
   if (st != GDN_OK) return st;
-  if (num_rows == 0) return GDN_ERR_INVALID_ARG;
-  if (!pool || !table || !counts || !refs || !num_live || !table_out || !refs_out)
-    return GDN_ERR_INVALID_ARG;
+  if (!pool || !refs || !num_live || !refs_out) return GDN_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!table || !counts || !table_out)) return GDN_ERR_INVALID_ARG;
   const void *ptrs[] = {pool, table, counts, refs, num_live, table_out, refs_out};
   for (const void *q : ptrs)
     if (q && !aligned16(q)) return GDN_ERR_INVALID_ARG;

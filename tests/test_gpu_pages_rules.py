@@ -1,5 +1,5 @@
 """Page calls whose bookkeeping is out of step (jobs that break a rule are left out and
-recorded).  Whole numbers: no tolerance."""
+recorded) and tables without rows.  Whole numbers: no tolerance."""
 from __future__ import annotations
 
 import numpy as np
@@ -96,3 +96,32 @@ def test_compact_drops_a_free_page_that_a_row_names(in_place, P):
     assert np.array_equal(t, [[0, -1], [-1, 3], [2, -1], [1, -1]])
     assert np.array_equal(np.flatnonzero(r), [0, 1, 2, 3])
     assert pool[:4, 0].tolist() == [0, P - 4, P - 1, 3]
+
+
+def test_a_table_without_rows():
+    """The reference counts come out as they went in; a pool with pages that no row names
+    is compacted all the same."""
+    P = 300
+    pool = torch.arange(P, dtype=torch.float32, device="cuda")[:, None].repeat(1, 4)
+    refs = np.zeros(P, int)
+    refs[[7, 299]] = 2, 1
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    table, counts = none.view(0, 3), none
+    for _ in range(3):
+        # what the allocator hands out next has been used for something else
+        junk = [torch.full((P,), 77, dtype=torch.int32, device="cuda") for _ in range(6)]
+        del junk
+        fresh, t, c, r = G.gdn_pages_fork(pool, table, counts, dev(refs), none, none, check=True)
+        assert fresh.numel() == 0 and t.shape == (0, 3) and c.shape == (0,)
+        assert np.array_equal(host(r)[0], refs)
+        junk = [torch.full((P,), 77, dtype=torch.int32, device="cuda") for _ in range(6)]
+        del junk
+        t, c, r = G.gdn_pages_free(table, counts, dev(refs), none, check=True)
+        assert t.shape == (0, 3) and np.array_equal(host(r)[0], refs)
+    r = dev(refs)
+    _, _, _, same = G.gdn_pages_fork(pool, table, counts, r, none, none, refs_out=r, check=True)
+    assert same is r and np.array_equal(host(r)[0], refs)
+    num, t, r = G.gdn_pages_compact(pool, table, counts, dev(refs), check=True)
+    assert num.item() == 2 and t.shape == (0, 3)
+    assert host(r)[0].tolist() == [2, 1] + [0] * (P - 2)   # 7 and 299 move to 0 and 1
+    assert pool[:2, 0].tolist() == [7, 299]
