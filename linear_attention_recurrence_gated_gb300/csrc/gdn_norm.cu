@@ -13,7 +13,9 @@
 // squared deviation) triples are joined.  Their means are kept relative to the
 // group's first value x0, and a value is normalised as ((x - x0) - mean) rstd:
 // a mean far from zero cancels nothing and is rounded once, as it is stored.
-// No sum runs over more than 128 values one after the other.
+// The gradients' sums over rows and samples are taken in blocks of kSum, whose results
+// are added up: one plain sum over the rows of a CTA was off by 4e-5 for 3449 rows of
+// equal terms.  Sums over lanes, threads and CTAs run over 512 values at most.
 #include <stdint.h>
 
 #include "gdn_internal.cuh"
@@ -26,7 +28,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSMs = 152;
 constexpr int kBlock = 16;   // rows summed by a thread before it joins them
-constexpr int kParts = 4 * kSMs;   // partial sums of dweight and dbias at most
+constexpr int kSum = 128;    // rows, or samples, that one plain sum of gradients runs over
+constexpr int kParts = 4 * kSMs;   // partial sums of dweight and dbias (slabs: one each)
 
 // Three forms, by the sample's size:
 //   rows    S = 1 and a group fits a warp's registers: a group is a power of two
@@ -414,45 +417,72 @@ gdn_norm_bwd_kernel(const Params p) {
   const T *xs = static_cast<const T *>(p.x), *zs = static_cast<const T *>(p.gate),
           *dys = static_cast<const T *>(p.dy);
   for (int i = tid; i < TY * p.C; i += kThreads) sc[i] = make_float2(0.f, 0.f);
+  // the channels' running sums into the CTA's partial ones
+  float *const part = p.part + (size_t)blockIdx.x * 2 * p.C;
+  int samples = 0;
+  bool fresh = true;
+  const auto close = [&]() {
+    __syncthreads();
+    for (int c = tid; c < p.C; c += kThreads) {
+      float2 a = make_float2(0.f, 0.f);
+      for (int r = 0; r < TY; ++r) {
+        a.x += sc[r * p.C + c].x;
+        a.y += sc[r * p.C + c].y;
+        sc[r * p.C + c] = make_float2(0.f, 0.f);
+      }
+      part[c] = fresh ? a.x : part[c] + a.x;
+      part[p.C + c] = fresh ? a.y : part[p.C + c] + a.y;
+    }
+    fresh = false;
+    samples = 0;
+  };
   const float inv = 1.f / ((float)p.S * (float)p.D);
   for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x) {
+    if (samples == kSum) close();
+    ++samples;
     const int64_t base = n * p.S * p.C;
     __syncthreads();
-    for (int cv = tx; cv < CV && ty < TY; cv += TX) {
-      const int g = cv / DV;
-      const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
-      float w[V], b[V], a1[V], a2[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        w[i] = p.w ? p.w[cv * V + i] : 1.f;
-        b[i] = p.b ? p.b[cv * V + i] : 0.f;
-        a1[i] = a2[i] = 0.f;
-      }
-      for (int64_t r = ty; r < p.S; r += TY) {
-        const int64_t at = base + r * p.C + cv * V;
-        float v[V], z[V], dy[V];
-        load<V>(xs + at, v);
-        load<V>(dys + at, dy);
-        if (gated) load<V>(zs + at, z);
+#pragma unroll 1
+    for (int64_t from = 0; from < p.S; from += kSum * TY) {
+      const int64_t to = from + kSum * TY < p.S ? from + kSum * TY : p.S;
+      for (int cv = tx; cv < CV && ty < TY; cv += TX) {
+        const int g = cv / DV;
+        const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
+        float w[V], b[V], a1[V], a2[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float xh = (v[i] - mean) * rstd;
-          float dz;
-          const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
-          a1[i] += du;
-          a2[i] = fmaf(du, xh, a2[i]);
+          w[i] = p.w ? p.w[cv * V + i] : 1.f;
+          b[i] = p.b ? p.b[cv * V + i] : 0.f;
+          a1[i] = a2[i] = 0.f;
         }
-      }
-      float t1 = 0.f, t2 = 0.f;
+        for (int64_t r = from + ty; r < to; r += TY) {
+          const int64_t at = base + r * p.C + cv * V;
+          float v[V], z[V], dy[V];
+          load<V>(xs + at, v);
+          load<V>(dys + at, dy);
+          if (gated) load<V>(zs + at, z);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        t1 = fmaf(a1[i], w[i], t1);
-        t2 = fmaf(a2[i], w[i], t2);
-        float2 &acc = sc[ty * p.C + cv * V + i];
-        acc.x += a2[i];
-        acc.y += a1[i];
+          for (int i = 0; i < V; ++i) {
+            const float xh = (v[i] - mean) * rstd;
+            float dz;
+            const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
+            a1[i] += du;
+            a2[i] = fmaf(du, xh, a2[i]);
+          }
+        }
+        float t1 = 0.f, t2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          t1 = fmaf(a1[i], w[i], t1);
+          t2 = fmaf(a2[i], w[i], t2);
+          float2 &acc = sc[ty * p.C + cv * V + i];
+          acc.x += a2[i];
+          acc.y += a1[i];
+        }
+        float2 &sum = st[ty * CV + cv];
+        if (from) t1 += sum.x, t2 += sum.y;
+        sum = make_float2(t1, t2);
       }
-      st[ty * CV + cv] = make_float2(t1, t2);
     }
     __syncthreads();
     for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
@@ -499,16 +529,7 @@ gdn_norm_bwd_kernel(const Params p) {
       }
     }
   }
-  __syncthreads();
-  for (int c = tid; c < p.C; c += kThreads) {
-    float2 a = make_float2(0.f, 0.f);
-    for (int r = 0; r < TY; ++r) {
-      a.x += sc[r * p.C + c].x;
-      a.y += sc[r * p.C + c].y;
-    }
-    p.part[(size_t)blockIdx.x * 2 * p.C + c] = a.x;
-    p.part[(size_t)blockIdx.x * 2 * p.C + p.C + c] = a.y;
-  }
+  close();
 }
 
 // dw and db: W columns for a CTA, its rows of threads over the partial sums, both in
@@ -518,8 +539,13 @@ __device__ __forceinline__ void sum_columns(const Params &p, int parts, int col0
   const int tx = threadIdx.x % W, ty = threadIdx.x / W, rows = blockDim.x / W, i = col0 + tx;
   float a = 0.f;
   if (i < 2 * p.C)
+    for (int k0 = ty; k0 < parts; k0 += kSum * rows) {
+      float t = 0.f;
 #pragma unroll 4
-    for (int k = ty; k < parts; k += rows) a += p.part[(size_t)k * 2 * p.C + i];
+      for (int k = k0; k < parts && k < k0 + kSum * rows; k += rows)
+        t += p.part[(size_t)k * 2 * p.C + i];
+      a += t;
+    }
   sm[ty * (W + 1) + tx] = a;
   __syncthreads();
   if (ty == 0) {
@@ -666,78 +692,94 @@ gdn_norm_rows_bwd_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) a1[r][i] = a2[r][i] = 0;
   }
-  const int64_t step = (int64_t)gridDim.x * m.rows;
-  for (int64_t n0 = (int64_t)blockIdx.x * m.rows; n0 < p.N; n0 += step) {
-    const int64_t n = n0 + ry;
-    const bool have = on && n < p.N;
-    const int64_t base = n * p.C + (int64_t)gx * p.D;
-    Raw<T, V> x[R], dy[R], z[R];
-    float mean = 0.f, rstd = 0.f;
-    if (have) {
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int cv = l + r * m.lpg;
-        if (FULL || cv < DV) {
-          x[r].load(xs + base + cv * V);
-          dy[r].load(dys + base + cv * V);
-          if (gated) z[r].load(zs + base + cv * V);
-        }
-      }
-      mean = p.mean[n * p.G + gx];
-      rstd = p.rstd[n * p.G + gx];
-    }
-    Pair xh[R][NP], du[R][NP], t1 = 0, t2 = 0;
-    if (have)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int cv = l + r * m.lpg;
-        if (FULL || cv < DV) {
-          Pair dz[NP];
-#pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            xh[r][i] = mul2(add2(x[r].at(i), both(-mean)), both(rstd));
-            dz[i] = 0;
-            du[r][i] = grad_u2<T, M>(fma2(xh[r][i], w[r][i], b[r][i]), gated ? z[r].at(i) : 0, dy[r].at(i),
-                                     p, dz[i]);
-            a1[r][i] = add2(a1[r][i], du[r][i]);
-            a2[r][i] = fma2(du[r][i], xh[r][i], a2[r][i]);
-            du[r][i] = mul2(du[r][i], w[r][i]);
-            t1 = add2(t1, du[r][i]);
-            t2 = fma2(du[r][i], xh[r][i], t2);
-          }
-          if (gated) put<T, V>(static_cast<T *>(p.dgate) + base + cv * V, dz);
-        }
-      }
-    // (a single value's empty second lane: du and w are zero there)
-    const float2 u1 = un(t1), u2 = un(t2);
-    const float c1 = lanes_sum<R>(u1.x + u1.y, m.lpg) * inv, c2 = lanes_sum<R>(u2.x + u2.y, m.lpg) * inv;
-    if (have)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int cv = l + r * m.lpg;
-        if (FULL || cv < DV) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            du[r][i] = mul2(both(rstd), fma2(xh[r][i], both(-c2), add2(du[r][i], both(-c1))));
-          put<T, V>(static_cast<T *>(p.dx) + base + cv * V, du[r]);
-        }
-      }
-  }
-  // the channels' sums of this CTA, over its rows of threads
+  // the thread's sums into their place in shared memory
   float2 *sc = reinterpret_cast<float2 *>(sm);
   const int width = m.groups * p.D;
-  if (on)
+  bool fresh = true;
+  const auto close = [&]() {
+    if (on)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int cv = l + r * m.lpg;
-      if (FULL || cv < DV)
+      for (int r = 0; r < R; ++r) {
+        const int cv = l + r * m.lpg;
+        if (FULL || cv < DV)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 q1 = un(a1[r][i / 2]), q2 = un(a2[r][i / 2]);
-          sc[(size_t)ry * width + (slot % m.groups) * p.D + cv * V + i] =
-              i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
+          for (int i = 0; i < V; ++i) {
+            const float2 q1 = un(a1[r][i / 2]), q2 = un(a2[r][i / 2]);
+            float2 &to = sc[(size_t)ry * width + (slot % m.groups) * p.D + cv * V + i];
+            float2 sum = i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
+            if (!fresh) sum.x += to.x, sum.y += to.y;
+            to = sum;
+          }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) a1[r][i] = a2[r][i] = 0;
+      }
+    fresh = false;
+  };
+  const int64_t step = (int64_t)gridDim.x * m.rows;
+  int64_t n0 = (int64_t)blockIdx.x * m.rows;
+#pragma unroll 1
+  for (int64_t stop = n0 + kSum * step;; stop += kSum * step) {
+    for (const int64_t end = stop < p.N ? stop : p.N; n0 < end; n0 += step) {
+      const int64_t n = n0 + ry;
+      const bool have = on && n < p.N;
+      const int64_t base = n * p.C + (int64_t)gx * p.D;
+      Raw<T, V> x[R], dy[R], z[R];
+      float mean = 0.f, rstd = 0.f;
+      if (have) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int cv = l + r * m.lpg;
+          if (FULL || cv < DV) {
+            x[r].load(xs + base + cv * V);
+            dy[r].load(dys + base + cv * V);
+            if (gated) z[r].load(zs + base + cv * V);
+          }
+        }
+        mean = p.mean[n * p.G + gx];
+        rstd = p.rstd[n * p.G + gx];
+      }
+      Pair xh[R][NP], du[R][NP], t1 = 0, t2 = 0;
+      if (have)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int cv = l + r * m.lpg;
+          if (FULL || cv < DV) {
+            Pair dz[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              xh[r][i] = mul2(add2(x[r].at(i), both(-mean)), both(rstd));
+              dz[i] = 0;
+              du[r][i] = grad_u2<T, M>(fma2(xh[r][i], w[r][i], b[r][i]),
+                                       gated ? z[r].at(i) : 0, dy[r].at(i), p, dz[i]);
+              a1[r][i] = add2(a1[r][i], du[r][i]);
+              a2[r][i] = fma2(du[r][i], xh[r][i], a2[r][i]);
+              du[r][i] = mul2(du[r][i], w[r][i]);
+              t1 = add2(t1, du[r][i]);
+              t2 = fma2(du[r][i], xh[r][i], t2);
+            }
+            if (gated) put<T, V>(static_cast<T *>(p.dgate) + base + cv * V, dz);
+          }
+        }
+      // (a single value's empty second lane: du and w are zero there)
+      const float2 u1 = un(t1), u2 = un(t2);
+      const float c1 = lanes_sum<R>(u1.x + u1.y, m.lpg) * inv,
+                  c2 = lanes_sum<R>(u2.x + u2.y, m.lpg) * inv;
+      if (have)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int cv = l + r * m.lpg;
+          if (FULL || cv < DV) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+              du[r][i] = mul2(both(rstd), fma2(xh[r][i], both(-c2), add2(du[r][i], both(-c1))));
+            put<T, V>(static_cast<T *>(p.dx) + base + cv * V, du[r]);
+          }
         }
     }
+    close();
+    if (n0 >= p.N) break;
+  }
+  // the channels' sums of this CTA, over its rows of threads
   __syncthreads();
   for (int i = tid; i < width; i += kThreads) {
     const int c = blockIdx.y * width + i;
@@ -832,7 +874,7 @@ struct Rows {
         x.load(reinterpret_cast<const T *>(from));
         if (DY) dy.load(reinterpret_cast<const T *>(from += th));
         if (gated) z.load(reinterpret_cast<const T *>(from += th));
-        use(o, x, dy, z);
+        use(i, o, x, dy, z);
         ahead = stage;
         stage = stage + 1 == kDepth ? 0 : stage + 1;
       }
@@ -844,7 +886,7 @@ struct Rows {
         x.load(xs + o);
         if (DY) dy.load(dys + o);
         if (gated) z.load(zs + o);
-        use(o, x, dy, z);
+        use(i, o, x, dy, z);
       }
     }
   }
@@ -882,7 +924,7 @@ gdn_norm_slab_stats_kernel(const Params p) {
       s1 = s2 = 0;
     };
     rows.run(
-        cv * V, [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &) {
+        cv * V, [&](int, int64_t, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &) {
           if (cnt == 0.f) c = un(x.at(0)).x;
 #pragma unroll
           for (int i = 0; i < (V + 1) / 2; ++i) {
@@ -957,7 +999,7 @@ gdn_norm_slab_apply_kernel(const Params p) {
     weights<V>(p.b, cv * V, true, 0.f, b);
     if (cv != tx) rows.start(cv * V);
     rows.run(
-        cv * V, [&](int64_t at, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &z) {
+        cv * V, [&](int, int64_t at, const Raw<T, V> &x, const Raw<T, V> &, const Raw<T, V> &z) {
           Pair y[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
@@ -997,8 +1039,23 @@ gdn_norm_slab_grads_kernel(const Params p) {
     weights<V>(p.b, cv * V, true, 0.f, b);
 #pragma unroll
     for (int i = 0; i < NP; ++i) a1[i] = a2[i] = 0;
+    float2 *const mine = sc + (size_t)ty * p.C + cv * V;
+    bool fresh = true;
+    const auto close = [&]() {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 q1 = un(a1[i / 2]), q2 = un(a2[i / 2]);
+        float2 sum = i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
+        if (!fresh) sum.x += mine[i].x, sum.y += mine[i].y;
+        mine[i] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) a1[i] = a2[i] = 0;
+      fresh = false;
+    };
     rows.run(
-        cv * V, [&](int64_t, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+        cv * V, [&](int row, int64_t, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+          if (row % kSum == kSum - 1) close();
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             const Pair xh = mul2(add2(x.at(i), both(-mean)), both(rstd));
@@ -1009,11 +1066,7 @@ gdn_norm_slab_grads_kernel(const Params p) {
             a2[i] = fma2(du, xh, a2[i]);
           }
         });
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float2 q1 = un(a1[i / 2]), q2 = un(a2[i / 2]);
-      sc[(size_t)ty * p.C + cv * V + i] = i & 1 ? make_float2(q2.y, q1.y) : make_float2(q2.x, q1.x);
-    }
+    close();
   }
   __syncthreads();
   const size_t slab = (size_t)n * p.slabs + blockIdx.x;
@@ -1097,7 +1150,7 @@ gdn_norm_slab_dx_kernel(const Params p) {
     weights<V>(p.b, cv * V, true, 0.f, b);
     if (cv != tx) rows.start(cv * V);
     rows.run(
-        cv * V, [&](int64_t at, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
+        cv * V, [&](int, int64_t at, const Raw<T, V> &x, const Raw<T, V> &dy, const Raw<T, V> &z) {
           Pair dx[NP], dz[NP];
 #pragma unroll
           for (int i = 0; i < NP; ++i) {

@@ -3,8 +3,8 @@ a long plain sum go the same way.
 
 Bound.  A sum of terms of one sign is off by at most 2^-24 of itself for each addition
 that a term passes through.  A thread adds up to 128 rows, and the results of these
-blocks; a CTA its rows of threads (64 or fewer at these sizes), and the call its CTAs in
-blocks of 64 by up to 64 rows of threads: fewer than 512 additions, 2^-15.  Adding one
+blocks; a CTA its rows of threads (64 or fewer at these sizes), and the call its CTAs by
+up to 64 rows of threads: fewer than 512 additions, 2^-15.  Adding one
 constant again and again is off by the same amount each time while the sum stays within
 a binade, so that the last binade of a stage (half its additions) decides, with an error
 that is a quarter of the largest in the mean: 2^-17 = 7.6e-6, and twice that is asked
