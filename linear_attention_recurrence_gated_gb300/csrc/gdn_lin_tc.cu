@@ -18,7 +18,8 @@
 // Rounding.  The state is a sum that runs over the whole sequence and is
 // returned in fp32, so X must be exact to fp32: b and c are bf16 already, and
 // V^ is split into three bf16 terms (8 + 8 + 8 bits of the 24 of w_j c_j), or
-// two where the third could not reach the returned state.  P' and the S that O1
+// two where what they leave out has decayed below 2^-24 by the returned state, or
+// where none is returned (the S that O1 reads has 8 bits).  P' and the S that O1
 // reads are rounded to bf16 once: each enters an output that is itself rounded
 // to bf16, so an output carries two such roundings in all.
 //
@@ -395,14 +396,15 @@ gdn_lin_tc_kernel(const __grid_constant__ TcArgs args) {
     return *reinterpret_cast<uint4 *>(smem + (addr - sb));
   };
 
-  // Steps from c3 on weigh with three terms, earlier ones with two: the third,
-  // 2^-17 of its row, reaches the returned state times lam^rest, rest the tokens
-  // that follow the tile; below lam^rest = 2^-5 that is less than fp32 holds.
+  // Steps from c3 on weigh with three terms, earlier ones with two.  Two leave out up to
+  // 2^-16 of what a token writes; it reaches the returned state times lam^rest, rest the
+  // tokens that follow the tile.  Below lam^rest = 2^-8 that is 2^-24 of what was written,
+  // as much as one fp32 rounding of the state at that time.
   int c3 = nc;
   if (scan.s_out && (STATES || last)) {
     const int64_t after =
         rev ? span.seg * p.seg_len : span.total - span.seg * p.seg_len - len;
-    const float reach = ld < 0.f ? 3.4657f / -ld : 1e9f;   // lam^reach = 2^-5
+    const float reach = ld < 0.f ? 5.5452f / -ld : 1e9f;   // lam^reach = 2^-8
     if (reach >= (float)after) c3 = nc - 2 - (int)(fminf(reach - (float)after, 1e9f) / kC);
   }
   // Where the o tile of step c waits for its store: a buffer of its own, or with DK
