@@ -693,23 +693,38 @@ def _call(name):
     return f
 
 
-def _dense(*tensors):
-    """Every tensor given (None: not given) is a contiguous CUDA tensor."""
+def _current_device():
+    return torch._C._cuda_getDevice()
+
+
+def _run(name, device, *args):
+    """The library's function of this name, with the tensors' device current: kernels
+    are launched on the current device, whatever the stream's."""
+    if device < 0 or _current_device() == device:
+        return _call(name)(*args)
+    with torch.cuda.device(device):
+        return _call(name)(*args)
+
+
+def _dense(device, *tensors):
+    """Every tensor given (None: not given) is a contiguous CUDA tensor on this device."""
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
+        if t is not None and not (t.is_cuda and t.get_device() == device and t.is_contiguous()):
             return False
     return True
 
 
-def _explain(where, tensors, specs, lists=()):
+def _explain(where, device, tensors, specs, lists=()):
     """Raise for the first thing wrong: ``tensors`` name -> tensor (or None) that
-    must be contiguous on a CUDA device; ``specs`` name -> (tensor, shape, dtype);
+    must be contiguous on CUDA device ``device``; ``specs`` name -> (tensor, shape, dtype);
     ``lists``: names whose tensors must be lists of one length."""
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"{where}: {name} must be on a CUDA device")
+        if t.get_device() != device:
+            raise ValueError(f"{where}: {name} must be on the device of the other tensors")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} must be contiguous")
     for name, (t, shape, dtype) in specs.items():
@@ -724,8 +739,12 @@ def _fits(t, shape, dtype):
 
 
 def _raw_stream(stream, device):
-    """The CUDA stream handle: of ``stream``, or the current one."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    """The CUDA stream handle: of ``stream``, or the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"gdn: a stream of device {stream.device_index} for tensors on {device}")
+    return stream.cuda_stream
 
 
 def _p(t):
@@ -754,6 +773,8 @@ def _like_new(stream, t):
 def _workspace(stream, like, given, size, status):
     """``given``, or a new one; its status word is zeroed if it will be read."""
     if given is not None:
+        if not _dense(like.get_device(), given):
+            raise ValueError("gdn: the workspace must be contiguous, on the device of the tensors")
         return given
     ws = _empty(stream, like, (size,), _U8)
     if status:
@@ -773,7 +794,8 @@ def _done(where, st, check, workspace, stream):
     if st:
         raise GdnError(st, where)
     if check:
-        st = gdn_check(workspace, stream)
+        with torch.cuda.device(workspace.get_device()):
+            st = gdn_check(workspace, stream)
         if st:
             raise GdnError(st, f"{where} (device)")
 
@@ -803,9 +825,11 @@ def _lin_check(where, q, k, v, log_decay, cu_seqlens, dense, specs):
     N = B if cu_seqlens is None else cu_seqlens.numel() - 1
     dt = q.dtype
     state = (N, H, dk, dv)
-    ok = q.is_cuda and k.is_cuda and v.is_cuda and dt in _CODES and k.dtype == dt and \
+    dev = q.get_device()
+    ok = q.is_cuda and k.is_cuda and v.is_cuda and k.get_device() == dev == v.get_device() and \
+        dt in _CODES and k.dtype == dt and \
         v.dtype == dt and k.shape == q.shape and v.shape[:3] == q.shape[:3] and \
-        _dense(log_decay, cu_seqlens, *dense) and log_decay.dtype == _F32 and \
+        _dense(dev, log_decay, cu_seqlens, *dense) and log_decay.dtype == _F32 and \
         log_decay.shape == (H,) and (cu_seqlens is None or (cu_seqlens.dtype == _I32 and
                                                             cu_seqlens.dim() == 1))
     if ok:
@@ -823,11 +847,13 @@ def _lin_check(where, q, k, v, log_decay, cu_seqlens, dense, specs):
         for name, t in (("q", q), ("k", k), ("v", v)):
             if not t.is_cuda:
                 raise ValueError(f"{where}: {name} must be on a CUDA device")
+            if t.get_device() != dev:
+                raise ValueError(f"{where}: {name} must be on the device of q")
         full = {n: (t, state if kind == 0 else q.shape if kind == 1 else v.shape,
                     _F32 if kind == 0 else dt) for n, (t, kind) in specs.items()}
         full["log_decay"] = (log_decay, (H,), _F32)
         full["cu_seqlens"] = (cu_seqlens, (N + 1,), _I32)
-        _explain(where, {n: e[0] for n, e in full.items()}, full)
+        _explain(where, dev, {n: e[0] for n, e in full.items()}, full)
     return B, T, H, dk, dv, N
 
 
@@ -861,10 +887,11 @@ def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=No
         final_state = _empty(stream, v, (N, H, dk, dv), _F32)
     flags = GDN_FORCE_SIMT if force_simt else 0
     ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
-    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                  _p(initial_state), _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk,
-                  dv, N, _stride(w, "q", q), _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype],
-                  flags, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, q.get_device()))
+    dev = q.get_device()
+    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+              _p(initial_state), _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk, dv, N,
+              _stride(w, "q", q), _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags,
+              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return o, final_state
@@ -890,12 +917,13 @@ def gdn_lin_bwd(q, k, v, log_decay, d_o, initial_state=None, cu_seqlens=None, d_
                  "dh0": _empty(stream, q, (N, H, dk, dv), _F32)}
     flags = GDN_FORCE_SIMT if force_simt else 0
     ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
-    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                  _p(initial_state), _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state),
-                  grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
-                  _p(grads.get("dh0")), B, T, H, dk, dv, N, _stride(w, "q", q),
-                  _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags,
-                  ws.data_ptr(), _nbytes(ws), _raw_stream(stream, q.get_device()))
+    dev = q.get_device()
+    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+              _p(initial_state), _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state),
+              grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
+              _p(grads.get("dh0")), B, T, H, dk, dv, N, _stride(w, "q", q), _stride(w, "k", k),
+              _stride(w, "v", v), _CODES[q.dtype], flags, ws.data_ptr(), _nbytes(ws),
+              _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return grads
@@ -924,15 +952,16 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
     P = state_out.shape[0]
     stride = state_out.stride(0) if P > 1 else 0
     page = (H, dk, dv)
-    ok = _dense(q, k, v, log_decay, pages, o) and dt in _CODES and k.dtype == dt and \
+    dev = q.get_device()
+    ok = _dense(dev, q, k, v, log_decay, pages, o) and dt in _CODES and k.dtype == dt and \
         v.dtype == dt and k.shape == q.shape and v.shape == (N, H, dv) and \
         log_decay.dtype == _F32 and log_decay.shape == (H,) and \
         _fits(pages, (N,), _I32) and _fits(o, v.shape, dt)
     if ok:
         for t in (state_out,) if state is state_out or state is None else (state_out, state):
             # a page is contiguous: [H, dk, dv] packed at every stride(0)
-            if not (t.is_cuda and t.dtype == _F32 and t.shape == (P, *page) and
-                    (P <= 1 or t.stride(0) == stride) and
+            if not (t.is_cuda and t.get_device() == dev and t.dtype == _F32 and
+                    t.shape == (P, *page) and (P <= 1 or t.stride(0) == stride) and
                     (t.is_contiguous() or (P > 0 and t[0].is_contiguous()))):
                 ok = False
     if not ok:
@@ -949,16 +978,17 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
             if t is not None and t.is_cuda and t.dim() == 4 and P > 0 and \
                     (not t[0].is_contiguous() or (P > 1 and t.stride(0) != stride)):
                 raise ValueError(f"{w}: {name} must have contiguous pages at one stride")
-        _explain(w, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o,
-                         state=None if state is None else state[0], state_out=state_out[0]), specs)
+        one = lambda t: t if t is None or t.shape[0] == 0 else t[0]  # noqa: E731
+        _explain(w, dev, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o,
+                              state=one(state), state_out=one(state_out)), specs)
     if o is None:
         o = _like_new(stream, v)
-    if check:
-        workspace = _workspace(stream, v, workspace, 256, True)
-    st = _call(w)(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
-                  state_out.data_ptr(), _p(pages), o.data_ptr(), N, H, dk, dv, P, stride,
-                  _CODES[dt], 0, _p(workspace), 0 if workspace is None else _nbytes(workspace),
-                  _raw_stream(stream, q.get_device()))
+    if check or workspace is not None:
+        workspace = _workspace(stream, v, workspace, 256, check)
+    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
+              state_out.data_ptr(), _p(pages), o.data_ptr(), N, H, dk, dv, P, stride, _CODES[dt], 0,
+              _p(workspace), 0 if workspace is None else _nbytes(workspace),
+              _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, workspace, stream)
     return o, state_out
@@ -974,12 +1004,12 @@ def _norm_check(where, x, weight, bias, gate, groups, specs):
     if x.dim() != 3:
         raise ValueError(f"{where}: x must be [N, S, C]")
     N, S, C = x.shape
-    dt, stat, chan = x.dtype, (N, groups), (C,)
-    ok = dt in _CODES and _dense(x, weight, bias, gate) and _fits(weight, chan, _F32) and \
+    dt, stat, chan, dev = x.dtype, (N, groups), (C,), x.get_device()
+    ok = dt in _CODES and _dense(dev, x, weight, bias, gate) and _fits(weight, chan, _F32) and \
         _fits(bias, chan, _F32) and _fits(gate, x.shape, dt)
     if ok:
         for t, kind in specs.values():
-            if t is not None and not (t.is_cuda and t.is_contiguous() and
+            if t is not None and not (_dense(dev, t) and
                                       (_fits(t, x.shape, dt) if kind == 0 else
                                        _fits(t, stat if kind == 1 else chan, _F32))):
                 ok = False
@@ -989,7 +1019,7 @@ def _norm_check(where, x, weight, bias, gate, groups, specs):
         full = {n: (t, x.shape if kind == 0 else stat if kind == 1 else chan,
                     dt if kind == 0 else _F32) for n, (t, kind) in specs.items()}
         full.update(weight=(weight, chan, _F32), bias=(bias, chan, _F32), gate=(gate, x.shape, dt))
-        _explain(where, {"x": x, **{n: e[0] for n, e in full.items()}}, full)
+        _explain(where, dev, {"x": x, **{n: e[0] for n, e in full.items()}}, full)
     return N, S, C
 
 
@@ -1010,10 +1040,10 @@ def gdn_group_norm(x, weight, bias, groups, *, gate=None, silu=False, eps=1e-5, 
     mean = _empty(stream, x, (N, groups), _F32) if mean is None else mean
     rstd = _empty(stream, x, (N, groups), _F32) if rstd is None else rstd
     ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
-    st = _call(w)(x.data_ptr(), _p(weight), _p(bias), _p(gate), y.data_ptr(), mean.data_ptr(),
-                  rstd.data_ptr(), N, S, C, groups, eps, _CODES[x.dtype],
-                  GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws),
-                  _raw_stream(stream, x.get_device()))
+    dev = x.get_device()
+    st = _run(w, dev, x.data_ptr(), _p(weight), _p(bias), _p(gate), y.data_ptr(), mean.data_ptr(),
+              rstd.data_ptr(), N, S, C, groups, eps, _CODES[x.dtype], GDN_NORM_SILU if silu else 0,
+              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st:
         raise GdnError(st, w)
     return y, mean, rstd
@@ -1036,11 +1066,11 @@ def gdn_group_norm_bwd(x, weight, bias, groups, mean, rstd, d_y, *, gate=None, s
                  "dgate": None if gate is None else _like_new(stream, gate),
                  "dweight": _empty(stream, x, (C,), _F32), "dbias": _empty(stream, x, (C,), _F32)}
     ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
-    st = _call(w)(x.data_ptr(), _p(weight), _p(bias), _p(gate), mean.data_ptr(), rstd.data_ptr(),
-                  d_y.data_ptr(), grads["dx"].data_ptr(), _p(grads.get("dgate")),
-                  _p(grads.get("dweight")), _p(grads.get("dbias")), N, S, C, groups,
-                  _CODES[x.dtype], GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws),
-                  _raw_stream(stream, x.get_device()))
+    dev = x.get_device()
+    st = _run(w, dev, x.data_ptr(), _p(weight), _p(bias), _p(gate), mean.data_ptr(),
+              rstd.data_ptr(), d_y.data_ptr(), grads["dx"].data_ptr(), _p(grads.get("dgate")),
+              _p(grads.get("dweight")), _p(grads.get("dbias")), N, S, C, groups, _CODES[x.dtype],
+              GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st:
         raise GdnError(st, w)
     return grads
@@ -1057,7 +1087,8 @@ def _pages_fine(pool, table, counts, refs, rows, own, table_out, counts_out, ref
     call's own one) but inputs updated in place."""
     return own is None and (table_out is None or table_out is table) and \
         (counts_out is None or counts_out is counts) and \
-        (refs_out is None or refs_out is refs) and _dense(pool, table, counts, refs, rows) and \
+        (refs_out is None or refs_out is refs) and \
+        _dense(table.get_device(), pool, table, counts, refs, rows) and \
         table.dtype == _I32 and counts.dtype == _I32 and refs.dtype == _I32 and \
         table.dim() == 2 and refs.dim() == 1 and counts.shape == table.shape[:1] and \
         (pool is None or pool.shape[0] == refs.shape[0]) and \
@@ -1070,7 +1101,8 @@ def _pages_check(where, pool, table, counts, refs, lists, outs):
     R, M = (0, 1) if table is None else table.shape
     P = pool.shape[0] if table is None else refs.shape[0]
     n = None
-    ok = _dense(pool, table, counts, refs, *lists.values(), *outs.values()) and \
+    dev = (pool if table is None else table).get_device()
+    ok = _dense(dev, pool, table, counts, refs, *lists.values(), *outs.values()) and \
         (pool is None or pool.shape[0] == P)
     if ok and table is not None:
         ok = table.dtype == _I32 and _fits(counts, (R,), _I32) and _fits(refs, (P,), _I32)
@@ -1088,7 +1120,7 @@ def _pages_check(where, pool, table, counts, refs, lists, outs):
         if table is not None:
             specs.update(table=(table, (R, M), _I32), counts=(counts, (R,), _I32),
                          refs=(refs, (P,), _I32))
-        _explain(where, dict(pool=pool, **{n_: e[0] for n_, e in specs.items()}), specs, lists)
+        _explain(where, dev, dict(pool=pool, **{n_: e[0] for n_, e in specs.items()}), specs, lists)
     bytes_ = 16 if pool is None or P == 0 else _nbytes(pool) // P
     return bytes_, P, R, M
 
@@ -1100,8 +1132,9 @@ def gdn_pages_copy(pool, src, dst, *, workspace=None, stream=None, check=False):
     bytes_, P, _, _ = _pages_check(w, pool, None, None, None, dict(src=src, dst=dst), {})
     n = src.numel()
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, 0, n), check)
-    st = _call(w)(pool.data_ptr(), bytes_, P, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(),
-                  _nbytes(ws), _raw_stream(stream, pool.get_device()))
+    dev = pool.get_device()
+    st = _run(w, dev, pool.data_ptr(), bytes_, P, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(),
+              _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return pool
@@ -1123,7 +1156,8 @@ def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, 
     raises if a job was left out (a bad row or too few free pages)."""
     w = "gdn_pages_fork"
     if _pages_fine(pool, table, counts, refs, parents, fresh, table_out, counts_out, refs_out) and \
-            _dense(children) and children.dtype == _I32 and children.shape == parents.shape:
+            _dense(table.get_device(), children) and children.dtype == _I32 and \
+            children.shape == parents.shape:
         (R, M), P = table.shape, refs.shape[0]
         bytes_ = _nbytes(pool) // P if P else 16
     else:
@@ -1137,11 +1171,11 @@ def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, 
     counts_out = _like_new(stream, counts) if counts_out is None else counts_out
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, n), check)
-    st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
-                  refs.data_ptr(), R, M, parents.data_ptr(), children.data_ptr(), n,
-                  fresh.data_ptr(), table_out.data_ptr(), counts_out.data_ptr(),
-                  refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                  _raw_stream(stream, pool.get_device()))
+    dev = pool.get_device()
+    st = _run(w, dev, pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
+              refs.data_ptr(), R, M, parents.data_ptr(), children.data_ptr(), n, fresh.data_ptr(),
+              table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(),
+              _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return fresh, table_out, counts_out, refs_out
@@ -1164,9 +1198,10 @@ def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None
     counts_out = _like_new(stream, counts) if counts_out is None else counts_out
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, table, workspace, gdn_pages_workspace_size(P, R, n), check)
-    st = _call(w)(table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M, rows.data_ptr(),
-                  n, table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(),
-                  ws.data_ptr(), _nbytes(ws), _raw_stream(stream, table.get_device()))
+    dev = table.get_device()
+    st = _run(w, dev, table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M,
+              rows.data_ptr(), n, table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(),
+              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return table_out, counts_out, refs_out
@@ -1189,10 +1224,10 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     table_out = _like_new(stream, table) if table_out is None else table_out
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, 0), check)
-    st = _call(w)(pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
-                  refs.data_ptr(), R, M, num_live.data_ptr(), table_out.data_ptr(),
-                  refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
-                  _raw_stream(stream, pool.get_device()))
+    dev = pool.get_device()
+    st = _run(w, dev, pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
+              refs.data_ptr(), R, M, num_live.data_ptr(), table_out.data_ptr(),
+              refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return num_live, table_out, refs_out
