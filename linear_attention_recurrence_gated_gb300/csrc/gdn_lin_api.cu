@@ -67,25 +67,23 @@ size_t gdn_lin_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_hea
   using namespace gdn::lin;
   if (num_seqs <= 0 || seq_len < 0 || num_heads <= 0 || head_dim_k <= 0 || head_dim_v <= 0)
     return 0;
-  (void)flags;
+  (void)flags;   // enough for either form
   // the largest of every launch that a forward or backward call of these sizes
   // may make (packed or not, each storage type)
   size_t most = 0;
-  const int dims[] = {head_dim_k, head_dim_v};
+  const auto room = [&](const Plan &plan, int scans) {
+    const size_t n = split_bytes(plan, scans, num_heads, head_dim_k, head_dim_v);
+    most = n > most ? n : most;
+  };
   for (int scans = 1; scans <= 3; ++scans)
-    for (int d : dims)
+    for (int d : {head_dim_k, head_dim_v})
       for (int tile : {32, 64})
         for (bool packed : {false, true}) {
           const int64_t units = (int64_t)(d / tile) * scans * num_heads;
           if (units == 0) continue;
-          const Plan plan =
-              tile == 64 ? plan_segments(num_seqs, seq_len, packed, units, kSMs, 128, 3.0, 0.6)
-                         : plan_segments(num_seqs, seq_len, packed, units, kSimtWidth, 64, 0.4, 0.4);
-          const Plan wide = plan_segments(num_seqs, seq_len, packed, units, kSimtWidth, 64, 0.4, 0.4);
-          const size_t w = split_bytes(wide, scans, num_heads, head_dim_k, head_dim_v);
-          most = w > most ? w : most;
-          const size_t n = split_bytes(plan, scans, num_heads, head_dim_k, head_dim_v);
-          most = n > most ? n : most;
+          room(plan_segments(num_seqs, seq_len, packed, units, kSimtWidth, 64, 0.4, 0.4), scans);
+          if (tile == 64)
+            room(plan_segments(num_seqs, seq_len, packed, units, kSMs, 128, 3.0, 0.6), scans);
         }
   return gdn::kStatusBytes + most;
 }

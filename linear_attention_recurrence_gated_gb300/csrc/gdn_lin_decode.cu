@@ -114,7 +114,7 @@ cudaError_t launch_c(const DecodeParams &p, int num_seqs, cudaStream_t stream) {
   }
   return cudaGetLastError();
 }
-// 64 columns a CTA where that still gives every SM two rounds of eight CTAs.
+// 64 columns a CTA wherever dv holds whole ones (measured at the top).
 template <typename T>
 cudaError_t launch_t(const DecodeParams &p, int num_seqs, cudaStream_t stream) {
   return p.dv % 64 == 0 ? launch_c<T, 64>(p, num_seqs, stream)

@@ -150,12 +150,10 @@ __device__ __forceinline__ Stat join(const Stat &a, const Stat &b) {
 }
 
 // y of one value.
-template <typename T, int M>
+template <typename T>
 __device__ __forceinline__ float activate(float u, float z, const Params &p) {
-  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
-  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
-  if (silu) u *= sigmoid<T>(u);
-  return gated ? u * z * sigmoid<T>(z) : u;
+  if (p.silu) u *= sigmoid<T>(u);
+  return p.gate ? u * z * sigmoid<T>(z) : u;
 }
 
 // ---- pairs of values: two lanes of packed fp32 arithmetic ----------------------
@@ -303,10 +301,10 @@ __device__ __forceinline__ void weights(const float *w, int c, bool in, float ot
 // normalisation in a second (which finds a small sample in L1 or L2).  Threads
 // are tiled over (row, vector of V channels).  Shared memory: a (count, mean,
 // m2) triple per channel vector, then mean and rstd per group.
-template <typename T, int V, int M>
+template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_fwd_kernel(const Params p) {
-  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
+  const bool gated = p.gate != nullptr;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -373,7 +371,7 @@ gdn_norm_fwd_kernel(const Params p) {
         if (gated) load<V>(zs + at, z);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          v[i] = activate<T, M>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), gated ? z[i] : 0.f, p);
+          v[i] = activate<T>(fmaf(((v[i] - x0) - mean) * rstd, w[i], b[i]), gated ? z[i] : 0.f, p);
         store<V>(static_cast<T *>(p.y) + at, v);
       }
     }
@@ -381,17 +379,15 @@ gdn_norm_fwd_kernel(const Params p) {
 }
 
 // du of one value, and dz where there is a gate.
-template <typename T, int M>
+template <typename T>
 __device__ __forceinline__ float grad_u(float u, float z, float dy, const Params &p, float &dz) {
-  const bool silu = M == kAny ? p.silu : (M & 1) != 0;
-  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
   float act = u, dact = 1.f;
-  if (silu) {
+  if (p.silu) {
     const float s = sigmoid<T>(u);
     act = u * s;
     dact = s * (1.f + u * (1.f - s));
   }
-  if (gated) {
+  if (p.gate) {
     const float s = sigmoid<T>(z);
     dz = dy * act * s * (1.f + z * (1.f - s));
     dy *= z * s;
@@ -403,10 +399,10 @@ __device__ __forceinline__ float grad_u(float u, float z, float dy, const Params
 // of du xh and du) in one pass, dx in a second.  Shared memory: two sums per
 // channel vector and row of threads, two means per group, then the channels'
 // running sums over the CTA's samples.
-template <typename T, int V, int M>
+template <typename T, int V>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_bwd_kernel(const Params p) {
-  const bool gated = M == kAny ? p.gate != nullptr : (M & 2) != 0;
+  const bool gated = p.gate != nullptr;
   extern __shared__ __align__(16) float sm[];
   const int tid = threadIdx.x, CV = p.C / V, DV = p.D / V;
   const int TX = CV < kThreads ? CV : kThreads, TY = kThreads / TX;
@@ -465,7 +461,7 @@ gdn_norm_bwd_kernel(const Params p) {
           for (int i = 0; i < V; ++i) {
             const float xh = (v[i] - mean) * rstd;
             float dz;
-            const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
+            const float du = grad_u<T>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
             a1[i] += du;
             a2[i] = fmaf(du, xh, a2[i]);
           }
@@ -520,7 +516,7 @@ gdn_norm_bwd_kernel(const Params p) {
         for (int i = 0; i < V; ++i) {
           const float xh = (v[i] - mean) * rstd;
           float dz = 0.f;
-          const float du = grad_u<T, M>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
+          const float du = grad_u<T>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
           v[i] = rstd * (du * w[i] - m.x - xh * m.y);
           z[i] = dz;
         }
@@ -1266,8 +1262,8 @@ cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
     if (use_slabs(p.N, p.S, p.C, backward)) return run_slabs<T, V, kAny>(p, backward, stream);
   const int grid = (int)(p.N < kParts ? p.N : kParts);
   if (!backward)
-    return go<gdn_norm_fwd_kernel<T, V, kAny>>(grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
-  const cudaError_t err = go<gdn_norm_bwd_kernel<T, V, kAny>>(grid,
+    return go<gdn_norm_fwd_kernel<T, V>>(grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
+  const cudaError_t err = go<gdn_norm_bwd_kernel<T, V>>(grid,
                              ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8, p, stream);
   return err == cudaSuccess ? sum_parts(p, grid, stream) : err;
 }
