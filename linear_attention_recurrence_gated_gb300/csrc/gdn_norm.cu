@@ -398,8 +398,8 @@ __device__ __forceinline__ float grad_u(float u, float z, float dy, const Params
 // One CTA per sample: the group sums of dxh and dxh xh (and the channels' sums
 // of du xh and du) in one pass, dx in a second.  Shared memory: two sums per
 // channel vector and row of threads, two means per group, then the channels'
-// running sums over the CTA's samples.
-template <typename T, int V>
+// running sums over the CTA's samples.  LONG: a thread has more than kSum rows of a sample.
+template <typename T, int V, bool LONG>
 __global__ void __launch_bounds__(kThreads)
 gdn_norm_bwd_kernel(const Params p) {
   const bool gated = p.gate != nullptr;
@@ -438,35 +438,17 @@ gdn_norm_bwd_kernel(const Params p) {
     ++samples;
     const int64_t base = n * p.S * p.C;
     __syncthreads();
-#pragma unroll 1
-    for (int64_t from = 0; from < p.S; from += kSum * TY) {
-      const int64_t to = from + kSum * TY < p.S ? from + kSum * TY : p.S;
-      for (int cv = tx; cv < CV && ty < TY; cv += TX) {
-        const int g = cv / DV;
-        const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
-        float w[V], b[V], a1[V], a2[V];
+    for (int cv = tx; cv < CV && ty < TY; cv += TX) {
+      const int g = cv / DV;
+      const float mean = p.mean[n * p.G + g], rstd = p.rstd[n * p.G + g];
+      float w[V], b[V], a1[V], a2[V], t1 = 0.f, t2 = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          w[i] = p.w ? p.w[cv * V + i] : 1.f;
-          b[i] = p.b ? p.b[cv * V + i] : 0.f;
-          a1[i] = a2[i] = 0.f;
-        }
-        for (int64_t r = from + ty; r < to; r += TY) {
-          const int64_t at = base + r * p.C + cv * V;
-          float v[V], z[V], dy[V];
-          load<V>(xs + at, v);
-          load<V>(dys + at, dy);
-          if (gated) load<V>(zs + at, z);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float xh = (v[i] - mean) * rstd;
-            float dz;
-            const float du = grad_u<T>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
-            a1[i] += du;
-            a2[i] = fmaf(du, xh, a2[i]);
-          }
-        }
-        float t1 = 0.f, t2 = 0.f;
+      for (int i = 0; i < V; ++i) {
+        w[i] = p.w ? p.w[cv * V + i] : 1.f;
+        b[i] = p.b ? p.b[cv * V + i] : 0.f;
+        a1[i] = a2[i] = 0.f;
+      }
+      const auto close_rows = [&]() {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           t1 = fmaf(a1[i], w[i], t1);
@@ -474,11 +456,31 @@ gdn_norm_bwd_kernel(const Params p) {
           float2 &acc = sc[ty * p.C + cv * V + i];
           acc.x += a2[i];
           acc.y += a1[i];
+          a1[i] = a2[i] = 0.f;
         }
-        float2 &sum = st[ty * CV + cv];
-        if (from) t1 += sum.x, t2 += sum.y;
-        sum = make_float2(t1, t2);
+      };
+      int summed = 0;
+      for (int64_t r = ty; r < p.S; r += TY) {
+        if (LONG && summed++ == kSum) {
+          close_rows();
+          summed = 1;
+        }
+        const int64_t at = base + r * p.C + cv * V;
+        float v[V], z[V], dy[V];
+        load<V>(xs + at, v);
+        load<V>(dys + at, dy);
+        if (gated) load<V>(zs + at, z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float xh = (v[i] - mean) * rstd;
+          float dz;
+          const float du = grad_u<T>(fmaf(xh, w[i], b[i]), gated ? z[i] : 0.f, dy[i], p, dz);
+          a1[i] += du;
+          a2[i] = fmaf(du, xh, a2[i]);
+        }
       }
+      close_rows();
+      st[ty * CV + cv] = make_float2(t1, t2);
     }
     __syncthreads();
     for (int g = tid >> 5; g < p.G; g += kThreads / 32) {
@@ -1263,8 +1265,10 @@ cudaError_t run(const Params &p, bool backward, cudaStream_t stream) {
   const int grid = (int)(p.N < kParts ? p.N : kParts);
   if (!backward)
     return go<gdn_norm_fwd_kernel<T, V>>(grid, ((size_t)3 * TY * CV + 2 * p.G) * 4, p, stream);
-  const cudaError_t err = go<gdn_norm_bwd_kernel<T, V>>(grid,
-                             ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8, p, stream);
+  const size_t bytes = ((size_t)TY * CV + p.G + (size_t)TY * p.C) * 8;
+  const cudaError_t err = p.S > (int64_t)kSum * TY
+                              ? go<gdn_norm_bwd_kernel<T, V, true>>(grid, bytes, p, stream)
+                              : go<gdn_norm_bwd_kernel<T, V, false>>(grid, bytes, p, stream);
   return err == cudaSuccess ? sum_parts(p, grid, stream) : err;
 }
 

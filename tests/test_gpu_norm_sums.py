@@ -22,11 +22,12 @@ pytestmark = pytest.mark.gpu
 BOUND = 2.0 ** -16 + 2.0 ** -21
 
 
-# a group in a warp's registers; groups wider than that; samples of two rows; slabs with
-# 16-byte vectors and without; the sums of many slabs
+# a group in a warp's registers; groups wider than that; samples of two rows and, many of
+# them, of more than a thread sums at once; slabs with 16-byte vectors and without; the
+# sums of many slabs
 @pytest.mark.parametrize("N,S,C,groups", [
-    (1 << 19, 1, 4096, 32), (1 << 21, 1, 516, 1), (1 << 21, 2, 64, 4), (1, 1 << 22, 512, 8),
-    (1, 1 << 25, 20, 2), (65535, 16, 1024, 8)])
+    (1 << 19, 1, 4096, 32), (1 << 21, 1, 516, 1), (1 << 21, 2, 64, 4), (1 << 16, 11000, 3, 1),
+    (1, 1 << 22, 512, 8), (1, 1 << 25, 20, 2), (65535, 16, 1024, 8)])
 @pytest.mark.parametrize("z", [0.7, 1.3])
 def test_terms_that_are_the_same(N, S, C, groups, z):
     """x is the same in every row, so a channel's xh is too; with one d_y and one gate a
