@@ -693,23 +693,27 @@ def _call(name):
     return f
 
 
-def _current_device():
-    return torch._C._cuda_getDevice()
+_current_device = getattr(torch._C, "_cuda_getDevice", None)   # (a build without CUDA)
 
 
-def _run(name, device, *args):
-    """The library's function of this name, with the tensors' device current: kernels
-    are launched on the current device, whatever the stream's."""
-    if device < 0 or _current_device() == device:
-        return _call(name)(*args)
+def _elsewhere(name, device, *args):
     with torch.cuda.device(device):
         return _call(name)(*args)
+
+
+def _on(name, device):
+    """The library's function of this name, called with the tensors' device current:
+    kernels are launched on the current device, whatever the stream's."""
+    if device < 0 or _current_device() == device:
+        return _call(name)
+    return functools.partial(_elsewhere, name, device)
 
 
 def _dense(device, *tensors):
     """Every tensor given (None: not given) is a contiguous CUDA tensor on this device."""
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.get_device() == device and t.is_contiguous()):
+        if t is not None and not (t.get_device() == device and t.is_contiguous() and
+                                  (device >= 0 or t.is_cuda)):
             return False
     return True
 
@@ -826,8 +830,8 @@ def _lin_check(where, q, k, v, log_decay, cu_seqlens, dense, specs):
     dt = q.dtype
     state = (N, H, dk, dv)
     dev = q.get_device()
-    ok = q.is_cuda and k.is_cuda and v.is_cuda and k.get_device() == dev == v.get_device() and \
-        dt in _CODES and k.dtype == dt and \
+    ok = k.get_device() == dev == v.get_device() and \
+        (dev >= 0 or (q.is_cuda and k.is_cuda and v.is_cuda)) and dt in _CODES and k.dtype == dt and \
         v.dtype == dt and k.shape == q.shape and v.shape[:3] == q.shape[:3] and \
         _dense(dev, log_decay, cu_seqlens, *dense) and log_decay.dtype == _F32 and \
         log_decay.shape == (H,) and (cu_seqlens is None or (cu_seqlens.dtype == _I32 and
@@ -888,10 +892,11 @@ def gdn_lin_fwd(q, k, v, log_decay, initial_state=None, cu_seqlens=None, *, o=No
     flags = GDN_FORCE_SIMT if force_simt else 0
     ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
     dev = q.get_device()
-    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-              _p(initial_state), _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk, dv, N,
-              _stride(w, "q", q), _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags,
-              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(initial_state),
+        _p(cu_seqlens), o.data_ptr(), _p(final_state), B, T, H, dk, dv, N, _stride(w, "q", q),
+        _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags, ws.data_ptr(), _nbytes(ws),
+        _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return o, final_state
@@ -918,12 +923,12 @@ def gdn_lin_bwd(q, k, v, log_decay, d_o, initial_state=None, cu_seqlens=None, d_
     flags = GDN_FORCE_SIMT if force_simt else 0
     ws = _workspace(stream, v, workspace, gdn_lin_workspace_size(N, T, H, dk, dv, flags), check)
     dev = q.get_device()
-    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-              _p(initial_state), _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state),
-              grads["dq"].data_ptr(), grads["dk"].data_ptr(), grads["dv"].data_ptr(),
-              _p(grads.get("dh0")), B, T, H, dk, dv, N, _stride(w, "q", q), _stride(w, "k", k),
-              _stride(w, "v", v), _CODES[q.dtype], flags, ws.data_ptr(), _nbytes(ws),
-              _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(initial_state),
+        _p(cu_seqlens), d_o.data_ptr(), _p(d_final_state), grads["dq"].data_ptr(),
+        grads["dk"].data_ptr(), grads["dv"].data_ptr(), _p(grads.get("dh0")), B, T, H, dk, dv, N,
+        _stride(w, "q", q), _stride(w, "k", k), _stride(w, "v", v), _CODES[q.dtype], flags,
+        ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return grads
@@ -960,7 +965,7 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
     if ok:
         for t in (state_out,) if state is state_out or state is None else (state_out, state):
             # a page is contiguous: [H, dk, dv] packed at every stride(0)
-            if not (t.is_cuda and t.get_device() == dev and t.dtype == _F32 and
+            if not (t.get_device() == dev and (dev >= 0 or t.is_cuda) and t.dtype == _F32 and
                     t.shape == (P, *page) and (P <= 1 or t.stride(0) == stride) and
                     (t.is_contiguous() or (P > 0 and t[0].is_contiguous()))):
                 ok = False
@@ -985,10 +990,10 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
         o = _like_new(stream, v)
     if check or workspace is not None:
         workspace = _workspace(stream, v, workspace, 256, check)
-    st = _run(w, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
-              state_out.data_ptr(), _p(pages), o.data_ptr(), N, H, dk, dv, P, stride, _CODES[dt], 0,
-              _p(workspace), 0 if workspace is None else _nbytes(workspace),
-              _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _p(state),
+        state_out.data_ptr(), _p(pages), o.data_ptr(), N, H, dk, dv, P, stride, _CODES[dt], 0,
+        _p(workspace), 0 if workspace is None else _nbytes(workspace), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, workspace, stream)
     return o, state_out
@@ -1041,9 +1046,10 @@ def gdn_group_norm(x, weight, bias, groups, *, gate=None, silu=False, eps=1e-5, 
     rstd = _empty(stream, x, (N, groups), _F32) if rstd is None else rstd
     ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
     dev = x.get_device()
-    st = _run(w, dev, x.data_ptr(), _p(weight), _p(bias), _p(gate), y.data_ptr(), mean.data_ptr(),
-              rstd.data_ptr(), N, S, C, groups, eps, _CODES[x.dtype], GDN_NORM_SILU if silu else 0,
-              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        x.data_ptr(), _p(weight), _p(bias), _p(gate), y.data_ptr(), mean.data_ptr(),
+        rstd.data_ptr(), N, S, C, groups, eps, _CODES[x.dtype], GDN_NORM_SILU if silu else 0,
+        ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st:
         raise GdnError(st, w)
     return y, mean, rstd
@@ -1067,10 +1073,11 @@ def gdn_group_norm_bwd(x, weight, bias, groups, mean, rstd, d_y, *, gate=None, s
                  "dweight": _empty(stream, x, (C,), _F32), "dbias": _empty(stream, x, (C,), _F32)}
     ws = _workspace(stream, x, workspace, gdn_group_norm_workspace_size(N, S, C, groups), False)
     dev = x.get_device()
-    st = _run(w, dev, x.data_ptr(), _p(weight), _p(bias), _p(gate), mean.data_ptr(),
-              rstd.data_ptr(), d_y.data_ptr(), grads["dx"].data_ptr(), _p(grads.get("dgate")),
-              _p(grads.get("dweight")), _p(grads.get("dbias")), N, S, C, groups, _CODES[x.dtype],
-              GDN_NORM_SILU if silu else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        x.data_ptr(), _p(weight), _p(bias), _p(gate), mean.data_ptr(), rstd.data_ptr(),
+        d_y.data_ptr(), grads["dx"].data_ptr(), _p(grads.get("dgate")), _p(grads.get("dweight")),
+        _p(grads.get("dbias")), N, S, C, groups, _CODES[x.dtype], GDN_NORM_SILU if silu else 0,
+        ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st:
         raise GdnError(st, w)
     return grads
@@ -1133,8 +1140,9 @@ def gdn_pages_copy(pool, src, dst, *, workspace=None, stream=None, check=False):
     n = src.numel()
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, 0, n), check)
     dev = pool.get_device()
-    st = _run(w, dev, pool.data_ptr(), bytes_, P, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(),
-              _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        pool.data_ptr(), bytes_, P, src.data_ptr(), dst.data_ptr(), n, ws.data_ptr(), _nbytes(ws),
+        _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return pool
@@ -1172,10 +1180,11 @@ def gdn_pages_fork(pool, table, counts, refs, parents, children, *, fresh=None, 
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, n), check)
     dev = pool.get_device()
-    st = _run(w, dev, pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
-              refs.data_ptr(), R, M, parents.data_ptr(), children.data_ptr(), n, fresh.data_ptr(),
-              table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(),
-              _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(), refs.data_ptr(), R, M,
+        parents.data_ptr(), children.data_ptr(), n, fresh.data_ptr(), table_out.data_ptr(),
+        counts_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
+        _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return fresh, table_out, counts_out, refs_out
@@ -1199,9 +1208,10 @@ def gdn_pages_free(table, counts, refs, rows, *, table_out=None, counts_out=None
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, table, workspace, gdn_pages_workspace_size(P, R, n), check)
     dev = table.get_device()
-    st = _run(w, dev, table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M,
-              rows.data_ptr(), n, table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(),
-              ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        table.data_ptr(), counts.data_ptr(), refs.data_ptr(), P, R, M, rows.data_ptr(), n,
+        table_out.data_ptr(), counts_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(),
+        _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return table_out, counts_out, refs_out
@@ -1225,9 +1235,10 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     refs_out = _like_new(stream, refs) if refs_out is None else refs_out
     ws = _workspace(stream, pool, workspace, gdn_pages_workspace_size(P, R, 0), check)
     dev = pool.get_device()
-    st = _run(w, dev, pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(),
-              refs.data_ptr(), R, M, num_live.data_ptr(), table_out.data_ptr(),
-              refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    st = _on(w, dev)(
+        pool.data_ptr(), bytes_, P, table.data_ptr(), counts.data_ptr(), refs.data_ptr(), R, M,
+        num_live.data_ptr(), table_out.data_ptr(), refs_out.data_ptr(), ws.data_ptr(), _nbytes(ws),
+        _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
     return num_live, table_out, refs_out
