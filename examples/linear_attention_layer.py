@@ -87,7 +87,9 @@ class Layer:
         return y.view(*o.shape[:-2], -1) @ self.w_out
 
     def train_forward(self, x):
-        """The layer, then a norm with SiLU over all tokens' features of a sample."""
+        """The layer, then a norm with SiLU over all tokens' features of a sample (which
+        lets later tokens into earlier ones: for training on whole samples, not for
+        generation, and not part of ``serve``)."""
         q, k, v, gate = self.project(x)
         y = self.finish(Attention.apply(q, k, v, self.log_decay), gate)
         return GroupNorm.apply(x + y, *self.feature_norm, None, 8, True)

@@ -11,8 +11,8 @@
 // The four products are fp32 fused multiply-adds on 4 x 4 register tiles: two
 // 16-byte shared loads for every sixteen of them, so the fp32 pipes bound it (a
 // chunk of 64 x 64 x 64 takes 4 x 2^18 of them, eight times what its bytes cost).
-// [8, 2048, 16 heads, 64/64] takes 388 us, its backward pass 890, [4, 2048, 16, 128/128]
-// 739 and 1700: the fp32 pipes are busy 45 % of the time and an instruction is issued
+// [8, 2048, 16 heads, 64/64] takes 385 us, its backward pass 883, [4, 2048, 16, 128/128]
+// 725 and 1647: the fp32 pipes are busy 45 % of the time and an instruction is issued
 // in 66 % of the cycles (the rest waits for shared memory).  Small calls are latency:
 // [1, 256, 2, 32/32], four chunks cut apart, takes 12 us on the device (28 uncut).
 // P and its product skip what the mask leaves out, in blocks of 16 rows and columns.

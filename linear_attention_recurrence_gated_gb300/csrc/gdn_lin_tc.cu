@@ -28,16 +28,19 @@
 // three terms of V^ and S).  The three tiles of a stage are freed and loaded one by one:
 // B after P and X, A after P and O1, V after O2.
 //
-// Bound.  Head size 64: memory.  [8, 4096, 16 heads, 64/64], 270 MB, takes 48 us, 5.6
+// Bound.  Head size 64: memory.  [8, 4096, 16 heads, 64/64], 270 MB, takes 49 us, 5.5
 // TB/s with the start and the end of its one wave; in between a chunk takes as long as
-// its tiles at the copy bandwidth.  Head size 128: the chain O1, O2, read o, O1 of the
-// next chunk (each accumulator is there once: P twice, X, O1 and O2 fill the 512
-// columns), some 3100 cycles a chunk of which the tensor pipe is busy for half:
-//   packed, 140k tokens, 8 heads, 128/256    405 us (1.54 GB: 3.8 TB/s)
-//   [1, 65536, 16, 128/128], cut along time  311 us (1.08 GB; 781 us uncut)
-//   backward [4, 8192, 16, 128/128]          310 us (0.95 GB; 384 CTAs: 2.5 waves)
+// its tiles at the copy bandwidth.  Its backward pass takes 139 us (0.48 GB at least;
+// three scans ask for twelve tensors' bytes where seven would do, 384 CTAs are 2.5
+// waves).  Head size 128: the chain O1, O2, read o, O1 of the next chunk (each
+// accumulator is there once: with P in whole columns, twice, X, O1 and O2 fill the 512),
+// some 3100 cycles a chunk of which the tensor pipe is busy for half:
+//   packed, 140k tokens, 8 heads, 128/256    415 us (1.54 GB: 3.7 TB/s)
+//   [1, 65536, 16, 128/128], cut along time  316 us (1.08 GB; 781 us uncut)
+//   backward [4, 8192, 16, 128/128]          321 us (0.95 GB; 384 CTAs: 2.5 waves)
 // Tried and slower (packed 440 us before each): O1 twice in place of X's second half
-// (448 us: X then reads B twice), o by the V^ warps (503 us), shares of equal size handed
+// (448 us: X then reads B twice; not tried: P' packed into half of its P, which leaves
+// room for a second O1), o by the V^ warps (503 us), shares of equal size handed
 // on between resident CTAs (532 us: the heads of one token are no longer read together).
 //
 // Roles (16 warps): P' (warps 0-3), S and o (4-7), V^ (8-11), TMA (12), and the
@@ -54,7 +57,11 @@
 // mask by zero, and 0 * NaN makes NaN of a token's output that only a later token's
 // value could spoil.  The o warps look for it (one packed operation for four outputs) and
 // take such an output's sum again, over the tokens that it may see (`causal_sums`).  It
-// happens in the tile where a bad value first appears; from then on S has it too.
+// happens in the tile where a bad value first appears; from then on S has it too.  The
+// look costs 4 us of 139 ([8, 4096, 16, 64/64] backward) and 6 of 321 (by the V^ warps,
+// on the values themselves: 10 in place of 6); such a tile takes 0.35 ms once with
+// 64-wide heads and 0.6 with 128-wide ones, latencies of memory one after the other (with
+// more loads on their way the call needs registers of the loops: 321 -> 355 us).
 #include "gdn_lin.cuh"
 #include "gdn_launch.cuh"
 #include "gdn_tc_common.cuh"

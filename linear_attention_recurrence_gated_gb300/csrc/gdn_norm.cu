@@ -40,9 +40,13 @@ constexpr int kParts = 4 * kSMs;   // partial sums of dweight and dbias (slabs: 
 //   sample  otherwise: one CTA per sample, two passes over it.
 // All are bound by memory (forward: x, gate and y once; the slabs' backward pass reads x
 // and dy twice).  Measured, bf16: rows, gated, [32768, 1, 1024], 201 MB, 35.9 us (5.6
-// TB/s; a CTA for each place on the SMs: a second wave cost 1 us); slabs backward with
-// SiLU, [4, 4096, 1280], 126 MB, 41 us (two passes at 5.2 TB/s; without its arithmetic
-// 34 us: five warps a scheduler cover most of it).
+// TB/s; a CTA for each place on the SMs: a second wave cost 1 us), backward, 336 MB, 82
+// us (no row is sent for ahead of its turn); slabs backward with SiLU, [4, 4096, 1280],
+// 126 MB, 41.5 us (two passes at 5 TB/s; without its arithmetic 34 us: five warps a
+// scheduler cover most of it; at 64 registers a thread the widest bf16 instances spill,
+// 32 bytes here, 86 and 40 in the two passes with SiLU and a gate).  One CTA a sample is
+// left for many small samples and for groups beyond a warp's registers (gated, [16384, 1,
+// 2048] as one group: 171 us, backward 299, six times its bytes).
 struct Params {
   const void *x, *gate, *dy;
   const float *w, *b;
