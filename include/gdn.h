@@ -121,7 +121,13 @@ enum {
    * Other calls ignore the flag. */
   GDN_SEQ_SPLIT = 1u << 5,
   /* gdn_group_norm and gdn_group_norm_bwd: SiLU on the normalised value. */
-  GDN_NORM_SILU = 1u << 6
+  GDN_NORM_SILU = 1u << 6,
+  /* gdn_ssm_*: delta = softplus(dt + dt_bias) instead of dt + dt_bias. */
+  GDN_DT_SOFTPLUS = 1u << 7,
+  /* gdn_conv_fwd, gdn_conv_bwd, gdn_conv_step: SiLU on the sum. */
+  GDN_CONV_SILU = 1u << 8,
+  /* gdn_qk_norm, gdn_qk_norm_bwd: pairs are neighbours (2i, 2i + 1), not halves apart. */
+  GDN_ROPE_INTERLEAVED = 1u << 9
 };
 
 /* Bytes of device workspace gdn_fwd needs for these sizes (>= 256; the first
@@ -779,6 +785,234 @@ gdn_status gdn_pages_compact(void *pool, int64_t page_bytes, int32_t num_pages,
                              int32_t num_rows, int32_t max_pages, int32_t *num_live,
                              int32_t *table_out, int32_t *refs_out, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_ssm_fwd -- selective state space scan, the form for prompts.  Per sequence and
+ * channel d of group g(d) = d / (channels / groups), states s = 1..d_state:
+ *
+ *     delta_t = softplus(dt_t + dt_bias)     (dt_t + dt_bias without GDN_DT_SOFTPLUS)
+ *     h_t[s]  = exp(delta_t A[d, s]) h_{t-1}[s] + delta_t x_t b_t[g, s],   A = -exp(A_log)
+ *     y_t     = (sum_s c_t[g, s] h_t[s] + D_skip[d] x_t) silu(gate_t)
+ *
+ * the recurrence of gdn_diag_fwd with a step size for each channel instead of each head
+ * and a rate for each (channel, state).  Sums and states are fp32; y is rounded once, to
+ * the caller's dtype.
+ *
+ *   x, dt, gate    [batch, seq_len, channels]                dtype    device (gate or NULL: no factor)
+ *   b, c           [batch, seq_len, groups, d_state]         dtype    device
+ *   A_log          [channels, d_state]                       float32  device
+ *   D_skip, dt_bias [channels]                               float32  device, or NULL (= 0)
+ *   initial_state  [num_seqs, channels, d_state]             float32  device, or NULL (= zeros)
+ *   cu_seqlens     [num_seqs + 1] int32 device, or NULL      (sequences as in gdn_fwd)
+ *   y              [batch, seq_len, channels]                dtype    device (written)
+ *   final_state    as initial_state                          float32  device (written), or NULL
+ *
+ * x_stride .. gate_stride: elements from one token row to the next (the rows of a batch
+ * follow one another), so that the inputs may be slices of projections; 0 stands for
+ * densely packed rows.  A row is contiguous, and strides are multiples of 16 bytes.
+ *
+ * Supported sizes: d_state in {8, 16, 32, 64}; channels / groups a multiple of 8;
+ * channels <= 2^20; num_seqs <= 16384.  flags: GDN_DT_SOFTPLUS or 0.  Steps are expected
+ * >= 0 (a negative delta grows a state; it is not clamped).  Empty sequences and
+ * seq_len = 0 are legal (states pass through).  y and final_state overlap no input, but
+ * final_state may be initial_state.  A value that is not finite reaches its own token and
+ * later ones of its sequence, where the recurrence takes it, and nothing else.
+ *
+ * workspace: the first 256 bytes are the status word (zeroed once with
+ * gdn_workspace_init); the bytes after it, of any contents, hold the states of segments
+ * when sequences are cut along time to fill the GPU.  gdn_ssm_workspace_size(...) is
+ * enough for any call of these sizes; with less (at least 256 bytes) sequences run uncut,
+ * with the same results up to rounding.  Calls sharing a workspace are ordered (same
+ * stream).  Errors as gdn_fwd (bad cu_seqlens: gdn_check).
+ */
+size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
+                              int32_t d_state, int32_t groups);
+gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const void *b,
+                       const void *c, const float *D_skip, const void *gate, const float *dt_bias,
+                       const float *initial_state, const int32_t *cu_seqlens, void *y,
+                       float *final_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t d_state, int32_t groups, int32_t num_seqs, int64_t x_stride,
+                       int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t gate_stride,
+                       gdn_dtype dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * gdn_ssm_bwd -- backward pass of gdn_ssm_fwd, from its inputs (nothing is kept from the
+ * forward pass).  With G_t the gradient of h_t and ds = d_y silu(gate):
+ *
+ *     G_t = c_t ds_t + exp(delta_{t+1} A) G_{t+1},   db_t = sum_d delta x G,  dc_t = sum_d ds h,
+ *     dx = delta (b.G) + D_skip ds,   ddelta = x (b.G) + sum_s A exp(delta A) G h_{t-1},
+ *     ddt = ddelta softplus'(dt + dt_bias),   dA_log = A sum_t delta exp(delta A) G h_{t-1},
+ *     dgate = d_y (c.h + D_skip x) silu'(gate),   d_initial_state = exp(delta_1 A) G_1
+ *
+ *   d_y                 as y                                 dtype    device
+ *   d_final_state       as initial_state                     float32  device, or NULL (= zeros)
+ *   dx, ddt, dgate      as x, densely packed                 dtype    device (written; dgate with a
+ *                       gate, and only then)
+ *   db, dc              as b, densely packed (sums over the group's channels)  dtype  device (written)
+ *   dA_log              as A_log                             float32  device (written), or NULL
+ *   dD_skip, ddt_bias   [channels]                           float32  device (written), or NULL
+ *   d_initial_state     as initial_state                     float32  device (written), or NULL
+ *
+ * Sums over tokens, sequences and channels are fp32, in a fixed order: results are bitwise
+ * reproducible.  No output may overlap an input or another output.  Sizes, strides, flags
+ * and errors as gdn_ssm_fwd.  workspace: at least gdn_ssm_bwd_workspace_size(...) bytes,
+ * its first 256 the status word.
+ */
+size_t gdn_ssm_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
+                                  int32_t d_state, int32_t groups);
+gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const void *b,
+                       const void *c, const float *D_skip, const void *gate, const float *dt_bias,
+                       const float *initial_state, const int32_t *cu_seqlens, const void *d_y,
+                       const float *d_final_state, void *dx, void *ddt, float *dA_log, void *db,
+                       void *dc, float *dD_skip, void *dgate, float *ddt_bias,
+                       float *d_initial_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t d_state, int32_t groups, int32_t num_seqs, int64_t x_stride,
+                       int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t gate_stride,
+                       gdn_dtype dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * gdn_ssm_step -- one token of gdn_ssm_fwd's recurrence per sequence, on states held in
+ * the pages of a pool.
+ *
+ *   x, dt, gate, y  [num_seqs, channels]                    dtype    device (gate or NULL; y written)
+ *   b, c            [num_seqs, groups, d_state]             dtype    device
+ *   A_log, D_skip, dt_bias   as gdn_ssm_fwd
+ *   state_in        num_pages pages of [channels, d_state] float32 device, page_stride floats apart
+ *                   (0: densely packed; a multiple of 4), or NULL (= zeros)
+ *   state_out       laid out as state_in                    float32  device (written)
+ *   pages           [num_seqs] int32 device: the page of each sequence, or NULL (sequence n: page n)
+ *
+ * state_out may be state_in (the usual call: pages updated in place).  Padded rows (page
+ * -1), numbers out of range, the optional workspace and aliasing as gdn_lin_decode.
+ * Sequences of one call name different pages.  Sizes and flags as gdn_ssm_fwd.
+ */
+gdn_status gdn_ssm_step(const void *x, const void *dt, const float *A_log, const void *b,
+                        const void *c, const float *D_skip, const void *gate, const float *dt_bias,
+                        const float *state_in, float *state_out, const int32_t *pages, void *y,
+                        int32_t num_seqs, int32_t channels, int32_t d_state, int32_t groups,
+                        int32_t num_pages, int64_t page_stride, gdn_dtype dtype, uint32_t flags,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_conv_fwd -- short causal depthwise convolution with a bias, gdn_conv_silu for packed
+ * sequences and with a backward pass.  Per sequence, token t and channel ch:
+ *
+ *     z_t = bias[ch] + sum_{k < taps} w[ch, k] x_{t - (taps - 1) + k},   y = silu(z) with
+ *     GDN_CONV_SILU, else z
+ *
+ * with x before the sequence's start taken from x_prev (else zero).  fp32 arithmetic.
+ *
+ *   x              [batch, seq_len, channels]               dtype    device
+ *   w              [channels, taps]                         float32  device
+ *   bias           [channels]                               float32  device, or NULL (= 0)
+ *   x_prev         [num_seqs, taps - 1, channels]           dtype    device, or NULL (= zeros)
+ *   cu_seqlens     [num_seqs + 1] int32 device, or NULL     (sequences as in gdn_fwd)
+ *   y              [batch, seq_len, channels]               dtype    device (written)
+ *   x_tail         as x_prev                                dtype    device (written), or NULL: the
+ *                  last taps - 1 inputs (of x_prev followed by x)
+ *
+ * x_stride as in gdn_ssm_fwd.  1 <= taps <= 4; channels a multiple of 8, <= 2^20;
+ * num_seqs <= 16384.  Outputs overlap no input (x_tail is not x_prev).  workspace: the
+ * status word (256 bytes; zeroed once with gdn_workspace_init).  seq_len = 0 and empty
+ * sequences are legal.
+ */
+gdn_status gdn_conv_fwd(const void *x, const float *w, const float *bias, const void *x_prev,
+                        const int32_t *cu_seqlens, void *y, void *x_tail, int32_t batch,
+                        int32_t seq_len, int32_t channels, int32_t taps, int32_t num_seqs,
+                        int64_t x_stride, gdn_dtype dtype, uint32_t flags, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_conv_bwd -- backward pass of gdn_conv_fwd, from its inputs.  With dz = d_y silu'(z):
+ *
+ *     dx_t = sum_k w[ch, k] dz_{t + (taps - 1) - k},   dw[ch, k] = sum_t dz_t x_{t - (taps - 1) + k},
+ *     dbias = sum_t dz_t
+ *
+ *   d_y            as y                                     dtype    device
+ *   d_x_tail       as x_prev: the gradient of x_tail        dtype    device, or NULL (= zeros)
+ *   dx             as x, densely packed                     dtype    device (written)
+ *   dw, dbias      as w and bias                            float32  device (written), or NULL
+ *   dx_prev        as x_prev                                dtype    device (written), or NULL
+ *
+ * Sums over tokens are fp32, in a fixed order: bitwise reproducible.  No output may overlap
+ * an input or another output.  workspace: at least gdn_conv_workspace_size(...) bytes, its
+ * first 256 the status word.
+ */
+size_t gdn_conv_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels, int32_t taps);
+gdn_status gdn_conv_bwd(const void *x, const float *w, const float *bias, const void *x_prev,
+                        const int32_t *cu_seqlens, const void *d_y, const void *d_x_tail, void *dx,
+                        float *dw, float *dbias, void *dx_prev, int32_t batch, int32_t seq_len,
+                        int32_t channels, int32_t taps, int32_t num_seqs, int64_t x_stride,
+                        gdn_dtype dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/*
+ * gdn_conv_step -- one token of gdn_conv_fwd per sequence.  A page of `state` holds the
+ * sequence's last taps - 1 inputs ([taps - 1, channels], dtype, as x_tail; the oldest
+ * first), which move on by one in place; pages are page_stride elements apart (0: densely
+ * packed; a multiple of 16 bytes).
+ *
+ *   x, y     [num_seqs, channels]    dtype    device (y written)
+ *   pages    as gdn_ssm_step (padded rows: y = 0)
+ */
+gdn_status gdn_conv_step(const void *x, const float *w, const float *bias, void *state,
+                         const int32_t *pages, void *y, int32_t num_seqs, int32_t channels,
+                         int32_t taps, int32_t num_pages, int64_t page_stride, gdn_dtype dtype,
+                         uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_qk_norm -- norm of each head of q and k, then the rotation of its first rotary_dim
+ * elements by the token's position: the prologue of gdn_fwd, gdn_lin_fwd and gdn_lin_decode
+ * (single tokens: seq_len 1, with positions).  With x one head of a token, scale = q_scale
+ * for q and 1 for k:
+ *
+ *     u = scale x w / sqrt(mean(x^2) + eps)     (GDN_QK_L2NORM: sum(x^2) instead of the mean)
+ *     phi_i = position inv_freq[i],  i < rotary_dim / 2;   pairs (a, b) of u become
+ *     (a cos phi_i - b sin phi_i, a sin phi_i + b cos phi_i)
+ *
+ * with (a, b) = (u[i], u[i + rotary_dim / 2]), or (u[2i], u[2i + 1]) with
+ * GDN_ROPE_INTERLEAVED.  fp32 arithmetic; the angle's whole turns are taken off exactly.
+ *
+ *   q, q_out   [batch, seq_len, q_heads, head_dim]    dtype    device (q_out written)
+ *   k, k_out   [batch, seq_len, k_heads, head_dim]    dtype    device (k_out written)
+ *   q_weight, k_weight   [head_dim]                   float32  device, or NULL (= 1)
+ *   positions  [batch, seq_len] int32 device, or NULL (token t of a row: t)
+ *   inv_freq   [rotary_dim / 2]                       float32  device (not read if rotary_dim is 0)
+ *
+ * q_stride, k_stride as in gdn_lin_fwd.  head_dim a multiple of 8, <= 256; rotary_dim even,
+ * <= head_dim; q_heads, k_heads <= 4096.  Outputs overlap neither inputs nor one another.
+ * No workspace; no device-detected error.
+ */
+gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, const float *k_weight,
+                       const int32_t *positions, const float *inv_freq, void *q_out, void *k_out,
+                       int32_t batch, int32_t seq_len, int32_t q_heads, int32_t k_heads,
+                       int32_t head_dim, int32_t rotary_dim, int64_t q_stride, int64_t k_stride,
+                       float q_scale, float eps, gdn_dtype dtype, uint32_t flags, void *stream);
+
+/*
+ * gdn_qk_norm_bwd -- backward pass of gdn_qk_norm, from its inputs.  With du the gradient
+ * turned back and scaled, r the norm's factor and g = du w:
+ *
+ *     dx = r (g - x r^2 mean(x g))  (GDN_QK_L2NORM: sum),   dw = sum du x r  (tokens and heads)
+ *
+ *   d_q_out, d_k_out     as q_out, k_out              dtype    device
+ *   dq, dk               as q, k, densely packed      dtype    device (written)
+ *   dq_weight, dk_weight [head_dim]                   float32  device (written), or NULL
+ *
+ * Sums are fp32, in a fixed order: bitwise reproducible.  workspace: at least
+ * gdn_qk_norm_workspace_size(...) bytes, of any contents.
+ */
+size_t gdn_qk_norm_workspace_size(int32_t batch, int32_t seq_len, int32_t head_dim);
+gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
+                           const float *k_weight, const int32_t *positions, const float *inv_freq,
+                           const void *d_q_out, const void *d_k_out, void *dq, void *dk,
+                           float *dq_weight, float *dk_weight, int32_t batch, int32_t seq_len,
+                           int32_t q_heads, int32_t k_heads, int32_t head_dim, int32_t rotary_dim,
+                           int64_t q_stride, int64_t k_stride, float q_scale, float eps,
+                           gdn_dtype dtype, uint32_t flags, void *workspace,
+                           size_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, read the status word in `workspace`, clear it, and
  * return it (GDN_OK if no kernel recorded an error since the last check).

@@ -1,0 +1,795 @@
+// Selective state space scan, backward pass (gdn_ssm.cuh has the recurrence).  With
+// ds = dy silu(gate), G_t the gradient of h_t and g what a token passes to the one before,
+//
+//   G_t = g_{t+1} + c_t ds_t,  dc_t = sum_ch ds h_t,  db_t = sum_ch delta x G_t,
+//   q = sum_s b G_t,  dx = delta q + D_skip ds,  g_t = exp(delta A) G_t,
+//   w = g_t h_{t-1},  ddelta = x q + sum_s A w,  dA += delta w,
+//   ddt = ddelta sigmoid(dt + dt_bias),  dgate = dy s silu'(gate),  dA_log = A dA
+//
+// The states of a token are needed in the reverse order of their making.  One launch
+// runs the scan forward and keeps every kL-th state; the next takes the tiles of kL
+// tokens from the last to the first, makes a tile's states again from the kept one (they
+// stay in shared memory) and goes through them backward.  12 multiply-adds and two
+// exponentials an element there, 3 and one in the first (7 where sequences are cut along
+// time: it leaves each segment's gradient of its start from zero too, by running products
+// of the decays).  Sums over a CTA's channels (db, dc) and over tokens (dA_log, dD_skip,
+// ddt_bias) are left in the workspace and added up in a fixed order by the last launch:
+// results are bitwise reproducible.
+#include "gdn_ssm.cuh"
+
+namespace gdn {
+gdn_status pass_states(const float *from, float *to, size_t bytes, cudaStream_t s);
+
+namespace ssm {
+namespace {
+
+constexpr int kL = 8;   // tokens from one kept state to the next, and of a tile
+
+struct BwdParams : Params {
+  const void *dy;
+  const float *dhT;
+  void *dx, *ddt, *db, *dc, *dgate;
+  float *dA_log, *dD_skip, *ddt_bias, *dh0;
+  float *seg_y;      // [slot][D][S] gradient that a segment passes to the one before
+  float *ckpt;       // [tokens / kL][D][S] kept states (of later segments: from zero)
+  float *ckpt_d;     // [tokens / kL][D] sum of delta since the segment's start
+  float *part_bc;    // [block][token][G][2][S]
+  float *part_w;     // [gridDim.y][D S + 2 D] sums for dA, dD_skip, ddt_bias
+  int32_t G, parts;
+  __host__ __device__ int64_t rows() const {
+    return seq.cu ? seq.seq_len : seq.seq_len * seq.num_seqs;
+  }
+};
+
+// The place of the state before token t (a multiple of kL, > 0) of a sequence that begins
+// at token `start`: floor(start / kL) + t / kL - 1, never that of another sequence.
+__device__ __forceinline__ int64_t kept(int64_t start, int64_t t) { return start / kL + t / kL - 1; }
+
+// The inputs of tiles of TT tokens, eight channels (or states of b, c) a thread at a time.
+template <typename T, int S, int TT, bool GRAD>
+struct Inputs {
+  static constexpr int CB = Geo<S>::CB, VB = CB / 8, RT = kThreads / VB;
+  static constexpr int NV = (TT + RT - 1) / RT;
+  static constexpr int NBC = 2 * TT * S / 8, NB = (NBC + kThreads - 1) / kThreads;
+  Raw8<T> x[NV], dt[NV], dy[NV], gate[NV], bc[NB];
+  __device__ __forceinline__ void fetch(const BwdParams &p, int64_t first, int cnt, int group,
+                                        int vch, bool von) {
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int row = tid / VB + i * RT;
+      x[i].zero();
+      dt[i].zero();
+      if (GRAD) {
+        dy[i].zero();
+        gate[i].zero();
+      }
+      if (!von || row >= cnt) continue;
+      const int64_t at = first + row;
+      x[i].load(static_cast<const T *>(p.x) + at * p.sx + vch);
+      dt[i].load(static_cast<const T *>(p.dt) + at * p.sdt + vch);
+      if (GRAD) {
+        dy[i].load(static_cast<const T *>(p.dy) + at * p.D + vch);
+        if (p.gate) gate[i].load(static_cast<const T *>(p.gate) + at * p.sg + vch);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int idx = tid + i * kThreads, row = idx % (NBC / 2) / (S / 8), v = idx % (S / 8);
+      bc[i].zero();
+      if (idx >= NBC || row >= cnt) continue;
+      if (idx < NBC / 2)
+        bc[i].load(static_cast<const T *>(p.b) + (first + row) * p.sb + group * S + 8 * v);
+      else if (GRAD)
+        bc[i].load(static_cast<const T *>(p.c) + (first + row) * p.sc + group * S + 8 * v);
+    }
+  }
+  // delta, delta x and ds of the tile, b and c twice over, to shared memory
+  __device__ __forceinline__ void form(const BwdParams &p, int cnt, bool von, const float (&bias)[8],
+                                       float *sd, float *su, float *ss, float *sbc) const {
+    const int tid = threadIdx.x, vec = tid % VB;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int row = tid / VB + i * RT;
+      if (row >= TT) continue;
+      float xv[8], dv[8];
+      x[i].get(xv);
+      dt[i].get(dv);
+      const bool on = von && row < cnt;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = dv[j] + bias[j];
+        dv[j] = on ? (p.softplus ? softplus<T>(v) : v) : 0.f;
+        xv[j] *= dv[j];
+      }
+      put(sd + row * CB + 8 * vec, dv);
+      put(su + row * CB + 8 * vec, xv);
+      if (GRAD) {
+        float gv[8];
+        dy[i].get(dv);
+        if (p.gate) {
+          gate[i].get(gv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dv[j] *= gv[j] * sigmoid(gv[j]);
+        }
+        put(ss + row * CB + 8 * vec, dv);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int idx = tid + i * kThreads;
+      if (idx >= (GRAD ? NBC : NBC / 2)) continue;
+      float v[8];
+      bc[i].get(v);
+      store_twice(sbc + 16 * idx, v);
+    }
+  }
+  static __device__ __forceinline__ void put(float *at, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  static __device__ __forceinline__ void take(const float *at, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4 *>(at)[0];
+    const float4 b = reinterpret_cast<const float4 *>(at)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+
+// First launch: the kept states, and of segments their end state, sum of delta and
+// gradient from zero.
+template <typename T, int S, bool CUT>
+__global__ void __launch_bounds__(kThreads)
+gdn_ssm_keep_kernel(const BwdParams p) {
+  constexpr int TT = S <= 16 ? 16 : 32, CB = Geo<S>::CB;
+  static_assert(TT % kL == 0 && kChunkTokens % TT == 0, "tiles of whole runs of kL tokens");
+  using In = Inputs<T, S, TT, CUT>;
+  extern __shared__ __align__(16) float smem[];
+  float *sd = smem, *su = sd + TT * CB, *sbc = su + TT * CB, *ss = sbc + 4 * TT * S;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks, slot = blockIdx.y;
+  const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
+  const int sl = lane % Geo<S>::LS, cl = warp * Geo<S>::CL + lane / Geo<S>::LS;
+  const Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
+  let_second();
+  lin::Span s;
+  if (!lin::span_of(p.seq, slot, 0, s)) return;
+  const int64_t D = p.D, state = D * S, begin = s.start - s.seg * p.seq.seg_len;
+  const int64_t off = s.seg * p.seq.seg_len;   // the segment's first token in its sequence
+  const bool last = s.seg == s.count - 1;
+  // tokens up to the last kept state, or all where what follows needs the end
+  const bool whole = CUT && s.count > 1;
+  const int64_t len = whole ? s.len : s.len > 0 ? (s.len - 1) / kL * kL : 0;
+  if (len == 0) return;
+
+  uint64_t A[2][4], h[2][4], P[2][4], Y[2][4];
+  load_rates<S>(p.A_log, own, A);
+  load_own<S>(s.seg == 0 && p.h0 ? p.h0 + s.n * state : nullptr, own, h);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      P[k][j] = pk(1.f, 1.f);
+      Y[k][j] = 0ull;
+    }
+  const int vec = tid % In::VB, vch = first_ch + 8 * vec;
+  const bool von = vch < end_ch;
+  float bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
+
+  const auto keep = [&](int64_t t, const uint64_t (&sum)[2]) {
+    const int64_t at = kept(begin, off + t);
+    store_own<S>(p.ckpt + at * state, own, h);
+    if (CUT && s.seg > 0 && own.on && sl == 0) {
+      float v[4];
+      unpk(sum[0], v[0], v[1]);
+      unpk(sum[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(p.ckpt_d + at * D + own.ch) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  };
+  In in;
+  uint64_t total[2] = {0ull, 0ull};
+  in.fetch(p, s.start, (int)(len < TT ? len : TT), group, vch, von);
+  for (int64_t t0 = 0; t0 < len; t0 += TT) {
+    const int cnt = (int)(len - t0 < TT ? len - t0 : TT);
+    in.form(p, cnt, von, bias, sd, su, ss, sbc);
+    __syncthreads();
+    if (t0 + TT < len)
+      in.fetch(p, s.start + t0 + TT, (int)(len - t0 - TT < TT ? len - t0 - TT : TT), group, vch, von);
+    for (int r = 0; r < cnt; r += kL) {
+      if (t0 + r > 0) keep(t0 + r, total);
+      uint64_t part[2] = {0ull, 0ull};
+#pragma unroll 4
+      for (int t = r; t < r + kL; ++t) {   // (tokens past the last: zeros)
+        const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
+        const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
+        const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
+        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
+        uint64_t cc[4], yy[2];
+        if constexpr (CUT) {
+          const float *at = sbc + TT * S * 2 + t * 2 * S + 8 * sl;
+          const Pairs c0 = lds2(at), c1 = lds2(at + 4), y = lds2(ss + t * CB + 4 * cl);
+          cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
+          yy[0] = y.a; yy[1] = y.b;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
+            h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
+            if constexpr (CUT) {
+              P[k][j] = mul2(P[k][j], a);
+              Y[k][j] = fma2(P[k][j], mul2(cc[j], yy[k]), Y[k][j]);
+            }
+          }
+          part[k] = add2(part[k], dd[k]);
+        }
+      }
+      total[0] = add2(total[0], part[0]);
+      total[1] = add2(total[1], part[1]);
+    }
+    __syncthreads();
+  }
+  if (!whole) {   // the last kept state comes behind the last token that was run
+    keep(len, total);
+    return;
+  }
+  if (!last) store_own<S>(p.seg_x + slot * state, own, h);
+  if (s.seg > 0) store_own<S>(p.seg_y + slot * state, own, Y);
+  if (own.on && sl == 0) {
+    float v[4];
+    unpk(total[0], v[0], v[1]);
+    unpk(total[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p.seg_d + (int64_t)slot * D + own.ch) =
+        make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+template <int S, bool CUT>
+constexpr size_t keep_smem() {
+  constexpr int TT = S <= 16 ? 16 : 32;
+  return 4u * (TT * Geo<S>::CB * (CUT ? 3 : 2) + 4 * TT * S);
+}
+
+// v[8]: four values of db and four of dc of a lane's states, summed over the warp's CL
+// groups of channels.  A lane keeps 8 / CL of them (one for CL of 8 and 16), from `first`.
+template <int CL, int LS>
+__device__ __forceinline__ int sum_groups(float (&v)[8], int grp) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  int first = 0;
+#pragma unroll
+  for (int n = 4, bit = 1; bit < CL; n /= 2, bit *= 2) {
+    const bool up = grp & bit;
+    if (n >= 1) {
+#pragma unroll
+      for (int i = 0; i < (n ? n : 1); ++i) {
+        const float give = up ? v[i] : v[i + n], mine = up ? v[i + n] : v[i];
+        v[i] = mine + __shfl_xor_sync(kAll, give, bit * LS);
+      }
+      first += up ? n : 0;
+    } else {
+      v[0] += __shfl_xor_sync(kAll, v[0], bit * LS);
+    }
+  }
+  return first;
+}
+
+template <int S>
+struct Bwd {
+  static constexpr int CB = Geo<S>::CB, TILE = kL * CB;
+  // delta, delta x (later q), ds (later sum A w), s, b and c, sums of b and c, the tile's
+  // states, the segment's start, sums of dA
+  static constexpr size_t kFloats =
+      4 * TILE + 4 * kL * S + 4 * kL * 2 * S + (size_t)kL * 16 * kThreads + 2 * 16 * kThreads;
+};
+
+// Second launch: tiles from the last token to the first.
+template <typename T, int S, bool GATE>
+__global__ void __launch_bounds__(kThreads, 2)
+gdn_ssm_grad_kernel(const BwdParams p) {
+  constexpr int CB = Geo<S>::CB, LS = Geo<S>::LS, CL = Geo<S>::CL, TILE = Bwd<S>::TILE;
+  using In = Inputs<T, S, kL, true>;
+  extern __shared__ __align__(16) float smem[];
+  float *sd = smem, *su = sd + TILE, *ss = su + TILE, *sy = ss + TILE, *sbc = sy + TILE;
+  float *sred = sbc + 4 * kL * S, *shist = sred + 4 * kL * 2 * S;
+  float *sstart = shist + kL * 16 * kThreads, *sdA = sstart + 16 * kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks;
+  const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
+  const int sl = lane % LS, grp = lane / LS, cl = warp * CL + grp;
+  const Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
+  const int64_t D = p.D, state = D * S;
+
+  // a thread's 16 values in shared memory: four float4, a row of threads each
+  const auto put16 = [&](float *at, const uint64_t (&a)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<ulonglong2 *>(at)[i * kThreads + tid] =
+          make_ulonglong2(a[i >> 1][2 * (i & 1)], a[i >> 1][2 * (i & 1) + 1]);
+  };
+  const auto get16 = [&](const float *at, uint64_t (&a)[2][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const ulonglong2 v = reinterpret_cast<const ulonglong2 *>(at)[i * kThreads + tid];
+      a[i >> 1][2 * (i & 1)] = v.x;
+      a[i >> 1][2 * (i & 1) + 1] = v.y;
+    }
+  };
+
+  uint64_t A[2][4], dA[2][4], g[2][4], h[2][4];
+  load_rates<S>(p.A_log, own, A);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dA[k][j] = 0ull;
+  put16(sdA, dA);
+  const int vec = tid % In::VB, vch = first_ch + 8 * vec;
+  const bool von = vch < end_ch;
+  float bias[8], skip[8], sum_bias[2][8] = {}, sum_skip[2][8] = {};   // of some tiles, of all
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
+    skip[i] = von && p.d_skip ? p.d_skip[vch + i] : 0.f;
+  }
+  int tiles_summed = 0;
+  const auto flush = [&] {   // at most 16 tiles in one run of an accumulator
+    uint64_t sum[2][4];
+    get16(sdA, sum);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[k][j] = add2(sum[k][j], dA[k][j]);
+        dA[k][j] = 0ull;
+      }
+    put16(sdA, sum);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum_bias[1][i] += sum_bias[0][i];
+      sum_skip[1][i] += sum_skip[0][i];
+      sum_bias[0][i] = sum_skip[0][i] = 0.f;
+    }
+    tiles_summed = 0;
+  };
+  wait_first();
+
+  for (int slot = blockIdx.y; slot < p.seq.slots; slot += gridDim.y) {
+    lin::Span s;
+    if (!lin::span_of(p.seq, slot, 0, s)) continue;
+    const int64_t begin = s.start - s.seg * p.seq.seg_len, off = s.seg * p.seq.seg_len;
+    // the gradient that comes from behind the segment, and the state at its start
+    load_own<S>(p.dhT ? p.dhT + s.n * state : nullptr, own, g);
+    for (int i = s.count - 1; i > s.seg; --i)
+      join<S>(g, A, p.seg_y, p.seg_d, slot - s.seg + i, p.D, own);
+    if (s.seg == 0) {
+      load_own<S>(p.h0 ? p.h0 + s.n * state : nullptr, own, h);
+    } else {
+      load_own<S>(p.seg_x + (int64_t)(slot - s.seg) * state, own, h);
+      for (int i = 1; i < s.seg; ++i)
+        join<S>(h, A, p.seg_x, p.seg_d, slot - s.seg + i, p.D, own);
+    }
+    put16(sstart, h);
+
+    const int64_t tiles = (s.len + kL - 1) / kL;
+    In in;
+    if (tiles > 0)
+      in.fetch(p, s.start + (tiles - 1) * kL, (int)(s.len - (tiles - 1) * kL), group, vch, von);
+    for (int64_t tile = tiles - 1; tile >= 0; --tile) {
+      const int64_t t0 = tile * kL;
+      const int cnt = (int)(s.len - t0 < kL ? s.len - t0 : kL);
+      in.form(p, cnt, von, bias, sd, su, ss, sbc);
+      In now = in;   // for the tile's gradients
+      __syncthreads();
+      if (tile > 0) in.fetch(p, s.start + t0 - kL, kL, group, vch, von);
+      if (tile == 0) {
+        get16(sstart, h);
+      } else {
+        const int64_t at = kept(begin, off + t0);
+        if (s.seg > 0) {
+          get16(sstart, h);
+          join<S>(h, A, p.ckpt, p.ckpt_d, at, p.D, own);
+        } else {
+          load_own<S>(p.ckpt + at * state, own, h);
+        }
+      }
+      // the tile's states
+#pragma unroll 4
+      for (int t = 0; t < cnt; ++t) {
+        put16(shist + t * 16 * kThreads, h);
+        const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
+        const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
+        const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
+        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
+        uint64_t cc[4], y[2];
+        if constexpr (GATE) {
+          const float *at = sbc + kL * S * 2 + t * 2 * S + 8 * sl;
+          const Pairs c0 = lds2(at), c1 = lds2(at + 4);
+          cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
+            h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
+            if constexpr (GATE) y[k] = j ? fma2(cc[j], h[k][j], y[k]) : mul2(cc[j], h[k][j]);
+          }
+        if constexpr (GATE) {
+          float v[4];
+          unpk(y[0], v[0], v[1]);
+          unpk(y[1], v[2], v[3]);
+          sum_channels<LS>(v, sl);
+          store_channels<LS>(sy + t * CB + 4 * cl, v, sl);
+        }
+      }
+      // and backward through them
+#pragma unroll 2
+      for (int t = cnt - 1; t >= 0; --t) {
+        const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl),
+                    e = lds2(ss + t * CB + 4 * cl);
+        const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b}, ee[2] = {e.a, e.b};
+        const float *bt = sbc + t * 2 * S + 8 * sl, *ct = bt + kL * S * 2;
+        const Pairs b0 = lds2(bt), b1 = lds2(bt + 4), c0 = lds2(ct), c1 = lds2(ct + 4);
+        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b}, cc[4] = {c0.a, c0.b, c1.a, c1.b};
+        uint64_t before[2][4], db[4], dc[4], q[2], aw[2];
+        get16(shist + t * 16 * kThreads, before);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t G = fma2(cc[j], ee[k], g[k][j]);
+            dc[j] = k ? fma2(ee[k], h[k][j], dc[j]) : mul2(ee[k], h[k][j]);
+            db[j] = k ? fma2(uu[k], G, db[j]) : mul2(uu[k], G);
+            q[k] = j ? fma2(bb[j], G, q[k]) : mul2(bb[j], G);
+            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
+            g[k][j] = mul2(a, G);
+            const uint64_t w = mul2(g[k][j], before[k][j]);
+            aw[k] = j ? fma2(A[k][j], w, aw[k]) : mul2(A[k][j], w);
+            dA[k][j] = fma2(dd[k], w, dA[k][j]);
+            h[k][j] = before[k][j];
+          }
+        float v[4], r[8];
+        __syncwarp();   // delta x and ds of this token are read: q and sum A w take their place
+        unpk(q[0], v[0], v[1]);
+        unpk(q[1], v[2], v[3]);
+        sum_channels<LS>(v, sl);
+        store_channels<LS>(su + t * CB + 4 * cl, v, sl);
+        unpk(aw[0], v[0], v[1]);
+        unpk(aw[1], v[2], v[3]);
+        sum_channels<LS>(v, sl);
+        store_channels<LS>(ss + t * CB + 4 * cl, v, sl);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo, hi;
+          unpk(db[j], lo, hi);
+          r[j] = lo + hi;
+          unpk(dc[j], lo, hi);
+          r[4 + j] = lo + hi;
+        }
+        const int first = sum_groups<CL, LS>(r, grp);
+        float *red = sred + (warp * kL + t) * 2 * S;
+        constexpr int KEEP = CL >= 8 ? 1 : 8 / CL;
+        if (CL <= 8 || grp < 8)
+#pragma unroll
+          for (int i = 0; i < KEEP; ++i) {
+            const int id = first + i;   // 0-3: db of its states, 4-7: dc
+            red[(id >> 2) * S + 4 * sl + (id & 3)] = r[i];
+          }
+      }
+      __syncthreads();
+      // db and dc of this CTA's channels
+      for (int i = tid; i < cnt * 2 * S; i += kThreads) {
+        const int row = i / (2 * S), at = i % (2 * S);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) sum += sred[(w * kL + row) * 2 * S + at];
+        p.part_bc[(((int64_t)cb * p.rows() + s.start + t0 + row) * p.G + group) * 2 * S + at] = sum;
+      }
+#pragma unroll
+      for (int i = 0; i < In::NV; ++i) {
+        const int row = tid / In::VB + i * In::RT;
+        if (!von || row >= cnt) continue;
+        const int64_t out = (s.start + t0 + row) * D + vch;
+        float xv[8], tv[8], yv[8], dl[8], qv[8], wv[8], o[8];
+        now.x[i].get(xv);
+        now.dt[i].get(tv);
+        now.dy[i].get(yv);
+        In::take(sd + row * CB + 8 * vec, dl);
+        In::take(su + row * CB + 8 * vec, qv);
+        In::take(ss + row * CB + 8 * vec, wv);
+        Raw8<T> r;
+        if constexpr (GATE) {
+          float gv[8], sv[8];
+          now.gate[i].get(gv);
+          In::take(sy + row * CB + 8 * vec, sv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float sg = sigmoid(gv[j]), total = fmaf(skip[j], p.d_skip ? xv[j] : 0.f, sv[j]);
+            o[j] = yv[j] * total * (sg * fmaf(gv[j], 1.f - sg, 1.f));
+            yv[j] *= gv[j] * sg;
+          }
+          r.set(o);
+          r.store(static_cast<T *>(p.dgate) + out);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = fmaf(dl[j], qv[j], skip[j] * yv[j]);
+          sum_skip[0][j] = fmaf(yv[j], xv[j], sum_skip[0][j]);
+        }
+        r.set(o);
+        r.store(static_cast<T *>(p.dx) + out);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = fmaf(xv[j], qv[j], 0.6931471805599453f * wv[j]);   // (rates carry log2 e)
+          if (p.softplus) o[j] *= sigmoid(tv[j] + bias[j]);
+          sum_bias[0][j] += o[j];
+        }
+        r.set(o);
+        r.store(static_cast<T *>(p.ddt) + out);
+      }
+      if (++tiles_summed == 16) flush();
+      __syncthreads();
+    }
+    if (p.dh0 && s.seg == 0) store_own<S>(p.dh0 + s.n * state, own, g);
+  }
+
+  // this CTA's sums over its tokens
+  flush();
+  get16(sdA, dA);
+  float *part = p.part_w + (int64_t)blockIdx.y * (state + 2 * D);
+  store_own<S>(part, own, dA);
+  __syncthreads();
+  float *sum = shist;   // [2][rows of threads][CB]
+  constexpr int RT = In::RT;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sum[(tid / In::VB) * CB + 8 * vec + i] = sum_skip[1][i];
+    sum[(RT + tid / In::VB) * CB + 8 * vec + i] = sum_bias[1][i];
+  }
+  __syncthreads();
+  for (int i = tid; i < 2 * CB; i += kThreads) {
+    const int which = i / CB, ch = i % CB;
+    if (first_ch + ch >= end_ch) continue;
+    float r = 0.f;
+    for (int k = 0; k < RT; ++k) r += sum[(which * RT + k) * CB + ch];
+    part[state + which * D + first_ch + ch] = r;
+  }
+}
+
+// Third launch: the sums over blocks of channels (one of a token's 2 G S values a
+// thread), and behind them those over the tokens of the second launch's CTAs.
+template <typename T>
+__global__ void __launch_bounds__(256)
+gdn_ssm_sum_kernel(const BwdParams p, int S, int64_t bc_blocks) {
+  if (blockIdx.x < bc_blocks) {
+    const int64_t per = (int64_t)p.G * 2 * S, n = p.rows() * per;
+    const int64_t i0 = (int64_t)blockIdx.x * 256, i = i0 + threadIdx.x;
+    if (p.seq.cu) {   // rows of a sequence whose offsets are bad stay as they are
+      const Sequences q{p.seq.cu, p.seq.status, p.seq.seq_len, p.seq.num_seqs};
+      const int64_t row = (i < n ? i : n - 1) / per;
+      const int64_t first = (i0 + (threadIdx.x & ~31)) / per;
+      int at = q.find(first < p.rows() ? first : p.rows() - 1);
+      while (at + 1 < p.seq.num_seqs && p.seq.cu[at + 1] <= row) ++at;
+      int64_t start, len;
+      if (!q.bounds(at, start, len) || row < start || row >= start + len) return;
+    }
+    if (i >= n) return;
+    float sum = 0.f;
+    for (int b = 0; b < p.blocks; ++b) sum += p.part_bc[b * n + i];
+    const int64_t row = i / per;
+    const int r = (int)(i % per), grp = r / (2 * S), which = r / S % 2, st = r % S;
+    T *out = static_cast<T *>(which ? p.dc : p.db) + (row * p.G + grp) * S + st;
+    store_out(out, sum);
+    return;
+  }
+  const int64_t state = (int64_t)p.D * S, n = state + 2 * p.D;
+  const int64_t i = (blockIdx.x - bc_blocks) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float sum = 0.f;
+  for (int k = 0; k < p.parts; ++k) sum += p.part_w[k * n + i];
+  if (i < state) {
+    if (p.dA_log) p.dA_log[i] = -expf(p.A_log[i]) * sum;
+  } else if (i < state + p.D) {
+    if (p.dD_skip) p.dD_skip[i - state] = sum;
+  } else if (p.ddt_bias) {
+    p.ddt_bias[i - state - p.D] = sum;
+  }
+}
+
+// The arrays of the workspace behind the status word, in floats.
+struct Layout {
+  size_t x, y, d, ckpt, ckpt_d, bc, w, total;
+};
+Layout layout(int64_t rows, int64_t D, int64_t S, int64_t groups, int64_t blocks, int64_t parts,
+              const lin::Plan &pl) {
+  const auto round = [](size_t n) { return (n + 3) / 4 * 4; };
+  const size_t state = (size_t)(D * S), slots = pl.seg_len ? (size_t)pl.slots : 0;
+  Layout l;
+  l.x = 0;
+  l.y = l.x + slots * state;
+  l.d = l.y + slots * state;
+  l.ckpt = l.d + slots * D;
+  l.ckpt_d = l.ckpt + (size_t)(rows / kL) * state;
+  l.bc = l.ckpt_d + (slots ? (size_t)(rows / kL) * D : 0);
+  l.w = l.bc + round((size_t)blocks * rows * groups * 2 * S);
+  l.total = l.w + (size_t)parts * (state + 2 * D);
+  return l;
+}
+constexpr double kFirst = 0.5;
+// CTAs of the second launch over the slots: two an SM, four rounds of them at most
+int64_t parts_of(int64_t slots, int64_t blocks) {
+  const int64_t most = (4 * kSMs + blocks - 1) / blocks;
+  return slots < most ? slots : most;
+}
+
+template <typename T, int S>
+cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
+  const dim3 grid(groups * p.blocks, p.seq.slots);
+  cudaError_t err;
+  if (p.seq.seg_len) {
+    constexpr size_t kBytes = keep_smem<S, true>();
+    err = allow_smem<gdn_ssm_keep_kernel<T, S, true>>(kBytes);
+    if (err != cudaSuccess) return err;
+    gdn_ssm_keep_kernel<T, S, true><<<grid, kThreads, kBytes, stream>>>(p);
+  } else {
+    constexpr size_t kBytes = keep_smem<S, false>();
+    err = allow_smem<gdn_ssm_keep_kernel<T, S, false>>(kBytes);
+    if (err != cudaSuccess) return err;
+    gdn_ssm_keep_kernel<T, S, false><<<grid, kThreads, kBytes, stream>>>(p);
+  }
+  err = taken(cudaGetLastError());
+  if (err != cudaSuccess) return err;
+  const dim3 tiles(groups * p.blocks, p.parts);
+  constexpr size_t kGrad = 4 * Bwd<S>::kFloats;
+  if (p.gate) {
+    err = allow_smem<gdn_ssm_grad_kernel<T, S, true>>(kGrad);
+    if (err == cudaSuccess)
+      err = launch_beside(gdn_ssm_grad_kernel<T, S, true>, tiles, kThreads, kGrad, stream, p);
+  } else {
+    err = allow_smem<gdn_ssm_grad_kernel<T, S, false>>(kGrad);
+    if (err == cudaSuccess)
+      err = launch_beside(gdn_ssm_grad_kernel<T, S, false>, tiles, kThreads, kGrad, stream, p);
+  }
+  if (err != cudaSuccess) return err;
+  const int64_t bc = (p.rows() * groups * 2 * S + 255) / 256;
+  const int64_t w = ((int64_t)p.D * (S + 2) + 255) / 256;
+  if (bc + w > 0x7fffffff) return cudaErrorInvalidValue;
+  gdn_ssm_sum_kernel<T><<<(unsigned)(bc + w), 256, 0, stream>>>(p, S, bc);
+  return taken(cudaGetLastError());
+}
+template <typename T>
+cudaError_t launch_t(const BwdParams &p, int S, int groups, cudaStream_t stream) {
+  switch (S) {
+    case 8: return launch_s<T, 8>(p, groups, stream);
+    case 16: return launch_s<T, 16>(p, groups, stream);
+    case 32: return launch_s<T, 32>(p, groups, stream);
+    default: return launch_s<T, 64>(p, groups, stream);
+  }
+}
+
+}  // namespace
+}  // namespace ssm
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_ssm_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
+                                  int32_t d_state, int32_t groups) {
+  using namespace gdn::ssm;
+  if (num_seqs <= 0 || seq_len < 0 || channels <= 0 || d_state <= 0 || groups <= 0 ||
+      channels % groups || !state_size(d_state))
+    return 0;
+  const int64_t blocks = channel_blocks(channels / groups, d_state), all = blocks * groups;
+  size_t most = 0;
+  for (bool packed : {false, true}) {
+    const int64_t rows = packed ? seq_len : (int64_t)num_seqs * seq_len;
+    const auto pl = plan(num_seqs, seq_len, packed, all, kFirst);
+    for (const auto &one : {pl, gdn::lin::Plan{0, num_seqs}}) {
+      const size_t n = layout(rows, channels, d_state, groups, blocks, parts_of(one.slots, all),
+                              one).total;
+      most = n > most ? n : most;
+    }
+  }
+  return gdn::kStatusBytes + 4 * most;
+}
+
+gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const void *b,
+                       const void *c, const float *D_skip, const void *gate, const float *dt_bias,
+                       const float *initial_state, const int32_t *cu_seqlens, const void *d_y,
+                       const float *d_final_state, void *dx, void *ddt, float *dA_log, void *db,
+                       void *dc, float *dD_skip, void *dgate, float *ddt_bias,
+                       float *d_initial_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t d_state, int32_t groups, int32_t num_seqs, int64_t x_stride,
+                       int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t gate_stride,
+                       gdn_dtype dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+  using namespace gdn;
+  using namespace gdn::ssm;
+  const gdn_status st = check_sizes(batch, seq_len, channels, d_state, groups, num_seqs,
+                                    cu_seqlens, dtype, flags);
+  if (st != GDN_OK) return st;
+  Sizes z{(size_t)batch * seq_len, dtype == GDN_F32 ? 4u : 2u, channels,
+          (int64_t)groups * d_state};
+  z.state = (size_t)num_seqs * channels * d_state * 4;
+  const size_t ds_bytes = (size_t)channels * d_state * 4, ch_bytes = (size_t)channels * 4;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (seq_len == 0) {   // no tokens: the weights' gradients are zero, the states' pass through
+    const gdn_status r = pass_states(d_final_state, d_initial_state, z.state, s);
+    if (r != GDN_OK) return r;
+    for (const auto &w : {Range{dA_log, ds_bytes}, Range{dD_skip, ch_bytes},
+                          Range{ddt_bias, ch_bytes}})
+      if (w.p && taken(cudaMemsetAsync(const_cast<void *>(w.p), 0, w.n, s)) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return GDN_OK;
+  }
+  if (!strides_of(z, x_stride, dt_stride, b_stride, c_stride, gate_stride))
+    return GDN_ERR_INVALID_ARG;
+  if (!x || !dt || !A_log || !b || !c || !d_y || !dx || !ddt || !db || !dc)
+    return GDN_ERR_INVALID_ARG;
+  if ((gate != nullptr) != (dgate != nullptr)) return GDN_ERR_INVALID_ARG;
+  const void *ptrs[] = {x, dt, A_log, b, c, D_skip, gate, dt_bias, initial_state, cu_seqlens, d_y,
+                        d_final_state, dx, ddt, dA_log, db, dc, dD_skip, dgate, ddt_bias,
+                        d_initial_state, workspace};
+  if (!all_aligned(ptrs)) return GDN_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < kStatusBytes) return GDN_ERR_WORKSPACE;
+
+  const size_t wide = z.rows * channels * z.e, thin = z.rows * z.gs * z.e;
+  const Range outs[] = {{dx, wide}, {ddt, wide}, {db, thin}, {dc, thin}, {dgate, wide},
+                        {dA_log, ds_bytes}, {dD_skip, ch_bytes}, {ddt_bias, ch_bytes},
+                        {d_initial_state, z.state}};
+  const Range ins[] = {{workspace, workspace_bytes},
+                       {x, span_bytes(z.rows, z.sx, z.D, z.e)},
+                       {dt, span_bytes(z.rows, z.sdt, z.D, z.e)},
+                       {b, span_bytes(z.rows, z.sb, z.gs, z.e)},
+                       {c, span_bytes(z.rows, z.sc, z.gs, z.e)},
+                       {gate, span_bytes(z.rows, z.sg, z.D, z.e)},
+                       {A_log, ds_bytes}, {D_skip, ch_bytes}, {dt_bias, ch_bytes},
+                       {cu_seqlens, (size_t)(num_seqs + 1) * 4}, {d_y, wide},
+                       {initial_state, z.state}, {d_final_state, z.state}};
+  if (!apart(outs, ins)) return GDN_ERR_INVALID_ARG;
+  for (int i = 1; i < 13; ++i)
+    if (overlaps(ins[0], ins[i])) return GDN_ERR_INVALID_ARG;
+
+  BwdParams p{};
+  p.x = x; p.dt = dt; p.b = b; p.c = c; p.gate = gate; p.dy = d_y;
+  p.A_log = A_log; p.d_skip = D_skip; p.dt_bias = dt_bias;
+  p.h0 = initial_state; p.dhT = d_final_state;
+  p.dx = dx; p.ddt = ddt; p.db = db; p.dc = dc; p.dgate = dgate;
+  p.dA_log = dA_log; p.dD_skip = dD_skip; p.ddt_bias = ddt_bias; p.dh0 = d_initial_state;
+  p.sx = z.sx; p.sdt = z.sdt; p.sb = z.sb; p.sc = z.sc; p.sg = z.sg;
+  p.D = channels;
+  p.G = groups;
+  p.Dg = channels / groups;
+  p.blocks = channel_blocks(p.Dg, d_state);
+  p.softplus = flags & GDN_DT_SOFTPLUS;
+  p.seq.cu = cu_seqlens;
+  p.seq.status = static_cast<DeviceStatus *>(workspace);
+  p.seq.seq_len = seq_len;
+  p.seq.num_seqs = num_seqs;
+  const int64_t all = (int64_t)groups * p.blocks;
+  auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, all, kFirst);
+  Layout l;
+  for (;;) {   // uncut where the workspace is too small for the segments
+    p.parts = (int32_t)parts_of(pl.slots, all);
+    l = layout((int64_t)z.rows, channels, d_state, groups, p.blocks, p.parts, pl);
+    if (4 * l.total <= workspace_bytes - kStatusBytes) break;
+    if (!pl.seg_len) return GDN_ERR_WORKSPACE;
+    pl = {0, num_seqs};
+  }
+  p.seq.seg_len = pl.seg_len;
+  p.seq.slots = pl.slots;
+  float *ws = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+  p.seg_x = ws + l.x;
+  p.seg_y = ws + l.y;
+  p.seg_d = ws + l.d;
+  p.ckpt = ws + l.ckpt;
+  p.ckpt_d = ws + l.ckpt_d;
+  p.part_bc = ws + l.bc;
+  p.part_w = ws + l.w;
+  const cudaError_t err = dtype == GDN_F32 ? launch_t<float>(p, d_state, groups, s)
+                                           : launch_t<__nv_bfloat16>(p, d_state, groups, s);
+  return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,373 @@
+// Selective state space scan, prompts: host checks and the forward kernels (gdn_ssm.cuh
+// has the mathematics and the layout of the work).
+//
+// A CTA walks over its tokens in tiles: delta and delta x are formed from the tile's
+// inputs by threads that own eight channels of a token, and left in shared memory as
+// fp32 together with b and c; then every thread runs its 16 elements over the tile while
+// the next tile's inputs are on their way to registers; then the tile's outputs take the
+// skip and the gate on their way out.
+#include "gdn_ssm.cuh"
+
+namespace gdn {
+gdn_status pass_states(const float *from, float *to, size_t bytes, cudaStream_t s);
+
+namespace ssm {
+namespace {
+
+template <int S>
+struct Fwd : Geo<S> {
+  using Geo<S>::CB;
+  static constexpr int TT = S <= 16 ? S : 32;                    // tokens of a tile
+  static constexpr int NV = (TT * CB / 8 + kThreads - 1) / kThreads;   // vectors of a thread
+  static constexpr int NB = (2 * TT * S / 8 + kThreads - 1) / kThreads;
+  static constexpr int VB = CB / 8;                               // vectors of a token
+  static_assert(kThreads % VB == 0 && TT * CB / 8 == NV * kThreads, "whole rows of vectors");
+};
+
+template <typename T, int S, bool OUT>
+__global__ void __launch_bounds__(kThreads)
+gdn_ssm_scan_kernel(const Params p) {
+  using F = Fwd<S>;
+  constexpr int TT = F::TT, CB = F::CB, LS = F::LS;
+  __shared__ __align__(16) float sd[TT * CB], su[TT * CB], sy[OUT ? TT * CB : 4];
+  __shared__ __align__(16) float sbc[(OUT ? 2 : 1) * TT * S * 2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks, slot = blockIdx.y;
+  const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
+  const int sl = lane % LS, cl = warp * F::CL + lane / LS;   // its states, its four channels
+  Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
+
+  uint64_t A[2][4], h[2][4];
+  load_rates<S>(p.A_log, own, A);
+  // its eight channels where tiles are formed and left
+  const int vec = tid % F::VB, vch = first_ch + 8 * vec;
+  const bool von = vch < end_ch;
+  float bias[8], skip[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
+    skip[i] = OUT && von && p.d_skip ? p.d_skip[vch + i] : 0.f;
+  }
+  if (OUT && p.seq.seg_len) wait_first();   // every CTA: none may end before the first launch
+  if (!OUT) let_second();
+  lin::Span s;
+  if (!lin::span_of(p.seq, slot, 0, s)) return;
+  const int64_t state = (int64_t)p.D * S;
+  if (!OUT && s.seg == s.count - 1) {   // nothing follows; keep what the last launch overwrites
+    if (p.keep) {
+      load_own<S>(p.h0 + s.n * state, own, h);
+      store_own<S>(p.seg_x + slot * state, own, h);
+    }
+    return;
+  }
+  if (s.seg == 0) {
+    const bool kept = OUT && p.keep && p.seq.seg_len;
+    load_own<S>(kept ? p.seg_x + (slot + s.count - 1) * state : p.h0 ? p.h0 + s.n * state : nullptr,
+                own, h);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[k][j] = 0ull;
+    if (OUT) {
+      load_own<S>(p.seg_x + (slot - s.seg) * state, own, h);   // the first one's end state
+      for (int i = 1; i < s.seg; ++i)
+        join<S>(h, A, p.seg_x, p.seg_d, slot - s.seg + i, p.D, own);
+    }
+  }
+
+  Raw8<T> xr[F::NV], dr[F::NV], gr[F::NV], br[F::NB];
+  const T *x = static_cast<const T *>(p.x) + s.start * p.sx + vch;
+  const T *dt = static_cast<const T *>(p.dt) + s.start * p.sdt + vch;
+  const T *gate = OUT && p.gate ? static_cast<const T *>(p.gate) + s.start * p.sg + vch : nullptr;
+  const T *b = static_cast<const T *>(p.b) + s.start * p.sb + group * S;
+  const T *c = static_cast<const T *>(p.c) + s.start * p.sc + group * S;
+  const auto fetch = [&](int64_t t0) {
+    const int cnt = (int)(s.len - t0 < TT ? s.len - t0 : TT);
+#pragma unroll
+    for (int i = 0; i < F::NV; ++i) {
+      const int row = tid / F::VB + i * (kThreads / F::VB);
+      const bool on = von && row < cnt;
+      xr[i].zero();
+      dr[i].zero();
+      gr[i].zero();
+      if (on) {
+        xr[i].load(x + (t0 + row) * p.sx);
+        dr[i].load(dt + (t0 + row) * p.sdt);
+        if (gate) gr[i].load(gate + (t0 + row) * p.sg);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < F::NB; ++i) {
+      const int idx = tid + i * kThreads, row = idx % (TT * S / 8) / (S / 8), v = idx % (S / 8);
+      const bool second = idx >= TT * S / 8;
+      br[i].zero();
+      if (row < cnt && idx < 2 * TT * S / 8) {
+        if (!second) br[i].load(b + (t0 + row) * p.sb + 8 * v);
+        else if (OUT) br[i].load(c + (t0 + row) * p.sc + 8 * v);
+      }
+    }
+  };
+
+  uint64_t total[2] = {0ull, 0ull};
+  fetch(0);
+  for (int64_t t0 = 0; t0 < s.len; t0 += TT) {
+    const int cnt = (int)(s.len - t0 < TT ? s.len - t0 : TT);
+#pragma unroll
+    for (int i = 0; i < F::NV; ++i) {
+      const int row = tid / F::VB + i * (kThreads / F::VB);
+      float xv[8], dv[8], uv[8];
+      xr[i].get(xv);
+      dr[i].get(dv);
+      const bool on = von && row < cnt;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = dv[j] + bias[j];
+        dv[j] = on ? (p.softplus ? softplus<T>(v) : v) : 0.f;
+        uv[j] = dv[j] * xv[j];
+      }
+      float4 *d = reinterpret_cast<float4 *>(sd + row * CB + 8 * vec);
+      float4 *u = reinterpret_cast<float4 *>(su + row * CB + 8 * vec);
+      d[0] = make_float4(dv[0], dv[1], dv[2], dv[3]);
+      d[1] = make_float4(dv[4], dv[5], dv[6], dv[7]);
+      u[0] = make_float4(uv[0], uv[1], uv[2], uv[3]);
+      u[1] = make_float4(uv[4], uv[5], uv[6], uv[7]);
+    }
+#pragma unroll
+    for (int i = 0; i < F::NB; ++i) {
+      const int idx = tid + i * kThreads;
+      if (idx < (OUT ? 2 : 1) * TT * S / 8) {
+        float v[8];
+        br[i].get(v);
+        store_twice(sbc + 16 * idx, v);
+      }
+    }
+    Raw8<T> xo[F::NV], go[F::NV];   // kept for the tile's outputs
+#pragma unroll
+    for (int i = 0; i < F::NV; ++i) {
+      xo[i] = xr[i];
+      go[i] = gr[i];
+    }
+    __syncthreads();
+    if (t0 + TT < s.len) fetch(t0 + TT);
+
+    uint64_t part[2] = {0ull, 0ull};
+    const int steps = (cnt + 3) & ~3;   // (rows past the last token are zeros: no change)
+#pragma unroll 4
+    for (int t = 0; t < steps; ++t) {
+      const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
+      const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
+      const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
+      const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
+      uint64_t cc[4];
+      if constexpr (OUT) {
+        const float *at = sbc + TT * S * 2 + t * 2 * S + 8 * sl;
+        const Pairs c0 = lds2(at), c1 = lds2(at + 4);
+        cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
+      }
+      uint64_t y[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
+          h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
+          if constexpr (OUT) y[k] = j ? fma2(cc[j], h[k][j], y[k]) : mul2(cc[j], h[k][j]);
+        }
+        if constexpr (!OUT) part[k] = add2(part[k], dd[k]);
+      }
+      if constexpr (OUT) {
+        float v[4];
+        unpk(y[0], v[0], v[1]);
+        unpk(y[1], v[2], v[3]);
+        sum_channels<LS>(v, sl);
+        store_channels<LS>(sy + t * CB + 4 * cl, v, sl);
+      }
+    }
+    if constexpr (!OUT) {   // a sum of sums over tiles: no long run of one accumulator
+      total[0] = add2(total[0], part[0]);
+      total[1] = add2(total[1], part[1]);
+    }
+    __syncthreads();
+    if constexpr (OUT) {
+      T *y = static_cast<T *>(p.y) + (s.start + t0) * p.D + vch;
+#pragma unroll
+      for (int i = 0; i < F::NV; ++i) {
+        const int row = tid / F::VB + i * (kThreads / F::VB);
+        if (!von || row >= cnt) continue;
+        float xv[8], gv[8], yv[8];
+        xo[i].get(xv);
+        const float4 *at = reinterpret_cast<const float4 *>(sy + row * CB + 8 * vec);
+        const float4 lo = at[0], hi = at[1];
+        yv[0] = lo.x; yv[1] = lo.y; yv[2] = lo.z; yv[3] = lo.w;
+        yv[4] = hi.x; yv[5] = hi.y; yv[6] = hi.z; yv[7] = hi.w;
+        if (p.d_skip)   // (an infinite x has no part in y without a skip)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) yv[j] = fmaf(skip[j], xv[j], yv[j]);
+        if (gate) {
+          go[i].get(gv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) yv[j] *= gv[j] * sigmoid(gv[j]);
+        }
+        Raw8<T> out;
+        out.set(yv);
+        out.store(y + (int64_t)row * p.D);
+      }
+    }
+  }
+  if (!OUT) {
+    store_own<S>(p.seg_x + slot * state, own, h);
+    if (own.on && sl == 0) {
+      float v[4];
+      unpk(total[0], v[0], v[1]);
+      unpk(total[1], v[2], v[3]);
+      *reinterpret_cast<float4 *>(p.seg_d + (int64_t)slot * p.D + own.ch) =
+          make_float4(v[0], v[1], v[2], v[3]);
+    }
+  } else if (p.hT && s.seg == s.count - 1) {
+    store_own<S>(p.hT + s.n * state, own, h);
+  }
+}
+
+template <typename T, int S>
+cudaError_t launch_s(const Params &p, int groups, cudaStream_t stream) {
+  const dim3 grid(groups * p.blocks, p.seq.slots);
+  if (p.seq.seg_len == 0) {
+    gdn_ssm_scan_kernel<T, S, true><<<grid, kThreads, 0, stream>>>(p);
+    return taken(cudaGetLastError());
+  }
+  gdn_ssm_scan_kernel<T, S, false><<<grid, kThreads, 0, stream>>>(p);
+  const cudaError_t err = taken(cudaGetLastError());
+  if (err != cudaSuccess) return err;
+  return launch_beside(gdn_ssm_scan_kernel<T, S, true>, grid, kThreads, 0, stream, p);
+}
+template <typename T>
+cudaError_t launch_t(const Params &p, int S, int groups, cudaStream_t stream) {
+  switch (S) {
+    case 8: return launch_s<T, 8>(p, groups, stream);
+    case 16: return launch_s<T, 16>(p, groups, stream);
+    case 32: return launch_s<T, 32>(p, groups, stream);
+    default: return launch_s<T, 64>(p, groups, stream);
+  }
+}
+constexpr double kFirst = 0.7;   // the first launch forms no outputs
+
+}  // namespace
+
+gdn_status check_sizes(int32_t batch, int32_t seq_len, int32_t channels, int32_t d_state,
+                       int32_t groups, int32_t num_seqs, const void *cu, gdn_dtype dtype,
+                       uint32_t flags) {
+  if (batch <= 0 || seq_len < 0 || channels <= 0 || d_state <= 0 || groups <= 0 || num_seqs <= 0)
+    return GDN_ERR_INVALID_ARG;
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return GDN_ERR_INVALID_ARG;
+  if (flags & ~(uint32_t)GDN_DT_SOFTPLUS) return GDN_ERR_INVALID_ARG;
+  if (cu ? batch != 1 : num_seqs != batch) return GDN_ERR_INVALID_ARG;
+  if (channels % groups) return GDN_ERR_INVALID_ARG;
+  if (!state_size(d_state) || channels / groups % 8) return GDN_ERR_UNSUPPORTED;
+  if (num_seqs > 16384 || channels > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+bool strides_of(Sizes &z, int64_t x, int64_t dt, int64_t b, int64_t c, int64_t gate) {
+  z.sx = row_stride(x, z.D, z.e);
+  z.sdt = row_stride(dt, z.D, z.e);
+  z.sb = row_stride(b, z.gs, z.e);
+  z.sc = row_stride(c, z.gs, z.e);
+  z.sg = row_stride(gate, z.D, z.e);
+  return z.sx && z.sdt && z.sb && z.sc && z.sg;
+}
+
+}  // namespace ssm
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
+                              int32_t d_state, int32_t groups) {
+  using namespace gdn::ssm;
+  if (num_seqs <= 0 || seq_len < 0 || channels <= 0 || d_state <= 0 || groups <= 0 ||
+      channels % groups || !state_size(d_state))
+    return 0;
+  const int64_t blocks = (int64_t)groups * channel_blocks(channels / groups, d_state);
+  size_t most = 0;
+  for (bool packed : {false, true}) {
+    const auto pl = plan(num_seqs, seq_len, packed, blocks, kFirst);
+    const size_t n = pl.seg_len ? (size_t)pl.slots * channels * (d_state + 1) * 4 : 0;
+    most = n > most ? n : most;
+  }
+  return gdn::kStatusBytes + most;
+}
+
+gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const void *b,
+                       const void *c, const float *D_skip, const void *gate, const float *dt_bias,
+                       const float *initial_state, const int32_t *cu_seqlens, void *y,
+                       float *final_state, int32_t batch, int32_t seq_len, int32_t channels,
+                       int32_t d_state, int32_t groups, int32_t num_seqs, int64_t x_stride,
+                       int64_t dt_stride, int64_t b_stride, int64_t c_stride, int64_t gate_stride,
+                       gdn_dtype dtype, uint32_t flags, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+  using namespace gdn;
+  using namespace gdn::ssm;
+  const gdn_status st = check_sizes(batch, seq_len, channels, d_state, groups, num_seqs,
+                                    cu_seqlens, dtype, flags);
+  if (st != GDN_OK) return st;
+  Sizes z{(size_t)batch * seq_len, dtype == GDN_F32 ? 4u : 2u, channels,
+          (int64_t)groups * d_state};
+  z.state = (size_t)num_seqs * channels * d_state * 4;
+  if (seq_len == 0) return pass_states(initial_state, final_state, z.state, (cudaStream_t)stream);
+  if (!strides_of(z, x_stride, dt_stride, b_stride, c_stride, gate_stride))
+    return GDN_ERR_INVALID_ARG;
+  if (!x || !dt || !A_log || !b || !c || !y) return GDN_ERR_INVALID_ARG;
+  const void *ptrs[] = {x, dt, A_log, b, c, D_skip, gate, dt_bias, initial_state, cu_seqlens, y,
+                        final_state, workspace};
+  if (!all_aligned(ptrs)) return GDN_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < kStatusBytes) return GDN_ERR_WORKSPACE;
+
+  const Range outs[] = {{y, z.rows * channels * z.e}, {final_state, z.state}};
+  const Range ins[] = {{x, span_bytes(z.rows, z.sx, z.D, z.e)},
+                       {dt, span_bytes(z.rows, z.sdt, z.D, z.e)},
+                       {b, span_bytes(z.rows, z.sb, z.gs, z.e)},
+                       {c, span_bytes(z.rows, z.sc, z.gs, z.e)},
+                       {gate, span_bytes(z.rows, z.sg, z.D, z.e)},
+                       {A_log, (size_t)channels * d_state * 4},
+                       {D_skip, (size_t)channels * 4},
+                       {dt_bias, (size_t)channels * 4},
+                       {cu_seqlens, (size_t)(num_seqs + 1) * 4},
+                       {initial_state == final_state ? nullptr : initial_state, z.state},
+                       {workspace, workspace_bytes}};
+  if (!apart(outs, ins)) return GDN_ERR_INVALID_ARG;
+  for (int i = 0; i < 10; ++i)
+    if (overlaps(ins[10], ins[i])) return GDN_ERR_INVALID_ARG;
+  if (overlaps(outs[0], {initial_state, z.state}) || overlaps(ins[10], {initial_state, z.state}))
+    return GDN_ERR_INVALID_ARG;
+
+  Params p{};
+  p.x = x; p.dt = dt; p.b = b; p.c = c; p.gate = gate;
+  p.A_log = A_log; p.d_skip = D_skip; p.dt_bias = dt_bias; p.h0 = initial_state;
+  p.y = y; p.hT = final_state;
+  p.sx = z.sx; p.sdt = z.sdt; p.sb = z.sb; p.sc = z.sc; p.sg = z.sg;
+  p.D = channels;
+  p.Dg = channels / groups;
+  p.blocks = channel_blocks(p.Dg, d_state);
+  p.softplus = flags & GDN_DT_SOFTPLUS;
+  p.seq.cu = cu_seqlens;
+  p.seq.status = static_cast<DeviceStatus *>(workspace);
+  p.seq.seq_len = seq_len;
+  p.seq.num_seqs = num_seqs;
+  const int64_t blocks = (int64_t)groups * p.blocks;
+  const auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, blocks, kFirst);
+  const bool cut = pl.seg_len && (size_t)pl.slots * channels * (d_state + 1) * 4 <=
+                                     workspace_bytes - kStatusBytes;
+  p.seq.seg_len = cut ? pl.seg_len : 0;
+  p.seq.slots = cut ? pl.slots : num_seqs;
+  p.seq.ranked = cu_seqlens && !cut && num_seqs > 1 && num_seqs <= lin::kRanked &&
+                 blocks * num_seqs > 2 * kSMs;
+  p.seg_x = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+  p.seg_d = p.seg_x + (size_t)p.seq.slots * channels * d_state;
+  p.keep = initial_state && initial_state == final_state;
+  const cudaError_t err = dtype == GDN_F32
+                              ? launch_t<float>(p, d_state, groups, (cudaStream_t)stream)
+                              : launch_t<__nv_bfloat16>(p, d_state, groups, (cudaStream_t)stream);
+  return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -32,6 +32,9 @@ GDN_BETA_LOGITS = 1 << 3
 GDN_DEBUG_CHECKS = 1 << 4
 GDN_SEQ_SPLIT = 1 << 5
 GDN_NORM_SILU = 1 << 6
+GDN_DT_SOFTPLUS = 1 << 7
+GDN_CONV_SILU = 1 << 8
+GDN_ROPE_INTERLEAVED = 1 << 9
 # site codes of a GDN_ERR_DEVICE_CHECK record (gdn_check_record)
 DEBUG_SITES = {1: "q", 2: "k", 3: "v", 4: "g", 5: "beta", 6: "o", 7: "initial_state",
                8: "final_state", 9: "out_gate", 10: "tma_x"}
@@ -47,7 +50,10 @@ EXPORTED = ("gdn_fwd_workspace_size", "gdn_workspace_init", "gdn_fwd", "gdn_chec
             "gdn_lin_workspace_size", "gdn_lin_fwd", "gdn_lin_bwd", "gdn_lin_decode",
             "gdn_group_norm_workspace_size", "gdn_group_norm", "gdn_group_norm_bwd",
             "gdn_pages_workspace_size", "gdn_pages_copy", "gdn_pages_fork", "gdn_pages_free",
-            "gdn_pages_compact")
+            "gdn_pages_compact",
+            "gdn_ssm_workspace_size", "gdn_ssm_fwd", "gdn_ssm_bwd_workspace_size", "gdn_ssm_bwd",
+            "gdn_ssm_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd",
+            "gdn_conv_step", "gdn_qk_norm", "gdn_qk_norm_workspace_size", "gdn_qk_norm_bwd")
 # ... and include/gdn_debug.h (self-tests of the failure reporting).
 DEBUG_EXPORTED = ("gdn_debug_wait_timeout",)
 
@@ -142,7 +148,21 @@ def lib() -> ctypes.CDLL:
                                             vp, vp, vp, sz, vp]),
                     ("gdn_pages_free", st, [vp] * 3 + [i32] * 3 + [vp, i32] + [vp] * 4 + [sz, vp]),
                     ("gdn_pages_compact", st, [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp,
-                                               sz, vp])):
+                                               sz, vp]),
+                    ("gdn_ssm_workspace_size", sz, [i32] * 5),
+                    ("gdn_ssm_fwd", st, [vp] * 12 + [i32] * 6 + [i64] * 5 + [st, u32, vp, sz, vp]),
+                    ("gdn_ssm_bwd_workspace_size", sz, [i32] * 5),
+                    ("gdn_ssm_bwd", st, [vp] * 21 + [i32] * 6 + [i64] * 5 + [st, u32, vp, sz, vp]),
+                    ("gdn_ssm_step", st, [vp] * 12 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
+                    ("gdn_conv_fwd", st, [vp] * 7 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
+                    ("gdn_conv_workspace_size", sz, [i32] * 4),
+                    ("gdn_conv_bwd", st, [vp] * 11 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
+                    ("gdn_conv_step", st, [vp] * 6 + [i32] * 4 + [i64, st, u32, vp, sz, vp]),
+                    ("gdn_qk_norm", st, [vp] * 8 + [i32] * 6 + [i64] * 2 + [ctypes.c_float] * 2 +
+                     [st, u32, vp]),
+                    ("gdn_qk_norm_workspace_size", sz, [i32] * 3),
+                    ("gdn_qk_norm_bwd", st, [vp] * 12 + [i32] * 6 + [i64] * 2 +
+                     [ctypes.c_float] * 2 + [st, u32, vp, sz, vp])):
                 getattr(L, name).restype = res
                 getattr(L, name).argtypes = args
             _lib = L
@@ -1242,3 +1262,416 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
     if st or check:
         _done(w, st, check, ws, stream)
     return num_live, table_out, refs_out
+
+
+# ---------------------------------------------------------------------------
+# Selective state space scan, its short convolution, and the prologue of q and k
+# ---------------------------------------------------------------------------
+def _row_stride(where, name, t):
+    """Elements from one token row of ``t`` ``[B, T, ...]`` to the next (rows
+    contiguous, the rows of a batch one after the other); 0: packed."""
+    if t is None or t.is_contiguous():
+        return 0
+    B, T = t.shape[:2]
+    width, run = 1, True
+    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
+        run = run and (size == 1 or stride == width)
+        width *= size
+    s = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else width)
+    if not run or s < width or (B > 1 and T > 0 and t.stride(0) != T * s):
+        raise ValueError(f"{where}: {name} must have contiguous rows at one stride")
+    if s * t.element_size() % 16:
+        raise ValueError(f"{where}: the row stride of {name} must be a multiple of 16 bytes")
+    return s
+
+
+def _specs_check(where, device, rows, dense):
+    """``rows`` and ``dense``: name -> (tensor or None, shape, dtype); those of ``dense`` are
+    contiguous."""
+    ok = True
+    for t, shape, dtype in rows.values():
+        if t is not None and not (t.dtype == dtype and t.shape == shape and
+                                  t.get_device() == device and (device >= 0 or t.is_cuda)):
+            ok = False
+            break
+    if ok:
+        for t, shape, dtype in dense.values():
+            if t is not None and not (t.dtype == dtype and t.shape == shape and
+                                      t.get_device() == device and t.is_contiguous() and
+                                      (device >= 0 or t.is_cuda)):
+                ok = False
+                break
+    if ok:
+        return
+    for name, (t, _, _) in rows.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be on a CUDA device")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{where}: {name} must be on the device of the other tensors")
+    for name, (t, shape, dtype) in rows.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {str(dtype).split('.')[-1]}")
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} must be {list(shape)}")
+    _explain(where, device, {n: e[0] for n, e in dense.items()}, dense)
+
+
+def _sequences(where, B, cu_seqlens):
+    if cu_seqlens is None:
+        return B
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError(f"{where}: cu_seqlens must be int32 [N + 1]")
+    return cu_seqlens.shape[0] - 1
+
+
+def _ssm_specs(where, x, dt, A_log, b, c, D_skip, gate, dt_bias, h0, cu_seqlens):
+    """Sizes of a scan's call, and the specs of its inputs."""
+    if x.dim() != 3 or b.dim() != 4 or A_log.dim() != 2:
+        raise ValueError(f"{where}: x must be [B, T, D], b and c [B, T, G, S], A_log [D, S]")
+    B, T, D = x.shape
+    G, S = b.shape[2:]
+    dtype = x.dtype
+    _dtype_code(dtype)
+    N = _sequences(where, B, cu_seqlens)
+    rows = dict(x=(x, x.shape, dtype), dt=(dt, x.shape, dtype), b=(b, (B, T, G, S), dtype),
+                c=(c, (B, T, G, S), dtype), gate=(gate, x.shape, dtype))
+    dense = dict(A_log=(A_log, (D, S), _F32), D_skip=(D_skip, (D,), _F32),
+                 dt_bias=(dt_bias, (D,), _F32), initial_state=(h0, (N, D, S), _F32),
+                 cu_seqlens=(cu_seqlens, (N + 1,), _I32))
+    return (B, T, D, S, G, N), rows, dense
+
+
+@functools.lru_cache(maxsize=256)
+def gdn_ssm_workspace_size(num_seqs: int, seq_len: int, channels: int, d_state: int,
+                           groups: int = 1) -> int:
+    return int(lib().gdn_ssm_workspace_size(num_seqs, seq_len, channels, d_state, groups))
+
+
+@functools.lru_cache(maxsize=256)
+def gdn_ssm_bwd_workspace_size(num_seqs: int, seq_len: int, channels: int, d_state: int,
+                               groups: int = 1) -> int:
+    return int(lib().gdn_ssm_bwd_workspace_size(num_seqs, seq_len, channels, d_state, groups))
+
+
+def gdn_ssm_fwd(x, dt, A_log, b, c, initial_state=None, cu_seqlens=None, *, D_skip=None, gate=None,
+                dt_bias=None, dt_softplus=False, y=None, final_state=None,
+                output_final_state=True, workspace=None, stream=None, check=False):
+    """Selective state space scan through the C ABI: h_t = exp(delta A) h_{t-1} + delta x_t b_t,
+    y_t = (c_t . h_t + D_skip x_t) silu(gate_t), delta = dt + dt_bias (with ``dt_softplus``
+    the softplus of it), A = -exp(A_log).
+
+    x, dt, gate ``[B, T, D]``; b, c ``[B, T, G, S]`` (D / G channels share a group's; one
+    storage dtype, float32 or bfloat16; slices of projections are taken as they are: rows
+    contiguous, one stride between tokens); A_log ``[D, S]``, D_skip, dt_bias ``[D]`` fp32;
+    initial_state ``[N, D, S]`` fp32 or None; cu_seqlens int32 ``[N+1]`` on the device (then
+    B must be 1) or None.  ``y`` / ``final_state`` may be given (``final_state`` may be
+    ``initial_state``).  Returns ``(y, final_state)``.  With ``check=True`` the call
+    synchronises and raises on a device-side error."""
+    w = "gdn_ssm_fwd"
+    (B, T, D, S, G, N), rows, dense = _ssm_specs(w, x, dt, A_log, b, c, D_skip, gate, dt_bias,
+                                                 initial_state, cu_seqlens)
+    dense.update(y=(y, x.shape, x.dtype), final_state=(final_state, (N, D, S), _F32))
+    dev = x.get_device()
+    _specs_check(w, dev, rows, dense)
+    y = _like_new(stream, x) if y is None else y
+    if final_state is None and output_final_state:
+        final_state = _empty(stream, x, (N, D, S), _F32)
+    ws = _workspace(stream, x, workspace, gdn_ssm_workspace_size(N, T, D, S, G), check)
+    st = _on(w, dev)(
+        x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
+        _p(gate), _p(dt_bias), _p(initial_state), _p(cu_seqlens), y.data_ptr(), _p(final_state), B,
+        T, D, S, G, N, _row_stride(w, "x", x), _row_stride(w, "dt", dt), _row_stride(w, "b", b),
+        _row_stride(w, "c", c), _row_stride(w, "gate", gate), _CODES[x.dtype],
+        GDN_DT_SOFTPLUS if dt_softplus else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    if st or check:
+        _done(w, st, check, ws, stream)
+    return y, final_state
+
+
+def gdn_ssm_bwd(x, dt, A_log, b, c, d_y, initial_state=None, cu_seqlens=None, d_final_state=None, *,
+                D_skip=None, gate=None, dt_bias=None, dt_softplus=False, grads=None,
+                workspace=None, stream=None, check=False):
+    """Backward pass of ``gdn_ssm_fwd`` from its inputs and ``d_y`` (like y), ``d_final_state``
+    (``[N, D, S]`` fp32 or None).  Returns a dict ``dx, ddt, db, dc, dgate`` (storage dtype;
+    dgate None without a gate) and ``dA_log, dD_skip, ddt_bias, dh0`` (fp32; ``dD_skip`` and
+    ``ddt_bias`` None without the input); ``grads`` may supply them (one of the fp32 ones
+    left out is not computed)."""
+    w = "gdn_ssm_bwd"
+    (B, T, D, S, G, N), rows, dense = _ssm_specs(w, x, dt, A_log, b, c, D_skip, gate, dt_bias,
+                                                 initial_state, cu_seqlens)
+    given = grads or {}
+    dtype, wide, thin, state = x.dtype, x.shape, (B, T, G, S), (N, D, S)
+    kinds = dict(dx=(wide, dtype), ddt=(wide, dtype), db=(thin, dtype), dc=(thin, dtype),
+                 dgate=(wide, dtype), dA_log=((D, S), _F32), dD_skip=((D,), _F32),
+                 ddt_bias=((D,), _F32), dh0=(state, _F32))
+    dense.update(d_y=(d_y, wide, dtype), d_final_state=(d_final_state, state, _F32))
+    for n, t in given.items():
+        dense[n] = (t, *kinds[n])
+    dev = x.get_device()
+    _specs_check(w, dev, rows, dense)
+    if grads is None:
+        left = {n for n, t in (("dgate", gate), ("dD_skip", D_skip), ("ddt_bias", dt_bias))
+                if t is None}
+        grads = {n: None if n in left else _empty(stream, x, *kind) for n, kind in kinds.items()}
+    ws = _workspace(stream, x, workspace, gdn_ssm_bwd_workspace_size(N, T, D, S, G), check)
+    st = _on(w, dev)(
+        x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
+        _p(gate), _p(dt_bias), _p(initial_state), _p(cu_seqlens), d_y.data_ptr(),
+        _p(d_final_state), grads["dx"].data_ptr(), grads["ddt"].data_ptr(), _p(grads.get("dA_log")),
+        grads["db"].data_ptr(), grads["dc"].data_ptr(), _p(grads.get("dD_skip")),
+        _p(grads.get("dgate")), _p(grads.get("ddt_bias")), _p(grads.get("dh0")), B, T, D, S, G, N,
+        _row_stride(w, "x", x), _row_stride(w, "dt", dt), _row_stride(w, "b", b),
+        _row_stride(w, "c", c), _row_stride(w, "gate", gate), _CODES[dtype],
+        GDN_DT_SOFTPLUS if dt_softplus else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    if st or check:
+        _done(w, st, check, ws, stream)
+    return grads
+
+
+def _pool_check(where, device, name, t, shape, dtype, like=None):
+    """A pool ``[P, ...]`` of contiguous pages at one stride; returns (pages, stride)."""
+    if t.dtype != dtype or t.dim() != len(shape) + 1 or tuple(t.shape[1:]) != tuple(shape):
+        raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]} [P, "
+                         f"{', '.join(map(str, shape))}]")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be on a CUDA device")
+    if t.get_device() != device:
+        raise ValueError(f"{where}: {name} must be on the device of the other tensors")
+    P = t.shape[0]
+    stride = t.stride(0) if P > 1 else 0
+    if not (t.is_contiguous() or (P > 0 and t[0].is_contiguous())) or \
+            (like is not None and (like.shape[0] != P or (P > 1 and like.stride(0) != stride))):
+        raise ValueError(f"{where}: {name} must have contiguous pages at one stride")
+    return P, stride
+
+
+def gdn_ssm_step(x, dt, A_log, b, c, state, pages=None, *, D_skip=None, gate=None, dt_bias=None,
+                 dt_softplus=False, y=None, state_out=None, workspace=None, stream=None,
+                 check=False):
+    """One token per sequence of ``gdn_ssm_fwd``'s recurrence.
+
+    x, dt, gate ``[N, D]``; b, c ``[N, G, S]``; ``state`` ``[P, D, S]`` fp32: the pages of a
+    pool, each contiguous, at any stride (``pool[:, layer]``), or None (zeros; then give
+    ``state_out``).  ``pages`` int32 ``[N]``: the page of each sequence (-1: a padded row,
+    y = 0), or None (sequence n has page n).  The pages are updated in place unless
+    ``state_out`` (laid out like ``state``) is given.  Returns ``(y, state_out)``.  With
+    ``check=True`` the call synchronises and raises if a page number was out of range."""
+    w = "gdn_ssm_step"
+    if x.dim() != 2 or b.dim() != 3 or A_log.dim() != 2:
+        raise ValueError(f"{w}: x must be [N, D], b and c [N, G, S], A_log [D, S]")
+    N, D = x.shape
+    G, S = b.shape[1:]
+    dtype, dev = x.dtype, x.get_device()
+    _dtype_code(dtype)
+    if state_out is None:
+        if state is None:
+            raise ValueError(f"{w}: give state, or state_out")
+        state_out = state
+    _specs_check(w, dev, {}, dict(
+        x=(x, x.shape, dtype), dt=(dt, x.shape, dtype), b=(b, (N, G, S), dtype),
+        c=(c, (N, G, S), dtype), gate=(gate, x.shape, dtype), A_log=(A_log, (D, S), _F32),
+        D_skip=(D_skip, (D,), _F32), dt_bias=(dt_bias, (D,), _F32), pages=(pages, (N,), _I32),
+        y=(y, x.shape, dtype)))
+    P, stride = _pool_check(w, dev, "state_out", state_out, (D, S), _F32)
+    if state is not None and state is not state_out:
+        _pool_check(w, dev, "state", state, (D, S), _F32, state_out)
+    y = _like_new(stream, x) if y is None else y
+    if check or workspace is not None:
+        workspace = _workspace(stream, x, workspace, 256, check)
+    st = _on(w, dev)(
+        x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
+        _p(gate), _p(dt_bias), _p(state), state_out.data_ptr(), _p(pages), y.data_ptr(), N, D, S, G,
+        P, stride, _CODES[dtype], GDN_DT_SOFTPLUS if dt_softplus else 0, _p(workspace),
+        0 if workspace is None else _nbytes(workspace), _raw_stream(stream, dev))
+    if st or check:
+        _done(w, st, check, workspace, stream)
+    return y, state_out
+
+
+@functools.lru_cache(maxsize=256)
+def gdn_conv_workspace_size(num_seqs: int, seq_len: int, channels: int, taps: int) -> int:
+    return int(lib().gdn_conv_workspace_size(num_seqs, seq_len, channels, taps))
+
+
+def _conv_specs(where, x, w, bias, x_prev, cu_seqlens):
+    if x.dim() != 3 or w.dim() != 2:
+        raise ValueError(f"{where}: x must be [B, T, C], w [C, K]")
+    B, T, C = x.shape
+    K = w.shape[1]
+    _dtype_code(x.dtype)
+    N = _sequences(where, B, cu_seqlens)
+    return (B, T, C, K, N), dict(x=(x, x.shape, x.dtype)), dict(
+        w=(w, (C, K), _F32), bias=(bias, (C,), _F32), x_prev=(x_prev, (N, K - 1, C), x.dtype),
+        cu_seqlens=(cu_seqlens, (N + 1,), _I32))
+
+
+def gdn_conv_fwd(x, w, bias=None, x_prev=None, cu_seqlens=None, *, silu=True, y=None, x_tail=None,
+                 output_tail=True, workspace=None, stream=None, check=False):
+    """Short causal depthwise convolution with a bias and (``silu``) SiLU, through the C ABI.
+
+    x ``[B, T, C]`` (float32 or bfloat16; a slice of a projection is taken as it is: rows
+    contiguous, one stride between tokens); w ``[C, K]``, bias ``[C]`` fp32; x_prev
+    ``[N, K-1, C]``: the inputs before each sequence, or None (zeros); cu_seqlens int32
+    ``[N+1]`` on the device (then B must be 1) or None.  Returns ``(y, x_tail)``, x_tail
+    ``[N, K-1, C]`` the last inputs of each sequence (a page of ``gdn_conv_step``)."""
+    f = "gdn_conv_fwd"
+    (B, T, C, K, N), rows, dense = _conv_specs(f, x, w, bias, x_prev, cu_seqlens)
+    dense.update(y=(y, x.shape, x.dtype), x_tail=(x_tail, (N, K - 1, C), x.dtype))
+    dev = x.get_device()
+    _specs_check(f, dev, rows, dense)
+    y = _like_new(stream, x) if y is None else y
+    if x_tail is None and output_tail:
+        x_tail = _empty(stream, x, (N, K - 1, C), x.dtype)
+    ws = _workspace(stream, x, workspace, 256, check)
+    st = _on(f, dev)(
+        x.data_ptr(), w.data_ptr(), _p(bias), _p(x_prev), _p(cu_seqlens), y.data_ptr(), _p(x_tail),
+        B, T, C, K, N, _row_stride(f, "x", x), _CODES[x.dtype], GDN_CONV_SILU if silu else 0,
+        ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    if st or check:
+        _done(f, st, check, ws, stream)
+    return y, x_tail
+
+
+def gdn_conv_bwd(x, w, d_y, bias=None, x_prev=None, cu_seqlens=None, d_x_tail=None, *, silu=True,
+                 grads=None, workspace=None, stream=None, check=False):
+    """Backward pass of ``gdn_conv_fwd`` from its inputs and ``d_y`` (like y), ``d_x_tail``
+    (``[N, K-1, C]`` or None).  Returns a dict ``dx``, ``dx_prev`` (storage dtype; dx_prev
+    None without x_prev), ``dw``, ``dbias`` (fp32; dbias None without a bias); ``grads`` may
+    supply them (one left out is not computed)."""
+    f = "gdn_conv_bwd"
+    (B, T, C, K, N), rows, dense = _conv_specs(f, x, w, bias, x_prev, cu_seqlens)
+    given = grads or {}
+    kinds = dict(dx=(x.shape, x.dtype), dw=((C, K), _F32), dbias=((C,), _F32),
+                 dx_prev=((N, K - 1, C), x.dtype))
+    dense.update(d_y=(d_y, x.shape, x.dtype), d_x_tail=(d_x_tail, (N, K - 1, C), x.dtype))
+    for n, t in given.items():
+        dense[n] = (t, *kinds[n])
+    dev = x.get_device()
+    _specs_check(f, dev, rows, dense)
+    if grads is None:
+        left = {n for n, t in (("dbias", bias), ("dx_prev", x_prev)) if t is None}
+        grads = {n: None if n in left else _empty(stream, x, *kind) for n, kind in kinds.items()}
+    ws = _workspace(stream, x, workspace, gdn_conv_workspace_size(N, T, C, K), check)
+    st = _on(f, dev)(
+        x.data_ptr(), w.data_ptr(), _p(bias), _p(x_prev), _p(cu_seqlens), d_y.data_ptr(),
+        _p(d_x_tail), grads["dx"].data_ptr(), _p(grads.get("dw")), _p(grads.get("dbias")),
+        _p(grads.get("dx_prev")), B, T, C, K, N, _row_stride(f, "x", x), _CODES[x.dtype],
+        GDN_CONV_SILU if silu else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    if st or check:
+        _done(f, st, check, ws, stream)
+    return grads
+
+
+def gdn_conv_step(x, w, state, bias=None, pages=None, *, silu=True, y=None, workspace=None,
+                  stream=None, check=False):
+    """One token per sequence of ``gdn_conv_fwd``: x ``[N, C]``; ``state`` ``[P, K-1, C]`` in
+    x's dtype: pages with the last inputs of a sequence (``x_tail``), each contiguous, at any
+    stride, which move on by one in place; ``pages`` int32 ``[N]`` as in ``gdn_ssm_step``.
+    Returns ``(y, state)``."""
+    f = "gdn_conv_step"
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError(f"{f}: x must be [N, C], w [C, K]")
+    N, C = x.shape
+    K = w.shape[1]
+    dtype, dev = x.dtype, x.get_device()
+    _dtype_code(dtype)
+    _specs_check(f, dev, {}, dict(x=(x, x.shape, dtype), w=(w, (C, K), _F32),
+                                  bias=(bias, (C,), _F32), pages=(pages, (N,), _I32),
+                                  y=(y, x.shape, dtype)))
+    P, stride = _pool_check(f, dev, "state", state, (K - 1, C), dtype)
+    y = _like_new(stream, x) if y is None else y
+    if check or workspace is not None:
+        workspace = _workspace(stream, x, workspace, 256, check)
+    st = _on(f, dev)(
+        x.data_ptr(), w.data_ptr(), _p(bias), state.data_ptr(), _p(pages), y.data_ptr(), N, C, K, P,
+        stride, _CODES[dtype], GDN_CONV_SILU if silu else 0, _p(workspace),
+        0 if workspace is None else _nbytes(workspace), _raw_stream(stream, dev))
+    if st or check:
+        _done(f, st, check, workspace, stream)
+    return y, state
+
+
+@functools.lru_cache(maxsize=256)
+def gdn_qk_norm_workspace_size(batch: int, seq_len: int, head_dim: int) -> int:
+    return int(lib().gdn_qk_norm_workspace_size(batch, seq_len, head_dim))
+
+
+def _qk_specs(where, q, k, q_weight, k_weight, positions, inv_freq):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"{where}: q and k must be [B, T, H, D]")
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    _dtype_code(q.dtype)
+    R = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
+            raise ValueError(f"{where}: inv_freq must be float32 [R / 2], R at most the head size")
+        R = 2 * inv_freq.shape[0]
+    elif positions is not None:
+        raise ValueError(f"{where}: positions without inv_freq")
+    rows = dict(q=(q, q.shape, q.dtype), k=(k, (B, T, Hk, D), q.dtype))
+    dense = dict(q_weight=(q_weight, (D,), _F32), k_weight=(k_weight, (D,), _F32),
+                 positions=(positions, (B, T), _I32), inv_freq=(inv_freq, (R // 2,), _F32))
+    return (B, T, Hq, Hk, D, R), rows, dense
+
+
+def gdn_qk_norm(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, q_scale=1.0,
+                eps=1e-6, l2norm=False, interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of each head of q ``[B, T, Hq, D]`` and k ``[B, T, Hk, D]`` (root mean square, or
+    l2 with ``l2norm``; weights ``[D]`` fp32 or None) and the rotation of its first R = 2
+    len(inv_freq) elements by positions x inv_freq, through the C ABI.
+
+    Slices of one projection are taken as they are (rows ``[H, D]`` contiguous, one stride
+    between tokens).  positions int32 ``[B, T]`` or None (0 .. T-1); inv_freq fp32
+    ``[R/2]`` or None (no rotation); pairs are R/2 apart, or neighbours with
+    ``interleaved``.  q is multiplied by ``q_scale``.  Returns ``(q_out, k_out)``, densely
+    packed."""
+    f = "gdn_qk_norm"
+    (B, T, Hq, Hk, D, R), rows, dense = _qk_specs(f, q, k, q_weight, k_weight, positions, inv_freq)
+    dense.update(q_out=(q_out, q.shape, q.dtype), k_out=(k_out, k.shape, q.dtype))
+    dev = q.get_device()
+    _specs_check(f, dev, rows, dense)
+    q_out = _empty(stream, q, q.shape, q.dtype) if q_out is None else q_out
+    k_out = _empty(stream, q, k.shape, q.dtype) if k_out is None else k_out
+    st = _on(f, dev)(
+        q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
+        q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hk, D, R, _row_stride(f, "q", q),
+        _row_stride(f, "k", k), q_scale, eps, _CODES[q.dtype],
+        (GDN_QK_L2NORM if l2norm else 0) | (GDN_ROPE_INTERLEAVED if interleaved else 0),
+        _raw_stream(stream, dev))
+    if st:
+        raise GdnError(st, f)
+    return q_out, k_out
+
+
+def gdn_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, positions=None,
+                    inv_freq=None, *, q_scale=1.0, eps=1e-6, l2norm=False, interleaved=False,
+                    grads=None, workspace=None, stream=None):
+    """Backward pass of ``gdn_qk_norm`` from its inputs and the gradients of its outputs
+    (densely packed).  Returns a dict ``dq, dk`` (storage dtype) and ``dq_weight,
+    dk_weight`` (fp32; None without the weight); ``grads`` may supply them (a weight's left
+    out is not computed)."""
+    f = "gdn_qk_norm_bwd"
+    (B, T, Hq, Hk, D, R), rows, dense = _qk_specs(f, q, k, q_weight, k_weight, positions, inv_freq)
+    given = grads or {}
+    kinds = dict(dq=(q.shape, q.dtype), dk=(k.shape, q.dtype), dq_weight=((D,), _F32),
+                 dk_weight=((D,), _F32))
+    dense.update(d_q_out=(d_q_out, q.shape, q.dtype), d_k_out=(d_k_out, k.shape, q.dtype))
+    for n, t in given.items():
+        dense[n] = (t, *kinds[n])
+    dev = q.get_device()
+    _specs_check(f, dev, rows, dense)
+    if grads is None:
+        left = {n for n, t in (("dq_weight", q_weight), ("dk_weight", k_weight)) if t is None}
+        grads = {n: None if n in left else _empty(stream, q, *kind) for n, kind in kinds.items()}
+    ws = _workspace(stream, q, workspace, gdn_qk_norm_workspace_size(B, T, D), False)
+    st = _on(f, dev)(
+        q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
+        d_q_out.data_ptr(), d_k_out.data_ptr(), grads["dq"].data_ptr(), grads["dk"].data_ptr(),
+        _p(grads.get("dq_weight")), _p(grads.get("dk_weight")), B, T, Hq, Hk, D, R,
+        _row_stride(f, "q", q), _row_stride(f, "k", k), q_scale, eps, _CODES[q.dtype],
+        (GDN_QK_L2NORM if l2norm else 0) | (GDN_ROPE_INTERLEAVED if interleaved else 0),
+        ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+    if st:
+        raise GdnError(st, f)
+    return grads
