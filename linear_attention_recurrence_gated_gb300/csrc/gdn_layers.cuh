@@ -101,6 +101,41 @@ __device__ __forceinline__ float rcp(float x) {
 // 1 / (1 + exp(-z)); exact limits for infinite z.
 __device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
 
+// 1 / (1 + exp(-g)) of two values.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  float a, b;
+  unpk(mul2(g, pk(-kLog2e, -kLog2e)), a, b);
+  unpk(add2(pk(ex2(a), ex2(b)), pk(1.f, 1.f)), a, b);
+  return pk(rcp(a), rcp(b));
+}
+// Four consecutive elements: 8 bytes of bf16, 16 of fp32.
+template <typename T> struct Raw4;
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 a;
+  __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint2 *>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16 *p) const { *reinterpret_cast<uint2 *>(p) = a; }
+  __device__ __forceinline__ void get(uint64_t (&v)[2]) const {
+    v[0] = pk(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u));
+    v[1] = pk(__uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
+  }
+  __device__ __forceinline__ void set(const uint64_t (&v)[2]) {   // rounds to nearest even
+    float x, y, z, w;
+    unpk(v[0], x, y);
+    unpk(v[1], z, w);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y), i = __floats2bfloat162_rn(z, w);
+    a = make_uint2(*reinterpret_cast<const uint32_t *>(&h), *reinterpret_cast<const uint32_t *>(&i));
+  }
+};
+template <> struct Raw4<float> {
+  ulonglong2 a;
+  __device__ __forceinline__ void zero() { a = make_ulonglong2(0, 0); }
+  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const ulonglong2 *>(p); }
+  __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<ulonglong2 *>(p) = a; }
+  __device__ __forceinline__ void get(uint64_t (&v)[2]) const { v[0] = a.x; v[1] = a.y; }
+  __device__ __forceinline__ void set(const uint64_t (&v)[2]) { a = make_ulonglong2(v[0], v[1]); }
+};
+
 // The sequences of a call: rows of seq_len tokens, or packed ones between offsets in
 // device memory.
 struct Sequences {

@@ -8,11 +8,14 @@
 //   backward: du = s (pairs turned back), dw = sum du x r, g = du w,
 //             dx = r (g - x r^2 mean(x g))
 //
-// Bound by HBM bandwidth: every element is read and written once.  A head takes D / 8
-// lanes with eight elements each, four rows of a thread are on their way together; the
-// cosines and sines of a token are computed once, in shared memory, for all of its heads.
-// An angle's whole turns are taken off exactly: inv_freq / 2 pi is held as a fraction of
-// 2^64, whose product with the position drops them by overflowing.
+// Bound by HBM bandwidth: every element is read and written once.  A head takes D / 16
+// lanes with sixteen elements each: two runs of eight columns, whose pairs of the rotation
+// are both in the thread (columns 8 v and R / 2 + 8 v for pairs R / 2 apart), so that
+// packed arithmetic turns them without exchanges between lanes; where R / 2 is not a
+// multiple of eight a row goes through shared memory.  The cosines and sines of a token
+// are computed once, in shared memory, for all of its heads of q, or of k: a CTA takes one
+// of the two.  An angle's whole turns are taken off exactly: inv_freq / 2 pi is held as a
+// fraction of 2^64, whose product with the position drops them by overflowing.
 #include "gdn_launch.cuh"
 #include "gdn_layers.cuh"
 
@@ -23,37 +26,59 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;       // rows of a thread that are loaded together
+// Rows of a thread that are loaded together.
+template <typename T, bool BACK> constexpr int kRowsOf = BACK || sizeof(T) == 4 ? 1 : 2;
 constexpr int kTokens = 8;     // most tokens of a CTA at a time
 constexpr int kMaxHalf = 128;  // most pairs of a head
 
+// q, or k.
+struct Side {
+  const void *x, *g;      // rows; gradients of the outputs (densely packed)
+  void *out;              // densely packed
+  const float *w;
+  float *dw;
+  int64_t stride;
+  int32_t heads, ctas;    // CTAs that take this side
+  float scale;
+};
 struct Params {
-  const void *q, *k, *dq_in, *dk_in;
-  const float *wq, *wk, *inv_freq;
+  Side side[2];
+  const float *inv_freq;
   const int32_t *positions;
-  void *oq, *ok;          // outputs, or dq and dk
-  float *part, *dwq, *dwk;
-  int64_t sq, sk, tokens, seq_len;
-  int32_t Hq, Hk, D, R, tile, parts;
-  float eps, scale;
+  float *part;
+  int64_t tokens, seq_len;
+  int32_t D, R, pitch, tile;   // pitch: R / 2 rounded up to 4
+  float eps;
   bool l2, interleaved;
 };
 
-// cos and sin of positions x inv_freq for the tile's tokens, [token][R / 2].
-__device__ __forceinline__ void turn_table(const Params &p, int64_t tok0, int cnt,
-                                           const uint64_t *freq, float2 *table) {
-  const int half = p.R / 2;
-  for (int i = threadIdx.x; i < cnt * half; i += kThreads) {
-    const int64_t tok = tok0 + i / half;
+// cos and sin of r, |r| <= pi / 4, by the polynomials that minimise the largest error
+// (2e-9 and 4e-10 there, far below the rounding of an fp32 result).
+__device__ __forceinline__ void cos_sin(float r, float &c, float &s) {
+  const float q = r * r;
+  s = fmaf(fmaf(fmaf(-0.00019495601009111851f, q, 0.00833197869360447f), q, -0.16666650772094727f), q * r, r);
+  c = fmaf(fmaf(fmaf(fmaf(2.4390410544583574e-05f, q, -0.0013886763481423259f), q, 0.04166662320494652f), q, -0.5f), q, 1.f);
+}
+// Cosines and sines of positions x inv_freq for the tile's tokens: [token][2][pitch].
+__device__ __forceinline__ void turn_table(const Params &p, int64_t tok0, int cnt, int lanes,
+                                           const uint64_t *freq, float *table) {
+  const int half = p.R / 2;   // lanes: the power of two that holds it, at most 256
+  for (int t = threadIdx.x / lanes; t < cnt; t += kThreads / lanes) {
+    const int f = threadIdx.x & (lanes - 1);
+    if (f >= half) break;
+    const int64_t tok = tok0 + t;
     const int64_t pos = p.positions ? (int64_t)p.positions[tok] : tok % p.seq_len;
-    const uint64_t turns = (uint64_t)pos * freq[i % half];   // of 2^64; whole turns overflow
+    // of 2^32; whole turns overflow
+    const uint32_t turns = (uint32_t)(((uint64_t)pos * freq[f]) >> 32);
     // to the nearest quarter turn, whose cosine and sine are exact, and the rest
-    const uint32_t quarter = (uint32_t)((turns + (1ull << 61)) >> 62) & 3u;
-    const int64_t rest = (int64_t)(turns - ((uint64_t)quarter << 62));
+    const uint32_t quarter = (turns + (1u << 29)) >> 30;   // (0 .. 4, 4 being none)
+    const int32_t rest = (int32_t)(turns - (quarter << 30));
     float c, s;
-    sincospif((float)rest * 0x1p-63f, &s, &c);   // half turns
+    cos_sin((float)rest * 1.4629180792671596e-9f, c, s);   // 2 pi / 2^32
     const float a = quarter & 1 ? -s : c, b = quarter & 1 ? c : s;
-    table[i] = quarter & 2 ? make_float2(-a, -b) : make_float2(a, b);
+    float *at = table + t * 2 * p.pitch + f;
+    at[0] = quarter & 2 ? -a : a;
+    at[p.pitch] = quarter & 2 ? -b : b;
   }
 }
 // The frequencies as fractions of a turn, whole turns left out.
@@ -72,217 +97,299 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// The pairs of eight elements u from column 8 v turned by the table's angles (back: the
-// other way).  All lanes of the warp together.
-template <int LR>
-__device__ __forceinline__ void turn(const Params &p, const float2 *cs, float *row, int v, bool back,
-                                     float (&u)[8]) {
+// How the pairs lie: R / 2 apart with R / 2 a multiple of eight, neighbours, or otherwise
+// (no rotation at all, too).
+enum Mode { kApart, kNext, kOther };
+
+// A thread's columns: c[0] .. c[0] + 7 and c[1] .. c[1] + 7, where on[].
+struct Cols {
+  int c[2];
+  bool on[2];
+  bool split;    // pairs (c[0] + i, c[1] + i)
+};
+template <Mode M>
+__device__ __forceinline__ Cols cols_of(const Params &p, int v) {
+  if (M == kApart && 16 * v < p.R) return {{8 * v, p.R / 2 + 8 * v}, {true, true}, true};
+  return {{16 * v, 16 * v + 8}, {16 * v < p.D, 16 * v + 8 < p.D}, false};
+}
+__device__ __forceinline__ void load_pairs(const float *at, uint64_t (&v)[4]) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(at)[0];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(at)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
+// The thread's pairs turned by the token's angles cs (BACK: the other way).  All lanes of
+// the warp together.
+template <Mode M, bool BACK>
+__device__ __forceinline__ void turn(const Params &p, const Cols &col, const float *cs, float *row,
+                                     uint64_t (&u)[2][4]) {
+  constexpr float sign = BACK ? -1.f : 1.f;
   const int half = p.R / 2;
-  const float sign = back ? -1.f : 1.f;
-  if (p.interleaved) {
+  if constexpr (M == kNext) {   // a column and its neighbour
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      if (col.c[g] >= p.R) continue;
+      const float4 x = *reinterpret_cast<const float4 *>(cs + col.c[g] / 2);
+      const float4 y = *reinterpret_cast<const float4 *>(cs + p.pitch + col.c[g] / 2);
+      const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (col.c[g] + 2 * m >= p.R) continue;
+        float a, b;
+        unpk(u[g][m], a, b);
+        const float s = sign * ys[m];
+        u[g][m] = pk(fmaf(a, xs[m], -(b * s)), fmaf(a, s, b * xs[m]));
+      }
+    }
+  } else if constexpr (M == kApart) {
+    if (!col.split) return;
+    uint64_t x[4], y[4];
+    load_pairs(cs + col.c[0], x);
+    load_pairs(cs + p.pitch + col.c[0], y);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int i = 4 * v + m;
-      if (i >= half) continue;
-      const float2 t = cs[i];
-      const float a = u[2 * m], b = u[2 * m + 1], s = sign * t.y;
-      u[2 * m] = fmaf(a, t.x, -(b * s));
-      u[2 * m + 1] = fmaf(a, s, b * t.x);
-    }
-  } else if (half % 8 == 0) {   // the partners of a lane's elements are all in one other lane
-    const int w = half / 8, lane = threadIdx.x & 31, first = lane - v;
-    const bool low = v < w, on = v < 2 * w;
-    const int from = on ? first + (low ? v + w : v - w) : lane;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float o = __shfl_sync(0xffffffffu, u[j], from);
-      if (!on) continue;
-      const float2 t = cs[8 * (low ? v : v - w) + j];
-      const float s = sign * t.y;
-      u[j] = low ? fmaf(u[j], t.x, -(o * s)) : fmaf(o, s, u[j] * t.x);
+      const uint64_t a = u[0][m], b = u[1][m], neg = mul2(y[m], pk(-1.f, -1.f));
+      u[0][m] = fma2(b, BACK ? y[m] : neg, mul2(a, x[m]));
+      u[1][m] = fma2(a, BACK ? neg : y[m], mul2(b, x[m]));
     }
   } else {
-    float4 *at = reinterpret_cast<float4 *>(row + 8 * v);
-    at[0] = make_float4(u[0], u[1], u[2], u[3]);
-    at[1] = make_float4(u[4], u[5], u[6], u[7]);
-    __syncwarp();
+    if (p.R == 0) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = 8 * v + j;
-      if (i >= p.R) continue;
-      const bool low = i < half;
-      const float o = row[low ? i + half : i - half];
-      const float2 t = cs[low ? i : i - half];
-      const float s = sign * t.y;
-      u[j] = low ? fmaf(u[j], t.x, -(o * s)) : fmaf(o, s, u[j] * t.x);
+    for (int g = 0; g < 2; ++g) {
+      ulonglong2 *at = reinterpret_cast<ulonglong2 *>(row + col.c[g]);
+      at[0] = make_ulonglong2(u[g][0], u[g][1]);
+      at[1] = make_ulonglong2(u[g][2], u[g][3]);
     }
     __syncwarp();
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float w[2];
+        unpk(u[g][m], w[0], w[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = col.c[g] + 2 * m + j;
+          if (i >= p.R) continue;
+          const bool low = i < half;
+          const float o = row[low ? i + half : i - half];
+          const float x = cs[low ? i : i - half], s = sign * cs[p.pitch + (low ? i : i - half)];
+          w[j] = low ? fmaf(w[j], x, -(o * s)) : fmaf(o, s, w[j] * x);
+        }
+        u[g][m] = pk(w[0], w[1]);
+      }
+    __syncwarp();
   }
 }
-
-// Rows of a tile: token by token, its heads of q, then of k.
-struct Row {
-  bool on, key;
-  int tok, head;
-};
-__device__ __forceinline__ Row row_of(const Params &p, int r, int rows) {
-  const int H = p.Hq + p.Hk, tok = r / H, h = r - tok * H;
-  return {r < rows, h >= p.Hq, tok, h >= p.Hq ? h - p.Hq : h};
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw8<T> &r, uint64_t (&u)[4]) {
+  float v[8];
+  r.get(v);
+#pragma unroll
+  for (int m = 0; m < 4; ++m) u[m] = pk(v[2 * m], v[2 * m + 1]);
 }
 
-template <typename T, int LR, bool BACK>
-__global__ void __launch_bounds__(kThreads)
+template <typename T, int LR, Mode M, bool BACK>
+__global__ void __launch_bounds__(kThreads, BACK ? 2 : 3)
 gdn_qk_norm_kernel(const Params p) {
-  constexpr int RG = kThreads / LR;   // rows side by side
-  __shared__ float2 table[kTokens * kMaxHalf];
-  __shared__ __align__(16) float rows_buf[RG * LR * 8];
+  constexpr int RG = kThreads / LR, kRows = kRowsOf<T, BACK>;   // rows side by side, in turn
+  __shared__ __align__(16) float table[kTokens * 2 * kMaxHalf];
+  __shared__ __align__(16) float rows_buf[RG * LR * 16];
   __shared__ uint64_t freq[kMaxHalf];
-  const int tid = threadIdx.x, v = tid % LR, rg = tid / LR;
-  const bool von = 8 * v < p.D;
-  float *buf = rows_buf + rg * LR * 8;
-  float w[2][8];
-  float own[BACK ? 2 : 1][8] = {}, all[BACK ? 2 : 1][8] = {};   // sums for the weights
+  const int tid = threadIdx.x, rg = tid / LR, which = (int)blockIdx.x >= p.side[0].ctas;
+  const Side &s = p.side[which];
+  const Cols col = cols_of<M>(p, tid % LR);
+  // (lanes without columns read the first ones, and store nothing)
+  const int c0 = col.on[0] ? col.c[0] : 0, c1 = col.on[1] ? col.c[1] : 0;
+  float *buf = rows_buf + rg * LR * 16;
+  if (BACK) let_second();
+  uint64_t w[2][4], own[2][4] = {}, all[2][4] = {};   // own, all: sums for the weight
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w[0][j] = von && p.wq ? p.wq[8 * v + j] : 1.f;
-    w[1][j] = von && p.wk ? p.wk[8 * v + j] : 1.f;
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int c = (g ? c1 : c0) + 2 * m;
+      w[g][m] = s.w ? pk(s.w[c], s.w[c + 1]) : pk(1.f, 1.f);
+      w[g][m] = mul2(w[g][m], pk(s.scale, s.scale));
+    }
+  int lanes = 32;
+  if (p.R) {
+    load_freq(p, freq);
+    while (lanes < p.R / 2) lanes *= 2;
   }
-  if (p.R) load_freq(p, freq);
   const float over = p.l2 ? 1.f : 1.f / (float)p.D;
+  const uint32_t magic = 0xffffffffu / s.heads + 1;   // 2^32 / heads, rounded up: rows < 2^16
   const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
+  const int width = s.heads * p.D;
   int summed = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+  for (int64_t tile = blockIdx.x - (which ? p.side[0].ctas : 0); tile < tiles; tile += s.ctas) {
     const int64_t tok0 = tile * p.tile;
-    const int cnt = (int)(p.tokens - tok0 < p.tile ? p.tokens - tok0 : p.tile);
-    const int rows = cnt * (p.Hq + p.Hk);
-    __syncthreads();   // the last tile's table has been read
-    if (p.R) turn_table(p, tok0, cnt, freq, table);
-    __syncthreads();
-    for (int r0 = 0; r0 < rows; r0 += kRows * RG) {
-      Raw8<T> x[kRows], d[BACK ? kRows : 1];
+    const int cnt = (int)(p.tokens - tok0 < p.tile ? p.tokens - tok0 : p.tile), rows = cnt * s.heads;
+    const T *xs = static_cast<const T *>(s.x) + tok0 * s.stride;
+    const T *gs = static_cast<const T *>(s.g) + tok0 * width;
+    T *out = static_cast<T *>(s.out) + tok0 * width;
+    Raw8<T> x[kRows][2], d[BACK ? kRows : 1][2];
+    int tok[kRows], at[kRows];
+    const auto fetch = [&](int r0) {   // (rows behind the last: the last)
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const Row row = row_of(p, r0 + i * RG + rg, rows);
-        x[i].zero();
-        if (BACK) d[i].zero();
-        if (!row.on || !von) continue;
-        const int64_t tok = tok0 + row.tok;
-        x[i].load(row.key ? static_cast<const T *>(p.k) + tok * p.sk + row.head * p.D + 8 * v
-                          : static_cast<const T *>(p.q) + tok * p.sq + row.head * p.D + 8 * v);
-        if (BACK)
-          d[i].load(row.key
-                        ? static_cast<const T *>(p.dk_in) + (tok * p.Hk + row.head) * p.D + 8 * v
-                        : static_cast<const T *>(p.dq_in) + (tok * p.Hq + row.head) * p.D + 8 * v);
+        const int r = r0 + i * RG < rows ? r0 + i * RG : rows - 1;
+        tok[i] = s.heads == 1 ? r : (int)__umulhi((uint32_t)r, magic);
+        const int head = (r - tok[i] * s.heads) * p.D;
+        at[i] = tok[i] * width + head;
+        const T *from = xs + tok[i] * s.stride + head;
+        x[i][0].load(from + c0);
+        x[i][1].load(from + c1);
+        if (BACK) {
+          d[i][0].load(gs + at[i] + c0);
+          d[i][1].load(gs + at[i] + c1);
+        }
       }
+    };
+    fetch(rg);   // on its way while the table is made
+    if (p.R) {
+      __syncthreads();   // the last tile's table has been read
+      turn_table(p, tok0, cnt, lanes, freq, table);
+      __syncthreads();
+    }
+    for (int base = 0; base < rows; base += kRows * RG) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        if (r0 + i * RG >= rows) break;   // the same for the whole CTA
-        const Row row = row_of(p, r0 + i * RG + rg, rows);
-        const float2 *cs = table + (row.on ? row.tok : 0) * (p.R / 2);
-        float xv[8], u[8], ss = 0.f;
-        x[i].get(xv);
+        if (base + i * RG >= rows) break;   // the same for the whole CTA
+        const bool on = base + i * RG + rg < rows;
+        const float *cs = table + tok[i] * 2 * p.pitch;
+        T *to = out + at[i];
+        uint64_t xv[2][4], u[2][4], ss = 0ull;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(xv[j], xv[j], ss);
-        const float sq = row_sum<LR>(ss);
-        const float r = row.on ? rsqrtf(fmaf(sq, over, p.eps)) : 0.f;
-        const float scale = row.key ? 1.f : p.scale;
+        for (int g = 0; g < 2; ++g) {
+          unpack(x[i][g], xv[g]);
+          if (LR * 16 != p.D && !col.on[g]) xv[g][0] = xv[g][1] = xv[g][2] = xv[g][3] = 0ull;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) ss = fma2(xv[g][m], xv[g][m], ss);
+          if (BACK) unpack(d[i][g], u[g]);
+        }
+        if (i == kRows - 1 && base + kRows * RG < rows) fetch(base + kRows * RG + rg);
+        float lo, hi;
+        unpk(ss, lo, hi);
+        const float r = rsqrtf(fmaf(row_sum<LR>(lo + hi), over, p.eps));
+        const uint64_t rr = pk(r, r);
         if constexpr (!BACK) {
-          const float f = r * scale;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = xv[j] * f * (row.key ? w[1][j] : w[0][j]);
-          if (p.R) turn<LR>(p, cs, buf, v, false, u);
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) u[g][m] = mul2(mul2(xv[g][m], rr), w[g][m]);
+          turn<M, BACK>(p, col, cs, buf, u);
         } else {
-          d[i].get(u);
-          if (p.R) turn<LR>(p, cs, buf, v, true, u);
-          float m = 0.f;
+          turn<M, BACK>(p, col, cs, buf, u);
+          uint64_t m2 = 0ull;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            u[j] *= scale;
-            const float t = u[j] * xv[j] * r;
-            if (row.key) own[1][j] += t;
-            else own[0][j] += t;
-            u[j] *= row.key ? w[1][j] : w[0][j];
-            m = fmaf(xv[j], u[j], m);
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const uint64_t t = mul2(u[g][m], xv[g][m]);
+              if (on) own[g][m] = fma2(t, rr, own[g][m]);
+              m2 = fma2(t, w[g][m], m2);
+            }
+          unpk(m2, lo, hi);
+          const float f = -(row_sum<LR>(lo + hi) * over * r * r);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              u[g][m] = mul2(rr, fma2(xv[g][m], pk(f, f), mul2(u[g][m], w[g][m])));
+        }
+        if (on)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float v[8];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) unpk(u[g][m], v[2 * m], v[2 * m + 1]);
+            Raw8<T> o;
+            o.set(v);
+            if (col.on[g]) o.store(to + (g ? c1 : c0));
           }
-          m = row_sum<LR>(m) * over * r * r;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = r * fmaf(-xv[j], m, u[j]);
-        }
-        if (row.on && von) {
-          const int64_t tok = tok0 + row.tok;
-          Raw8<T> out;
-          out.set(u);
-          out.store(row.key ? static_cast<T *>(p.ok) + (tok * p.Hk + row.head) * p.D + 8 * v
-                            : static_cast<T *>(p.oq) + (tok * p.Hq + row.head) * p.D + 8 * v);
-        }
       }
-      if (BACK && ++summed == 16) {   // at most 64 rows in one run of an accumulator
+      if (BACK && ++summed == 64 / kRows) {   // at most 64 rows in one run of an accumulator
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          all[0][j] += own[0][j];
-          all[BACK][j] += own[BACK][j];
-          own[0][j] = own[BACK][j] = 0.f;
-        }
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            all[g][m] = add2(all[g][m], own[g][m]);
+            own[g][m] = 0ull;
+          }
         summed = 0;
       }
     }
   }
   if constexpr (BACK) {   // the CTA's sums, in the order of its rows of threads
+    __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      __syncthreads();
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) buf[8 * v + j] = all[s][j] + own[s][j];
-      __syncthreads();
-      for (int c = tid; c < p.D; c += kThreads) {
-        float sum = 0.f;
-        for (int i = 0; i < RG; ++i) sum += rows_buf[i * LR * 8 + c];
-        p.part[((int64_t)blockIdx.x * 2 + s) * p.D + c] = sum;
-      }
+      for (int m = 0; m < 4; ++m)   // (du carries q's scale)
+        *reinterpret_cast<uint64_t *>(buf + col.c[g] + 2 * m) =
+            mul2(add2(all[g][m], own[g][m]), pk(s.scale, s.scale));
+    __syncthreads();
+    for (int c = tid; c < p.D; c += kThreads) {
+      float sum = 0.f;
+      for (int i = 0; i < RG; ++i) sum += rows_buf[i * LR * 16 + c];
+      p.part[(int64_t)blockIdx.x * p.D + c] = sum;
     }
   }
 }
 
-// The weights' gradients: 32 columns a CTA, its 32 warps over the partial sums.
+// The weights' gradients: 32 columns of q's or k's a CTA, its 32 warps over the partial sums.
 __global__ void __launch_bounds__(1024) gdn_qk_weights_kernel(const Params p) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  const int n = 2 * p.D;
+  const Side &s = p.side[blockIdx.y];
+  wait_first();
   float sum = 0.f;
-  if (c < n)
-    for (int i = warp; i < p.parts; i += 32) sum += p.part[(int64_t)i * n + c];
+  if (c < p.D) {
+    const float *part = p.part + (blockIdx.y ? (int64_t)p.side[0].ctas * p.D : 0) + c;
+#pragma unroll 4
+    for (int i = warp; i < s.ctas; i += 32) sum += part[(int64_t)i * p.D];
+  }
   red[warp][lane] = sum;
   __syncthreads();
   if (warp) return;
   sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) sum += red[i][lane];
-  if (c >= n) return;
-  float *out = c < p.D ? p.dwq : p.dwk;
-  if (out) out[c < p.D ? c : c - p.D] = sum;
+  if (c < p.D && s.dw) s.dw[c] = sum;
 }
 
-// Tokens of a tile and CTAs: one token where there are few.
+// Tokens of a tile (one where there are few) and CTAs, those that fit on the GPU, in
+// proportion to the heads.
 struct Grid {
   int tile;
-  int64_t ctas;
+  int64_t ctas[2];
 };
-Grid grid_of(int64_t tokens, bool back) {
+Grid grid_of(int64_t tokens, int64_t Hq, int64_t Hk, bool back) {
   Grid g;
+  const int64_t fit = (back ? 2 : 3) * kSMs;
   g.tile = tokens >= 2 * kTokens * kSMs ? kTokens : 1;
-  const int64_t tiles = (tokens + g.tile - 1) / g.tile, most = (back ? 3 : 5) * kSMs;
-  g.ctas = tiles < most ? tiles : most;
+  const int64_t tiles = (tokens + g.tile - 1) / g.tile;
+  int64_t q = fit * Hq / (Hq + Hk);
+  q = q < 1 ? 1 : q > fit - 1 ? fit - 1 : q;
+  const int64_t k = fit - q;
+  g.ctas[0] = q < tiles ? q : tiles;
+  g.ctas[1] = k < tiles ? k : tiles;
   return g;
 }
 
-template <typename T, bool BACK>
-cudaError_t launch_t(const Params &p, int64_t ctas, cudaStream_t stream) {
-  const unsigned n = (unsigned)ctas;
-  if (p.D <= 32) gdn_qk_norm_kernel<T, 4, BACK><<<n, kThreads, 0, stream>>>(p);
-  else if (p.D <= 64) gdn_qk_norm_kernel<T, 8, BACK><<<n, kThreads, 0, stream>>>(p);
-  else if (p.D <= 128) gdn_qk_norm_kernel<T, 16, BACK><<<n, kThreads, 0, stream>>>(p);
-  else gdn_qk_norm_kernel<T, 32, BACK><<<n, kThreads, 0, stream>>>(p);
+template <typename T, Mode M, bool BACK>
+cudaError_t launch_m(const Params &p, cudaStream_t stream) {
+  const unsigned n = (unsigned)(p.side[0].ctas + p.side[1].ctas);
+  if (p.D <= 64) gdn_qk_norm_kernel<T, 4, M, BACK><<<n, kThreads, 0, stream>>>(p);
+  else if (p.D <= 128) gdn_qk_norm_kernel<T, 8, M, BACK><<<n, kThreads, 0, stream>>>(p);
+  else gdn_qk_norm_kernel<T, 16, M, BACK><<<n, kThreads, 0, stream>>>(p);
   return taken(cudaGetLastError());
+}
+template <typename T, bool BACK>
+cudaError_t launch_t(const Params &p, cudaStream_t stream) {
+  if (p.R && p.interleaved) return launch_m<T, kNext, BACK>(p, stream);
+  if (p.R && p.R % 16 == 0) return launch_m<T, kApart, BACK>(p, stream);
+  return launch_m<T, kOther, BACK>(p, stream);
 }
 
 gdn_status check_sizes(int32_t batch, int32_t seq_len, int32_t Hq, int32_t Hk, int32_t D, int32_t R,
@@ -325,28 +432,30 @@ gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, cons
                        {positions, rows * 4}, {inv_freq, (size_t)rotary_dim * 2}};
   if (!apart(outs, ins)) return GDN_ERR_INVALID_ARG;
   Params p{};
-  p.q = q; p.k = k; p.wq = q_weight; p.wk = k_weight;
-  p.positions = positions; p.inv_freq = inv_freq;
-  p.oq = q_out; p.ok = k_out;
-  p.sq = sq; p.sk = sk;
+  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, false);
+  p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale};
+  p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f};
+  p.positions = positions;
+  p.inv_freq = inv_freq;
   p.tokens = (int64_t)rows;
   p.seq_len = seq_len;
-  p.Hq = q_heads; p.Hk = k_heads; p.D = head_dim; p.R = rotary_dim;
+  p.D = head_dim; p.R = rotary_dim;
+  p.pitch = (rotary_dim / 2 + 3) / 4 * 4;
   p.eps = eps;
-  p.scale = q_scale;
   p.l2 = flags & GDN_QK_L2NORM;
   p.interleaved = flags & GDN_ROPE_INTERLEAVED;
-  const Grid g = grid_of(p.tokens, false);
   p.tile = g.tile;
   cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t err = dtype == GDN_F32 ? launch_t<float, false>(p, g.ctas, s)
-                                           : launch_t<__nv_bfloat16, false>(p, g.ctas, s);
+  const cudaError_t err = dtype == GDN_F32 ? launch_t<float, false>(p, s)
+                                           : launch_t<__nv_bfloat16, false>(p, s);
   return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_qk_norm_workspace_size(int32_t batch, int32_t seq_len, int32_t head_dim) {
   if (batch <= 0 || seq_len < 0 || head_dim <= 0) return 0;
-  return (size_t)gdn::qk::grid_of((int64_t)batch * seq_len, true).ctas * 2 * head_dim * 4;
+  // (of every number of heads; calls without tokens need none)
+  const int64_t tokens = (int64_t)batch * seq_len, most = 2 * gdn::layer::kSMs;
+  return (size_t)(tokens < most ? 2 * tokens < most ? 2 * tokens : most : most) * head_dim * 4;
 }
 
 gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
@@ -378,9 +487,9 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   const void *ptrs[] = {q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, dq, dk,
                         dq_weight, dk_weight, workspace};
   if (!all_aligned(ptrs)) return GDN_ERR_INVALID_ARG;
-  const Grid g = grid_of((int64_t)rows, true);
+  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, true);
   const bool sums = dq_weight || dk_weight;
-  if (!workspace || workspace_bytes < (size_t)g.ctas * 2 * w_bytes) return GDN_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < (size_t)(g.ctas[0] + g.ctas[1]) * w_bytes) return GDN_ERR_WORKSPACE;
   const Range outs[] = {{dq, rows * wq * e}, {dk, rows * wk * e}, {dq_weight, w_bytes},
                         {dk_weight, w_bytes}};
   const Range ins[] = {{workspace, workspace_bytes},
@@ -392,28 +501,22 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   for (int i = 1; i < 9; ++i)
     if (overlaps(ins[0], ins[i])) return GDN_ERR_INVALID_ARG;
   Params p{};
-  p.q = q; p.k = k; p.wq = q_weight; p.wk = k_weight;
-  p.positions = positions; p.inv_freq = inv_freq;
-  p.dq_in = d_q_out; p.dk_in = d_k_out;
-  p.oq = dq; p.ok = dk;
-  p.dwq = dq_weight; p.dwk = dk_weight;
+  p.side[0] = {q, d_q_out, dq, q_weight, dq_weight, sq, q_heads, (int32_t)g.ctas[0], q_scale};
+  p.side[1] = {k, d_k_out, dk, k_weight, dk_weight, sk, k_heads, (int32_t)g.ctas[1], 1.f};
+  p.positions = positions;
+  p.inv_freq = inv_freq;
   p.part = static_cast<float *>(workspace);
-  p.sq = sq; p.sk = sk;
   p.tokens = (int64_t)rows;
   p.seq_len = seq_len;
-  p.Hq = q_heads; p.Hk = k_heads; p.D = head_dim; p.R = rotary_dim;
+  p.D = head_dim; p.R = rotary_dim;
+  p.pitch = (rotary_dim / 2 + 3) / 4 * 4;
   p.eps = eps;
-  p.scale = q_scale;
   p.l2 = flags & GDN_QK_L2NORM;
   p.interleaved = flags & GDN_ROPE_INTERLEAVED;
   p.tile = g.tile;
-  p.parts = (int32_t)g.ctas;
-  cudaError_t err = dtype == GDN_F32 ? launch_t<float, true>(p, g.ctas, s)
-                                     : launch_t<__nv_bfloat16, true>(p, g.ctas, s);
-  if (err == cudaSuccess && sums) {
-    gdn_qk_weights_kernel<<<(2 * head_dim + 31) / 32, 1024, 0, s>>>(p);
-    err = taken(cudaGetLastError());
-  }
+  cudaError_t err = dtype == GDN_F32 ? launch_t<float, true>(p, s) : launch_t<__nv_bfloat16, true>(p, s);
+  if (err == cudaSuccess && sums)
+    err = launch_beside(gdn_qk_weights_kernel, dim3((head_dim + 31) / 32, 2), 1024, 0, s, p);
   return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -5,11 +5,12 @@
 //   dz = dy silu'(z),   dx_t = sum_k w[ch, k] dz[t + (K - 1) - k],
 //   dw[ch, k] = sum_t dz_t x[t - (K - 1) + k],   dbias = sum_t dz_t
 //
-// with x before a sequence's start taken from its prefix (else zero).  Forward: a thread
-// takes eight channels of a run of eight tokens, all of whose loads are under way
-// together; backward: four channels of some tens of tokens, which it walks over once,
-// keeping the last K - 1 inputs and the K - 1 unfinished rows of dx in registers.  Both
-// are bound by HBM bandwidth.
+// with x before a sequence's start taken from its prefix (else zero).  A thread walks over
+// some tens or hundreds of tokens of four channels, in packed fp32 arithmetic, and keeps
+// the last K - 1 inputs (backward: and the K - 1 unfinished rows of dx) in registers, so
+// that a row is read once but at the segments' seams.  Its rows come through a ring in
+// shared memory that asynchronous copies fill some batches ahead (each thread its own
+// part: no barriers).  Both passes are bound by HBM bandwidth.
 #include "gdn_launch.cuh"
 #include "gdn_layers.cuh"
 
@@ -20,37 +21,36 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 256;
-constexpr int kRun = 8;
+constexpr int kBatch = 4;   // rows copied, and gone over, together
+constexpr int kFar = 1 << 30;   // tokens counted from a thread's first: farther ones do not matter
 
-// Four consecutive elements: 8 bytes of bf16, 16 of fp32.
-template <typename T> struct Raw4;
-template <> struct Raw4<__nv_bfloat16> {
-  uint2 a;
-  __device__ __forceinline__ void zero() { a = make_uint2(0, 0); }
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint2 *>(p); }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    v[0] = __uint_as_float(a.x << 16);
-    v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16);
-    v[3] = __uint_as_float(a.y & 0xffff0000u);
+// A thread's part of the ring: `stages` batches of kBatch rows, four elements each.
+template <typename T, int STAGES>
+struct Ring {
+  Raw4<T> *at;   // [stage][row][thread]
+  __device__ __forceinline__ void copy(int batch, const T *row, int64_t stride, int rows) const {
+    Raw4<T> *to = at + batch % STAGES * kBatch * kThreads;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i, to += kThreads, row += stride)
+      if (i < rows) {
+        const uint32_t s = (uint32_t)__cvta_generic_to_shared(to);
+        if constexpr (sizeof(T) == 2)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(row) : "memory");
+        else
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(row) : "memory");
+      }
+  }
+  __device__ __forceinline__ Raw4<T> row(int batch, int i) const {
+    return at[(batch % STAGES * kBatch + i) * kThreads];
   }
 };
-template <> struct Raw4<float> {
-  float4 a;
-  __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void load(const float *p) { a = *reinterpret_cast<const float4 *>(p); }
-  __device__ __forceinline__ void get(float (&v)[4]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  }
-};
-__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
-  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void close_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups() {   // all but the last N have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float (&v)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-  *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                             *reinterpret_cast<const uint32_t *>(&b));
-}
+// (fp32: 48 KB a CTA of the forward pass, three an SM; 85 KB of the backward pass, two)
+template <typename T, bool BACK> constexpr int kStages = sizeof(T) == 2 ? 4 : BACK ? 2 : 3;
 
 struct Params {
   Sequences seq;
@@ -61,8 +61,9 @@ struct Params {
   float *part;          // [parts][C][K + 1]
   int64_t sx;           // elements from token to token of x
   int32_t C, lanes;     // lanes: threads side by side along the channels (a power of two)
-  int32_t runs_y;       // grid rows that take tokens; the rest take the sequences' ends
-  int32_t segment, parts;
+  int32_t walks_y;      // forward: grid rows that take tokens; the rest take the sequences' ends
+  int64_t segment;
+  int32_t parts;
   bool silu;
 };
 
@@ -114,25 +115,122 @@ __device__ __forceinline__ void load_prev(const Params &p, int n, int i, int ch,
     r.load(static_cast<const T *>(p.x_prev) + ((int64_t)n * (K - 1) + i) * p.C + ch);
 }
 
+// w[k] and the bias of four channels, in pairs.
+template <int K>
+__device__ __forceinline__ void load_weights(const Params &p, int ch, bool on, uint64_t (&w)[K][2],
+                                             uint64_t (&bias)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = ch + 2 * i;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      w[k][i] = on ? pk(p.w[(int64_t)c * K + k], p.w[(int64_t)(c + 1) * K + k]) : 0ull;
+    bias[i] = on && p.bias ? pk(p.bias[c], p.bias[c + 1]) : 0ull;
+  }
+}
+
+// A thread's segment of tokens, counted from its first in 32 bits, and the sequence that it
+// is in.
+struct Segment {
+  int64_t a;             // its first token
+  int mine, last;        // tokens; those and the next ones that it has to look at
+  int n, start, end;     // the sequence, its bounds (cut off at +-kFar)
+  bool good;
+  // All lanes of the warp together; false where the thread has no tokens.
+  __device__ __forceinline__ bool begin(const Params &p, int64_t row, int64_t warp_row, int64_t total,
+                                        int beyond, bool on) {
+    const int64_t first = warp_row * p.segment;
+    if (first >= total) return false;
+    a = row * p.segment;
+    At s;
+    s.find(p.seq, first, a < total ? a : total - 1);
+    if (!on || a >= total) return false;
+    const int64_t b = a + p.segment < total ? a + p.segment : total;
+    mine = (int)(b - a);
+    last = (int)((b + beyond < total ? b + beyond : total) - a);
+    set(s);
+    return true;
+  }
+  __device__ __forceinline__ void next(const Params &p, int t) {
+    At s{n, a + start, a + end, good};
+    s.next_to(p.seq, a + t);
+    set(s);
+  }
+  __device__ __forceinline__ void set(const At &s) {
+    n = s.n;
+    start = near(s.start);
+    end = near(s.end);
+    good = s.good;
+  }
+  __device__ __forceinline__ int near(int64_t t) const {
+    t -= a;
+    return (int)(t < -kFar ? -kFar : t > kFar ? kFar : t);
+  }
+};
+// The K - 1 inputs before the segment's first token.
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ void first_window(const Params &p, const Segment &s, const T *xa, int ch,
+                                             uint64_t (&win)[K > 1 ? K - 1 : 1][2]) {
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) {
+    const int t = i - (K - 1);
+    Raw4<T> r;
+    r.zero();
+    if (s.good && t >= s.start) r.load(xa + t * p.sx);
+    else if (s.good) load_prev<K, T>(p, s.n, t - s.start + K - 1, ch, r);
+    r.get(win[i]);
+  }
+}
+// ... and those before a sequence's.
+template <typename T, int K>
+__device__ __forceinline__ void prefix_window(const Params &p, const Segment &s, int ch,
+                                              uint64_t (&win)[K > 1 ? K - 1 : 1][2]) {
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) {
+    Raw4<T> r;
+    r.zero();
+    if (s.good) load_prev<K, T>(p, s.n, i, ch, r);
+    r.get(win[i]);
+  }
+}
+// z of a token, whose input then moves into the window.
+template <int K>
+__device__ __forceinline__ uint64_t sum_taps(const uint64_t (&w)[K][2], const uint64_t (&bias)[2],
+                                             uint64_t (&win)[K > 1 ? K - 1 : 1][2], uint64_t v, int j) {
+  uint64_t z = bias[j];
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k) z = fma2(w[k][j], win[k][j], z);
+  return fma2(w[K - 1][j], v, z);
+}
+template <int K>
+__device__ __forceinline__ void move_on(uint64_t (&win)[K > 1 ? K - 1 : 1][2], uint64_t v, int j) {
+#pragma unroll
+  for (int k = 0; k + 1 < K - 1; ++k) win[k][j] = win[k + 1][j];
+  if constexpr (K > 1) win[K - 2][j] = v;
+}
+
+template <typename T> constexpr int kFwdCtas = sizeof(T) == 2 ? 4 : 3;   // an SM
+
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(kThreads, kFwdCtas<T>)
 gdn_conv_fwd_kernel(const Params p) {
-  constexpr int P = K - 1, PA = P ? P : 1;
+  constexpr int P = K - 1, PA = P ? P : 1, ST = kStages<T, false>;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, tx = tid % p.lanes, ty = tid / p.lanes, per = kThreads / p.lanes;
-  const int ch = (blockIdx.x * p.lanes + tx) * 8;
+  const int ch = (blockIdx.x * p.lanes + tx) * 4;
   const bool on = ch < p.C;
   const int64_t total = p.seq.tokens();
   const T *x = static_cast<const T *>(p.x) + ch;
 
-  if ((int)blockIdx.y >= p.runs_y) {   // the last inputs of the sequences
-    const int64_t rows = p.seq.num_seqs, step = (int64_t)(gridDim.y - p.runs_y) * per;
-    for (int64_t n = (int64_t)(blockIdx.y - p.runs_y) * per + ty; n < rows; n += step) {
+  if ((int)blockIdx.y >= p.walks_y) {   // the last inputs of the sequences
+    const int64_t rows = p.seq.num_seqs, step = (int64_t)(gridDim.y - p.walks_y) * per;
+    for (int64_t n = (int64_t)(blockIdx.y - p.walks_y) * per + ty; n < rows; n += step) {
       int64_t start, len;
       if (!p.seq.bounds((int)n, start, len) || !p.x_tail || !on) continue;
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         const int64_t t = len - P + i;   // in the sequence; before it: the prefix
-        Raw8<T> r;
+        Raw4<T> r;
         if (t >= 0) r.load(x + (start + t) * p.sx);
         else load_prev<K, T>(p, (int)n, (int)(t + P), ch, r);
         r.store(static_cast<T *>(p.x_tail) + (n * P + i) * p.C + ch);
@@ -141,248 +239,236 @@ gdn_conv_fwd_kernel(const Params p) {
     return;
   }
 
-  float w[K][8], bias[8];
+  const int64_t row = (int64_t)blockIdx.y * per + ty;
+  Segment s;
+  if (!s.begin(p, row, row - ty + (tid & ~31) / p.lanes, total, 0, on)) return;
+  const Ring<T, ST> ring{reinterpret_cast<Raw4<T> *>(smem) + tid};
+  const T *xa = x + s.a * p.sx;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) w[k][j] = on ? p.w[(int64_t)(ch + j) * K + k] : 0.f;
-    bias[j] = on && p.bias ? p.bias[ch + j] : 0.f;
+  for (int b = 0; b < ST - 1; ++b) {
+    ring.copy(b, xa + b * kBatch * p.sx, p.sx, s.mine - b * kBatch);
+    close_group();
   }
-  const int64_t runs = (total + kRun - 1) / kRun, step = (int64_t)p.runs_y * per;
-  const int wrow = (tid & ~31) / p.lanes;   // the warp's first run of the CTA's
-  for (int64_t base = (int64_t)blockIdx.y * per; base + wrow < runs; base += step) {
-    const int64_t run = base + ty, t0 = run * kRun;
-    const bool mine = on && run < runs;
-    At s;
-    s.find(p.seq, (base + wrow) * kRun, t0 < total ? t0 : total - 1);
-    if (!mine) continue;
-    Raw8<T> r[kRun + P];
+  uint64_t w[K][2], bias[2], win[PA][2];
+  load_weights<K>(p, ch, on, w, bias);
+  first_window<T, K>(p, s, xa, ch, win);
+  T *y = static_cast<T *>(p.y) + s.a * p.C + ch;
+  const auto token = [&](const Raw4<T> &r) {
+    uint64_t v[2], z[2];
+    r.get(v);
 #pragma unroll
-    for (int i = 0; i < kRun + P; ++i) {
-      const int64_t t = t0 - P + i;
-      r[i].zero();
-      if (t < total && (i >= P || (s.good && t >= s.start))) r[i].load(x + t * p.sx);
-      else if (i < P && s.good) load_prev<K, T>(p, s.n, (int)(t - s.start) + P, ch, r[i]);
+    for (int j = 0; j < 2; ++j) {
+      z[j] = sum_taps<K>(w, bias, win, v[j], j);
+      if constexpr (SILU) z[j] = mul2(z[j], sigmoid2(z[j]));
+      move_on<K>(win, v[j], j);
     }
-    float win[PA][8];
+    Raw4<T> out;
+    out.set(z);
+    return out;
+  };
+  const T *ahead = xa + (ST - 1) * kBatch * p.sx;
+  for (int t0 = 0, b = 0; t0 < s.mine; t0 += kBatch, ++b) {
+    ring.copy(b + ST - 1, ahead, p.sx, s.mine - t0 - (ST - 1) * kBatch);
+    close_group();
+    ahead += kBatch * p.sx;
+    wait_groups<ST - 1>();
+    if (s.good && t0 + kBatch <= s.mine && t0 + kBatch <= s.end) {   // one sequence
 #pragma unroll
-    for (int i = 0; i < P; ++i) r[i].get(win[i]);
-    T *y = static_cast<T *>(p.y) + t0 * p.C + ch;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int64_t t = t0 + i;
-      if (t >= total) break;
-      if (t == s.end) {
-        s.next_to(p.seq, t);
-#pragma unroll
-        for (int m = 0; m < P; ++m) {
-          Raw8<T> q;
-          q.zero();
-          if (s.good) load_prev<K, T>(p, s.n, m, ch, q);
-          q.get(win[m]);
-        }
+      for (int i = 0; i < kBatch; ++i, y += p.C) token(ring.row(b, i)).store(y);
+      continue;
+    }
+    for (int i = 0; i < kBatch && t0 + i < s.mine; ++i, y += p.C) {
+      if (t0 + i == s.end) {
+        s.next(p, t0 + i);
+        prefix_window<T, K>(p, s, ch, win);
       }
-      float v[8], z[8];
-      r[i + P].get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        z[j] = bias[j];
-#pragma unroll
-        for (int k = 0; k < P; ++k) z[j] = fmaf(w[k][j], win[k][j], z[j]);
-        z[j] = fmaf(w[P][j], v[j], z[j]);
-        if (p.silu) z[j] *= sigmoid(z[j]);
-      }
-#pragma unroll
-      for (int k = 0; k + 1 < P; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) win[k][j] = win[k + 1][j];
-      if (P)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) win[PA - 1][j] = v[j];
-      if (s.good) {
-        Raw8<T> out;
-        out.set(z);
-        out.store(y + (int64_t)i * p.C);
-      }
+      const Raw4<T> out = token(ring.row(b, i));
+      if (s.good) out.store(y);
     }
   }
 }
 
-// silu'(z) (or 1)
-__device__ __forceinline__ float slope(float z, bool silu) {
-  if (!silu) return 1.f;
-  const float s = sigmoid(z);
-  return s * fmaf(z, 1.f - s, 1.f);
+// dy silu'(z), or dy; silu'(z) = s (1 + z (1 - s))
+template <bool SILU>
+__device__ __forceinline__ uint64_t through(uint64_t dy, uint64_t z) {
+  if constexpr (!SILU) return dy;
+  const uint64_t s = sigmoid2(z), one = pk(1.f, 1.f);
+  return mul2(dy, mul2(s, fma2(z, fma2(s, pk(-1.f, -1.f), one), one)));
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads)
+constexpr int kSum = 64;   // tokens that one plain sum of dw, dbias runs over
+
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(kThreads, 2)
 gdn_conv_bwd_kernel(const Params p) {
-  constexpr int P = K - 1, PA = P ? P : 1;
-  __shared__ float red[kThreads][4];
+  constexpr int P = K - 1, PA = P ? P : 1, ST = kStages<T, true>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float4 *sums = reinterpret_cast<float4 *>(smem);   // [K + 1][thread]: over blocks of kSum tokens
   const int tid = threadIdx.x, tx = tid % p.lanes, ty = tid / p.lanes, per = kThreads / p.lanes;
   const int ch = (blockIdx.x * p.lanes + tx) * 4;
   const bool on = ch < p.C;
   const int64_t total = p.seq.tokens();
   const T *x = static_cast<const T *>(p.x) + ch, *dy = static_cast<const T *>(p.dy) + ch;
-  T *dx = static_cast<T *>(p.dx) + ch;
-  float w[K][4], bias[4], sum[K + 1][4] = {};   // sums: over all of the thread's segments
+  let_second();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int k = 0; k <= K; ++k) sums[k * kThreads + tid] = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  const int64_t row = (int64_t)blockIdx.y * per + ty;
+  Segment s;
+  if (s.begin(p, row, row - ty + (tid & ~31) / p.lanes, total, P, on)) {
+    const Ring<T, ST> rx{reinterpret_cast<Raw4<T> *>(sums + (K + 1) * kThreads) + tid};
+    const Ring<T, ST> ry{rx.at + ST * kBatch * kThreads};
+    const T *xa = x + s.a * p.sx, *ya = dy + s.a * p.C;
+    T *da = static_cast<T *>(p.dx) + ch + s.a * p.C;
 #pragma unroll
-    for (int k = 0; k < K; ++k) w[k][j] = on ? p.w[(int64_t)(ch + j) * K + k] : 0.f;
-    bias[j] = on && p.bias ? p.bias[ch + j] : 0.f;
-  }
-  const int64_t segs = (total + p.segment - 1) / p.segment, step = (int64_t)gridDim.y * per;
-  const int wrow = (tid & ~31) / p.lanes;
-  for (int64_t base = (int64_t)blockIdx.y * per; base + wrow < segs; base += step) {
-    const int64_t seg = base + ty, a = seg * p.segment;
-    const int64_t b = a + p.segment < total ? a + p.segment : total;
-    const int64_t stop = b + P < total ? b + P : total;   // tokens that reach back into a .. b - 1
-    At s;
-    s.find(p.seq, (base + wrow) * p.segment, a < total ? a : total - 1);
-    if (!on || seg >= segs) continue;
-    float win[PA][4], acc[PA][4], own[K + 1][4];   // acc[j]: row t - 1 - j, unfinished
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int64_t t = a - P + i;
-      Raw4<T> r;
-      r.zero();
-      if (s.good && t >= s.start) r.load(x + t * p.sx);
-      else if (s.good) load_prev<K, T>(p, s.n, (int)(t - s.start) + P, ch, r);
-      r.get(win[i]);
+    for (int b = 0; b < ST - 1; ++b) {
+      rx.copy(b, xa + b * kBatch * p.sx, p.sx, s.last - b * kBatch);
+      ry.copy(b, ya + b * kBatch * (int64_t)p.C, p.C, s.last - b * kBatch);
+      close_group();
     }
+    uint64_t w[K][2], bias[2], win[PA][2], acc[PA][2], own[K + 1][2];   // acc[j]: row t - 1 - j, unfinished
+    load_weights<K>(p, ch, on, w, bias);
+    first_window<T, K>(p, s, xa, ch, win);
 #pragma unroll
-    for (int i = 0; i < PA; ++i)
+    for (int i = 0; i < P; ++i) acc[i][0] = acc[i][1] = 0ull;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int k = 0; k <= K; ++k) own[k][0] = own[k][1] = 0ull;
+    const auto flush = [&] {
 #pragma unroll
-    for (int k = 0; k <= K; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) own[k][j] = 0.f;
+      for (int k = 0; k <= K; ++k) {
+        float4 &at = sums[k * kThreads + tid];
+        float v[4];
+        unpk(own[k][0], v[0], v[1]);
+        unpk(own[k][1], v[2], v[3]);
+        at = make_float4(at.x + v[0], at.y + v[1], at.z + v[2], at.w + v[3]);
+        own[k][0] = own[k][1] = 0ull;
+      }
+    };
     // rows t - 1 .. t - P of the sequence that ends before token t
-    const auto finish = [&](int64_t t) {
+    const auto finish = [&](int t) {
       if (!s.good) return;
 #pragma unroll
       for (int m = 0; m < P; ++m) {
-        const int64_t row = t - 1 - m;
-        if (row < a || row < s.start || row >= b) continue;
+        const int r = t - 1 - m;
+        if (r < 0 || r < s.start || r >= s.mine) continue;
+        Raw4<T> out;
         if (p.d_tail) {
-          Raw4<T> r;
-          float v[4];
-          r.load(static_cast<const T *>(p.d_tail) + ((int64_t)s.n * P + P - 1 - m) * p.C + ch);
-          r.get(v);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[m][j] += v[j];
+          uint64_t v[2];
+          out.load(static_cast<const T *>(p.d_tail) + ((int64_t)s.n * P + P - 1 - m) * p.C + ch);
+          out.get(v);
+          acc[m][0] = add2(acc[m][0], v[0]);
+          acc[m][1] = add2(acc[m][1], v[1]);
         }
-        store4(dx + row * p.C, acc[m]);
+        out.set(acc[m]);
+        out.store(da + (int64_t)r * p.C);
       }
     };
-    Raw4<T> rx[kRun], ry[kRun];
-    const auto fetch = [&](int64_t t0) {
+    // the next token; returns row t - P of dx, which it finishes
+    const auto token = [&](const Raw4<T> &xt, const Raw4<T> &yt, bool counts) {
+      uint64_t v[2], d[2], done[2];
+      xt.get(v);
+      yt.get(d);
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        rx[i].zero();
-        ry[i].zero();
-        if (t0 + i < stop) {
-          rx[i].load(x + (t0 + i) * p.sx);
-          ry[i].load(dy + (t0 + i) * p.C);
+      for (int j = 0; j < 2; ++j) {
+        d[j] = through<SILU>(d[j], sum_taps<K>(w, bias, win, v[j], j));
+        if (counts) {
+#pragma unroll
+          for (int k = 0; k < P; ++k) own[k][j] = fma2(d[j], win[k][j], own[k][j]);
+          own[P][j] = fma2(d[j], v[j], own[P][j]);
+          own[K][j] = add2(own[K][j], d[j]);
         }
+        done[j] = P ? fma2(w[0][j], d[j], acc[PA - 1][j]) : mul2(w[0][j], d[j]);
+#pragma unroll
+        for (int m = P - 1; m > 0; --m) acc[m][j] = fma2(w[P - m][j], d[j], acc[m - 1][j]);
+        if (P) acc[0][j] = mul2(w[P][j], d[j]);
+        move_on<K>(win, v[j], j);
       }
+      Raw4<T> out;
+      out.set(done);
+      return out;
     };
-    fetch(a);
     bool over = false;
-    for (int64_t t0 = a; t0 < stop && !over; t0 += kRun) {
-      Raw4<T> cx[kRun], cy[kRun];
+    const T *xn = xa + (ST - 1) * kBatch * p.sx, *yn = ya + (ST - 1) * kBatch * (int64_t)p.C;
+    for (int t0 = 0, b = 0; t0 < s.last && !over; t0 += kBatch, ++b) {
+      const int left = s.last - t0 - (ST - 1) * kBatch;
+      rx.copy(b + ST - 1, xn, p.sx, left);
+      ry.copy(b + ST - 1, yn, p.C, left);
+      close_group();
+      xn += kBatch * p.sx;
+      yn += kBatch * p.C;
+      wait_groups<ST - 1>();
+      if (t0 && t0 % kSum == 0) flush();
+      T *to = da + (int64_t)(t0 - P) * p.C;
+      if (s.good && t0 + kBatch <= s.mine && t0 + kBatch <= s.end) {   // one sequence, own tokens
+        const int skip = (s.start > 0 ? s.start : 0) - (t0 - P);   // rows before that are not its own
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        cx[i] = rx[i];
-        cy[i] = ry[i];
+        for (int i = 0; i < kBatch; ++i, to += p.C) {
+          const Raw4<T> out = token(rx.row(b, i), ry.row(b, i), true);
+          if (i >= skip) out.store(to);
+        }
+        continue;
       }
-      fetch(t0 + kRun);
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const int64_t t = t0 + i;
-        if (t >= stop || over) break;
+      for (int i = 0; i < kBatch; ++i, to += p.C) {
+        const int t = t0 + i;
+        if (t >= s.last) break;
         if (t == s.end) {
           finish(t);
-          if (t >= b) {   // what follows is another sequence's, and not this thread's
+          if (t >= s.mine) {   // what follows is another sequence's, and not this thread's
             over = true;
             break;
           }
-          s.next_to(p.seq, t);
+          s.next(p, t);
+          prefix_window<T, K>(p, s, ch, win);
 #pragma unroll
-          for (int m = 0; m < P; ++m) {
-            Raw4<T> q;
-            q.zero();
-            if (s.good) load_prev<K, T>(p, s.n, m, ch, q);
-            q.get(win[m]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
-          }
+          for (int m = 0; m < P; ++m) acc[m][0] = acc[m][1] = 0ull;
         }
-        float v[4], d[4], row[4];
-        cx[i].get(v);
-        cy[i].get(d);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float z = bias[j];
-#pragma unroll
-          for (int k = 0; k < P; ++k) z = fmaf(w[k][j], win[k][j], z);
-          z = fmaf(w[P][j], v[j], z);
-          d[j] *= slope(z, p.silu);
-          if (t < b && s.good) {
-#pragma unroll
-            for (int k = 0; k < P; ++k) own[k][j] = fmaf(d[j], win[k][j], own[k][j]);
-            own[P][j] = fmaf(d[j], v[j], own[P][j]);
-            own[K][j] += d[j];
-          }
-          // row t - P is finished; the others move on by one
-          row[j] = P ? fmaf(w[0][j], d[j], acc[PA - 1][j]) : w[0][j] * d[j];
-#pragma unroll
-          for (int m = P - 1; m > 0; --m) acc[m][j] = fmaf(w[P - m][j], d[j], acc[m - 1][j]);
-          if (P) acc[0][j] = w[P][j] * d[j];
-#pragma unroll
-          for (int k = 0; k + 1 < P; ++k) win[k][j] = win[k + 1][j];
-          if (P) win[PA - 1][j] = v[j];
-        }
-        if (s.good && t - P >= a && t - P >= s.start) store4(dx + (t - P) * p.C, row);
+        const Raw4<T> out = token(rx.row(b, i), ry.row(b, i), t < s.mine && s.good);
+        if (s.good && t - P >= 0 && t - P >= s.start) out.store(to);
       }
     }
-    if (!over && stop == total && s.end == total) finish(total);
-#pragma unroll
-    for (int k = 0; k <= K; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[k][j] += own[k][j];
+    if (!over && s.a + s.last == total && s.end == s.last) finish(s.last);
+    flush();
+    wait_groups<0>();
   }
   // the CTA's sums, in the order of its rows of threads
-#pragma unroll
-  for (int k = 0; k <= K; ++k) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) red[tid][j] = sum[k][j];
-    __syncthreads();
-    if (ty == 0 && on)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float r = 0.f;
-        for (int i = 0; i < per; ++i) r += red[i * p.lanes + tx][j];
-        p.part[((int64_t)blockIdx.y * p.C + ch + j) * (K + 1) + k] = r;
-      }
+  __syncthreads();
+  for (int i = tid; i < (K + 1) * p.lanes; i += kThreads) {
+    const int k = i / p.lanes, l = i % p.lanes, c = (blockIdx.x * p.lanes + l) * 4;
+    if (c >= p.C) continue;
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < per; ++j) {
+      const float4 v = sums[k * kThreads + j * p.lanes + l];
+      r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
+    }
+    float *at = p.part + ((int64_t)blockIdx.y * p.C + c) * (K + 1) + k;
+    at[0] = r.x;
+    at[K + 1] = r.y;
+    at[2 * (K + 1)] = r.z;
+    at[3 * (K + 1)] = r.w;
   }
 }
 
-// The sums over the CTAs (a thread for each of C (K + 1)), and behind them the gradient of
-// the prefixes (four channels of a sequence a thread).
+// The sums over the CTAs (32 of the C (K + 1) a CTA), and behind them the gradient of the
+// prefixes (four channels of a sequence a thread).
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads)
 gdn_conv_ends_kernel(const Params p, int sum_blocks) {
   constexpr int P = K - 1, PA = P ? P : 1;
-  if ((int)blockIdx.x < sum_blocks) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, n = (int64_t)p.C * (K + 1);
-    if (i >= n) return;
+  wait_first();
+  if ((int)blockIdx.x < sum_blocks) {   // its eight warps share the partial sums
+    __shared__ float red[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = (int64_t)p.C * (K + 1);
     float r = 0.f;
-    for (int k = 0; k < p.parts; ++k) r += p.part[k * n + i];
+    if (i < n)
+#pragma unroll 4
+      for (int k = warp; k < p.parts; k += kThreads / 32) r += p.part[k * n + i];
+    red[warp][lane] = r;
+    __syncthreads();
+    if (warp || i >= n) return;
+    r = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) r += red[w][lane];
     const int64_t c = i / (K + 1);
     const int k = (int)(i % (K + 1));
     if (k == K) {
@@ -397,14 +483,14 @@ gdn_conv_ends_kernel(const Params p, int sum_blocks) {
   const int n = (int)(i / vecs), ch = (int)(i % vecs) * 4;
   int64_t start, len;
   if (!p.seq.bounds(n, start, len) || !p.dx_prev) return;
-  float win[PA][4], d[PA][4], g[PA][4];   // g: of the prefix's rows
+  uint64_t w[K][2], bias[2], win[PA][2], g[PA][2];   // g: of the prefix's rows
+  load_weights<K>(p, ch, true, w, bias);
 #pragma unroll
   for (int m = 0; m < P; ++m) {
     Raw4<T> r;
     load_prev<K, T>(p, n, m, ch, r);
     r.get(win[m]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) g[m][j] = 0.f;
+    g[m][0] = g[m][1] = 0ull;
     if (p.d_tail && m >= len) {   // with fewer tokens than that the tail begins in the prefix
       r.load(static_cast<const T *>(p.d_tail) + ((int64_t)n * P + m - len) * p.C + ch);
       r.get(g[m]);
@@ -412,33 +498,33 @@ gdn_conv_ends_kernel(const Params p, int sum_blocks) {
   }
 #pragma unroll
   for (int t = 0; t < P; ++t) {
-    float v[4] = {}, e[4] = {};
-    if (t < len) {
-      Raw4<T> r;
-      r.load(static_cast<const T *>(p.x) + (start + t) * p.sx + ch);
-      r.get(v);
-      r.load(static_cast<const T *>(p.dy) + (start + t) * p.C + ch);
-      r.get(e);
-    }
+    if (t >= len) break;
+    uint64_t v[2], e[2];
+    Raw4<T> r;
+    r.load(static_cast<const T *>(p.x) + (start + t) * p.sx + ch);
+    r.get(v);
+    r.load(static_cast<const T *>(p.dy) + (start + t) * p.C + ch);
+    r.get(e);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float *w = p.w + (int64_t)(ch + j) * K;
-      float z = p.bias ? p.bias[ch + j] : 0.f;
+    for (int j = 0; j < 2; ++j) {
+      uint64_t z = bias[j];
 #pragma unroll
-      for (int k = 0; k < P; ++k) z = fmaf(w[k], win[k][j], z);
-      z = fmaf(w[P], v[j], z);
-      d[t][j] = t < len ? e[j] * slope(z, p.silu) : 0.f;
+      for (int k = 0; k < P; ++k) z = fma2(w[k][j], win[k][j], z);
+      z = fma2(w[P][j], v[j], z);
+      e[j] = p.silu ? through<true>(e[j], z) : e[j];
 #pragma unroll
-      for (int m = 0; m < P; ++m)
-        if (m >= t) g[m][j] = fmaf(w[m - t], d[t][j], g[m][j]);
+      for (int m = t; m < P; ++m) g[m][j] = fma2(w[m - t][j], e[j], g[m][j]);
 #pragma unroll
       for (int k = 0; k + 1 < P; ++k) win[k][j] = win[k + 1][j];
       win[PA - 1][j] = v[j];
     }
   }
 #pragma unroll
-  for (int m = 0; m < P; ++m)
-    store4(static_cast<T *>(p.dx_prev) + ((int64_t)n * P + m) * p.C + ch, g[m]);
+  for (int m = 0; m < P; ++m) {
+    Raw4<T> r;
+    r.set(g[m]);
+    r.store(static_cast<T *>(p.dx_prev) + ((int64_t)n * P + m) * p.C + ch);
+  }
 }
 
 // One token per sequence: a page holds the last K - 1 inputs, the oldest first.
@@ -464,30 +550,40 @@ gdn_conv_step_kernel(const StepParams p) {
   if (page < 0 || page >= p.num_pages) {
     if (page != -1 && ch == 0 && p.status)
       report(p.status, GDN_ERR_DEVICE_CHECK, (uint32_t)n, 0u, 0u);
-    const float zero[4] = {};
-    store4(y, zero);
+    Raw4<T> zero;
+    zero.zero();
+    zero.store(y);
     return;
   }
   T *at = static_cast<T *>(p.pool) + page * p.page_stride + ch;
-  float win[K][4];
   Raw4<T> r[K];
 #pragma unroll
   for (int k = 0; k < P; ++k) r[k].load(at + (int64_t)k * p.C);
   r[P].load(static_cast<const T *>(p.x) + (int64_t)n * p.C + ch);
+  uint64_t z[2];
 #pragma unroll
-  for (int k = 0; k < K; ++k) r[k].get(win[k]);
-  float z[4];
+  for (int j = 0; j < 2; ++j) z[j] = p.bias ? pk(p.bias[ch + 2 * j], p.bias[ch + 2 * j + 1]) : 0ull;
+  float w[4 * K];   // [channel][tap], together 16 K bytes
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float *w = p.w + (int64_t)(ch + j) * K;
-    z[j] = p.bias ? p.bias[ch + j] : 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) z[j] = fmaf(w[k], win[k][j], z[j]);
-    if (p.silu) z[j] *= sigmoid(z[j]);
+  for (int k = 0; k < K; ++k) {
+    const float4 v = reinterpret_cast<const float4 *>(p.w + (int64_t)ch * K)[k];
+    w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
   }
-  store4(y, z);
 #pragma unroll
-  for (int k = 0; k < P; ++k) store4(at + (int64_t)k * p.C, win[k + 1]);
+  for (int k = 0; k < K; ++k) {
+    uint64_t v[2];
+    r[k].get(v);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) z[j] = fma2(pk(w[2 * j * K + k], w[(2 * j + 1) * K + k]), v[j], z[j]);
+  }
+  if (p.silu)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) z[j] = mul2(z[j], sigmoid2(z[j]));
+  Raw4<T> out;
+  out.set(z);
+  out.store(y);
+#pragma unroll
+  for (int k = 0; k < P; ++k) r[k + 1].store(at + (int64_t)k * p.C);
 }
 
 int lanes_of(int vecs) {
@@ -497,54 +593,72 @@ int lanes_of(int vecs) {
 }
 int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
 
-template <typename T, int K>
-cudaError_t launch_fwd(Params p, int64_t total, cudaStream_t stream) {
-  const int vecs = p.C / 8;
-  p.lanes = lanes_of(vecs);
-  const int per = kThreads / p.lanes, gx = (vecs + p.lanes - 1) / p.lanes;
-  const int64_t runs = (total + kRun - 1) / kRun;
-  // CTAs that fit at a time (registers), each going over several runs of tokens
-  const int64_t most = (3 * kSMs + gx - 1) / gx;
-  p.runs_y = (int32_t)least((runs + per - 1) / per, most);
-  const int64_t ends = p.seq.cu || (p.x_tail && K > 1)
-                           ? least((p.seq.num_seqs + per - 1) / per, 64) : 0;
-  gdn_conv_fwd_kernel<T, K><<<dim3(gx, (unsigned)(p.runs_y + ends)), kThreads, 0, stream>>>(p);
-  return taken(cudaGetLastError());
-}
-// Tokens that a thread of the backward pass walks over, and the CTAs along them: long
-// segments read few rows twice, short ones fill the GPU.
+// A launch over the tokens: every thread that fits on the GPU (`ctas` CTAs an SM) walks
+// over one segment of at least `least_` tokens.
 struct Walk {
-  int segment, lanes, gx;
+  int64_t segment;
+  int lanes, gx;
   int64_t gy;
 };
-Walk walk(int C, int64_t total) {
+Walk walk(int C, int64_t total, int ctas, int64_t least_) {
   Walk k;
   const int vecs = C / 4;
   k.lanes = lanes_of(vecs);
   k.gx = (vecs + k.lanes - 1) / k.lanes;
   const int per = kThreads / k.lanes;
-  k.segment = 64;
-  const int64_t want = 2 * kSMs;
-  while (k.segment > 8 && k.gx * ((total + k.segment * per - 1) / (k.segment * per)) < want)
-    k.segment /= 2;
-  const int64_t segs = (total + k.segment - 1) / k.segment;
-  k.gy = least((segs + per - 1) / per, (4 * kSMs + k.gx - 1) / k.gx);
+  const int64_t y = ctas * kSMs / k.gx;
+  const int64_t rows = (y > 1 ? y : 1) * per;   // of threads
+  k.segment = ((total + rows - 1) / rows + kBatch - 1) / kBatch * kBatch;
+  if (k.segment < least_) k.segment = least_;
+  k.gy = ((total + k.segment - 1) / k.segment + per - 1) / per;
   return k;
+}
+// (Backward: a segment goes over K - 1 tokens of the next one too, and leaves a partial sum.)
+Walk walk_bwd(int C, int64_t total) { return walk(C, total, 2, 16); }
+
+template <typename T, int K, bool SILU>
+cudaError_t launch_fwd_s(const Params &p, dim3 grid, cudaStream_t stream) {
+  constexpr size_t kBytes = sizeof(Raw4<T>) * kStages<T, false> * kBatch * kThreads;
+  const cudaError_t err = allow_smem<gdn_conv_fwd_kernel<T, K, SILU>>(kBytes);
+  if (err != cudaSuccess) return err;
+  gdn_conv_fwd_kernel<T, K, SILU><<<grid, kThreads, kBytes, stream>>>(p);
+  return taken(cudaGetLastError());
+}
+template <typename T, int K>
+cudaError_t launch_fwd(Params p, int64_t total, cudaStream_t stream) {
+  const Walk k = walk(p.C, total, kFwdCtas<T>, 8);
+  p.lanes = k.lanes;
+  p.segment = k.segment;
+  p.walks_y = (int32_t)k.gy;
+  const int per = kThreads / k.lanes;
+  const int64_t ends = p.seq.cu || (p.x_tail && K > 1)
+                           ? least((p.seq.num_seqs + per - 1) / per, 64) : 0;
+  const dim3 grid(k.gx, (unsigned)(k.gy + ends));
+  return p.silu ? launch_fwd_s<T, K, true>(p, grid, stream) : launch_fwd_s<T, K, false>(p, grid, stream);
+}
+template <typename T, int K, bool SILU>
+cudaError_t launch_bwd_s(const Params &p, dim3 grid, cudaStream_t stream) {
+  constexpr size_t kBytes = 16 * (K + 1) * kThreads + 2 * sizeof(Raw4<T>) * kStages<T, true> * kBatch * kThreads;
+  const cudaError_t err = allow_smem<gdn_conv_bwd_kernel<T, K, SILU>>(kBytes);
+  if (err != cudaSuccess) return err;
+  gdn_conv_bwd_kernel<T, K, SILU><<<grid, kThreads, kBytes, stream>>>(p);
+  return taken(cudaGetLastError());
 }
 template <typename T, int K>
 cudaError_t launch_bwd(Params p, int64_t total, cudaStream_t stream) {
-  const Walk k = walk(p.C, total);
+  const Walk k = walk_bwd(p.C, total);
   p.lanes = k.lanes;
   p.segment = k.segment;
   p.parts = (int32_t)k.gy;
-  gdn_conv_bwd_kernel<T, K><<<dim3(k.gx, (unsigned)k.gy), kThreads, 0, stream>>>(p);
-  const cudaError_t err = taken(cudaGetLastError());
+  const dim3 grid(k.gx, (unsigned)k.gy);
+  const cudaError_t err = p.silu ? launch_bwd_s<T, K, true>(p, grid, stream)
+                                 : launch_bwd_s<T, K, false>(p, grid, stream);
   if (err != cudaSuccess) return err;
-  const int sums = (int)(((int64_t)p.C * (K + 1) + kThreads - 1) / kThreads);
+  const int sums = (int)(((int64_t)p.C * (K + 1) + 31) / 32);
   const int64_t ends = p.seq.cu || (p.dx_prev && K > 1)
                            ? ((int64_t)p.C / 4 * p.seq.num_seqs + kThreads - 1) / kThreads : 0;
-  gdn_conv_ends_kernel<T, K><<<(unsigned)(sums + ends), kThreads, 0, stream>>>(p, sums);
-  return taken(cudaGetLastError());
+  return launch_beside(gdn_conv_ends_kernel<T, K>, dim3((unsigned)(sums + ends)), kThreads, 0, stream, p,
+                       sums);
 }
 template <typename T, int K>
 cudaError_t launch_step(const StepParams &p, cudaStream_t stream) {
@@ -634,8 +748,8 @@ gdn_status gdn_conv_fwd(const void *x, const float *w, const float *bias, const 
 size_t gdn_conv_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels, int32_t taps) {
   using namespace gdn::conv;
   if (num_seqs <= 0 || seq_len < 0 || channels <= 0 || channels % 4 || taps <= 0) return 0;
-  const int64_t dense = walk(channels, (int64_t)num_seqs * seq_len).gy;
-  const int64_t packed = walk(channels, seq_len).gy, most = dense > packed ? dense : packed;
+  const int64_t dense = walk_bwd(channels, (int64_t)num_seqs * seq_len).gy;
+  const int64_t packed = walk_bwd(channels, seq_len).gy, most = dense > packed ? dense : packed;
   return gdn::kStatusBytes + (size_t)most * channels * (taps + 1) * 4;
 }
 
@@ -672,7 +786,7 @@ gdn_status gdn_conv_bwd(const void *x, const float *w, const float *bias, const 
     return GDN_OK;
   }
   if (!x || !w || !d_y || !dx) return GDN_ERR_INVALID_ARG;
-  const Walk k = walk(channels, (int64_t)rows);
+  const Walk k = walk_bwd(channels, (int64_t)rows);
   if (!workspace || workspace_bytes < kStatusBytes + (size_t)k.gy * channels * (taps + 1) * 4)
     return GDN_ERR_WORKSPACE;
   for (int i = 0; i < 7; ++i)

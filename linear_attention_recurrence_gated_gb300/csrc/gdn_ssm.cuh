@@ -53,20 +53,78 @@ struct Params {
   float *seg_d;                  // [slot][D] its sum of delta
 };
 
-// log(1 + exp(v)): with e = exp(-|v|) <= 1 and s = e / (2 + e) <= 1/3 it is
-// max(v, 0) + 2 artanh(s), and the series of artanh leaves out s^15 / 15 < 2^-27 s.
+// log(1 + exp(v)) of two values: with e = exp(-|v|) <= 1 and s = e / (2 + e) <= 1/3 it is
+// max(v, 0) + 2 artanh(s).  artanh(s) = s + s^3 f(s^2), f(q) = 1/3 + q/5 + q^2/7 + ..., by
+// the cubic that minimises the largest q |error| over [0, 1/9] (4e-9, a fifteenth of
+// fp32's half step).
 template <typename T>
-__device__ __forceinline__ float softplus(float v) {
-  // (for bf16 inputs the exponent's rounding, some 2^-21, is far below dt's own)
-  const float e = sizeof(T) == 4 ? expf(-fabsf(v)) : ex2(-kLog2e * fabsf(v));
-  const float s = e * rcp(2.f + e), q = s * s;
-  float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  r = fmaf(q, r, 1.f / 9.f);
-  r = fmaf(q, r, 1.f / 7.f);
-  r = fmaf(q, r, 1.f / 5.f);
-  r = fmaf(q, r, 1.f / 3.f);
-  r = fmaf(q * s, r, s);
-  return fmaxf(v, 0.f) + (r + r);
+__device__ __forceinline__ uint64_t softplus2(uint64_t v) {
+  float a, b;
+  unpk(v, a, b);
+  float ea, eb;
+  if constexpr (sizeof(T) == 4) {   // the argument's rounding, up to 2^-21 of e, is put right
+    constexpr float kLow = 1.9259629911266175e-8f;   // log2(e) - kLog2e
+    const float ta = -fabsf(a) * kLog2e, tb = -fabsf(b) * kLog2e;
+    const float la = fmaf(-fabsf(a), kLow, fmaf(-fabsf(a), kLog2e, -ta));
+    const float lb = fmaf(-fabsf(b), kLow, fmaf(-fabsf(b), kLog2e, -tb));
+    ea = ex2(ta);
+    eb = ex2(tb);
+    ea = ea > 0.f ? fmaf(ea, 0.6931472f * la, ea) : ea;   // (0 for -inf, whose la is NaN)
+    eb = eb > 0.f ? fmaf(eb, 0.6931472f * lb, eb) : eb;
+  } else {
+    ea = ex2(-kLog2e * fabsf(a));
+    eb = ex2(-kLog2e * fabsf(b));
+  }
+  const uint64_t e = pk(ea, eb);
+  float wa, wb;
+  unpk(add2(e, pk(2.f, 2.f)), wa, wb);
+  const uint64_t s = mul2(e, pk(rcp(wa), rcp(wb))), q = mul2(s, s);
+  uint64_t r = fma2(pk(0.14012232422828674f, 0.14012232422828674f), q, pk(0.13999569416046143f, 0.13999569416046143f));
+  r = fma2(r, q, pk(0.20010849833488464f, 0.20010849833488464f));
+  r = fma2(r, q, pk(0.3333320617675781f, 0.3333320617675781f));
+  r = fma2(mul2(q, s), r, s);
+  return fma2(r, pk(2.f, 2.f), pk(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+// delta of eight channels: pairs of dt + dt_bias, its softplus if asked for.
+template <typename T>
+__device__ __forceinline__ void steps_of(const Raw8<T> &dt, const uint64_t (&bias)[4], bool soft,
+                                         uint64_t (&d)[4]) {
+  float v[8];
+  dt.get(v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = add2(pk(v[2 * i], v[2 * i + 1]), bias[i]);
+  if (soft)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = softplus2<T>(d[i]);
+}
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Raw8<T> &r, uint64_t (&p)[4]) {
+  float v[8];
+  r.get(v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pk(v[2 * i], v[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void set_pairs(Raw8<T> &r, const uint64_t (&p)[4]) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpk(p[i], v[2 * i], v[2 * i + 1]);
+  r.set(v);
+}
+__device__ __forceinline__ void put8(float *at, const uint64_t (&p)[4]) {
+  reinterpret_cast<ulonglong2 *>(at)[0] = make_ulonglong2(p[0], p[1]);
+  reinterpret_cast<ulonglong2 *>(at)[1] = make_ulonglong2(p[2], p[3]);
+}
+__device__ __forceinline__ void take8(const float *at, uint64_t (&p)[4]) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(at)[0];
+  const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(at)[1];
+  p[0] = a.x; p[1] = a.y; p[2] = b.x; p[3] = b.y;
+}
+// Eight channels' values of an fp32 array, 0 without one.
+__device__ __forceinline__ void load8(const float *base, int ch, bool on, uint64_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    p[i] = base && on ? *reinterpret_cast<const uint64_t *>(base + ch + 2 * i) : 0ull;
 }
 
 // v[4] summed over the LS lanes that share channels, each lane keeping some of them:
@@ -156,6 +214,14 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   unpk(x, lo, hi);
   return pk(ex2(lo), ex2(hi));
 }
+// exp(delta A) of a token.  The hardware's exp2 is low by 2e-8 on average for arguments
+// of -0.1 to 0 (measured over 10^6 arguments a range: -1.7e-8 to -2.6e-8), which a state
+// that lasts a thousand tokens would add up to 2e-5; kLift in the exponent takes the mean
+// away (below 1.3e-8 there; 2^kLift itself still gives 1, so that delta = 0 keeps a state).
+constexpr float kLift = 2e-8f;
+__device__ __forceinline__ uint64_t decay(uint64_t delta, uint64_t A) {
+  return ex2_pair(fma2(delta, A, pk(kLift, kLift)));
+}
 // h <- exp(A sum) h + X of the segment in `slot` (its arrays x [slot][D][S], d [slot][D]).
 template <int S>
 __device__ __forceinline__ void join(uint64_t (&h)[2][4], const uint64_t (&A)[2][4],
@@ -172,6 +238,88 @@ __device__ __forceinline__ void join(uint64_t (&h)[2][4], const uint64_t (&A)[2]
     for (int j = 0; j < 4; ++j)
       h[k][j] = fma2(ex2_pair(mul2(s[k], A[k][j])), h[k][j], add[k][j]);
 }
+
+// The forward scans' threads: 16 consecutive elements of [D][S], that is 16 states of one
+// channel (8 of two for S = 8), pairs of states in packed arithmetic.  c . h is summed
+// inside a thread up to S = 16, over S / 16 lanes beyond; b and c are read by whole warps
+// from one address.  (With 4 channels x 4 states a thread the
+// call took 204 us where this takes 179, [4, 4096, 1280], S = 16: three shuffles and their
+// selects a token.)
+template <int S>
+struct Run {
+  static constexpr int SPT = S < 16 ? S : 16;   // states of a channel
+  static constexpr int CPT = 16 / SPT;          // channels
+  static constexpr int LS = S / SPT;            // lanes that share a channel
+  static constexpr int NP = SPT / 2;            // pairs of states
+};
+__device__ __forceinline__ void load16(const float *at, bool on, uint64_t (&a)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const ulonglong2 v = on && at ? reinterpret_cast<const ulonglong2 *>(at)[i] : make_ulonglong2(0, 0);
+    a[2 * i] = v.x;
+    a[2 * i + 1] = v.y;
+  }
+}
+__device__ __forceinline__ void store16(float *at, bool on, const uint64_t (&a)[8]) {
+  if (!on) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<ulonglong2 *>(at)[i] = make_ulonglong2(a[2 * i], a[2 * i + 1]);
+}
+__device__ __forceinline__ void rates16(const float *at, bool on, uint64_t (&a)[8]) {
+  load16(at, on, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    unpk(a[i], lo, hi);
+    a[i] = on ? pk(rate(lo), rate(hi)) : 0ull;
+  }
+}
+// h <- exp(A sum) h + x, from a segment's state x and its sum of delta for the thread's
+// channels.
+template <int S>
+__device__ __forceinline__ void join16(uint64_t (&h)[8], const uint64_t (&A)[8], const float *x,
+                                       const float *sum, bool on) {
+  uint64_t add[8];
+  load16(x, on, add);
+#pragma unroll
+  for (int k = 0; k < Run<S>::CPT; ++k) {
+    const float d = on ? sum[k] : 0.f;
+#pragma unroll
+    for (int i = 0; i < Run<S>::NP; ++i) {
+      const int e = k * Run<S>::NP + i;
+      h[e] = fma2(ex2_pair(mul2(pk(d, d), A[e])), h[e], add[e]);
+    }
+  }
+}
+// Shared memory: the steps of a thread's channels at token t, each twice; n pairs.
+template <int CPT>
+__device__ __forceinline__ void twice(const float *at, uint64_t (&d)[CPT]) {
+  if constexpr (CPT == 2) {
+    const float2 v = *reinterpret_cast<const float2 *>(at);
+    d[0] = pk(v.x, v.x);
+    d[1] = pk(v.y, v.y);
+  } else {
+    d[0] = pk(at[0], at[0]);
+  }
+}
+// (S = 64: the upper half of a row's 16-byte pieces lies with neighbours exchanged, so that
+// the four lanes of a channel read from different banks.)
+template <int N>
+__device__ __forceinline__ void pairs(const float *at, int swap, uint64_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const ulonglong2 w = reinterpret_cast<const ulonglong2 *>(at)[i ^ swap];
+    v[2 * i] = w.x;
+    v[2 * i + 1] = w.y;
+  }
+}
+__device__ __forceinline__ float total(uint64_t v) {
+  float lo, hi;
+  unpk(v, lo, hi);
+  return lo + hi;
+}
+
 struct Pairs {
   uint64_t a, b;
 };
@@ -179,12 +327,24 @@ __device__ __forceinline__ Pairs lds2(const float *p) {
   const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
   return {v.x, v.y};
 }
-// Eight values, each twice: the operand of packed arithmetic on two channels.
-__device__ __forceinline__ void store_twice(float *at, const float (&v)[8]) {
+// b and c of a tile of L tokens for threads of 4 channels x 4 states, each value twice (the
+// operand of packed arithmetic on two channels): [b, c][token][first, second two of four
+// states][S / 4][2 x 2], so that the lanes of a channel read neighbouring 16 bytes.
+// Vector v (eight states) of token t of b (w = 0) or c (1):
+template <int S>
+__device__ __forceinline__ void store_twice(float *sbc, int idx, const float (&v)[8]) {
+  const int row = idx / (S / 8), k = idx % (S / 8);   // row: [b, c][token]
+  float *at = sbc + row * 2 * S + 8 * k;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4 *>(at)[i] =
+    *reinterpret_cast<float4 *>(at + (i & 1) * S + 4 * (i >> 1)) =
         make_float4(v[2 * i], v[2 * i], v[2 * i + 1], v[2 * i + 1]);
+}
+template <int S, int L = 8>
+__device__ __forceinline__ void load_twice(const float *sbc, int t, int which, int sl, uint64_t (&v)[4]) {
+  const float *at = sbc + (which * L + t) * 2 * S + 4 * sl;
+  const Pairs a = lds2(at), b = lds2(at + S);
+  v[0] = a.a; v[1] = a.b; v[2] = b.a; v[3] = b.b;
 }
 
 // The split along time of a launch of `blocks` CTAs per segment: chunks of 32 tokens, two
@@ -193,7 +353,7 @@ __device__ __forceinline__ void store_twice(float *at, const float (&v)[8]) {
 constexpr int kChunkTokens = 32;
 inline lin::Plan plan(int64_t num_seqs, int64_t seq_len, bool packed, int64_t blocks,
                       double first) {
-  return lin::plan_segments(num_seqs, seq_len, packed, blocks, 2 * kSMs, kChunkTokens, 1.0, first);
+  return lin::plan_segments(num_seqs, seq_len, packed, blocks, 3 * kSMs, kChunkTokens, 1.0, first);
 }
 inline int channel_blocks(int Dg, int S) { return (Dg + 2048 / S - 1) / (2048 / S); }
 inline bool state_size(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }

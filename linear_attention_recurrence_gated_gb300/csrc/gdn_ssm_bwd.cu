@@ -8,13 +8,15 @@
 //
 // The states of a token are needed in the reverse order of their making.  One launch
 // runs the scan forward and keeps every kL-th state; the next takes the tiles of kL
-// tokens from the last to the first, makes a tile's states again from the kept one (they
-// stay in shared memory) and goes through them backward.  12 multiply-adds and two
+// tokens from the last to the first, makes a tile's states again from the kept one and goes
+// through them backward: they wait in tensor memory, 16 columns a token, which leaves
+// shared memory and registers for three CTAs an SM.  12 multiply-adds and two
 // exponentials an element there, 3 and one in the first (7 where sequences are cut along
 // time: it leaves each segment's gradient of its start from zero too, by running products
 // of the decays).  Sums over a CTA's channels (db, dc) and over tokens (dA_log, dD_skip,
 // ddt_bias) are left in the workspace and added up in a fixed order by the last launch:
 // results are bitwise reproducible.
+#include "gdn_ptx.cuh"
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -51,7 +53,7 @@ struct Inputs {
   static constexpr int CB = Geo<S>::CB, VB = CB / 8, RT = kThreads / VB;
   static constexpr int NV = (TT + RT - 1) / RT;
   static constexpr int NBC = 2 * TT * S / 8, NB = (NBC + kThreads - 1) / kThreads;
-  Raw8<T> x[NV], dt[NV], dy[NV], gate[NV], bc[NB];
+  Raw8<T> x[NV], dt[NV], dy[GRAD ? NV : 1], gate[GRAD ? NV : 1], bc[NB];
   __device__ __forceinline__ void fetch(const BwdParams &p, int64_t first, int cnt, int group,
                                         int vch, bool von) {
     const int tid = threadIdx.x;
@@ -84,73 +86,58 @@ struct Inputs {
         bc[i].load(static_cast<const T *>(p.c) + (first + row) * p.sc + group * S + 8 * v);
     }
   }
-  // delta, delta x and ds of the tile, b and c twice over, to shared memory
-  __device__ __forceinline__ void form(const BwdParams &p, int cnt, bool von, const float (&bias)[8],
-                                       float *sd, float *su, float *ss, float *sbc) const {
+  // delta, delta x and ds of the tile, to shared memory
+  __device__ __forceinline__ void form(const BwdParams &p, int cnt, int vch, bool von, float *sd,
+                                       float *su, float *ss) const {
     const int tid = threadIdx.x, vec = tid % VB;
+    uint64_t bias[4];
+    load8(p.dt_bias, vch, von, bias);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int row = tid / VB + i * RT;
       if (row >= TT) continue;
-      float xv[8], dv[8];
-      x[i].get(xv);
-      dt[i].get(dv);
-      const bool on = von && row < cnt;
+      uint64_t v[4], d[4];
+      steps_of(dt[i], bias, p.softplus, d);
+      if (row >= cnt)   // tokens that do not exist leave the states as they are
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = dv[j] + bias[j];
-        dv[j] = on ? (p.softplus ? softplus<T>(v) : v) : 0.f;
-        xv[j] *= dv[j];
-      }
-      put(sd + row * CB + 8 * vec, dv);
-      put(su + row * CB + 8 * vec, xv);
+        for (int j = 0; j < 4; ++j) d[j] = 0ull;
+      pairs_of(x[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = mul2(d[j], v[j]);
+      put8(sd + row * CB + 8 * vec, d);
+      put8(su + row * CB + 8 * vec, v);
       if (GRAD) {
-        float gv[8];
-        dy[i].get(dv);
+        pairs_of(dy[i], d);
         if (p.gate) {
-          gate[i].get(gv);
+          pairs_of(gate[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dv[j] *= gv[j] * sigmoid(gv[j]);
+          for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], mul2(v[j], sigmoid2(v[j])));
         }
-        put(ss + row * CB + 8 * vec, dv);
+        put8(ss + row * CB + 8 * vec, d);
       }
     }
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int idx = tid + i * kThreads;
-      if (idx >= (GRAD ? NBC : NBC / 2)) continue;
-      float v[8];
-      bc[i].get(v);
-      store_twice(sbc + 16 * idx, v);
-    }
-  }
-  static __device__ __forceinline__ void put(float *at, const float (&v)[8]) {
-    reinterpret_cast<float4 *>(at)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(at)[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-  static __device__ __forceinline__ void take(const float *at, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(at)[0];
-    const float4 b = reinterpret_cast<const float4 *>(at)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
 };
+
+template <int S> constexpr int kKeepTile = S < 32 ? S : 32;   // tokens of a tile of the first launch
 
 // First launch: the kept states, and of segments their end state, sum of delta and
 // gradient from zero.
 template <typename T, int S, bool CUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, !CUT ? 4 : sizeof(T) == 2 ? 3 : 2)
 gdn_ssm_keep_kernel(const BwdParams p) {
-  constexpr int TT = S <= 16 ? 16 : 32, CB = Geo<S>::CB;
+  constexpr int TT = kKeepTile<S>, CB = Geo<S>::CB;
+  constexpr int LS = Run<S>::LS, CPT = Run<S>::CPT, NP = Run<S>::NP;
   static_assert(TT % kL == 0 && kChunkTokens % TT == 0, "tiles of whole runs of kL tokens");
   using In = Inputs<T, S, TT, CUT>;
   extern __shared__ __align__(16) float smem[];
-  float *sd = smem, *su = sd + TT * CB, *sbc = su + TT * CB, *ss = sbc + 4 * TT * S;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float *sd = smem, *su = sd + TT * CB, *sbc = su + TT * CB, *ss = sbc + (CUT ? 2 : 1) * TT * S;
+  const int tid = threadIdx.x;
   const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks, slot = blockIdx.y;
   const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
-  const int sl = lane % Geo<S>::LS, cl = warp * Geo<S>::CL + lane / Geo<S>::LS;
-  const Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
+  const int sl = tid % LS, cl = tid / LS * CPT, swap = S == 64 ? sl >> 1 : 0;
+  const bool on = first_ch + cl < end_ch;
+  const int64_t own = (int64_t)first_ch * S + 16 * tid;   // its elements of [D][S]
   let_second();
   lin::Span s;
   if (!lin::span_of(p.seq, slot, 0, s)) return;
@@ -162,94 +149,97 @@ gdn_ssm_keep_kernel(const BwdParams p) {
   const int64_t len = whole ? s.len : s.len > 0 ? (s.len - 1) / kL * kL : 0;
   if (len == 0) return;
 
-  uint64_t A[2][4], h[2][4], P[2][4], Y[2][4];
-  load_rates<S>(p.A_log, own, A);
-  load_own<S>(s.seg == 0 && p.h0 ? p.h0 + s.n * state : nullptr, own, h);
+  uint64_t A[8], h[8], P[CUT ? 8 : 1], Y[CUT ? 8 : 1];
+  rates16(p.A_log + own, on, A);
+  load16(s.seg == 0 && p.h0 ? p.h0 + s.n * state + own : nullptr, on, h);
+  if constexpr (CUT)
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      P[k][j] = pk(1.f, 1.f);
-      Y[k][j] = 0ull;
+    for (int i = 0; i < 8; ++i) {
+      P[i] = pk(1.f, 1.f);
+      Y[i] = 0ull;
     }
   const int vec = tid % In::VB, vch = first_ch + 8 * vec;
   const bool von = vch < end_ch;
-  float bias[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
 
-  const auto keep = [&](int64_t t, const uint64_t (&sum)[2]) {
+  float sums[CPT] = {};
+  const auto keep = [&](int64_t t) {
     const int64_t at = kept(begin, off + t);
-    store_own<S>(p.ckpt + at * state, own, h);
-    if (CUT && s.seg > 0 && own.on && sl == 0) {
-      float v[4];
-      unpk(sum[0], v[0], v[1]);
-      unpk(sum[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(p.ckpt_d + at * D + own.ch) = make_float4(v[0], v[1], v[2], v[3]);
-    }
+    store16(p.ckpt + at * state + own, on, h);
+    if (CUT && s.seg > 0 && on && sl == 0)
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) p.ckpt_d[at * D + first_ch + cl + k] = sums[k];
   };
   In in;
-  uint64_t total[2] = {0ull, 0ull};
   in.fetch(p, s.start, (int)(len < TT ? len : TT), group, vch, von);
   for (int64_t t0 = 0; t0 < len; t0 += TT) {
     const int cnt = (int)(len - t0 < TT ? len - t0 : TT);
-    in.form(p, cnt, von, bias, sd, su, ss, sbc);
+    in.form(p, cnt, vch, von, sd, su, ss);
+#pragma unroll
+    for (int i = 0; i < In::NB; ++i) {
+      const int idx = tid + i * kThreads;
+      if (idx >= (CUT ? In::NBC : In::NBC / 2)) continue;
+      uint64_t v[4];
+      pairs_of(in.bc[i], v);
+      if (S == 64 && (idx & 4)) {   // see pairs()
+        const uint64_t w[4] = {v[2], v[3], v[0], v[1]};
+        put8(sbc + 8 * idx, w);
+      } else {
+        put8(sbc + 8 * idx, v);
+      }
+    }
     __syncthreads();
     if (t0 + TT < len)
       in.fetch(p, s.start + t0 + TT, (int)(len - t0 - TT < TT ? len - t0 - TT : TT), group, vch, von);
     for (int r = 0; r < cnt; r += kL) {
-      if (t0 + r > 0) keep(t0 + r, total);
-      uint64_t part[2] = {0ull, 0ull};
+      if (t0 + r > 0) keep(t0 + r);
+      float part[CPT] = {};
 #pragma unroll 4
       for (int t = r; t < r + kL; ++t) {   // (tokens past the last: zeros)
-        const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
-        const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
-        const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
-        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
-        uint64_t cc[4], yy[2];
+        uint64_t d[CPT], u[CPT], y[CPT], b2[NP], c2[NP];
+        twice<CPT>(sd + t * CB + cl, d);
+        twice<CPT>(su + t * CB + cl, u);
+        pairs<NP>(sbc + t * S + 16 * sl, swap, b2);
         if constexpr (CUT) {
-          const float *at = sbc + TT * S * 2 + t * 2 * S + 8 * sl;
-          const Pairs c0 = lds2(at), c1 = lds2(at + 4), y = lds2(ss + t * CB + 4 * cl);
-          cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
-          yy[0] = y.a; yy[1] = y.b;
+          twice<CPT>(ss + t * CB + cl, y);
+          pairs<NP>(sbc + TT * S + t * S + 16 * sl, swap, c2);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < CPT; ++k) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
-            h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
+          for (int i = 0; i < NP; ++i) {
+            const int e = k * NP + i;
+            const uint64_t a = decay(d[k], A[e]);
+            h[e] = fma2(a, h[e], mul2(u[k], b2[i]));
             if constexpr (CUT) {
-              P[k][j] = mul2(P[k][j], a);
-              Y[k][j] = fma2(P[k][j], mul2(cc[j], yy[k]), Y[k][j]);
+              P[e] = mul2(P[e], a);
+              Y[e] = fma2(P[e], mul2(c2[i], y[k]), Y[e]);
             }
           }
-          part[k] = add2(part[k], dd[k]);
+          float lo, hi;
+          unpk(d[k], lo, hi);
+          part[k] += lo;
         }
       }
-      total[0] = add2(total[0], part[0]);
-      total[1] = add2(total[1], part[1]);
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) sums[k] += part[k];
     }
     __syncthreads();
   }
   if (!whole) {   // the last kept state comes behind the last token that was run
-    keep(len, total);
+    keep(len);
     return;
   }
-  if (!last) store_own<S>(p.seg_x + slot * state, own, h);
-  if (s.seg > 0) store_own<S>(p.seg_y + slot * state, own, Y);
-  if (own.on && sl == 0) {
-    float v[4];
-    unpk(total[0], v[0], v[1]);
-    unpk(total[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p.seg_d + (int64_t)slot * D + own.ch) =
-        make_float4(v[0], v[1], v[2], v[3]);
-  }
+  if (!last) store16(p.seg_x + slot * state + own, on, h);
+  if constexpr (CUT)
+    if (s.seg > 0) store16(p.seg_y + slot * state + own, on, Y);
+  if (on && sl == 0)
+#pragma unroll
+    for (int k = 0; k < CPT; ++k) p.seg_d[(int64_t)slot * D + first_ch + cl + k] = sums[k];
 }
 template <int S, bool CUT>
 constexpr size_t keep_smem() {
-  constexpr int TT = S <= 16 ? 16 : 32;
-  return 4u * (TT * Geo<S>::CB * (CUT ? 3 : 2) + 4 * TT * S);
+  constexpr int TT = kKeepTile<S>;
+  return 4u * (TT * Geo<S>::CB * (CUT ? 3 : 2) + (CUT ? 2 : 1) * TT * S);
 }
 
 // v[8]: four values of db and four of dc of a lane's states, summed over the warp's CL
@@ -275,25 +265,31 @@ __device__ __forceinline__ int sum_groups(float (&v)[8], int grp) {
   return first;
 }
 
-template <int S>
+// Shared memory of the second launch, in floats.
+template <typename T, int S>
 struct Bwd {
-  static constexpr int CB = Geo<S>::CB, TILE = kL * CB;
-  // delta, delta x (later q), ds (later sum A w), s, b and c, sums of b and c, the tile's
-  // states, the segment's start, sums of dA
-  static constexpr size_t kFloats =
-      4 * TILE + 4 * kL * S + 4 * kL * 2 * S + (size_t)kL * 16 * kThreads + 2 * 16 * kThreads;
+  static constexpr int CB = Geo<S>::CB, TILE = kL * CB, OWN = 16 * kThreads;
+  static constexpr int kRaw = Inputs<T, S, kL, true>::NV * kThreads * 8 * sizeof(T) / 4;
+  static constexpr int D = 0, U = D + TILE, E = U + TILE;   // delta; delta x, later q; ds, later sum A w
+  static constexpr int Y = E + TILE, BC = Y + TILE;         // c . h; b and c, each value twice
+  static constexpr int RED = BC + 4 * kL * S;               // the warps' sums for db and dc
+  static constexpr int START = RED + 4 * kL * 2 * S;        // a thread's states at the segment's start
+  static constexpr int DA = START + OWN;                    // ... sums for dA
+  static constexpr int SUM = DA + OWN;                      // ... for dD_skip and ddt_bias: [2][16]
+  static constexpr int RAW = SUM + 2 * OWN;                 // the tile's x, dt, dy and gate
+  static constexpr size_t kFloats = RAW + 4 * kRaw + 4;     // (and the place in tensor memory)
 };
+constexpr uint32_t kColumns = 16 * kL;   // of tensor memory: a thread's 16 values for each token
 
 // Second launch: tiles from the last token to the first.
 template <typename T, int S, bool GATE>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 gdn_ssm_grad_kernel(const BwdParams p) {
-  constexpr int CB = Geo<S>::CB, LS = Geo<S>::LS, CL = Geo<S>::CL, TILE = Bwd<S>::TILE;
+  using B = Bwd<T, S>;
   using In = Inputs<T, S, kL, true>;
+  constexpr int CB = B::CB, LS = Geo<S>::LS, CL = Geo<S>::CL;
   extern __shared__ __align__(16) float smem[];
-  float *sd = smem, *su = sd + TILE, *ss = su + TILE, *sy = ss + TILE, *sbc = sy + TILE;
-  float *sred = sbc + 4 * kL * S, *shist = sred + 4 * kL * 2 * S;
-  float *sstart = shist + kL * 16 * kThreads, *sdA = sstart + 16 * kThreads;
+  float *sd = smem + B::D, *su = smem + B::U, *ss = smem + B::E, *sy = smem + B::Y, *sbc = smem + B::BC;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks;
   const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
@@ -301,7 +297,23 @@ gdn_ssm_grad_kernel(const BwdParams p) {
   const Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
   const int64_t D = p.D, state = D * S;
 
-  // a thread's 16 values in shared memory: four float4, a row of threads each
+  uint32_t *place = reinterpret_cast<uint32_t *>(smem + B::kFloats - 4);
+  if (warp == 0) ptx::tmem_alloc((uint32_t)__cvta_generic_to_shared(place), kColumns);
+  __syncthreads();
+  const uint32_t columns = *place, mine = columns + ((uint32_t)(warp * 32) << 16);
+
+  // a thread's 16 values: in tensor memory ...
+  const auto store_tm = [&](int t, const uint64_t (&a)[2][4]) {
+    uint32_t r[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      r[2 * i] = (uint32_t)a[i >> 2][i & 3];
+      r[2 * i + 1] = (uint32_t)(a[i >> 2][i & 3] >> 32);
+    }
+    ptx::tmem_st16(mine + 16 * t, r);
+  };
+  const auto load_tm = [&](int t, uint32_t (&r)[16]) { ptx::tmem_ld16(mine + 16 * t, r); };
+  // ... and in shared memory, four float4, a row of threads each
   const auto put16 = [&](float *at, const uint64_t (&a)[2][4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -323,19 +335,15 @@ gdn_ssm_grad_kernel(const BwdParams p) {
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dA[k][j] = 0ull;
-  put16(sdA, dA);
+  put16(smem + B::DA, dA);
+  put16(smem + B::SUM, dA);
+  put16(smem + B::SUM + B::OWN, dA);
   const int vec = tid % In::VB, vch = first_ch + 8 * vec;
   const bool von = vch < end_ch;
-  float bias[8], skip[8], sum_bias[2][8] = {}, sum_skip[2][8] = {};   // of some tiles, of all
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
-    skip[i] = von && p.d_skip ? p.d_skip[vch + i] : 0.f;
-  }
   int tiles_summed = 0;
   const auto flush = [&] {   // at most 16 tiles in one run of an accumulator
     uint64_t sum[2][4];
-    get16(sdA, sum);
+    get16(smem + B::DA, sum);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -343,16 +351,23 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         sum[k][j] = add2(sum[k][j], dA[k][j]);
         dA[k][j] = 0ull;
       }
-    put16(sdA, sum);
+    put16(smem + B::DA, sum);
+    uint64_t some[2][4];
+    get16(smem + B::SUM, some);
+    get16(smem + B::SUM + B::OWN, sum);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sum_bias[1][i] += sum_bias[0][i];
-      sum_skip[1][i] += sum_skip[0][i];
-      sum_bias[0][i] = sum_skip[0][i] = 0.f;
-    }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[k][j] = add2(sum[k][j], some[k][j]);
+        some[k][j] = 0ull;
+      }
+    put16(smem + B::SUM, some);
+    put16(smem + B::SUM + B::OWN, sum);
     tiles_summed = 0;
   };
   wait_first();
+  let_second();   // the sums' CTAs, as these leave room
 
   for (int slot = blockIdx.y; slot < p.seq.slots; slot += gridDim.y) {
     lin::Span s;
@@ -369,7 +384,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       for (int i = 1; i < s.seg; ++i)
         join<S>(h, A, p.seg_x, p.seg_d, slot - s.seg + i, p.D, own);
     }
-    put16(sstart, h);
+    put16(smem + B::START, h);
 
     const int64_t tiles = (s.len + kL - 1) / kL;
     In in;
@@ -378,41 +393,51 @@ gdn_ssm_grad_kernel(const BwdParams p) {
     for (int64_t tile = tiles - 1; tile >= 0; --tile) {
       const int64_t t0 = tile * kL;
       const int cnt = (int)(s.len - t0 < kL ? s.len - t0 : kL);
-      in.form(p, cnt, von, bias, sd, su, ss, sbc);
-      In now = in;   // for the tile's gradients
+      in.form(p, cnt, vch, von, sd, su, ss);
+#pragma unroll
+      for (int i = 0; i < In::NB; ++i) {
+        const int idx = tid + i * kThreads;
+        if (idx >= In::NBC) continue;
+        float v[8];
+        in.bc[i].get(v);
+        store_twice<S>(sbc, idx, v);
+      }
+      Raw8<T> *raw = reinterpret_cast<Raw8<T> *>(smem + B::RAW) + tid;   // for the tile's gradients
+#pragma unroll
+      for (int i = 0; i < In::NV; ++i) {
+        raw[(4 * i) * kThreads] = in.x[i];
+        raw[(4 * i + 1) * kThreads] = in.dt[i];
+        raw[(4 * i + 2) * kThreads] = in.dy[i];
+        if (GATE) raw[(4 * i + 3) * kThreads] = in.gate[i];
+      }
       __syncthreads();
       if (tile > 0) in.fetch(p, s.start + t0 - kL, kL, group, vch, von);
       if (tile == 0) {
-        get16(sstart, h);
+        get16(smem + B::START, h);
       } else {
         const int64_t at = kept(begin, off + t0);
         if (s.seg > 0) {
-          get16(sstart, h);
+          get16(smem + B::START, h);
           join<S>(h, A, p.ckpt, p.ckpt_d, at, p.D, own);
         } else {
           load_own<S>(p.ckpt + at * state, own, h);
         }
       }
       // the tile's states
-#pragma unroll 4
+#pragma unroll 2
       for (int t = 0; t < cnt; ++t) {
-        put16(shist + t * 16 * kThreads, h);
+        __syncwarp();
+        store_tm(t, h);
         const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
         const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
-        const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
-        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
-        uint64_t cc[4], y[2];
-        if constexpr (GATE) {
-          const float *at = sbc + kL * S * 2 + t * 2 * S + 8 * sl;
-          const Pairs c0 = lds2(at), c1 = lds2(at + 4);
-          cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
-        }
+        uint64_t bb[4], cc[4], y[2];
+        load_twice<S>(sbc, t, 0, sl, bb);
+        if constexpr (GATE) load_twice<S>(sbc, t, 1, sl, cc);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
-            h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
+            h[k][j] = fma2(decay(dd[k], A[k][j]), h[k][j], mul2(uu[k], bb[j]));
             if constexpr (GATE) y[k] = j ? fma2(cc[j], h[k][j], y[k]) : mul2(cc[j], h[k][j]);
           }
         if constexpr (GATE) {
@@ -423,17 +448,25 @@ gdn_ssm_grad_kernel(const BwdParams p) {
           store_channels<LS>(sy + t * CB + 4 * cl, v, sl);
         }
       }
+      __syncwarp();
+      ptx::tmem_wait_st();
       // and backward through them
+      uint32_t ahead[16];
+      load_tm(cnt - 1, ahead);
 #pragma unroll 2
       for (int t = cnt - 1; t >= 0; --t) {
         const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl),
                     e = lds2(ss + t * CB + 4 * cl);
         const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b}, ee[2] = {e.a, e.b};
-        const float *bt = sbc + t * 2 * S + 8 * sl, *ct = bt + kL * S * 2;
-        const Pairs b0 = lds2(bt), b1 = lds2(bt + 4), c0 = lds2(ct), c1 = lds2(ct + 4);
-        const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b}, cc[4] = {c0.a, c0.b, c1.a, c1.b};
-        uint64_t before[2][4], db[4], dc[4], q[2], aw[2];
-        get16(shist + t * 16 * kThreads, before);
+        uint64_t bb[4], cc[4], before[2][4], db[4], dc[4], q[2], aw[2];
+        load_twice<S>(sbc, t, 0, sl, bb);
+        load_twice<S>(sbc, t, 1, sl, cc);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          before[i >> 2][i & 3] = ((uint64_t)ahead[2 * i + 1] << 32) | ahead[2 * i];
+        __syncwarp();   // delta x and ds of this token are read: q and sum A w take their place
+        if (t > 0) load_tm(t - 1, ahead);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -442,15 +475,13 @@ gdn_ssm_grad_kernel(const BwdParams p) {
             dc[j] = k ? fma2(ee[k], h[k][j], dc[j]) : mul2(ee[k], h[k][j]);
             db[j] = k ? fma2(uu[k], G, db[j]) : mul2(uu[k], G);
             q[k] = j ? fma2(bb[j], G, q[k]) : mul2(bb[j], G);
-            const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
-            g[k][j] = mul2(a, G);
+            g[k][j] = mul2(decay(dd[k], A[k][j]), G);
             const uint64_t w = mul2(g[k][j], before[k][j]);
             aw[k] = j ? fma2(A[k][j], w, aw[k]) : mul2(A[k][j], w);
             dA[k][j] = fma2(dd[k], w, dA[k][j]);
             h[k][j] = before[k][j];
           }
         float v[4], r[8];
-        __syncwarp();   // delta x and ds of this token are read: q and sum A w take their place
         unpk(q[0], v[0], v[1]);
         unpk(q[1], v[2], v[3]);
         sum_channels<LS>(v, sl);
@@ -461,14 +492,11 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         store_channels<LS>(ss + t * CB + 4 * cl, v, sl);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float lo, hi;
-          unpk(db[j], lo, hi);
-          r[j] = lo + hi;
-          unpk(dc[j], lo, hi);
-          r[4 + j] = lo + hi;
+          r[j] = total(db[j]);
+          r[4 + j] = total(dc[j]);
         }
         const int first = sum_groups<CL, LS>(r, grp);
-        float *red = sred + (warp * kL + t) * 2 * S;
+        float *red = smem + B::RED + (warp * kL + t) * 2 * S;
         constexpr int KEEP = CL >= 8 ? 1 : 8 / CL;
         if (CL <= 8 || grp < 8)
 #pragma unroll
@@ -481,53 +509,65 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       // db and dc of this CTA's channels
       for (int i = tid; i < cnt * 2 * S; i += kThreads) {
         const int row = i / (2 * S), at = i % (2 * S);
+        const float *red = smem + B::RED;
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) sum += sred[(w * kL + row) * 2 * S + at];
+        for (int w = 0; w < kThreads / 32; ++w) sum += red[(w * kL + row) * 2 * S + at];
         p.part_bc[(((int64_t)cb * p.rows() + s.start + t0 + row) * p.G + group) * 2 * S + at] = sum;
       }
+      uint64_t bias[4], skip[4], sums[2][4];   // sums: for dD_skip and ddt_bias
+      load8(p.dt_bias, vch, von, bias);
+      load8(p.d_skip, vch, von, skip);
+      get16(smem + B::SUM, sums);
 #pragma unroll
       for (int i = 0; i < In::NV; ++i) {
         const int row = tid / In::VB + i * In::RT;
         if (!von || row >= cnt) continue;
         const int64_t out = (s.start + t0 + row) * D + vch;
-        float xv[8], tv[8], yv[8], dl[8], qv[8], wv[8], o[8];
-        now.x[i].get(xv);
-        now.dt[i].get(tv);
-        now.dy[i].get(yv);
-        In::take(sd + row * CB + 8 * vec, dl);
-        In::take(su + row * CB + 8 * vec, qv);
-        In::take(ss + row * CB + 8 * vec, wv);
+        const int at = row * CB + 8 * vec;
+        uint64_t xv[4], yv[4], qv[4], v[4], o[4];
         Raw8<T> r;
+        pairs_of(raw[(4 * i) * kThreads], xv);
+        pairs_of(raw[(4 * i + 2) * kThreads], yv);
         if constexpr (GATE) {
-          float gv[8], sv[8];
-          now.gate[i].get(gv);
-          In::take(sy + row * CB + 8 * vec, sv);
+          uint64_t gv[4];
+          pairs_of(raw[(4 * i + 3) * kThreads], gv);
+          take8(sy + at, v);
+          if (p.d_skip)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float sg = sigmoid(gv[j]), total = fmaf(skip[j], p.d_skip ? xv[j] : 0.f, sv[j]);
-            o[j] = yv[j] * total * (sg * fmaf(gv[j], 1.f - sg, 1.f));
-            yv[j] *= gv[j] * sg;
+            for (int j = 0; j < 4; ++j) v[j] = fma2(skip[j], xv[j], v[j]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {   // silu'(g) = sg (1 + g (1 - sg))
+            const uint64_t sg = sigmoid2(gv[j]), one = pk(1.f, 1.f);
+            const uint64_t slope = mul2(sg, fma2(gv[j], fma2(sg, pk(-1.f, -1.f), one), one));
+            o[j] = mul2(mul2(yv[j], v[j]), slope);
+            yv[j] = mul2(yv[j], mul2(gv[j], sg));
           }
-          r.set(o);
+          set_pairs(r, o);
           r.store(static_cast<T *>(p.dgate) + out);
         }
+        take8(sd + at, v);
+        take8(su + at, qv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = fmaf(dl[j], qv[j], skip[j] * yv[j]);
-          sum_skip[0][j] = fmaf(yv[j], xv[j], sum_skip[0][j]);
+        for (int j = 0; j < 4; ++j) {
+          o[j] = fma2(v[j], qv[j], mul2(skip[j], yv[j]));
+          sums[0][j] = fma2(yv[j], xv[j], sums[0][j]);
         }
-        r.set(o);
+        set_pairs(r, o);
         r.store(static_cast<T *>(p.dx) + out);
+        take8(ss + at, v);
+        uint64_t tv[4];
+        pairs_of(raw[(4 * i + 1) * kThreads], tv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = fmaf(xv[j], qv[j], 0.6931471805599453f * wv[j]);   // (rates carry log2 e)
-          if (p.softplus) o[j] *= sigmoid(tv[j] + bias[j]);
-          sum_bias[0][j] += o[j];
+        for (int j = 0; j < 4; ++j) {   // (rates carry log2 e)
+          o[j] = fma2(xv[j], qv[j], mul2(pk(0.6931471805599453f, 0.6931471805599453f), v[j]));
+          if (p.softplus) o[j] = mul2(o[j], sigmoid2(add2(tv[j], bias[j])));
+          sums[1][j] = add2(sums[1][j], o[j]);
         }
-        r.set(o);
+        set_pairs(r, o);
         r.store(static_cast<T *>(p.ddt) + out);
       }
+      put16(smem + B::SUM, sums);
       if (++tiles_summed == 16) flush();
       __syncthreads();
     }
@@ -536,58 +576,76 @@ gdn_ssm_grad_kernel(const BwdParams p) {
 
   // this CTA's sums over its tokens
   flush();
-  get16(sdA, dA);
+  get16(smem + B::DA, dA);
   float *part = p.part_w + (int64_t)blockIdx.y * (state + 2 * D);
   store_own<S>(part, own, dA);
+  uint64_t sums[2][4];
+  get16(smem + B::SUM + B::OWN, sums);
   __syncthreads();
-  float *sum = shist;   // [2][rows of threads][CB]
-  constexpr int RT = In::RT;
+  float *sum = smem;   // [2][rows of threads][CB]: 2048 floats
+  static_assert(2 * In::RT * CB <= B::START, "room for the sums");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    sum[(tid / In::VB) * CB + 8 * vec + i] = sum_skip[1][i];
-    sum[(RT + tid / In::VB) * CB + 8 * vec + i] = sum_bias[1][i];
-  }
+  for (int which = 0; which < 2; ++which)
+    put8(sum + (which * In::RT + tid / In::VB) * CB + 8 * vec, sums[which]);
   __syncthreads();
   for (int i = tid; i < 2 * CB; i += kThreads) {
     const int which = i / CB, ch = i % CB;
     if (first_ch + ch >= end_ch) continue;
     float r = 0.f;
-    for (int k = 0; k < RT; ++k) r += sum[(which * RT + k) * CB + ch];
+    for (int k = 0; k < In::RT; ++k) r += sum[(which * In::RT + k) * CB + ch];
     part[state + which * D + first_ch + ch] = r;
   }
+  if (warp == 0) ptx::tmem_dealloc(columns, kColumns);
 }
 
-// Third launch: the sums over blocks of channels (one of a token's 2 G S values a
-// thread), and behind them those over the tokens of the second launch's CTAs.
+// Third launch: the sums over blocks of channels, and behind them those over the tokens of
+// the second launch's CTAs.
 template <typename T>
 __global__ void __launch_bounds__(256)
 gdn_ssm_sum_kernel(const BwdParams p, int S, int64_t bc_blocks) {
-  if (blockIdx.x < bc_blocks) {
+  wait_first();
+  if (blockIdx.x < bc_blocks) {   // four values a thread
     const int64_t per = (int64_t)p.G * 2 * S, n = p.rows() * per;
-    const int64_t i0 = (int64_t)blockIdx.x * 256, i = i0 + threadIdx.x;
+    const int64_t i0 = (int64_t)blockIdx.x * 1024, i = i0 + 4 * threadIdx.x;
     if (p.seq.cu) {   // rows of a sequence whose offsets are bad stay as they are
       const Sequences q{p.seq.cu, p.seq.status, p.seq.seq_len, p.seq.num_seqs};
       const int64_t row = (i < n ? i : n - 1) / per;
-      const int64_t first = (i0 + (threadIdx.x & ~31)) / per;
+      const int64_t first = (i0 + 4 * (threadIdx.x & ~31)) / per;
       int at = q.find(first < p.rows() ? first : p.rows() - 1);
       while (at + 1 < p.seq.num_seqs && p.seq.cu[at + 1] <= row) ++at;
       int64_t start, len;
       if (!q.bounds(at, start, len) || row < start || row >= start + len) return;
     }
     if (i >= n) return;
-    float sum = 0.f;
-    for (int b = 0; b < p.blocks; ++b) sum += p.part_bc[b * n + i];
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int b = 0; b < p.blocks; ++b) {
+      const float4 v = *reinterpret_cast<const float4 *>(p.part_bc + b * n + i);
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
     const int64_t row = i / per;
-    const int r = (int)(i % per), grp = r / (2 * S), which = r / S % 2, st = r % S;
-    T *out = static_cast<T *>(which ? p.dc : p.db) + (row * p.G + grp) * S + st;
-    store_out(out, sum);
+    const int r = (int)(i - row * per), grp = r / (2 * S), which = r / S % 2, st = r % S;
+    Raw4<T> out;
+    const uint64_t v[2] = {pk(sum.x, sum.y), pk(sum.z, sum.w)};
+    out.set(v);
+    out.store(static_cast<T *>(which ? p.dc : p.db) + (row * p.G + grp) * S + st);
     return;
   }
+  // 32 of the weights' sums, shared by eight warps
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t state = (int64_t)p.D * S, n = state + 2 * p.D;
-  const int64_t i = (blockIdx.x - bc_blocks) * 256 + threadIdx.x;
-  if (i >= n) return;
+  const int64_t i = (blockIdx.x - bc_blocks) * 32 + lane;
   float sum = 0.f;
-  for (int k = 0; k < p.parts; ++k) sum += p.part_w[k * n + i];
+  if (i < n)
+#pragma unroll 4
+    for (int k = warp; k < p.parts; k += 8) sum += p.part_w[k * n + i];
+  red[warp][lane] = sum;
+  __syncthreads();
+  if (warp || i >= n) return;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) sum += red[w][lane];
   if (i < state) {
     if (p.dA_log) p.dA_log[i] = -expf(p.A_log[i]) * sum;
   } else if (i < state + p.D) {
@@ -617,9 +675,10 @@ Layout layout(int64_t rows, int64_t D, int64_t S, int64_t groups, int64_t blocks
   return l;
 }
 constexpr double kFirst = 0.5;
-// CTAs of the second launch over the slots: two an SM, four rounds of them at most
+// CTAs of the second launch over the slots: at most as many as three an SM, and one more
+// round of them
 int64_t parts_of(int64_t slots, int64_t blocks) {
-  const int64_t most = (4 * kSMs + blocks - 1) / blocks;
+  const int64_t most = (6 * kSMs + blocks - 1) / blocks;
   return slots < most ? slots : most;
 }
 
@@ -641,7 +700,7 @@ cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
   err = taken(cudaGetLastError());
   if (err != cudaSuccess) return err;
   const dim3 tiles(groups * p.blocks, p.parts);
-  constexpr size_t kGrad = 4 * Bwd<S>::kFloats;
+  constexpr size_t kGrad = 4 * Bwd<T, S>::kFloats;
   if (p.gate) {
     err = allow_smem<gdn_ssm_grad_kernel<T, S, true>>(kGrad);
     if (err == cudaSuccess)
@@ -652,11 +711,10 @@ cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
       err = launch_beside(gdn_ssm_grad_kernel<T, S, false>, tiles, kThreads, kGrad, stream, p);
   }
   if (err != cudaSuccess) return err;
-  const int64_t bc = (p.rows() * groups * 2 * S + 255) / 256;
-  const int64_t w = ((int64_t)p.D * (S + 2) + 255) / 256;
+  const int64_t bc = (p.rows() * groups * 2 * S + 1023) / 1024;
+  const int64_t w = ((int64_t)p.D * (S + 2) + 31) / 32;
   if (bc + w > 0x7fffffff) return cudaErrorInvalidValue;
-  gdn_ssm_sum_kernel<T><<<(unsigned)(bc + w), 256, 0, stream>>>(p, S, bc);
-  return taken(cudaGetLastError());
+  return launch_beside(gdn_ssm_sum_kernel<T>, dim3((unsigned)(bc + w)), 256, 0, stream, p, S, bc);
 }
 template <typename T>
 cudaError_t launch_t(const BwdParams &p, int S, int groups, cudaStream_t stream) {

@@ -25,29 +25,29 @@ struct Fwd : Geo<S> {
 };
 
 template <typename T, int S, bool OUT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, OUT ? 3 : 4)
 gdn_ssm_scan_kernel(const Params p) {
   using F = Fwd<S>;
-  constexpr int TT = F::TT, CB = F::CB, LS = F::LS;
+  using R = Run<S>;
+  constexpr int TT = F::TT, CB = F::CB, LS = R::LS, CPT = R::CPT, NP = R::NP;
   __shared__ __align__(16) float sd[TT * CB], su[TT * CB], sy[OUT ? TT * CB : 4];
-  __shared__ __align__(16) float sbc[(OUT ? 2 : 1) * TT * S * 2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ __align__(16) float sbc[(OUT ? 2 : 1) * TT * S];
+  const int tid = threadIdx.x;
   const int group = blockIdx.x / p.blocks, cb = blockIdx.x % p.blocks, slot = blockIdx.y;
   const int first_ch = group * p.Dg + cb * CB, end_ch = (group + 1) * p.Dg;
-  const int sl = lane % LS, cl = warp * F::CL + lane / LS;   // its states, its four channels
-  Own own{first_ch + 4 * cl, 4 * sl, first_ch + 4 * cl < end_ch};
+  const int sl = tid % LS, cl = tid / LS * CPT;   // its part of the states, its first channel
+  const int swap = S == 64 ? sl >> 1 : 0;
+  const bool on = first_ch + cl < end_ch;
+  const int64_t own = (int64_t)first_ch * S + 16 * tid;   // its elements of [D][S]
 
-  uint64_t A[2][4], h[2][4];
-  load_rates<S>(p.A_log, own, A);
+  uint64_t A[8], h[8];
+  rates16(p.A_log + own, on, A);
   // its eight channels where tiles are formed and left
   const int vec = tid % F::VB, vch = first_ch + 8 * vec;
   const bool von = vch < end_ch;
-  float bias[8], skip[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bias[i] = von && p.dt_bias ? p.dt_bias[vch + i] : 0.f;
-    skip[i] = OUT && von && p.d_skip ? p.d_skip[vch + i] : 0.f;
-  }
+  uint64_t bias[4], skip[4];
+  load8(p.dt_bias, vch, von, bias);
+  if (OUT) load8(p.d_skip, vch, von, skip);
   if (OUT && p.seq.seg_len) wait_first();   // every CTA: none may end before the first launch
   if (!OUT) let_second();
   lin::Span s;
@@ -55,25 +55,23 @@ gdn_ssm_scan_kernel(const Params p) {
   const int64_t state = (int64_t)p.D * S;
   if (!OUT && s.seg == s.count - 1) {   // nothing follows; keep what the last launch overwrites
     if (p.keep) {
-      load_own<S>(p.h0 + s.n * state, own, h);
-      store_own<S>(p.seg_x + slot * state, own, h);
+      load16(p.h0 + s.n * state + own, on, h);
+      store16(p.seg_x + slot * state + own, on, h);
     }
     return;
   }
   if (s.seg == 0) {
     const bool kept = OUT && p.keep && p.seq.seg_len;
-    load_own<S>(kept ? p.seg_x + (slot + s.count - 1) * state : p.h0 ? p.h0 + s.n * state : nullptr,
-                own, h);
+    const float *from = kept ? p.seg_x + (slot + s.count - 1) * state : p.h0 ? p.h0 + s.n * state : nullptr;
+    load16(from ? from + own : nullptr, on, h);
+  } else if (!OUT) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 0ull;
   } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[k][j] = 0ull;
-    if (OUT) {
-      load_own<S>(p.seg_x + (slot - s.seg) * state, own, h);   // the first one's end state
-      for (int i = 1; i < s.seg; ++i)
-        join<S>(h, A, p.seg_x, p.seg_d, slot - s.seg + i, p.D, own);
-    }
+    const int64_t one = slot - s.seg;
+    load16(p.seg_x + one * state + own, on, h);   // the first one's end state
+    for (int i = 1; i < s.seg; ++i)
+      join16<S>(h, A, p.seg_x + (one + i) * state + own, p.seg_d + (one + i) * p.D + first_ch + cl, on);
   }
 
   Raw8<T> xr[F::NV], dr[F::NV], gr[F::NV], br[F::NB];
@@ -109,37 +107,36 @@ gdn_ssm_scan_kernel(const Params p) {
     }
   };
 
-  uint64_t total[2] = {0ull, 0ull};
+  float sums[CPT] = {};
   fetch(0);
   for (int64_t t0 = 0; t0 < s.len; t0 += TT) {
     const int cnt = (int)(s.len - t0 < TT ? s.len - t0 : TT);
 #pragma unroll
     for (int i = 0; i < F::NV; ++i) {
       const int row = tid / F::VB + i * (kThreads / F::VB);
-      float xv[8], dv[8], uv[8];
-      xr[i].get(xv);
-      dr[i].get(dv);
-      const bool on = von && row < cnt;
+      uint64_t xv[4], dv[4];
+      steps_of(dr[i], bias, p.softplus, dv);
+      if (row >= cnt)   // tokens that do not exist leave the states as they are
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = dv[j] + bias[j];
-        dv[j] = on ? (p.softplus ? softplus<T>(v) : v) : 0.f;
-        uv[j] = dv[j] * xv[j];
-      }
-      float4 *d = reinterpret_cast<float4 *>(sd + row * CB + 8 * vec);
-      float4 *u = reinterpret_cast<float4 *>(su + row * CB + 8 * vec);
-      d[0] = make_float4(dv[0], dv[1], dv[2], dv[3]);
-      d[1] = make_float4(dv[4], dv[5], dv[6], dv[7]);
-      u[0] = make_float4(uv[0], uv[1], uv[2], uv[3]);
-      u[1] = make_float4(uv[4], uv[5], uv[6], uv[7]);
+        for (int j = 0; j < 4; ++j) dv[j] = 0ull;
+      pairs_of(xr[i], xv);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xv[j] = mul2(dv[j], xv[j]);
+      put8(sd + row * CB + 8 * vec, dv);
+      put8(su + row * CB + 8 * vec, xv);
     }
 #pragma unroll
     for (int i = 0; i < F::NB; ++i) {
       const int idx = tid + i * kThreads;
       if (idx < (OUT ? 2 : 1) * TT * S / 8) {
-        float v[8];
-        br[i].get(v);
-        store_twice(sbc + 16 * idx, v);
+        uint64_t v[4];
+        pairs_of(br[i], v);
+        if (S == 64 && (idx & 4)) {   // see pairs()
+          const uint64_t w[4] = {v[2], v[3], v[0], v[1]};
+          put8(sbc + 8 * idx, w);
+        } else {
+          put8(sbc + 8 * idx, v);
+        }
       }
     }
     Raw8<T> xo[F::NV], go[F::NV];   // kept for the tile's outputs
@@ -151,43 +148,39 @@ gdn_ssm_scan_kernel(const Params p) {
     __syncthreads();
     if (t0 + TT < s.len) fetch(t0 + TT);
 
-    uint64_t part[2] = {0ull, 0ull};
+    float part[CPT] = {};
     const int steps = (cnt + 3) & ~3;   // (rows past the last token are zeros: no change)
 #pragma unroll 4
     for (int t = 0; t < steps; ++t) {
-      const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
-      const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
-      const Pairs b0 = lds2(sbc + t * 2 * S + 8 * sl), b1 = lds2(sbc + t * 2 * S + 8 * sl + 4);
-      const uint64_t bb[4] = {b0.a, b0.b, b1.a, b1.b};
-      uint64_t cc[4];
-      if constexpr (OUT) {
-        const float *at = sbc + TT * S * 2 + t * 2 * S + 8 * sl;
-        const Pairs c0 = lds2(at), c1 = lds2(at + 4);
-        cc[0] = c0.a; cc[1] = c0.b; cc[2] = c1.a; cc[3] = c1.b;
-      }
-      uint64_t y[2];
+      uint64_t d[CPT], u[CPT], b2[NP], c2[NP];
+      twice<CPT>(sd + t * CB + cl, d);
+      twice<CPT>(su + t * CB + cl, u);
+      pairs<NP>(sbc + t * S + 16 * sl, swap, b2);
+      if constexpr (OUT) pairs<NP>(sbc + TT * S + t * S + 16 * sl, swap, c2);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < CPT; ++k) {
+        uint64_t y[2];   // two sums: half the chain of dependent additions
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t a = ex2_pair(mul2(dd[k], A[k][j]));
-          h[k][j] = fma2(a, h[k][j], mul2(uu[k], bb[j]));
-          if constexpr (OUT) y[k] = j ? fma2(cc[j], h[k][j], y[k]) : mul2(cc[j], h[k][j]);
+        for (int i = 0; i < NP; ++i) {
+          uint64_t &e = h[k * NP + i];
+          e = fma2(decay(d[k], A[k * NP + i]), e, mul2(u[k], b2[i]));
+          if constexpr (OUT) y[i & 1] = i > 1 ? fma2(c2[i], e, y[i & 1]) : mul2(c2[i], e);
         }
-        if constexpr (!OUT) part[k] = add2(part[k], dd[k]);
-      }
-      if constexpr (OUT) {
-        float v[4];
-        unpk(y[0], v[0], v[1]);
-        unpk(y[1], v[2], v[3]);
-        sum_channels<LS>(v, sl);
-        store_channels<LS>(sy + t * CB + 4 * cl, v, sl);
+        if constexpr (OUT) {
+          float v = total(add2(y[0], y[1]));
+#pragma unroll
+          for (int m = 1; m < LS; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+          if (LS == 1 || sl == 0) sy[t * CB + cl + k] = v;
+        } else {
+          float lo, hi;
+          unpk(d[k], lo, hi);
+          part[k] += lo;
+        }
       }
     }
-    if constexpr (!OUT) {   // a sum of sums over tiles: no long run of one accumulator
-      total[0] = add2(total[0], part[0]);
-      total[1] = add2(total[1], part[1]);
-    }
+    if constexpr (!OUT)   // a sum of sums over tiles: no long run of one accumulator
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) sums[k] += part[k];
     __syncthreads();
     if constexpr (OUT) {
       T *y = static_cast<T *>(p.y) + (s.start + t0) * p.D + vch;
@@ -195,37 +188,31 @@ gdn_ssm_scan_kernel(const Params p) {
       for (int i = 0; i < F::NV; ++i) {
         const int row = tid / F::VB + i * (kThreads / F::VB);
         if (!von || row >= cnt) continue;
-        float xv[8], gv[8], yv[8];
-        xo[i].get(xv);
-        const float4 *at = reinterpret_cast<const float4 *>(sy + row * CB + 8 * vec);
-        const float4 lo = at[0], hi = at[1];
-        yv[0] = lo.x; yv[1] = lo.y; yv[2] = lo.z; yv[3] = lo.w;
-        yv[4] = hi.x; yv[5] = hi.y; yv[6] = hi.z; yv[7] = hi.w;
-        if (p.d_skip)   // (an infinite x has no part in y without a skip)
+        uint64_t v[4], yv[4];
+        take8(sy + row * CB + 8 * vec, yv);
+        if (p.d_skip) {   // (an infinite x has no part in y without a skip)
+          pairs_of(xo[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) yv[j] = fmaf(skip[j], xv[j], yv[j]);
+          for (int j = 0; j < 4; ++j) yv[j] = fma2(skip[j], v[j], yv[j]);
+        }
         if (gate) {
-          go[i].get(gv);
+          pairs_of(go[i], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) yv[j] *= gv[j] * sigmoid(gv[j]);
+          for (int j = 0; j < 4; ++j) yv[j] = mul2(yv[j], mul2(v[j], sigmoid2(v[j])));
         }
         Raw8<T> out;
-        out.set(yv);
+        set_pairs(out, yv);
         out.store(y + (int64_t)row * p.D);
       }
     }
   }
   if (!OUT) {
-    store_own<S>(p.seg_x + slot * state, own, h);
-    if (own.on && sl == 0) {
-      float v[4];
-      unpk(total[0], v[0], v[1]);
-      unpk(total[1], v[2], v[3]);
-      *reinterpret_cast<float4 *>(p.seg_d + (int64_t)slot * p.D + own.ch) =
-          make_float4(v[0], v[1], v[2], v[3]);
-    }
+    store16(p.seg_x + slot * state + own, on, h);
+    if (on && sl == 0)
+#pragma unroll
+      for (int k = 0; k < CPT; ++k) p.seg_d[(int64_t)slot * p.D + first_ch + cl + k] = sums[k];
   } else if (p.hT && s.seg == s.count - 1) {
-    store_own<S>(p.hT + s.n * state, own, h);
+    store16(p.hT + s.n * state + own, on, h);
   }
 }
 

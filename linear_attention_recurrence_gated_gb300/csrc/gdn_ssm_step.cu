@@ -36,10 +36,11 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16 *p) {
 template <typename T, int S, int SEQS>
 __global__ void __launch_bounds__(kStepThreads)
 gdn_ssm_step_kernel(const StepParams p) {
-  constexpr int LS = S / 4, CH = kStepThreads / LS;
+  constexpr int LS = S / 4, CH = kStepThreads / LS, PER = (SEQS + LS - 1) / LS;
+  constexpr uint32_t kAll = 0xffffffffu;
   const int tid = threadIdx.x, sl = tid % LS, ch = blockIdx.x * CH + tid / LS;
   const bool on = ch < p.D;
-  const int n0 = blockIdx.y * SEQS;
+  const int n0 = blockIdx.y * SEQS, lane0 = (tid & 31) - sl;
   const int64_t at = (int64_t)ch * S + 4 * sl;
 
   float4 h[SEQS];
@@ -58,44 +59,71 @@ gdn_ssm_step_kernel(const StepParams p) {
     h[i] = on && good && p.s_in ? four(p.s_in + page[i] * p.page_stride + at)
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float4 al = on ? four(p.A_log + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 A = make_float4(rate(al.x), rate(al.y), rate(al.z), rate(al.w));
+  // The steps of sequences n0 + sl, n0 + sl + LS, ...: the LS lanes of a channel share them.
   const float bias = on && p.dt_bias ? p.dt_bias[ch] : 0.f;
   const float skip = on && p.d_skip ? p.d_skip[ch] : 0.f;
+  const int64_t tok = (int64_t)(n0 + sl) * p.D + ch;
+  float x[PER], d[PER], gate[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const bool go = on && sl + k * LS < SEQS && n0 + sl + k * LS < p.num_seqs;
+    const int64_t i = tok + (int64_t)k * LS * p.D;
+    x[k] = go ? to_f32(static_cast<const T *>(p.x)[i]) : 0.f;
+    d[k] = go ? to_f32(static_cast<const T *>(p.dt)[i]) + bias : 0.f;
+    gate[k] = go && p.gate ? to_f32(static_cast<const T *>(p.gate)[i]) : 0.f;
+  }
+  const float4 al = on ? four(p.A_log + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 A = make_float4(rate(al.x), rate(al.y), rate(al.z), rate(al.w));
+  if (p.softplus) {
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) {
+      float a, b;
+      unpk(softplus2<T>(pk(d[k], k + 1 < PER ? d[k + 1] : 0.f)), a, b);
+      d[k] = a;
+      if (k + 1 < PER) d[k + 1] = b;
+    }
+  }
   const int group = on ? ch / p.Dg : 0;
+  const T *b = static_cast<const T *>(p.b) + ((int64_t)n0 * p.G + group) * S + 4 * sl;
+  const T *c = static_cast<const T *>(p.c) + ((int64_t)n0 * p.G + group) * S + 4 * sl;
+  const int next = p.G * S;
+  float sum[SEQS];
 #pragma unroll
   for (int i = 0; i < SEQS; ++i) {
-    const int n = n0 + i;
-    const bool go = on && n < p.num_seqs;
-    float sum = 0.f, x = 0.f;
-    if (go && page[i] >= 0) {
-      const int64_t tok = (int64_t)n * p.D + ch, bc = ((int64_t)n * p.G + group) * S + 4 * sl;
-      x = to_f32(static_cast<const T *>(p.x)[tok]);
-      const float v = to_f32(static_cast<const T *>(p.dt)[tok]) + bias;
-      const float d = p.softplus ? softplus<T>(v) : v, u = d * x;
-      const float4 b = four(static_cast<const T *>(p.b) + bc), c = four(static_cast<const T *>(p.c) + bc);
-      float4 s = h[i];
-      s.x = fmaf(ex2(d * A.x), s.x, u * b.x);
-      s.y = fmaf(ex2(d * A.y), s.y, u * b.y);
-      s.z = fmaf(ex2(d * A.z), s.z, u * b.z);
-      s.w = fmaf(ex2(d * A.w), s.w, u * b.w);
-      *reinterpret_cast<float4 *>(p.s_out + page[i] * p.page_stride + at) = s;
-      sum = fmaf(c.x, s.x, c.y * s.y) + fmaf(c.z, s.z, c.w * s.w);
-    }
+    const float di = __shfl_sync(kAll, d[i / LS], lane0 + i % LS);
+    const float ui = di * __shfl_sync(kAll, x[i / LS], lane0 + i % LS);
+    sum[i] = 0.f;
+    if (!on || page[i] < 0) continue;
+    const float4 bv = four(b + i * next), cv = four(c + i * next);
+    float4 s = h[i];
+    s.x = fmaf(ex2(fmaf(di, A.x, kLift)), s.x, ui * bv.x);
+    s.y = fmaf(ex2(fmaf(di, A.y, kLift)), s.y, ui * bv.y);
+    s.z = fmaf(ex2(fmaf(di, A.z, kLift)), s.z, ui * bv.z);
+    s.w = fmaf(ex2(fmaf(di, A.w, kLift)), s.w, ui * bv.w);
+    *reinterpret_cast<float4 *>(p.s_out + page[i] * p.page_stride + at) = s;
+    sum[i] = fmaf(cv.x, s.x, cv.y * s.y) + fmaf(cv.z, s.z, cv.w * s.w);
+  }
+  // c . h of a sequence to the lane that holds its step
 #pragma unroll
-    for (int m = 1; m < LS; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (go && sl == 0) {
-      const int64_t tok = (int64_t)n * p.D + ch;
-      float y = sum;
-      if (page[i] >= 0) {
-        if (p.d_skip) y = fmaf(skip, x, y);
-        if (p.gate) {
-          const float g = to_f32(static_cast<const T *>(p.gate)[tok]);
-          y *= g * sigmoid(g);
-        }
+  for (int i = 0; i < SEQS; ++i)
+#pragma unroll
+    for (int m = 1; m < LS; m *= 2) sum[i] += __shfl_xor_sync(kAll, sum[i], m);
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    float y = 0.f;
+    int mine = -1;
+#pragma unroll
+    for (int i = 0; i < SEQS; ++i)
+      if (i == sl + k * LS) {
+        y = sum[i];
+        mine = page[i];
       }
-      store_out(static_cast<T *>(p.y) + tok, y);
+    if (!on || sl + k * LS >= SEQS || n0 + sl + k * LS >= p.num_seqs) continue;
+    if (mine >= 0) {
+      if (p.d_skip) y = fmaf(skip, x[k], y);
+      if (p.gate) y *= gate[k] * sigmoid(gate[k]);
     }
+    store_out(static_cast<T *>(p.y) + tok + (int64_t)k * LS * p.D, y);
   }
 }
 
