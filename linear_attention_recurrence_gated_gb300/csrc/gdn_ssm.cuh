@@ -215,10 +215,12 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   return pk(ex2(lo), ex2(hi));
 }
 // exp(delta A) of a token.  The hardware's exp2 is low by 2e-8 on average for arguments
-// of -0.1 to 0 (measured over 10^6 arguments a range: -1.7e-8 to -2.6e-8), which a state
-// that lasts a thousand tokens would add up to 2e-5; kLift in the exponent takes the mean
-// away (below 1.3e-8 there; 2^kLift itself still gives 1, so that delta = 0 keeps a state).
-constexpr float kLift = 2e-8f;
+// of -0.1 to -0.001 (measured over 10^6 arguments a range: -1.4e-8 to -2.6e-8), which a
+// state that lasts a thousand tokens would add up to 2e-5.  kLift in the exponent takes
+// most of it away (-0.7e-8 to -1.6e-8 there, +0.5e-8 for arguments of -0.001 and less:
+// larger values of it make the longest memories worse); 2^kLift itself still gives 1, so
+// that delta = 0 keeps a state.
+constexpr float kLift = 1.5e-8f;
 __device__ __forceinline__ uint64_t decay(uint64_t delta, uint64_t A) {
   return ex2_pair(fma2(delta, A, pk(kLift, kLift)));
 }

@@ -37,6 +37,7 @@ struct BwdParams : Params {
   float *ckpt_d;     // [tokens / kL][D] sum of delta since the segment's start
   float *part_bc;    // [block][token][G][2][S]
   float *part_w;     // [gridDim.y][D S + 2 D] sums for dA, dD_skip, ddt_bias
+  float *own_w;      // [CTA][2][16][thread] a thread's sums for them so far
   int32_t G, parts;
   __host__ __device__ int64_t rows() const {
     return seq.cu ? seq.seq_len : seq.seq_len * seq.num_seqs;
@@ -191,7 +192,15 @@ gdn_ssm_keep_kernel(const BwdParams p) {
     if (t0 + TT < len)
       in.fetch(p, s.start + t0 + TT, (int)(len - t0 - TT < TT ? len - t0 - TT : TT), group, vch, von);
     for (int r = 0; r < cnt; r += kL) {
-      if (t0 + r > 0) keep(t0 + r);
+      if (t0 + r > 0) {
+        keep(t0 + r);
+        if constexpr (CUT)   // the product so far, from the sum: kL factors' roundings at most
+#pragma unroll
+          for (int k = 0; k < CPT; ++k)
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+              P[k * NP + i] = ex2_pair(mul2(pk(sums[k], sums[k]), A[k * NP + i]));
+      }
       float part[CPT] = {};
 #pragma unroll 4
       for (int t = r; t < r + kL; ++t) {   // (tokens past the last: zeros)
@@ -230,8 +239,7 @@ gdn_ssm_keep_kernel(const BwdParams p) {
     return;
   }
   if (!last) store16(p.seg_x + slot * state + own, on, h);
-  if constexpr (CUT)
-    if (s.seg > 0) store16(p.seg_y + slot * state + own, on, Y);
+  if constexpr (CUT) store16(p.seg_y + slot * state + own, on, Y);
   if (on && sl == 0)
 #pragma unroll
     for (int k = 0; k < CPT; ++k) p.seg_d[(int64_t)slot * D + first_ch + cl + k] = sums[k];
@@ -268,25 +276,42 @@ __device__ __forceinline__ int sum_groups(float (&v)[8], int grp) {
 // Shared memory of the second launch, in floats.
 template <typename T, int S>
 struct Bwd {
-  static constexpr int CB = Geo<S>::CB, TILE = kL * CB, OWN = 16 * kThreads;
-  static constexpr int kRaw = Inputs<T, S, kL, true>::NV * kThreads * 8 * sizeof(T) / 4;
+  static constexpr int CB = Geo<S>::CB, VB = CB / 8, RT = kThreads / VB, TILE = kL * CB, OWN = 16 * kThreads;
+  static constexpr int NV = (kL + RT - 1) / RT;             // a thread's vectors of x, dt, dy, gate
+  static constexpr int NBC = 2 * kL * S / 8, NB = (NBC + kThreads - 1) / kThreads;   // ... of b and c
+  static constexpr int VEC = kThreads * 8 * sizeof(T) / 4;  // a vector of every thread
   static constexpr int D = 0, U = D + TILE, E = U + TILE;   // delta; delta x, later q; ds, later sum A w
   static constexpr int Y = E + TILE, BC = Y + TILE;         // c . h; b and c, each value twice
   static constexpr int RED = BC + 4 * kL * S;               // the warps' sums for db and dc
   static constexpr int START = RED + 4 * kL * 2 * S;        // a thread's states at the segment's start
-  static constexpr int DA = START + OWN;                    // ... sums for dA
-  static constexpr int SUM = DA + OWN;                      // ... for dD_skip and ddt_bias: [2][16]
-  static constexpr int RAW = SUM + 2 * OWN;                 // the tile's x, dt, dy and gate
-  static constexpr size_t kFloats = RAW + 4 * kRaw + 4;     // (and the place in tensor memory)
+  static constexpr int SUM = START + OWN;                   // ... sums for dD_skip and ddt_bias
+  static constexpr int KEPT = SUM + OWN;                    // ... kept states of the next tile
+  static constexpr int RAW = KEPT + OWN;                    // inputs of this tile and the next
+  static constexpr int TILE_RAW = (4 * NV + NB) * VEC;
+  static constexpr size_t kFloats = RAW + 2 * TILE_RAW + 4; // (and the place in tensor memory)
+  static constexpr int kCtas = 3 * (4 * kFloats + 1024) <= 228 * 1024 ? 3 : 2;   // an SM
 };
 constexpr uint32_t kColumns = 16 * kL;   // of tensor memory: a thread's 16 values for each token
 
+// 16 bytes from global to shared memory, zeros where there are none.
+__device__ __forceinline__ void copy16(void *to, const void *from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(there ? 16 : 0)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void copy_vec(Raw8<T> *to, const T *from, bool there) {
+  copy16(to, from, there);
+  if constexpr (sizeof(T) == 4)
+    copy16(reinterpret_cast<float *>(to) + 4, reinterpret_cast<const float *>(from) + 4, there);
+}
+
 // Second launch: tiles from the last token to the first.
 template <typename T, int S, bool GATE>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, Bwd<T, S>::kCtas)
 gdn_ssm_grad_kernel(const BwdParams p) {
   using B = Bwd<T, S>;
-  using In = Inputs<T, S, kL, true>;
   constexpr int CB = B::CB, LS = Geo<S>::LS, CL = Geo<S>::CL;
   extern __shared__ __align__(16) float smem[];
   float *sd = smem + B::D, *su = smem + B::U, *ss = smem + B::E, *sy = smem + B::Y, *sbc = smem + B::BC;
@@ -335,35 +360,69 @@ gdn_ssm_grad_kernel(const BwdParams p) {
   for (int k = 0; k < 2; ++k)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dA[k][j] = 0ull;
-  put16(smem + B::DA, dA);
   put16(smem + B::SUM, dA);
-  put16(smem + B::SUM + B::OWN, dA);
-  const int vec = tid % In::VB, vch = first_ch + 8 * vec;
+  const int vec = tid % B::VB, vch = first_ch + 8 * vec;
   const bool von = vch < end_ch;
+  // The inputs of a tile, and the states kept before it, on their way to shared memory;
+  // every thread waits for its own.
+  const auto raw = [&](int64_t tile, int i) {
+    return reinterpret_cast<Raw8<T> *>(smem + B::RAW + (tile & 1) * B::TILE_RAW + i * B::VEC) + tid;
+  };
+  const auto fetch = [&](int64_t tile, int64_t first, int cnt, const float *kept_at) {
+#pragma unroll
+    for (int i = 0; i < B::NV; ++i) {
+      const int row = tid / B::VB + i * B::RT;
+      const bool there = von && row < cnt;
+      const int64_t at = there ? first + row : 0;
+      const int c = there ? vch : 0;
+      copy_vec(raw(tile, 4 * i), static_cast<const T *>(p.x) + at * p.sx + c, there);
+      copy_vec(raw(tile, 4 * i + 1), static_cast<const T *>(p.dt) + at * p.sdt + c, there);
+      copy_vec(raw(tile, 4 * i + 2), static_cast<const T *>(p.dy) + at * D + c, there);
+      if (GATE) copy_vec(raw(tile, 4 * i + 3), static_cast<const T *>(p.gate) + at * p.sg + c, there);
+    }
+#pragma unroll
+    for (int i = 0; i < B::NB; ++i) {
+      const int idx = tid + i * kThreads, row = idx % (B::NBC / 2) / (S / 8), v = idx % (S / 8);
+      const bool there = idx < B::NBC && row < cnt;
+      const int64_t at = there ? first + row : 0;
+      const T *from = idx < B::NBC / 2 ? static_cast<const T *>(p.b) + at * p.sb
+                                       : static_cast<const T *>(p.c) + at * p.sc;
+      copy_vec(raw(tile, 4 * B::NV + i), from + group * S + 8 * v, there);
+    }
+    if (kept_at)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // channel i of the thread's four
+        copy16(smem + B::KEPT + 4 * (i * kThreads + tid),
+               own.on ? kept_at + (int64_t)(own.ch + i) * S + own.st : p.A_log, own.on);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // A thread's sums, for dA and for dD_skip and ddt_bias, run over 16 tiles at most; then
+  // they join those before, in the workspace.
   int tiles_summed = 0;
-  const auto flush = [&] {   // at most 16 tiles in one run of an accumulator
-    uint64_t sum[2][4];
-    get16(smem + B::DA, sum);
+  bool joined = false;
+  float *before_sums = p.own_w + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * B::OWN;
+  const auto joint = [&](const float *at, uint64_t (&a)[2][4]) {
+    if (!joined) return;
+    uint64_t b[2][4];
+    get16(at, b);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum[k][j] = add2(sum[k][j], dA[k][j]);
-        dA[k][j] = 0ull;
-      }
-    put16(smem + B::DA, sum);
+      for (int j = 0; j < 4; ++j) a[k][j] = add2(a[k][j], b[k][j]);
+  };
+  const auto flush = [&] {
+    joint(before_sums, dA);
+    put16(before_sums, dA);
     uint64_t some[2][4];
     get16(smem + B::SUM, some);
-    get16(smem + B::SUM + B::OWN, sum);
+    joint(before_sums + B::OWN, some);
+    put16(before_sums + B::OWN, some);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum[k][j] = add2(sum[k][j], some[k][j]);
-        some[k][j] = 0ull;
-      }
-    put16(smem + B::SUM, some);
-    put16(smem + B::SUM + B::OWN, sum);
+      for (int j = 0; j < 4; ++j) dA[k][j] = 0ull;
+    put16(smem + B::SUM, dA);
+    joined = true;
     tiles_summed = 0;
   };
   wait_first();
@@ -373,10 +432,24 @@ gdn_ssm_grad_kernel(const BwdParams p) {
     lin::Span s;
     if (!lin::span_of(p.seq, slot, 0, s)) continue;
     const int64_t begin = s.start - s.seg * p.seq.seg_len, off = s.seg * p.seq.seg_len;
+    const int64_t tiles = (s.len + kL - 1) / kL;
+    const auto kept_at = [&](int64_t tile) {
+      return tile ? p.ckpt + kept(begin, off + tile * kL) * state : nullptr;
+    };
+    if (tiles > 0)
+      fetch(tiles - 1, s.start + (tiles - 1) * kL, (int)(s.len - (tiles - 1) * kL), kept_at(tiles - 1));
     // the gradient that comes from behind the segment, and the state at its start
     load_own<S>(p.dhT ? p.dhT + s.n * state : nullptr, own, g);
     for (int i = s.count - 1; i > s.seg; --i)
       join<S>(g, A, p.seg_y, p.seg_d, slot - s.seg + i, p.D, own);
+    if (p.dh0 && s.seg == 0 && s.count > 1) {   // (not through the segment's hundreds of roundings)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[k][j] = g[k][j];
+      join<S>(h, A, p.seg_y, p.seg_d, slot, p.D, own);
+      store_own<S>(p.dh0 + s.n * state, own, h);
+    }
     if (s.seg == 0) {
       load_own<S>(p.h0 ? p.h0 + s.n * state : nullptr, own, h);
     } else {
@@ -386,47 +459,75 @@ gdn_ssm_grad_kernel(const BwdParams p) {
     }
     put16(smem + B::START, h);
 
-    const int64_t tiles = (s.len + kL - 1) / kL;
-    In in;
-    if (tiles > 0)
-      in.fetch(p, s.start + (tiles - 1) * kL, (int)(s.len - (tiles - 1) * kL), group, vch, von);
     for (int64_t tile = tiles - 1; tile >= 0; --tile) {
       const int64_t t0 = tile * kL;
       const int cnt = (int)(s.len - t0 < kL ? s.len - t0 : kL);
-      in.form(p, cnt, vch, von, sd, su, ss);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      // delta, delta x and ds of the tile; tokens that do not exist are zeros, which leave
+      // states and gradients as they are
+      uint64_t bias[4], skip[4];
+      load8(p.dt_bias, vch, von, bias);
 #pragma unroll
-      for (int i = 0; i < In::NB; ++i) {
+      for (int i = 0; i < B::NV; ++i) {
+        const int row = tid / B::VB + i * B::RT;
+        if (row >= kL) continue;
+        uint64_t v[4], d[4];
+        steps_of(*raw(tile, 4 * i + 1), bias, p.softplus, d);
+        if (row >= cnt) d[0] = d[1] = d[2] = d[3] = 0ull;
+        pairs_of(*raw(tile, 4 * i), v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = mul2(d[j], v[j]);
+        put8(sd + row * CB + 8 * vec, d);
+        put8(su + row * CB + 8 * vec, v);
+        pairs_of(*raw(tile, 4 * i + 2), d);
+        if constexpr (GATE) {
+          pairs_of(*raw(tile, 4 * i + 3), v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = mul2(d[j], mul2(v[j], sigmoid2(v[j])));
+        }
+        put8(ss + row * CB + 8 * vec, d);
+      }
+#pragma unroll
+      for (int i = 0; i < B::NB; ++i) {
         const int idx = tid + i * kThreads;
-        if (idx >= In::NBC) continue;
+        if (idx >= B::NBC) continue;
         float v[8];
-        in.bc[i].get(v);
+        raw(tile, 4 * B::NV + i)->get(v);
         store_twice<S>(sbc, idx, v);
       }
-      Raw8<T> *raw = reinterpret_cast<Raw8<T> *>(smem + B::RAW) + tid;   // for the tile's gradients
-#pragma unroll
-      for (int i = 0; i < In::NV; ++i) {
-        raw[(4 * i) * kThreads] = in.x[i];
-        raw[(4 * i + 1) * kThreads] = in.dt[i];
-        raw[(4 * i + 2) * kThreads] = in.dy[i];
-        if (GATE) raw[(4 * i + 3) * kThreads] = in.gate[i];
-      }
-      __syncthreads();
-      if (tile > 0) in.fetch(p, s.start + t0 - kL, kL, group, vch, von);
+      // the state before the tile
       if (tile == 0) {
         get16(smem + B::START, h);
       } else {
-        const int64_t at = kept(begin, off + t0);
-        if (s.seg > 0) {
+        float v[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 f = *reinterpret_cast<const float4 *>(smem + B::KEPT + 4 * (i * kThreads + tid));
+          v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
+        }
+        if (s.seg == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[k][j] = pk(v[2 * k][j], v[2 * k + 1][j]);
+        } else {   // kept from zero: and what the segment's start has become
           get16(smem + B::START, h);
-          join<S>(h, A, p.ckpt, p.ckpt_d, at, p.D, own);
-        } else {
-          load_own<S>(p.ckpt + at * state, own, h);
+          const float4 sum = own.on ? *reinterpret_cast<const float4 *>(
+                                          p.ckpt_d + kept(begin, off + t0) * D + own.ch)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          const uint64_t past[2] = {pk(sum.x, sum.y), pk(sum.z, sum.w)};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              h[k][j] = fma2(ex2_pair(mul2(past[k], A[k][j])), h[k][j], pk(v[2 * k][j], v[2 * k + 1][j]));
         }
       }
+      __syncthreads();
+      if (tile > 0) fetch(tile - 1, s.start + t0 - kL, kL, kept_at(tile - 1));
       // the tile's states
-#pragma unroll 2
-      for (int t = 0; t < cnt; ++t) {
-        __syncwarp();
+#pragma unroll 4
+      for (int t = 0; t < kL; ++t) {
         store_tm(t, h);
         const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);
         const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b};
@@ -446,15 +547,15 @@ gdn_ssm_grad_kernel(const BwdParams p) {
           unpk(y[1], v[2], v[3]);
           sum_channels<LS>(v, sl);
           store_channels<LS>(sy + t * CB + 4 * cl, v, sl);
+          __syncwarp();
         }
       }
-      __syncwarp();
       ptx::tmem_wait_st();
       // and backward through them
       uint32_t ahead[16];
-      load_tm(cnt - 1, ahead);
-#pragma unroll 2
-      for (int t = cnt - 1; t >= 0; --t) {
+      load_tm(kL - 1, ahead);
+#pragma unroll 4
+      for (int t = kL - 1; t >= 0; --t) {
         const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl),
                     e = lds2(ss + t * CB + 4 * cl);
         const uint64_t dd[2] = {d.a, d.b}, uu[2] = {u.a, u.b}, ee[2] = {e.a, e.b};
@@ -504,34 +605,39 @@ gdn_ssm_grad_kernel(const BwdParams p) {
             const int id = first + i;   // 0-3: db of its states, 4-7: dc
             red[(id >> 2) * S + 4 * sl + (id & 3)] = r[i];
           }
+        __syncwarp();
       }
       __syncthreads();
-      // db and dc of this CTA's channels
-      for (int i = tid; i < cnt * 2 * S; i += kThreads) {
+      // db and dc of this CTA's channels, four values a thread
+      for (int i = 4 * tid; i < cnt * 2 * S; i += 4 * kThreads) {
         const int row = i / (2 * S), at = i % (2 * S);
-        const float *red = smem + B::RED;
-        float sum = 0.f;
+        const float *red = smem + B::RED + row * 2 * S + at;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) sum += red[(w * kL + row) * 2 * S + at];
-        p.part_bc[(((int64_t)cb * p.rows() + s.start + t0 + row) * p.G + group) * 2 * S + at] = sum;
+        for (int w = 0; w < kThreads / 32; ++w) {
+          const float4 v = *reinterpret_cast<const float4 *>(red + w * kL * 2 * S);
+          sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+        }
+        *reinterpret_cast<float4 *>(
+            p.part_bc + (((int64_t)cb * p.rows() + s.start + t0 + row) * p.G + group) * 2 * S + at) = sum;
       }
-      uint64_t bias[4], skip[4], sums[2][4];   // sums: for dD_skip and ddt_bias
+      uint64_t sums[2][4];   // for dD_skip and ddt_bias
       load8(p.dt_bias, vch, von, bias);
       load8(p.d_skip, vch, von, skip);
       get16(smem + B::SUM, sums);
 #pragma unroll
-      for (int i = 0; i < In::NV; ++i) {
-        const int row = tid / In::VB + i * In::RT;
+      for (int i = 0; i < B::NV; ++i) {
+        const int row = tid / B::VB + i * B::RT;
         if (!von || row >= cnt) continue;
         const int64_t out = (s.start + t0 + row) * D + vch;
         const int at = row * CB + 8 * vec;
         uint64_t xv[4], yv[4], qv[4], v[4], o[4];
         Raw8<T> r;
-        pairs_of(raw[(4 * i) * kThreads], xv);
-        pairs_of(raw[(4 * i + 2) * kThreads], yv);
+        pairs_of(*raw(tile, 4 * i), xv);
+        pairs_of(*raw(tile, 4 * i + 2), yv);
         if constexpr (GATE) {
           uint64_t gv[4];
-          pairs_of(raw[(4 * i + 3) * kThreads], gv);
+          pairs_of(*raw(tile, 4 * i + 3), gv);
           take8(sy + at, v);
           if (p.d_skip)
 #pragma unroll
@@ -557,7 +663,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         r.store(static_cast<T *>(p.dx) + out);
         take8(ss + at, v);
         uint64_t tv[4];
-        pairs_of(raw[(4 * i + 1) * kThreads], tv);
+        pairs_of(*raw(tile, 4 * i + 1), tv);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // (rates carry log2 e)
           o[j] = fma2(xv[j], qv[j], mul2(pk(0.6931471805599453f, 0.6931471805599453f), v[j]));
@@ -571,28 +677,28 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       if (++tiles_summed == 16) flush();
       __syncthreads();
     }
-    if (p.dh0 && s.seg == 0) store_own<S>(p.dh0 + s.n * state, own, g);
+    if (p.dh0 && s.count == 1) store_own<S>(p.dh0 + s.n * state, own, g);
   }
 
   // this CTA's sums over its tokens
-  flush();
-  get16(smem + B::DA, dA);
+  joint(before_sums, dA);
   float *part = p.part_w + (int64_t)blockIdx.y * (state + 2 * D);
   store_own<S>(part, own, dA);
   uint64_t sums[2][4];
-  get16(smem + B::SUM + B::OWN, sums);
+  get16(smem + B::SUM, sums);
+  joint(before_sums + B::OWN, sums);
   __syncthreads();
   float *sum = smem;   // [2][rows of threads][CB]: 2048 floats
-  static_assert(2 * In::RT * CB <= B::START, "room for the sums");
+  static_assert(2 * B::RT * CB <= B::START, "room for the sums");
 #pragma unroll
   for (int which = 0; which < 2; ++which)
-    put8(sum + (which * In::RT + tid / In::VB) * CB + 8 * vec, sums[which]);
+    put8(sum + (which * B::RT + tid / B::VB) * CB + 8 * vec, sums[which]);
   __syncthreads();
   for (int i = tid; i < 2 * CB; i += kThreads) {
     const int which = i / CB, ch = i % CB;
     if (first_ch + ch >= end_ch) continue;
     float r = 0.f;
-    for (int k = 0; k < In::RT; ++k) r += sum[(which * In::RT + k) * CB + ch];
+    for (int k = 0; k < B::RT; ++k) r += sum[(which * B::RT + k) * CB + ch];
     part[state + which * D + first_ch + ch] = r;
   }
   if (warp == 0) ptx::tmem_dealloc(columns, kColumns);
@@ -657,7 +763,7 @@ gdn_ssm_sum_kernel(const BwdParams p, int S, int64_t bc_blocks) {
 
 // The arrays of the workspace behind the status word, in floats.
 struct Layout {
-  size_t x, y, d, ckpt, ckpt_d, bc, w, total;
+  size_t x, y, d, ckpt, ckpt_d, bc, w, own, total;
 };
 Layout layout(int64_t rows, int64_t D, int64_t S, int64_t groups, int64_t blocks, int64_t parts,
               const lin::Plan &pl) {
@@ -671,7 +777,8 @@ Layout layout(int64_t rows, int64_t D, int64_t S, int64_t groups, int64_t blocks
   l.ckpt_d = l.ckpt + (size_t)(rows / kL) * state;
   l.bc = l.ckpt_d + (slots ? (size_t)(rows / kL) * D : 0);
   l.w = l.bc + round((size_t)blocks * rows * groups * 2 * S);
-  l.total = l.w + (size_t)parts * (state + 2 * D);
+  l.own = l.w + (size_t)parts * (state + 2 * D);
+  l.total = l.own + (size_t)parts * groups * blocks * 2 * 16 * kThreads;
   return l;
 }
 constexpr double kFirst = 0.5;
@@ -845,6 +952,7 @@ gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const 
   p.ckpt_d = ws + l.ckpt_d;
   p.part_bc = ws + l.bc;
   p.part_w = ws + l.w;
+  p.own_w = ws + l.own;
   const cudaError_t err = dtype == GDN_F32 ? launch_t<float>(p, d_state, groups, s)
                                            : launch_t<__nv_bfloat16>(p, d_state, groups, s);
   return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;

@@ -1272,6 +1272,12 @@ def _row_stride(where, name, t):
     contiguous, the rows of a batch one after the other); 0: packed."""
     if t is None or t.is_contiguous():
         return 0
+    if t.dim() == 3:   # (the usual slice, with few calls)
+        s0, s1, s2 = t.stride()
+        B, T, width = t.shape
+        if s2 == 1 and s1 >= width and T > 1 and (B == 1 or s0 == T * s1) and \
+                s1 * t.element_size() % 16 == 0:
+            return s1
     B, T = t.shape[:2]
     width, run = 1, True
     for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
@@ -1285,24 +1291,28 @@ def _row_stride(where, name, t):
     return s
 
 
-def _specs_check(where, device, rows, dense):
-    """``rows`` and ``dense``: name -> (tensor or None, shape, dtype); those of ``dense`` are
-    contiguous."""
-    ok = True
-    for t, shape, dtype in rows.values():
-        if t is not None and not (t.dtype == dtype and t.shape == shape and
+def _rows_fit(device, shape, dtype, *tensors):
+    """Every tensor given has this shape and dtype and is on this device, at any stride."""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and
                                   t.get_device() == device and (device >= 0 or t.is_cuda)):
-            ok = False
-            break
-    if ok:
-        for t, shape, dtype in dense.values():
-            if t is not None and not (t.dtype == dtype and t.shape == shape and
-                                      t.get_device() == device and t.is_contiguous() and
-                                      (device >= 0 or t.is_cuda)):
-                ok = False
-                break
-    if ok:
-        return
+            return False
+    return True
+
+
+def _fit(device, shape, dtype, *tensors):
+    """... and contiguous."""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and
+                                  t.get_device() == device and t.is_contiguous() and
+                                  (device >= 0 or t.is_cuda)):
+            return False
+    return True
+
+
+def _misfit(where, device, rows, dense):
+    """Raise for the first tensor that does not fit.  ``rows`` and ``dense``: name ->
+    (tensor or None, shape, dtype); those of ``dense`` are contiguous."""
     for name, (t, _, _) in rows.items():
         if t is not None and not t.is_cuda:
             raise ValueError(f"{where}: {name} must be on a CUDA device")
@@ -1316,29 +1326,57 @@ def _specs_check(where, device, rows, dense):
     _explain(where, device, {n: e[0] for n, e in dense.items()}, dense)
 
 
-def _sequences(where, B, cu_seqlens):
-    if cu_seqlens is None:
-        return B
+def _grads_of(where, given, names):
+    """The tensors of ``grads`` in the order of ``names``."""
+    if not given:
+        return (None,) * len(names)
+    for n in given:
+        if n not in names:
+            raise ValueError(f"{where}: unknown gradient {n}")
+    return tuple(given.get(n) for n in names)
+
+
+def _sequences(where, cu_seqlens):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError(f"{where}: cu_seqlens must be int32 [N + 1]")
     return cu_seqlens.shape[0] - 1
 
 
-def _ssm_specs(where, x, dt, A_log, b, c, D_skip, gate, dt_bias, h0, cu_seqlens):
-    """Sizes of a scan's call, and the specs of its inputs."""
-    if x.dim() != 3 or b.dim() != 4 or A_log.dim() != 2:
+def _ssm_check(where, x, dt, A_log, b, c, D_skip, gate, dt_bias, h0, cu_seqlens, y, dx=None,
+               ddt=None, dgate=None, db=None, dc=None, dA=None, dskip=None, dbias=None, hT=None,
+               dh0=None):
+    """The sizes of a scan's call, whose tensors fit (y stands for d_y, hT for d_final_state
+    in the backward pass)."""
+    wide, thin = x.shape, b.shape
+    if len(wide) != 3 or len(thin) != 4 or A_log.dim() != 2:
         raise ValueError(f"{where}: x must be [B, T, D], b and c [B, T, G, S], A_log [D, S]")
-    B, T, D = x.shape
-    G, S = b.shape[2:]
-    dtype = x.dtype
+    B, T, D = wide
+    _, _, G, S = thin
+    dtype, dev = x.dtype, x.get_device()
+    N = B if cu_seqlens is None else _sequences(where, cu_seqlens)
+    if dtype in _CODES and thin[0] == B and thin[1] == T and \
+            _rows_fit(dev, wide, dtype, x, dt, gate) and _rows_fit(dev, thin, dtype, b, c) and \
+            _fit(dev, (D, S), _F32, A_log, dA) and \
+            _fit(dev, (D,), _F32, D_skip, dt_bias, dskip, dbias) and \
+            (h0 is hT is dh0 is None or _fit(dev, (N, D, S), _F32, h0, hT, dh0)) and \
+            (cu_seqlens is None or _fit(dev, (N + 1,), _I32, cu_seqlens)) and \
+            _fit(dev, wide, dtype, y, dx, ddt, dgate) and \
+            (db is dc is None or _fit(dev, thin, dtype, db, dc)):
+        return B, T, D, S, G, N, dev
     _dtype_code(dtype)
-    N = _sequences(where, B, cu_seqlens)
-    rows = dict(x=(x, x.shape, dtype), dt=(dt, x.shape, dtype), b=(b, (B, T, G, S), dtype),
-                c=(c, (B, T, G, S), dtype), gate=(gate, x.shape, dtype))
-    dense = dict(A_log=(A_log, (D, S), _F32), D_skip=(D_skip, (D,), _F32),
-                 dt_bias=(dt_bias, (D,), _F32), initial_state=(h0, (N, D, S), _F32),
-                 cu_seqlens=(cu_seqlens, (N + 1,), _I32))
-    return (B, T, D, S, G, N), rows, dense
+    rows = dict(x=(x, wide, dtype), dt=(dt, wide, dtype), b=(b, (B, T, G, S), dtype),
+                c=(c, (B, T, G, S), dtype), gate=(gate, wide, dtype))
+    dense = dict(cu_seqlens=(cu_seqlens, (N + 1,), _I32))
+    back = where.endswith("bwd")
+    for shape, kind, group in (
+            ((D, S), _F32, dict(A_log=A_log, dA_log=dA)),
+            ((D,), _F32, dict(D_skip=D_skip, dt_bias=dt_bias, dD_skip=dskip, ddt_bias=dbias)),
+            ((N, D, S), _F32, {"initial_state": h0, "dh0": dh0,
+                               "d_final_state" if back else "final_state": hT}),
+            (wide, dtype, {"d_y" if back else "y": y, "dx": dx, "ddt": ddt, "dgate": dgate}),
+            ((B, T, G, S), dtype, dict(db=db, dc=dc))):
+        dense.update({n: (t, shape, kind) for n, t in group.items()})
+    _misfit(where, dev, rows, dense)
 
 
 @functools.lru_cache(maxsize=256)
@@ -1368,11 +1406,8 @@ def gdn_ssm_fwd(x, dt, A_log, b, c, initial_state=None, cu_seqlens=None, *, D_sk
     ``initial_state``).  Returns ``(y, final_state)``.  With ``check=True`` the call
     synchronises and raises on a device-side error."""
     w = "gdn_ssm_fwd"
-    (B, T, D, S, G, N), rows, dense = _ssm_specs(w, x, dt, A_log, b, c, D_skip, gate, dt_bias,
-                                                 initial_state, cu_seqlens)
-    dense.update(y=(y, x.shape, x.dtype), final_state=(final_state, (N, D, S), _F32))
-    dev = x.get_device()
-    _specs_check(w, dev, rows, dense)
+    B, T, D, S, G, N, dev = _ssm_check(w, x, dt, A_log, b, c, D_skip, gate, dt_bias, initial_state,
+                                       cu_seqlens, y, hT=final_state)
     y = _like_new(stream, x) if y is None else y
     if final_state is None and output_final_state:
         final_state = _empty(stream, x, (N, D, S), _F32)
@@ -1397,31 +1432,31 @@ def gdn_ssm_bwd(x, dt, A_log, b, c, d_y, initial_state=None, cu_seqlens=None, d_
     ``ddt_bias`` None without the input); ``grads`` may supply them (one of the fp32 ones
     left out is not computed)."""
     w = "gdn_ssm_bwd"
-    (B, T, D, S, G, N), rows, dense = _ssm_specs(w, x, dt, A_log, b, c, D_skip, gate, dt_bias,
-                                                 initial_state, cu_seqlens)
-    given = grads or {}
-    dtype, wide, thin, state = x.dtype, x.shape, (B, T, G, S), (N, D, S)
-    kinds = dict(dx=(wide, dtype), ddt=(wide, dtype), db=(thin, dtype), dc=(thin, dtype),
-                 dgate=(wide, dtype), dA_log=((D, S), _F32), dD_skip=((D,), _F32),
-                 ddt_bias=((D,), _F32), dh0=(state, _F32))
-    dense.update(d_y=(d_y, wide, dtype), d_final_state=(d_final_state, state, _F32))
-    for n, t in given.items():
-        dense[n] = (t, *kinds[n])
-    dev = x.get_device()
-    _specs_check(w, dev, rows, dense)
+    dx, ddt, db, dc, dgate, dA, dskip, dbias, dh0 = _grads_of(
+        w, grads, ("dx", "ddt", "db", "dc", "dgate", "dA_log", "dD_skip", "ddt_bias", "dh0"))
+    B, T, D, S, G, N, dev = _ssm_check(
+        w, x, dt, A_log, b, c, D_skip, gate, dt_bias, initial_state, cu_seqlens, d_y, dx, ddt, dgate,
+        db, dc, dA, dskip, dbias, d_final_state, dh0)
     if grads is None:
-        left = {n for n, t in (("dgate", gate), ("dD_skip", D_skip), ("ddt_bias", dt_bias))
-                if t is None}
-        grads = {n: None if n in left else _empty(stream, x, *kind) for n, kind in kinds.items()}
+        dx, ddt = _like_new(stream, x), _like_new(stream, dt)
+        db, dc = _like_new(stream, b), _like_new(stream, c)
+        dgate = None if gate is None else _like_new(stream, gate)
+        dA = _like_new(stream, A_log)
+        dskip = None if D_skip is None else _like_new(stream, D_skip)
+        dbias = None if dt_bias is None else _like_new(stream, dt_bias)
+        dh0 = _empty(stream, x, (N, D, S), _F32)
+        grads = dict(dx=dx, ddt=ddt, db=db, dc=dc, dgate=dgate, dA_log=dA, dD_skip=dskip,
+                     ddt_bias=dbias, dh0=dh0)
+    elif dx is None or ddt is None or db is None or dc is None:
+        raise ValueError(f"{w}: grads must hold dx, ddt, db and dc")
     ws = _workspace(stream, x, workspace, gdn_ssm_bwd_workspace_size(N, T, D, S, G), check)
     st = _on(w, dev)(
         x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
         _p(gate), _p(dt_bias), _p(initial_state), _p(cu_seqlens), d_y.data_ptr(),
-        _p(d_final_state), grads["dx"].data_ptr(), grads["ddt"].data_ptr(), _p(grads.get("dA_log")),
-        grads["db"].data_ptr(), grads["dc"].data_ptr(), _p(grads.get("dD_skip")),
-        _p(grads.get("dgate")), _p(grads.get("ddt_bias")), _p(grads.get("dh0")), B, T, D, S, G, N,
-        _row_stride(w, "x", x), _row_stride(w, "dt", dt), _row_stride(w, "b", b),
-        _row_stride(w, "c", c), _row_stride(w, "gate", gate), _CODES[dtype],
+        _p(d_final_state), dx.data_ptr(), ddt.data_ptr(), _p(dA), db.data_ptr(), dc.data_ptr(),
+        _p(dskip), _p(dgate), _p(dbias), _p(dh0), B, T, D, S, G, N, _row_stride(w, "x", x),
+        _row_stride(w, "dt", dt), _row_stride(w, "b", b), _row_stride(w, "c", c),
+        _row_stride(w, "gate", gate), _CODES[x.dtype],
         GDN_DT_SOFTPLUS if dt_softplus else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(w, st, check, ws, stream)
@@ -1430,6 +1465,9 @@ def gdn_ssm_bwd(x, dt, A_log, b, c, d_y, initial_state=None, cu_seqlens=None, d_
 
 def _pool_check(where, device, name, t, shape, dtype, like=None):
     """A pool ``[P, ...]`` of contiguous pages at one stride; returns (pages, stride)."""
+    if like is None and t.dtype is dtype and t.dim() == len(shape) + 1 and t.shape[1:] == shape and \
+            t.get_device() == device and t.is_contiguous() and (device >= 0 or t.is_cuda):
+        return t.shape[0], 0
     if t.dtype != dtype or t.dim() != len(shape) + 1 or tuple(t.shape[1:]) != tuple(shape):
         raise ValueError(f"{where}: {name} must be {str(dtype).split('.')[-1]} [P, "
                          f"{', '.join(map(str, shape))}]")
@@ -1462,16 +1500,19 @@ def gdn_ssm_step(x, dt, A_log, b, c, state, pages=None, *, D_skip=None, gate=Non
     N, D = x.shape
     G, S = b.shape[1:]
     dtype, dev = x.dtype, x.get_device()
-    _dtype_code(dtype)
     if state_out is None:
         if state is None:
             raise ValueError(f"{w}: give state, or state_out")
         state_out = state
-    _specs_check(w, dev, {}, dict(
-        x=(x, x.shape, dtype), dt=(dt, x.shape, dtype), b=(b, (N, G, S), dtype),
-        c=(c, (N, G, S), dtype), gate=(gate, x.shape, dtype), A_log=(A_log, (D, S), _F32),
-        D_skip=(D_skip, (D,), _F32), dt_bias=(dt_bias, (D,), _F32), pages=(pages, (N,), _I32),
-        y=(y, x.shape, dtype)))
+    if not (dtype in _CODES and b.shape[0] == N and _fit(dev, x.shape, dtype, x, dt, gate, y) and
+            _fit(dev, b.shape, dtype, b, c) and _fit(dev, (D, S), _F32, A_log) and
+            _fit(dev, (D,), _F32, D_skip, dt_bias) and _fit(dev, (N,), _I32, pages)):
+        _dtype_code(dtype)
+        _misfit(w, dev, {}, dict(
+            x=(x, x.shape, dtype), dt=(dt, x.shape, dtype), b=(b, (N, G, S), dtype),
+            c=(c, (N, G, S), dtype), gate=(gate, x.shape, dtype), A_log=(A_log, (D, S), _F32),
+            D_skip=(D_skip, (D,), _F32), dt_bias=(dt_bias, (D,), _F32), pages=(pages, (N,), _I32),
+            y=(y, x.shape, dtype)))
     P, stride = _pool_check(w, dev, "state_out", state_out, (D, S), _F32)
     if state is not None and state is not state_out:
         _pool_check(w, dev, "state", state, (D, S), _F32, state_out)
@@ -1493,16 +1534,32 @@ def gdn_conv_workspace_size(num_seqs: int, seq_len: int, channels: int, taps: in
     return int(lib().gdn_conv_workspace_size(num_seqs, seq_len, channels, taps))
 
 
-def _conv_specs(where, x, w, bias, x_prev, cu_seqlens):
-    if x.dim() != 3 or w.dim() != 2:
+def _conv_check(where, x, w, bias, x_prev, cu_seqlens, y, dx=None, tail=None, dx_prev=None,
+                dw=None, dbias=None):
+    """The sizes of a convolution's call, whose tensors fit (y stands for d_y, tail for
+    d_x_tail in the backward pass)."""
+    wide = x.shape
+    if len(wide) != 3 or w.dim() != 2:
         raise ValueError(f"{where}: x must be [B, T, C], w [C, K]")
-    B, T, C = x.shape
+    B, T, C = wide
     K = w.shape[1]
-    _dtype_code(x.dtype)
-    N = _sequences(where, B, cu_seqlens)
-    return (B, T, C, K, N), dict(x=(x, x.shape, x.dtype)), dict(
-        w=(w, (C, K), _F32), bias=(bias, (C,), _F32), x_prev=(x_prev, (N, K - 1, C), x.dtype),
-        cu_seqlens=(cu_seqlens, (N + 1,), _I32))
+    dtype, dev = x.dtype, x.get_device()
+    N = B if cu_seqlens is None else _sequences(where, cu_seqlens)
+    end = (N, K - 1, C)
+    if dtype in _CODES and _rows_fit(dev, wide, dtype, x) and _fit(dev, (C, K), _F32, w, dw) and \
+            _fit(dev, (C,), _F32, bias, dbias) and \
+            (cu_seqlens is None or _fit(dev, (N + 1,), _I32, cu_seqlens)) and \
+            (x_prev is tail is dx_prev is None or _fit(dev, end, dtype, x_prev, tail, dx_prev)) and \
+            _fit(dev, wide, dtype, y, dx):
+        return B, T, C, K, N, dev
+    _dtype_code(dtype)
+    back = where.endswith("bwd")
+    _misfit(where, dev, dict(x=(x, wide, dtype)), {
+        "w": (w, (C, K), _F32), "bias": (bias, (C,), _F32), "x_prev": (x_prev, end, dtype),
+        "cu_seqlens": (cu_seqlens, (N + 1,), _I32), "dw": (dw, (C, K), _F32),
+        "dbias": (dbias, (C,), _F32), "d_y" if back else "y": (y, wide, dtype),
+        "dx": (dx, wide, dtype), "d_x_tail" if back else "x_tail": (tail, end, dtype),
+        "dx_prev": (dx_prev, end, dtype)})
 
 
 def gdn_conv_fwd(x, w, bias=None, x_prev=None, cu_seqlens=None, *, silu=True, y=None, x_tail=None,
@@ -1515,10 +1572,7 @@ def gdn_conv_fwd(x, w, bias=None, x_prev=None, cu_seqlens=None, *, silu=True, y=
     ``[N+1]`` on the device (then B must be 1) or None.  Returns ``(y, x_tail)``, x_tail
     ``[N, K-1, C]`` the last inputs of each sequence (a page of ``gdn_conv_step``)."""
     f = "gdn_conv_fwd"
-    (B, T, C, K, N), rows, dense = _conv_specs(f, x, w, bias, x_prev, cu_seqlens)
-    dense.update(y=(y, x.shape, x.dtype), x_tail=(x_tail, (N, K - 1, C), x.dtype))
-    dev = x.get_device()
-    _specs_check(f, dev, rows, dense)
+    B, T, C, K, N, dev = _conv_check(f, x, w, bias, x_prev, cu_seqlens, y, tail=x_tail)
     y = _like_new(stream, x) if y is None else y
     if x_tail is None and output_tail:
         x_tail = _empty(stream, x, (N, K - 1, C), x.dtype)
@@ -1539,23 +1593,20 @@ def gdn_conv_bwd(x, w, d_y, bias=None, x_prev=None, cu_seqlens=None, d_x_tail=No
     None without x_prev), ``dw``, ``dbias`` (fp32; dbias None without a bias); ``grads`` may
     supply them (one left out is not computed)."""
     f = "gdn_conv_bwd"
-    (B, T, C, K, N), rows, dense = _conv_specs(f, x, w, bias, x_prev, cu_seqlens)
-    given = grads or {}
-    kinds = dict(dx=(x.shape, x.dtype), dw=((C, K), _F32), dbias=((C,), _F32),
-                 dx_prev=((N, K - 1, C), x.dtype))
-    dense.update(d_y=(d_y, x.shape, x.dtype), d_x_tail=(d_x_tail, (N, K - 1, C), x.dtype))
-    for n, t in given.items():
-        dense[n] = (t, *kinds[n])
-    dev = x.get_device()
-    _specs_check(f, dev, rows, dense)
+    dx, dw, dbias, dx_prev = _grads_of(f, grads, ("dx", "dw", "dbias", "dx_prev"))
+    B, T, C, K, N, dev = _conv_check(f, x, w, bias, x_prev, cu_seqlens, d_y, dx, d_x_tail, dx_prev,
+                                     dw, dbias)
     if grads is None:
-        left = {n for n, t in (("dbias", bias), ("dx_prev", x_prev)) if t is None}
-        grads = {n: None if n in left else _empty(stream, x, *kind) for n, kind in kinds.items()}
+        dx, dw = _like_new(stream, x), _like_new(stream, w)
+        dbias = None if bias is None else _like_new(stream, bias)
+        dx_prev = None if x_prev is None else _like_new(stream, x_prev)
+        grads = dict(dx=dx, dw=dw, dbias=dbias, dx_prev=dx_prev)
+    elif dx is None:
+        raise ValueError(f"{f}: grads must hold dx")
     ws = _workspace(stream, x, workspace, gdn_conv_workspace_size(N, T, C, K), check)
     st = _on(f, dev)(
         x.data_ptr(), w.data_ptr(), _p(bias), _p(x_prev), _p(cu_seqlens), d_y.data_ptr(),
-        _p(d_x_tail), grads["dx"].data_ptr(), _p(grads.get("dw")), _p(grads.get("dbias")),
-        _p(grads.get("dx_prev")), B, T, C, K, N, _row_stride(f, "x", x), _CODES[x.dtype],
+        _p(d_x_tail), dx.data_ptr(), _p(dw), _p(dbias), _p(dx_prev), B, T, C, K, N, _row_stride(f, "x", x), _CODES[x.dtype],
         GDN_CONV_SILU if silu else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(f, st, check, ws, stream)
@@ -1574,10 +1625,11 @@ def gdn_conv_step(x, w, state, bias=None, pages=None, *, silu=True, y=None, work
     N, C = x.shape
     K = w.shape[1]
     dtype, dev = x.dtype, x.get_device()
-    _dtype_code(dtype)
-    _specs_check(f, dev, {}, dict(x=(x, x.shape, dtype), w=(w, (C, K), _F32),
-                                  bias=(bias, (C,), _F32), pages=(pages, (N,), _I32),
-                                  y=(y, x.shape, dtype)))
+    if not (dtype in _CODES and _fit(dev, x.shape, dtype, x, y) and _fit(dev, (C, K), _F32, w) and
+            _fit(dev, (C,), _F32, bias) and _fit(dev, (N,), _I32, pages)):
+        _dtype_code(dtype)
+        _misfit(f, dev, {}, dict(x=(x, x.shape, dtype), w=(w, (C, K), _F32), bias=(bias, (C,), _F32),
+                                 pages=(pages, (N,), _I32), y=(y, x.shape, dtype)))
     P, stride = _pool_check(f, dev, "state", state, (K - 1, C), dtype)
     y = _like_new(stream, x) if y is None else y
     if check or workspace is not None:
@@ -1596,23 +1648,35 @@ def gdn_qk_norm_workspace_size(batch: int, seq_len: int, head_dim: int) -> int:
     return int(lib().gdn_qk_norm_workspace_size(batch, seq_len, head_dim))
 
 
-def _qk_specs(where, q, k, q_weight, k_weight, positions, inv_freq):
-    if q.dim() != 4 or k.dim() != 4:
+def _qk_check(where, q, k, q_weight, k_weight, positions, inv_freq, q2, k2, dq=None, dk=None,
+              dqw=None, dkw=None):
+    """The sizes of a call whose tensors fit (q2, k2: the outputs, or their gradients)."""
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError(f"{where}: q and k must be [B, T, H, D]")
-    B, T, Hq, D = q.shape
-    Hk = k.shape[2]
-    _dtype_code(q.dtype)
+    B, T, Hq, D = qs
+    Hk = ks[2]
+    dtype, dev = q.dtype, q.get_device()
     R = 0
     if inv_freq is not None:
-        if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
+        R = 2 * inv_freq.shape[0] if inv_freq.dim() == 1 else D + 1
+        if R > D:
             raise ValueError(f"{where}: inv_freq must be float32 [R / 2], R at most the head size")
-        R = 2 * inv_freq.shape[0]
     elif positions is not None:
         raise ValueError(f"{where}: positions without inv_freq")
-    rows = dict(q=(q, q.shape, q.dtype), k=(k, (B, T, Hk, D), q.dtype))
-    dense = dict(q_weight=(q_weight, (D,), _F32), k_weight=(k_weight, (D,), _F32),
-                 positions=(positions, (B, T), _I32), inv_freq=(inv_freq, (R // 2,), _F32))
-    return (B, T, Hq, Hk, D, R), rows, dense
+    if dtype in _CODES and ks[0] == B and ks[1] == T and ks[3] == D and \
+            _rows_fit(dev, qs, dtype, q) and _rows_fit(dev, ks, dtype, k) and \
+            _fit(dev, (D,), _F32, q_weight, k_weight, dqw, dkw) and \
+            _fit(dev, (B, T), _I32, positions) and _fit(dev, (R // 2,), _F32, inv_freq) and \
+            _fit(dev, qs, dtype, q2, dq) and _fit(dev, ks, dtype, k2, dk):
+        return B, T, Hq, Hk, D, R, dev
+    _dtype_code(dtype)
+    out = ("d_q_out", "d_k_out") if where.endswith("bwd") else ("q_out", "k_out")
+    _misfit(where, dev, dict(q=(q, qs, dtype), k=(k, (B, T, Hk, D), dtype)), {
+        "q_weight": (q_weight, (D,), _F32), "k_weight": (k_weight, (D,), _F32),
+        "positions": (positions, (B, T), _I32), "inv_freq": (inv_freq, (R // 2,), _F32),
+        out[0]: (q2, qs, dtype), out[1]: (k2, ks, dtype), "dq": (dq, qs, dtype),
+        "dk": (dk, ks, dtype), "dq_weight": (dqw, (D,), _F32), "dk_weight": (dkw, (D,), _F32)})
 
 
 def gdn_qk_norm(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, q_scale=1.0,
@@ -1627,12 +1691,10 @@ def gdn_qk_norm(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=Non
     ``interleaved``.  q is multiplied by ``q_scale``.  Returns ``(q_out, k_out)``, densely
     packed."""
     f = "gdn_qk_norm"
-    (B, T, Hq, Hk, D, R), rows, dense = _qk_specs(f, q, k, q_weight, k_weight, positions, inv_freq)
-    dense.update(q_out=(q_out, q.shape, q.dtype), k_out=(k_out, k.shape, q.dtype))
-    dev = q.get_device()
-    _specs_check(f, dev, rows, dense)
-    q_out = _empty(stream, q, q.shape, q.dtype) if q_out is None else q_out
-    k_out = _empty(stream, q, k.shape, q.dtype) if k_out is None else k_out
+    B, T, Hq, Hk, D, R, dev = _qk_check(f, q, k, q_weight, k_weight, positions, inv_freq, q_out,
+                                        k_out)
+    q_out = _like_new(stream, q) if q_out is None else q_out
+    k_out = _like_new(stream, k) if k_out is None else k_out
     st = _on(f, dev)(
         q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
         q_out.data_ptr(), k_out.data_ptr(), B, T, Hq, Hk, D, R, _row_stride(f, "q", q),
@@ -1652,24 +1714,21 @@ def gdn_qk_norm_bwd(q, k, d_q_out, d_k_out, q_weight=None, k_weight=None, positi
     dk_weight`` (fp32; None without the weight); ``grads`` may supply them (a weight's left
     out is not computed)."""
     f = "gdn_qk_norm_bwd"
-    (B, T, Hq, Hk, D, R), rows, dense = _qk_specs(f, q, k, q_weight, k_weight, positions, inv_freq)
-    given = grads or {}
-    kinds = dict(dq=(q.shape, q.dtype), dk=(k.shape, q.dtype), dq_weight=((D,), _F32),
-                 dk_weight=((D,), _F32))
-    dense.update(d_q_out=(d_q_out, q.shape, q.dtype), d_k_out=(d_k_out, k.shape, q.dtype))
-    for n, t in given.items():
-        dense[n] = (t, *kinds[n])
-    dev = q.get_device()
-    _specs_check(f, dev, rows, dense)
+    dq, dk, dqw, dkw = _grads_of(f, grads, ("dq", "dk", "dq_weight", "dk_weight"))
+    B, T, Hq, Hk, D, R, dev = _qk_check(f, q, k, q_weight, k_weight, positions, inv_freq, d_q_out,
+                                        d_k_out, dq, dk, dqw, dkw)
     if grads is None:
-        left = {n for n, t in (("dq_weight", q_weight), ("dk_weight", k_weight)) if t is None}
-        grads = {n: None if n in left else _empty(stream, q, *kind) for n, kind in kinds.items()}
+        dq, dk = _like_new(stream, q), _like_new(stream, k)
+        dqw = None if q_weight is None else _like_new(stream, q_weight)
+        dkw = None if k_weight is None else _like_new(stream, k_weight)
+        grads = dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
+    elif dq is None or dk is None:
+        raise ValueError(f"{f}: grads must hold dq and dk")
     ws = _workspace(stream, q, workspace, gdn_qk_norm_workspace_size(B, T, D), False)
     st = _on(f, dev)(
         q.data_ptr(), k.data_ptr(), _p(q_weight), _p(k_weight), _p(positions), _p(inv_freq),
-        d_q_out.data_ptr(), d_k_out.data_ptr(), grads["dq"].data_ptr(), grads["dk"].data_ptr(),
-        _p(grads.get("dq_weight")), _p(grads.get("dk_weight")), B, T, Hq, Hk, D, R,
-        _row_stride(f, "q", q), _row_stride(f, "k", k), q_scale, eps, _CODES[q.dtype],
+        d_q_out.data_ptr(), d_k_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _p(dqw), _p(dkw), B, T,
+        Hq, Hk, D, R, _row_stride(f, "q", q), _row_stride(f, "k", k), q_scale, eps, _CODES[q.dtype],
         (GDN_QK_L2NORM if l2norm else 0) | (GDN_ROPE_INTERLEAVED if interleaved else 0),
         ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
     if st:
