@@ -26,8 +26,9 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 256;
-// Rows of a thread that are loaded together.
-template <typename T, bool BACK> constexpr int kRowsOf = BACK || sizeof(T) == 4 ? 1 : 2;
+// CTAs an SM.  (bf16 forward: two rows of a thread together in three CTAs took 63 us where one
+// row in four takes 61, [8, 4096, 16 + 16, 64]; four rows in two 69.)
+template <typename T, bool BACK> constexpr int kCtas = BACK ? 2 : sizeof(T) == 2 ? 4 : 3;
 constexpr int kTokens = 8;     // most tokens of a CTA at a time
 constexpr int kMaxHalf = 128;  // most pairs of a head
 
@@ -189,10 +190,10 @@ __device__ __forceinline__ void unpack(const Raw8<T> &r, uint64_t (&u)[4]) {
 }
 
 template <typename T, int LR, Mode M, bool BACK>
-__global__ void __launch_bounds__(kThreads, BACK ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, kCtas<T, BACK>)
 gdn_qk_norm_kernel(const Params p) {
-  constexpr int RG = kThreads / LR, kRows = kRowsOf<T, BACK>;   // rows side by side, in turn
-  __shared__ __align__(16) float table[kTokens * 2 * kMaxHalf];
+  constexpr int RG = kThreads / LR;   // rows side by side
+  __shared__ __align__(16) float tables[2][kTokens * 2 * kMaxHalf];   // of a tile and the next
   __shared__ __align__(16) float rows_buf[RG * LR * 16];
   __shared__ uint64_t freq[kMaxHalf];
   const int tid = threadIdx.x, rg = tid / LR, which = (int)blockIdx.x >= p.side[0].ctas;
@@ -220,95 +221,91 @@ gdn_qk_norm_kernel(const Params p) {
   const uint32_t magic = 0xffffffffu / s.heads + 1;   // 2^32 / heads, rounded up: rows < 2^16
   const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
   const int width = s.heads * p.D;
-  int summed = 0;
+  int summed = 0, which_table = 0;
+  if (p.R) __syncthreads();
   for (int64_t tile = blockIdx.x - (which ? p.side[0].ctas : 0); tile < tiles; tile += s.ctas) {
     const int64_t tok0 = tile * p.tile;
     const int cnt = (int)(p.tokens - tok0 < p.tile ? p.tokens - tok0 : p.tile), rows = cnt * s.heads;
     const T *xs = static_cast<const T *>(s.x) + tok0 * s.stride;
     const T *gs = static_cast<const T *>(s.g) + tok0 * width;
     T *out = static_cast<T *>(s.out) + tok0 * width;
-    Raw8<T> x[kRows][2], d[BACK ? kRows : 1][2];
-    int tok[kRows], at[kRows];
-    const auto fetch = [&](int r0) {   // (rows behind the last: the last)
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i * RG < rows ? r0 + i * RG : rows - 1;
-        tok[i] = s.heads == 1 ? r : (int)__umulhi((uint32_t)r, magic);
-        const int head = (r - tok[i] * s.heads) * p.D;
-        at[i] = tok[i] * width + head;
-        const T *from = xs + tok[i] * s.stride + head;
-        x[i][0].load(from + c0);
-        x[i][1].load(from + c1);
-        if (BACK) {
-          d[i][0].load(gs + at[i] + c0);
-          d[i][1].load(gs + at[i] + c1);
-        }
+    Raw8<T> x[2], d[BACK ? 2 : 1];
+    int tok, at;
+    const auto fetch = [&](int r) {   // (rows behind the last: the last)
+      r = r < rows ? r : rows - 1;
+      tok = s.heads == 1 ? r : (int)__umulhi((uint32_t)r, magic);
+      const int head = (r - tok * s.heads) * p.D;
+      at = tok * width + head;
+      const T *from = xs + tok * s.stride + head;
+      x[0].load(from + c0);
+      x[1].load(from + c1);
+      if constexpr (BACK) {
+        d[0].load(gs + at + c0);
+        d[1].load(gs + at + c1);
       }
     };
     fetch(rg);   // on its way while the table is made
+    // (a table is made again two tiles later: every thread has passed a barrier after reading it)
+    which_table ^= 1;
+    float *table = tables[which_table];
     if (p.R) {
-      __syncthreads();   // the last tile's table has been read
       turn_table(p, tok0, cnt, lanes, freq, table);
       __syncthreads();
     }
-    for (int base = 0; base < rows; base += kRows * RG) {
+    for (int base = 0; base < rows; base += RG) {
+      const bool on = base + rg < rows;
+      const float *cs = table + tok * 2 * p.pitch;
+      T *to = out + at;
+      uint64_t xv[2][4], u[2][4], ss = 0ull;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (base + i * RG >= rows) break;   // the same for the whole CTA
-        const bool on = base + i * RG + rg < rows;
-        const float *cs = table + tok[i] * 2 * p.pitch;
-        T *to = out + at[i];
-        uint64_t xv[2][4], u[2][4], ss = 0ull;
+      for (int g = 0; g < 2; ++g) {
+        unpack(x[g], xv[g]);
+        if (LR * 16 != p.D && !col.on[g]) xv[g][0] = xv[g][1] = xv[g][2] = xv[g][3] = 0ull;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) ss = fma2(xv[g][m], xv[g][m], ss);
+        if constexpr (BACK) unpack(d[g], u[g]);
+      }
+      if (base + RG < rows) fetch(base + RG + rg);
+      float lo, hi;
+      unpk(ss, lo, hi);
+      const float r = rsqrtf(fmaf(row_sum<LR>(lo + hi), over, p.eps));
+      const uint64_t rr = pk(r, r);
+      if constexpr (!BACK) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) u[g][m] = mul2(mul2(xv[g][m], rr), w[g][m]);
+        turn<M, BACK>(p, col, cs, buf, u);
+      } else {
+        turn<M, BACK>(p, col, cs, buf, u);
+        uint64_t m2 = 0ull;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint64_t t = mul2(u[g][m], xv[g][m]);
+            if (on) own[g][m] = fma2(t, rr, own[g][m]);
+            m2 = fma2(t, w[g][m], m2);
+          }
+        unpk(m2, lo, hi);
+        const float f = -(row_sum<LR>(lo + hi) * over * r * r);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            u[g][m] = mul2(rr, fma2(xv[g][m], pk(f, f), mul2(u[g][m], w[g][m])));
+      }
+      if (on)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          unpack(x[i][g], xv[g]);
-          if (LR * 16 != p.D && !col.on[g]) xv[g][0] = xv[g][1] = xv[g][2] = xv[g][3] = 0ull;
+          float v[8];
 #pragma unroll
-          for (int m = 0; m < 4; ++m) ss = fma2(xv[g][m], xv[g][m], ss);
-          if (BACK) unpack(d[i][g], u[g]);
+          for (int m = 0; m < 4; ++m) unpk(u[g][m], v[2 * m], v[2 * m + 1]);
+          Raw8<T> o;
+          o.set(v);
+          if (col.on[g]) o.store(to + (g ? c1 : c0));
         }
-        if (i == kRows - 1 && base + kRows * RG < rows) fetch(base + kRows * RG + rg);
-        float lo, hi;
-        unpk(ss, lo, hi);
-        const float r = rsqrtf(fmaf(row_sum<LR>(lo + hi), over, p.eps));
-        const uint64_t rr = pk(r, r);
-        if constexpr (!BACK) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) u[g][m] = mul2(mul2(xv[g][m], rr), w[g][m]);
-          turn<M, BACK>(p, col, cs, buf, u);
-        } else {
-          turn<M, BACK>(p, col, cs, buf, u);
-          uint64_t m2 = 0ull;
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const uint64_t t = mul2(u[g][m], xv[g][m]);
-              if (on) own[g][m] = fma2(t, rr, own[g][m]);
-              m2 = fma2(t, w[g][m], m2);
-            }
-          unpk(m2, lo, hi);
-          const float f = -(row_sum<LR>(lo + hi) * over * r * r);
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              u[g][m] = mul2(rr, fma2(xv[g][m], pk(f, f), mul2(u[g][m], w[g][m])));
-        }
-        if (on)
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float v[8];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) unpk(u[g][m], v[2 * m], v[2 * m + 1]);
-            Raw8<T> o;
-            o.set(v);
-            if (col.on[g]) o.store(to + (g ? c1 : c0));
-          }
-      }
-      if (BACK && ++summed == 64 / kRows) {   // at most 64 rows in one run of an accumulator
+      if (BACK && ++summed == 64) {   // at most 64 rows in one run of an accumulator
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -364,9 +361,9 @@ struct Grid {
   int tile;
   int64_t ctas[2];
 };
-Grid grid_of(int64_t tokens, int64_t Hq, int64_t Hk, bool back) {
+Grid grid_of(int64_t tokens, int64_t Hq, int64_t Hk, int ctas) {
   Grid g;
-  const int64_t fit = (back ? 2 : 3) * kSMs;
+  const int64_t fit = ctas * kSMs;
   g.tile = tokens >= 2 * kTokens * kSMs ? kTokens : 1;
   const int64_t tiles = (tokens + g.tile - 1) / g.tile;
   int64_t q = fit * Hq / (Hq + Hk);
@@ -432,7 +429,8 @@ gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, cons
                        {positions, rows * 4}, {inv_freq, (size_t)rotary_dim * 2}};
   if (!apart(outs, ins)) return GDN_ERR_INVALID_ARG;
   Params p{};
-  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, false);
+  const Grid g = grid_of((int64_t)rows, q_heads, k_heads,
+                         dtype == GDN_F32 ? kCtas<float, false> : kCtas<__nv_bfloat16, false>);
   p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale};
   p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f};
   p.positions = positions;
@@ -454,7 +452,7 @@ gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, cons
 size_t gdn_qk_norm_workspace_size(int32_t batch, int32_t seq_len, int32_t head_dim) {
   if (batch <= 0 || seq_len < 0 || head_dim <= 0) return 0;
   // (of every number of heads; calls without tokens need none)
-  const int64_t tokens = (int64_t)batch * seq_len, most = 2 * gdn::layer::kSMs;
+  const int64_t tokens = (int64_t)batch * seq_len, most = gdn::qk::kCtas<float, true> * gdn::layer::kSMs;
   return (size_t)(tokens < most ? 2 * tokens < most ? 2 * tokens : most : most) * head_dim * 4;
 }
 
@@ -487,7 +485,7 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   const void *ptrs[] = {q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, dq, dk,
                         dq_weight, dk_weight, workspace};
   if (!all_aligned(ptrs)) return GDN_ERR_INVALID_ARG;
-  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, true);
+  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, kCtas<float, true>);
   const bool sums = dq_weight || dk_weight;
   if (!workspace || workspace_bytes < (size_t)(g.ctas[0] + g.ctas[1]) * w_bytes) return GDN_ERR_WORKSPACE;
   const Range outs[] = {{dq, rows * wq * e}, {dk, rows * wk * e}, {dq_weight, w_bytes},

@@ -115,18 +115,25 @@ __device__ __forceinline__ void load_prev(const Params &p, int n, int i, int ch,
     r.load(static_cast<const T *>(p.x_prev) + ((int64_t)n * (K - 1) + i) * p.C + ch);
 }
 
-// w[k] and the bias of four channels, in pairs.
+// w[k] and the bias of four channels, in pairs (their 4 K weights lie together).
 template <int K>
-__device__ __forceinline__ void load_weights(const Params &p, int ch, bool on, uint64_t (&w)[K][2],
-                                             uint64_t (&bias)[2]) {
+__device__ __forceinline__ void load_weights(const float *w_all, const float *bias_all, int ch, bool on,
+                                             uint64_t (&w)[K][2], uint64_t (&bias)[2]) {
+  float v[4 * K];   // [channel][tap]
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = ch + 2 * i;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      w[k][i] = on ? pk(p.w[(int64_t)c * K + k], p.w[(int64_t)(c + 1) * K + k]) : 0ull;
-    bias[i] = on && p.bias ? pk(p.bias[c], p.bias[c + 1]) : 0ull;
+  for (int k = 0; k < K; ++k) {
+    const float4 f = on ? reinterpret_cast<const float4 *>(w_all + (int64_t)ch * K)[k]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[4 * k] = f.x; v[4 * k + 1] = f.y; v[4 * k + 2] = f.z; v[4 * k + 3] = f.w;
   }
+  const float4 b = on && bias_all ? *reinterpret_cast<const float4 *>(bias_all + ch)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k][i] = pk(v[2 * i * K + k], v[(2 * i + 1) * K + k]);
+  bias[0] = pk(b.x, b.y);
+  bias[1] = pk(b.z, b.w);
 }
 
 // A thread's segment of tokens, counted from its first in 32 bits, and the sequence that it
@@ -250,7 +257,7 @@ gdn_conv_fwd_kernel(const Params p) {
     close_group();
   }
   uint64_t w[K][2], bias[2], win[PA][2];
-  load_weights<K>(p, ch, on, w, bias);
+  load_weights<K>(p.w, p.bias, ch, on, w, bias);
   first_window<T, K>(p, s, xa, ch, win);
   T *y = static_cast<T *>(p.y) + s.a * p.C + ch;
   const auto token = [&](const Raw4<T> &r) {
@@ -327,7 +334,7 @@ gdn_conv_bwd_kernel(const Params p) {
       close_group();
     }
     uint64_t w[K][2], bias[2], win[PA][2], acc[PA][2], own[K + 1][2];   // acc[j]: row t - 1 - j, unfinished
-    load_weights<K>(p, ch, on, w, bias);
+    load_weights<K>(p.w, p.bias, ch, on, w, bias);
     first_window<T, K>(p, s, xa, ch, win);
 #pragma unroll
     for (int i = 0; i < P; ++i) acc[i][0] = acc[i][1] = 0ull;
@@ -484,7 +491,7 @@ gdn_conv_ends_kernel(const Params p, int sum_blocks) {
   int64_t start, len;
   if (!p.seq.bounds(n, start, len) || !p.dx_prev) return;
   uint64_t w[K][2], bias[2], win[PA][2], g[PA][2];   // g: of the prefix's rows
-  load_weights<K>(p, ch, true, w, bias);
+  load_weights<K>(p.w, p.bias, ch, true, w, bias);
 #pragma unroll
   for (int m = 0; m < P; ++m) {
     Raw4<T> r;
@@ -560,21 +567,14 @@ gdn_conv_step_kernel(const StepParams p) {
 #pragma unroll
   for (int k = 0; k < P; ++k) r[k].load(at + (int64_t)k * p.C);
   r[P].load(static_cast<const T *>(p.x) + (int64_t)n * p.C + ch);
-  uint64_t z[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) z[j] = p.bias ? pk(p.bias[ch + 2 * j], p.bias[ch + 2 * j + 1]) : 0ull;
-  float w[4 * K];   // [channel][tap], together 16 K bytes
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const float4 v = reinterpret_cast<const float4 *>(p.w + (int64_t)ch * K)[k];
-    w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-  }
+  uint64_t w[K][2], z[2];
+  load_weights<K>(p.w, p.bias, ch, true, w, z);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     uint64_t v[2];
     r[k].get(v);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) z[j] = fma2(pk(w[2 * j * K + k], w[(2 * j + 1) * K + k]), v[j], z[j]);
+    for (int j = 0; j < 2; ++j) z[j] = fma2(w[k][j], v[j], z[j]);
   }
   if (p.silu)
 #pragma unroll

@@ -1268,23 +1268,18 @@ def gdn_pages_compact(pool, table, counts, refs, *, num_live=None, table_out=Non
 # Selective state space scan, its short convolution, and the prologue of q and k
 # ---------------------------------------------------------------------------
 def _row_stride(where, name, t):
-    """Elements from one token row of ``t`` ``[B, T, ...]`` to the next (rows
-    contiguous, the rows of a batch one after the other); 0: packed."""
+    """Elements from one token row of ``t`` ``[B, T, C]`` or ``[B, T, H, C]`` to the next
+    (rows contiguous, the rows of a batch one after the other); 0: packed."""
     if t is None or t.is_contiguous():
         return 0
-    if t.dim() == 3:   # (the usual slice, with few calls)
-        s0, s1, s2 = t.stride()
-        B, T, width = t.shape
-        if s2 == 1 and s1 >= width and T > 1 and (B == 1 or s0 == T * s1) and \
-                s1 * t.element_size() % 16 == 0:
-            return s1
-    B, T = t.shape[:2]
-    width, run = 1, True
-    for size, stride in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-        run = run and (size == 1 or stride == width)
-        width *= size
-    s = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else width)
-    if not run or s < width or (B > 1 and T > 0 and t.stride(0) != T * s):
+    sizes, strides = t.shape, t.stride()
+    B, T, width = sizes[0], sizes[1], sizes[-1]
+    run = strides[-1] == 1 or width == 1
+    if len(sizes) == 4:
+        run = run and (strides[2] == width or sizes[2] == 1)
+        width *= sizes[2]
+    s = strides[1] if T > 1 else strides[0] if B > 1 else width
+    if not run or s < width or (B > 1 and T > 0 and strides[0] != T * s):
         raise ValueError(f"{where}: {name} must have contiguous rows at one stride")
     if s * t.element_size() % 16:
         raise ValueError(f"{where}: the row stride of {name} must be a multiple of 16 bytes")
@@ -1294,8 +1289,8 @@ def _row_stride(where, name, t):
 def _rows_fit(device, shape, dtype, *tensors):
     """Every tensor given has this shape and dtype and is on this device, at any stride."""
     for t in tensors:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and
-                                  t.get_device() == device and (device >= 0 or t.is_cuda)):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or
+                              t.get_device() != device or (device < 0 and not t.is_cuda)):
             return False
     return True
 
@@ -1303,9 +1298,9 @@ def _rows_fit(device, shape, dtype, *tensors):
 def _fit(device, shape, dtype, *tensors):
     """... and contiguous."""
     for t in tensors:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and
-                                  t.get_device() == device and t.is_contiguous() and
-                                  (device >= 0 or t.is_cuda)):
+        if t is not None and (t.dtype is not dtype or t.shape != shape or
+                              t.get_device() != device or not t.is_contiguous() or
+                              (device < 0 and not t.is_cuda)):
             return False
     return True
 
@@ -1444,7 +1439,8 @@ def gdn_ssm_bwd(x, dt, A_log, b, c, d_y, initial_state=None, cu_seqlens=None, d_
         dA = _like_new(stream, A_log)
         dskip = None if D_skip is None else _like_new(stream, D_skip)
         dbias = None if dt_bias is None else _like_new(stream, dt_bias)
-        dh0 = _empty(stream, x, (N, D, S), _F32)
+        dh0 = _empty(stream, x, (N, D, S), _F32) if initial_state is None else \
+            _like_new(stream, initial_state)
         grads = dict(dx=dx, ddt=ddt, db=db, dc=dc, dgate=dgate, dA_log=dA, dD_skip=dskip,
                      ddt_bias=dbias, dh0=dh0)
     elif dx is None or ddt is None or db is None or dc is None:
