@@ -214,13 +214,13 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   unpk(x, lo, hi);
   return pk(ex2(lo), ex2(hi));
 }
-// exp(delta A) of a token.  The hardware's exp2 is low by 2e-8 on average for arguments
-// of -0.1 to -0.001 (measured over 10^6 arguments a range: -1.4e-8 to -2.6e-8), which a
-// state that lasts a thousand tokens would add up to 2e-5.  kLift in the exponent takes
-// most of it away (-0.7e-8 to -1.6e-8 there, +0.5e-8 for arguments of -0.001 and less:
-// larger values of it make the longest memories worse); 2^kLift itself still gives 1, so
-// that delta = 0 keeps a state.
-constexpr float kLift = 1.5e-8f;
+// exp(delta A) of a token.  The hardware's exp2 is low on average, by 1.4e-8 to 2.6e-8 for
+// arguments of -0.25 to -0.001 (measured over 10^6 arguments a range), and a state adds up
+// 1 / (1 - a) such errors: 2e-6 for a decay of 1 %.  kLift in the exponent takes the mean
+// away where most decays lie (below 1e-9 for -0.1 to -0.03 and -0.01 to -0.001, -1e-8
+// between; +1.2e-8 for arguments nearer to zero): sums over tokens were off by 5e-7 with
+// it, 1e-6 with a fifth of it.  2^kLift itself still gives 1: delta = 0 keeps a state.
+constexpr float kLift = 2.5e-8f;
 __device__ __forceinline__ uint64_t decay(uint64_t delta, uint64_t A) {
   return ex2_pair(fma2(delta, A, pk(kLift, kLift)));
 }
@@ -349,13 +349,15 @@ __device__ __forceinline__ void load_twice(const float *sbc, int t, int which, i
   v[0] = a.a; v[1] = a.b; v[2] = b.a; v[3] = b.b;
 }
 
-// The split along time of a launch of `blocks` CTAs per segment: chunks of 32 tokens, two
-// CTAs an SM at a time; a segment's start costs about a chunk, the first launch of it
-// `first` of the second.
+// The split along time of launches of `blocks` CTAs per segment, `ctas` an SM at a time, in
+// chunks of 32 tokens; a segment's start costs about half a chunk, the first launch of it
+// `first` of the second.  (Forward, [4, 4096, 1280] / [1, 65536, 2048]: 179 / 992 us; a
+// start of a whole chunk 179 / 1027, of two 179 / 1027; two CTAs an SM 241 / 1310, four
+// 192 / 1031, six 186 / 992.)
 constexpr int kChunkTokens = 32;
-inline lin::Plan plan(int64_t num_seqs, int64_t seq_len, bool packed, int64_t blocks,
+inline lin::Plan plan(int64_t num_seqs, int64_t seq_len, bool packed, int64_t blocks, int ctas,
                       double first) {
-  return lin::plan_segments(num_seqs, seq_len, packed, blocks, 3 * kSMs, kChunkTokens, 1.0, first);
+  return lin::plan_segments(num_seqs, seq_len, packed, blocks, ctas * kSMs, kChunkTokens, 0.4, first);
 }
 inline int channel_blocks(int Dg, int S) { return (Dg + 2048 / S - 1) / (2048 / S); }
 inline bool state_size(int S) { return S == 8 || S == 16 || S == 32 || S == 64; }

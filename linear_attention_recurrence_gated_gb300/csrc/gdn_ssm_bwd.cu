@@ -808,6 +808,7 @@ cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   const dim3 tiles(groups * p.blocks, p.parts);
   constexpr size_t kGrad = 4 * Bwd<T, S>::kFloats;
+  static_assert(Bwd<T, S>::kCtas == (sizeof(T) == 4 || S == 8 ? 2 : 3), "the plan's CTAs an SM");
   if (p.gate) {
     err = allow_smem<gdn_ssm_grad_kernel<T, S, true>>(kGrad);
     if (err == cudaSuccess)
@@ -849,8 +850,9 @@ size_t gdn_ssm_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t cha
   size_t most = 0;
   for (bool packed : {false, true}) {
     const int64_t rows = packed ? seq_len : (int64_t)num_seqs * seq_len;
-    const auto pl = plan(num_seqs, seq_len, packed, all, kFirst);
-    for (const auto &one : {pl, gdn::lin::Plan{0, num_seqs}}) {
+    for (const auto &one : {plan(num_seqs, seq_len, packed, all, 2, kFirst),
+                            plan(num_seqs, seq_len, packed, all, 3, kFirst),
+                            gdn::lin::Plan{0, num_seqs}}) {
       const size_t n = layout(rows, channels, d_state, groups, blocks, parts_of(one.slots, all),
                               one).total;
       most = n > most ? n : most;
@@ -933,7 +935,9 @@ gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const 
   p.seq.seq_len = seq_len;
   p.seq.num_seqs = num_seqs;
   const int64_t all = (int64_t)groups * p.blocks;
-  auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, all, kFirst);
+  // CTAs an SM of the second launch: see Bwd::kCtas
+  const int ctas = dtype == GDN_F32 || d_state == 8 ? 2 : 3;
+  auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, all, ctas, kFirst);
   Layout l;
   for (;;) {   // uncut where the workspace is too small for the segments
     p.parts = (int32_t)parts_of(pl.slots, all);

@@ -238,6 +238,7 @@ cudaError_t launch_t(const Params &p, int S, int groups, cudaStream_t stream) {
   }
 }
 constexpr double kFirst = 0.7;   // the first launch forms no outputs
+constexpr int kCtas = 3;         // an SM (the outputs' kernel's registers)
 
 }  // namespace
 
@@ -277,7 +278,7 @@ size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channel
   const int64_t blocks = (int64_t)groups * channel_blocks(channels / groups, d_state);
   size_t most = 0;
   for (bool packed : {false, true}) {
-    const auto pl = plan(num_seqs, seq_len, packed, blocks, kFirst);
+    const auto pl = plan(num_seqs, seq_len, packed, blocks, kCtas, kFirst);
     const size_t n = pl.seg_len ? (size_t)pl.slots * channels * (d_state + 1) * 4 : 0;
     most = n > most ? n : most;
   }
@@ -341,13 +342,13 @@ gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const 
   p.seq.seq_len = seq_len;
   p.seq.num_seqs = num_seqs;
   const int64_t blocks = (int64_t)groups * p.blocks;
-  const auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, blocks, kFirst);
+  const auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, blocks, kCtas, kFirst);
   const bool cut = pl.seg_len && (size_t)pl.slots * channels * (d_state + 1) * 4 <=
                                      workspace_bytes - kStatusBytes;
   p.seq.seg_len = cut ? pl.seg_len : 0;
   p.seq.slots = cut ? pl.slots : num_seqs;
   p.seq.ranked = cu_seqlens && !cut && num_seqs > 1 && num_seqs <= lin::kRanked &&
-                 blocks * num_seqs > 2 * kSMs;
+                 blocks * num_seqs > kCtas * kSMs;
   p.seg_x = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
   p.seg_d = p.seg_x + (size_t)p.seq.slots * channels * d_state;
   p.keep = initial_state && initial_state == final_state;
