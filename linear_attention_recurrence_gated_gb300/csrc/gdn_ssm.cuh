@@ -214,15 +214,24 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   unpk(x, lo, hi);
   return pk(ex2(lo), ex2(hi));
 }
-// exp(delta A) of a token.  The hardware's exp2 is low on average, by 1.4e-8 to 2.6e-8 for
-// arguments of -0.25 to -0.001 (measured over 10^6 arguments a range), and a state adds up
-// 1 / (1 - a) such errors: 2e-6 for a decay of 1 %.  kLift in the exponent takes the mean
-// away where most decays lie (below 1e-9 for -0.1 to -0.03 and -0.01 to -0.001, -1e-8
-// between; +1.2e-8 for arguments nearer to zero): sums over tokens were off by 5e-7 with
-// it, 1e-6 with a fifth of it.  2^kLift itself still gives 1: delta = 0 keeps a state.
-constexpr float kLift = 2.5e-8f;
-__device__ __forceinline__ uint64_t decay(uint64_t delta, uint64_t A) {
-  return ex2_pair(fma2(delta, A, pk(kLift, kLift)));
+// exp(delta A) of a token.  The hardware's exp2 is low on average, and a state adds up
+// 1 / (1 - a) such errors.  Measured over 2^18 arguments an eighth of an octave: 6e-9 to 9e-9
+// from -2^-8 to 0, 1.3e-8 at -2^-8, 3.1e-8 at -2^-7, 2.4e-8 on average from there to -1/2.
+// A lift of the exponent takes the mean away: by the slowest rate of the 4 or 8 elements that
+// share it, whose errors a state keeps longest, and one step of a tile.  (2^lift itself still
+// gives 1: delta = 0 keeps a state.  One lift for all, 2.5e-8, is a third operand less to
+// read, 179 us for 185, [4, 4096, 1280], S = 16, and left states of slow decays 1.1e-6 off for
+// 2.9e-7, and dA_log 2.2e-6 for 1.3e-6, over some 1000 tokens.)
+__device__ __forceinline__ float lift_of(float delta, float rate) {
+  return fminf(fmaxf(-5e-6f * rate * delta, 0.85e-8f), 3.1e-8f);
+}
+__device__ __forceinline__ uint64_t decay(uint64_t delta, uint64_t A, uint64_t lift) {
+  return ex2_pair(fma2(delta, A, lift));
+}
+__device__ __forceinline__ float slower(uint64_t a) {
+  float lo, hi;
+  unpk(a, lo, hi);
+  return fmaxf(lo, hi);
 }
 // h <- exp(A sum) h + X of the segment in `slot` (its arrays x [slot][D][S], d [slot][D]).
 template <int S>
@@ -322,6 +331,18 @@ __device__ __forceinline__ float total(uint64_t v) {
   return lo + hi;
 }
 
+// The lifts of a thread of 16 elements, one for eight of them; d: a step of each channel.
+template <int CPT>
+__device__ __forceinline__ void lifts16(const uint64_t (&A)[8], const float *d, uint64_t (&lift)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float slow = fmaxf(fmaxf(slower(A[4 * i]), slower(A[4 * i + 1])),
+                             fmaxf(slower(A[4 * i + 2]), slower(A[4 * i + 3])));
+    const float v = lift_of(d[CPT == 2 ? i : 0], slow);
+    lift[i] = pk(v, v);
+  }
+}
+
 struct Pairs {
   uint64_t a, b;
 };
@@ -347,6 +368,18 @@ __device__ __forceinline__ void load_twice(const float *sbc, int t, int which, i
   const float *at = sbc + (which * L + t) * 2 * S + 4 * sl;
   const Pairs a = lds2(at), b = lds2(at + S);
   v[0] = a.a; v[1] = a.b; v[2] = b.a; v[3] = b.b;
+}
+
+// The lifts of a thread of 4 channels x 4 states, one for each channel.
+__device__ __forceinline__ void lifts4(const uint64_t (&A)[2][4], const float *d, uint64_t (&lift)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float lo[4], hi[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpk(A[k][j], lo[j], hi[j]);
+    lift[k] = pk(lift_of(d[2 * k], fmaxf(fmaxf(lo[0], lo[1]), fmaxf(lo[2], lo[3]))),
+                 lift_of(d[2 * k + 1], fmaxf(fmaxf(hi[0], hi[1]), fmaxf(hi[2], hi[3]))));
+  }
 }
 
 // The split along time of launches of `blocks` CTAs per segment, `ctas` an SM at a time, in

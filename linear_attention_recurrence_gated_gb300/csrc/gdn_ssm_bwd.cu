@@ -202,6 +202,8 @@ gdn_ssm_keep_kernel(const BwdParams p) {
               P[k * NP + i] = ex2_pair(mul2(pk(sums[k], sums[k]), A[k * NP + i]));
       }
       float part[CPT] = {};
+      uint64_t lift[2];
+      lifts16<CPT>(A, sd + r * CB + cl, lift);
 #pragma unroll 4
       for (int t = r; t < r + kL; ++t) {   // (tokens past the last: zeros)
         uint64_t d[CPT], u[CPT], y[CPT], b2[NP], c2[NP];
@@ -217,7 +219,7 @@ gdn_ssm_keep_kernel(const BwdParams p) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
             const int e = k * NP + i;
-            const uint64_t a = decay(d[k], A[e]);
+            const uint64_t a = decay(d[k], A[e], lift[e / 4]);
             h[e] = fma2(a, h[e], mul2(u[k], b2[i]));
             if constexpr (CUT) {
               P[e] = mul2(P[e], a);
@@ -525,6 +527,8 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       }
       __syncthreads();
       if (tile > 0) fetch(tile - 1, s.start + t0 - kL, kL, kept_at(tile - 1));
+      uint64_t lift[2];
+      lifts4(A, sd + 4 * cl, lift);
       // the tile's states
 #pragma unroll 4
       for (int t = 0; t < kL; ++t) {
@@ -538,7 +542,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            h[k][j] = fma2(decay(dd[k], A[k][j]), h[k][j], mul2(uu[k], bb[j]));
+            h[k][j] = fma2(decay(dd[k], A[k][j], lift[k]), h[k][j], mul2(uu[k], bb[j]));
             if constexpr (GATE) y[k] = j ? fma2(cc[j], h[k][j], y[k]) : mul2(cc[j], h[k][j]);
           }
         if constexpr (GATE) {
@@ -576,7 +580,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
             dc[j] = k ? fma2(ee[k], h[k][j], dc[j]) : mul2(ee[k], h[k][j]);
             db[j] = k ? fma2(uu[k], G, db[j]) : mul2(uu[k], G);
             q[k] = j ? fma2(bb[j], G, q[k]) : mul2(bb[j], G);
-            g[k][j] = mul2(decay(dd[k], A[k][j]), G);
+            g[k][j] = mul2(decay(dd[k], A[k][j], lift[k]), G);
             const uint64_t w = mul2(g[k][j], before[k][j]);
             aw[k] = j ? fma2(A[k][j], w, aw[k]) : mul2(A[k][j], w);
             dA[k][j] = fma2(dd[k], w, dA[k][j]);

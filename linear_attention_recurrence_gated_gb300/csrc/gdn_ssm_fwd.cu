@@ -149,6 +149,8 @@ gdn_ssm_scan_kernel(const Params p) {
     if (t0 + TT < s.len) fetch(t0 + TT);
 
     float part[CPT] = {};
+    uint64_t lift[2];
+    lifts16<CPT>(A, sd + cl, lift);
     const int steps = (cnt + 3) & ~3;   // (rows past the last token are zeros: no change)
 #pragma unroll 4
     for (int t = 0; t < steps; ++t) {
@@ -163,7 +165,7 @@ gdn_ssm_scan_kernel(const Params p) {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint64_t &e = h[k * NP + i];
-          e = fma2(decay(d[k], A[k * NP + i]), e, mul2(u[k], b2[i]));
+          e = fma2(decay(d[k], A[k * NP + i], lift[(k * NP + i) / 4]), e, mul2(u[k], b2[i]));
           if constexpr (OUT) y[i & 1] = i > 1 ? fma2(c2[i], e, y[i & 1]) : mul2(c2[i], e);
         }
         if constexpr (OUT) {

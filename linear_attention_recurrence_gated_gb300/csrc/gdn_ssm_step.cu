@@ -77,6 +77,7 @@ gdn_ssm_step_kernel(const StepParams p) {
   }
   const float4 al = on ? four(p.A_log + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float4 A = make_float4(rate(al.x), rate(al.y), rate(al.z), rate(al.w));
+  const float slow = fmaxf(fmaxf(A.x, A.y), fmaxf(A.z, A.w));
   if (p.softplus) {
 #pragma unroll
     for (int k = 0; k < PER; k += 2) {
@@ -99,10 +100,11 @@ gdn_ssm_step_kernel(const StepParams p) {
     if (!on || page[i] < 0) continue;
     const float4 bv = four(b + i * next), cv = four(c + i * next);
     float4 s = h[i];
-    s.x = fmaf(ex2(fmaf(di, A.x, kLift)), s.x, ui * bv.x);
-    s.y = fmaf(ex2(fmaf(di, A.y, kLift)), s.y, ui * bv.y);
-    s.z = fmaf(ex2(fmaf(di, A.z, kLift)), s.z, ui * bv.z);
-    s.w = fmaf(ex2(fmaf(di, A.w, kLift)), s.w, ui * bv.w);
+    const float lift = lift_of(di, slow);
+    s.x = fmaf(ex2(fmaf(di, A.x, lift)), s.x, ui * bv.x);
+    s.y = fmaf(ex2(fmaf(di, A.y, lift)), s.y, ui * bv.y);
+    s.z = fmaf(ex2(fmaf(di, A.z, lift)), s.z, ui * bv.z);
+    s.w = fmaf(ex2(fmaf(di, A.w, lift)), s.w, ui * bv.w);
     *reinterpret_cast<float4 *>(p.s_out + page[i] * p.page_stride + at) = s;
     sum[i] = fmaf(cv.x, s.x, cv.y * s.y) + fmaf(cv.z, s.z, cv.w * s.w);
   }
