@@ -4,7 +4,7 @@
 //
 // A state is read and written once for five operations on an element, so the step is
 // bound by HBM bandwidth (by latency for a few sequences).  S / 4 lanes share a channel,
-// each with four states in one 16-byte load; a CTA owns 1024 / S channels and goes over
+// each with four states in one 16-byte load; a CTA owns 512 / S channels and goes over
 // SEQS sequences with all of their loads on the way at once, its rates computed once.
 #include "gdn_ssm.cuh"
 
@@ -12,10 +12,12 @@ namespace gdn {
 namespace ssm {
 namespace {
 
-// Sequences of a CTA.  (1024 of [1280, 16]: 44 us; with 2, 6 or 8 of them 48, 52, 61; by CTAs
-// that stay and go over several groups, asked for one ahead, 70: the registers are missed.)
+// Sequences of a CTA, its threads, CTAs an SM.  (1024 of [1280, 16]: 35.4 us, 4.7 TB/s; with
+// 3, 6 or 8 sequences 39, 51, 51; 256 threads in 4 or 5 CTAs 37 and 41, 128 in 7, 8 or 10 37,
+// 36 and 39.  By CTAs that stay, the next states on their way to shared memory by asynchronous
+// copies, 42; to registers, 70.)
 constexpr int kSeqs = 4;
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = 128, kCtas = 9;
 
 struct StepParams {
   const void *x, *dt, *b, *c, *gate;
@@ -37,7 +39,7 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16 *p) {
 }
 
 template <typename T, int S, int SEQS>
-__global__ void __launch_bounds__(kStepThreads)
+__global__ void __launch_bounds__(kStepThreads, kCtas)
 gdn_ssm_step_kernel(const StepParams p) {
   constexpr int LS = S / 4, CH = kStepThreads / LS, PER = (SEQS + LS - 1) / LS;
   constexpr uint32_t kAll = 0xffffffffu;
@@ -134,9 +136,9 @@ gdn_ssm_step_kernel(const StepParams p) {
 
 template <typename T, int S>
 cudaError_t launch_s(const StepParams &p, cudaStream_t stream) {
-  constexpr int CH = 1024 / S;
+  constexpr int CH = 4 * kStepThreads / S;
   const int blocks = (p.D + CH - 1) / CH;
-  if ((int64_t)blocks * p.num_seqs >= 16 * kSMs) {
+  if ((int64_t)blocks * p.num_seqs >= 32 * kSMs) {
     const dim3 grid(blocks, (p.num_seqs + kSeqs - 1) / kSeqs);
     gdn_ssm_step_kernel<T, S, kSeqs><<<grid, kStepThreads, 0, stream>>>(p);
   } else {
