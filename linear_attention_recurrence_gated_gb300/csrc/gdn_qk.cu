@@ -13,9 +13,12 @@
 // are both in the thread (columns 8 v and R / 2 + 8 v for pairs R / 2 apart), so that
 // packed arithmetic turns them without exchanges between lanes; where R / 2 is not a
 // multiple of eight a row goes through shared memory.  The cosines and sines of a token
-// are computed once, in shared memory, for all of its heads of q, or of k: a CTA takes one
-// of the two.  An angle's whole turns are taken off exactly: inv_freq / 2 pi is held as a
-// fraction of 2^64, whose product with the position drops them by overflowing.
+// are computed once, in shared memory, for all of its heads: forward of q and k in turn
+// ([8, 4096, 16 + 16, 64], bf16: 49 us, 5.5 TB/s; with CTAs of their own for q and for k, 55:
+// the table was a third of their instructions), backward, where a thread's sums for the
+// weight are of one of the two, of q or of k.  An angle's whole turns are taken off exactly:
+// inv_freq / 2 pi is held as a fraction of 2^64, whose product with the position drops them
+// by overflowing.
 #include "gdn_launch.cuh"
 #include "gdn_layers.cuh"
 
@@ -26,10 +29,12 @@ namespace {
 using namespace layer;
 
 constexpr int kThreads = 256;
-// CTAs an SM.  (bf16 forward: two rows of a thread together in three CTAs took 63 us where one
-// row in four takes 61, [8, 4096, 16 + 16, 64]; four rows in two 69.)
+// CTAs an SM.  (bf16 forward, [8, 4096, 16 + 16, 64]: 49 us, 53 with three, 59 with six.)
 template <typename T, bool BACK> constexpr int kCtas = BACK ? 2 : sizeof(T) == 2 ? 4 : 3;
-constexpr int kTokens = 8;     // most tokens of a CTA at a time
+// Most tokens of a CTA at a time.  (Forward as above, with 4, 6, 12: 51, 59, 49 us; backward,
+// [4, 8192, 16 + 16, 128], 151, with them 168, 158, 149, and fp32, [4, 4096, 32 + 8, 64], 104,
+// with them 142, 115, 109.)
+constexpr int kTokens = 8;
 constexpr int kMaxHalf = 128;  // most pairs of a head
 
 // q, or k.
@@ -39,8 +44,9 @@ struct Side {
   const float *w;
   float *dw;
   int64_t stride;
-  int32_t heads, ctas;    // CTAs that take this side
+  int32_t heads, ctas;    // backward: CTAs that take this side; forward: all, of the first
   float scale;
+  uint32_t magic;         // 2^32 / heads, rounded up: rows of a tile < 2^16
 };
 struct Params {
   Side side[2];
@@ -196,55 +202,65 @@ gdn_qk_norm_kernel(const Params p) {
   __shared__ __align__(16) float tables[2][kTokens * 2 * kMaxHalf];   // of a tile and the next
   __shared__ __align__(16) float rows_buf[RG * LR * 16];
   __shared__ uint64_t freq[kMaxHalf];
-  const int tid = threadIdx.x, rg = tid / LR, which = (int)blockIdx.x >= p.side[0].ctas;
-  const Side &s = p.side[which];
+  __shared__ __align__(16) float weights[BACK ? 1 : 2][LR * 16];   // times q's scale
+  const int tid = threadIdx.x, rg = tid / LR;
+  // the sides that this CTA takes
+  const int side0 = BACK && (int)blockIdx.x >= p.side[0].ctas, side1 = BACK ? side0 : 1;
   const Cols col = cols_of<M>(p, tid % LR);
   // (lanes without columns read the first ones, and store nothing)
   const int c0 = col.on[0] ? col.c[0] : 0, c1 = col.on[1] ? col.c[1] : 0;
   float *buf = rows_buf + rg * LR * 16;
   if (BACK) let_second();
   uint64_t w[2][4], own[2][4] = {}, all[2][4] = {};   // own, all: sums for the weight
+  if constexpr (BACK) {
+    const Side &s = p.side[side0];
 #pragma unroll
-  for (int g = 0; g < 2; ++g)
+    for (int g = 0; g < 2; ++g)
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int c = (g ? c1 : c0) + 2 * m;
-      w[g][m] = s.w ? pk(s.w[c], s.w[c + 1]) : pk(1.f, 1.f);
-      w[g][m] = mul2(w[g][m], pk(s.scale, s.scale));
+      for (int m = 0; m < 4; ++m) {
+        const int c = (g ? c1 : c0) + 2 * m;
+        w[g][m] = s.w ? pk(s.w[c], s.w[c + 1]) : pk(1.f, 1.f);
+        w[g][m] = mul2(w[g][m], pk(s.scale, s.scale));
+      }
+  } else {
+    for (int i = tid; i < 2 * LR * 16; i += kThreads) {
+      const Side &s = p.side[i / (LR * 16)];
+      const int c = i % (LR * 16);
+      weights[i / (LR * 16)][c] = s.w && c < p.D ? s.w[c] * s.scale : s.scale;
     }
+  }
   int lanes = 32;
   if (p.R) {
     load_freq(p, freq);
     while (lanes < p.R / 2) lanes *= 2;
   }
   const float over = p.l2 ? 1.f : 1.f / (float)p.D;
-  const uint32_t magic = 0xffffffffu / s.heads + 1;   // 2^32 / heads, rounded up: rows < 2^16
   const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
-  const int width = s.heads * p.D;
+  const int ctas = p.side[side0].ctas;
   int summed = 0, which_table = 0;
-  if (p.R) __syncthreads();
-  for (int64_t tile = blockIdx.x - (which ? p.side[0].ctas : 0); tile < tiles; tile += s.ctas) {
+  __syncthreads();
+  for (int64_t tile = blockIdx.x - (side0 ? p.side[0].ctas : 0); tile < tiles; tile += ctas) {
     const int64_t tok0 = tile * p.tile;
-    const int cnt = (int)(p.tokens - tok0 < p.tile ? p.tokens - tok0 : p.tile), rows = cnt * s.heads;
-    const T *xs = static_cast<const T *>(s.x) + tok0 * s.stride;
-    const T *gs = static_cast<const T *>(s.g) + tok0 * width;
-    T *out = static_cast<T *>(s.out) + tok0 * width;
+    const int cnt = (int)(p.tokens - tok0 < p.tile ? p.tokens - tok0 : p.tile);
     Raw8<T> x[2], d[BACK ? 2 : 1];
-    int tok, at;
-    const auto fetch = [&](int r) {   // (rows behind the last: the last)
+    int tok, at, rows;
+    const auto fetch = [&](int side, int r) {   // (rows behind the last: the last)
+      const Side &s = p.side[side];
+      rows = cnt * s.heads;
       r = r < rows ? r : rows - 1;
-      tok = s.heads == 1 ? r : (int)__umulhi((uint32_t)r, magic);
+      tok = s.heads == 1 ? r : (int)__umulhi((uint32_t)r, s.magic);
       const int head = (r - tok * s.heads) * p.D;
-      at = tok * width + head;
-      const T *from = xs + tok * s.stride + head;
+      at = tok * s.heads * p.D + head;
+      const T *from = static_cast<const T *>(s.x) + tok0 * s.stride + tok * s.stride + head;
       x[0].load(from + c0);
       x[1].load(from + c1);
       if constexpr (BACK) {
-        d[0].load(gs + at + c0);
-        d[1].load(gs + at + c1);
+        const T *g = static_cast<const T *>(s.g) + tok0 * (s.heads * p.D) + at;
+        d[0].load(g + c0);
+        d[1].load(g + c1);
       }
     };
-    fetch(rg);   // on its way while the table is made
+    fetch(side0, rg);   // on its way while the table is made
     // (a table is made again two tiles later: every thread has passed a barrier after reading it)
     which_table ^= 1;
     float *table = tables[which_table];
@@ -252,10 +268,13 @@ gdn_qk_norm_kernel(const Params p) {
       turn_table(p, tok0, cnt, lanes, freq, table);
       __syncthreads();
     }
-    for (int base = 0; base < rows; base += RG) {
+    int side = side0, base = 0;
+    while (side <= side1) {
+      const Side &s = p.side[side];
       const bool on = base + rg < rows;
       const float *cs = table + tok * 2 * p.pitch;
-      T *to = out + at;
+      T *to = static_cast<T *>(s.out) + tok0 * (s.heads * p.D) + at;
+      const float *ws = weights[BACK ? 0 : side];
       uint64_t xv[2][4], u[2][4], ss = 0ull;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -265,12 +284,19 @@ gdn_qk_norm_kernel(const Params p) {
         for (int m = 0; m < 4; ++m) ss = fma2(xv[g][m], xv[g][m], ss);
         if constexpr (BACK) unpack(d[g], u[g]);
       }
-      if (base + RG < rows) fetch(base + RG + rg);
+      base += RG;
+      if (base >= rows) {
+        base = 0;
+        ++side;
+      }
+      if (side <= side1) fetch(side, base + rg);
       float lo, hi;
       unpk(ss, lo, hi);
       const float r = rsqrtf(fmaf(row_sum<LR>(lo + hi), over, p.eps));
       const uint64_t rr = pk(r, r);
       if constexpr (!BACK) {
+        load_pairs(ws + c0, w[0]);
+        load_pairs(ws + c1, w[1]);
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
@@ -324,7 +350,7 @@ gdn_qk_norm_kernel(const Params p) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)   // (du carries q's scale)
         *reinterpret_cast<uint64_t *>(buf + col.c[g] + 2 * m) =
-            mul2(add2(all[g][m], own[g][m]), pk(s.scale, s.scale));
+            mul2(add2(all[g][m], own[g][m]), pk(p.side[side0].scale, p.side[side0].scale));
     __syncthreads();
     for (int c = tid; c < p.D; c += kThreads) {
       float sum = 0.f;
@@ -355,19 +381,19 @@ __global__ void __launch_bounds__(1024) gdn_qk_weights_kernel(const Params p) {
   if (c < p.D && s.dw) s.dw[c] = sum;
 }
 
-// Tokens of a tile (one where there are few) and CTAs, those that fit on the GPU, in
+// Tokens of a tile (one where there are few) and CTAs, those that fit on the GPU; backward in
 // proportion to the heads.
 struct Grid {
   int tile;
   int64_t ctas[2];
 };
-Grid grid_of(int64_t tokens, int64_t Hq, int64_t Hk, int ctas) {
+Grid grid_of(int64_t tokens, int64_t Hq, int64_t Hk, int ctas, bool back) {
   Grid g;
   const int64_t fit = ctas * kSMs;
   g.tile = tokens >= 2 * kTokens * kSMs ? kTokens : 1;
   const int64_t tiles = (tokens + g.tile - 1) / g.tile;
   int64_t q = fit * Hq / (Hq + Hk);
-  q = q < 1 ? 1 : q > fit - 1 ? fit - 1 : q;
+  q = !back ? fit : q < 1 ? 1 : q > fit - 1 ? fit - 1 : q;
   const int64_t k = fit - q;
   g.ctas[0] = q < tiles ? q : tiles;
   g.ctas[1] = k < tiles ? k : tiles;
@@ -430,9 +456,9 @@ gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, cons
   if (!apart(outs, ins)) return GDN_ERR_INVALID_ARG;
   Params p{};
   const Grid g = grid_of((int64_t)rows, q_heads, k_heads,
-                         dtype == GDN_F32 ? kCtas<float, false> : kCtas<__nv_bfloat16, false>);
-  p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale};
-  p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f};
+                         dtype == GDN_F32 ? kCtas<float, false> : kCtas<__nv_bfloat16, false>, false);
+  p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale, 0xffffffffu / q_heads + 1};
+  p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f, 0xffffffffu / k_heads + 1};
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.tokens = (int64_t)rows;
@@ -485,7 +511,7 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   const void *ptrs[] = {q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k_out, dq, dk,
                         dq_weight, dk_weight, workspace};
   if (!all_aligned(ptrs)) return GDN_ERR_INVALID_ARG;
-  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, kCtas<float, true>);
+  const Grid g = grid_of((int64_t)rows, q_heads, k_heads, kCtas<float, true>, true);
   const bool sums = dq_weight || dk_weight;
   if (!workspace || workspace_bytes < (size_t)(g.ctas[0] + g.ctas[1]) * w_bytes) return GDN_ERR_WORKSPACE;
   const Range outs[] = {{dq, rows * wq * e}, {dk, rows * wk * e}, {dq_weight, w_bytes},
@@ -499,8 +525,8 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   for (int i = 1; i < 9; ++i)
     if (overlaps(ins[0], ins[i])) return GDN_ERR_INVALID_ARG;
   Params p{};
-  p.side[0] = {q, d_q_out, dq, q_weight, dq_weight, sq, q_heads, (int32_t)g.ctas[0], q_scale};
-  p.side[1] = {k, d_k_out, dk, k_weight, dk_weight, sk, k_heads, (int32_t)g.ctas[1], 1.f};
+  p.side[0] = {q, d_q_out, dq, q_weight, dq_weight, sq, q_heads, (int32_t)g.ctas[0], q_scale, 0xffffffffu / q_heads + 1};
+  p.side[1] = {k, d_k_out, dk, k_weight, dk_weight, sk, k_heads, (int32_t)g.ctas[1], 1.f, 0xffffffffu / k_heads + 1};
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.part = static_cast<float *>(workspace);
