@@ -49,8 +49,10 @@ template <int N>
 __device__ __forceinline__ void wait_groups() {   // all but the last N have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// (fp32: 48 KB a CTA of the forward pass, three an SM; 85 KB of the backward pass, two)
-template <typename T, bool BACK> constexpr int kStages = sizeof(T) == 2 ? 4 : BACK ? 2 : 3;
+// (fp32: 48 KB a CTA of the forward pass, three an SM; 85 KB of the backward pass, two.  bf16,
+// backward, [4, 4096, 1280]: two stages 33 us, three and four 35, six 43; forward, packed,
+// three or four 106 to 108)
+template <typename T, bool BACK> constexpr int kStages = BACK ? 2 : sizeof(T) == 2 ? 4 : 3;
 
 struct Params {
   Sequences seq;
@@ -200,14 +202,22 @@ __device__ __forceinline__ void prefix_window(const Params &p, const Segment &s,
     r.get(win[i]);
   }
 }
-// z of a token, whose input then moves into the window.
+// z of a token, whose input then moves into the window.  (Scalar sums: their operands need
+// not lie in pairs.  In packed ones the backward pass took 37 us where it takes 33,
+// [4, 4096, 1280], bf16; dw and dx in scalar arithmetic too, 35.)
 template <int K>
 __device__ __forceinline__ uint64_t sum_taps(const uint64_t (&w)[K][2], const uint64_t (&bias)[2],
                                              uint64_t (&win)[K > 1 ? K - 1 : 1][2], uint64_t v, int j) {
-  uint64_t z = bias[j];
+  float lo, hi, w0, w1, x0, x1;
+  unpk(bias[j], lo, hi);
 #pragma unroll
-  for (int k = 0; k < K - 1; ++k) z = fma2(w[k][j], win[k][j], z);
-  return fma2(w[K - 1][j], v, z);
+  for (int k = 0; k < K; ++k) {
+    unpk(w[k][j], w0, w1);
+    unpk(k < K - 1 ? win[k][j] : v, x0, x1);
+    lo = fmaf(w0, x0, lo);
+    hi = fmaf(w1, x1, hi);
+  }
+  return pk(lo, hi);
 }
 template <int K>
 __device__ __forceinline__ void move_on(uint64_t (&win)[K > 1 ? K - 1 : 1][2], uint64_t v, int j) {
