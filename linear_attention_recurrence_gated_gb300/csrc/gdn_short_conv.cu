@@ -10,7 +10,10 @@
 // the last K - 1 inputs (backward: and the K - 1 unfinished rows of dx) in registers, so
 // that a row is read once but at the segments' seams.  Its rows come through a ring in
 // shared memory that asynchronous copies fill some batches ahead (each thread its own
-// part: no barriers).  Both passes are bound by HBM bandwidth.
+// part: no barriers).  Forward, 32 packed sequences of 120k tokens together, 1280 channels,
+// bf16: 108 us, 5.7 TB/s, bound by HBM (with rows asked for a batch ahead in registers 155).
+// Backward, [4, 4096, 1280]: 33 us, 3.8 TB/s, 5 of them the second launch; its multiply-adds'
+// pipe is busy for half of the rest (in registers 50).
 #include "gdn_launch.cuh"
 #include "gdn_layers.cuh"
 

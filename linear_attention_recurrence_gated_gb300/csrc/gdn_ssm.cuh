@@ -7,14 +7,13 @@
 // Every (channel, state) decays at a rate of its own, so there is no product that the
 // tensor cores could take: each of the T D S elements costs an exponential and four
 // multiply-adds on the CUDA cores, and that is what bounds the scan (a GB300 SM does 32
-// exponentials and 128 multiply-adds a clock; the bytes of a token's channel, 8 in bf16,
-// would take a third of the time of its 16 states).
+// exponentials and 128 multiply-adds a clock: 33 us each for [4, 4096, 1280], S = 16, whose
+// bytes take 25).
 //
-// A thread holds 4 channels x 4 states in registers, pairs of channels in packed fp32
-// arithmetic.  S / 4 lanes share 4 channels, so that a token's c . h is summed over S / 4
-// lanes, its gradients of b and c over the 128 / S others; four states of b and c and four
-// channels of delta and delta x come from shared memory in 16-byte loads that all lanes
-// of a row share.  A CTA of 4 warps owns 2048 / S channels of one group.
+// A CTA of 4 warps owns 2048 / S channels of one group, a thread 16 elements in registers,
+// in packed fp32 arithmetic.  Forward, 16 states of a channel (8 of two for S = 8): c . h is
+// a sum inside the thread.  In the backward pass, 4 channels x 4 states: sums over states
+// (b . G, A w) and over channels (db, dc) meet half-way, over S / 4 and 128 / S lanes.
 //
 // Sequences are cut along time where their channels alone leave SMs idle: a first launch
 // leaves each segment's state from zero and its sum of delta, and a segment's start is
@@ -253,9 +252,8 @@ __device__ __forceinline__ void join(uint64_t (&h)[2][4], const uint64_t (&A)[2]
 // The forward scans' threads: 16 consecutive elements of [D][S], that is 16 states of one
 // channel (8 of two for S = 8), pairs of states in packed arithmetic.  c . h is summed
 // inside a thread up to S = 16, over S / 16 lanes beyond; b and c are read by whole warps
-// from one address.  (With 4 channels x 4 states a thread the
-// call took 204 us where this takes 179, [4, 4096, 1280], S = 16: three shuffles and their
-// selects a token.)
+// from one address.  (With 4 channels x 4 states a thread the call took 204 us where this
+// took 179, [4, 4096, 1280], S = 16: three shuffles and their selects a token.)
 template <int S>
 struct Run {
   static constexpr int SPT = S < 16 ? S : 16;   // states of a channel
@@ -384,9 +382,9 @@ __device__ __forceinline__ void lifts4(const uint64_t (&A)[2][4], const float *d
 
 // The split along time of launches of `blocks` CTAs per segment, `ctas` an SM at a time, in
 // chunks of 32 tokens; a segment's start costs about half a chunk, the first launch of it
-// `first` of the second.  (Forward, [4, 4096, 1280] / [1, 65536, 2048]: 179 / 992 us; a
-// start of a whole chunk 179 / 1027, of two 179 / 1027; two CTAs an SM 241 / 1310, four
-// 192 / 1031, six 186 / 992.)
+// `first` of the second.  (Forward, [4, 4096, 1280] / [1, 65536, 2048], before the lifts
+// went by tiles: 179 / 992 us; a start of a whole chunk 179 / 1027, of two 179 / 1027; two
+// CTAs an SM 241 / 1310, four 192 / 1031, six 186 / 992.)
 constexpr int kChunkTokens = 32;
 inline lin::Plan plan(int64_t num_seqs, int64_t seq_len, bool packed, int64_t blocks, int ctas,
                       double first) {

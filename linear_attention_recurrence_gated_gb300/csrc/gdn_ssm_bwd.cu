@@ -16,6 +16,13 @@
 // of the decays).  Sums over a CTA's channels (db, dc) and over tokens (dA_log, dD_skip,
 // ddt_bias) are left in the workspace and added up in a fixed order by the last launch:
 // results are bitwise reproducible.
+//
+// [4, 4096, 1280], S = 16, bf16 with a gate: 561 us; the launches 153, 404 and 10.  375
+// instructions a token and channel in the second: 136 of them the products and
+// exponentials, some 80 the sums over lanes, the rest inputs, softplus, the gate and their
+// gradients.  The multiply-adds' pipe is busy for 42 %, issue 52 %.  (States in shared
+// memory, two CTAs an SM: 763 us in all; in tensor memory 603; inputs and kept states by
+// asynchronous copies 554; lifts by tiles, for their accuracy, 561.)
 #include "gdn_ptx.cuh"
 #include "gdn_ssm.cuh"
 

@@ -6,6 +6,14 @@
 // fp32 together with b and c; then every thread runs its 16 elements over the tile while
 // the next tile's inputs are on their way to registers; then the tile's outputs take the
 // skip and the gate on their way out.
+//
+// [4, 4096, 1280], S = 16, bf16 with a gate: 181 us, 75 of them the first launch; 107
+// instructions a token and channel where outputs are formed, of which 32 packed
+// multiply-adds and 16 exponentials are the scan itself, the rest its operands, softplus and
+// the gate.  No pipe is full (multiply-adds 50 %, exponentials 42 %, issue 56 %): a warp's
+// exponentials and products follow one another.  More warps do not help (inputs by
+// asynchronous copies, four CTAs an SM without spills: 189), nor the next token's
+// exponentials between this one's products (192).  [1, 65536, 2048]: 1024 us.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
