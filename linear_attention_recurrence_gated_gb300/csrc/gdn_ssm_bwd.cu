@@ -17,12 +17,13 @@
 // ddt_bias) are left in the workspace and added up in a fixed order by the last launch:
 // results are bitwise reproducible.
 //
-// [4, 4096, 1280], S = 16, bf16 with a gate: 561 us; the launches 153, 404 and 10.  375
+// [4, 4096, 1280], S = 16, bf16 with a gate: 554 us; the launches 150, 400 and 10.  375
 // instructions a token and channel in the second: 136 of them the products and
 // exponentials, some 80 the sums over lanes, the rest inputs, softplus, the gate and their
 // gradients.  The multiply-adds' pipe is busy for 42 %, issue 52 %.  (States in shared
 // memory, two CTAs an SM: 763 us in all; in tensor memory 603; inputs and kept states by
-// asynchronous copies 554; lifts by tiles, for their accuracy, 561.)
+// asynchronous copies 554; lifts by tiles, for their accuracy, 561; the first two loops over
+// a tile unrolled whole 554, the third too 563.)
 #include "gdn_ptx.cuh"
 #include "gdn_ssm.cuh"
 
@@ -211,7 +212,7 @@ gdn_ssm_keep_kernel(const BwdParams p) {
       float part[CPT] = {};
       uint64_t lift[2];
       lifts16<CPT>(A, sd + r * CB + cl, lift);
-#pragma unroll 4
+#pragma unroll
       for (int t = r; t < r + kL; ++t) {   // (tokens past the last: zeros)
         uint64_t d[CPT], u[CPT], y[CPT], b2[NP], c2[NP];
         twice<CPT>(sd + t * CB + cl, d);
@@ -537,7 +538,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       uint64_t lift[2];
       lifts4(A, sd + 4 * cl, lift);
       // the tile's states
-#pragma unroll 4
+#pragma unroll
       for (int t = 0; t < kL; ++t) {
         store_tm(t, h);
         const Pairs d = lds2(sd + t * CB + 4 * cl), u = lds2(su + t * CB + 4 * cl);

@@ -7,13 +7,14 @@
 // the next tile's inputs are on their way to registers; then the tile's outputs take the
 // skip and the gate on their way out.
 //
-// [4, 4096, 1280], S = 16, bf16 with a gate: 181 us, 75 of them the first launch; 107
+// [4, 4096, 1280], S = 16, bf16 with a gate: 178 us, 74 of them the first launch; 107
 // instructions a token and channel where outputs are formed, of which 32 packed
 // multiply-adds and 16 exponentials are the scan itself, the rest its operands, softplus and
 // the gate.  No pipe is full (multiply-adds 50 %, exponentials 42 %, issue 56 %): a warp's
-// exponentials and products follow one another.  More warps do not help (inputs by
-// asynchronous copies, four CTAs an SM without spills: 189), nor the next token's
-// exponentials between this one's products (192).  [1, 65536, 2048]: 1024 us.
+// exponentials and products follow one another.  More warps do not help (four CTAs an SM
+// without spills, inputs by asynchronous copies or gate and x read when they are needed:
+// 189 and 185), nor the next token's exponentials between this one's products (192), nor 32
+// elements a thread, which halve the loads of b and c (200).  [1, 65536, 2048]: 1004 us.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -159,8 +160,9 @@ gdn_ssm_scan_kernel(const Params p) {
     float part[CPT] = {};
     uint64_t lift[2];
     lifts16<CPT>(A, sd + cl, lift);
-    const int steps = (cnt + 3) & ~3;   // (rows past the last token are zeros: no change)
-#pragma unroll 4
+    // (rows past the last token are zeros: no change.  Four tokens at a time 185 us, two 189)
+    const int steps = (cnt + 7) & ~7;
+#pragma unroll 8
     for (int t = 0; t < steps; ++t) {
       uint64_t d[CPT], u[CPT], b2[NP], c2[NP];
       twice<CPT>(sd + t * CB + cl, d);
