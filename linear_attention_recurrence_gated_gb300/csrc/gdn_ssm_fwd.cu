@@ -7,14 +7,15 @@
 // the next tile's inputs are on their way to registers; then the tile's outputs take the
 // skip and the gate on their way out.
 //
-// [4, 4096, 1280], S = 16, bf16 with a gate: 178 us, 74 of them the first launch; 107
+// [4, 4096, 1280], S = 16, bf16 with a gate: 176 us, 73 of them the first launch; some 105
 // instructions a token and channel where outputs are formed, of which 32 packed
 // multiply-adds and 16 exponentials are the scan itself, the rest its operands, softplus and
-// the gate.  No pipe is full (multiply-adds 50 %, exponentials 42 %, issue 56 %): a warp's
-// exponentials and products follow one another.  More warps do not help (four CTAs an SM
-// without spills, inputs by asynchronous copies or gate and x read when they are needed:
-// 189 and 185), nor the next token's exponentials between this one's products (192), nor 32
-// elements a thread, which halve the loads of b and c (200).  [1, 65536, 2048]: 1004 us.
+// the gate.  No pipe is full (multiply-adds 50 %, exponentials 43 %, shared memory 62 %,
+// issue 56 %), but each is near what warps that take turns at them reach: fewer instructions
+// help, more warps do not (four CTAs an SM without spills, inputs by asynchronous copies or
+// gate and x read when they are needed: 189 and 185), nor the next token's exponentials
+// between this one's products (192), nor 32 elements a thread, which halve the loads of b
+// and c (200).  [1, 65536, 2048]: 995 us.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -171,15 +172,15 @@ gdn_ssm_scan_kernel(const Params p) {
       if constexpr (OUT) pairs<NP>(sbc + TT * S + t * S + 16 * sl, swap, c2);
 #pragma unroll
       for (int k = 0; k < CPT; ++k) {
-        uint64_t y[2];   // two sums: half the chain of dependent additions
+        uint64_t y;   // (one chain of additions: with two of them 178 us for 176, with four 180)
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           uint64_t &e = h[k * NP + i];
           e = fma2(decay(d[k], A[k * NP + i], lift[(k * NP + i) / 4]), e, mul2(u[k], b2[i]));
-          if constexpr (OUT) y[i & 1] = i > 1 ? fma2(c2[i], e, y[i & 1]) : mul2(c2[i], e);
+          if constexpr (OUT) y = i ? fma2(c2[i], e, y) : mul2(c2[i], e);
         }
         if constexpr (OUT) {
-          float v = total(add2(y[0], y[1]));
+          float v = total(y);
 #pragma unroll
           for (int m = 1; m < LS; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
           if (LS == 1 || sl == 0) sy[t * CB + cl + k] = v;
