@@ -11,7 +11,7 @@
 // that a row is read once but at the segments' seams.  Its rows come through a ring in
 // shared memory that asynchronous copies fill some batches ahead (each thread its own
 // part: no barriers).  Forward, 32 packed sequences of 120k tokens together, 1280 channels,
-// bf16: 108 us, 5.7 TB/s, bound by HBM (with rows asked for a batch ahead in registers 155).
+// bf16: 106 us, 5.8 TB/s, bound by HBM (with rows asked for a batch ahead in registers 155).
 // Backward, [4, 4096, 1280]: 33 us, 3.8 TB/s, 5 of them the second launch; its multiply-adds'
 // pipe is busy for half of the rest (in registers 50).
 #include "gdn_launch.cuh"
@@ -205,12 +205,18 @@ __device__ __forceinline__ void prefix_window(const Params &p, const Segment &s,
     r.get(win[i]);
   }
 }
-// z of a token, whose input then moves into the window.  (Scalar sums: their operands need
-// not lie in pairs.  In packed ones the backward pass took 37 us where it takes 33,
-// [4, 4096, 1280], bf16; dw and dx in scalar arithmetic too, 35.)
-template <int K>
+// z of a token, whose input then moves into the window.  Backward in scalar arithmetic, whose
+// operands need not lie in pairs: 33 us where packed sums took 37, [4, 4096, 1280], bf16 (dw
+// and dx in scalar arithmetic too, 35); forward 106 us packed, 108 scalar.
+template <int K, bool PACKED>
 __device__ __forceinline__ uint64_t sum_taps(const uint64_t (&w)[K][2], const uint64_t (&bias)[2],
                                              uint64_t (&win)[K > 1 ? K - 1 : 1][2], uint64_t v, int j) {
+  if constexpr (PACKED) {
+    uint64_t z = bias[j];
+#pragma unroll
+    for (int k = 0; k < K; ++k) z = fma2(w[k][j], k < K - 1 ? win[k][j] : v, z);
+    return z;
+  }
   float lo, hi, w0, w1, x0, x1;
   unpk(bias[j], lo, hi);
 #pragma unroll
@@ -278,7 +284,7 @@ gdn_conv_fwd_kernel(const Params p) {
     r.get(v);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      z[j] = sum_taps<K>(w, bias, win, v[j], j);
+      z[j] = sum_taps<K, true>(w, bias, win, v[j], j);
       if constexpr (SILU) z[j] = mul2(z[j], sigmoid2(z[j]));
       move_on<K>(win, v[j], j);
     }
@@ -390,7 +396,7 @@ gdn_conv_bwd_kernel(const Params p) {
       yt.get(d);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        d[j] = through<SILU>(d[j], sum_taps<K>(w, bias, win, v[j], j));
+        d[j] = through<SILU>(d[j], sum_taps<K, false>(w, bias, win, v[j], j));
         if (counts) {
 #pragma unroll
           for (int k = 0; k < P; ++k) own[k][j] = fma2(d[j], win[k][j], own[k][j]);
