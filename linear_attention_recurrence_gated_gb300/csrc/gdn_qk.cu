@@ -457,8 +457,10 @@ gdn_status gdn_qk_norm(const void *q, const void *k, const float *q_weight, cons
   Params p{};
   const Grid g = grid_of((int64_t)rows, q_heads, k_heads,
                          dtype == GDN_F32 ? kCtas<float, false> : kCtas<__nv_bfloat16, false>, false);
-  p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale, 0xffffffffu / q_heads + 1};
-  p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f, 0xffffffffu / k_heads + 1};
+  p.side[0] = {q, nullptr, q_out, q_weight, nullptr, sq, q_heads, (int32_t)g.ctas[0], q_scale,
+               0xffffffffu / q_heads + 1};
+  p.side[1] = {k, nullptr, k_out, k_weight, nullptr, sk, k_heads, (int32_t)g.ctas[1], 1.f,
+               0xffffffffu / k_heads + 1};
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.tokens = (int64_t)rows;
@@ -525,8 +527,10 @@ gdn_status gdn_qk_norm_bwd(const void *q, const void *k, const float *q_weight,
   for (int i = 1; i < 9; ++i)
     if (overlaps(ins[0], ins[i])) return GDN_ERR_INVALID_ARG;
   Params p{};
-  p.side[0] = {q, d_q_out, dq, q_weight, dq_weight, sq, q_heads, (int32_t)g.ctas[0], q_scale, 0xffffffffu / q_heads + 1};
-  p.side[1] = {k, d_k_out, dk, k_weight, dk_weight, sk, k_heads, (int32_t)g.ctas[1], 1.f, 0xffffffffu / k_heads + 1};
+  p.side[0] = {q, d_q_out, dq, q_weight, dq_weight, sq, q_heads, (int32_t)g.ctas[0], q_scale,
+               0xffffffffu / q_heads + 1};
+  p.side[1] = {k, d_k_out, dk, k_weight, dk_weight, sk, k_heads, (int32_t)g.ctas[1], 1.f,
+               0xffffffffu / k_heads + 1};
   p.positions = positions;
   p.inv_freq = inv_freq;
   p.part = static_cast<float *>(workspace);

@@ -1602,8 +1602,9 @@ def gdn_conv_bwd(x, w, d_y, bias=None, x_prev=None, cu_seqlens=None, d_x_tail=No
     ws = _workspace(stream, x, workspace, gdn_conv_workspace_size(N, T, C, K), check)
     st = _on(f, dev)(
         x.data_ptr(), w.data_ptr(), _p(bias), _p(x_prev), _p(cu_seqlens), d_y.data_ptr(),
-        _p(d_x_tail), dx.data_ptr(), _p(dw), _p(dbias), _p(dx_prev), B, T, C, K, N, _row_stride(f, "x", x), _CODES[x.dtype],
-        GDN_CONV_SILU if silu else 0, ws.data_ptr(), _nbytes(ws), _raw_stream(stream, dev))
+        _p(d_x_tail), dx.data_ptr(), _p(dw), _p(dbias), _p(dx_prev), B, T, C, K, N,
+        _row_stride(f, "x", x), _CODES[x.dtype], GDN_CONV_SILU if silu else 0, ws.data_ptr(),
+        _nbytes(ws), _raw_stream(stream, dev))
     if st or check:
         _done(f, st, check, ws, stream)
     return grads
