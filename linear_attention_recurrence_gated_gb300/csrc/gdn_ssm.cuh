@@ -218,9 +218,9 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
 // from -2^-8 to 0, 1.3e-8 at -2^-8, 3.1e-8 at -2^-7, 2.4e-8 on average from there to -1/2.
 // A lift of the exponent takes the mean away: by the slowest rate of the 4 or 8 elements that
 // share it, whose errors a state keeps longest, and one step of a tile.  (2^lift itself still
-// gives 1: delta = 0 keeps a state.  One lift for all, 2.5e-8, is a third operand less to
-// read, 179 us for 185, [4, 4096, 1280], S = 16, and left states of slow decays 1.1e-6 off for
-// 2.9e-7, and dA_log 2.2e-6 for 1.3e-6, over some 1000 tokens.)
+// gives 1: delta = 0 keeps a state.  One lift for all, 2.5e-8, left states of slow decays
+// 1.1e-6 off for 2.9e-7, and dA_log 2.2e-6 for 1.3e-6, over some 1000 tokens; it takes the
+// same time within 3 %, and so do lifts that go into a state once a tile.)
 __device__ __forceinline__ float lift_of(float delta, float rate) {
   return fminf(fmaxf(-5e-6f * rate * delta, 0.85e-8f), 3.1e-8f);
 }
