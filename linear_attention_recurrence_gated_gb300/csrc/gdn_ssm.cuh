@@ -214,8 +214,8 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
   return pk(ex2(lo), ex2(hi));
 }
 // exp(delta A) of a token.  The hardware's exp2 is low on average, and a state adds up
-// 1 / (1 - a) such errors.  Measured over 2^18 arguments an eighth of an octave: 6e-9 to 9e-9
-// from -2^-8 to 0, 1.3e-8 at -2^-8, 3.1e-8 at -2^-7, 2.4e-8 on average from there to -1/2.
+// 1 / (1 - a) such errors.  Measured over 2^18 arguments an eighth of an octave: 4e-9 to 1e-8
+// from -2^-8 to 0, 1.3e-8 at -2^-8, 3.0e-8 at -2^-7, 2.2e-8 on average from there to -1/2.
 // A lift of the exponent takes the mean away: by the slowest rate of the 4 or 8 elements that
 // share it, whose errors a state keeps longest, and one step of a tile.  (2^lift itself still
 // gives 1: delta = 0 keeps a state.  One lift for all, 2.5e-8, left states of slow decays
