@@ -821,12 +821,15 @@ gdn_status gdn_pages_compact(void *pool, int64_t page_bytes, int32_t num_pages,
  * workspace: the first 256 bytes are the status word (zeroed once with
  * gdn_workspace_init); the bytes after it, of any contents, hold the states of segments
  * when sequences are cut along time to fill the GPU.  gdn_ssm_workspace_size(...) is
- * enough for any call of these sizes; with less (at least 256 bytes) sequences run uncut,
- * with the same results up to rounding.  Calls sharing a workspace are ordered (same
+ * enough for any call of these sizes, gdn_ssm_packed_workspace_size(...) for one of
+ * num_seqs packed sequences with total_tokens tokens together; with less (at least 256
+ * bytes) sequences run uncut, with the same results up to rounding.  Calls sharing a workspace are ordered (same
  * stream).  Errors as gdn_fwd (bad cu_seqlens: gdn_check).
  */
 size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
                               int32_t d_state, int32_t groups);
+size_t gdn_ssm_packed_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                     int32_t d_state, int32_t groups);
 gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const void *b,
                        const void *c, const float *D_skip, const void *gate, const float *dt_bias,
                        const float *initial_state, const int32_t *cu_seqlens, void *y,
@@ -857,10 +860,14 @@ gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const 
  * Sums over tokens, sequences and channels are fp32, in a fixed order: results are bitwise
  * reproducible.  No output may overlap an input or another output.  Sizes, strides, flags
  * and errors as gdn_ssm_fwd.  workspace: at least gdn_ssm_bwd_workspace_size(...) bytes,
- * its first 256 the status word.
+ * its first 256 the status word.  That size holds num_seqs rows of seq_len tokens; packed
+ * sequences need the gdn_ssm_bwd_packed_workspace_size(...) bytes of their total_tokens
+ * (with cu_seqlens, where seq_len is that total, num_seqs times fewer).
  */
 size_t gdn_ssm_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
                                   int32_t d_state, int32_t groups);
+size_t gdn_ssm_bwd_packed_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                         int32_t d_state, int32_t groups);
 gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const void *b,
                        const void *c, const float *D_skip, const void *gate, const float *dt_bias,
                        const float *initial_state, const int32_t *cu_seqlens, const void *d_y,

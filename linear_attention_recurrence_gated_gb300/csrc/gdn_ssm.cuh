@@ -400,6 +400,8 @@ struct Sizes {
   int64_t sx, sdt, sb, sc, sg;
   size_t state;
 };
+bool some_sizes(int32_t num_seqs, int32_t seq_len, int32_t channels, int32_t d_state,
+                int32_t groups);   // that a workspace can be sized for
 gdn_status check_sizes(int32_t batch, int32_t seq_len, int32_t channels, int32_t d_state,
                        int32_t groups, int32_t num_seqs, const void *cu, gdn_dtype dtype,
                        uint32_t flags);

@@ -800,6 +800,21 @@ int64_t parts_of(int64_t slots, int64_t blocks) {
   const int64_t most = (6 * kSMs + blocks - 1) / blocks;
   return slots < most ? slots : most;
 }
+// The workspace of a call in any form that it may take (storage types, and uncut).
+size_t workspace_bytes_of(int32_t num_seqs, int32_t seq_len, bool packed, int32_t channels,
+                          int32_t d_state, int32_t groups) {
+  const int64_t blocks = channel_blocks(channels / groups, d_state), all = blocks * groups;
+  const int64_t rows = packed ? seq_len : (int64_t)num_seqs * seq_len;
+  size_t most = 0;
+  for (const auto &one : {plan(num_seqs, seq_len, packed, all, 2, kFirst),
+                          plan(num_seqs, seq_len, packed, all, 3, kFirst),
+                          lin::Plan{0, num_seqs}}) {
+    const size_t n = layout(rows, channels, d_state, groups, blocks, parts_of(one.slots, all),
+                            one).total;
+    most = n > most ? n : most;
+  }
+  return kStatusBytes + 4 * most;
+}
 
 template <typename T, int S>
 cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
@@ -855,22 +870,16 @@ extern "C" {
 size_t gdn_ssm_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
                                   int32_t d_state, int32_t groups) {
   using namespace gdn::ssm;
-  if (num_seqs <= 0 || seq_len < 0 || channels <= 0 || d_state <= 0 || groups <= 0 ||
-      channels % groups || !state_size(d_state))
-    return 0;
-  const int64_t blocks = channel_blocks(channels / groups, d_state), all = blocks * groups;
-  size_t most = 0;
-  for (bool packed : {false, true}) {
-    const int64_t rows = packed ? seq_len : (int64_t)num_seqs * seq_len;
-    for (const auto &one : {plan(num_seqs, seq_len, packed, all, 2, kFirst),
-                            plan(num_seqs, seq_len, packed, all, 3, kFirst),
-                            gdn::lin::Plan{0, num_seqs}}) {
-      const size_t n = layout(rows, channels, d_state, groups, blocks, parts_of(one.slots, all),
-                              one).total;
-      most = n > most ? n : most;
-    }
-  }
-  return gdn::kStatusBytes + 4 * most;
+  if (!some_sizes(num_seqs, seq_len, channels, d_state, groups)) return 0;
+  const size_t dense = workspace_bytes_of(num_seqs, seq_len, false, channels, d_state, groups);
+  const size_t packed = workspace_bytes_of(num_seqs, seq_len, true, channels, d_state, groups);
+  return dense > packed ? dense : packed;
+}
+size_t gdn_ssm_bwd_packed_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                         int32_t d_state, int32_t groups) {
+  using namespace gdn::ssm;
+  if (!some_sizes(num_seqs, total_tokens, channels, d_state, groups)) return 0;
+  return workspace_bytes_of(num_seqs, total_tokens, true, channels, d_state, groups);
 }
 
 gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const void *b,

@@ -253,8 +253,21 @@ cudaError_t launch_t(const Params &p, int S, int groups, cudaStream_t stream) {
 constexpr double kFirst = 0.7;   // the first launch forms no outputs
 constexpr int kCtas = 3;         // an SM (the outputs' kernel's registers)
 
+// What the segments of a call take behind the status word.
+size_t segment_bytes(int32_t num_seqs, int32_t seq_len, bool packed, int32_t channels,
+                     int32_t d_state, int32_t groups) {
+  const int64_t blocks = (int64_t)groups * channel_blocks(channels / groups, d_state);
+  const auto pl = plan(num_seqs, seq_len, packed, blocks, kCtas, kFirst);
+  return pl.seg_len ? (size_t)pl.slots * channels * (d_state + 1) * 4 : 0;
+}
+
 }  // namespace
 
+bool some_sizes(int32_t num_seqs, int32_t seq_len, int32_t channels, int32_t d_state,
+                int32_t groups) {
+  return num_seqs > 0 && seq_len >= 0 && channels > 0 && d_state > 0 && groups > 0 &&
+         channels % groups == 0 && state_size(d_state);
+}
 gdn_status check_sizes(int32_t batch, int32_t seq_len, int32_t channels, int32_t d_state,
                        int32_t groups, int32_t num_seqs, const void *cu, gdn_dtype dtype,
                        uint32_t flags) {
@@ -285,17 +298,17 @@ extern "C" {
 size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
                               int32_t d_state, int32_t groups) {
   using namespace gdn::ssm;
-  if (num_seqs <= 0 || seq_len < 0 || channels <= 0 || d_state <= 0 || groups <= 0 ||
-      channels % groups || !state_size(d_state))
-    return 0;
-  const int64_t blocks = (int64_t)groups * channel_blocks(channels / groups, d_state);
-  size_t most = 0;
-  for (bool packed : {false, true}) {
-    const auto pl = plan(num_seqs, seq_len, packed, blocks, kCtas, kFirst);
-    const size_t n = pl.seg_len ? (size_t)pl.slots * channels * (d_state + 1) * 4 : 0;
-    most = n > most ? n : most;
-  }
-  return gdn::kStatusBytes + most;
+  if (!some_sizes(num_seqs, seq_len, channels, d_state, groups)) return 0;
+  const size_t dense = segment_bytes(num_seqs, seq_len, false, channels, d_state, groups);
+  const size_t packed = segment_bytes(num_seqs, seq_len, true, channels, d_state, groups);
+  return gdn::kStatusBytes + (dense > packed ? dense : packed);
+}
+size_t gdn_ssm_packed_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t channels,
+                                     int32_t d_state, int32_t groups) {
+  using namespace gdn::ssm;
+  if (!some_sizes(num_seqs, total_tokens, channels, d_state, groups)) return 0;
+  return gdn::kStatusBytes +
+         segment_bytes(num_seqs, total_tokens, true, channels, d_state, groups);
 }
 
 gdn_status gdn_ssm_fwd(const void *x, const void *dt, const float *A_log, const void *b,

@@ -51,7 +51,8 @@ EXPORTED = ("gdn_fwd_workspace_size", "gdn_workspace_init", "gdn_fwd", "gdn_chec
             "gdn_group_norm_workspace_size", "gdn_group_norm", "gdn_group_norm_bwd",
             "gdn_pages_workspace_size", "gdn_pages_copy", "gdn_pages_fork", "gdn_pages_free",
             "gdn_pages_compact",
-            "gdn_ssm_workspace_size", "gdn_ssm_fwd", "gdn_ssm_bwd_workspace_size", "gdn_ssm_bwd",
+            "gdn_ssm_workspace_size", "gdn_ssm_packed_workspace_size", "gdn_ssm_fwd",
+            "gdn_ssm_bwd_workspace_size", "gdn_ssm_bwd_packed_workspace_size", "gdn_ssm_bwd",
             "gdn_ssm_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd",
             "gdn_conv_step", "gdn_qk_norm", "gdn_qk_norm_workspace_size", "gdn_qk_norm_bwd")
 # ... and include/gdn_debug.h (self-tests of the failure reporting).
@@ -150,8 +151,10 @@ def lib() -> ctypes.CDLL:
                     ("gdn_pages_compact", st, [vp, i64, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp,
                                                sz, vp]),
                     ("gdn_ssm_workspace_size", sz, [i32] * 5),
+                    ("gdn_ssm_packed_workspace_size", sz, [i32] * 5),
                     ("gdn_ssm_fwd", st, [vp] * 12 + [i32] * 6 + [i64] * 5 + [st, u32, vp, sz, vp]),
                     ("gdn_ssm_bwd_workspace_size", sz, [i32] * 5),
+                    ("gdn_ssm_bwd_packed_workspace_size", sz, [i32] * 5),
                     ("gdn_ssm_bwd", st, [vp] * 21 + [i32] * 6 + [i64] * 5 + [st, u32, vp, sz, vp]),
                     ("gdn_ssm_step", st, [vp] * 12 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
                     ("gdn_conv_fwd", st, [vp] * 7 + [i32] * 5 + [i64, st, u32, vp, sz, vp]),
@@ -1376,14 +1379,19 @@ def _ssm_check(where, x, dt, A_log, b, c, D_skip, gate, dt_bias, h0, cu_seqlens,
 
 @functools.lru_cache(maxsize=256)
 def gdn_ssm_workspace_size(num_seqs: int, seq_len: int, channels: int, d_state: int,
-                           groups: int = 1) -> int:
-    return int(lib().gdn_ssm_workspace_size(num_seqs, seq_len, channels, d_state, groups))
+                           groups: int = 1, packed: bool = False) -> int:
+    """Bytes for a call of ``num_seqs`` rows of ``seq_len`` tokens; ``packed``: of ``num_seqs``
+    packed sequences, ``seq_len`` tokens together."""
+    size = lib().gdn_ssm_packed_workspace_size if packed else lib().gdn_ssm_workspace_size
+    return int(size(num_seqs, seq_len, channels, d_state, groups))
 
 
 @functools.lru_cache(maxsize=256)
 def gdn_ssm_bwd_workspace_size(num_seqs: int, seq_len: int, channels: int, d_state: int,
-                               groups: int = 1) -> int:
-    return int(lib().gdn_ssm_bwd_workspace_size(num_seqs, seq_len, channels, d_state, groups))
+                               groups: int = 1, packed: bool = False) -> int:
+    """As ``gdn_ssm_workspace_size``, of a backward pass."""
+    size = lib().gdn_ssm_bwd_packed_workspace_size if packed else lib().gdn_ssm_bwd_workspace_size
+    return int(size(num_seqs, seq_len, channels, d_state, groups))
 
 
 def gdn_ssm_fwd(x, dt, A_log, b, c, initial_state=None, cu_seqlens=None, *, D_skip=None, gate=None,
@@ -1406,7 +1414,8 @@ def gdn_ssm_fwd(x, dt, A_log, b, c, initial_state=None, cu_seqlens=None, *, D_sk
     y = _like_new(stream, x) if y is None else y
     if final_state is None and output_final_state:
         final_state = _empty(stream, x, (N, D, S), _F32)
-    ws = _workspace(stream, x, workspace, gdn_ssm_workspace_size(N, T, D, S, G), check)
+    ws = _workspace(stream, x, workspace,
+                    gdn_ssm_workspace_size(N, T, D, S, G, cu_seqlens is not None), check)
     st = _on(w, dev)(
         x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
         _p(gate), _p(dt_bias), _p(initial_state), _p(cu_seqlens), y.data_ptr(), _p(final_state), B,
@@ -1445,7 +1454,8 @@ def gdn_ssm_bwd(x, dt, A_log, b, c, d_y, initial_state=None, cu_seqlens=None, d_
                      ddt_bias=dbias, dh0=dh0)
     elif dx is None or ddt is None or db is None or dc is None:
         raise ValueError(f"{w}: grads must hold dx, ddt, db and dc")
-    ws = _workspace(stream, x, workspace, gdn_ssm_bwd_workspace_size(N, T, D, S, G), check)
+    ws = _workspace(stream, x, workspace,
+                    gdn_ssm_bwd_workspace_size(N, T, D, S, G, cu_seqlens is not None), check)
     st = _on(w, dev)(
         x.data_ptr(), dt.data_ptr(), A_log.data_ptr(), b.data_ptr(), c.data_ptr(), _p(D_skip),
         _p(gate), _p(dt_bias), _p(initial_state), _p(cu_seqlens), d_y.data_ptr(),
