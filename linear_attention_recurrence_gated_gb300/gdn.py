@@ -990,7 +990,7 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
             # a page is contiguous: [H, dk, dv] packed at every stride(0)
             if not (t.get_device() == dev and (dev >= 0 or t.is_cuda) and t.dtype == _F32 and
                     t.shape == (P, *page) and (P <= 1 or t.stride(0) == stride) and
-                    (t.is_contiguous() or (P > 0 and t[0].is_contiguous()))):
+                    (t.is_contiguous() or (P > 0 and t[0].is_contiguous() and stride > 0))):
                 ok = False
     if not ok:
         _dtype_code(dt)
@@ -1004,7 +1004,8 @@ def gdn_lin_decode(q, k, v, log_decay, state, pages=None, *, o=None, state_out=N
         for name in ("state", "state_out"):
             t = specs[name][0]
             if t is not None and t.is_cuda and t.dim() == 4 and P > 0 and \
-                    (not t[0].is_contiguous() or (P > 1 and t.stride(0) != stride)):
+                    (not t[0].is_contiguous() or
+                     (P > 1 and (t.stride(0) != stride or stride <= 0))):
                 raise ValueError(f"{w}: {name} must have contiguous pages at one stride")
         one = lambda t: t if t is None or t.shape[0] == 0 else t[0]  # noqa: E731
         _explain(w, dev, dict(q=q, k=k, v=v, log_decay=log_decay, pages=pages, o=o,
@@ -1483,7 +1484,8 @@ def _pool_check(where, device, name, t, shape, dtype, like=None):
         raise ValueError(f"{where}: {name} must be on the device of the other tensors")
     P = t.shape[0]
     stride = t.stride(0) if P > 1 else 0
-    if not (t.is_contiguous() or (P > 0 and t[0].is_contiguous())) or \
+    # (pages on top of one another, of an expanded tensor: the library takes 0 for packed pages)
+    if not (t.is_contiguous() or (P > 0 and t[0].is_contiguous() and stride > 0)) or \
             (like is not None and (like.shape[0] != P or (P > 1 and like.stride(0) != stride))):
         raise ValueError(f"{where}: {name} must have contiguous pages at one stride")
     return P, stride
