@@ -374,16 +374,18 @@ gdn_ssm_grad_kernel(const BwdParams p) {
   const int vec = tid % B::VB, vch = first_ch + 8 * vec;
   const bool von = vch < end_ch;
   // The inputs of a tile, and the states kept before it, on their way to shared memory;
-  // every thread waits for its own.
+  // every thread waits for its own.  A tile of fewer than kL tokens begins at row `lead`
+  // (rows before it do not exist): behind its last token there is no step of zero that a
+  // last state that is not finite would turn into a part of dA.
   const auto raw = [&](int64_t tile, int i) {
     return reinterpret_cast<Raw8<T> *>(smem + B::RAW + (tile & 1) * B::TILE_RAW + i * B::VEC) + tid;
   };
-  const auto fetch = [&](int64_t tile, int64_t first, int cnt, const float *kept_at) {
+  const auto fetch = [&](int64_t tile, int64_t first, int lead, const float *kept_at) {
 #pragma unroll
     for (int i = 0; i < B::NV; ++i) {
       const int row = tid / B::VB + i * B::RT;
-      const bool there = von && row < cnt;
-      const int64_t at = there ? first + row : 0;
+      const bool there = von && row >= lead && (B::NV * B::RT == kL || row < kL);
+      const int64_t at = there ? first + row - lead : 0;
       const int c = there ? vch : 0;
       copy_vec(raw(tile, 4 * i), static_cast<const T *>(p.x) + at * p.sx + c, there);
       copy_vec(raw(tile, 4 * i + 1), static_cast<const T *>(p.dt) + at * p.sdt + c, there);
@@ -393,8 +395,8 @@ gdn_ssm_grad_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < B::NB; ++i) {
       const int idx = tid + i * kThreads, row = idx % (B::NBC / 2) / (S / 8), v = idx % (S / 8);
-      const bool there = idx < B::NBC && row < cnt;
-      const int64_t at = there ? first + row : 0;
+      const bool there = idx < B::NBC && row >= lead;
+      const int64_t at = there ? first + row - lead : 0;
       const T *from = idx < B::NBC / 2 ? static_cast<const T *>(p.b) + at * p.sb
                                        : static_cast<const T *>(p.c) + at * p.sc;
       copy_vec(raw(tile, 4 * B::NV + i), from + group * S + 8 * v, there);
@@ -447,7 +449,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       return tile ? p.ckpt + kept(begin, off + tile * kL) * state : nullptr;
     };
     if (tiles > 0)
-      fetch(tiles - 1, s.start + (tiles - 1) * kL, (int)(s.len - (tiles - 1) * kL), kept_at(tiles - 1));
+      fetch(tiles - 1, s.start + (tiles - 1) * kL, (int)(tiles * kL - s.len), kept_at(tiles - 1));
     // the gradient that comes from behind the segment, and the state at its start
     load_own<S>(p.dhT ? p.dhT + s.n * state : nullptr, own, g);
     for (int i = s.count - 1; i > s.seg; --i)
@@ -471,7 +473,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
 
     for (int64_t tile = tiles - 1; tile >= 0; --tile) {
       const int64_t t0 = tile * kL;
-      const int cnt = (int)(s.len - t0 < kL ? s.len - t0 : kL);
+      const int cnt = (int)(s.len - t0 < kL ? s.len - t0 : kL), lead = kL - cnt;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       // delta, delta x and ds of the tile; tokens that do not exist are zeros, which leave
       // states and gradients as they are
@@ -483,7 +485,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         if (row >= kL) continue;
         uint64_t v[4], d[4];
         steps_of(*raw(tile, 4 * i + 1), bias, p.softplus, d);
-        if (row >= cnt) d[0] = d[1] = d[2] = d[3] = 0ull;
+        if (row < lead) d[0] = d[1] = d[2] = d[3] = 0ull;
         pairs_of(*raw(tile, 4 * i), v);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = mul2(d[j], v[j]);
@@ -534,9 +536,9 @@ gdn_ssm_grad_kernel(const BwdParams p) {
         }
       }
       __syncthreads();
-      if (tile > 0) fetch(tile - 1, s.start + t0 - kL, kL, kept_at(tile - 1));
+      if (tile > 0) fetch(tile - 1, s.start + t0 - kL, 0, kept_at(tile - 1));
       uint64_t lift[2];
-      lifts4(A, sd + 4 * cl, lift);
+      lifts4(A, sd + lead * CB + 4 * cl, lift);
       // the tile's states
 #pragma unroll
       for (int t = 0; t < kL; ++t) {
@@ -623,7 +625,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
       // db and dc of this CTA's channels, four values a thread
       for (int i = 4 * tid; i < cnt * 2 * S; i += 4 * kThreads) {
         const int row = i / (2 * S), at = i % (2 * S);
-        const float *red = smem + B::RED + row * 2 * S + at;
+        const float *red = smem + B::RED + (lead + row) * 2 * S + at;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
@@ -640,8 +642,8 @@ gdn_ssm_grad_kernel(const BwdParams p) {
 #pragma unroll
       for (int i = 0; i < B::NV; ++i) {
         const int row = tid / B::VB + i * B::RT;
-        if (!von || row >= cnt) continue;
-        const int64_t out = (s.start + t0 + row) * D + vch;
+        if (!von || row < lead || (B::NV * B::RT > kL && row >= kL)) continue;
+        const int64_t out = (s.start + t0 + row - lead) * D + vch;
         const int at = row * CB + 8 * vec;
         uint64_t xv[4], yv[4], qv[4], v[4], o[4];
         Raw8<T> r;
