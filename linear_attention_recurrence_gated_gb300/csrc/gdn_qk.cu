@@ -68,7 +68,8 @@ __device__ __forceinline__ void cos_sin(float r, float &c, float &s) {
 }
 // Cosines and sines of positions x inv_freq for the tile's tokens: [token][2][pitch].
 __device__ __forceinline__ void turn_table(const Params &p, int64_t tok0, int cnt, int lanes,
-                                           const uint64_t *freq, float *table) {
+                                           const uint64_t *freq, const float *unit,
+                                           float *table) {
   const int half = p.R / 2;   // lanes: the power of two that holds it, at most 256
   for (int t = threadIdx.x / lanes; t < cnt; t += kThreads / lanes) {
     const int f = threadIdx.x & (lanes - 1);
@@ -81,19 +82,21 @@ __device__ __forceinline__ void turn_table(const Params &p, int64_t tok0, int cn
     const uint32_t quarter = (turns + (1u << 29)) >> 30;   // (0 .. 4, 4 being none)
     const int32_t rest = (int32_t)(turns - (quarter << 30));
     float c, s;
-    cos_sin((float)rest * 1.4629180792671596e-9f, c, s);   // 2 pi / 2^32
+    cos_sin((float)rest * unit[f], c, s);
     const float a = quarter & 1 ? -s : c, b = quarter & 1 ? c : s;
     float *at = table + t * 2 * p.pitch + f;
     at[0] = quarter & 2 ? -a : a;
     at[p.pitch] = quarter & 2 ? -b : b;
   }
 }
-// The frequencies as fractions of a turn, whole turns left out.
-__device__ __forceinline__ void load_freq(const Params &p, uint64_t *freq) {
+// The frequencies as fractions of a turn, whole turns left out, and the angle of 2^-32 of
+// one: NaN for a frequency that is not finite, so that its cosines and sines are.
+__device__ __forceinline__ void load_freq(const Params &p, uint64_t *freq, float *unit) {
   for (int i = threadIdx.x; i < p.R / 2; i += kThreads) {
     const double t = (double)p.inv_freq[i] * 0.15915494309189533577;   // / (2 pi)
     const double f = t - floor(t);
     freq[i] = f < 1.0 ? (uint64_t)(f * 0x1p53) << 11 : 0ull;
+    unit[i] = f == f ? 1.4629180792671596e-9f : __int_as_float(0x7fffffff);   // 2 pi / 2^32
   }
 }
 
@@ -202,6 +205,7 @@ gdn_qk_norm_kernel(const Params p) {
   __shared__ __align__(16) float tables[2][kTokens * 2 * kMaxHalf];   // of a tile and the next
   __shared__ __align__(16) float rows_buf[RG * LR * 16];
   __shared__ uint64_t freq[kMaxHalf];
+  __shared__ float unit[kMaxHalf];
   __shared__ __align__(16) float weights[BACK ? 1 : 2][LR * 16];   // times q's scale
   const int tid = threadIdx.x, rg = tid / LR;
   // the sides that this CTA takes
@@ -231,7 +235,7 @@ gdn_qk_norm_kernel(const Params p) {
   }
   int lanes = 32;
   if (p.R) {
-    load_freq(p, freq);
+    load_freq(p, freq, unit);
     while (lanes < p.R / 2) lanes *= 2;
   }
   const float over = p.l2 ? 1.f : 1.f / (float)p.D;
@@ -265,7 +269,7 @@ gdn_qk_norm_kernel(const Params p) {
     which_table ^= 1;
     float *table = tables[which_table];
     if (p.R) {
-      turn_table(p, tok0, cnt, lanes, freq, table);
+      turn_table(p, tok0, cnt, lanes, freq, unit, table);
       __syncthreads();
     }
     int side = side0, base = 0;
