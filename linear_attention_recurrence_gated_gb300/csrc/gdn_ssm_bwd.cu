@@ -299,7 +299,8 @@ struct Bwd {
   static constexpr int RAW = KEPT + OWN;                    // inputs of this tile and the next
   static constexpr int TILE_RAW = (4 * NV + NB) * VEC;
   static constexpr size_t kFloats = RAW + 2 * TILE_RAW + 4; // (and the place in tensor memory)
-  static constexpr int kCtas = 3 * (4 * kFloats + 1024) <= 228 * 1024 ? 3 : 2;   // an SM
+  static constexpr int kFit = 228 * 1024 / (4 * kFloats + 1024);   // (1 KB a CTA is the system's)
+  static constexpr int kCtas = kFit < 3 ? kFit : 3;                // an SM
 };
 constexpr uint32_t kColumns = 16 * kL;   // of tensor memory: a thread's 16 values for each token
 
@@ -802,6 +803,12 @@ int64_t parts_of(int64_t slots, int64_t blocks) {
   const int64_t most = (6 * kSMs + blocks - 1) / blocks;
   return slots < most ? slots : most;
 }
+// CTAs an SM that the plan counts on: those of the second launch (Bwd::kCtas), but two for
+// fp32 with S = 8, of which one fits.  (Planned with one, fp32, S 8: [8, 1024, 2560] 927 us,
+// [1, 16384, 1280] 660, [4, 4096, 2560] 1166, [2, 2048, 1024] 158, [3, 3000, 512] 165; with
+// two 592, 619, 1115, 166, 185.)
+constexpr int plan_ctas(bool wide, int S) { return wide || S == 8 ? 2 : 3; }
+
 // The workspace of a call in any form that it may take (storage types, and uncut).
 size_t workspace_bytes_of(int32_t num_seqs, int32_t seq_len, bool packed, int32_t channels,
                           int32_t d_state, int32_t groups) {
@@ -837,7 +844,9 @@ cudaError_t launch_s(const BwdParams &p, int groups, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   const dim3 tiles(groups * p.blocks, p.parts);
   constexpr size_t kGrad = 4 * Bwd<T, S>::kFloats;
-  static_assert(Bwd<T, S>::kCtas == (sizeof(T) == 4 || S == 8 ? 2 : 3), "the plan's CTAs an SM");
+  static_assert(Bwd<T, S>::kCtas * (kGrad + 1024) <= 228 * 1024, "CTAs that fit an SM");
+  static_assert(Bwd<T, S>::kCtas == (sizeof(T) == 4 && S == 8 ? 1 : plan_ctas(sizeof(T) == 4, S)),
+                "what the plan's comment says of them");
   if (p.gate) {
     err = allow_smem<gdn_ssm_grad_kernel<T, S, true>>(kGrad);
     if (err == cudaSuccess)
@@ -958,9 +967,8 @@ gdn_status gdn_ssm_bwd(const void *x, const void *dt, const float *A_log, const 
   p.seq.seq_len = seq_len;
   p.seq.num_seqs = num_seqs;
   const int64_t all = (int64_t)groups * p.blocks;
-  // CTAs an SM of the second launch: see Bwd::kCtas
-  const int ctas = dtype == GDN_F32 || d_state == 8 ? 2 : 3;
-  auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, all, ctas, kFirst);
+  auto pl = plan(num_seqs, seq_len, cu_seqlens != nullptr, all,
+                 plan_ctas(dtype == GDN_F32, d_state), kFirst);
   Layout l;
   for (;;) {   // uncut where the workspace is too small for the segments
     p.parts = (int32_t)parts_of(pl.slots, all);
