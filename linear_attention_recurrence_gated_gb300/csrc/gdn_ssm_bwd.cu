@@ -682,7 +682,7 @@ gdn_ssm_grad_kernel(const BwdParams p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {   // (rates carry log2 e)
           o[j] = fma2(xv[j], qv[j], mul2(pk(0.6931471805599453f, 0.6931471805599453f), v[j]));
-          if (p.softplus) o[j] = mul2(o[j], sigmoid2(add2(tv[j], bias[j])));
+          if (p.softplus) o[j] = mul2(o[j], softplus_slope2<T>(add2(tv[j], bias[j])));
           sums[1][j] = add2(sums[1][j], o[j]);
         }
         set_pairs(r, o);
