@@ -96,3 +96,54 @@ def grads(fn, inputs, d_outs, **how):
     total = sum((o * _d(d)).sum() for o, d in zip(outs, d_outs) if d is not None)
     total.backward()
     return {n: torch.zeros_like(t) if t.grad is None else t.grad for n, t in leaf.items()}
+
+
+def scan_grads(i, d_y, d_last=None, mask=None, softplus=True):
+    """(y, last states, gradients) of sequences side by side, by the recurrence and its adjoint
+    written out, in fp64 on the tensors' device.  ``i``: x, dt, A_log, b, c and h0, D_skip,
+    gate, dt_bias (or None) of [N, T, ..] rows; mask [N, T]: which rows are tokens (or None:
+    all)."""
+    i = {n: None if t is None else t.double() for n, t in i.items()}
+    x, (D, S) = i["x"], i["A_log"].shape
+    N, T, _ = x.shape
+    per = D // i["b"].shape[2]
+    wide = lambda t: t.repeat_interleave(per, -2)  # noqa: E731
+    A = -torch.exp(i["A_log"])
+    v = i["dt"] if i["dt_bias"] is None else i["dt"] + i["dt_bias"]
+    delta = v.clamp(min=0) + torch.log1p(torch.exp(-v.abs())) if softplus else v
+    skip = x.new_zeros(D) if i["D_skip"] is None else i["D_skip"]
+    sig = None if i["gate"] is None else torch.sigmoid(i["gate"])
+    silu = x.new_ones(()) if sig is None else i["gate"] * sig
+    d_y = d_y.double()
+    if mask is not None:
+        delta, d_y = delta * mask[..., None], d_y * mask[..., None]
+    h = x.new_zeros(N, D, S) if i["h0"] is None else i["h0"]
+    states, s = [h], torch.empty_like(x)
+    for t in range(T):
+        h = torch.exp(delta[:, t, :, None] * A) * h + (delta[:, t] * x[:, t])[..., None] * wide(i["b"][:, t])
+        states.append(h)
+        s[:, t] = (wide(i["c"][:, t]) * h).sum(-1) + skip * x[:, t]
+    last, ds = h, d_y * silu
+    g = torch.zeros_like(h) if d_last is None else d_last.double()
+    dx, ddelta = skip * ds, torch.empty_like(x)
+    db, dc, dA = torch.empty_like(i["b"]), torch.empty_like(i["c"]), torch.zeros_like(A)
+    group = lambda t: t.view(N, -1, per, S).sum(2)  # noqa: E731
+    for t in range(T - 1, -1, -1):
+        bt, step = wide(i["b"][:, t]), delta[:, t, :, None]
+        G = g + ds[:, t, :, None] * wide(i["c"][:, t])
+        dc[:, t] = group(ds[:, t, :, None] * states[t + 1])
+        db[:, t] = group(step * x[:, t, :, None] * G)
+        q = (bt * G).sum(-1)
+        dx[:, t] += delta[:, t] * q
+        g = torch.exp(step * A) * G
+        w = g * states[t]
+        ddelta[:, t] = x[:, t] * q + (A * w).sum(-1)
+        dA += (step * w).sum(0)
+    ddt = ddelta * torch.sigmoid(v) if softplus else ddelta
+    if mask is not None:
+        ddt = ddt * mask[..., None]
+    out = dict(dx=dx, ddt=ddt, db=db, dc=dc, dA_log=A * dA, dD_skip=(ds * x).sum((0, 1)),
+               ddt_bias=ddt.sum((0, 1)), dh0=g)
+    if sig is not None:
+        out["dgate"] = d_y * s * sig * (1 + i["gate"] * (1 - sig))
+    return s * silu, last, out
