@@ -904,7 +904,10 @@ gdn_status gdn_ssm_step(const void *x, const void *dt, const float *A_log, const
 
 /*
  * gdn_conv_fwd -- short causal depthwise convolution with a bias, gdn_conv_silu for packed
- * sequences and with a backward pass.  Per sequence, token t and channel ch:
+ * sequences and with a backward pass.  (Dense rows with SiLU and no bias may take either:
+ * the same values up to rounding in the same time.  gdn_conv_silu needs no workspace and
+ * takes any multiple of 4 channels; gdn_conv_fwd what gdn_conv_bwd and gdn_conv_step go
+ * with.)  Per sequence, token t and channel ch:
  *
  *     z_t = bias[ch] + sum_{k < taps} w[ch, k] x_{t - (taps - 1) + k},   y = silu(z) with
  *     GDN_CONV_SILU, else z

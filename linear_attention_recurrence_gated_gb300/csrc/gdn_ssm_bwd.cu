@@ -17,13 +17,13 @@
 // ddt_bias) are left in the workspace and added up in a fixed order by the last launch:
 // results are bitwise reproducible.
 //
-// [4, 4096, 1280], S = 16, bf16 with a gate: 554 us; the launches 150, 400 and 10.  375
-// instructions a token and channel in the second: 136 of them the products and
+// [4, 4096, 1280], S = 16, bf16 with a gate: 557 us; the launches 147, 405 and 10.  367
+// instructions a token and 32 channels in the second: 136 of them the products and
 // exponentials, some 80 the sums over lanes, the rest inputs, softplus, the gate and their
-// gradients.  The multiply-adds' pipe is busy for 42 %, issue 52 %.  (States in shared
+// gradients.  The multiply-adds' pipe is busy for 40 %, issue 51 %.  (States in shared
 // memory, two CTAs an SM: 763 us in all; in tensor memory 603; inputs and kept states by
 // asynchronous copies 554; lifts by tiles, for their accuracy, 561; the first two loops over
-// a tile unrolled whole 554, the third too 563.)
+// a tile unrolled whole 554, the third too 563; the rows of a short tile before its tokens 557.)
 #include "gdn_ptx.cuh"
 #include "gdn_ssm.cuh"
 

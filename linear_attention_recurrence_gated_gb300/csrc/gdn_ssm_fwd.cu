@@ -7,8 +7,8 @@
 // the next tile's inputs are on their way to registers; then the tile's outputs take the
 // skip and the gate on their way out.
 //
-// [4, 4096, 1280], S = 16, bf16 with a gate: 176 us, 73 of them the first launch; some 105
-// instructions a token and channel where outputs are formed, of which 32 packed
+// [4, 4096, 1280], S = 16, bf16 with a gate: 176 us, 73 of them the first launch; some 104
+// instructions a token and 32 channels where outputs are formed, of which 32 packed
 // multiply-adds and 16 exponentials are the scan itself, the rest its operands, softplus and
 // the gate.  No pipe is full (multiply-adds 50 %, exponentials 43 %, shared memory 62 %,
 // issue 56 %), but each is near what warps that take turns at them reach: fewer instructions
