@@ -535,8 +535,9 @@ gdn_status gdn_conv_silu(const void *x, const float *w, const void *x_prev, void
  * Sizes as gdn_fwd (chunk 64); flags must be 0.  No gradient buffer may
  * overlap an input or another gradient.  workspace: at least
  * gdn_bwd_workspace_size(...) bytes, enough for either path (per-chunk
- * records of the chunked form, or state checkpoints and per-CTA scratch); the
- * first 256 bytes are the status word (zero it once with gdn_workspace_init).
+ * records of the chunked form, or state checkpoints and per-CTA scratch) and
+ * num_seqs rows of seq_len tokens; packed sequences need the
+ * gdn_bwd_packed_workspace_size(...) bytes of their total_tokens.  The first 256 bytes are the status word (zero it once with gdn_workspace_init).
  * Device-detected errors (bad cu_seqlens) are reported by gdn_check.  Returns
  * GDN_OK once enqueued, or an error code with nothing enqueued.  seq_len is
  * the packed token count when cu_seqlens is given.  Empty sequences and
@@ -545,6 +546,8 @@ gdn_status gdn_conv_silu(const void *x, const float *w, const void *x_prev, void
  */
 size_t gdn_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_heads,
                               int32_t head_dim_k, int32_t head_dim_v);
+size_t gdn_bwd_packed_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t num_heads,
+                                     int32_t head_dim_k, int32_t head_dim_v);
 gdn_status gdn_bwd(const void *q, const void *k, const void *v, const float *g,
                    const void *beta, const float *initial_state, const int32_t *cu_seqlens,
                    const void *d_o, const float *d_final_state, float *dq, float *dk,

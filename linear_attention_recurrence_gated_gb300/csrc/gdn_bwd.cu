@@ -500,8 +500,8 @@ cudaError_t launch_bwd_t(const BwdParams &P, cudaStream_t s) {
 // Checkpoints per 64-token chunk: one at every sub-chunk start while that
 // array stays within 4 GiB (the backward then skips recomputing the sub-chunk
 // starts), else one per chunk.
-int ckpt_per_chunk(int64_t num_seqs, int64_t seq_len, int64_t H, int64_t dk, int64_t dv) {
-  const int64_t fine = ckpt_slots(num_seqs, seq_len) * (kCk / kSub) * H * dk * dv * 4;
+int ckpt_per_chunk(int64_t slots, int64_t H, int64_t dk, int64_t dv) {
+  const int64_t fine = slots * (kCk / kSub) * H * dk * dv * 4;
   return fine <= (int64_t(4) << 30) ? kCk / kSub : 1;
 }
 
@@ -527,25 +527,40 @@ size_t bwd_chunked_ws_bytes(int64_t units, int dk, int dv);
 cudaError_t launch_bwd_chunked(const FwdParams &f, const void *dO, const float *dHN, float *dq,
                                float *dk, float *dv, float *dg, float *dbeta, float *dh0,
                                void *ws, int64_t slots, cudaStream_t s);
+
+namespace {
+size_t workspace_bytes_of(int32_t num_seqs, int32_t seq_len, bool packed, int32_t num_heads,
+                          int32_t head_dim_k, int32_t head_dim_v) {
+  if (num_seqs <= 0 || seq_len < 0 || num_heads <= 0 || head_dim_k <= 0 || head_dim_v <= 0)
+    return 0;
+  if (head_dim_v % kCols) return 0;
+  const int64_t slots = ckpt_slots(num_seqs, seq_len, packed);
+  const int per = ckpt_per_chunk(slots, num_heads, head_dim_k, head_dim_v);
+  const size_t ck = (size_t)slots * per * num_heads * head_dim_k * head_dim_v;
+  size_t need = kStatusBytes + 4 * (ck + scratch_floats(num_seqs, num_heads, head_dim_k, head_dim_v));
+  // bf16 storage with small heads takes the chunked path, with its own records
+  if (bwd_chunked_supported(head_dim_k, head_dim_v)) {
+    const size_t chunked =
+        kStatusBytes + bwd_chunked_ws_bytes(slots * num_heads, head_dim_k, head_dim_v);
+    if (chunked > need) need = chunked;
+  }
+  return need;
+}
+}  // namespace
 }  // namespace gdn
 
 extern "C" size_t gdn_bwd_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t num_heads,
                                          int32_t head_dim_k, int32_t head_dim_v) {
-  using namespace gdn;
-  if (num_seqs <= 0 || seq_len < 0 || num_heads <= 0 || head_dim_k <= 0 || head_dim_v <= 0)
-    return 0;
-  if (head_dim_v % kCols) return 0;
-  const int per = ckpt_per_chunk(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v);
-  const size_t ck =
-      (size_t)ckpt_slots(num_seqs, seq_len) * per * num_heads * head_dim_k * head_dim_v;
-  size_t need = kStatusBytes + 4 * (ck + scratch_floats(num_seqs, num_heads, head_dim_k, head_dim_v));
-  // bf16 storage with small heads takes the chunked path, with its own records
-  if (bwd_chunked_supported(head_dim_k, head_dim_v)) {
-    const size_t chunked = kStatusBytes + bwd_chunked_ws_bytes(
-        ckpt_slots(num_seqs, seq_len) * num_heads, head_dim_k, head_dim_v);
-    if (chunked > need) need = chunked;
-  }
-  return need;
+  const size_t dense =
+      gdn::workspace_bytes_of(num_seqs, seq_len, false, num_heads, head_dim_k, head_dim_v);
+  const size_t packed =
+      gdn::workspace_bytes_of(num_seqs, seq_len, true, num_heads, head_dim_k, head_dim_v);
+  return dense > packed ? dense : packed;
+}
+extern "C" size_t gdn_bwd_packed_workspace_size(int32_t num_seqs, int32_t total_tokens,
+                                                int32_t num_heads, int32_t head_dim_k,
+                                                int32_t head_dim_v) {
+  return gdn::workspace_bytes_of(num_seqs, total_tokens, true, num_heads, head_dim_k, head_dim_v);
 }
 
 extern "C" gdn_status gdn_bwd(const void *q, const void *k, const void *v, const float *g,
@@ -579,8 +594,10 @@ extern "C" gdn_status gdn_bwd(const void *q, const void *k, const void *v, const
     if (ptr && !aligned16(ptr)) return GDN_ERR_INVALID_ARG;
   if (!workspace) return GDN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return GDN_ERR_INVALID_ARG;
-  const size_t need = gdn_bwd_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v);
-  if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  const int64_t slots = ckpt_slots(num_seqs, seq_len, cu_seqlens != nullptr);
+  if (workspace_bytes < workspace_bytes_of(num_seqs, seq_len, cu_seqlens != nullptr, num_heads,
+                                           head_dim_k, head_dim_v))
+    return GDN_ERR_WORKSPACE;
 
   // aliasing: the gradients overlap no input and no other gradient
   const size_t e = dtype == GDN_F32 ? 4 : 2;
@@ -622,15 +639,14 @@ extern "C" gdn_status gdn_bwd(const void *q, const void *k, const void *v, const
   // which writes every gradient once (no zero fills, no atomics)
   if (dtype == GDN_BF16 && bwd_chunked_supported(head_dim_k, head_dim_v)) {
     const cudaError_t err = launch_bwd_chunked(
-        f, d_o, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, ws + kStatusBytes,
-        ckpt_slots(num_seqs, seq_len), s);
+        f, d_o, d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, ws + kStatusBytes, slots,
+        s);
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
   }
 
   float *ckpt = reinterpret_cast<float *>(ws + kStatusBytes);
-  const int per = ckpt_per_chunk(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v);
-  float *scratch = ckpt + (size_t)ckpt_slots(num_seqs, seq_len) * per * num_heads * head_dim_k *
-                              head_dim_v;
+  const int per = ckpt_per_chunk(slots, num_heads, head_dim_k, head_dim_v);
+  float *scratch = ckpt + (size_t)slots * per * num_heads * head_dim_k * head_dim_v;
 
   // the gradients gathered with atomics start from zero
   if (cudaMemsetAsync(dq, 0, rows * head_dim_k * 4, s) != cudaSuccess ||

@@ -174,9 +174,11 @@ __host__ __device__ inline int64_t ckpt_first_slot(int64_t n, int64_t start, int
                                                    bool varlen) {
   return varlen ? start / 64 + n : n * ((seq_len + 63) / 64);
 }
-__host__ __device__ inline int64_t ckpt_slots(int64_t num_seqs, int64_t seq_len) {
-  const int64_t dense = num_seqs * ((seq_len + 63) / 64), packed = seq_len / 64 + num_seqs + 1;
-  return dense > packed ? dense : packed;
+// Slots of num_seqs rows of seq_len tokens, or of as many packed sequences with seq_len
+// tokens together.
+__host__ __device__ inline int64_t ckpt_slots(int64_t num_seqs, int64_t seq_len, bool packed) {
+  const int64_t least = seq_len / 64 + num_seqs + 1, dense = num_seqs * ((seq_len + 63) / 64);
+  return packed || dense < least ? least : dense;
 }
 
 // A forward call that passed the host-side checks, ready to launch.

@@ -44,7 +44,8 @@ CHUNK_SIZE = 64
 EXPORTED = ("gdn_fwd_workspace_size", "gdn_workspace_init", "gdn_fwd", "gdn_check",
             "gdn_status_string", "gdn_fwd_kernel_name", "gdn_fwd_static_scratch",
             "gdn_decode", "gdn_diag_workspace_size", "gdn_diag_fwd", "gdn_conv_silu",
-            "gdn_bwd_workspace_size", "gdn_bwd", "gdn_fwd_debug", "gdn_check_record",
+            "gdn_bwd_workspace_size", "gdn_bwd_packed_workspace_size", "gdn_bwd", "gdn_fwd_debug",
+            "gdn_check_record",
             "gdn_fwd_kernel_name_chunk", "gdn_fwd_split_segments", "gdn_fwd_split_workspace_size",
             "gdn_diag_delta_workspace_size", "gdn_diag_delta_fwd",
             "gdn_lin_workspace_size", "gdn_lin_fwd", "gdn_lin_bwd", "gdn_lin_decode",
@@ -118,6 +119,8 @@ def lib() -> ctypes.CDLL:
                                      i32, i32, i32, i32, ctypes.c_int, u32, vp]
             L.gdn_bwd_workspace_size.restype = sz
             L.gdn_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+            L.gdn_bwd_packed_workspace_size.restype = sz
+            L.gdn_bwd_packed_workspace_size.argtypes = [i32, i32, i32, i32, i32]
             L.gdn_bwd.restype = ctypes.c_int
             L.gdn_bwd.argtypes = [vp] * 15 + [i32] * 6 + [ctypes.c_int, u32, vp, sz, vp]
             L.gdn_conv_silu.restype = ctypes.c_int
@@ -641,8 +644,11 @@ def gdn_conv_silu(x, w, x_prev=None, *, y=None, x_tail=None, stream=None):
 
 
 def gdn_bwd_workspace_size(num_seqs: int, seq_len: int, num_heads: int, head_dim_k: int,
-                           head_dim_v: int) -> int:
-    return int(lib().gdn_bwd_workspace_size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v))
+                           head_dim_v: int, packed: bool = False) -> int:
+    """Bytes for ``num_seqs`` rows of ``seq_len`` tokens; ``packed``: for ``num_seqs`` packed
+    sequences, ``seq_len`` tokens together."""
+    size = lib().gdn_bwd_packed_workspace_size if packed else lib().gdn_bwd_workspace_size
+    return int(size(num_seqs, seq_len, num_heads, head_dim_k, head_dim_v))
 
 
 def gdn_bwd(q, k, v, g, beta, d_o, initial_state=None, cu_seqlens=None, d_final_state=None, *,
@@ -679,7 +685,7 @@ def gdn_bwd(q, k, v, g, beta, d_o, initial_state=None, cu_seqlens=None, d_final_
                  "dbeta": torch.empty((B, T, H), **f32),
                  "dh0": torch.empty((N, H, dk, dv), **f32)}
     if workspace is None:
-        n = gdn_bwd_workspace_size(N, T, H, dk, dv)
+        n = gdn_bwd_workspace_size(N, T, H, dk, dv, cu_seqlens is not None)
         workspace = torch.zeros(n, dtype=torch.uint8, device=q.device)
     st = lib().gdn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                        _ptr(cu_seqlens), _ptr(d_o), _ptr(d_final_state), _ptr(grads["dq"]),
