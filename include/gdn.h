@@ -528,7 +528,8 @@ gdn_status gdn_conv_silu(const void *x, const float *w, const void *x_prev, void
  * - bf16 storage with head_dim_k, head_dim_v in {32, 64}: the same algebra in
  *   the chunked (WY) form of gdn_fwd, with bf16 tensor-core products and fp32
  *   accumulation (the precision class of gdn_fwd's tensor-core path); every
- *   gradient is written once, so results are bitwise reproducible;
+ *   gradient is written once, so results are bitwise reproducible, but for dg:
+ *   its terms are sums of partial ones by atomics, the same to fp32 rounding;
  * - otherwise: the recurrence above token by token in fp32, from state
  *   checkpoints; dq, dk, dg and dbeta are summed with atomics over
  *   value-column slices, so they agree from run to run to fp32 rounding only.
