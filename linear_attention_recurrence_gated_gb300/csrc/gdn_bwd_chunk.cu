@@ -580,7 +580,8 @@ __global__ void __launch_bounds__(kThreads) gdn_bwdc_chain_kernel(const ChunkBwd
       x = (src != nullptr && active) ? src[sbase + (size_t)d * DV + c] : 0.f;
     });
   }
-  stage(0, REV ? nck - 1 : 0);
+  // (an empty sequence has no records: the one before its first slot may lie before the arrays)
+  if (nck > 0) stage(0, REV ? nck - 1 : 0);
   for (int it = 0; it < nck; ++it) {
     const int cc = REV ? nck - 1 - it : it, buf = it & 1;
     if (it + 1 < nck) {

@@ -41,7 +41,8 @@ def test_packed_training_of_128_sequences(dtype, D):
 
 
 def test_ragged_sequences_with_empty_ones():
-    """Chunks that end inside sequences, empty sequences, one of a single token: as the sequences
+    """Chunks that end inside sequences, empty sequences (the first among them, before whose slot
+    there is no record to read), one of a single token: as the sequences
     by themselves (bf16, heads of 64: bits, dg as above)."""
     lens = [0, 1, 64, 65, 0, 130, 7, 63, 200, 0]
     H, D = 3, 64
