@@ -538,7 +538,8 @@ gdn_status gdn_conv_silu(const void *x, const float *w, const void *x_prev, void
  * gdn_bwd_workspace_size(...) bytes, enough for either path (per-chunk
  * records of the chunked form, or state checkpoints and per-CTA scratch) and
  * num_seqs rows of seq_len tokens; packed sequences need the
- * gdn_bwd_packed_workspace_size(...) bytes of their total_tokens.  The first 256 bytes are the status word (zero it once with gdn_workspace_init).
+ * gdn_bwd_packed_workspace_size(...) bytes of their total_tokens.  The first
+ * 256 bytes are the status word (zero it once with gdn_workspace_init).
  * Device-detected errors (bad cu_seqlens) are reported by gdn_check.  Returns
  * GDN_OK once enqueued, or an error code with nothing enqueued.  seq_len is
  * the packed token count when cu_seqlens is given.  Empty sequences and
@@ -827,8 +828,8 @@ gdn_status gdn_pages_compact(void *pool, int64_t page_bytes, int32_t num_pages,
  * when sequences are cut along time to fill the GPU.  gdn_ssm_workspace_size(...) is
  * enough for any call of these sizes, gdn_ssm_packed_workspace_size(...) for one of
  * num_seqs packed sequences with total_tokens tokens together; with less (at least 256
- * bytes) sequences run uncut, with the same results up to rounding.  Calls sharing a workspace are ordered (same
- * stream).  Errors as gdn_fwd (bad cu_seqlens: gdn_check).
+ * bytes) sequences run uncut, with the same results up to rounding.  Calls sharing a
+ * workspace are ordered (same stream).  Errors as gdn_fwd (bad cu_seqlens: gdn_check).
  */
 size_t gdn_ssm_workspace_size(int32_t num_seqs, int32_t seq_len, int32_t channels,
                               int32_t d_state, int32_t groups);
